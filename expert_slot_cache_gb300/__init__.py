@@ -11,4 +11,6 @@ from .binding import (MODE_GATHER, MODE_RESIDENT, MODE_ZERO_RETURN, POLICY_LFU, 
                       cache_gather, cache_manage, combine, expert_ffn, ffn_workspace_bytes, layer_workspace_bytes,
                       lib, permute, route, status_str, LayerStack, BIAS_GRADED, BIAS_FLAT, BIAS_HARD,
                       ROUTE_SIGMOID, ROUTE_DAMPED, cache_count, cache_repick,
-                      q8_slab_bytes, quantize_slabs, expert_ffn_q8, SCHED_CHUNKS, SCHED_WAVES)
+                      q8_slab_bytes, quantize_slabs, expert_ffn_q8, SCHED_CHUNKS, SCHED_WAVES,
+                      w4_bytes, w4_slab_bytes, w4_pack, w4_quantize, w4_pack_slabs, w4_quantize_slabs, W4Linear,
+                      expert_ffn_w4, W4Experts, Balance, BalanceLoss, balance_loss)

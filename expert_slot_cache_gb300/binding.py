@@ -11,7 +11,7 @@ import ctypes
 import os
 from ctypes import POINTER, c_float, c_int, c_int32, c_size_t, c_void_p
 from dataclasses import dataclass
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -48,7 +48,7 @@ class LayerArgs(ctypes.Structure):
                 ("out_miss", c_void_p), ("stats", c_void_p), ("dev_status", c_void_p),
                 ("workspace", c_void_p), ("workspace_bytes", c_size_t), ("prof", POINTER(Prof)),
                 ("affinity", c_float), ("route_flags", c_int32), ("window_counts", c_void_p), ("quant", c_int32),
-                ("schedule", c_int32), ("decode_kernels", c_int32)]
+                ("schedule", c_int32), ("decode_kernels", c_int32), ("quant_group", c_int32)]
 
 
 def _sig(name, argtypes, restype=c_int):
@@ -83,6 +83,21 @@ _repick = _sig("moe_cache_repick", [V, I32, I32, V, V, V, V, V, V])
 _ffn = _sig("moe_expert_ffn", [V, I32, I32, I32, I32, I32, V, V, V, V, I32, V, I32, V, V, V, V, c_size_t, V, V])
 _ffn_ws = _sig("moe_ffn_workspace_bytes", [I32, I32, I32, I32], c_size_t)
 _combine = _sig("moe_combine", [V, V, V, V, V, I32, I32, I32, I32, I32, V, V, V, V])
+LL = ctypes.c_longlong
+_w4_bytes = _sig("moe_w4_bytes", [I32, I32, I32], c_size_t)
+_w4_slab = _sig("moe_w4_slab_bytes", [I32, I32, I32], c_size_t)
+_w4_pack = _sig("moe_w4_pack", [V, V, I32, I32, I32, I32, V, V])
+_w4_quantize = _sig("moe_w4_quantize", [V, I32, I32, I32, I32, V, V])
+_w4_pack_slabs = _sig("moe_w4_pack_slabs", [V, V, I32, I32, I32, I32, V, V])
+_w4_quantize_slabs = _sig("moe_w4_quantize_slabs", [V, I32, I32, I32, I32, V, V])
+_w4_linear_ws = _sig("moe_w4_linear_workspace_bytes", [I32, I32, I32, I32], c_size_t)
+_w4_linear = _sig("moe_w4_linear", [V, LL, I32, I32, I32, I32, V, V, LL, I32, V, c_size_t, V, V])
+_ffn_w4_ws = _sig("moe_ffn_w4_workspace_bytes", [I32, I32, I32, I32], c_size_t)
+_ffn_w4 = _sig("moe_expert_ffn_w4", [V, I32, I32, I32, I32, I32, I32, V, V, V, V, I32, V, I32, V, V, V, c_size_t, V, V])
+_experts_w4_ws = _sig("moe_experts_w4_workspace_bytes", [I32, I32, I32, I32, I32], c_size_t)
+_experts_w4 = _sig("moe_experts_w4", [V, V, V, I32, I32, I32, I32, I32, I32, V, I32, V, V, V, c_size_t, V, V])
+_balance_ws = _sig("moe_balance_workspace_bytes", [I32], c_size_t)
+_balance = _sig("moe_balance_loss", [V, I32, V, V, V, I32, I32, I32, I32, I32, c_float, V, V, V, V, V, c_size_t, V, V])
 _layer = _sig("moe_layer_forward", [POINTER(LayerArgs), V, V])
 _layer_ws = _sig("moe_layer_workspace_bytes", [I32, I32, I32, I32, I32, I32], c_size_t)
 
@@ -269,6 +284,212 @@ def expert_ffn_q8(x, k, I, E, offset, rows, list_e, n_list, max_list, pool_q, e2
     return y
 
 
+# ---------------------------------------------------------------------------
+# 4-bit weights with group scales
+# ---------------------------------------------------------------------------
+
+def w4_bytes(K: int, N: int, group: int) -> int:
+    """Bytes of a packed K x N matrix (0: shape out of range)."""
+    return int(_w4_bytes(K, N, group))
+
+
+def w4_slab_bytes(H: int, I: int, group: int) -> int:
+    return int(_w4_slab(H, I, group))
+
+
+def _want(t: torch.Tensor, what: str, dtype, shape=None) -> None:
+    if t.dtype != dtype or not t.is_contiguous() or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{what}: need a contiguous {dtype} tensor" + (f" of shape {tuple(shape)}" if shape is not None else "")
+                         + f", got {t.dtype} {tuple(t.shape)}")
+
+
+def w4_pack(codes: torch.Tensor, scales: torch.Tensor, group: int, stream=None) -> torch.Tensor:
+    """codes uint8 [..., K, N] (0..15), scales bf16 [..., ceil(K / group), N] -> packed uint8 [..., w4_bytes]."""
+    K, N = codes.shape[-2:]
+    _want(codes, "codes", torch.uint8)
+    _want(scales, "scales", torch.bfloat16, (*codes.shape[:-2], -(-K // group) if group > 0 else 0, N))
+    out = torch.empty(*codes.shape[:-2], w4_bytes(K, N, group), dtype=torch.uint8, device=codes.device)
+    _ck(_w4_pack(_p(codes), _p(scales), codes[..., 0, 0].numel(), K, N, group, _p(out), _s(stream)), "moe_w4_pack")
+    return out
+
+
+def w4_quantize(w: torch.Tensor, group: int, stream=None) -> torch.Tensor:
+    """bf16 [..., K, N] -> packed uint8 [..., w4_bytes]."""
+    K, N = w.shape[-2:]
+    _want(w, "w", torch.bfloat16)
+    out = torch.empty(*w.shape[:-2], w4_bytes(K, N, group), dtype=torch.uint8, device=w.device)
+    _ck(_w4_quantize(_p(w), w[..., 0, 0].numel(), K, N, group, _p(out), _s(stream)), "moe_w4_quantize")
+    return out
+
+
+def w4_pack_slabs(codes: torch.Tensor, scales: torch.Tensor, H: int, I: int, group: int, stream=None) -> torch.Tensor:
+    """Expert slabs: codes uint8 [n][3HI], scales bf16 [n][2 ceil(H/group) I + ceil(I/group) H] -> [n][w4_slab_bytes]."""
+    n = codes.shape[0]
+    _want(codes, "codes", torch.uint8, (n, 3 * H * I))
+    if group > 0:
+        _want(scales, "scales", torch.bfloat16, (n, 2 * -(-H // group) * I + -(-I // group) * H))
+    out = torch.empty(n, w4_slab_bytes(H, I, group), dtype=torch.uint8, device=codes.device)
+    _ck(_w4_pack_slabs(_p(codes), _p(scales), n, H, I, group, _p(out), _s(stream)), "moe_w4_pack_slabs")
+    return out
+
+
+def w4_quantize_slabs(slabs: torch.Tensor, H: int, I: int, group: int, stream=None) -> torch.Tensor:
+    """bf16 slabs [n][3HI] (device) -> packed 4-bit slabs uint8 [n][w4_slab_bytes] (device)."""
+    n = slabs.shape[0]
+    _want(slabs, "slabs", torch.bfloat16, (n, 3 * H * I))
+    out = torch.empty(n, w4_slab_bytes(H, I, group), dtype=torch.uint8, device=slabs.device)
+    _ck(_w4_quantize_slabs(_p(slabs), n, H, I, group, _p(out), _s(stream)), "moe_w4_quantize_slabs")
+    return out
+
+
+class W4Linear:
+    """y = x W with a packed 4-bit matrix (w4_pack, w4_quantize) of K inputs and N outputs, for up to max_tokens rows.
+
+    x may be a row-strided view (last dimension contiguous).  One call at a time: calls share the workspace.
+    """
+
+    def __init__(self, packed: torch.Tensor, K: int, N: int, group: int, max_tokens: int = 1,
+                 out_dtype=torch.bfloat16):
+        if w4_bytes(K, N, group) == 0:
+            raise MoeError(-1, "W4Linear")
+        _want(packed, "packed", torch.uint8, (w4_bytes(K, N, group),))
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"out_dtype: bfloat16 or float32, got {out_dtype}")
+        self.packed, self.K, self.N, self.group = packed, K, N, group
+        self.max_tokens, self.out_dtype = max_tokens, out_dtype
+        self.dev_status = torch.zeros(1, dtype=torch.int32, device=packed.device)
+        self.workspace = torch.empty(int(_w4_linear_ws(max_tokens, K, N, group)), dtype=torch.uint8,
+                                     device=packed.device)
+
+    def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        T, K = x.shape
+        if T > self.max_tokens or K != self.K:
+            raise ValueError(f"x is {T} x {K}; the layer takes up to {self.max_tokens} rows of {self.K}")
+        if x.dtype != torch.bfloat16 or x.stride(1) != 1:
+            raise ValueError("x: need bf16 rows with a contiguous last dimension")
+        if out is None:
+            out = torch.empty(T, self.N, dtype=self.out_dtype, device=x.device)
+        elif out.dtype != self.out_dtype or out.shape != (T, self.N) or out.stride(1) != 1:
+            raise ValueError(f"out: need {self.out_dtype} ({T}, {self.N}) with a contiguous last dimension")
+        _ck(_w4_linear(x.data_ptr(), x.stride(0) if T > 1 else self.K, T, K, self.N, self.group,
+                       self.packed.data_ptr(), out.data_ptr(), out.stride(0) if T > 1 else self.N,
+                       int(self.out_dtype == torch.float32), self.workspace.data_ptr(), self.workspace.numel(),
+                       self.dev_status.data_ptr(), _s(stream)), "moe_w4_linear")
+        return out
+
+
+def expert_ffn_w4(x, k, I, E, group, offset, rows, list_e, n_list, max_list, pool, e2s=None, y=None, workspace=None,
+                  dev_status=None, stream=None) -> torch.Tensor:
+    T, H = x.shape
+    if y is None:
+        y = torch.zeros(T * k, H, dtype=torch.float32, device=x.device)
+    if workspace is None:
+        workspace = torch.empty(int(_ffn_w4_ws(T, H, k, I)), dtype=torch.uint8, device=x.device)
+    _ck(_ffn_w4(_p(x), T, H, I, k, E, group, _p(offset), _p(rows), _p(list_e), _p(n_list), max_list, _p(pool),
+                pool.shape[0], _p(e2s), _p(y), _p(workspace), workspace.numel(), _p(dev_status), _s(stream)),
+        "moe_expert_ffn_w4")
+    return y
+
+
+class W4Experts:
+    """The routed experts of one layer over a pool of packed 4-bit slabs ([S][w4_slab_bytes] uint8, device).
+
+    forward(x, ids, w) -> bf16 [T][H]: sum_j w[t][j] * FFN_{ids[t][j]}(x[t]).  One call at a time: calls share the
+    workspace.
+    """
+
+    def __init__(self, pool: torch.Tensor, H: int, I: int, k: int, E: int, group: int,
+                 e2s: Optional[torch.Tensor] = None, max_tokens: int = 64):
+        if w4_slab_bytes(H, I, group) == 0 or int(_experts_w4_ws(max_tokens, H, I, k, E)) == 0:
+            raise MoeError(-1, "W4Experts")
+        _want(pool, "pool", torch.uint8, (pool.shape[0], w4_slab_bytes(H, I, group)))
+        if e2s is not None:
+            _want(e2s, "e2s", torch.int32, (E,))
+        self.pool, self.H, self.I, self.k, self.E, self.group, self.e2s = pool, H, I, k, E, group, e2s
+        self.S, self.max_tokens = pool.shape[0], max_tokens
+        self.dev_status = torch.zeros(1, dtype=torch.int32, device=pool.device)
+        self.workspace = torch.empty(int(_experts_w4_ws(max_tokens, H, I, k, E)), dtype=torch.uint8,
+                                     device=pool.device)
+
+    def forward(self, x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, out: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+        T = x.shape[0]
+        if T > self.max_tokens:
+            raise ValueError(f"T={T} > max_tokens={self.max_tokens}")
+        _want(x, "x", torch.bfloat16, (T, self.H))
+        _want(ids, "ids", torch.int32, (T, self.k))
+        _want(w, "w", torch.float32, (T, self.k))
+        if out is None:
+            out = torch.empty(T, self.H, dtype=torch.bfloat16, device=x.device)
+        else:
+            _want(out, "out", torch.bfloat16, (T, self.H))
+        _ck(_experts_w4(x.data_ptr(), ids.data_ptr(), w.data_ptr(), T, self.H, self.I, self.k, self.E, self.group,
+                        self.pool.data_ptr(), self.S, None if self.e2s is None else self.e2s.data_ptr(),
+                        out.data_ptr(), self.workspace.data_ptr(), self.workspace.numel(),
+                        self.dev_status.data_ptr(), _s(stream)), "moe_experts_w4")
+        return out
+
+
+# ---------------------------------------------------------------------------
+# The router's balance loss
+# ---------------------------------------------------------------------------
+
+class Balance(NamedTuple):
+    loss: Optional[torch.Tensor]   # fp32 scalar
+    counts: torch.Tensor           # int32 [n_seq][E]
+    grad: Optional[torch.Tensor]   # [T][E], the type of the logits
+
+
+def balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float, seq_start: Optional[torch.Tensor] = None,
+                 token_mask: Optional[torch.Tensor] = None, sigmoid: bool = False, with_loss: bool = True,
+                 with_grad: bool = False, grad_loss: Optional[torch.Tensor] = None, dev_status=None,
+                 stream=None) -> Balance:
+    """Loss, per-sequence expert counts and (with_grad) the gradient in the logits times ``grad_loss`` (1 if None)."""
+    T, E = logits.shape
+    if logits.dtype != torch.float32:
+        _want(logits, "logits", torch.bfloat16, (T, E))
+    _want(logits, "logits", logits.dtype)
+    _want(ids, "ids", torch.int32, (T, ids.shape[1]))
+    if token_mask is not None and token_mask.dtype != torch.bool:
+        _want(token_mask, "token_mask", torch.uint8)
+    if token_mask is not None:
+        _want(token_mask, "token_mask", token_mask.dtype, (T,))
+    if seq_start is not None:
+        _want(seq_start, "seq_start", torch.int32)
+    if grad_loss is not None and (grad_loss.dtype != torch.float32 or grad_loss.numel() != 1):
+        raise ValueError("grad_loss: need one fp32 value")
+    n_seq = 1 if seq_start is None else seq_start.numel() - 1
+    dev = logits.device
+    loss = torch.empty((), dtype=torch.float32, device=dev) if with_loss else None
+    counts = torch.empty(max(n_seq, 0), E, dtype=torch.int32, device=dev)
+    grad = torch.empty_like(logits) if with_grad else None
+    ws = torch.empty(int(_balance_ws(n_seq)), dtype=torch.uint8, device=dev)
+    _ck(_balance(logits.data_ptr(), int(logits.dtype == torch.bfloat16), ids.data_ptr(), _ptr(token_mask) or None,
+                 _ptr(seq_start) or None, n_seq, T, E, ids.shape[1], ROUTE_SIGMOID if sigmoid else 0, coef,
+                 _ptr(grad_loss) or None, counts.data_ptr(), _ptr(loss) or None, _ptr(grad) or None, ws.data_ptr(),
+                 ws.numel(), _ptr(dev_status) or None, _s(stream)), "moe_balance_loss")
+    return Balance(loss, counts, grad)
+
+
+class BalanceLoss(torch.autograd.Function):
+    """balance_loss for autograd: ``loss, counts = BalanceLoss.apply(logits, ids, coef, seq_start, token_mask, sigmoid)``."""
+
+    @staticmethod
+    def forward(ctx, logits, ids, coef, seq_start=None, token_mask=None, sigmoid=False):
+        r = balance_loss(logits, ids, coef, seq_start, token_mask, sigmoid)
+        ctx.save_for_backward(logits, ids, seq_start, token_mask)
+        ctx.coef, ctx.sigmoid = coef, sigmoid
+        ctx.mark_non_differentiable(r.counts)
+        return r.loss, r.counts
+
+    @staticmethod
+    def backward(ctx, grad_loss, _):
+        logits, ids, seq_start, token_mask = ctx.saved_tensors
+        r = balance_loss(logits, ids, ctx.coef, seq_start, token_mask, ctx.sigmoid, with_loss=False, with_grad=True,
+                         grad_loss=grad_loss.float().contiguous())
+        return r.grad, None, None, None, None, None
+
+
 def ffn_workspace_bytes(T: int, H: int, k: int, I: int) -> int:
     return int(_ffn_ws(T, H, k, I))
 
@@ -315,7 +536,7 @@ class SlotCachedMoELayer:
 
     def __init__(self, w_router, pool, k, I, mode, policy=POLICY_LRU, host_slabs=None, state=None,
                  logit_offset=None, sel_bias=None, max_tokens=64, side_stream=True, affinity=0.0,
-                 route_flags=0, window_counts=None, quant=0, schedule=0, decode_kernels=0):
+                 route_flags=0, window_counts=None, quant=0, schedule=0, decode_kernels=0, quant_group=0):
         self.w_router, self.pool, self.k, self.I = w_router, pool, k, I
         self.H, self.E = w_router.shape
         self.S = pool.shape[0]
@@ -325,7 +546,8 @@ class SlotCachedMoELayer:
         self.affinity = float(affinity)
         self.route_flags = int(route_flags)
         self.window_counts = window_counts
-        self.quant = int(quant)  # pool / host hold W8A8 slabs (quantize_slabs)
+        self.quant = int(quant)  # pool / host hold W8A8 slabs (1: quantize_slabs) or 4-bit slabs (2: w4_pack_slabs)
+        self.quant_group = int(quant_group)  # inputs per scale group of 4-bit slabs
         self.schedule = int(schedule)  # SCHED_CHUNKS or SCHED_WAVES (GATHER steps larger than the pool)
         self.decode_kernels = int(decode_kernels)  # 0: persistent decode kernel where it applies, 1: separate
         dev = pool.device
@@ -358,7 +580,7 @@ class SlotCachedMoELayer:
                       self.stats.data_ptr(), self.dev_status.data_ptr(), self.workspace.data_ptr(),
                       self.workspace.numel(), ctypes.pointer(prof) if prof is not None else None, self.affinity,
                       self.route_flags, _ptr(self.window_counts), self.quant, self.schedule,
-                      self.decode_kernels)
+                      self.decode_kernels, self.quant_group)
         main = torch.cuda.current_stream() if stream is None else stream
         # the library forks to and joins back from the side stream itself
         _ck(_layer(ctypes.byref(a), c_void_p(main.cuda_stream),

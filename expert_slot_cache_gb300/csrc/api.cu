@@ -92,7 +92,8 @@ static LayerWs carve(void* base, int n, int H, int E, int I, int T) {
     w.xp = (uint16_t*)take(2 * (size_t)n * H);
     w.hb = (uint16_t*)take(2 * (size_t)n * I);
   }
-  w.skp_bytes = std::max(sk_part_bytes(n, H, I), q8_ws_bytes(n, H, I));  // bf16 stream or W8A8 buffers
+  // bf16 stream, W8A8 or 4-bit buffers
+  w.skp_bytes = std::max(std::max(sk_part_bytes(n, H, I), q8_ws_bytes(n, H, I)), w4_ws_bytes(n, H, I));
   if (w.skp_bytes) w.skp = (float*)take(w.skp_bytes);
   w.bytes = off;
   return w;
@@ -230,8 +231,10 @@ extern "C" int moe_layer_forward(const moe_layer_args* a, moe_stream_t main_s, m
     return MOE_ERR_ARG;
   }
   if (mode == MOE_MODE_ZERO_RETURN && (!a->out_res || !a->out_miss)) return MOE_ERR_ARG;
-  if (a->quant != 0 && a->quant != 1) return MOE_ERR_ARG;
+  if (a->quant < 0 || a->quant > 2) return MOE_ERR_ARG;
   if (a->quant && (mode == MOE_MODE_ZERO_RETURN || H % 16 || I % 16)) return MOE_ERR_ARG;
+  const bool q8_slabs = a->quant == 1, w4_slabs = a->quant == 2;
+  if (w4_slabs && !w4_slab_shape_ok(H, I, a->quant_group)) return MOE_ERR_ARG;
   if (a->schedule != MOE_SCHED_CHUNKS && a->schedule != MOE_SCHED_WAVES) return MOE_ERR_ARG;
   if (a->decode_kernels != 0 && a->decode_kernels != 1) return MOE_ERR_ARG;
   if (a->route_flags & ~(MOE_ROUTE_SIGMOID | MOE_ROUTE_DAMPED)) return MOE_ERR_ARG;
@@ -257,15 +260,17 @@ extern "C" int moe_layer_forward(const moe_layer_args* a, moe_stream_t main_s, m
   Prof prof;
   prof.p = a->prof;
   if (prof.p) prof.p->used = 0;
-  const size_t slab_bytes = a->quant ? q8_slab_bytes_h(H, I) : (size_t)6 * H * I;
-  if (mode == MOE_MODE_GATHER && !a->window_counts && a->decode_kernels == 0 && C >= T && ws.skp) {
+  const size_t slab_bytes = q8_slabs   ? q8_slab_bytes_h(H, I)
+                            : w4_slabs ? w4_slab_bytes_h(H, I, a->quant_group)
+                                       : (size_t)6 * H * I;
+  if (mode == MOE_MODE_GATHER && !a->window_counts && a->decode_kernels == 0 && C >= T && ws.skp && !w4_slabs) {
     // a small expert-cache step: manage, gather and the whole layer in one persistent launch
     int dev = 0, sms = 0;
     MOE_CUDA_TRY(cudaGetDevice(&dev));
     MOE_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
     const bool bf = !a->quant && decode_gather_eligible(T, H, E, k, I, S, policy, a->x, a->w_router, a->pool,
                                                         a->host_slabs, sms);
-    const bool q8 = a->quant && decode_q8_gather_eligible(T, H, E, k, I, S, policy, a->x, a->w_router, a->pool,
+    const bool q8 = q8_slabs && decode_q8_gather_eligible(T, H, E, k, I, S, policy, a->x, a->w_router, a->pool,
                                                           a->host_slabs, sms);
     if (bf || q8) {
       prof.begin(MOE_PROF_DECODE, ms);
@@ -275,13 +280,13 @@ extern "C" int moe_layer_forward(const moe_layer_args* a, moe_stream_t main_s, m
       return rd;
     }
   }
-  if (mode == MOE_MODE_RESIDENT && !a->window_counts && a->decode_kernels == 0 && H % 8 == 0 && ws.skp) {
+  if (mode == MOE_MODE_RESIDENT && !a->window_counts && a->decode_kernels == 0 && H % 8 == 0 && ws.skp && !w4_slabs) {
     // a small all-resident step: the whole layer in one persistent launch
     int dev = 0, sms = 0;
     MOE_CUDA_TRY(cudaGetDevice(&dev));
     MOE_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
     const bool bf = !a->quant && decode_eligible(T, H, E, k, I, S, a->x, a->w_router, a->pool);
-    const bool q8 = a->quant && decode_q8_eligible(T, H, E, k, I, S, a->x, a->w_router, a->pool, sms);
+    const bool q8 = q8_slabs && decode_q8_eligible(T, H, E, k, I, S, a->x, a->w_router, a->pool, sms);
     if (bf || q8) {
       prof.begin(MOE_PROF_DECODE, ms);
       const int rd = bf ? launch_decode(a, ws.route, ws.logits, ws.skp, ws.skp_bytes, ws.ctr, ms)
@@ -319,10 +324,13 @@ extern "C" int moe_layer_forward(const moe_layer_args* a, moe_stream_t main_s, m
               a->dev_status, S, 1, ws.xp, ws.hb, nullptr, ws.skp, ws.skp_bytes};
     // tensor-core path: y travels as bf16 through the same buffer (half the bytes)
     const bool y_bf16 = !a->quant && mode != MOE_MODE_ZERO_RETURN && prefill_eligible(f, n);
-    // the FFN of one expert list: bf16 slabs (stream / prefill / CUDA-core paths) or W8A8 slabs
-    auto ffn = [&](const FfnArgs& fa, cudaStream_t st) {
-      return a->quant ? launch_ffn_q8(fa, ws.skp, ws.skp_bytes, lmax, st, &prof) : launch_ffn(fa, lmax, st, &prof);
+    // the FFN of one expert list: bf16 slabs (stream / prefill / CUDA-core paths), W8A8 or 4-bit slabs
+    auto ffn_of = [&](const FfnArgs& fa, int maxl, cudaStream_t st) {
+      return q8_slabs   ? launch_ffn_q8(fa, ws.skp, ws.skp_bytes, maxl, st, &prof)
+             : w4_slabs ? launch_ffn_w4(fa, a->quant_group, ws.skp, ws.skp_bytes, maxl, st, &prof)
+                        : launch_ffn(fa, maxl, st, &prof);
     };
+    auto ffn = [&](const FfnArgs& fa, cudaStream_t st) { return ffn_of(fa, lmax, st); };
     if (y_bf16) f.yb = (uint16_t*)ws.y;
     if (mode == MOE_MODE_RESIDENT) {
       f.list_e = ws.act_e;
@@ -361,7 +369,7 @@ extern "C" int moe_layer_forward(const moe_layer_args* a, moe_stream_t main_s, m
           fb.list_e = le;
           fb.list_s = ls;
           fb.n_list = nl;
-          return a->quant ? launch_ffn_q8(fb, ws.skp, ws.skp_bytes, maxl, ms, &prof) : launch_ffn(fb, maxl, ms, &prof);
+          return ffn_of(fb, maxl, ms);
         };
         auto gather_list = [&](const int32_t* le, const int32_t* ls, const int32_t* nl, int maxl) -> int {
           prof.begin(MOE_PROF_GATHER, side);

@@ -76,6 +76,11 @@ bool sk_part_layout(int n, int H, int I, float* skp, size_t skp_bytes, float** g
 size_t q8_slab_bytes_h(int H, int I);
 size_t q8_ws_bytes(int n, int H, int I);
 int launch_ffn_q8(const FfnArgs& a, void* ws, size_t ws_bytes, int max_list, cudaStream_t stream, Prof* prof);
+size_t w4_slab_bytes_h(int H, int I, int group);
+size_t w4_ws_bytes(int n, int H, int I);
+bool w4_slab_shape_ok(int H, int I, int group);
+int launch_ffn_w4(const FfnArgs& a, int group, void* ws, size_t ws_bytes, int max_list, cudaStream_t stream,
+                  Prof* prof);
 bool sk_eligible(const FfnArgs& a);
 int launch_ffn_sk(const FfnArgs& a, int max_list, cudaStream_t stream, Prof* prof);
 size_t prefill_extra_bytes(int n, int H, int I);

@@ -401,6 +401,134 @@ int moe_expert_ffn_q8(const void* x, int T, int H, int I, int k, int E, const in
                       moe_stream_t stream);
 
 /*
+ * 4-bit weights with group scales.
+ * Source: "RTX 3060 runs a 35B MoE with llama.cpp" and "Betelgeuse ... on an
+ * RTX 3060": the models that the pages cache run from 4-bit weights.
+ *
+ * A K x N matrix W (y = x W) is code[k][n] in 0..15 and one bf16 scale per
+ * `group` (32, 64 or 128) consecutive inputs of an output column:
+ *   W[k][n] = (code[k][n] - 8) * scale[k / group][n];
+ * the last group of a column may be short.  K % 8 == 0, K <= 2^20, N <= 2^24.
+ * Packed, a matrix takes moe_w4_bytes(K, N, group) bytes (a multiple of 16;
+ * 0 for a shape out of range): the codes in the order the kernels read them,
+ * the scales as fp16 times a power of two per column, those powers, and the
+ * largest column 2-norm.  A scale keeps its value exactly unless it is below
+ * 2^-14 of its column's largest.  A packed expert slab is the packed gate and
+ * up (H x I) and down (I x H), moe_w4_slab_bytes(H, I, group) bytes; manage and
+ * gather move it as any slab.
+ *
+ * moe_w4_pack: codes device uint8 [n][K][N] (one per byte, values above 15 are
+ * masked), scales device bf16 [n][ceil(K / group)][N] -> dst device
+ * [n][moe_w4_bytes].
+ * moe_w4_quantize: w device bf16 [n][K][N] -> dst.  Per group and column: m =
+ * the element furthest from zero (the positive one of equal ones is taken only
+ * if it is larger), scale = bf16(m / -8), code = clamp(rint(w / scale), -8, 7)
+ * + 8 in fp32 (scale 0: code 8).
+ * The _slabs forms take the slab layout of moe_expert_ffn (codes or bf16
+ * weights [n][3HI]) with scales [n][2 ceil(H / group) I + ceil(I / group) H]
+ * (gate, up, down).
+ * Errors: MOE_ERR_ARG on NULL pointers or shapes out of range; MOE_ERR_ALIGN
+ * if dst is not 16-byte aligned.
+ */
+size_t moe_w4_bytes(int K, int N, int group);
+size_t moe_w4_slab_bytes(int H, int I, int group);
+int moe_w4_pack(const uint8_t* codes, const void* scales, int n, int K, int N, int group, void* dst,
+                moe_stream_t stream);
+int moe_w4_quantize(const void* w, int n, int K, int N, int group, void* dst, moe_stream_t stream);
+int moe_w4_pack_slabs(const uint8_t* codes, const void* scales, int n, int H, int I, int group, void* dst,
+                      moe_stream_t stream);
+int moe_w4_quantize_slabs(const void* w, int n, int H, int I, int group, void* dst, moe_stream_t stream);
+
+/*
+ * y = x W with a packed 4-bit matrix: projections beside the layer, a shared
+ * expert, the vocabulary head.
+ *   x    device bf16 [T] rows of K, ldx elements apart (ldx >= K, ldx % 8 == 0)
+ *   w    device, one packed matrix
+ *   out  device [T] rows of N, ldo elements apart (ldo >= N): bf16, or fp32
+ *        with out_f32 = 1
+ *   workspace  device, moe_w4_linear_workspace_bytes(T, K, N, group) bytes,
+ *        256-byte aligned (may be NULL where that is 0)
+ * Sums are fp32; the result does not depend on thread timing.
+ * Errors: MOE_ERR_ARG on NULL pointers, T < 1 or shapes out of range;
+ * MOE_ERR_ALIGN if x or w is not 16-byte aligned, ldx % 8 != 0, or the
+ * workspace is unaligned or too small.
+ */
+size_t moe_w4_linear_workspace_bytes(int T, int K, int N, int group);
+int moe_w4_linear(const void* x, long long ldx, int T, int K, int N, int group, const void* w, void* out,
+                  long long ldo, int out_f32, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                  moe_stream_t stream);
+
+/*
+ * The grouped SwiGLU expert FFN over a pool of packed 4-bit slabs: arguments,
+ * lists and y as moe_expert_ffn_q8 (rows of a listed expert without a slot are
+ * written as zeros and MOE_DEV_BAD_SLOT is set).  Workspace of
+ * moe_ffn_w4_workspace_bytes(T, H, k, I) bytes, 256-byte aligned; T*k <= 2^24.
+ * Errors: as moe_expert_ffn_q8; MOE_ERR_ARG for a group size other than 32, 64, 128.
+ */
+size_t moe_ffn_w4_workspace_bytes(int T, int H, int k, int I);
+int moe_expert_ffn_w4(const void* x, int T, int H, int I, int k, int E, int group, const int32_t* offset,
+                      const int32_t* rows, const int32_t* list_e, const int32_t* n_list, int max_list,
+                      const void* pool, int S, const int32_t* e2s, float* y, void* workspace,
+                      size_t workspace_bytes, int32_t* dev_status, moe_stream_t stream);
+
+/*
+ * The routed experts of a token batch in one call, from routing to output:
+ *   out[t] = bf16( sum_{j=0..k-1} w[t][j] * FFN_{ids[t][j]}(x[t]) ), j ascending, fp32,
+ * over a pool of packed 4-bit slabs (S slots; e2s as in moe_expert_ffn).
+ *   x device bf16 [T][H]; ids device int32 [T][k]; w device fp32 [T][k]
+ *   out device bf16 [T][H]
+ *   workspace device, moe_experts_w4_workspace_bytes(T, H, I, k, E) bytes,
+ *        256-byte aligned
+ * An id outside [0, E) sets MOE_DEV_BAD_EXPERT, an expert without a slot
+ * MOE_DEV_BAD_SLOT; either adds nothing to the sum.
+ * Errors: as moe_expert_ffn_w4.
+ */
+size_t moe_experts_w4_workspace_bytes(int T, int H, int I, int k, int E);
+int moe_experts_w4(const void* x, const int32_t* ids, const float* w, int T, int H, int I, int k, int E, int group,
+                   const void* pool, int S, const int32_t* e2s, void* out, void* workspace,
+                   size_t workspace_bytes, int32_t* dev_status, moe_stream_t stream);
+
+/*
+ * The router's balance loss over packed sequences, with its gradient.
+ * The pages have no training; their brightness profiles and window counts are
+ * this call's counts, taken per sequence.
+ * Over the valid tokens of sequence s (T_s of them; T_v in all sequences),
+ *   counts[s][e] = routings of expert e,   f[s][e] = E counts[s][e] / (k T_s),
+ *   p[t] = softmax(logits[t]), or with MOE_ROUTE_SIGMOID sigmoid(logits[t])
+ *          over its sum,
+ *   loss = coef / T_v * sum_t sum_e f[s(t)][e] p[t][e]
+ * (the mean over tokens; each sequence is balanced by itself).  f is constant
+ * in the gradient:
+ *   grad[t][e] = grad_loss * coef / T_v * p[t][e] (f[e] - sum_j f[j] p[t][j])
+ *                [* (1 - sigmoid(logits[t][e]))].
+ *   logits     device [T][E], fp32 or bf16 (bf16 = 1)
+ *   ids        device int32 [T][k]
+ *   token_mask device uint8 [T], 0 = padding, or NULL
+ *   seq_start  device int32 [n_seq + 1], ascending, sequence s is the tokens
+ *              [seq_start[s], seq_start[s + 1]), empty ones allowed; NULL with
+ *              n_seq = 1: one sequence of T tokens
+ *   grad_loss  device fp32 [1] (the loss's own gradient) or NULL = 1
+ *   counts     device int32 [n_seq][E] output
+ *   loss       device fp32 [1] output, or NULL
+ *   grad_logits device [T][E] output in the type of logits, or NULL
+ *   workspace  device, moe_balance_workspace_bytes(n_seq), 256-byte aligned
+ * Tokens masked or in no sequence add nothing, their logits are not read into
+ * any result and their gradient is 0; with no valid token the loss is 0.  A row
+ * of -inf has no probabilities: it adds 0 and gets a zero gradient.  The result
+ * does not depend on thread timing.
+ * An id outside [0, E) of a valid token sets MOE_DEV_BAD_EXPERT and is not
+ * counted; a descending seq_start sets MOE_DEV_BAD_GROUPS.
+ * Errors: MOE_ERR_ARG on NULL pointers, neither loss nor grad_logits, T < 1, E
+ * not in [1, 1024], k not in [1, min(16, E)], n_seq < 1 or unknown flags;
+ * MOE_ERR_ALIGN for an unaligned or small workspace.
+ */
+size_t moe_balance_workspace_bytes(int n_seq);
+int moe_balance_loss(const void* logits, int bf16, const int32_t* ids, const uint8_t* token_mask,
+                     const int32_t* seq_start, int n_seq, int T, int E, int k, int rflags, float coef,
+                     const float* grad_loss, int32_t* counts, float* loss, void* grad_logits, void* workspace,
+                     size_t workspace_bytes, int32_t* dev_status, moe_stream_t stream);
+
+/*
  * How GATHER mode serves a step that needs more experts than the pool holds
  * ("Porting vllm-expert-cache to NVIDIA GPUs", "Measuring, without fooling
  * yourself": a step is served from slots only when tokens x top_k <= slots;
@@ -453,9 +581,11 @@ typedef struct moe_layer_args {
   float affinity;            /* live-cache affinity lambda (0 = off); uses e2s before this step's manage */
   int32_t route_flags;       /* moe_route_ex flags (0 = softmax router, selection-only bias) */
   int32_t* window_counts;    /* device int32 [E] or NULL: each chunk's routings are added (moe_cache_count) */
-  int32_t quant;             /* 0: bf16 slabs; 1: W8A8 slabs (moe_quantize_slabs), RESIDENT or GATHER mode */
+  int32_t quant;             /* 0: bf16 slabs; 1: W8A8 slabs (moe_quantize_slabs); 2: 4-bit slabs
+                                (moe_w4_pack_slabs); 1 and 2 in RESIDENT or GATHER mode */
   int32_t schedule;          /* GATHER steps larger than the pool: MOE_SCHED_CHUNKS or MOE_SCHED_WAVES */
   int32_t decode_kernels;    /* 0: persistent decode kernels where they apply (RESIDENT, GATHER); 1: separate */
+  int32_t quant_group;       /* quant == 2: inputs per scale group (32, 64 or 128) */
 } moe_layer_args;
 
 /*
