@@ -24,7 +24,7 @@ struct W4Tile {
 
 __device__ __forceinline__ W4Tile w4_tile(const uint8_t* m, const W4Dims& d, int tile, int lane) {
   W4Tile t;
-  t.codes = reinterpret_cast<const uint4*>(m) + (size_t)tile * d.Kb * 32 + lane;
+  t.codes = reinterpret_cast<const uint4*>(m) + (size_t)tile * d.Kb * 32 + w4_chunk(lane >> 2, lane & 3);
   t.scales = reinterpret_cast<const uint32_t*>(m + d.scales) + (size_t)tile * d.Kg * 8 + (lane >> 2);
   return t;
 }
@@ -250,9 +250,14 @@ static int w4_sms(int* sms) {
   return MOE_OK;
 }
 
+// Rows from which the tensor-core path takes over.
+constexpr int kGemmRows = 512;
+
+static bool w4_gemm_ffn(int n) { return n >= kGemmRows; }
+
 size_t w4_ws_bytes(int n, int H, int I) {
-  (void)H;
-  return ((size_t)n * I * 4 + 255) & ~size_t(255);
+  const size_t h = ((size_t)n * I * 4 + 255) & ~size_t(255);
+  return w4_gemm_ffn(n) ? std::max(h, w4_ffn_gemm_ws(n, H, I, false)) : h;
 }
 
 // y rows of the listed experts; ws holds h (w4_ws_bytes).
@@ -261,6 +266,7 @@ int launch_ffn_w4(const FfnArgs& f, int group, void* ws, size_t ws_bytes, int ma
   const int n = f.T * f.k;
   if (ws_bytes < w4_ws_bytes(n, f.H, f.I)) return MOE_ERR_ALIGN;
   if (max_list <= 0) return MOE_OK;
+  if (w4_gemm_ffn(n)) return launch_ffn_w4_gemm(f, group, ws, nullptr, nullptr, stream, prof);
   int sms = 0;
   const int r = w4_sms(&sms);
   if (r != MOE_OK) return r;
@@ -305,12 +311,15 @@ static W4ExpWs w4_exp_ws(void* base, int T, int H, int I, int k, int E) {
   w.act_e = (int32_t*)take(4 * (size_t)E);
   w.n_act = (int32_t*)take(4);
   w.perm = (int32_t*)take(moe_permute_scratch_bytes(n, E) + 4);
-  w.y = (float*)take(4 * (size_t)n * H);
-  w.ffn_bytes = w4_ws_bytes(n, H, I);
+  const bool gemm = w4_gemm_ffn(n);  // its y is fp16 inside its own workspace
+  w.y = gemm ? nullptr : (float*)take(4 * (size_t)n * H);
+  w.ffn_bytes = gemm ? w4_ffn_gemm_ws(n, H, I, true) : w4_ws_bytes(n, H, I);
   w.ffn = take(w.ffn_bytes);
   w.bytes = off;
   return w;
 }
+
+static bool w4_gemm_linear(int T) { return T >= 64; }
 
 // Routing slots and hidden sizes whose products the kernels index with 32 bits.
 static bool w4_rows_ok(int T, int k) { return (int64_t)T * k <= (1 << 24); }
@@ -320,19 +329,22 @@ static bool w4_rows_ok(int T, int k) { return (int64_t)T * k <= (1 << 24); }
 using namespace moe;
 
 extern "C" size_t moe_w4_linear_workspace_bytes(int T, int K, int N, int group) {
-  (void)T, (void)K, (void)N, (void)group;
-  return 0;
+  if (T < 1 || !w4_shape_ok(K, N, group)) return 0;
+  return w4_gemm_linear(T) ? w4_linear_gemm_ws(T, K) : 0;
 }
 
 extern "C" int moe_w4_linear(const void* x, long long ldx, int T, int K, int N, int group, const void* w, void* out,
                              long long ldo, int out_f32, void* workspace, size_t workspace_bytes,
                              int32_t* dev_status, moe_stream_t stream) {
-  (void)workspace, (void)dev_status;
   if (!x || !w || !out || T < 1 || T > (1 << 24) || !w4_shape_ok(K, N, group) || ldx < K || ldo < N)
     return MOE_ERR_ARG;
   if (out_f32 != 0 && out_f32 != 1) return MOE_ERR_ARG;
   if ((uintptr_t)x % 16 || ldx % 8 || (uintptr_t)w % 16 || (uintptr_t)out % (out_f32 ? 4 : 2)) return MOE_ERR_ALIGN;
-  if (workspace_bytes < moe_w4_linear_workspace_bytes(T, K, N, group)) return MOE_ERR_ALIGN;
+  if (workspace_bytes < moe_w4_linear_workspace_bytes(T, K, N, group) || (uintptr_t)workspace % 256)
+    return MOE_ERR_ALIGN;
+  if (w4_gemm_linear(T))
+    return launch_w4_linear_gemm((const uint16_t*)x, (size_t)ldx, T, (const uint8_t*)w, w4_dims(K, N, group), out,
+                                 (size_t)ldo, out_f32, workspace, dev_status, (cudaStream_t)stream);
   int sms = 0;
   const int r = w4_sms(&sms);
   if (r != MOE_OK) return r;
@@ -403,6 +415,12 @@ extern "C" int moe_experts_w4(const void* x, const int32_t* ids, const float* w,
   f.offset = ws.offset, f.rows = ws.rows, f.list_e = ws.act_e, f.n_list = ws.n_act;
   f.pool = (const uint16_t*)pool, f.e2s = e2s, f.S = S, f.pool_only = 1;
   f.y = ws.y, f.status = dev_status;
+  if (w4_gemm_ffn(n)) {
+    const uint16_t* yh = nullptr;
+    const int32_t* yexp = nullptr;
+    if ((r = launch_ffn_w4_gemm(f, group, ws.ffn, &yh, &yexp, s, nullptr)) != MOE_OK) return r;
+    return launch_w4_combine(yh, yexp, w, ws.pos, T, k, H, out, s);
+  }
   if ((r = launch_ffn_w4(f, group, ws.ffn, ws.ffn_bytes, std::min(n, E), s, nullptr)) != MOE_OK) return r;
   return launch_combine(ws.y, w, ws.pos, ids, nullptr, T, k, H, E, 0, out, nullptr, nullptr, s);
 }

@@ -4,14 +4,19 @@
 // one scale per G = 32, 64 or 128 consecutive inputs of an output column.  Packed:
 //
 //   codes   [Mt][Kb][512 B]  Mt = ceil(N / 16) tiles of 16 output columns, Kb = ceil(K / 64) blocks of
-//                            64 inputs.  A tile block is 32 lanes x 16 bytes: lane 4g + q holds, for
-//                            columns g and g + 8 of the tile, the 16 inputs 32h + 8q + i (h = 0, 1;
-//                            i = 0..7) in four 32-bit words.  Word s covers the four inputs
-//                            k0 = 32(s >> 1) + 8q + 4(s & 1): nibbles 0 and 4 are column g's inputs
-//                            k0, k0 + 1, nibbles 1 and 5 column g + 8's, nibbles 2, 6 and 3, 7 the same
-//                            for k0 + 2, k0 + 3.  That is the A fragment of a 16 x 16 MMA: one 16-byte
-//                            load per lane feeds four of them, and the matching B fragment is 16
-//                            consecutive bytes of a bf16 row.
+//                            64 inputs.  A tile block is 32 chunks of 16 bytes, four for each pair of
+//                            columns g and g + 8 (g = 0..7): chunk 4g + (q + g / 2) % 4 holds the 16
+//                            inputs 32h + 8q + i (h = 0, 1; i = 0..7) in four 32-bit words.  Word s
+//                            covers the four inputs k0 = 32(s >> 1) + 8q + 4(s & 1), k0 + 1, .. k0 + 3:
+//                            bits 2-5 / 18-21 column g's inputs k0 + 2 / k0 + 3, bits 6-9 / 22-25 its
+//                            k0 / k0 + 1; the same 8 bits further up (bits 30 and 31 wrap to 0 and 1)
+//                            column g + 8's.
+//   The two readers this serves: in a warp, lane 4g + q's chunk is its A fragment of four 16 x 16 MMAs
+//   (one coalesced 16-byte load each), whose B fragment is 16 consecutive bytes of a bf16 row; and a
+//   thread that owns one column reads its 64 inputs as four chunks from shared memory, where the
+//   rotation by g / 2 spreads the eight columns over all banks.  A code in bits 6-9 of a half is the
+//   top of an fp16 mantissa: 0x4c00 | code << 6 is 16 + code, so (code - 8) * scale is one fused
+//   multiply-add with -24 * scale, exact for a scale of 8 significant bits.
 //   scales  [Mt][Kg][8 words] Kg groups per tile; word g = (column g, column g + 8) as two fp16, divided
 //                            by the column's multiplier
 //   mult    [Mt * 16] fp32   power of two per column: 2^floor(log2(max |scale|)), 1 where that is 0 or
@@ -25,7 +30,7 @@
 
 #include <cuda_fp16.h>
 
-#include "common.cuh"
+#include "internal.cuh"
 
 namespace moe {
 
@@ -74,14 +79,26 @@ __host__ __device__ inline W4Slab w4_slab(int H, int I, int G) {
   return s;
 }
 
-// Word w of a lane's 16 bytes -> the four bf16x2 registers of a 16 x 16 A fragment, as code - 8:
-// a nibble in the low mantissa bits of 0x4300 is 128 + code, and 128 + code - 136 is exact.
+// The bits of one code inside its column's byte pairs (see above): columns g (hi = 0) and g + 8, input
+// k0 + 2p (the partner k0 + 2p + 1 sits 16 bits further).
+__host__ __device__ constexpr int w4_code_bit(int hi, int p) { return (p ? 2 : 6) + 8 * hi; }
+__host__ __device__ inline uint32_t w4_put(int code, int bit) {
+  const uint32_t c = (uint32_t)code;
+  return bit > 28 ? (c << bit) | (c >> (32 - bit)) : c << bit;
+}
+
+// A lane's chunk within a tile block.
+__device__ __forceinline__ int w4_chunk(int g, int q) { return 4 * g + ((q + (g >> 1)) & 3); }
+
+// Word w of a lane's chunk -> the four bf16x2 registers of a 16 x 16 A fragment, as code - 8: a code in
+// mantissa bits 2-5 of 0x4300 is 128 + 4 code, and a quarter of that minus 40 is exact.
 __device__ __forceinline__ void w4_frag_bf16(uint32_t w, uint32_t (&a)[4]) {
-  const uint32_t off = 0x43084308u;  // 136, 136
+  const uint32_t quarter = 0x3e803e80u, off = 0xc220c220u;  // 0.25, -40
+  const uint32_t r[4] = {w >> 4, __funnelshift_r(w, w, 12), w, w >> 8};  // (g, p 0), (g + 8, p 0), (g, p 1), (g + 8, p 1)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(a[i]) : "r"(v), "r"(off));
+    const uint32_t v = (r[i] & 0x003c003cu) | 0x43004300u;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(a[i]) : "r"(v), "r"(quarter), "r"(off));
   }
 }
 
@@ -91,5 +108,15 @@ __device__ __forceinline__ void mma_bf16_16816(float (&c)[4], const uint32_t (&a
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+
+// The tensor-core path (w4_gemm.cu).
+size_t w4_linear_gemm_ws(int T, int K);
+int launch_w4_linear_gemm(const uint16_t* x, size_t ldx, int T, const uint8_t* w, const W4Dims& d, void* out,
+                          size_t ldo, int out_f32, void* ws, int32_t* status, cudaStream_t s);
+size_t w4_ffn_gemm_ws(size_t n, int H, int I, bool yh);
+int launch_ffn_w4_gemm(const FfnArgs& f, int group, void* ws, const uint16_t** yh, const int32_t** yexp,
+                       cudaStream_t s, Prof* prof);
+int launch_w4_combine(const uint16_t* yh, const int32_t* yexp, const float* w, const int32_t* pos, int T, int k, int H,
+                      void* out, cudaStream_t s);
 
 }  // namespace moe

@@ -90,16 +90,15 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const W4PackArgs a) {
   uint32_t* out = reinterpret_cast<uint32_t*>(dst);
   for (int i = threadIdx.x; i < nt * nb * 128; i += 256) {
     const int wd = i & 127, b = (i >> 7) % nb, t = (i >> 7) / nb;
-    const int lane = wd >> 2, s = wd & 3, g = lane >> 2, q = lane & 3;
+    const int ch = wd >> 2, s = wd & 3, g = ch >> 2, q = (ch - (g >> 1)) & 3;
     const int k = b * 64 + 32 * (s >> 1) + 8 * q + 4 * (s & 1), c = t * 16 + g;
     uint32_t v = 0;
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int nib = 2 * p + h;
-        v |= (uint32_t)sc[k + 2 * p][c + 8 * h] << (4 * nib);
-        v |= (uint32_t)sc[k + 2 * p + 1][c + 8 * h] << (4 * nib + 16);
+        const int bit = w4_code_bit(h, p);
+        v |= w4_put(sc[k + 2 * p][c + 8 * h], bit) | w4_put(sc[k + 2 * p + 1][c + 8 * h], (bit + 16) & 31);
       }
     out[((size_t)(n0 / 16 + t) * d.Kb + k0 / 64 + b) * 128 + wd] = v;
   }
@@ -130,9 +129,10 @@ __global__ void __launch_bounds__(128) w4_scale_kernel(const W4PackArgs a) {
     for (int b = i * d.G / 32; b < (i + 1) * d.G / 32 && b < d.Kb * 2; ++b)  // blocks of 32 inputs
       for (int q = 0; q < 4; ++q)
         for (int s = 0; s < 2; ++s) {
-          const uint32_t w = words[(size_t)(b >> 1) * 128 + (4 * g + q) * 4 + 2 * (b & 1) + s] >> (4 * h);
-          const int c0 = (int)(w & 15) - 8, c1 = (int)((w >> 8) & 15) - 8, c2 = (int)((w >> 16) & 15) - 8,
-                    c3 = (int)((w >> 24) & 15) - 8;
+          const uint32_t v = words[(size_t)(b >> 1) * 128 + w4_chunk(g, q) * 4 + 2 * (b & 1) + s];
+          const uint32_t w = __funnelshift_r(v, v, 8 * h);
+          const int c0 = (int)((w >> 6) & 15) - 8, c1 = (int)((w >> 22) & 15) - 8, c2 = (int)((w >> 2) & 15) - 8,
+                    c3 = (int)((w >> 18) & 15) - 8;
           sq += c0 * c0 + c1 * c1 + c2 * c2 + c3 * c3;
         }
     const float r = raw * f0 * f1;
