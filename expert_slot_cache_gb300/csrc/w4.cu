@@ -18,14 +18,16 @@ constexpr int kW4Threads = 32 * kW4Warps;
 
 // One matrix's view for a tile: lane's code words, the tile's scale words, the multipliers.
 struct W4Tile {
-  const uint4* codes;      // + kb * 32
-  const uint32_t* scales;  // + kg * 8
+  const uint4* codes;      // + kb * 32 * mates
+  const uint32_t* scales;  // + kg * 8 * mates
+  int mates;
 };
 
 __device__ __forceinline__ W4Tile w4_tile(const uint8_t* m, const W4Dims& d, int tile, int lane) {
   W4Tile t;
-  t.codes = reinterpret_cast<const uint4*>(m) + (size_t)tile * d.Kb * 32 + w4_chunk(lane >> 2, lane & 3);
-  t.scales = reinterpret_cast<const uint32_t*>(m + d.scales) + (size_t)tile * d.Kg * 8 + (lane >> 2);
+  t.codes = reinterpret_cast<const uint4*>(m) + w4_code_at(d, tile, 0) * 32 + w4_chunk(lane >> 2, lane & 3);
+  t.scales = reinterpret_cast<const uint32_t*>(m + d.scales) + w4_scale_at(d, tile, 0) * 8 + (lane >> 2);
+  t.mates = w4_mates(d, tile);
   return t;
 }
 
@@ -39,7 +41,7 @@ __device__ __forceinline__ void w4_accumulate(const W4Tile (&t)[NM], const uint1
   for (int kb = kb0; kb < kb1; ++kb) {
     uint4 w[NM];
 #pragma unroll
-    for (int m = 0; m < NM; ++m) w[m] = ldg_stream(t[m].codes + (size_t)kb * 32);
+    for (int m = 0; m < NM; ++m) w[m] = ldg_stream(t[m].codes + (size_t)kb * (32 * t[0].mates));
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int k = kb * 64 + 32 * h;
@@ -56,7 +58,7 @@ __device__ __forceinline__ void w4_accumulate(const W4Tile (&t)[NM], const uint1
         uint32_t a0[4], a1[4];
         w4_frag_bf16(h ? w[m].z : w[m].x, a0);
         w4_frag_bf16(h ? w[m].w : w[m].y, a1);
-        const uint32_t sw = __ldg(t[m].scales + (size_t)kg * 8);
+        const uint32_t sw = __ldg(t[m].scales + (size_t)kg * (8 * t[0].mates));
         const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&sw));
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {

@@ -3,8 +3,10 @@
 // A K x N matrix W (y = x W) holds W[k][n] = (code[k][n] - 8) * scale[k / G][n] with codes 0..15 and
 // one scale per G = 32, 64 or 128 consecutive inputs of an output column.  Packed:
 //
-//   codes   [Mt][Kb][512 B]  Mt = ceil(N / 16) tiles of 16 output columns, Kb = ceil(K / 64) blocks of
-//                            64 inputs.  A tile block is 32 chunks of 16 bytes, four for each pair of
+//   codes   [Mt / 8][Kb][8][512 B]  Mt = ceil(N / 16) tiles of 16 output columns, Kb = ceil(K / 64)
+//                            blocks of 64 inputs; eight tiles' blocks are neighbours (the last tiles, fewer
+//                            than eight, among themselves), so 128 columns x 64 inputs are one copy of
+//                            4 KB.  A tile block is 32 chunks of 16 bytes, four for each pair of
 //                            columns g and g + 8 (g = 0..7): chunk 4g + (q + g / 2) % 4 holds the 16
 //                            inputs 32h + 8q + i (h = 0, 1; i = 0..7) in four 32-bit words.  Word s
 //                            covers the four inputs k0 = 32(s >> 1) + 8q + 4(s & 1), k0 + 1, .. k0 + 3:
@@ -17,8 +19,8 @@
 //   rotation by g / 2 spreads the eight columns over all banks.  A code in bits 6-9 of a half is the
 //   top of an fp16 mantissa: 0x4c00 | code << 6 is 16 + code, so (code - 8) * scale is one fused
 //   multiply-add with -24 * scale, exact for a scale of 8 significant bits.
-//   scales  [Mt][Kg][8 words] Kg groups per tile; word g = (column g, column g + 8) as two fp16, divided
-//                            by the column's multiplier
+//   scales  [Mt / 8][Kg][8][8 words] Kg groups, neighbours as for the codes; word g = (column g, column
+//                            g + 8) of the tile as two fp16, divided by the column's multiplier
 //   mult    [Mt * 16] fp32   power of two per column: 2^floor(log2(max |scale|)), 1 where that is 0 or
 //                            not finite.  fp16 scales below 2 then keep every bit of a bf16 scale down
 //                            to 2^-14 of the column's largest one, and (code - 8) * scale has at most 11
@@ -53,6 +55,18 @@ __host__ __device__ inline W4Dims w4_dims(int K, int N, int G) {
   d.meta = d.mult + (size_t)d.Mt * 64;
   d.bytes = d.meta + 16;
   return d;
+}
+
+// Tiles that lie together with tile mt, and the place of its block kb (512 B units) and group kg (32 B units).
+__host__ __device__ __forceinline__ int w4_mates(const W4Dims& d, int mt) {
+  const int left = d.Mt - (mt & ~7);
+  return left < 8 ? left : 8;
+}
+__host__ __device__ __forceinline__ size_t w4_code_at(const W4Dims& d, int mt, int kb) {
+  return (size_t)(mt & ~7) * d.Kb + (size_t)kb * w4_mates(d, mt) + (mt & 7);
+}
+__host__ __device__ __forceinline__ size_t w4_scale_at(const W4Dims& d, int mt, int kg) {
+  return (size_t)(mt & ~7) * d.Kg + (size_t)kg * w4_mates(d, mt) + (mt & 7);
 }
 
 inline bool w4_group_ok(int G) { return G == 32 || G == 64 || G == 128; }

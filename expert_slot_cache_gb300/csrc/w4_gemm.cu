@@ -14,8 +14,8 @@
 // bound; typical values are 2^-11 (h) and 2^-16 (y) of it.  So x (8 bits) is exact and only h and, on its
 // way to the combine, y are rounded, to 11 bits.
 //
-// Warps: 0 TMA producer, 1 TMEM allocation and MMA issue (one thread), 2-9 workers (dequantise, then
-// drain the accumulators).  TMEM: 2 x 128 accumulator columns, 4 weight stages of 2 x 32 columns.
+// Warps: 0 TMA producer, 1 TMEM allocation and MMA issue (one thread), 2-17 workers (two sets that
+// dequantise stages in turn, then all drain the accumulators).  TMEM: 2 x 128 accumulator columns, 4 weight stages of 2 x 32 columns.
 #include <limits.h>
 
 #include <algorithm>
@@ -31,11 +31,12 @@ constexpr int kGN = 128;       // rows per tile
 constexpr int kGK = 64;        // inputs per stage
 constexpr int kGRing = 6;      // shared-memory stages
 constexpr int kGAStages = 4;   // TMEM weight stages
-constexpr int kGWorkers = 8;   // worker warps
+constexpr int kGSet = 8;        // worker warps of a stage
+constexpr int kGWorkers = 16;  // worker warps: two sets, taking stages in turn
 constexpr int kGThreads = 64 + 32 * kGWorkers;
 constexpr int kGXBytes = kGN * kGK * 2;
-constexpr int kGCodeBytes = 2 * 8 * 512;       // two blocks of 8 tiles x 512 B
-constexpr int kGScaleBytes = 2 * 8 * 64;       // up to two groups of 32 B per tile
+constexpr int kGCodeBytes = 2 * 4096;          // 128 features x 64 codes, twice
+constexpr int kGScaleBytes = 2 * 512;          // up to two groups of 128 fp16 scales, twice
 constexpr int kGStageBytes = kGXBytes + kGCodeBytes + kGScaleBytes;
 constexpr int kGEpiBytes = 32 * 32 * 4;        // staging per worker warp
 constexpr uint32_t kGTmemCols = 512;
@@ -183,10 +184,10 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
       mbar_init(&xfull[s], 1);
       mbar_init(&xempty[s], 1);
       mbar_init(&wfull[s], 1);
-      mbar_init(&wempty[s], kGWorkers);
+      mbar_init(&wempty[s], kGSet);
     }
     for (int s = 0; s < kGAStages; ++s) {
-      mbar_init(&afull[s], kGWorkers);
+      mbar_init(&afull[s], kGSet);
       mbar_init(&aempty[s], 1);
     }
     mbar_init(tfull, 1);
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   volatile int* abort_flag = &s_abort;
   // a wait that gives up ends the work of every role; the barriers are then no longer waited for
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!*abort_flag && !mbar_wait(bar, parity)) {
+    if (!mbar_try_wait(bar, parity) && !*abort_flag && !mbar_wait(bar, parity)) {
       *abort_flag = 1;
       set_status(a.status, MOE_DEV_TIMEOUT);
     }
@@ -240,10 +241,8 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
       const int groups = d.G == 32 ? 2 : 1;
       // the tiles of 16 columns that exist, per block
       const int nm0 = min(8, d.Mt - w4g_mt0<kMode>(ti.ft, 0)), nm1 = max(0, min(8, d.Mt - w4g_mt0<kMode>(ti.ft, 1)));
-      const int b = (lane >> 3) & 1, m = lane & 7;  // lanes 0-15: codes of (block, tile); lanes 16-31: its scales
-      const uint8_t* mat = ti.base + (b ? a.mat1 : a.mat0);
-      const int mt = w4g_mt0<kMode>(ti.ft, b) + m;
-      const bool mine = m < (b ? nm1 : nm0);
+      const uint8_t* mat[2] = {ti.base + a.mat0, ti.base + a.mat1};
+      const int mt[2] = {w4g_mt0<kMode>(ti.ft, 0), w4g_mt0<kMode>(ti.ft, 1)}, nm[2] = {nm0, nm1};
       const uint32_t wbytes = (uint32_t)(nm0 + nm1) * (512 + 32 * groups);
       for (int kb = 0; kb < nkb; ++kb, ++it) {
         const uint32_t s = it % kGRing, use = it / kGRing;
@@ -258,16 +257,14 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
           mbar_expect_tx(&xfull[s], kGXBytes);
           tma_load_3d(xs + s * kGXBytes, &mapX, &xfull[s], kb * kGK, ti.row0, 0);
         }
-        __syncwarp();
-        if (mine) {
-          if (lane < 16) {
-            bulk_load(cs + s * kGCodeBytes + (b * 8 + m) * 512, mat + ((size_t)mt * d.Kb + kb) * 512, 512, &wfull[s]);
-          } else {
-            const int kg = kb * kGK / d.G;
-            bulk_load(ss + s * kGScaleBytes + (b * 8 + m) * 64, mat + d.scales + ((size_t)mt * d.Kg + kg) * 32,
-                      32 * groups, &wfull[s]);
+        if (lane == 0)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            if (nm[b] == 0) continue;
+            bulk_load(cs + s * kGCodeBytes + b * 4096, mat[b] + w4_code_at(d, mt[b], kb) * 512, 512 * nm[b], &wfull[s]);
+            bulk_load(ss + s * kGScaleBytes + b * 512, mat[b] + d.scales + w4_scale_at(d, mt[b], kb * kGK / d.G) * 32,
+                      32 * nm[b] * groups, &wfull[s]);
           }
-        }
         __syncwarp();
       }
     }
@@ -310,7 +307,8 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
       mbar_wait(done, 0);
     }
   } else {
-    const int q = warp & 3, b = (warp - 2) >> 2;  // TMEM lane quarter; block (dequantising), row half (draining)
+    // TMEM lane quarter; block and set (dequantising); 32-row chunk of the tile (draining)
+    const int q = warp & 3, b = ((warp - 2) >> 2) & 1, set = (warp - 2) >> 3, chunk = (warp - 2) >> 2;
     const int r = 32 * q + lane, g = r & 7, hi = (r >> 3) & 1;
     const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
     const int rot = (g >> 1) & 3;
@@ -318,15 +316,17 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     uint32_t it = 0, tc = 0;
     for (int t = blockIdx.x; t < total && !__any_sync(MOE_FULL_MASK, *abort_flag); t += gridDim.x, ++tc) {
       const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
+      const int nm = max(1, min(8, d.Mt - w4g_mt0<kMode>(ti.ft, b)));
       for (int kb = 0; kb < nkb; ++kb, ++it) {
+        if ((it & 1) != (uint32_t)set) continue;
         const uint32_t s = it % kGRing, as = it % kGAStages;
         wait(&wfull[s], (it / kGRing) & 1u);
         const unsigned char* code = cs + s * kGCodeBytes + b * 4096 + (r >> 4) * 512 + g * 64;
-        const __half* sp = reinterpret_cast<const __half*>(ss + s * kGScaleBytes + (b * 8 + (r >> 4)) * 64 + g * 4) + hi;
+        const __half* sp = reinterpret_cast<const __half*>(ss + s * kGScaleBytes + b * 512 + (r >> 4) * 32 + g * 4) + hi;
         uint4 c[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) c[j] = *reinterpret_cast<const uint4*>(code + ((j + rot) & 3) * 16);
-        const __half2 s0 = __half2half2(sp[0]), s1 = d.G == 32 ? __half2half2(sp[16]) : s0;
+        const __half2 s0 = __half2half2(sp[0]), s1 = d.G == 32 ? __half2half2(sp[16 * nm]) : s0;
         const __half2 m24 = __float2half2_rn(-24.f), n0 = __hmul2(s0, m24), n1 = __hmul2(s1, m24);
         uint32_t o[32];
 #pragma unroll
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
         __syncwarp();
         if (lane == 0) mbar_arrive(&afull[as]);
       }
-      // drain: this warp's 32 features of both blocks, rows 64 b .. 64 b + 63 of the tile
+      // drain: this warp's 32 features of both blocks, 32 rows of the tile
       wait(tfull, tc & 1u);
       tc_fence_after();
       const bool store = !*abort_flag;
@@ -364,8 +364,8 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
         const float* mu = reinterpret_cast<const float*>(ti.base + a.mat1 + d.mult);
         const float cg = f < d.N ? mg[f] : 0.f, cu = f < d.N ? mu[f] : 0.f;
         uint16_t* st = reinterpret_cast<uint16_t*>(stage);
-#pragma unroll 1
-        for (int c = 2 * b; c < 2 * b + 2 && 32 * c < ti.ntok; ++c) {
+        const int c = chunk;
+        if (32 * c < ti.ntok) {
           float gv[32], uv[32];
           tmem_ld32(tmem + lane_addr + 32 * c, gv);
           tmem_ld32(tmem + lane_addr + kGN + 32 * c, uv);
@@ -398,8 +398,8 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
           if (f0 >= d.N) break;
           float cm = f < d.N ? mc[f] : 0.f;
           if (kMode == kDown && a.yh) cm = ldexpf(cm, -w4_y_exp(ti.base + a.mat0, d));
-#pragma unroll 1
-          for (int c = 2 * b; c < 2 * b + 2 && 32 * c < ti.ntok; ++c) {
+          const int c = chunk;
+          if (32 * c < ti.ntok) {
             float v[32];
             tmem_ld32(tmem + lane_addr + kGN * blk + 32 * c, v);
             const int tok = 32 * c + lane;
@@ -419,6 +419,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
                   else reinterpret_cast<uint16_t*>(a.out)[at] = f32_to_bf16(o);
                 }
               }
+              __syncwarp();
               continue;
             }
             const bool f32 = kMode == kLinear ? a.out_f32 != 0 : a.yh == nullptr;

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const W4PackArgs a) {
     for (int i = threadIdx.x; i < gpc * kPackCols; i += 256) {
       const int g = k0 / d.G + i / kPackCols, n = n0 + i % kPackCols;
       if (g < d.Kg && n < d.Mt * 16)
-        dsc[((size_t)(n >> 4) * d.Kg + g) * 16 + (n & 7) * 2 + ((n >> 3) & 1)] =
+        dsc[w4_scale_at(d, n >> 4, g) * 16 + (n & 7) * 2 + ((n >> 3) & 1)] =
             g < src_groups(d) && n < d.N ? ss[(size_t)g * d.N + n] : 0;
     }
   } else {
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const W4PackArgs a) {
         }
         sc[k - k0][c] = (uint8_t)code;
       }
-      if (n < d.Mt * 16) dsc[((size_t)(n >> 4) * d.Kg + g) * 16 + (n & 7) * 2 + ((n >> 3) & 1)] = sb;
+      if (n < d.Mt * 16) dsc[w4_scale_at(d, n >> 4, g) * 16 + (n & 7) * 2 + ((n >> 3) & 1)] = sb;
     }
   }
   __syncthreads();
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const W4PackArgs a) {
         const int bit = w4_code_bit(h, p);
         v |= w4_put(sc[k + 2 * p][c + 8 * h], bit) | w4_put(sc[k + 2 * p + 1][c + 8 * h], (bit + 16) & 31);
       }
-    out[((size_t)(n0 / 16 + t) * d.Kb + k0 / 64 + b) * 128 + wd] = v;
+    out[w4_code_at(d, n0 / 16 + t, k0 / 64 + b) * 128 + wd] = v;
   }
 }
 
@@ -115,21 +115,22 @@ __global__ void __launch_bounds__(128) w4_scale_kernel(const W4PackArgs a) {
   if (n >= d.Mt * 16) return;
   uint8_t* dst = a.dst + item * a.dst_item + m * a.d[0].bytes;
   const int tile = n >> 4, g = n & 7, h = (n >> 3) & 1;
-  uint16_t* sc = reinterpret_cast<uint16_t*>(dst + d.scales) + (size_t)tile * d.Kg * 16 + g * 2 + h;
+  uint16_t* sc = reinterpret_cast<uint16_t*>(dst + d.scales) + g * 2 + h;
   float amax = 0.f;
-  for (int i = 0; i < d.Kg; ++i) amax = fmaxf(amax, fabsf(bf16_to_f32(sc[i * 16])));
+  for (int i = 0; i < d.Kg; ++i) amax = fmaxf(amax, fabsf(bf16_to_f32(sc[w4_scale_at(d, tile, i) * 16])));
   const int e = amax > 0.f && amax < INFINITY ? ilogbf(amax) : 0;
   // 2^-e as two factors, so that a subnormal largest scale does not overflow it
   const float f0 = ldexpf(1.f, -e / 2), f1 = ldexpf(1.f, -(e - e / 2));
-  const uint32_t* words = reinterpret_cast<const uint32_t*>(dst) + (size_t)tile * d.Kb * 128;
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(dst);
   float norm = 0.f;
   for (int i = 0; i < d.Kg; ++i) {
-    const float raw = bf16_to_f32(sc[i * 16]);
+    const size_t at = w4_scale_at(d, tile, i) * 16;
+    const float raw = bf16_to_f32(sc[at]);
     int sq = 0;  // sum of (code - 8)^2 of the group: at most 128 * 64
     for (int b = i * d.G / 32; b < (i + 1) * d.G / 32 && b < d.Kb * 2; ++b)  // blocks of 32 inputs
       for (int q = 0; q < 4; ++q)
         for (int s = 0; s < 2; ++s) {
-          const uint32_t v = words[(size_t)(b >> 1) * 128 + w4_chunk(g, q) * 4 + 2 * (b & 1) + s];
+          const uint32_t v = words[w4_code_at(d, tile, b >> 1) * 128 + w4_chunk(g, q) * 4 + 2 * (b & 1) + s];
           const uint32_t w = __funnelshift_r(v, v, 8 * h);
           const int c0 = (int)((w >> 6) & 15) - 8, c1 = (int)((w >> 22) & 15) - 8, c2 = (int)((w >> 2) & 15) - 8,
                     c3 = (int)((w >> 18) & 15) - 8;
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(128) w4_scale_kernel(const W4PackArgs a) {
         }
     const float r = raw * f0 * f1;
     norm = fmaf(r * r, (float)sq, norm);
-    sc[i * 16] = __half_as_ushort(__float2half_rn(r));
+    sc[at] = __half_as_ushort(__float2half_rn(r));
   }
   reinterpret_cast<float*>(dst + d.mult)[n] = ldexpf(1.f, e);
   // 1e-3 up: the sum above is rounded, the bound must not be below the norm
