@@ -29,15 +29,17 @@ namespace moe {
 constexpr int kGM = 128;       // features per accumulator
 constexpr int kGN = 128;       // rows per tile
 constexpr int kGK = 64;        // inputs per stage
-constexpr int kGRing = 6;      // shared-memory stages
+constexpr int kGXRing = 5;     // stages of rows in shared memory
+constexpr int kGChunk = 4;     // stages of codes that are copied together
+constexpr int kGWRing = 2;     // chunks of codes in shared memory
 constexpr int kGAStages = 4;   // TMEM weight stages
-constexpr int kGSet = 8;        // worker warps of a stage
+constexpr int kGSet = 8;       // worker warps of a stage
 constexpr int kGWorkers = 16;  // worker warps: two sets, taking stages in turn
 constexpr int kGThreads = 64 + 32 * kGWorkers;
 constexpr int kGXBytes = kGN * kGK * 2;
-constexpr int kGCodeBytes = 2 * 4096;          // 128 features x 64 codes, twice
-constexpr int kGScaleBytes = 2 * 512;          // up to two groups of 128 fp16 scales, twice
-constexpr int kGStageBytes = kGXBytes + kGCodeBytes + kGScaleBytes;
+constexpr int kGCodeBlock = kGChunk * 4096;    // a chunk's codes of 128 features
+constexpr int kGScaleBlock = kGChunk * 2 * 256;  // its fp16 scales (two groups a stage at most)
+constexpr int kGWBytes = 2 * (kGCodeBlock + kGScaleBlock);
 constexpr int kGEpiBytes = 32 * 32 * 4;        // staging per worker warp
 constexpr uint32_t kGTmemCols = 512;
 constexpr uint32_t kGACol = 2 * kGN;           // first weight column
@@ -65,6 +67,14 @@ struct W4GemmArgs {
   size_t ldo;
   int out_f32;
 };
+
+// One lane of the (converged) warp.  The loops that issue copies and MMAs are run by whole warps, so that
+// their operands stay in uniform registers; only the issue itself is one lane's.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
 
 // D[tmem] (+)= A[tmem] x B[smem].
 __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -157,15 +167,14 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   extern __shared__ __align__(16) unsigned char gsm_raw[];
   unsigned char* sm =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(gsm_raw) + 1023) & ~uintptr_t(1023));
-  unsigned char* xs = sm;                                    // [ring][16 KB]
-  unsigned char* cs = sm + kGRing * kGXBytes;                // [ring][8 KB]
-  unsigned char* ss = cs + kGRing * kGCodeBytes;             // [ring][1 KB]
-  unsigned char* epi = ss + kGRing * kGScaleBytes;           // [workers][4 KB]
+  unsigned char* xs = sm;                             // [ring][16 KB]
+  unsigned char* wsm = sm + kGXRing * kGXBytes;       // [ring][codes of both blocks | scales of both blocks]
+  unsigned char* epi = wsm + kGWRing * kGWBytes;      // [workers][4 KB]
   uint64_t* xfull = reinterpret_cast<uint64_t*>(epi + kGWorkers * kGEpiBytes);
-  uint64_t* xempty = xfull + kGRing;
-  uint64_t* wfull = xempty + kGRing;
-  uint64_t* wempty = wfull + kGRing;
-  uint64_t* afull = wempty + kGRing;
+  uint64_t* xempty = xfull + kGXRing;
+  uint64_t* wfull = xempty + kGXRing;
+  uint64_t* wempty = wfull + kGWRing;
+  uint64_t* afull = wempty + kGWRing;
   uint64_t* aempty = afull + kGAStages;
   uint64_t* tfull = aempty + kGAStages;
   uint64_t* tempty = tfull + 1;
@@ -180,11 +189,13 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   int nl = 0, total;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kGRing; ++s) {
+    for (int s = 0; s < kGXRing; ++s) {
       mbar_init(&xfull[s], 1);
       mbar_init(&xempty[s], 1);
+    }
+    for (int s = 0; s < kGWRing; ++s) {
       mbar_init(&wfull[s], 1);
-      mbar_init(&wempty[s], kGSet);
+      mbar_init(&wempty[s], kGWorkers);
     }
     for (int s = 0; s < kGAStages; ++s) {
       mbar_init(&afull[s], kGSet);
@@ -234,78 +245,86 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   };
 
   if (warp == 0) {
-    uint32_t it = 0;
+    uint32_t xi = 0, wi = 0;  // stages of rows and chunks of codes issued
     bool dead = false;
+    const bool lead = elect_one();
     for (int t = blockIdx.x; t < total && !dead; t += gridDim.x) {
       const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
-      const int groups = d.G == 32 ? 2 : 1;
+      const int mt0 = w4g_mt0<kMode>(ti.ft, 0), mt1 = w4g_mt0<kMode>(ti.ft, 1);
       // the tiles of 16 columns that exist, per block
-      const int nm0 = min(8, d.Mt - w4g_mt0<kMode>(ti.ft, 0)), nm1 = max(0, min(8, d.Mt - w4g_mt0<kMode>(ti.ft, 1)));
-      const uint8_t* mat[2] = {ti.base + a.mat0, ti.base + a.mat1};
-      const int mt[2] = {w4g_mt0<kMode>(ti.ft, 0), w4g_mt0<kMode>(ti.ft, 1)}, nm[2] = {nm0, nm1};
-      const uint32_t wbytes = (uint32_t)(nm0 + nm1) * (512 + 32 * groups);
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const uint32_t s = it % kGRing, use = it / kGRing;
-        if (use > 0) {
-          wait(&xempty[s], (use - 1) & 1u);
-          wait(&wempty[s], (use - 1) & 1u);
+      const uint32_t nm0 = min(8, d.Mt - mt0), nm1 = max(0, min(8, d.Mt - mt1));
+      const uint8_t *m0 = ti.base + a.mat0, *m1 = ti.base + a.mat1;
+      for (int kb = 0; kb < nkb; ++kb, ++xi) {
+        if (kb % kGChunk == 0) {
+          const uint32_t s = wi % kGWRing, use = wi / kGWRing, nb = min(kGChunk, nkb - kb);
+          const uint32_t ng = d.G == 128 ? (nb + 1) / 2 : d.G == 64 ? nb : 2 * nb;
+          const int kg = kb * kGK / d.G;
+          if (use > 0) wait(&wempty[s], (use - 1) & 1u);
+          dead = __any_sync(MOE_FULL_MASK, *abort_flag);
+          if (dead) break;
+          unsigned char* dst = wsm + s * kGWBytes;
+          if (lead) {
+            mbar_expect_tx(&wfull[s], (nm0 + nm1) * (512 * nb + 32 * ng));
+            bulk_load(dst, m0 + w4_code_at(d, mt0, kb) * 512, nm0 * 512 * nb, &wfull[s]);
+            bulk_load(dst + 2 * kGCodeBlock, m0 + d.scales + w4_scale_at(d, mt0, kg) * 32, nm0 * 32 * ng, &wfull[s]);
+            if (nm1 > 0) {
+              bulk_load(dst + kGCodeBlock, m1 + w4_code_at(d, mt1, kb) * 512, nm1 * 512 * nb, &wfull[s]);
+              bulk_load(dst + 2 * kGCodeBlock + kGScaleBlock, m1 + d.scales + w4_scale_at(d, mt1, kg) * 32,
+                        nm1 * 32 * ng, &wfull[s]);
+            }
+          }
+          __syncwarp();
+          ++wi;
         }
+        const uint32_t s = xi % kGXRing, use = xi / kGXRing;
+        if (use > 0) wait(&xempty[s], (use - 1) & 1u);
         dead = __any_sync(MOE_FULL_MASK, *abort_flag);
         if (dead) break;
-        if (lane == 0) {
-          mbar_expect_tx(&wfull[s], wbytes);
+        if (lead) {
           mbar_expect_tx(&xfull[s], kGXBytes);
           tma_load_3d(xs + s * kGXBytes, &mapX, &xfull[s], kb * kGK, ti.row0, 0);
         }
-        if (lane == 0)
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            if (nm[b] == 0) continue;
-            bulk_load(cs + s * kGCodeBytes + b * 4096, mat[b] + w4_code_at(d, mt[b], kb) * 512, 512 * nm[b], &wfull[s]);
-            bulk_load(ss + s * kGScaleBytes + b * 512, mat[b] + d.scales + w4_scale_at(d, mt[b], kb * kGK / d.G) * 32,
-                      32 * nm[b] * groups, &wfull[s]);
-          }
         __syncwarp();
       }
     }
     // after a timeout: let every copy land before the CTA can exit
-    if (dead)
-      for (uint32_t j = it > kGRing ? it - kGRing : 0; j < it; ++j) {
-        mbar_wait(&xfull[j % kGRing], (j / kGRing) & 1u);
-        mbar_wait(&wfull[j % kGRing], (j / kGRing) & 1u);
-      }
+    if (dead) {
+      for (uint32_t j = xi > kGXRing ? xi - kGXRing : 0; j < xi; ++j) mbar_wait(&xfull[j % kGXRing], (j / kGXRing) & 1u);
+      for (uint32_t j = wi > kGWRing ? wi - kGWRing : 0; j < wi; ++j) mbar_wait(&wfull[j % kGWRing], (j / kGWRing) & 1u);
+    }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint64_t bd0 = smem_desc_l(smem_u32(xs), 16, 1024, kLayoutSw128);
-      uint32_t it = 0, tc = 0;
-      for (int t = blockIdx.x; t < total && !*abort_flag; t += gridDim.x, ++tc) {
-        const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
-        const uint32_t idesc = idesc_f16(kGM, (ti.ntok + 15) & ~15);
-        const bool two = kMode == kGateUp || w4g_mt0<kMode>(ti.ft, 1) < d.Mt;
-        if (tc > 0) wait(tempty, (tc - 1) & 1u);
+    const uint64_t bd0 = smem_desc_l(smem_u32(xs), 16, 1024, kLayoutSw128);
+    const bool lead = elect_one();
+    uint32_t it = 0, tc = 0;
+    for (int t = blockIdx.x; t < total && !__any_sync(MOE_FULL_MASK, *abort_flag); t += gridDim.x, ++tc) {
+      const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
+      const uint32_t idesc = idesc_f16(kGM, (ti.ntok + 15) & ~15);
+      const bool two = kMode == kGateUp || w4g_mt0<kMode>(ti.ft, 1) < d.Mt;
+      if (tc > 0) wait(tempty, (tc - 1) & 1u);
+      tc_fence_after();
+      for (int kb = 0; kb < nkb; ++kb, ++it) {
+        const uint32_t s = it % kGXRing, as = it % kGAStages;
+        wait(&xfull[s], (it / kGXRing) & 1u);
+        wait(&afull[as], (it / kGAStages) & 1u);
         tc_fence_after();
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const uint32_t s = it % kGRing, as = it % kGAStages;
-          wait(&xfull[s], (it / kGRing) & 1u);
-          wait(&afull[as], (it / kGAStages) & 1u);
-          tc_fence_after();
-          if (!*abort_flag) {
-            const uint32_t ac = tmem + kGACol + as * 64;
-            const uint64_t bd = bd0 + (uint64_t)(s * (kGXBytes >> 4));
+        const uint32_t ac = tmem + kGACol + as * 64;
+        const uint64_t bd = bd0 + (uint64_t)(s * (kGXBytes >> 4));
+        if (lead) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) umma_f16_ts(tmem, ac + 8 * k, bd + 2 * k, idesc, kb > 0 || k > 0);
-            if (two)
+          for (int k = 0; k < 4; ++k) umma_f16_ts(tmem, ac + 8 * k, bd + 2 * k, idesc, kb > 0 || k > 0);
+          if (two)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) umma_f16_ts(tmem + kGN, ac + 32 + 8 * k, bd + 2 * k, idesc, kb > 0 || k > 0);
-          }
+            for (int k = 0; k < 4; ++k) umma_f16_ts(tmem + kGN, ac + 32 + 8 * k, bd + 2 * k, idesc, kb > 0 || k > 0);
           umma_commit(&xempty[s]);
           umma_commit(&aempty[as]);
+          if (kb + 1 == nkb) umma_commit(tfull);
         }
-        umma_commit(tfull);
+        __syncwarp();
       }
-      umma_commit(done);
-      mbar_wait(done, 0);
     }
+    if (lead) umma_commit(done);
+    __syncwarp();
+    mbar_wait(done, 0);
   } else {
     // TMEM lane quarter; block and set (dequantising); 32-row chunk of the tile (draining)
     const int q = warp & 3, b = ((warp - 2) >> 2) & 1, set = (warp - 2) >> 3, chunk = (warp - 2) >> 2;
@@ -313,16 +332,29 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
     const int rot = (g >> 1) & 3;
     unsigned char* stage = epi + (warp - 2) * kGEpiBytes;
-    uint32_t it = 0, tc = 0;
+    uint32_t it = 0, wi = 0, tc = 0;
     for (int t = blockIdx.x; t < total && !__any_sync(MOE_FULL_MASK, *abort_flag); t += gridDim.x, ++tc) {
       const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
       const int nm = max(1, min(8, d.Mt - w4g_mt0<kMode>(ti.ft, b)));
       for (int kb = 0; kb < nkb; ++kb, ++it) {
-        if ((it & 1) != (uint32_t)set) continue;
-        const uint32_t s = it % kGRing, as = it % kGAStages;
-        wait(&wfull[s], (it / kGRing) & 1u);
-        const unsigned char* code = cs + s * kGCodeBytes + b * 4096 + (r >> 4) * 512 + g * 64;
-        const __half* sp = reinterpret_cast<const __half*>(ss + s * kGScaleBytes + b * 512 + (r >> 4) * 32 + g * 4) + hi;
+        const int j4 = kb % kGChunk;
+        const uint32_t ws = wi % kGWRing;
+        if (j4 == 0) wait(&wfull[ws], (wi / kGWRing) & 1u);
+        const bool last = j4 == kGChunk - 1 || kb + 1 == nkb;
+        if (last) ++wi;
+        if ((it & 1) != (uint32_t)set) {
+          if (last) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&wempty[ws]);
+          }
+          continue;
+        }
+        const uint32_t as = it % kGAStages;
+        const unsigned char* wst = wsm + ws * kGWBytes;
+        const unsigned char* code = wst + b * kGCodeBlock + (j4 * nm + (r >> 4)) * 512 + g * 64;
+        const int gi = d.G == 128 ? j4 >> 1 : d.G == 64 ? j4 : 2 * j4;
+        const __half* sp =
+            reinterpret_cast<const __half*>(wst + 2 * kGCodeBlock + b * kGScaleBlock + (gi * nm + (r >> 4)) * 32 + g * 4) + hi;
         uint4 c[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) c[j] = *reinterpret_cast<const uint4*>(code + ((j + rot) & 3) * 16);
@@ -344,8 +376,10 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
             o[col + 1] = *reinterpret_cast<const uint32_t*>(&h1);
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&wempty[s]);
+        if (last) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&wempty[ws]);
+        }
         if (it >= kGAStages) wait(&aempty[as], (it / kGAStages - 1) & 1u);
         tc_fence_after();
         tmem_st32(tmem + lane_addr + kGACol + as * 64 + b * 32, o);
@@ -615,7 +649,9 @@ __global__ void __launch_bounds__(128) w4_combine_kernel(const uint16_t* __restr
   *reinterpret_cast<uint4*>(out + (size_t)t * H + c) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-constexpr size_t kGSmem = 1024 + (size_t)kGRing * kGStageBytes + (size_t)kGWorkers * kGEpiBytes + 64 * sizeof(uint64_t);
+constexpr size_t kGSmem = 1024 + (size_t)kGXRing * kGXBytes + (size_t)kGWRing * kGWBytes +
+                          (size_t)kGWorkers * kGEpiBytes + 64 * sizeof(uint64_t);
+static_assert(kGSmem <= 220 * 1024, "shared memory of a CTA, with the 4.3 KB of static arrays");
 
 // [n][K] 16-bit rows; a box is one stage of one row tile (128 rows x 64 inputs; what lies outside reads as 0).
 static int row_map(CUtensorMap* m, const void* base, int n, int K) {
