@@ -56,8 +56,7 @@ __device__ __forceinline__ void w4_accumulate(const W4Tile (&t)[NM], const uint1
 #pragma unroll
       for (int m = 0; m < NM; ++m) {
         uint32_t a0[4], a1[4];
-        w4_frag_bf16(h ? w[m].z : w[m].x, a0);
-        w4_frag_bf16(h ? w[m].w : w[m].y, a1);
+        w4_frag_bf16(h ? w[m].y : w[m].x, h ? w[m].w : w[m].z, a0, a1);
         const uint32_t sw = __ldg(t[m].scales + (size_t)kg * (8 * t[0].mates));
         const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&sw));
 #pragma unroll

@@ -7,18 +7,17 @@
 //                            blocks of 64 inputs; eight tiles' blocks are neighbours (the last tiles, fewer
 //                            than eight, among themselves), so 128 columns x 64 inputs are one copy of
 //                            4 KB.  A tile block is 32 chunks of 16 bytes, four for each pair of
-//                            columns g and g + 8 (g = 0..7): chunk 4g + (q + g / 2) % 4 holds the 16
-//                            inputs 32h + 8q + i (h = 0, 1; i = 0..7) in four 32-bit words.  Word s
-//                            covers the four inputs k0 = 32(s >> 1) + 8q + 4(s & 1), k0 + 1, .. k0 + 3:
-//                            bits 2-5 / 18-21 column g's inputs k0 + 2 / k0 + 3, bits 6-9 / 22-25 its
-//                            k0 / k0 + 1; the same 8 bits further up (bits 30 and 31 wrap to 0 and 1)
-//                            column g + 8's.
+//                            columns g and g + 8 (g = 0..7): chunk 4g + (q + g / 2) % 4 holds inputs
+//                            8q .. 8q + 7 and 32 + 8q .. 32 + 8q + 7 of column g, then the same of
+//                            column g + 8, one 32-bit word for eight inputs.  In a word, the codes of
+//                            inputs 0, 2, 4, 6 start at bits 6, 2, 10, 14, those of 1, 3, 5, 7 sixteen
+//                            bits further (bits 30, 31 wrap to 0, 1).
 //   The two readers this serves: in a warp, lane 4g + q's chunk is its A fragment of four 16 x 16 MMAs
 //   (one coalesced 16-byte load each), whose B fragment is 16 consecutive bytes of a bf16 row; and a
-//   thread that owns one column reads its 64 inputs as four chunks from shared memory, where the
-//   rotation by g / 2 spreads the eight columns over all banks.  A code in bits 6-9 of a half is the
-//   top of an fp16 mantissa: 0x4c00 | code << 6 is 16 + code, so (code - 8) * scale is one fused
-//   multiply-add with -24 * scale, exact for a scale of 8 significant bits.
+//   thread that owns one column reads its 64 inputs as four 8-byte pieces from shared memory, where the
+//   rotation by g / 2 spreads sixteen columns over all banks.  A code in bits 6-9 of a half is the top of
+//   an fp16 mantissa: 0x4c00 | code << 6 is 16 + code, so (code - 8) * scale is one fused multiply-add
+//   with -24 * scale, exact for a scale of 8 significant bits.
 //   scales  [Mt / 8][Kg][8][8 words] Kg groups, neighbours as for the codes; word g = (column g, column
 //                            g + 8) of the tile as two fp16, divided by the column's multiplier
 //   mult    [Mt * 16] fp32   power of two per column: 2^floor(log2(max |scale|)), 1 where that is 0 or
@@ -93,9 +92,11 @@ __host__ __device__ inline W4Slab w4_slab(int H, int I, int G) {
   return s;
 }
 
-// The bits of one code inside its column's byte pairs (see above): columns g (hi = 0) and g + 8, input
-// k0 + 2p (the partner k0 + 2p + 1 sits 16 bits further).
-__host__ __device__ constexpr int w4_code_bit(int hi, int p) { return (p ? 2 : 6) + 8 * hi; }
+// First bit of the code of input i (0..7) in a word.
+__host__ __device__ constexpr int w4_code_bit(int i) {
+  const int b[4] = {6, 2, 10, 14};
+  return b[i >> 1] + 16 * (i & 1);
+}
 __host__ __device__ inline uint32_t w4_put(int code, int bit) {
   const uint32_t c = (uint32_t)code;
   return bit > 28 ? (c << bit) | (c >> (32 - bit)) : c << bit;
@@ -104,16 +105,25 @@ __host__ __device__ inline uint32_t w4_put(int code, int bit) {
 // A lane's chunk within a tile block.
 __device__ __forceinline__ int w4_chunk(int g, int q) { return 4 * g + ((q + (g >> 1)) & 3); }
 
-// Word w of a lane's chunk -> the four bf16x2 registers of a 16 x 16 A fragment, as code - 8: a code in
-// mantissa bits 2-5 of 0x4300 is 128 + 4 code, and a quarter of that minus 40 is exact.
-__device__ __forceinline__ void w4_frag_bf16(uint32_t w, uint32_t (&a)[4]) {
+// The words of columns g (w0) and g + 8 (w1) for one run of eight inputs -> the A fragments (bf16x2, as
+// code - 8) of two 16 x 16 MMAs, inputs 0-3 and 4-7 of the run: a code in mantissa bits 2-5 of 0x4300 is
+// 128 + 4 code, and a quarter of that minus 40 is exact.
+__device__ __forceinline__ void w4_frag_bf16(uint32_t w0, uint32_t w1, uint32_t (&a0)[4], uint32_t (&a1)[4]) {
   const uint32_t quarter = 0x3e803e80u, off = 0xc220c220u;  // 0.25, -40
-  const uint32_t r[4] = {w >> 4, __funnelshift_r(w, w, 12), w, w >> 8};  // (g, p 0), (g + 8, p 0), (g, p 1), (g + 8, p 1)
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t v = (r[i] & 0x003c003cu) | 0x43004300u;
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(a[i]) : "r"(v), "r"(quarter), "r"(off));
-  }
+  auto conv = [&](uint32_t v) {
+    uint32_t r;
+    v = (v & 0x003c003cu) | 0x43004300u;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(quarter), "r"(off));
+    return r;
+  };
+  a0[0] = conv(w0 >> 4);
+  a0[1] = conv(w1 >> 4);
+  a0[2] = conv(w0);
+  a0[3] = conv(w1);
+  a1[0] = conv(w0 >> 8);
+  a1[1] = conv(w1 >> 8);
+  a1[2] = conv(__funnelshift_r(w0, w0, 12));
+  a1[3] = conv(__funnelshift_r(w1, w1, 12));
 }
 
 // C += A(16 x 16, bf16) B(16 x 8, bf16), fp32 accumulators.

@@ -15,7 +15,7 @@
 // way to the combine, y are rounded, to 11 bits.
 //
 // Warps: 0 TMA producer, 1 TMEM allocation and MMA issue (one thread), 2-17 workers (two sets that
-// dequantise stages in turn, then all drain the accumulators).  TMEM: 2 x 128 accumulator columns, 4 weight stages of 2 x 32 columns.
+// dequantise 128 inputs in turn; all drain the accumulators).  TMEM: 2 x 128 accumulator columns, 4 weight stages of 2 x 32 columns.
 #include <limits.h>
 
 #include <algorithm>
@@ -32,15 +32,16 @@ constexpr int kGK = 64;        // inputs per stage
 constexpr int kGXRing = 5;     // stages of rows in shared memory
 constexpr int kGChunk = 4;     // stages of codes that are copied together
 constexpr int kGWRing = 2;     // chunks of codes in shared memory
-constexpr int kGAStages = 4;   // TMEM weight stages
-constexpr int kGSet = 8;       // worker warps of a stage
-constexpr int kGWorkers = 16;  // worker warps: two sets, taking stages in turn
+constexpr int kGVisit = 2;     // stages that a worker dequantises at a time
+constexpr int kGSet = 8;       // worker warps of a visit
+constexpr int kGWorkers = 16;  // worker warps: two sets, taking visits in turn, each with its TMEM columns
 constexpr int kGThreads = 64 + 32 * kGWorkers;
 constexpr int kGXBytes = kGN * kGK * 2;
 constexpr int kGCodeBlock = kGChunk * 4096;    // a chunk's codes of 128 features
 constexpr int kGScaleBlock = kGChunk * 2 * 256;  // its fp16 scales (two groups a stage at most)
 constexpr int kGWBytes = 2 * (kGCodeBlock + kGScaleBlock);
-constexpr int kGEpiBytes = 32 * 32 * 4;        // staging per worker warp
+constexpr int kGEpiBytes = 32 * 32 * 4 + 256;  // per worker warp: staging, and its 32 rows' powers of two
+static_assert(kGChunk == 2 * kGVisit, "a chunk is one visit of each set");
 constexpr uint32_t kGTmemCols = 512;
 constexpr uint32_t kGACol = 2 * kGN;           // first weight column
 
@@ -162,6 +163,153 @@ __device__ __forceinline__ int w4g_mt0(int ft, int b) {
   return kMode == kGateUp ? ft * 8 : (2 * ft + b) * 8;
 }
 
+// Eight codes of a word (w4.cuh) times their scale, fp16, inputs in order.
+__device__ __forceinline__ void w4_expand(uint32_t w, __half2 s, uint32_t* o) {
+  const __half2 m24s = __hmul2(s, __float2half2_rn(-24.f));
+  auto top = [&](uint32_t v) {  // codes in bits 6-9: 16 + code; (16 + code) s - 24 s is exact
+    v = (v & 0x03c003c0u) | 0x4c004c00u;
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&v), s, m24s);
+    return *reinterpret_cast<const uint32_t*>(&r);
+  };
+  o[0] = top(w);
+  // codes in bits 2-5: 256 + code; the shift is saved and one more half-precision operation spent,
+  // which keeps the integer and the floating-point pipe equally busy
+  const uint32_t v = (w & 0x003c003cu) | 0x5c005c00u;
+  const __half2 c = __hsub2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(264.f)), p = __hmul2(c, s);
+  o[1] = *reinterpret_cast<const uint32_t*>(&p);
+  o[2] = top(w >> 4);
+  o[3] = top(__funnelshift_r(w, w, 8));
+}
+
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+
+// Drains 32 rows (of chunk `chunk`) x this warp's 32 features of both accumulators: to registers, the
+// accumulators are handed back, then scaled, transposed through shared memory and stored.
+template <int kMode, class Wait>
+__device__ __forceinline__ void w4g_drain(const W4GemmArgs& a, const W4Dims& d, const W4GTile& ti, uint32_t taddr, int q,
+                                          int chunk, int lane, unsigned char* stage, uint64_t* tfull,
+                                          uint64_t* tempty, uint32_t tc, Wait&& wait, volatile int* abort_flag) {
+  const int tok0 = 32 * chunk;
+  const bool any = tok0 < ti.ntok, mine = tok0 + lane < ti.ntok;
+  const size_t row0 = (size_t)ti.row0 + tok0;
+  // the rows' powers of two, one lane each, for all lanes to read
+  float* fac = reinterpret_cast<float*>(stage + 4096);
+  if (any) {
+    const float rx = mine ? pow2(a.rexp[row0 + lane]) : 0.f;
+    if (kMode == kGateUp) {
+      fac[2 * lane] = rx;
+      fac[2 * lane + 1] = mine ? pow2(-a.oexp[row0 + lane]) : 0.f;
+    } else {
+      fac[lane] = kMode == kDown && a.yh ? 1.f : rx;  // scaled rows of y keep the row's own power of two apart
+    }
+  }
+  __syncwarp();
+  wait(tfull, tc & 1u);
+  tc_fence_after();
+  auto release = [&] {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(tempty);
+  };
+  if (!any) {
+    release();
+    return;
+  }
+  const bool store = !*abort_flag;
+  if (kMode == kGateUp) {
+    float v0[32], v1[32];
+    tmem_ld32(taddr + tok0, v0);
+    tmem_ld32(taddr + kGN + tok0, v1);
+    tmem_ld_wait();
+    release();
+    const int f0 = ti.ft * kGM + 32 * q, f = f0 + lane;
+    const float* mg = reinterpret_cast<const float*>(ti.base + a.mat0 + d.mult);
+    const float* mu = reinterpret_cast<const float*>(ti.base + a.mat1 + d.mult);
+    const float cg = f < d.N ? mg[f] : 0.f, cu = f < d.N ? mu[f] : 0.f;
+    uint16_t* st = reinterpret_cast<uint16_t*>(stage);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const float4 m = *reinterpret_cast<const float4*>(fac + 2 * j);  // x, 1 / h of rows j, j + 1
+      const float g0 = v0[j] * cg * m.x, g1 = v0[j + 1] * cg * m.z;
+      const float u0 = v1[j] * cu * m.x, u1 = v1[j + 1] * cu * m.z;
+      st[j * 32 + lane] = __half_as_ushort(__float2half_rn(__fdividef(g0, 1.f + __expf(-g0)) * u0 * m.y));
+      st[(j + 1) * 32 + lane] = __half_as_ushort(__float2half_rn(__fdividef(g1, 1.f + __expf(-g1)) * u1 * m.w));
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // 32 rows x 64 B: four 16-byte pieces per lane
+      const int idx = i * 32 + lane, row = idx >> 2, seg = idx & 3;
+      const uint4 v = *reinterpret_cast<const uint4*>(st + row * 32 + seg * 8);
+      if (store && tok0 + row < ti.ntok && f0 + seg * 8 < d.N)
+        *reinterpret_cast<uint4*>(a.h + (row0 + row) * d.N + f0 + seg * 8) = v;
+    }
+    __syncwarp();
+    return;
+  }
+  const float* mc = reinterpret_cast<const float*>(ti.base + a.mat0 + d.mult);
+#pragma unroll 1
+  for (int blk = 0; blk < 2; ++blk) {
+    float v[32];
+    tmem_ld32(taddr + blk * kGN + tok0, v);
+    tmem_ld_wait();
+    if (blk == 1) release();
+    const int f0 = (2 * ti.ft + blk) * kGM + 32 * q, f = f0 + lane;
+    if (f0 >= d.N) continue;
+    float cm = f < d.N ? mc[f] : 0.f;
+    if (kMode == kDown && a.yh) cm = ldexpf(cm, -w4_y_exp(ti.base + a.mat0, d));
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      const float4 m = *reinterpret_cast<const float4*>(fac + j);
+      v[j] = v[j] * cm * m.x;
+      v[j + 1] = v[j + 1] * cm * m.y;
+      v[j + 2] = v[j + 2] * cm * m.z;
+      v[j + 3] = v[j + 3] * cm * m.w;
+    }
+    if (kMode == kLinear && !(a.ldo % 8 == 0 && (uintptr_t)a.out % 16 == 0 && f0 + 32 <= d.N)) {
+      // unaligned or ragged rows of out: element stores, 32 consecutive features per row
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (store && tok0 + j < ti.ntok && f < d.N) {
+          const size_t at = (row0 + j) * a.ldo + f;
+          if (a.out_f32) reinterpret_cast<float*>(a.out)[at] = v[j];
+          else reinterpret_cast<uint16_t*>(a.out)[at] = f32_to_bf16(v[j]);
+        }
+      continue;
+    }
+    const bool f32 = kMode == kLinear ? a.out_f32 != 0 : a.yh == nullptr;
+    const size_t ld = kMode == kLinear ? a.ldo : (size_t)d.N;
+    if (f32) {
+      float* st = reinterpret_cast<float*>(stage);
+      float* out = kMode == kLinear ? reinterpret_cast<float*>(a.out) : a.y;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) st[j * 32 + lane] = v[j];
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {  // 32 rows x 128 B
+        const int idx = i * 32 + lane, row = idx >> 3, seg = idx & 7;
+        const uint4 o = *reinterpret_cast<const uint4*>(st + row * 32 + seg * 4);
+        if (store && tok0 + row < ti.ntok && f0 + seg * 4 < d.N)
+          *reinterpret_cast<uint4*>(out + (row0 + row) * ld + f0 + seg * 4) = o;
+      }
+    } else {
+      uint16_t* st = reinterpret_cast<uint16_t*>(stage);
+      uint16_t* out = kMode == kLinear ? reinterpret_cast<uint16_t*>(a.out) : a.yh;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        st[j * 32 + lane] = kMode == kLinear ? f32_to_bf16(v[j]) : __half_as_ushort(__float2half_rn(v[j]));
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // 32 rows x 64 B
+        const int idx = i * 32 + lane, row = idx >> 2, seg = idx & 3;
+        const uint4 o = *reinterpret_cast<const uint4*>(st + row * 32 + seg * 8);
+        if (store && tok0 + row < ti.ntok && f0 + seg * 8 < d.N)
+          *reinterpret_cast<uint4*>(out + (row0 + row) * ld + f0 + seg * 8) = o;
+      }
+    }
+    __syncwarp();
+  }
+}
+
 template <int kMode>
 __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs a, const __grid_constant__ CUtensorMap mapX) {
   extern __shared__ __align__(16) unsigned char gsm_raw[];
@@ -175,8 +323,8 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   uint64_t* wfull = xempty + kGXRing;
   uint64_t* wempty = wfull + kGWRing;
   uint64_t* afull = wempty + kGWRing;
-  uint64_t* aempty = afull + kGAStages;
-  uint64_t* tfull = aempty + kGAStages;
+  uint64_t* aempty = afull + 2;
+  uint64_t* tfull = aempty + 2;
   uint64_t* tempty = tfull + 1;
   uint64_t* done = tempty + 1;
   __shared__ uint32_t s_tmem;
@@ -197,7 +345,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
       mbar_init(&wfull[s], 1);
       mbar_init(&wempty[s], kGWorkers);
     }
-    for (int s = 0; s < kGAStages; ++s) {
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&afull[s], kGSet);
       mbar_init(&aempty[s], 1);
     }
@@ -295,32 +443,38 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   } else if (warp == 1) {
     const uint64_t bd0 = smem_desc_l(smem_u32(xs), 16, 1024, kLayoutSw128);
     const bool lead = elect_one();
-    uint32_t it = 0, tc = 0;
+    uint32_t xi = 0, vi = 0, tc = 0;  // stages of rows, visits, tiles
     for (int t = blockIdx.x; t < total && !__any_sync(MOE_FULL_MASK, *abort_flag); t += gridDim.x, ++tc) {
       const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
       const uint32_t idesc = idesc_f16(kGM, (ti.ntok + 15) & ~15);
       const bool two = kMode == kGateUp || w4g_mt0<kMode>(ti.ft, 1) < d.Mt;
       if (tc > 0) wait(tempty, (tc - 1) & 1u);
-      tc_fence_after();
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const uint32_t s = it % kGXRing, as = it % kGAStages;
-        wait(&xfull[s], (it / kGXRing) & 1u);
-        wait(&afull[as], (it / kGAStages) & 1u);
-        tc_fence_after();
-        const uint32_t ac = tmem + kGACol + as * 64;
-        const uint64_t bd = bd0 + (uint64_t)(s * (kGXBytes >> 4));
-        if (lead) {
+      for (int kb = 0; kb < nkb; ++vi) {
+        const uint32_t as = vi & 1;
+        wait(&afull[as], (vi >> 1) & 1u);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) umma_f16_ts(tmem, ac + 8 * k, bd + 2 * k, idesc, kb > 0 || k > 0);
-          if (two)
+        for (int h = 0; h < kGVisit; ++h, ++kb, ++xi) {
+          if (kb >= nkb) break;
+          const uint32_t s = xi % kGXRing;
+          wait(&xfull[s], (xi / kGXRing) & 1u);
+          tc_fence_after();
+          const uint32_t ac = tmem + kGACol + as * 128 + h * 32;
+          const uint64_t bd = bd0 + (uint64_t)(s * (kGXBytes >> 4));
+          if (lead) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) umma_f16_ts(tmem + kGN, ac + 32 + 8 * k, bd + 2 * k, idesc, kb > 0 || k > 0);
-          umma_commit(&xempty[s]);
-          umma_commit(&aempty[as]);
-          if (kb + 1 == nkb) umma_commit(tfull);
+            for (int k = 0; k < 4; ++k) umma_f16_ts(tmem, ac + 8 * k, bd + 2 * k, idesc, kb > 0 || k > 0);
+            if (two)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) umma_f16_ts(tmem + kGN, ac + 64 + 8 * k, bd + 2 * k, idesc, kb > 0 || k > 0);
+            umma_commit(&xempty[s]);
+          }
+          __syncwarp();
         }
+        if (lead) umma_commit(&aempty[as]);
         __syncwarp();
       }
+      if (lead) umma_commit(tfull);
+      __syncwarp();
     }
     if (lead) umma_commit(done);
     __syncwarp();
@@ -330,171 +484,73 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     const int q = warp & 3, b = ((warp - 2) >> 2) & 1, set = (warp - 2) >> 3, chunk = (warp - 2) >> 2;
     const int r = 32 * q + lane, g = r & 7, hi = (r >> 3) & 1;
     const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
-    const int rot = (g >> 1) & 3;
+    const uint32_t a_addr = tmem + lane_addr + kGACol + set * 128 + b * 64;
     unsigned char* stage = epi + (warp - 2) * kGEpiBytes;
-    uint32_t it = 0, wi = 0, tc = 0;
-    for (int t = blockIdx.x; t < total && !__any_sync(MOE_FULL_MASK, *abort_flag); t += gridDim.x, ++tc) {
-      const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
-      const int nm = max(1, min(8, d.Mt - w4g_mt0<kMode>(ti.ft, b)));
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const int j4 = kb % kGChunk;
-        const uint32_t ws = wi % kGWRing;
-        if (j4 == 0) wait(&wfull[ws], (wi / kGWRing) & 1u);
-        const bool last = j4 == kGChunk - 1 || kb + 1 == nkb;
-        if (last) ++wi;
-        if ((it & 1) != (uint32_t)set) {
-          if (last) {
+    uint32_t vi = 0, wi = 0, tc = 0;  // visits, chunks before this tile, tiles drained
+    W4GTile prev = {};
+    bool pending = false;  // prev has not been drained
+    for (int t = blockIdx.x;; t += gridDim.x) {
+      const bool real = t < total && !__any_sync(MOE_FULL_MASK, *abort_flag);
+      W4GTile ti = {};
+      if (real) ti = w4g_tile<kMode>(a, s_pre, nl, t);
+      const int nm = max(1, min(8, d.Mt - w4g_mt0<kMode>(ti.ft, b))), nk = real ? nkb : 0;
+      // one visit of each set, the last tile's drain, the other visits
+      int kb = 0;
+#pragma unroll 1
+      for (int phase = 0; phase < 2; ++phase) {
+#pragma unroll 1
+      for (const int end = phase ? nk : min(nk, 2 * kGVisit); kb < end; kb += kGVisit, ++vi) {
+        // a chunk of codes holds two visits, one of each set; a tile starts a chunk of its own
+        const uint32_t c = wi + kb / kGChunk, ws = c % kGWRing;
+        if ((vi & 1) != (uint32_t)set) {
+          if (kb % kGChunk == 0 && kb + kGVisit >= nkb) {  // a last chunk without a visit of this set
+            wait(&wfull[ws], (c / kGWRing) & 1u);
             __syncwarp();
             if (lane == 0) mbar_arrive(&wempty[ws]);
           }
           continue;
         }
-        const uint32_t as = it % kGAStages;
+        wait(&wfull[ws], (c / kGWRing) & 1u);
         const unsigned char* wst = wsm + ws * kGWBytes;
-        const unsigned char* code = wst + b * kGCodeBlock + (j4 * nm + (r >> 4)) * 512 + g * 64;
-        const int gi = d.G == 128 ? j4 >> 1 : d.G == 64 ? j4 : 2 * j4;
-        const __half* sp =
-            reinterpret_cast<const __half*>(wst + 2 * kGCodeBlock + b * kGScaleBlock + (gi * nm + (r >> 4)) * 32 + g * 4) + hi;
-        uint4 c[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c[j] = *reinterpret_cast<const uint4*>(code + ((j + rot) & 3) * 16);
-        const __half2 s0 = __half2half2(sp[0]), s1 = d.G == 32 ? __half2half2(sp[16 * nm]) : s0;
-        const __half2 m24 = __float2half2_rn(-24.f), n0 = __hmul2(s0, m24), n1 = __hmul2(s1, m24);
         uint32_t o[32];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t w[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
+        for (int h = 0; h < kGVisit; ++h) {
+          if (kb + h >= nkb) break;
+          const int j4 = kb % kGChunk + h;
+          const unsigned char* code = wst + b * kGCodeBlock + (j4 * nm + (r >> 4)) * 512 + g * 64 + hi * 8;
+          const int gi = d.G == 128 ? j4 >> 1 : d.G == 64 ? j4 : 2 * j4;
+          const __half* sp = reinterpret_cast<const __half*>(wst + 2 * kGCodeBlock + b * kGScaleBlock +
+                                                             (gi * nm + (r >> 4)) * 32 + g * 4) + hi;
+          uint2 w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t v = __funnelshift_r(w[i], w[i], 8 * hi);
-            const uint32_t p0 = (v & 0x03c003c0u) | 0x4c004c00u, p1 = ((v << 4) & 0x03c003c0u) | 0x4c004c00u;
-            const __half2 sc = i < 2 ? s0 : s1, nc = i < 2 ? n0 : n1;
-            const __half2 h0 = __hfma2(*reinterpret_cast<const __half2*>(&p0), sc, nc);
-            const __half2 h1 = __hfma2(*reinterpret_cast<const __half2*>(&p1), sc, nc);
-            const int col = 16 * (i >> 1) + 4 * j + 2 * (i & 1);
-            o[col] = *reinterpret_cast<const uint32_t*>(&h0);
-            o[col + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+          for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint2*>(code + ((j + (g >> 1)) & 3) * 16);
+          const __half2 s0 = __half2half2(sp[0]), s1 = d.G == 32 ? __half2half2(sp[16 * nm]) : s0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            w4_expand(w[j].x, s0, &o[4 * j]);
+            w4_expand(w[j].y, s1, &o[16 + 4 * j]);
           }
+          if (h == 0 && vi >= 2) wait(&aempty[set], ((vi >> 1) - 1) & 1u);
+          tc_fence_after();
+          tmem_st32(a_addr + 32 * h, o);
         }
-        if (last) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&wempty[ws]);
-        }
-        if (it >= kGAStages) wait(&aempty[as], (it / kGAStages - 1) & 1u);
-        tc_fence_after();
-        tmem_st32(tmem + lane_addr + kGACol + as * 64 + b * 32, o);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&afull[as]);
-      }
-      // drain: this warp's 32 features of both blocks, 32 rows of the tile
-      wait(tfull, tc & 1u);
-      tc_fence_after();
-      const bool store = !*abort_flag;
-      if (kMode == kGateUp) {
-        const int f0 = ti.ft * kGM + 32 * q, f = f0 + lane;
-        const float* mg = reinterpret_cast<const float*>(ti.base + a.mat0 + d.mult);
-        const float* mu = reinterpret_cast<const float*>(ti.base + a.mat1 + d.mult);
-        const float cg = f < d.N ? mg[f] : 0.f, cu = f < d.N ? mu[f] : 0.f;
-        uint16_t* st = reinterpret_cast<uint16_t*>(stage);
-        const int c = chunk;
-        if (32 * c < ti.ntok) {
-          float gv[32], uv[32];
-          tmem_ld32(tmem + lane_addr + 32 * c, gv);
-          tmem_ld32(tmem + lane_addr + kGN + 32 * c, uv);
-          const int tok = 32 * c + lane;
-          const float xm = tok < ti.ntok ? ldexpf(1.f, a.rexp[ti.row0 + tok]) : 0.f;
-          const float hm = tok < ti.ntok ? ldexpf(1.f, -a.oexp[ti.row0 + tok]) : 0.f;
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float x1 = __shfl_sync(MOE_FULL_MASK, xm, j), h1 = __shfl_sync(MOE_FULL_MASK, hm, j);
-            const float gg = gv[j] * cg * x1, uu = uv[j] * cu * x1;
-            const float h = __fdividef(gg, 1.f + __expf(-gg)) * uu;
-            st[j * 32 + lane] = __half_as_ushort(__float2half_rn(h * h1));
-          }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {  // 32 rows x 64 B: four 16-byte pieces per lane
-            const int idx = i * 32 + lane, row = idx >> 2, seg = idx & 3;
-            const uint4 v = *reinterpret_cast<const uint4*>(st + row * 32 + seg * 8);
-            if (store && 32 * c + row < ti.ntok && f0 + seg * 8 < d.N)
-              *reinterpret_cast<uint4*>(a.h + (size_t)(ti.row0 + 32 * c + row) * d.N + f0 + seg * 8) = v;
-          }
-          __syncwarp();
-        }
-      } else {
-        const float* mc = reinterpret_cast<const float*>(ti.base + a.mat0 + d.mult);
-#pragma unroll 1
-        for (int blk = 0; blk < 2; ++blk) {
-          const int f0 = (2 * ti.ft + blk) * kGM + 32 * q, f = f0 + lane;
-          if (f0 >= d.N) break;
-          float cm = f < d.N ? mc[f] : 0.f;
-          if (kMode == kDown && a.yh) cm = ldexpf(cm, -w4_y_exp(ti.base + a.mat0, d));
-          const int c = chunk;
-          if (32 * c < ti.ntok) {
-            float v[32];
-            tmem_ld32(tmem + lane_addr + kGN * blk + 32 * c, v);
-            const int tok = 32 * c + lane;
-            float rm = tok < ti.ntok ? ldexpf(1.f, a.rexp[ti.row0 + tok]) : 0.f;
-            if (kMode == kDown && a.yh) rm = 1.f;  // the row's own power of two stays in its exponent
-            tmem_ld_wait();
-            const size_t row0 = (size_t)ti.row0 + 32 * c;
-            if (kMode == kLinear && !(a.ldo % 8 == 0 && (uintptr_t)a.out % 16 == 0 && f0 + 32 <= d.N)) {
-              // unaligned or ragged rows of out: element stores, 32 consecutive features per row
-#pragma unroll
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const float o = v[j] * cm * __shfl_sync(MOE_FULL_MASK, rm, j);
-                if (store && 32 * c + j < ti.ntok && f < d.N) {
-                  const size_t at = (row0 + j) * a.ldo + f;
-                  if (a.out_f32) reinterpret_cast<float*>(a.out)[at] = o;
-                  else reinterpret_cast<uint16_t*>(a.out)[at] = f32_to_bf16(o);
-                }
-              }
-              __syncwarp();
-              continue;
-            }
-            const bool f32 = kMode == kLinear ? a.out_f32 != 0 : a.yh == nullptr;
-            const size_t ld = kMode == kLinear ? a.ldo : (size_t)d.N;
-            if (f32) {
-              float* st = reinterpret_cast<float*>(stage);
-              float* out = kMode == kLinear ? reinterpret_cast<float*>(a.out) : a.y;
-#pragma unroll
-              for (int j = 0; j < 32; ++j) st[j * 32 + lane] = v[j] * cm * __shfl_sync(MOE_FULL_MASK, rm, j);
-              __syncwarp();
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {  // 32 rows x 128 B
-                const int idx = i * 32 + lane, row = idx >> 3, seg = idx & 7;
-                const uint4 o = *reinterpret_cast<const uint4*>(st + row * 32 + seg * 4);
-                if (store && 32 * c + row < ti.ntok && f0 + seg * 4 < d.N)
-                  *reinterpret_cast<uint4*>(out + (row0 + row) * ld + f0 + seg * 4) = o;
-              }
-            } else {
-              uint16_t* st = reinterpret_cast<uint16_t*>(stage);
-              uint16_t* out = kMode == kLinear ? reinterpret_cast<uint16_t*>(a.out) : a.yh;
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const float o = v[j] * cm * __shfl_sync(MOE_FULL_MASK, rm, j);
-                st[j * 32 + lane] = kMode == kLinear ? f32_to_bf16(o) : __half_as_ushort(__float2half_rn(o));
-              }
-              __syncwarp();
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {  // 32 rows x 64 B
-                const int idx = i * 32 + lane, row = idx >> 2, seg = idx & 3;
-                const uint4 o = *reinterpret_cast<const uint4*>(st + row * 32 + seg * 8);
-                if (store && 32 * c + row < ti.ntok && f0 + seg * 8 < d.N)
-                  *reinterpret_cast<uint4*>(out + (row0 + row) * ld + f0 + seg * 8) = o;
-              }
-            }
-            __syncwarp();
-          }
+        if (lane == 0) {
+          mbar_arrive(&afull[set]);
+          mbar_arrive(&wempty[ws]);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tempty);
+      if (phase == 0 && pending) {
+        w4g_drain<kMode>(a, d, prev, tmem + lane_addr, q, chunk, lane, stage, tfull, tempty, tc, wait, abort_flag);
+        ++tc;
+      }
+      }
+      if (!real) break;
+      prev = ti;
+      pending = true;
+      wi += (nkb + kGChunk - 1) / kGChunk;
     }
   }
   __syncwarp();
@@ -542,7 +598,7 @@ __device__ __forceinline__ void w4_scale_row(const uint16_t* x, uint16_t* xp, in
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(MOE_FULL_MASK, amax, o));
-  xe = amax > 0.f ? ilogbf(amax) - 14 : 0;
+  xe = amax > 0.f ? max(ilogbf(amax) - 14, -126) : 0;
   const float f0 = ldexpf(1.f, -xe / 2), f1 = ldexpf(1.f, -xe - (-xe / 2));  // 2^-xe may overflow by itself
   float nrm = 0.f;
   auto conv = [&](uint32_t v) {
@@ -651,7 +707,7 @@ __global__ void __launch_bounds__(128) w4_combine_kernel(const uint16_t* __restr
 
 constexpr size_t kGSmem = 1024 + (size_t)kGXRing * kGXBytes + (size_t)kGWRing * kGWBytes +
                           (size_t)kGWorkers * kGEpiBytes + 64 * sizeof(uint64_t);
-static_assert(kGSmem <= 220 * 1024, "shared memory of a CTA, with the 4.3 KB of static arrays");
+static_assert(kGSmem <= 222 * 1024, "shared memory of a CTA, with the 4.3 KB of static arrays");
 
 // [n][K] 16-bit rows; a box is one stage of one row tile (128 rows x 64 inputs; what lies outside reads as 0).
 static int row_map(CUtensorMap* m, const void* base, int n, int K) {

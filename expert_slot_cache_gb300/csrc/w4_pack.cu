@@ -90,16 +90,11 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const W4PackArgs a) {
   uint32_t* out = reinterpret_cast<uint32_t*>(dst);
   for (int i = threadIdx.x; i < nt * nb * 128; i += 256) {
     const int wd = i & 127, b = (i >> 7) % nb, t = (i >> 7) / nb;
-    const int ch = wd >> 2, s = wd & 3, g = ch >> 2, q = (ch - (g >> 1)) & 3;
-    const int k = b * 64 + 32 * (s >> 1) + 8 * q + 4 * (s & 1), c = t * 16 + g;
+    const int ch = wd >> 2, g = ch >> 2, q = (ch - (g >> 1)) & 3;
+    const int k = b * 64 + 32 * (wd & 1) + 8 * q, c = t * 16 + g + 8 * ((wd >> 1) & 1);
     uint32_t v = 0;
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int bit = w4_code_bit(h, p);
-        v |= w4_put(sc[k + 2 * p][c + 8 * h], bit) | w4_put(sc[k + 2 * p + 1][c + 8 * h], (bit + 16) & 31);
-      }
+    for (int j = 0; j < 8; ++j) v |= w4_put(sc[k + j][c], w4_code_bit(j));
     out[w4_code_at(d, n0 / 16 + t, k0 / 64 + b) * 128 + wd] = v;
   }
 }
@@ -128,14 +123,14 @@ __global__ void __launch_bounds__(128) w4_scale_kernel(const W4PackArgs a) {
     const float raw = bf16_to_f32(sc[at]);
     int sq = 0;  // sum of (code - 8)^2 of the group: at most 128 * 64
     for (int b = i * d.G / 32; b < (i + 1) * d.G / 32 && b < d.Kb * 2; ++b)  // blocks of 32 inputs
-      for (int q = 0; q < 4; ++q)
-        for (int s = 0; s < 2; ++s) {
-          const uint32_t v = words[w4_code_at(d, tile, b >> 1) * 128 + w4_chunk(g, q) * 4 + 2 * (b & 1) + s];
-          const uint32_t w = __funnelshift_r(v, v, 8 * h);
-          const int c0 = (int)((w >> 6) & 15) - 8, c1 = (int)((w >> 22) & 15) - 8, c2 = (int)((w >> 2) & 15) - 8,
-                    c3 = (int)((w >> 18) & 15) - 8;
-          sq += c0 * c0 + c1 * c1 + c2 * c2 + c3 * c3;
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t v = words[w4_code_at(d, tile, b >> 1) * 128 + w4_chunk(g, q) * 4 + 2 * h + (b & 1)];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int c = (int)(__funnelshift_r(v, v, w4_code_bit(j)) & 15) - 8;
+          sq += c * c;
         }
+      }
     const float r = raw * f0 * f1;
     norm = fmaf(r * r, (float)sq, norm);
     sc[at] = __half_as_ushort(__float2half_rn(r));
