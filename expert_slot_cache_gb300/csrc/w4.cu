@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kW4Threads) w4_gateup_kernel(const W4FfnArgs a
   __shared__ float red[kW4Warps * 2 * NB * 4 * 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const W4Dims& d = a.sl.gu;
-  const int nl = *a.f.n_list, FT = d.Mt;
+  const int nl = *a.f.n_list, FT = d.Mt / 2, I = d.N / 2;  // a tile of gate and its neighbour of up
   for (int u = blockIdx.x; u < nl * FT; u += gridDim.x) {
     int e, slot;
     if (!w4_slot(a.f, u / FT, e, slot)) continue;
@@ -171,9 +171,9 @@ __global__ void __launch_bounds__(kW4Threads) w4_gateup_kernel(const W4FfnArgs a
     }
     const int tile = u % FT, pe = a.f.offset[e + 1];
     const uint8_t* base = reinterpret_cast<const uint8_t*>(a.f.pool) + (size_t)slot * a.sl.bytes;
-    const W4Tile t[2] = {w4_tile(base, d, tile, lane), w4_tile(base + d.bytes, d, tile, lane)};
-    const float* mg = reinterpret_cast<const float*>(base + d.mult) + tile * 16;
-    const float* mu = reinterpret_cast<const float*>(base + d.bytes + d.mult) + tile * 16;
+    const W4Tile t[2] = {w4_tile(base, d, 2 * tile, lane), w4_tile(base, d, 2 * tile + 1, lane)};
+    const float* mg = reinterpret_cast<const float*>(base + d.mult) + tile * 32;
+    const float* mu = mg + 16;
     const int per = (d.Kb + kW4Warps - 1) / kW4Warps;
     for (int p0 = a.f.offset[e]; p0 < pe; p0 += 8 * NB) {
       const int nt = min(8 * NB, pe - p0);
@@ -194,9 +194,9 @@ __global__ void __launch_bounds__(kW4Threads) w4_gateup_kernel(const W4FfnArgs a
         const float h = g / (1.f + __expf(-g)) * v;
         // h as the sum of two bf16: 16 significant bits reach the down product
         const uint16_t hi = f32_to_bf16(h);
-        const size_t o = (size_t)(p0 + row) * d.N + tile * 16 + col;
+        const size_t o = (size_t)(p0 + row) * I + tile * 16 + col;
         a.h[o] = hi;
-        a.h[a.n * d.N + o] = isfinite(bf16_to_f32(hi)) ? f32_to_bf16(h - bf16_to_f32(hi)) : 0;
+        a.h[a.n * I + o] = isfinite(bf16_to_f32(hi)) ? f32_to_bf16(h - bf16_to_f32(hi)) : 0;
       }
     }
   }
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kW4Threads) w4_down_kernel(const W4FfnArgs a) 
     const int tile0 = u % FT * TPC, tile = tile0 + warp / KS, part = warp % KS, pe = a.f.offset[e + 1];
     const bool ok = slot >= 0 && slot < a.f.S;
     const uint8_t* base =
-        reinterpret_cast<const uint8_t*>(a.f.pool) + (size_t)(ok ? slot : 0) * a.sl.bytes + 2 * a.sl.gu.bytes;
+        reinterpret_cast<const uint8_t*>(a.f.pool) + (size_t)(ok ? slot : 0) * a.sl.bytes + a.sl.dn_at;
     const float* mult = reinterpret_cast<const float*>(base + d.mult);
     const int per = (d.Kb + KS - 1) / KS;
     for (int p0 = a.f.offset[e]; p0 < pe; p0 += 8 * NB) {
@@ -272,7 +272,7 @@ int launch_ffn_w4(const FfnArgs& f, int group, void* ws, size_t ws_bytes, int ma
   const int r = w4_sms(&sms);
   if (r != MOE_OK) return r;
   W4FfnArgs a{f, w4_slab(f.H, f.I, group), (uint16_t*)ws, (size_t)n};
-  const int g1 = std::min(max_list * a.sl.gu.Mt, sms * 8), g2 = std::min(max_list * ((a.sl.dn.Mt + 1) / 2), sms * 8);
+  const int g1 = std::min(max_list * (a.sl.gu.Mt / 2), sms * 8), g2 = std::min(max_list * ((a.sl.dn.Mt + 1) / 2), sms * 8);
   if (prof) prof->begin(MOE_PROF_FFN_GATEUP, stream);
   if (f.T <= 8) w4_gateup_kernel<1><<<g1, kW4Threads, 0, stream>>>(a);
   else w4_gateup_kernel<2><<<g1, kW4Threads, 0, stream>>>(a);

@@ -79,16 +79,20 @@ inline bool w4_slab_ok(int H, int I, int G) {
   return H >= 64 && H % 64 == 0 && I >= 32 && I % 32 == 0 && w4_shape_ok(H, I, G) && w4_shape_ok(I, H, G);
 }
 
-// The three matrices of an expert slab: gate and up (H x I), down (I x H).
+// An expert slab: gate and up as one H x 2I matrix whose tiles of 16 columns alternate (gate 0, up 0,
+// gate 1, ..), so that a feature's two products are neighbours; a second meta (its own holds the gate
+// columns' largest norm, this one the up columns'); then down (I x H).
 struct W4Slab {
   W4Dims gu, dn;
-  size_t bytes;
+  size_t up_meta, dn_at, bytes;
 };
 __host__ __device__ inline W4Slab w4_slab(int H, int I, int G) {
   W4Slab s;
-  s.gu = w4_dims(H, I, G);
+  s.gu = w4_dims(H, 2 * I, G);
   s.dn = w4_dims(I, H, G);
-  s.bytes = 2 * s.gu.bytes + s.dn.bytes;
+  s.up_meta = s.gu.bytes;
+  s.dn_at = s.gu.bytes + 16;
+  s.bytes = s.dn_at + s.dn.bytes;
   return s;
 }
 

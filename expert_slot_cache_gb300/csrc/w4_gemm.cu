@@ -1,11 +1,11 @@
 // 4-bit products of many rows on the tcgen05 tensor cores: the linear layer, and the grouped gate / up
 // and down products of the expert FFN.
 //
-// Computed transposed, D^T = W^T X^T: a CTA's tile is two blocks of 128 output features (gate and up of
-// the same features, or 256 consecutive ones) x up to 128 rows.  The weights are the A operand and come
-// from TMEM: worker threads own one feature each, turn its 64 codes of a stage into fp16 with one fused
-// multiply-add per pair and write them to TMEM, so the weights cross shared memory only once, as 4-bit
-// codes.  The rows are the B operand, fp16 in shared memory (TMA, 128-byte swizzle).
+// Computed transposed, D^T = W^T X^T, by CTA pairs (a cluster of two): a tile is 256 packed columns of
+// W (128 in each CTA) x up to 256 rows (half of them in each CTA's shared memory).  The weights are the A
+// operand and come from TMEM: worker threads own one column each, turn its codes into fp16 with about one
+// fused multiply-add per pair and write them to TMEM, so the weights cross shared memory only once, as
+// 4-bit codes.  The rows are the B operand, fp16 in shared memory (TMA, 128-byte swizzle).
 //
 // fp16, not bf16: (code - 8) * scale has up to 11 significant bits, exact in fp16.  The ranges are kept
 // by powers of two: scales are stored relative to their column's largest (w4.cuh), each row of x is
@@ -14,8 +14,16 @@
 // bound; typical values are 2^-11 (h) and 2^-16 (y) of it.  So x (8 bits) is exact and only h and, on its
 // way to the combine, y are rounded, to 11 bits.
 //
-// Warps: 0 TMA producer, 1 TMEM allocation and MMA issue (one thread), 2-17 workers (two sets that
-// dequantise 128 inputs in turn; all drain the accumulators).  TMEM: 2 x 128 accumulator columns, 4 weight stages of 2 x 32 columns.
+// Why pairs and 256 rows: an MMA over 256 x 256 x 16 runs 128 cycles in each SM and one thread can issue
+// it in that time; a pair's SM needs 32 B of rows and 8 B of codes a cycle from L2, near the 40 B that
+// an SM gets; and each code is dequantised once per 256 rows.  (One CTA, 2 x 128 columns x 128 rows, took
+// 87 us for 4096 rows through 2048 x 4096: its MMAs of 64 cycles could not be issued fast enough.)
+//
+// Warps: 0 loads the rows, the last one the codes (which run further ahead), 1 allocates TMEM and, in the
+// pair's first CTA, issues the MMAs (one lane); 2-17 are workers: four sets of four warps (one per TMEM lane quarter) that dequantise 128 inputs in turn, each
+// set into TMEM columns of its own; all drain the accumulators.  Before a tile is drained every set has
+// dequantised its first inputs of the next one, so the MMAs go on while the drained values are stored.
+// TMEM: 256 accumulator columns, 4 x 64 columns of weights.
 #include <limits.h>
 
 #include <algorithm>
@@ -26,24 +34,27 @@
 
 namespace moe {
 
-constexpr int kGM = 128;       // features per accumulator
-constexpr int kGN = 128;       // rows per tile
+constexpr int kGM = 128;       // packed columns per CTA
+constexpr int kGN = 256;       // rows per tile
+constexpr int kGRows = 128;    // of them in one CTA's shared memory, at most
 constexpr int kGK = 64;        // inputs per stage
-constexpr int kGXRing = 5;     // stages of rows in shared memory
+constexpr int kGXRing = 4;     // stages of rows in shared memory
 constexpr int kGChunk = 4;     // stages of codes that are copied together
-constexpr int kGWRing = 2;     // chunks of codes in shared memory
+constexpr int kGWRing = 4;     // chunks of codes in shared memory
 constexpr int kGVisit = 2;     // stages that a worker dequantises at a time
-constexpr int kGSet = 8;       // worker warps of a visit
-constexpr int kGWorkers = 16;  // worker warps: two sets, taking visits in turn, each with its TMEM columns
-constexpr int kGThreads = 64 + 32 * kGWorkers;
-constexpr int kGXBytes = kGN * kGK * 2;
-constexpr int kGCodeBlock = kGChunk * 4096;    // a chunk's codes of 128 features
-constexpr int kGScaleBlock = kGChunk * 2 * 256;  // its fp16 scales (two groups a stage at most)
-constexpr int kGWBytes = 2 * (kGCodeBlock + kGScaleBlock);
-constexpr int kGEpiBytes = 32 * 32 * 4 + 256;  // per worker warp: staging, and its 32 rows' powers of two
-static_assert(kGChunk == 2 * kGVisit, "a chunk is one visit of each set");
+constexpr int kGSets = 4;      // sets of four worker warps, taking visits in turn
+constexpr int kGWorkers = 4 * kGSets;
+constexpr int kGThreads = 96 + 32 * kGWorkers;
+constexpr int kGXBytes = kGRows * kGK * 2;
+constexpr int kGCodeBytes = kGChunk * 4096;     // a chunk's codes of 128 columns
+constexpr int kGScaleBytes = kGChunk * 2 * 256; // its fp16 scales (two groups a stage at most)
+constexpr int kGWBytes = kGCodeBytes + kGScaleBytes;
+constexpr int kGLd = 36;                        // staging: floats per row of 32 (padded against bank conflicts)
+constexpr int kGEpiBytes = 32 * kGLd * 4;       // per worker warp
 constexpr uint32_t kGTmemCols = 512;
-constexpr uint32_t kGACol = 2 * kGN;           // first weight column
+constexpr uint32_t kGACol = kGN;                // first weight column
+static_assert(kGChunk == 2 * kGVisit, "a chunk is two visits, of different sets");
+static_assert(kGN == 64 * kGSets, "each set drains 64 rows");
 
 enum { kGateUp = 0, kDown = 1, kLinear = 2 };
 
@@ -51,8 +62,8 @@ struct W4GemmArgs {
   const uint8_t* w;        // slab pool, or the packed matrix
   size_t slab;             // bytes between slabs (0: one matrix)
   W4Dims d;
-  size_t mat0, mat1;       // offsets of the two blocks' matrices (gate, up) or of the one matrix
-  int K, NF;               // K of the rows; feature tiles
+  size_t mat;              // offset of the matrix in a slab
+  int K, NF;               // K of the rows; column tiles of 256
   int n;                   // rows
   // grouped rows
   const int32_t *offset, *list_e, *n_list, *e2s, *list_s;
@@ -61,12 +72,17 @@ struct W4GemmArgs {
   const int32_t* rexp;     // [n] the B operand's row p is 2^-rexp[p] times the true one
   const int32_t* oexp;     // [n] kGateUp: the same of h
   // outputs
-  uint16_t* h;             // kGateUp: fp16 [n][N]
+  uint16_t* h;             // kGateUp: fp16 [n][N / 2]
   uint16_t* yh;            // kDown: fp16 [n][N], 2^-(rexp + w4_y_exp) times y, or NULL
   float* y;                // kDown: fp32 [n][N]
   void* out;               // kLinear
   size_t ldo;
   int out_f32;
+};
+
+// The rows as tensor maps with boxes of 128, 64, 32 and 16 rows x 64 inputs.
+struct W4RowMaps {
+  CUtensorMap m[4];
 };
 
 // One lane of the (converged) warp.  The loops that issue copies and MMAs are run by whole warps, so that
@@ -77,27 +93,44 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// D[tmem] (+)= A[tmem] x B[smem].
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// D[tmem of both CTAs] (+)= A[tmem of both] x B[smem of both], over one 64-deep stage: four MMAs; the first
+// accumulates when `accumulate` is nonzero.
+__device__ __forceinline__ void umma_f16_ts_pair_k64(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                                     uint32_t accumulate) {
   asm volatile(
       "{\n"
-      " .reg .pred p;\n"
+      " .reg .pred p, t;\n"
       " setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " setp.eq.b32 t, 0, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%5], %6, %3, t;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%7], %8, %3, t;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%9], %10, %3, t;\n"
       "}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(a_tmem + 8), "l"(bdesc + 2), "r"(a_tmem + 16),
+      "l"(bdesc + 4), "r"(a_tmem + 24), "l"(bdesc + 6)
       : "memory");
 }
 
+// Arrive on an mbarrier of either CTA of the pair, by its shared::cluster address.  What such an arrival
+// hands over is in TMEM, which the tcgen05 waits and fences order; a release at cluster scope would wait for
+// the thread's global stores as well (about 1,000 cycles after a drain).
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t caddr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+
 // 2^e >= 1.001 |column|_2 of every column (0 for a matrix of zeros or a norm that is not finite).
-__device__ __forceinline__ int w4_norm_exp(const uint8_t* m, const W4Dims& d) {
-  const float c = *reinterpret_cast<const float*>(m + d.meta);
+__device__ __forceinline__ int w4_norm_exp(const uint8_t* meta) {
+  const float c = *reinterpret_cast<const float*>(meta);
   return c > 0.f && c < INFINITY ? ilogbf(c) + 1 : 0;
 }
 // |y| <= |h|_2 |column|_2 <= sqrt(I) 2^15 2^hexp 2^norm_exp: the exponent that takes y / 2^hexp below 2^15.
 __device__ __forceinline__ int w4_y_exp(const uint8_t* m, const W4Dims& d) {
-  return (32 - __clz(d.K) + 1) / 2 + w4_norm_exp(m, d);
+  return (32 - __clz(d.K) + 1) / 2 + w4_norm_exp(m + d.meta);
 }
 
 // 32 lanes x 32 consecutive 32-bit columns from registers.
@@ -127,11 +160,11 @@ __device__ __forceinline__ bool w4g_slot(const W4GemmArgs& a, int li, int& e, in
 }
 
 struct W4GTile {
-  const uint8_t* base;  // the slab or matrix
+  const uint8_t* base;  // the matrix
   int ft, row0, ntok;
 };
 
-// Tile t: row tile t / NF (by the prefix of row tiles over the list), feature tile t % NF.
+// Tile t: row tile t / NF (by the prefix of row tiles over the list), column tile t % NF.
 template <int kMode>
 __device__ __forceinline__ W4GTile w4g_tile(const W4GemmArgs& a, const int* pre, int nl, int t) {
   W4GTile r;
@@ -150,18 +183,15 @@ __device__ __forceinline__ W4GTile w4g_tile(const W4GemmArgs& a, const int* pre,
     }
     int e, slot;
     w4g_slot(a, lo, e, slot);
-    r.base = a.w + (size_t)slot * a.slab;
+    r.base = a.w + (size_t)slot * a.slab + a.mat;
     r.row0 = a.offset[e] + (i - pre[lo]) * kGN;
     r.ntok = min(kGN, a.offset[e + 1] - r.row0);
   }
   return r;
 }
 
-// First tile of 16 columns of block b, and its matrix.
-template <int kMode>
-__device__ __forceinline__ int w4g_mt0(int ft, int b) {
-  return kMode == kGateUp ? ft * 8 : (2 * ft + b) * 8;
-}
+// Rows of a tile in each CTA: half the MMA's N, which is a multiple of 32.
+__device__ __forceinline__ int w4g_half(int ntok) { return ((ntok + 31) & ~31) >> 1; }
 
 // Eight codes of a word (w4.cuh) times their scale, fp16, inputs in order.
 __device__ __forceinline__ void w4_expand(uint32_t w, __half2 s, uint32_t* o) {
@@ -183,148 +213,149 @@ __device__ __forceinline__ void w4_expand(uint32_t w, __half2 s, uint32_t* o) {
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
-// Drains 32 rows (of chunk `chunk`) x this warp's 32 features of both accumulators: to registers, the
-// accumulators are handed back, then scaled, transposed through shared memory and stored.
-template <int kMode, class Wait>
-__device__ __forceinline__ void w4g_drain(const W4GemmArgs& a, const W4Dims& d, const W4GTile& ti, uint32_t taddr, int q,
-                                          int chunk, int lane, unsigned char* stage, uint64_t* tfull,
-                                          uint64_t* tempty, uint32_t tc, Wait&& wait, volatile int* abort_flag) {
-  const int tok0 = 32 * chunk;
-  const bool any = tok0 < ti.ntok, mine = tok0 + lane < ti.ntok;
-  const size_t row0 = (size_t)ti.row0 + tok0;
-  // the rows' powers of two, one lane each, for all lanes to read
-  float* fac = reinterpret_cast<float*>(stage + 4096);
-  if (any) {
-    const float rx = mine ? pow2(a.rexp[row0 + lane]) : 0.f;
-    if (kMode == kGateUp) {
-      fac[2 * lane] = rx;
-      fac[2 * lane + 1] = mine ? pow2(-a.oexp[row0 + lane]) : 0.f;
-    } else {
-      fac[lane] = kMode == kDown && a.yh ? 1.f : rx;  // scaled rows of y keep the row's own power of two apart
+// Stores 32 rows x 32 packed columns that a warp has staged in shared memory, [row][kGLd] fp32: the values
+// still lack their row's power of two.  fac[row] is that power (kGateUp: of x, then of 1 / h).
+template <int kMode>
+__device__ __forceinline__ void w4g_store(const W4GemmArgs& a, const float* st, const float* fac, size_t row0, int nrow,
+                                          int c0, int lane) {
+  const W4Dims& d = a.d;
+  if (kMode == kGateUp) {  // columns 0-15: gate, 16-31: up of the same 16 features
+    const int f0 = c0 / 2, I = d.N / 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int idx = i * 32 + lane, row = idx >> 1, seg = (idx & 1) * 8;
+      const float x = fac[row], hinv = fac[32 + row];
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 8; j += 4) {
+        const float4 g = *reinterpret_cast<const float4*>(st + row * kGLd + seg + j);
+        const float4 u = *reinterpret_cast<const float4*>(st + row * kGLd + 16 + seg + j);
+        auto h = [&](float gv, float uv) {
+          gv *= x;
+          return __fdividef(gv, 1.f + __expf(-gv)) * (uv * x) * hinv;
+        };
+        const __half2 p0 = __floats2half2_rn(h(g.x, u.x), h(g.y, u.y)), p1 = __floats2half2_rn(h(g.z, u.z), h(g.w, u.w));
+        o[j / 2] = *reinterpret_cast<const uint32_t*>(&p0);
+        o[j / 2 + 1] = *reinterpret_cast<const uint32_t*>(&p1);
+      }
+      if (row < nrow)
+        *reinterpret_cast<uint4*>(a.h + (row0 + row) * I + f0 + seg) = make_uint4(o[0], o[1], o[2], o[3]);
     }
-  }
-  __syncwarp();
-  wait(tfull, tc & 1u);
-  tc_fence_after();
-  auto release = [&] {
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(tempty);
-  };
-  if (!any) {
-    release();
     return;
   }
-  const bool store = !*abort_flag;
-  if (kMode == kGateUp) {
-    float v0[32], v1[32];
-    tmem_ld32(taddr + tok0, v0);
-    tmem_ld32(taddr + kGN + tok0, v1);
-    tmem_ld_wait();
-    release();
-    const int f0 = ti.ft * kGM + 32 * q, f = f0 + lane;
-    const float* mg = reinterpret_cast<const float*>(ti.base + a.mat0 + d.mult);
-    const float* mu = reinterpret_cast<const float*>(ti.base + a.mat1 + d.mult);
-    const float cg = f < d.N ? mg[f] : 0.f, cu = f < d.N ? mu[f] : 0.f;
-    uint16_t* st = reinterpret_cast<uint16_t*>(stage);
-#pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      const float4 m = *reinterpret_cast<const float4*>(fac + 2 * j);  // x, 1 / h of rows j, j + 1
-      const float g0 = v0[j] * cg * m.x, g1 = v0[j + 1] * cg * m.z;
-      const float u0 = v1[j] * cu * m.x, u1 = v1[j + 1] * cu * m.z;
-      st[j * 32 + lane] = __half_as_ushort(__float2half_rn(__fdividef(g0, 1.f + __expf(-g0)) * u0 * m.y));
-      st[(j + 1) * 32 + lane] = __half_as_ushort(__float2half_rn(__fdividef(g1, 1.f + __expf(-g1)) * u1 * m.w));
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // 32 rows x 64 B: four 16-byte pieces per lane
-      const int idx = i * 32 + lane, row = idx >> 2, seg = idx & 3;
-      const uint4 v = *reinterpret_cast<const uint4*>(st + row * 32 + seg * 8);
-      if (store && tok0 + row < ti.ntok && f0 + seg * 8 < d.N)
-        *reinterpret_cast<uint4*>(a.h + (row0 + row) * d.N + f0 + seg * 8) = v;
-    }
-    __syncwarp();
+  const bool f32 = kMode == kLinear ? a.out_f32 != 0 : a.yh == nullptr;
+  const size_t ld = kMode == kLinear ? a.ldo : (size_t)d.N;
+  if (kMode == kLinear && !(ld % 8 == 0 && (uintptr_t)a.out % 16 == 0 && c0 + 32 <= d.N)) {
+    // unaligned or ragged rows of out: element stores, 32 consecutive columns per row
+    if (c0 + lane < d.N)
+      for (int row = 0; row < nrow; ++row) {
+        const float v = st[row * kGLd + lane] * fac[row];
+        const size_t at = (row0 + row) * ld + c0 + lane;
+        if (f32) reinterpret_cast<float*>(a.out)[at] = v;
+        else reinterpret_cast<uint16_t*>(a.out)[at] = f32_to_bf16(v);
+      }
     return;
   }
-  const float* mc = reinterpret_cast<const float*>(ti.base + a.mat0 + d.mult);
-#pragma unroll 1
-  for (int blk = 0; blk < 2; ++blk) {
-    float v[32];
-    tmem_ld32(taddr + blk * kGN + tok0, v);
-    tmem_ld_wait();
-    if (blk == 1) release();
-    const int f0 = (2 * ti.ft + blk) * kGM + 32 * q, f = f0 + lane;
-    if (f0 >= d.N) continue;
-    float cm = f < d.N ? mc[f] : 0.f;
-    if (kMode == kDown && a.yh) cm = ldexpf(cm, -w4_y_exp(ti.base + a.mat0, d));
+  if (f32) {
+    float* out = kMode == kLinear ? reinterpret_cast<float*>(a.out) : a.y;
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      const float4 m = *reinterpret_cast<const float4*>(fac + j);
-      v[j] = v[j] * cm * m.x;
-      v[j + 1] = v[j + 1] * cm * m.y;
-      v[j + 2] = v[j + 2] * cm * m.z;
-      v[j + 3] = v[j + 3] * cm * m.w;
+    for (int i = 0; i < 8; ++i) {  // 32 rows x 128 B
+      const int idx = i * 32 + lane, row = idx >> 3, seg = (idx & 7) * 4;
+      float4 v = *reinterpret_cast<const float4*>(st + row * kGLd + seg);
+      const float m = fac[row];
+      v.x *= m, v.y *= m, v.z *= m, v.w *= m;
+      if (row < nrow) *reinterpret_cast<float4*>(out + (row0 + row) * ld + c0 + seg) = v;
     }
-    if (kMode == kLinear && !(a.ldo % 8 == 0 && (uintptr_t)a.out % 16 == 0 && f0 + 32 <= d.N)) {
-      // unaligned or ragged rows of out: element stores, 32 consecutive features per row
+  } else {
+    uint16_t* out = kMode == kLinear ? reinterpret_cast<uint16_t*>(a.out) : a.yh;
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (store && tok0 + j < ti.ntok && f < d.N) {
-          const size_t at = (row0 + j) * a.ldo + f;
-          if (a.out_f32) reinterpret_cast<float*>(a.out)[at] = v[j];
-          else reinterpret_cast<uint16_t*>(a.out)[at] = f32_to_bf16(v[j]);
+    for (int i = 0; i < 4; ++i) {  // 32 rows x 64 B
+      const int idx = i * 32 + lane, row = idx >> 2, seg = (idx & 3) * 8;
+      const float4 v0 = *reinterpret_cast<const float4*>(st + row * kGLd + seg);
+      const float4 v1 = *reinterpret_cast<const float4*>(st + row * kGLd + seg + 4);
+      const float m = fac[row];
+      uint32_t o[4];
+      const float v[8] = {v0.x * m, v0.y * m, v0.z * m, v0.w * m, v1.x * m, v1.y * m, v1.z * m, v1.w * m};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (kMode == kLinear) {
+          o[j] = uint32_t(f32_to_bf16(v[2 * j])) | (uint32_t(f32_to_bf16(v[2 * j + 1])) << 16);
+        } else {
+          const __half2 p = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+          o[j] = *reinterpret_cast<const uint32_t*>(&p);
         }
-      continue;
-    }
-    const bool f32 = kMode == kLinear ? a.out_f32 != 0 : a.yh == nullptr;
-    const size_t ld = kMode == kLinear ? a.ldo : (size_t)d.N;
-    if (f32) {
-      float* st = reinterpret_cast<float*>(stage);
-      float* out = kMode == kLinear ? reinterpret_cast<float*>(a.out) : a.y;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) st[j * 32 + lane] = v[j];
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {  // 32 rows x 128 B
-        const int idx = i * 32 + lane, row = idx >> 3, seg = idx & 7;
-        const uint4 o = *reinterpret_cast<const uint4*>(st + row * 32 + seg * 4);
-        if (store && tok0 + row < ti.ntok && f0 + seg * 4 < d.N)
-          *reinterpret_cast<uint4*>(out + (row0 + row) * ld + f0 + seg * 4) = o;
       }
-    } else {
-      uint16_t* st = reinterpret_cast<uint16_t*>(stage);
-      uint16_t* out = kMode == kLinear ? reinterpret_cast<uint16_t*>(a.out) : a.yh;
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        st[j * 32 + lane] = kMode == kLinear ? f32_to_bf16(v[j]) : __half_as_ushort(__float2half_rn(v[j]));
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {  // 32 rows x 64 B
-        const int idx = i * 32 + lane, row = idx >> 2, seg = idx & 3;
-        const uint4 o = *reinterpret_cast<const uint4*>(st + row * 32 + seg * 8);
-        if (store && tok0 + row < ti.ntok && f0 + seg * 8 < d.N)
-          *reinterpret_cast<uint4*>(out + (row0 + row) * ld + f0 + seg * 8) = o;
-      }
+      if (row < nrow) *reinterpret_cast<uint4*>(out + (row0 + row) * ld + c0 + seg) = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    __syncwarp();
   }
 }
 
+// Drains 64 rows (of set `set`) x this warp's 32 columns: to registers, the accumulators are handed back
+// (tempty of the pair's first CTA), then 32 rows at a time through shared memory to their place.
+template <int kMode, class Wait>
+__device__ __forceinline__ void w4g_drain(const W4GemmArgs& a, const W4GTile& ti, int blk, uint32_t taddr, int q, int set,
+                                          int lane, float* st, float* fac, uint64_t* tfull, uint32_t tempty0,
+                                          uint32_t parity, Wait&& wait, volatile int* abort_flag) {
+  const W4Dims& d = a.d;
+  const int tok0 = 64 * set, nrow = ti.ntok - tok0, c0 = blk * kGM + 32 * q;
+  const bool any = nrow > 0 && c0 < d.N;
+  const size_t row0 = (size_t)ti.row0 + tok0;
+  float cm = 0.f;
+  if (any) {
+    // the rows' powers of two, and the column's
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int row = 32 * c + lane;
+      const bool mine = row < nrow;
+      // scaled rows of y keep the row's own power of two apart
+      fac[64 * c + lane] = !mine ? 0.f : kMode == kDown && a.yh ? 1.f : pow2(a.rexp[row0 + row]);
+      if (kMode == kGateUp) fac[64 * c + 32 + lane] = mine ? pow2(-a.oexp[row0 + row]) : 0.f;
+    }
+    if (c0 + lane < d.N) cm = reinterpret_cast<const float*>(ti.base + d.mult)[c0 + lane];
+    if (kMode == kDown && a.yh) cm = ldexpf(cm, -w4_y_exp(ti.base, d));
+  }
+  __syncwarp();
+  wait(tfull, parity);
+  tc_fence_after();
+  float v0[32], v1[32];
+  if (any) {
+    tmem_ld32(taddr + tok0, v0);
+    tmem_ld32(taddr + tok0 + 32, v1);
+    tmem_ld_wait();
+  }
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive_pair(tempty0);
+  if (!any || *abort_flag) return;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) st[j * kGLd + lane] = v0[j] * cm;
+  __syncwarp();
+  w4g_store<kMode>(a, st, fac, row0, min(nrow, 32), c0, lane);
+  __syncwarp();
+  if (nrow <= 32) return;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) st[j * kGLd + lane] = v1[j] * cm;
+  __syncwarp();
+  w4g_store<kMode>(a, st, fac + 64, row0 + 32, min(nrow - 32, 32), c0, lane);
+  __syncwarp();
+}
+
 template <int kMode>
-__global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs a, const __grid_constant__ CUtensorMap mapX) {
+__global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs a, const __grid_constant__ W4RowMaps mapX) {
   extern __shared__ __align__(16) unsigned char gsm_raw[];
   unsigned char* sm =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(gsm_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* xs = sm;                             // [ring][16 KB]
-  unsigned char* wsm = sm + kGXRing * kGXBytes;       // [ring][codes of both blocks | scales of both blocks]
-  unsigned char* epi = wsm + kGWRing * kGWBytes;      // [workers][4 KB]
-  uint64_t* xfull = reinterpret_cast<uint64_t*>(epi + kGWorkers * kGEpiBytes);
+  unsigned char* wsm = sm + kGXRing * kGXBytes;       // [ring][codes | scales]
+  float* epi = reinterpret_cast<float*>(wsm + kGWRing * kGWBytes);   // [workers][32][kGLd]
+  float* facs = epi + kGWorkers * (kGEpiBytes / 4);   // [workers][128]
+  uint64_t* xfull = reinterpret_cast<uint64_t*>(facs + kGWorkers * 128);
   uint64_t* xempty = xfull + kGXRing;
   uint64_t* wfull = xempty + kGXRing;
   uint64_t* wempty = wfull + kGWRing;
   uint64_t* afull = wempty + kGWRing;
-  uint64_t* aempty = afull + 2;
-  uint64_t* tfull = aempty + 2;
+  uint64_t* aempty = afull + kGSets;
+  uint64_t* tfull = aempty + kGSets;
   uint64_t* tempty = tfull + 1;
   uint64_t* done = tempty + 1;
   __shared__ uint32_t s_tmem;
@@ -332,6 +363,8 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   __shared__ int s_pre[kMode == kLinear ? 1 : kMaxE + 1];
   __shared__ int s_tmp[33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int cl = (int)cluster_index(), ncl = (int)cluster_count();
   const W4Dims& d = a.d;
   const int nkb = d.Kb;
   int nl = 0, total;
@@ -343,25 +376,24 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     }
     for (int s = 0; s < kGWRing; ++s) {
       mbar_init(&wfull[s], 1);
-      mbar_init(&wempty[s], kGWorkers);
+      mbar_init(&wempty[s], 8);  // two visits of four warps
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&afull[s], kGSet);
+    for (int s = 0; s < kGSets; ++s) {
+      mbar_init(&afull[s], 8);  // a set's four warps in each CTA
       mbar_init(&aempty[s], 1);
     }
     mbar_init(tfull, 1);
-    mbar_init(tempty, kGWorkers);
+    mbar_init(tempty, 2 * kGWorkers);
     mbar_init(done, 1);
     s_abort = 0;
     mbar_fence_init();
   }
   if (warp == 1) {
-    tmem_alloc(&s_tmem, kGTmemCols);
-    tmem_relinquish();
+    tmem_alloc_pair(&s_tmem, kGTmemCols);
+    tmem_relinquish_pair();
   }
   if (kMode == kLinear) {
     total = (a.n + kGN - 1) / kGN * a.NF;
-    __syncthreads();
   } else {
     // prefix of the listed experts' row tiles
     nl = min(*a.n_list, kMaxE);
@@ -376,11 +408,11 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
       carry += tot;
     }
     if (threadIdx.x == 0) s_pre[nl] = carry;
-    __syncthreads();
     total = carry * a.NF;
   }
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();  // barriers of both CTAs initialised, TMEM allocated on both, prefix complete
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* abort_flag = &s_abort;
@@ -393,159 +425,171 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   };
 
   if (warp == 0) {
-    uint32_t xi = 0, wi = 0;  // stages of rows and chunks of codes issued
+    uint32_t xi = 0;  // stages issued
     bool dead = false;
     const bool lead = elect_one();
-    for (int t = blockIdx.x; t < total && !dead; t += gridDim.x) {
+    for (int t = cl; t < total && !dead; t += ncl) {
       const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
-      const int mt0 = w4g_mt0<kMode>(ti.ft, 0), mt1 = w4g_mt0<kMode>(ti.ft, 1);
-      // the tiles of 16 columns that exist, per block
-      const uint32_t nm0 = min(8, d.Mt - mt0), nm1 = max(0, min(8, d.Mt - mt1));
-      const uint8_t *m0 = ti.base + a.mat0, *m1 = ti.base + a.mat1;
+      const int r = w4g_half(ti.ntok), row = ti.row0 + (int)rank * r;
       for (int kb = 0; kb < nkb; ++kb, ++xi) {
-        if (kb % kGChunk == 0) {
-          const uint32_t s = wi % kGWRing, use = wi / kGWRing, nb = min(kGChunk, nkb - kb);
-          const uint32_t ng = d.G == 128 ? (nb + 1) / 2 : d.G == 64 ? nb : 2 * nb;
-          const int kg = kb * kGK / d.G;
-          if (use > 0) wait(&wempty[s], (use - 1) & 1u);
-          dead = __any_sync(MOE_FULL_MASK, *abort_flag);
-          if (dead) break;
-          unsigned char* dst = wsm + s * kGWBytes;
-          if (lead) {
-            mbar_expect_tx(&wfull[s], (nm0 + nm1) * (512 * nb + 32 * ng));
-            bulk_load(dst, m0 + w4_code_at(d, mt0, kb) * 512, nm0 * 512 * nb, &wfull[s]);
-            bulk_load(dst + 2 * kGCodeBlock, m0 + d.scales + w4_scale_at(d, mt0, kg) * 32, nm0 * 32 * ng, &wfull[s]);
-            if (nm1 > 0) {
-              bulk_load(dst + kGCodeBlock, m1 + w4_code_at(d, mt1, kb) * 512, nm1 * 512 * nb, &wfull[s]);
-              bulk_load(dst + 2 * kGCodeBlock + kGScaleBlock, m1 + d.scales + w4_scale_at(d, mt1, kg) * 32,
-                        nm1 * 32 * ng, &wfull[s]);
-            }
-          }
-          __syncwarp();
-          ++wi;
-        }
         const uint32_t s = xi % kGXRing, use = xi / kGXRing;
         if (use > 0) wait(&xempty[s], (use - 1) & 1u);
         dead = __any_sync(MOE_FULL_MASK, *abort_flag);
         if (dead) break;
         if (lead) {
-          mbar_expect_tx(&xfull[s], kGXBytes);
-          tma_load_3d(xs + s * kGXBytes, &mapX, &xfull[s], kb * kGK, ti.row0, 0);
+          // the first CTA's barrier counts the bytes of both
+          if (rank == 0) mbar_expect_tx(&xfull[s], 2u * (uint32_t)r * (kGK * 2));
+          const uint32_t fb = mapa_shared(smem_u32(&xfull[s]), 0);
+          unsigned char* dst = xs + s * kGXBytes;
+          if (r == kGRows) {
+            tma_load_3d_pair(dst, &mapX.m[0], fb, kb * kGK, row, 0);
+          } else {
+            int o = 0;
+            if (r & 64) {
+              tma_load_3d_pair(dst, &mapX.m[1], fb, kb * kGK, row, 0);
+              o = 64;
+            }
+            if (r & 32) {
+              tma_load_3d_pair(dst + o * 128, &mapX.m[2], fb, kb * kGK, row + o, 0);
+              o += 32;
+            }
+            if (r & 16) tma_load_3d_pair(dst + o * 128, &mapX.m[3], fb, kb * kGK, row + o, 0);
+          }
         }
         __syncwarp();
       }
     }
-    // after a timeout: let every copy land before the CTA can exit
-    if (dead) {
+    // after a timeout: let every copy land before the CTAs can exit
+    if (dead && rank == 0)
       for (uint32_t j = xi > kGXRing ? xi - kGXRing : 0; j < xi; ++j) mbar_wait(&xfull[j % kGXRing], (j / kGXRing) & 1u);
-      for (uint32_t j = wi > kGWRing ? wi - kGWRing : 0; j < wi; ++j) mbar_wait(&wfull[j % kGWRing], (j / kGWRing) & 1u);
-    }
-  } else if (warp == 1) {
-    const uint64_t bd0 = smem_desc_l(smem_u32(xs), 16, 1024, kLayoutSw128);
+  } else if (warp == kGWorkers + 2) {
+    uint32_t wi = 0;  // chunks issued
+    bool dead = false;
     const bool lead = elect_one();
-    uint32_t xi = 0, vi = 0, tc = 0;  // stages of rows, visits, tiles
-    for (int t = blockIdx.x; t < total && !__any_sync(MOE_FULL_MASK, *abort_flag); t += gridDim.x, ++tc) {
+    for (int t = cl; t < total && !dead; t += ncl) {
       const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
-      const uint32_t idesc = idesc_f16(kGM, (ti.ntok + 15) & ~15);
-      const bool two = kMode == kGateUp || w4g_mt0<kMode>(ti.ft, 1) < d.Mt;
-      if (tc > 0) wait(tempty, (tc - 1) & 1u);
-      for (int kb = 0; kb < nkb; ++vi) {
-        const uint32_t as = vi & 1;
-        wait(&afull[as], (vi >> 1) & 1u);
-#pragma unroll
-        for (int h = 0; h < kGVisit; ++h, ++kb, ++xi) {
-          if (kb >= nkb) break;
-          const uint32_t s = xi % kGXRing;
-          wait(&xfull[s], (xi / kGXRing) & 1u);
-          tc_fence_after();
-          const uint32_t ac = tmem + kGACol + as * 128 + h * 32;
-          const uint64_t bd = bd0 + (uint64_t)(s * (kGXBytes >> 4));
-          if (lead) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) umma_f16_ts(tmem, ac + 8 * k, bd + 2 * k, idesc, kb > 0 || k > 0);
-            if (two)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) umma_f16_ts(tmem + kGN, ac + 64 + 8 * k, bd + 2 * k, idesc, kb > 0 || k > 0);
-            umma_commit(&xempty[s]);
+      const int blk = 2 * ti.ft + (int)rank;
+      const uint32_t nm = max(0, min(8, d.Mt - 8 * blk));  // the tiles of 16 columns that exist
+      for (int kb = 0; kb < nkb; kb += kGChunk, ++wi) {
+        const uint32_t s = wi % kGWRing, use = wi / kGWRing, nb = min(kGChunk, nkb - kb);
+        const uint32_t ng = d.G == 128 ? (nb + 1) / 2 : d.G == 64 ? nb : 2 * nb;
+        if (use > 0) wait(&wempty[s], (use - 1) & 1u);
+        dead = __any_sync(MOE_FULL_MASK, *abort_flag);
+        if (dead) break;
+        unsigned char* dst = wsm + s * kGWBytes;
+        if (lead) {
+          if (nm > 0) {
+            mbar_expect_tx(&wfull[s], nm * (512 * nb + 32 * ng));
+            bulk_load(dst, ti.base + w4_code_at(d, 8 * blk, kb) * 512, nm * 512 * nb, &wfull[s]);
+            bulk_load(dst + kGCodeBytes, ti.base + d.scales + w4_scale_at(d, 8 * blk, kb * kGK / d.G) * 32, nm * 32 * ng,
+                      &wfull[s]);
+          } else {
+            mbar_arrive(&wfull[s]);  // the pair's second CTA has no columns here: its results are dropped
           }
+        }
+        __syncwarp();
+      }
+    }
+    if (dead)
+      for (uint32_t j = wi > kGWRing ? wi - kGWRing : 0; j < wi; ++j) mbar_wait(&wfull[j % kGWRing], (j / kGWRing) & 1u);
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const uint64_t bd0 = smem_desc_l(smem_u32(xs), 16, 1024, kLayoutSw128);
+      const bool lead = elect_one();
+      uint32_t xi = 0, vi = 0, tc = 0;  // stages of rows, visits, tiles
+      for (int t = cl; t < total && !__any_sync(MOE_FULL_MASK, *abort_flag); t += ncl, ++tc) {
+        const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
+        const uint32_t idesc = idesc_f16(2 * kGM, 2 * w4g_half(ti.ntok));
+        if (tc > 0) wait(tempty, (tc - 1) & 1u);
+        for (int kb = 0; kb < nkb; ++vi) {
+          const uint32_t as = vi % kGSets;
+          wait(&afull[as], (vi / kGSets) & 1u);
+#pragma unroll
+          for (int h = 0; h < kGVisit; ++h, ++kb, ++xi) {
+            if (kb >= nkb) break;
+            const uint32_t s = xi % kGXRing;
+            wait(&xfull[s], (xi / kGXRing) & 1u);
+            tc_fence_after();
+            if (lead) {
+              umma_f16_ts_pair_k64(tmem, tmem + kGACol + as * 64 + h * 32, bd0 + (uint64_t)(s * (kGXBytes >> 4)), idesc,
+                                   kb > 0);
+              umma_commit_pair(&xempty[s]);
+            }
+            __syncwarp();
+          }
+          if (lead) umma_commit_pair(&aempty[as]);
           __syncwarp();
         }
-        if (lead) umma_commit(&aempty[as]);
+        if (lead) umma_commit_pair(tfull);
         __syncwarp();
       }
-      if (lead) umma_commit(tfull);
+      if (lead) umma_commit_pair(done);  // completes in both CTAs once every MMA has finished
       __syncwarp();
     }
-    if (lead) umma_commit(done);
-    __syncwarp();
     mbar_wait(done, 0);
   } else {
-    // TMEM lane quarter; block and set (dequantising); 32-row chunk of the tile (draining)
-    const int q = warp & 3, b = ((warp - 2) >> 2) & 1, set = (warp - 2) >> 3, chunk = (warp - 2) >> 2;
+    const int q = warp & 3, set = (warp - 2) >> 2;  // TMEM lane quarter; visits (dequantising) and rows (draining)
     const int r = 32 * q + lane, g = r & 7, hi = (r >> 3) & 1;
-    const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
-    const uint32_t a_addr = tmem + lane_addr + kGACol + set * 128 + b * 64;
-    unsigned char* stage = epi + (warp - 2) * kGEpiBytes;
+    const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
+    const uint32_t a_addr = lane_addr + kGACol + set * 64;
+    float* st = epi + (warp - 2) * (kGEpiBytes / 4);
+    float* fac = facs + (warp - 2) * 128;
+    const uint32_t afull0 = mapa_shared(smem_u32(&afull[set]), 0), tempty0 = mapa_shared(smem_u32(tempty), 0);
     uint32_t vi = 0, wi = 0, tc = 0;  // visits, chunks before this tile, tiles drained
     W4GTile prev = {};
     bool pending = false;  // prev has not been drained
-    for (int t = blockIdx.x;; t += gridDim.x) {
+    for (int t = cl;; t += ncl) {
       const bool real = t < total && !__any_sync(MOE_FULL_MASK, *abort_flag);
       W4GTile ti = {};
       if (real) ti = w4g_tile<kMode>(a, s_pre, nl, t);
-      const int nm = max(1, min(8, d.Mt - w4g_mt0<kMode>(ti.ft, b))), nk = real ? nkb : 0;
+      const int nm = max(1, min(8, d.Mt - 8 * (2 * ti.ft + (int)rank))), nk = real ? nkb : 0;
       // one visit of each set, the last tile's drain, the other visits
       int kb = 0;
 #pragma unroll 1
       for (int phase = 0; phase < 2; ++phase) {
+        const int end = phase ? nk : min(nk, kGSets * kGVisit);
 #pragma unroll 1
-      for (const int end = phase ? nk : min(nk, 2 * kGVisit); kb < end; kb += kGVisit, ++vi) {
-        // a chunk of codes holds two visits, one of each set; a tile starts a chunk of its own
-        const uint32_t c = wi + kb / kGChunk, ws = c % kGWRing;
-        if ((vi & 1) != (uint32_t)set) {
-          if (kb % kGChunk == 0 && kb + kGVisit >= nkb) {  // a last chunk without a visit of this set
-            wait(&wfull[ws], (c / kGWRing) & 1u);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&wempty[ws]);
+        for (; kb < end; kb += kGVisit, ++vi) {
+          if (vi % kGSets != (uint32_t)set) continue;
+          // a chunk of codes holds two visits; a tile starts a chunk of its own
+          const uint32_t c = wi + kb / kGChunk, ws = c % kGWRing;
+          wait(&wfull[ws], (c / kGWRing) & 1u);
+          const unsigned char* wst = wsm + ws * kGWBytes;
+          uint32_t o[32];
+#pragma unroll
+          for (int h = 0; h < kGVisit; ++h) {
+            if (kb + h >= nkb) break;
+            const int j4 = kb % kGChunk + h;
+            const unsigned char* code = wst + (j4 * nm + (r >> 4)) * 512 + g * 64 + hi * 8;
+            const int gi = d.G == 128 ? j4 >> 1 : d.G == 64 ? j4 : 2 * j4;
+            const __half* sp = reinterpret_cast<const __half*>(wst + kGCodeBytes + (gi * nm + (r >> 4)) * 32 + g * 4) + hi;
+            uint2 w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint2*>(code + ((j + (g >> 1)) & 3) * 16);
+            const __half2 s0 = __half2half2(sp[0]), s1 = d.G == 32 ? __half2half2(sp[16 * nm]) : s0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              w4_expand(w[j].x, s0, &o[4 * j]);
+              w4_expand(w[j].y, s1, &o[16 + 4 * j]);
+            }
+            if (h == 0 && vi >= kGSets) wait(&aempty[set], (vi / kGSets - 1) & 1u);
+            tc_fence_after();
+            tmem_st32(a_addr + 32 * h, o);
           }
-          continue;
-        }
-        wait(&wfull[ws], (c / kGWRing) & 1u);
-        const unsigned char* wst = wsm + ws * kGWBytes;
-        uint32_t o[32];
-#pragma unroll
-        for (int h = 0; h < kGVisit; ++h) {
-          if (kb + h >= nkb) break;
-          const int j4 = kb % kGChunk + h;
-          const unsigned char* code = wst + b * kGCodeBlock + (j4 * nm + (r >> 4)) * 512 + g * 64 + hi * 8;
-          const int gi = d.G == 128 ? j4 >> 1 : d.G == 64 ? j4 : 2 * j4;
-          const __half* sp = reinterpret_cast<const __half*>(wst + 2 * kGCodeBlock + b * kGScaleBlock +
-                                                             (gi * nm + (r >> 4)) * 32 + g * 4) + hi;
-          uint2 w[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint2*>(code + ((j + (g >> 1)) & 3) * 16);
-          const __half2 s0 = __half2half2(sp[0]), s1 = d.G == 32 ? __half2half2(sp[16 * nm]) : s0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            w4_expand(w[j].x, s0, &o[4 * j]);
-            w4_expand(w[j].y, s1, &o[16 + 4 * j]);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive_pair(afull0);
+            // a last chunk of one visit counts it twice
+            mbar_arrive_n(&wempty[ws], kb % kGChunk == 0 && kb + kGVisit >= nkb ? 2 : 1);
           }
-          if (h == 0 && vi >= 2) wait(&aempty[set], ((vi >> 1) - 1) & 1u);
-          tc_fence_after();
-          tmem_st32(a_addr + 32 * h, o);
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&afull[set]);
-          mbar_arrive(&wempty[ws]);
+        if (phase == 0 && pending) {
+          w4g_drain<kMode>(a, prev, 2 * prev.ft + (int)rank, lane_addr, q, set, lane, st, fac, tfull, tempty0, tc & 1u,
+                           wait, abort_flag);
+          ++tc;
         }
-      }
-      if (phase == 0 && pending) {
-        w4g_drain<kMode>(a, d, prev, tmem + lane_addr, q, chunk, lane, stage, tfull, tempty, tc, wait, abort_flag);
-        ++tc;
-      }
       }
       if (!real) break;
       prev = ti;
@@ -553,12 +597,14 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
       wi += (nkb + kGChunk - 1) / kGChunk;
     }
   }
+  // reconverge before the cluster barrier, which also keeps each CTA's shared memory alive while its peer
+  // may still signal it
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kGTmemCols);
+    tmem_dealloc_pair(tmem, kGTmemCols);
   }
 }
 
@@ -578,8 +624,7 @@ struct W4RowArgs {
   W4GemmArgs g;
   const int32_t* rows;
   int k;
-  W4Dims dn;               // the down matrix, and where it starts in a slab
-  size_t mat2;
+  W4Slab sl;
   int32_t *hexp, *yexp;    // [n]
   float* y;                // rows of experts without a slot are zeroed, or NULL (yexp says so)
 };
@@ -658,8 +703,8 @@ __global__ void __launch_bounds__(kRowThreads) w4_group_rows_kernel(const W4RowA
         a.yexp[p] = kNoRow;
       }
       if (a.y)
-        for (int c = lane; c < a.dn.N / 4; c += 32)
-          reinterpret_cast<float4*>(a.y + (size_t)p * a.dn.N)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = lane; c < a.sl.dn.N / 4; c += 32)
+          reinterpret_cast<float4*>(a.y + (size_t)p * a.sl.dn.N)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
       continue;
     }
     int xe, ln;
@@ -667,11 +712,11 @@ __global__ void __launch_bounds__(kRowThreads) w4_group_rows_kernel(const W4RowA
     if (lane == 0) {
       const uint8_t* base = a.g.w + (size_t)slot * a.g.slab;
       // |h| <= |g| |u| <= |x|^2 |Wg| |Wu|; h 2^-hexp stays below 2^15
-      const int b = ln + 2 * xe + w4_norm_exp(base + a.g.mat0, a.g.d) + w4_norm_exp(base + a.g.mat1, a.g.d);
+      const int b = ln + 2 * xe + w4_norm_exp(base + a.sl.gu.meta) + w4_norm_exp(base + a.sl.up_meta);
       const int he = min(max(b - 15, -126), 126);
       a.xexp[p] = xe;
       a.hexp[p] = he;
-      a.yexp[p] = he + w4_y_exp(base + a.mat2, a.dn);
+      a.yexp[p] = he + w4_y_exp(base + a.sl.dn_at, a.sl.dn);
     }
   }
 }
@@ -706,28 +751,52 @@ __global__ void __launch_bounds__(128) w4_combine_kernel(const uint16_t* __restr
 }
 
 constexpr size_t kGSmem = 1024 + (size_t)kGXRing * kGXBytes + (size_t)kGWRing * kGWBytes +
-                          (size_t)kGWorkers * kGEpiBytes + 64 * sizeof(uint64_t);
+                          (size_t)kGWorkers * (kGEpiBytes + 128 * 4) + 64 * sizeof(uint64_t);
 static_assert(kGSmem <= 222 * 1024, "shared memory of a CTA, with the 4.3 KB of static arrays");
 
-// [n][K] 16-bit rows; a box is one stage of one row tile (128 rows x 64 inputs; what lies outside reads as 0).
-static int row_map(CUtensorMap* m, const void* base, int n, int K) {
+// [n][K] 16-bit rows; boxes of 128, 64, 32 and 16 rows x one stage (what lies outside reads as 0).
+static int row_maps(W4RowMaps* rm, const void* base, int n, int K) {
   const uint64_t d[3] = {(uint64_t)K, (uint64_t)n, 1};
   const uint64_t s[2] = {(uint64_t)K * 2, (uint64_t)n * K * 2};
-  const uint32_t b[3] = {kGK, kGN, 1};
-  return encode_tmap_3d_bf16(m, base, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t b[3] = {kGK, (uint32_t)(kGRows >> i), 1};
+    const int r = encode_tmap_3d_bf16(&rm->m[i], base, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (r != MOE_OK) return r;
+  }
+  return MOE_OK;
 }
 
+// Persistent CTA pairs: as many clusters of two as fit at once (one CTA per SM).
 template <int kMode>
 static int launch_gemm(const W4GemmArgs& g, const void* rows, cudaStream_t s) {
   static bool done[64] = {};
+  static int clusters[64] = {};
   MOE_CUDA_TRY(ensure_smem(w4_gemm_kernel<kMode>, (int)kGSmem, done));
-  int dev = 0, sms = 0;
+  int dev = 0;
   MOE_CUDA_TRY(cudaGetDevice(&dev));
-  MOE_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-  CUtensorMap m;
-  if (row_map(&m, rows, g.n, g.K) != MOE_OK) return MOE_ERR_CUDA;
-  w4_gemm_kernel<kMode><<<sms, kGThreads, kGSmem, s>>>(g, m);
-  MOE_LAUNCH_CHECK();
+  W4RowMaps m;
+  if (row_maps(&m, rows, g.n, g.K) != MOE_OK) return MOE_ERR_CUDA;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kGThreads);
+  cfg.dynamicSmemBytes = kGSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (clusters[dev] == 0) {
+    int sms = 0, n = 0;
+    MOE_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    cfg.gridDim = dim3((unsigned)(sms & ~1));
+    MOE_CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, (void*)w4_gemm_kernel<kMode>, &cfg));
+    if (n < 1) return MOE_ERR_CUDA;
+    clusters[dev] = n;
+  }
+  cfg.gridDim = dim3((unsigned)(2 * clusters[dev]));
+  MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, w4_gemm_kernel<kMode>, g, m));
   return MOE_OK;
 }
 
@@ -775,12 +844,12 @@ int launch_ffn_w4_gemm(const FfnArgs& f, int group, void* ws, const uint16_t** y
   r.hexp = (int32_t*)take(4 * n);
   r.yexp = (int32_t*)take(4 * n);
   W4GemmArgs g{};
-  g.w = (const uint8_t*)f.pool, g.slab = sl.bytes, g.d = sl.gu, g.mat0 = 0, g.mat1 = sl.gu.bytes;
-  g.K = f.H, g.n = (int)n, g.NF = (f.I + kGM - 1) / kGM;
+  g.w = (const uint8_t*)f.pool, g.slab = sl.bytes, g.d = sl.gu, g.mat = 0;
+  g.K = f.H, g.n = (int)n, g.NF = (2 * f.I + 2 * kGM - 1) / (2 * kGM);
   g.offset = f.offset, g.list_e = f.list_e, g.n_list = f.n_list, g.e2s = f.e2s, g.list_s = f.list_s;
   g.E = f.E, g.S = f.S, g.status = f.status;
   g.rexp = r.xexp, g.oexp = r.hexp, g.h = h;
-  r.g = g, r.rows = f.rows, r.k = f.k, r.dn = sl.dn, r.mat2 = 2 * sl.gu.bytes;
+  r.g = g, r.rows = f.rows, r.k = f.k, r.sl = sl;
   r.y = yh ? nullptr : f.y;
   if (prof) prof->begin(MOE_PROF_FFN_ROWS, s);
   w4_group_rows_kernel<<<(int)std::min((n + 7) / 8, (size_t)1216), kRowThreads, 0, s>>>(r);
@@ -791,7 +860,7 @@ int launch_ffn_w4_gemm(const FfnArgs& f, int group, void* ws, const uint16_t** y
   if (rc != MOE_OK) return rc;
   if (prof) prof->end(s);
   W4GemmArgs gd = g;
-  gd.d = sl.dn, gd.mat0 = gd.mat1 = 2 * sl.gu.bytes;
+  gd.d = sl.dn, gd.mat = sl.dn_at;
   gd.K = f.I, gd.NF = (f.H + 2 * kGM - 1) / (2 * kGM);
   gd.rexp = r.hexp, gd.oexp = nullptr, gd.h = nullptr;
   gd.y = f.y;

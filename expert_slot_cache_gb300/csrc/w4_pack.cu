@@ -7,10 +7,18 @@
 
 namespace moe {
 
-// The matrices of one call: `count` items of one (a matrix) or three (a slab) matrices each.
+// One matrix of a call: where its columns come from and where it goes.
+struct W4PackMat {
+  W4Dims d;
+  int paired;           // gate and up: tile t of 16 columns is tile t / 2 of source t % 2 (N / 2 columns each)
+  size_t src, scale;    // first element of its codes or weights, and of its scales, in an item
+  size_t dst, meta;     // byte offsets in an item's packed form: the matrix, and a paired one's second meta
+};
+
+// The matrices of one call: `count` items of one matrix or, for a slab, two (gate / up, down).
 struct W4PackArgs {
-  int mats;            // 1, or 3: gate, up, down
-  W4Dims d[2];         // of matrices 0 (and 1), and of 2
+  int mats;
+  W4PackMat m[2];
   const uint8_t* codes;     // [item][...] bytes 0..15, or NULL: quantise `w`
   const uint16_t* scales;   // bf16 [item][...]
   const uint16_t* w;        // bf16 [item][...] weights
@@ -18,15 +26,15 @@ struct W4PackArgs {
   uint8_t* dst;
 };
 
-__device__ __forceinline__ const W4Dims& pack_dims(const W4PackArgs& a, int m) { return a.d[m == 2]; }
-__device__ __forceinline__ size_t pack_src(const W4PackArgs& a, int m) {
-  return m * (size_t)a.d[0].K * a.d[0].N;
-}
 // Groups of the source's scale array: ceil(K / G) (the packed form may hold one more).
-__device__ __forceinline__ int src_groups(const W4Dims& d) { return (d.K + d.G - 1) / d.G; }
-__device__ __forceinline__ size_t pack_scale_src(const W4PackArgs& a, int m) {
-  return m * (size_t)src_groups(a.d[0]) * a.d[0].N;
+__host__ __device__ __forceinline__ int src_groups(const W4Dims& d) { return (d.K + d.G - 1) / d.G; }
+// Source column of packed column n: its offset among the rows' first elements (of codes: k = 0; of scales: group 0).
+__device__ __forceinline__ size_t src_col(const W4PackMat& m, int n, int rows) {
+  if (!m.paired) return n;
+  const int t = n >> 4;
+  return (size_t)(t & 1) * rows * (m.d.N / 2) + (t >> 1) * 16 + (n & 15);
 }
+__device__ __forceinline__ int src_ld(const W4PackMat& m) { return m.paired ? m.d.N / 2 : m.d.N; }
 
 constexpr int kPackCols = 128;  // output columns of a CTA: 8 tiles
 constexpr int kPackRows = 128;  // inputs of a CTA: whole groups for every group size
@@ -35,39 +43,40 @@ constexpr int kPackRows = 128;  // inputs of a CTA: whole groups for every group
 // The scales are left in the packed array as raw bf16; w4_scale_kernel normalises them.
 __global__ void __launch_bounds__(256) w4_pack_kernel(const W4PackArgs a) {
   __shared__ uint8_t sc[kPackRows][kPackCols + 4];
-  const int m = blockIdx.z % a.mats;
+  const W4PackMat& m = a.m[blockIdx.z % a.mats];
   const size_t item = blockIdx.z / a.mats;
-  const W4Dims d = pack_dims(a, m);
-  const int k0 = blockIdx.x * kPackRows, n0 = blockIdx.y * kPackCols;
+  const W4Dims& d = m.d;
+  const int k0 = blockIdx.x * kPackRows, n0 = blockIdx.y * kPackCols, ld = src_ld(m);
   if (k0 >= d.Kb * 64 || n0 >= d.Mt * 16) return;
-  uint8_t* dst = a.dst + item * a.dst_item + m * a.d[0].bytes;
+  uint8_t* dst = a.dst + item * a.dst_item + m.dst;
   uint16_t* dsc = reinterpret_cast<uint16_t*>(dst + d.scales);
   const int rows = min(kPackRows, d.Kb * 64 - k0);
   const int gpc = kPackRows / d.G;  // groups of this CTA's inputs
   if (a.codes) {
-    const uint8_t* src = a.codes + item * a.src_item + pack_src(a, m);
+    const uint8_t* src = a.codes + item * a.src_item + m.src;
     for (int i = threadIdx.x; i < rows * kPackCols; i += 256) {
       const int r = i / kPackCols, c = i % kPackCols, k = k0 + r, n = n0 + c;
-      sc[r][c] = k < d.K && n < d.N ? src[(size_t)k * d.N + n] & 15 : 8;
+      sc[r][c] = k < d.K && n < d.N ? src[src_col(m, n, d.K) + (size_t)k * ld] & 15 : 8;
     }
-    const uint16_t* ss = a.scales + item * a.scale_item + pack_scale_src(a, m);
+    const uint16_t* ss = a.scales + item * a.scale_item + m.scale;
     for (int i = threadIdx.x; i < gpc * kPackCols; i += 256) {
       const int g = k0 / d.G + i / kPackCols, n = n0 + i % kPackCols;
       if (g < d.Kg && n < d.Mt * 16)
         dsc[w4_scale_at(d, n >> 4, g) * 16 + (n & 7) * 2 + ((n >> 3) & 1)] =
-            g < src_groups(d) && n < d.N ? ss[(size_t)g * d.N + n] : 0;
+            g < src_groups(d) && n < d.N ? ss[src_col(m, n, src_groups(d)) + (size_t)g * ld] : 0;
     }
   } else {
-    const uint16_t* src = a.w + item * a.src_item + pack_src(a, m);
+    const uint16_t* src = a.w + item * a.src_item + m.src;
     for (int i = threadIdx.x; i < gpc * kPackCols; i += 256) {
       const int lg = i / kPackCols, c = i % kPackCols, g = k0 / d.G + lg, n = n0 + c;
       if (g >= d.Kg) continue;
       const int kb = k0 + lg * d.G, ke = min(kb + d.G, d.K);
       // the weight furthest from zero gets code 0: scale = w / -8, rounded to bf16
       float hi = 0.f, lo = 0.f;
+      const uint16_t* col = src + src_col(m, min(n, d.N - 1), d.K);
       if (n < d.N)
         for (int k = kb; k < ke; ++k) {
-          const float v = bf16_to_f32(src[(size_t)k * d.N + n]);
+          const float v = bf16_to_f32(col[(size_t)k * ld]);
           hi = fmaxf(hi, v);
           lo = fminf(lo, v);
         }
@@ -76,7 +85,7 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const W4PackArgs a) {
       for (int k = kb; k < min(kb + d.G, d.Kb * 64); ++k) {
         int code = 8;
         if (n < d.N && k < ke && s != 0.f) {
-          const float q = rintf(__fdiv_rn(bf16_to_f32(src[(size_t)k * d.N + n]), s));
+          const float q = rintf(__fdiv_rn(bf16_to_f32(col[(size_t)k * ld]), s));
           code = (int)fminf(fmaxf(q, -8.f), 7.f) + 8;
         }
         sc[k - k0][c] = (uint8_t)code;
@@ -103,12 +112,12 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const W4PackArgs a) {
 // largest column 2-norm of the matrix (meta[0], zeroed before; an integer maximum of non-negative
 // floats, so the order of the columns does not matter).
 __global__ void __launch_bounds__(128) w4_scale_kernel(const W4PackArgs a) {
-  const int m = blockIdx.y % a.mats;
+  const W4PackMat& m = a.m[blockIdx.y % a.mats];
   const size_t item = blockIdx.y / a.mats;
-  const W4Dims d = pack_dims(a, m);
+  const W4Dims& d = m.d;
   const int n = blockIdx.x * 128 + threadIdx.x;
   if (n >= d.Mt * 16) return;
-  uint8_t* dst = a.dst + item * a.dst_item + m * a.d[0].bytes;
+  uint8_t* dst = a.dst + item * a.dst_item + m.dst;
   const int tile = n >> 4, g = n & 7, h = (n >> 3) & 1;
   uint16_t* sc = reinterpret_cast<uint16_t*>(dst + d.scales) + g * 2 + h;
   float amax = 0.f;
@@ -137,23 +146,26 @@ __global__ void __launch_bounds__(128) w4_scale_kernel(const W4PackArgs a) {
   }
   reinterpret_cast<float*>(dst + d.mult)[n] = ldexpf(1.f, e);
   // 1e-3 up: the sum above is rounded, the bound must not be below the norm
-  atomicMax(reinterpret_cast<int*>(dst + d.meta), __float_as_int(ldexpf(sqrtf(norm) * 1.001f, e)));
+  uint8_t* meta = m.paired && (tile & 1) ? a.dst + item * a.dst_item + m.meta : dst + d.meta;
+  atomicMax(reinterpret_cast<int*>(meta), __float_as_int(ldexpf(sqrtf(norm) * 1.001f, e)));
 }
 
 __global__ void w4_meta_kernel(const W4PackArgs a, int n) {
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= n) return;
-  const int m = i % a.mats;
-  uint8_t* dst = a.dst + (size_t)(i / a.mats) * a.dst_item + m * a.d[0].bytes;
-  *reinterpret_cast<float4*>(dst + pack_dims(a, m).meta) = make_float4(0.f, 0.f, 0.f, 0.f);
+  const W4PackMat& m = a.m[i % a.mats];
+  uint8_t* item = a.dst + (size_t)(i / a.mats) * a.dst_item;
+  *reinterpret_cast<float4*>(item + m.dst + m.d.meta) = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (m.paired) *reinterpret_cast<float4*>(item + m.meta) = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 static int launch_pack(const W4PackArgs& a, int count, cudaStream_t s) {
   int kc = 0, nc = 0, sc = 0;
-  for (int i = 0; i < (a.mats == 3 ? 2 : 1); ++i) {
-    kc = std::max(kc, (a.d[i].Kb * 64 + kPackRows - 1) / kPackRows);
-    nc = std::max(nc, (a.d[i].Mt * 16 + kPackCols - 1) / kPackCols);
-    sc = std::max(sc, (a.d[i].Mt * 16 + 127) / 128);
+  for (int i = 0; i < a.mats; ++i) {
+    const W4Dims& d = a.m[i].d;
+    kc = std::max(kc, (d.Kb * 64 + kPackRows - 1) / kPackRows);
+    nc = std::max(nc, (d.Mt * 16 + kPackCols - 1) / kPackCols);
+    sc = std::max(sc, (d.Mt * 16 + 127) / 128);
   }
   if (nc > 65535) return MOE_ERR_ARG;
   const int per = 65535 / a.mats;  // items per launch: the grid's z
@@ -180,11 +192,11 @@ static int pack_matrix(const uint8_t* codes, const uint16_t* scales, const uint1
   if ((uintptr_t)dst % 16) return MOE_ERR_ALIGN;
   W4PackArgs a{};
   a.mats = 1;
-  a.d[0] = a.d[1] = w4_dims(K, N, G);
+  a.m[0].d = w4_dims(K, N, G);
   a.codes = codes, a.scales = scales, a.w = w;
   a.src_item = (size_t)K * N;
   a.scale_item = (size_t)((K + G - 1) / G) * N;
-  a.dst_item = a.d[0].bytes;
+  a.dst_item = a.m[0].d.bytes;
   a.dst = (uint8_t*)dst;
   return launch_pack(a, n, s);
 }
@@ -195,8 +207,9 @@ static int pack_slabs(const uint8_t* codes, const uint16_t* scales, const uint16
   if ((uintptr_t)dst % 16) return MOE_ERR_ALIGN;
   const W4Slab sl = w4_slab(H, I, G);
   W4PackArgs a{};
-  a.mats = 3;
-  a.d[0] = sl.gu, a.d[1] = sl.dn;
+  a.mats = 2;
+  a.m[0] = W4PackMat{sl.gu, 1, 0, 0, 0, sl.up_meta};
+  a.m[1] = W4PackMat{sl.dn, 0, (size_t)2 * H * I, (size_t)2 * ((H + G - 1) / G) * I, sl.dn_at, 0};
   a.codes = codes, a.scales = scales, a.w = w;
   a.src_item = (size_t)3 * H * I;
   a.scale_item = (size_t)2 * ((H + G - 1) / G) * I + (size_t)((I + G - 1) / G) * H;
