@@ -21,8 +21,8 @@
 //
 // Warps: 0 loads the rows, the last one the codes (which run further ahead), 1 allocates TMEM and, in the
 // pair's first CTA, issues the MMAs (one lane); 2-17 are workers: four sets of four warps (one per TMEM lane quarter) that dequantise 128 inputs in turn, each
-// set into TMEM columns of its own; all drain the accumulators.  Before a tile is drained every set has
-// dequantised its first inputs of the next one, so the MMAs go on while the drained values are stored.
+// set into TMEM columns of its own; all drain the accumulators.  Before a tile is drained three sets
+// have dequantised inputs of the next one, so the MMAs go on while the drained values are stored.
 // TMEM: 256 accumulator columns, 4 x 64 columns of weights.
 #include <limits.h>
 
@@ -119,6 +119,31 @@ __device__ __forceinline__ void mbar_arrive_pair(uint32_t caddr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
 
+// Waits for a barrier's phase, `polls` tests at most, in as few instructions as there can be: waiting warps
+// share their schedulers with the workers.
+constexpr uint32_t kGPolls = 64;  // between looks at the abort flag
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n"
+      " .reg .pred p, q;\n"
+      " .reg .u32 n;\n"
+      " mov.u32 n, %3;\n"
+      "POLL:\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " @p bra DONE;\n"
+      " sub.u32 n, n, 1;\n"
+      " setp.ne.u32 q, n, 0;\n"
+      " @q bra POLL;\n"
+      "DONE:\n"
+      " selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "n"(kGPolls)
+      : "memory");
+  return ok != 0;
+}
+
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
@@ -213,18 +238,68 @@ __device__ __forceinline__ void w4_expand(uint32_t w, __half2 s, uint32_t* o) {
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
-// Stores 32 rows x 32 packed columns that a warp has staged in shared memory, [row][kGLd] fp32: the values
-// still lack their row's power of two.  fac[row] is that power (kGateUp: of x, then of 1 / h).
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// 32 rows x 32 packed columns of a warp (v[row], a column per lane, without the rows' powers of two) through
+// shared memory (st) to their place.  fac[row] is the row's power of two (kGateUp: of x, then of 1 / h).
 template <int kMode>
-__device__ __forceinline__ void w4g_store(const W4GemmArgs& a, const float* st, const float* fac, size_t row0, int nrow,
-                                          int c0, int lane) {
+__device__ __forceinline__ void w4g_store(const W4GemmArgs& a, const float (&v)[32], float cm, float* st,
+                                          const float* fac, size_t row0, int nrow, int c0, int lane) {
   const W4Dims& d = a.d;
+  const bool f32 = kMode == kGateUp || (kMode == kLinear ? a.out_f32 != 0 : a.yh == nullptr);
+  const size_t ld = kMode == kLinear ? a.ldo : (size_t)d.N;
+  const bool ragged = kMode == kLinear && !(ld % 8 == 0 && (uintptr_t)a.out % 16 == 0 && c0 + 32 <= d.N);
+  if (!f32 && !ragged) {
+    // 16-bit rows: two rows of a column in a word, [row pair][kGLd columns]; the powers of two are exact
+    // after the rounding too (a bf16 has fp32's range; y's fp16 rows carry none)
+    uint32_t* s2 = reinterpret_cast<uint32_t*>(st);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2)
+      s2[j / 2 * kGLd + lane] = kMode == kLinear ? pack_bf16(v[j] * cm, v[j + 1] * cm) : pack_f16(v[j] * cm, v[j + 1] * cm);
+    __syncwarp();
+    uint16_t* out = kMode == kLinear ? reinterpret_cast<uint16_t*>(a.out) : a.yh;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // 16 row pairs x 4 runs of 8 columns
+      const int idx = i * 32 + lane, rp = idx >> 2, seg = (idx & 3) * 8;
+      const uint4 w0 = *reinterpret_cast<const uint4*>(s2 + rp * kGLd + seg);
+      const uint4 w1 = *reinterpret_cast<const uint4*>(s2 + rp * kGLd + seg + 4);
+      const float2 f = *reinterpret_cast<const float2*>(fac + 2 * rp);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t sel = h ? 0x7632 : 0x5410;
+        uint32_t o[4] = {__byte_perm(w0.x, w0.y, sel), __byte_perm(w0.z, w0.w, sel), __byte_perm(w1.x, w1.y, sel),
+                         __byte_perm(w1.z, w1.w, sel)};
+        if (kMode == kLinear) {
+          const __nv_bfloat162 m = __float2bfloat162_rn(h ? f.y : f.x);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&o[j]), m);
+            o[j] = *reinterpret_cast<const uint32_t*>(&p);
+          }
+        }
+        if (2 * rp + h < nrow)
+          *reinterpret_cast<uint4*>(out + (row0 + 2 * rp + h) * ld + c0 + seg) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+    __syncwarp();
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 32; ++j) st[j * kGLd + lane] = v[j] * cm;
+  __syncwarp();
   if (kMode == kGateUp) {  // columns 0-15: gate, 16-31: up of the same 16 features
     const int f0 = c0 / 2, I = d.N / 2;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int idx = i * 32 + lane, row = idx >> 1, seg = (idx & 1) * 8;
-      const float x = fac[row], hinv = fac[32 + row];
+      const float x = fac[row], xh = x * fac[32 + row];
       uint32_t o[4];
 #pragma unroll
       for (int j = 0; j < 8; j += 4) {
@@ -232,88 +307,69 @@ __device__ __forceinline__ void w4g_store(const W4GemmArgs& a, const float* st, 
         const float4 u = *reinterpret_cast<const float4*>(st + row * kGLd + 16 + seg + j);
         auto h = [&](float gv, float uv) {
           gv *= x;
-          return __fdividef(gv, 1.f + __expf(-gv)) * (uv * x) * hinv;
+          return __fdividef(gv, 1.f + __expf(-gv)) * (uv * xh);
         };
-        const __half2 p0 = __floats2half2_rn(h(g.x, u.x), h(g.y, u.y)), p1 = __floats2half2_rn(h(g.z, u.z), h(g.w, u.w));
-        o[j / 2] = *reinterpret_cast<const uint32_t*>(&p0);
-        o[j / 2 + 1] = *reinterpret_cast<const uint32_t*>(&p1);
+        o[j / 2] = pack_f16(h(g.x, u.x), h(g.y, u.y));
+        o[j / 2 + 1] = pack_f16(h(g.z, u.z), h(g.w, u.w));
       }
       if (row < nrow)
         *reinterpret_cast<uint4*>(a.h + (row0 + row) * I + f0 + seg) = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    return;
-  }
-  const bool f32 = kMode == kLinear ? a.out_f32 != 0 : a.yh == nullptr;
-  const size_t ld = kMode == kLinear ? a.ldo : (size_t)d.N;
-  if (kMode == kLinear && !(ld % 8 == 0 && (uintptr_t)a.out % 16 == 0 && c0 + 32 <= d.N)) {
+  } else if (ragged) {
     // unaligned or ragged rows of out: element stores, 32 consecutive columns per row
     if (c0 + lane < d.N)
       for (int row = 0; row < nrow; ++row) {
-        const float v = st[row * kGLd + lane] * fac[row];
+        const float o = st[row * kGLd + lane] * fac[row];
         const size_t at = (row0 + row) * ld + c0 + lane;
-        if (f32) reinterpret_cast<float*>(a.out)[at] = v;
-        else reinterpret_cast<uint16_t*>(a.out)[at] = f32_to_bf16(v);
+        if (f32) reinterpret_cast<float*>(a.out)[at] = o;
+        else reinterpret_cast<uint16_t*>(a.out)[at] = f32_to_bf16(o);
       }
-    return;
-  }
-  if (f32) {
+  } else {
     float* out = kMode == kLinear ? reinterpret_cast<float*>(a.out) : a.y;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {  // 32 rows x 128 B
       const int idx = i * 32 + lane, row = idx >> 3, seg = (idx & 7) * 4;
-      float4 v = *reinterpret_cast<const float4*>(st + row * kGLd + seg);
+      float4 o = *reinterpret_cast<const float4*>(st + row * kGLd + seg);
       const float m = fac[row];
-      v.x *= m, v.y *= m, v.z *= m, v.w *= m;
-      if (row < nrow) *reinterpret_cast<float4*>(out + (row0 + row) * ld + c0 + seg) = v;
-    }
-  } else {
-    uint16_t* out = kMode == kLinear ? reinterpret_cast<uint16_t*>(a.out) : a.yh;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // 32 rows x 64 B
-      const int idx = i * 32 + lane, row = idx >> 2, seg = (idx & 3) * 8;
-      const float4 v0 = *reinterpret_cast<const float4*>(st + row * kGLd + seg);
-      const float4 v1 = *reinterpret_cast<const float4*>(st + row * kGLd + seg + 4);
-      const float m = fac[row];
-      uint32_t o[4];
-      const float v[8] = {v0.x * m, v0.y * m, v0.z * m, v0.w * m, v1.x * m, v1.y * m, v1.z * m, v1.w * m};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (kMode == kLinear) {
-          o[j] = uint32_t(f32_to_bf16(v[2 * j])) | (uint32_t(f32_to_bf16(v[2 * j + 1])) << 16);
-        } else {
-          const __half2 p = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
-          o[j] = *reinterpret_cast<const uint32_t*>(&p);
-        }
-      }
-      if (row < nrow) *reinterpret_cast<uint4*>(out + (row0 + row) * ld + c0 + seg) = make_uint4(o[0], o[1], o[2], o[3]);
+      o.x *= m, o.y *= m, o.z *= m, o.w *= m;
+      if (row < nrow) *reinterpret_cast<float4*>(out + (row0 + row) * ld + c0 + seg) = o;
     }
   }
+  __syncwarp();
+}
+
+// What the drain of 64 rows (of set `set`) multiplies with: the rows' powers of two, into fac, and the
+// lane's column's, returned.
+template <int kMode>
+__device__ __forceinline__ float w4g_factors(const W4GemmArgs& a, const W4GTile& ti, int blk, int q, int set, int lane,
+                                             float* fac) {
+  const W4Dims& d = a.d;
+  const int tok0 = 64 * set, nrow = ti.ntok - tok0, c = blk * kGM + 32 * q + lane;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = 32 * i + lane;
+    const bool mine = row < nrow;
+    const size_t p = (size_t)ti.row0 + tok0 + row;
+    // scaled rows of y keep the row's own power of two apart
+    fac[64 * i + lane] = !mine ? 0.f : kMode == kDown && a.yh ? 1.f : pow2(a.rexp[p]);
+    if (kMode == kGateUp) fac[64 * i + 32 + lane] = mine ? pow2(-a.oexp[p]) : 0.f;
+  }
+  float cm = 0.f;
+  if (c < d.N) cm = reinterpret_cast<const float*>(ti.base + d.mult)[c];
+  if (kMode == kDown && a.yh) cm = ldexpf(cm, -w4_y_exp(ti.base, d));
+  return cm;
 }
 
 // Drains 64 rows (of set `set`) x this warp's 32 columns: to registers, the accumulators are handed back
 // (tempty of the pair's first CTA), then 32 rows at a time through shared memory to their place.
 template <int kMode, class Wait>
 __device__ __forceinline__ void w4g_drain(const W4GemmArgs& a, const W4GTile& ti, int blk, uint32_t taddr, int q, int set,
-                                          int lane, float* st, float* fac, uint64_t* tfull, uint32_t tempty0,
-                                          uint32_t parity, Wait&& wait, volatile int* abort_flag) {
+                                          int lane, float* st, const float* fac, float cm, uint64_t* tfull,
+                                          uint32_t tempty0, uint32_t parity, Wait&& wait, const bool& dead) {
   const W4Dims& d = a.d;
   const int tok0 = 64 * set, nrow = ti.ntok - tok0, c0 = blk * kGM + 32 * q;
   const bool any = nrow > 0 && c0 < d.N;
   const size_t row0 = (size_t)ti.row0 + tok0;
-  float cm = 0.f;
-  if (any) {
-    // the rows' powers of two, and the column's
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int row = 32 * c + lane;
-      const bool mine = row < nrow;
-      // scaled rows of y keep the row's own power of two apart
-      fac[64 * c + lane] = !mine ? 0.f : kMode == kDown && a.yh ? 1.f : pow2(a.rexp[row0 + row]);
-      if (kMode == kGateUp) fac[64 * c + 32 + lane] = mine ? pow2(-a.oexp[row0 + row]) : 0.f;
-    }
-    if (c0 + lane < d.N) cm = reinterpret_cast<const float*>(ti.base + d.mult)[c0 + lane];
-    if (kMode == kDown && a.yh) cm = ldexpf(cm, -w4_y_exp(ti.base, d));
-  }
   __syncwarp();
   wait(tfull, parity);
   tc_fence_after();
@@ -326,25 +382,15 @@ __device__ __forceinline__ void w4g_drain(const W4GemmArgs& a, const W4GTile& ti
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive_pair(tempty0);
-  if (!any || *abort_flag) return;
-#pragma unroll
-  for (int j = 0; j < 32; ++j) st[j * kGLd + lane] = v0[j] * cm;
-  __syncwarp();
-  w4g_store<kMode>(a, st, fac, row0, min(nrow, 32), c0, lane);
-  __syncwarp();
-  if (nrow <= 32) return;
-#pragma unroll
-  for (int j = 0; j < 32; ++j) st[j * kGLd + lane] = v1[j] * cm;
-  __syncwarp();
-  w4g_store<kMode>(a, st, fac + 64, row0 + 32, min(nrow - 32, 32), c0, lane);
-  __syncwarp();
+  if (!any || dead) return;
+  w4g_store<kMode>(a, v0, cm, st, fac, row0, min(nrow, 32), c0, lane);
+  if (nrow > 32) w4g_store<kMode>(a, v1, cm, st, fac + 64, row0 + 32, min(nrow - 32, 32), c0, lane);
 }
 
 template <int kMode>
 __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs a, const __grid_constant__ W4RowMaps mapX) {
   extern __shared__ __align__(16) unsigned char gsm_raw[];
-  unsigned char* sm =
-      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(gsm_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* sm = gsm_raw + ((0u - smem_u32(gsm_raw)) & 1023u);  // (an offset: the accesses stay shared ones)
   unsigned char* xs = sm;                             // [ring][16 KB]
   unsigned char* wsm = sm + kGXRing * kGXBytes;       // [ring][codes | scales]
   float* epi = reinterpret_cast<float*>(wsm + kGWRing * kGWBytes);   // [workers][32][kGLd]
@@ -416,17 +462,22 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* abort_flag = &s_abort;
-  // a wait that gives up ends the work of every role; the barriers are then no longer waited for
+  // Waits as a whole warp.  A wait that gives up (or sees that another one did) ends the work of its role:
+  // `dead`, the same in every lane; a role that is dead waits no more.
+  bool dead = false;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!mbar_try_wait(bar, parity) && !*abort_flag && !mbar_wait(bar, parity)) {
+    if (dead || __all_sync(MOE_FULL_MASK, mbar_poll(bar, parity))) return;
+    bool ok = false;
+    for (int i = 0; i < int(kWaitPolls / kGPolls) && !ok && !*abort_flag; ++i) ok = mbar_poll(bar, parity);
+    if (!ok && !*abort_flag) {
       *abort_flag = 1;
       set_status(a.status, MOE_DEV_TIMEOUT);
     }
+    dead = __any_sync(MOE_FULL_MASK, !ok);
   };
 
   if (warp == 0) {
     uint32_t xi = 0;  // stages issued
-    bool dead = false;
     const bool lead = elect_one();
     for (int t = cl; t < total && !dead; t += ncl) {
       const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
@@ -434,7 +485,6 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
       for (int kb = 0; kb < nkb; ++kb, ++xi) {
         const uint32_t s = xi % kGXRing, use = xi / kGXRing;
         if (use > 0) wait(&xempty[s], (use - 1) & 1u);
-        dead = __any_sync(MOE_FULL_MASK, *abort_flag);
         if (dead) break;
         if (lead) {
           // the first CTA's barrier counts the bytes of both
@@ -464,7 +514,6 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
       for (uint32_t j = xi > kGXRing ? xi - kGXRing : 0; j < xi; ++j) mbar_wait(&xfull[j % kGXRing], (j / kGXRing) & 1u);
   } else if (warp == kGWorkers + 2) {
     uint32_t wi = 0;  // chunks issued
-    bool dead = false;
     const bool lead = elect_one();
     for (int t = cl; t < total && !dead; t += ncl) {
       const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
@@ -474,7 +523,6 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
         const uint32_t s = wi % kGWRing, use = wi / kGWRing, nb = min(kGChunk, nkb - kb);
         const uint32_t ng = d.G == 128 ? (nb + 1) / 2 : d.G == 64 ? nb : 2 * nb;
         if (use > 0) wait(&wempty[s], (use - 1) & 1u);
-        dead = __any_sync(MOE_FULL_MASK, *abort_flag);
         if (dead) break;
         unsigned char* dst = wsm + s * kGWBytes;
         if (lead) {
@@ -497,7 +545,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
       const uint64_t bd0 = smem_desc_l(smem_u32(xs), 16, 1024, kLayoutSw128);
       const bool lead = elect_one();
       uint32_t xi = 0, vi = 0, tc = 0;  // stages of rows, visits, tiles
-      for (int t = cl; t < total && !__any_sync(MOE_FULL_MASK, *abort_flag); t += ncl, ++tc) {
+      for (int t = cl; t < total && !dead; t += ncl, ++tc) {
         const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
         const uint32_t idesc = idesc_f16(2 * kGM, 2 * w4g_half(ti.ntok));
         if (tc > 0) wait(tempty, (tc - 1) & 1u);
@@ -510,7 +558,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
             const uint32_t s = xi % kGXRing;
             wait(&xfull[s], (xi / kGXRing) & 1u);
             tc_fence_after();
-            if (lead) {
+            if (lead && !dead) {
               umma_f16_ts_pair_k64(tmem, tmem + kGACol + as * 64 + h * 32, bd0 + (uint64_t)(s * (kGXBytes >> 4)), idesc,
                                    kb > 0);
               umma_commit_pair(&xempty[s]);
@@ -535,22 +583,24 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     float* st = epi + (warp - 2) * (kGEpiBytes / 4);
     float* fac = facs + (warp - 2) * 128;
     const uint32_t afull0 = mapa_shared(smem_u32(&afull[set]), 0), tempty0 = mapa_shared(smem_u32(tempty), 0);
-    uint32_t vi = 0, wi = 0, tc = 0;  // visits, chunks before this tile, tiles drained
+    uint32_t vi = 0, wi = 0, tc = 0;  // visits and chunks before this tile, tiles drained
+    uint32_t uses = 0;                // this set's visits
     W4GTile prev = {};
     bool pending = false;  // prev has not been drained
+    float cm = 0.f;
     for (int t = cl;; t += ncl) {
-      const bool real = t < total && !__any_sync(MOE_FULL_MASK, *abort_flag);
+      const bool real = t < total && !dead;
       W4GTile ti = {};
       if (real) ti = w4g_tile<kMode>(a, s_pre, nl, t);
       const int nm = max(1, min(8, d.Mt - 8 * (2 * ti.ft + (int)rank))), nk = real ? nkb : 0;
-      // one visit of each set, the last tile's drain, the other visits
-      int kb = 0;
+      // a visit of every set but one (whose columns the last tile's final MMAs still read), the last tile's
+      // drain, the other visits; this set's are every fourth one of the CTA's sequence
+      int kb = (int)((set - vi) % kGSets) * kGVisit;
 #pragma unroll 1
       for (int phase = 0; phase < 2; ++phase) {
-        const int end = phase ? nk : min(nk, kGSets * kGVisit);
+        const int end = phase ? nk : min(nk, (kGSets - 1) * kGVisit);
 #pragma unroll 1
-        for (; kb < end; kb += kGVisit, ++vi) {
-          if (vi % kGSets != (uint32_t)set) continue;
+        for (; kb < end; kb += kGSets * kGVisit) {
           // a chunk of codes holds two visits; a tile starts a chunk of its own
           const uint32_t c = wi + kb / kGChunk, ws = c % kGWRing;
           wait(&wfull[ws], (c / kGWRing) & 1u);
@@ -572,7 +622,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
               w4_expand(w[j].x, s0, &o[4 * j]);
               w4_expand(w[j].y, s1, &o[16 + 4 * j]);
             }
-            if (h == 0 && vi >= kGSets) wait(&aempty[set], (vi / kGSets - 1) & 1u);
+            if (h == 0 && uses > 0) wait(&aempty[set], (uses - 1) & 1u);
             tc_fence_after();
             tmem_st32(a_addr + 32 * h, o);
           }
@@ -584,16 +634,19 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
             // a last chunk of one visit counts it twice
             mbar_arrive_n(&wempty[ws], kb % kGChunk == 0 && kb + kGVisit >= nkb ? 2 : 1);
           }
+          ++uses;
         }
         if (phase == 0 && pending) {
-          w4g_drain<kMode>(a, prev, 2 * prev.ft + (int)rank, lane_addr, q, set, lane, st, fac, tfull, tempty0, tc & 1u,
-                           wait, abort_flag);
+          w4g_drain<kMode>(a, prev, 2 * prev.ft + (int)rank, lane_addr, q, set, lane, st, fac, cm, tfull, tempty0, tc & 1u,
+                           wait, dead);
           ++tc;
         }
       }
       if (!real) break;
       prev = ti;
       pending = true;
+      cm = w4g_factors<kMode>(a, ti, 2 * ti.ft + (int)rank, q, set, lane, fac);
+      vi += (nkb + kGVisit - 1) / kGVisit;
       wi += (nkb + kGChunk - 1) / kGChunk;
     }
   }
