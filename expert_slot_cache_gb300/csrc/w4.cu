@@ -1,11 +1,21 @@
-// Products with 4-bit weights and group scales (format: w4.cuh): the linear layer and the grouped
-// SwiGLU expert FFN.
+// Products with 4-bit weights and group scales (format: w4.cuh) for few rows: the linear layer and the
+// grouped SwiGLU expert FFN as weight streams.
 //
 //   y[t][n] = sum_k x[t][k] (code[k][n] - 8) scale[k / G][n]
 //
-// The codes become the A operand of 16 x 16 x 8 MMAs as exact bf16 integers, the bf16 activations the B
-// operand; a 64-input block's products (32 inputs where G = 32) are summed in fp32 by the tensor core,
-// then multiplied by their fp32 scale and added in fp32.  No weight and no activation is rounded.
+// The codes become the A operand of 16 x 16 x 8 MMAs as the exact bf16 integers 16 + code, the bf16
+// activations the B operand; a 64-input block's products (32 inputs where G = 32) are summed in fp32 by the
+// tensor core, 24 times the block's sum of activations (an MMA with ones, shared by all columns) is taken
+// off, the rest multiplied by its fp32 scale and added in fp32.  No weight and no activation is rounded.
+// (16 + code needs a mask and at most a shift; code - 8 would need a third operation for every pair, and the
+// stream is bound by its instructions: 64 codes of 16 columns are 512 bytes, 21 cycles of an SM's share of
+// the memory bandwidth.)
+//
+// A warp streams CM neighbouring tiles of 16 columns (CM x 512 bytes a block of 64 inputs, one 16-byte load
+// per lane and tile), every ks-th block of the inputs, two blocks ahead and on across the end of a unit, so
+// that its loads never pause; the activations of a block travel with its codes.  The ks warps that share a
+// unit add up in shared memory, in warp order.  ks is the split that costs least for the unit count at hand
+// (w4_split): few long shares while there are units for every warp, short ones for a few small matrices.
 #include <algorithm>
 
 #include "internal.cuh"
@@ -15,130 +25,229 @@ namespace moe {
 
 constexpr int kW4Warps = 8;
 constexpr int kW4Threads = 32 * kW4Warps;
+constexpr int kW4Ctas = 2;   // resident CTAs per SM that the registers allow
 
-// One matrix's view for a tile: lane's code words, the tile's scale words, the multipliers.
-struct W4Tile {
-  const uint4* codes;      // + kb * 32 * mates
-  const uint32_t* scales;  // + kg * 8 * mates
-  int mates;
+// One block of 64 inputs in registers: a lane's codes of CM tiles, their columns' scales, and the lane's inputs
+// of NB groups of eight rows (LO: as the sum of two bf16).
+template <int CM, int NB, bool LO, bool G32>
+struct W4Block {
+  uint4 w[CM];
+  uint32_t s[CM][G32 ? 2 : 1];
+  uint4 x[NB][LO ? 2 : 1][2];
 };
 
-__device__ __forceinline__ W4Tile w4_tile(const uint8_t* m, const W4Dims& d, int tile, int lane) {
-  W4Tile t;
-  t.codes = reinterpret_cast<const uint4*>(m) + w4_code_at(d, tile, 0) * 32 + w4_chunk(lane >> 2, lane & 3);
-  t.scales = reinterpret_cast<const uint32_t*>(m + d.scales) + w4_scale_at(d, tile, 0) * 8 + (lane >> 2);
-  t.mates = w4_mates(d, tile);
-  return t;
+// What a warp streams of one unit: its tiles' codes and scales, and the rows they meet.
+template <int NB>
+struct W4Unit {
+  const uint8_t* codes;   // the lane's chunk in block 0 of the first tile
+  const uint8_t* scales;  // the lane's columns in group 0
+  int mates;              // tiles that lie between one block and the next
+  int nm;                 // tiles that exist (0: nothing to do)
+  const uint16_t* x[NB];  // the lane's row of each group, at input 8 (lane & 3)
+};
+template <int NB>
+__device__ __forceinline__ void w4_at(W4Unit<NB>& u, const uint8_t* m, const W4Dims& d, int tile, int nm, int lane) {
+  u.codes = m + w4_code_at(d, tile, 0) * 512 + 16 * w4_chunk(lane >> 2, lane & 3);
+  u.scales = m + d.scales + w4_scale_at(d, tile, 0) * 32 + 4 * (lane >> 2);
+  u.mates = w4_mates(d, tile);
+  u.nm = nm;
 }
 
-// acc[m][nb] += tile products of blocks [kb0, kb1): NM matrices that share the rows of x, NB groups of
-// eight rows.  xr[nb]: the lane's row (column lane >> 2 of the group), already offset by 8 * (lane & 3).
-// LO: the rows come as a sum of two bf16 arrays, xr[nb] and xr[nb] + lo.
-template <int NM, int NB, bool LO>
-__device__ __forceinline__ void w4_accumulate(const W4Tile (&t)[NM], const uint16_t* const (&xr)[NB], size_t lo,
-                                              int K, int G, int kb0, int kb1, int q, float (&acc)[NM][NB][4]) {
-#pragma unroll 2
-  for (int kb = kb0; kb < kb1; ++kb) {
-    uint4 w[NM];
+template <int CM, int NB, bool LO, bool G32>
+__device__ __forceinline__ void w4_load(W4Block<CM, NB, LO, G32>& b, const W4Unit<NB>& u, const W4Dims& d, int kb, int q,
+                                        size_t lo) {
+  const uint8_t* c = u.codes + (size_t)(uint32_t)(kb * u.mates) * 512;
+  const int kg = G32 ? 2 * kb : d.G == 128 ? kb >> 1 : kb;
+  const uint8_t* s = u.scales + (uint32_t)(kg * u.mates) * 32u;
 #pragma unroll
-    for (int m = 0; m < NM; ++m) w[m] = ldg_stream(t[m].codes + (size_t)kb * (32 * t[0].mates));
+  for (int m = 0; m < CM; ++m)
+    if (m == 0 || m < u.nm) {
+      b.w[m] = ldg_stream(c + m * 512);
+      b.s[m][0] = __ldg(reinterpret_cast<const uint32_t*>(s + m * 32));
+      if (G32) b.s[m][G32 ? 1 : 0] = __ldg(reinterpret_cast<const uint32_t*>(s + (u.mates + m) * 32));
+    }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = kb * 64 + 32 * h;
-      const bool in = k + 8 * q < K;  // K % 8 == 0: a lane's eight inputs are inside or outside together
-      uint4 x[NB], xl[NB];
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int p = 0; p < (LO ? 2 : 1); ++p) {
+      const uint16_t* x = u.x[nb] + p * lo + kb * 64;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)  // K % 8 == 0: a lane's eight inputs are inside or outside together
+        b.x[nb][p][h] = kb * 64 + 32 * h + 8 * q < d.K ? __ldg(reinterpret_cast<const uint4*>(x + 32 * h)) : make_uint4(0, 0, 0, 0);
+    }
+}
+
+template <int CM, int NB, bool LO, bool G32>
+__device__ __forceinline__ void w4_block(const W4Block<CM, NB, LO, G32>& b, int nm, float (&acc)[CM][NB][4]) {
+  constexpr int P = LO ? 2 : 1;
+  const uint32_t one = 0x3f803f80u;
+  const uint32_t ones[4] = {one, one, one, one};
+#pragma unroll
+  for (int part = 0; part < (G32 ? 2 : 1); ++part) {
+    constexpr int H = G32 ? 1 : 2;  // halves of the block per scale
+    float off[NB][2];               // -24 sum of the rows' inputs
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const uint4 v = b.x[nb][p][part + h];
+          mma_bf16_16816(d, ones, v.x, v.y, d[0], d[1], d[2], d[3]);
+          mma_bf16_16816(d, ones, v.z, v.w, d[0], d[1], d[2], d[3]);
+        }
+      off[nb][0] = -24.f * d[0];
+      off[nb][1] = -24.f * d[1];
+    }
+#pragma unroll
+    for (int m = 0; m < CM; ++m) {
+      if (m > 0 && m >= nm) break;
+      float c[NB][4];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[nb][i] = off[nb][i & 1];
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        uint32_t a0[4], a1[4];
+        w4_frag_bf16(part + h ? b.w[m].y : b.w[m].x, part + h ? b.w[m].w : b.w[m].z, a0, a1);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            const uint4 v = b.x[nb][p][part + h];
+            mma_bf16_16816(c[nb], a0, v.x, v.y, c[nb][0], c[nb][1], c[nb][2], c[nb][3]);
+            mma_bf16_16816(c[nb], a1, v.z, v.w, c[nb][0], c[nb][1], c[nb][2], c[nb][3]);
+          }
+      }
+      const uint32_t sw = b.s[m][part];
+      const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&sw));
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        x[nb] = in ? __ldg(reinterpret_cast<const uint4*>(xr[nb] + k)) : make_uint4(0, 0, 0, 0);
-        if (LO) xl[nb] = in ? __ldg(reinterpret_cast<const uint4*>(xr[nb] + lo + k)) : make_uint4(0, 0, 0, 0);
-      }
-      const int kg = k / G;
-#pragma unroll
-      for (int m = 0; m < NM; ++m) {
-        uint32_t a0[4], a1[4];
-        w4_frag_bf16(h ? w[m].y : w[m].x, h ? w[m].w : w[m].z, a0, a1);
-        const uint32_t sw = __ldg(t[m].scales + (size_t)kg * (8 * t[0].mates));
-        const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&sw));
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_bf16_16816(c, a0, x[nb].x, x[nb].y);
-          mma_bf16_16816(c, a1, x[nb].z, x[nb].w);
-          if (LO) {
-            mma_bf16_16816(c, a0, xl[nb].x, xl[nb].y);
-            mma_bf16_16816(c, a1, xl[nb].z, xl[nb].w);
-          }
-          acc[m][nb][0] = fmaf(s.x, c[0], acc[m][nb][0]);
-          acc[m][nb][1] = fmaf(s.x, c[1], acc[m][nb][1]);
-          acc[m][nb][2] = fmaf(s.y, c[2], acc[m][nb][2]);
-          acc[m][nb][3] = fmaf(s.y, c[3], acc[m][nb][3]);
-        }
+        acc[m][nb][0] = fmaf(s.x, c[nb][0], acc[m][nb][0]);
+        acc[m][nb][1] = fmaf(s.x, c[nb][1], acc[m][nb][1]);
+        acc[m][nb][2] = fmaf(s.y, c[nb][2], acc[m][nb][2]);
+        acc[m][nb][3] = fmaf(s.y, c[nb][3], acc[m][nb][3]);
       }
     }
   }
 }
 
-// Sum of the `ks` warps' accumulators of one tile, parts in warp order: red[warp][m][nb][4][32].
-// Element (i, lane) is column (lane >> 2) + 8 * (i >> 1), row 2 * (lane & 3) + (i & 1).
-template <int NM, int NB>
-__device__ __forceinline__ void w4_store_part(float* red, int warp, int lane, const float (&acc)[NM][NB][4]) {
+// Sums of the ks warps of a subgroup, in warp order: red[warp][m][nb][4][32].  Element (i, lane) is column
+// (lane >> 2) + 8 * (i >> 1), row 2 * (lane & 3) + (i & 1).
+template <int CM, int NB>
+__device__ __forceinline__ void w4_put_part(float* red, int warp, int lane, const float (&acc)[CM][NB][4]) {
 #pragma unroll
-  for (int m = 0; m < NM; ++m)
+  for (int m = 0; m < CM; ++m)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) red[(((warp * NM + m) * NB + nb) * 4 + i) * 32 + lane] = acc[m][nb][i];
+      for (int i = 0; i < 4; ++i) red[(((warp * CM + m) * NB + nb) * 4 + i) * 32 + lane] = acc[m][nb][i];
 }
-
-template <int NM, int NB>
+template <int CM, int NB>
 __device__ __forceinline__ float w4_sum_part(const float* red, int w0, int ks, int m, int row, int col) {
   const int nb = row >> 3, i = 2 * (col >> 3) + (row & 1), lane = 4 * (col & 7) + ((row & 7) >> 1);
   float s = 0.f;
-  for (int w = 0; w < ks; ++w) s += red[((((w0 + w) * NM + m) * NB + nb) * 4 + i) * 32 + lane];
+  for (int w = 0; w < ks; ++w) s += red[((((w0 + w) * CM + m) * NB + nb) * 4 + i) * 32 + lane];
   return s;
+}
+
+// Warps per unit: the power of two with the least rounds x (blocks of a share + the cost of ending a round,
+// about three blocks).
+__host__ __device__ inline int w4_split(int units, int Kb, int ctas) {
+  int best = 1;
+  int64_t least = 0;
+  for (int ks = 1; ks <= kW4Warps; ks *= 2) {
+    const int64_t sub = (int64_t)ctas * (kW4Warps / ks), rounds = (units + sub - 1) / sub;
+    const int64_t cost = rounds * ((Kb + ks - 1) / ks + 3);
+    if (ks == 1 || cost < least) {
+      best = ks;
+      least = cost;
+    }
+  }
+  return best;
+}
+
+// The stream of one CTA: rounds 0 .. rounds - 1 of units; unit(round) gives this warp's unit (of its subgroup)
+// and done(round, red) is called by all threads once the subgroups' parts of a round are in red.
+template <int CM, int NB, bool LO, bool G32, class Unit, class Done>
+__device__ __forceinline__ void w4_stream(const W4Dims& d, int ks, int rounds, size_t lo, float* red, Unit&& unit,
+                                          Done&& done) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, part = warp % ks;
+  const int steps = ((d.Kb + ks - 1) / ks + 1) / 2;  // of two blocks
+  W4Block<CM, NB, LO, G32> ring[2];
+  W4Unit<NB> cur, nxt = unit(0);
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (nxt.nm > 0 && part + j * ks < d.Kb) w4_load<CM, NB, LO, G32>(ring[j], nxt, d, part + j * ks, q, lo);
+  for (int r = 0; r < rounds; ++r) {
+    cur = nxt;
+    if (r + 1 < rounds) nxt = unit(r + 1);
+    else nxt.nm = 0;
+    float acc[CM][NB][4] = {};
+    int kb = part;
+    for (int s = 0; s + 1 < steps; ++s, kb += 2 * ks)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (cur.nm > 0) w4_block<CM, NB, LO, G32>(ring[j], cur.nm, acc);  // all but a share's last two blocks exist
+        const int kn = kb + (2 + j) * ks;
+        if (cur.nm > 0 && kn < d.Kb) w4_load<CM, NB, LO, G32>(ring[j], cur, d, kn, q, lo);
+      }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {  // the slots' next blocks are the next unit's
+      if (cur.nm > 0 && kb + j * ks < d.Kb) w4_block<CM, NB, LO, G32>(ring[j], cur.nm, acc);
+      if (nxt.nm > 0 && part + j * ks < d.Kb) w4_load<CM, NB, LO, G32>(ring[j], nxt, d, part + j * ks, q, lo);
+    }
+    float* buf = red + (r & 1) * (kW4Warps * CM * NB * 128);  // two buffers: one barrier per round
+    w4_put_part<CM, NB>(buf, warp, lane, acc);
+    __syncthreads();
+    done(r, buf);
+  }
 }
 
 struct W4LinArgs {
   const uint16_t* x;
   size_t ldx, ldo;
-  int T, ks;  // ks warps share a tile
+  int T, ks;  // ks warps share CM tiles
   const uint8_t* w;
   W4Dims d;
   void* out;
   int out_f32;
 };
 
-// grid (ceil(Mt / (8 / ks)), ceil(T / (8 NB))).
-template <int NB>
-__global__ void __launch_bounds__(kW4Threads) w4_linear_kernel(const W4LinArgs a) {
-  __shared__ float red[kW4Warps * NB * 4 * 32];
+// grid (CTAs, ceil(T / (8 NB))).
+template <int CM, int NB, bool G32>
+__global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_linear_kernel(const W4LinArgs a) {
+  __shared__ float red[2 * kW4Warps * CM * NB * 128];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ks = a.ks, tpc = kW4Warps / ks;
-  const int tile0 = blockIdx.x * tpc, tile = tile0 + warp / ks, part = warp % ks;
+  const int ks = a.ks, sub = kW4Warps / ks;  // subgroups of the CTA
+  const int groups = (a.d.Mt + CM - 1) / CM;
+  const int rounds = (groups - (int)blockIdx.x * sub + (int)gridDim.x * sub - 1) / ((int)gridDim.x * sub);
   const int t0 = blockIdx.y * 8 * NB, nt = min(8 * NB, a.T - t0);
-  float acc[1][NB][4] = {};
-  if (tile < a.d.Mt) {
-    const uint16_t* xr[NB];
+  const float* mult = reinterpret_cast<const float*>(a.w + a.d.mult);
+  auto first = [&](int r, int g) { return ((r * (int)gridDim.x + (int)blockIdx.x) * sub + g) * CM; };  // tile
+  auto unit = [&](int r) {
+    W4Unit<NB> u;
+    const int tile = first(r, warp / ks);
+    w4_at(u, a.w, a.d, min(tile, a.d.Mt - 1), max(0, min(CM, a.d.Mt - tile)), lane);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)  // rows past the batch repeat its last one; their results are dropped
-      xr[nb] = a.x + (size_t)(t0 + min(8 * nb + (lane >> 2), nt - 1)) * a.ldx + 8 * (lane & 3);
-    const W4Tile t[1] = {w4_tile(a.w, a.d, tile, lane)};
-    const int per = (a.d.Kb + ks - 1) / ks;
-    w4_accumulate<1, NB, false>(t, xr, 0, a.d.K, a.d.G, min(part * per, a.d.Kb), min((part + 1) * per, a.d.Kb),
-                                lane & 3, acc);
-  }
-  w4_store_part<1, NB>(red, warp, lane, acc);
-  __syncthreads();
-  const float* mult = reinterpret_cast<const float*>(a.w + a.d.mult);
-  for (int i = threadIdx.x; i < tpc * 16 * nt; i += kW4Threads) {
-    const int col = i & 15, row = (i >> 4) % nt, tl = (i >> 4) / nt;
-    const int n = (tile0 + tl) * 16 + col;
-    if (n >= a.d.N) continue;
-    const float v = w4_sum_part<1, NB>(red, tl * ks, ks, 0, row, col) * mult[n];
-    const size_t o = (size_t)(t0 + row) * a.ldo + n;
-    if (a.out_f32) reinterpret_cast<float*>(a.out)[o] = v;
-    else reinterpret_cast<uint16_t*>(a.out)[o] = f32_to_bf16(v);
-  }
+      u.x[nb] = a.x + (size_t)(t0 + min(8 * nb + (lane >> 2), nt - 1)) * a.ldx + 8 * (lane & 3);
+    return u;
+  };
+  if (rounds <= 0) return;
+  w4_stream<CM, NB, false, G32>(a.d, ks, rounds, 0, red, unit, [&](int r, const float* buf) {
+    for (int i = threadIdx.x; i < sub * CM * 16 * nt; i += kW4Threads) {
+      const int col = i % (CM * 16), row = i / (CM * 16) % nt, g = i / (CM * 16 * nt);
+      const int n = first(r, g) * 16 + col;
+      if (n >= a.d.N) continue;
+      const float v = w4_sum_part<CM, NB>(buf, g * ks, ks, col >> 4, row, col & 15) * mult[n];
+      const size_t o = (size_t)(t0 + row) * a.ldo + n;
+      if (a.out_f32) reinterpret_cast<float*>(a.out)[o] = v;
+      else reinterpret_cast<uint16_t*>(a.out)[o] = f32_to_bf16(v);
+    }
+  });
 }
 
 struct W4FfnArgs {
@@ -148,100 +257,139 @@ struct W4FfnArgs {
   size_t n;
 };
 
-__device__ __forceinline__ bool w4_slot(const FfnArgs& a, int li, int& e, int& slot) {
-  e = a.list_e[li];
-  if (e < 0 || e >= a.E) return false;
-  slot = a.list_s ? a.list_s[li] : a.e2s ? a.e2s[e] : e;
-  return true;
+// A listed expert's batch of at most eight rows.
+constexpr int kW4Rows = 8;
+struct W4Batch {
+  int slot, p0, n;  // slot -1: no slot
+};
+
+// The listed experts' row batches, in shared memory: built by all threads, `most` entries at most.  Returns
+// their number.
+__device__ __forceinline__ int w4_batches(const FfnArgs& a, W4Batch* tab, int most, int* tmp) {
+  const int nl = min(*a.n_list, kMaxE);
+  int base = 0;
+  for (int l0 = 0; l0 < nl; l0 += kW4Threads) {
+    const int li = l0 + threadIdx.x;
+    int c = 0, p0 = 0, rows = 0, slot = -1;
+    if (li < nl) {
+      const int e = a.list_e[li];
+      if (e >= 0 && e < a.E) {
+        slot = a.list_s ? a.list_s[li] : a.e2s ? a.e2s[e] : e;
+        p0 = a.offset[e];
+        rows = max(a.offset[e + 1] - p0, 0);
+        c = (rows + kW4Rows - 1) / kW4Rows;
+        if (slot < 0 || slot >= a.S) {
+          if (c > 0) set_status(a.status, MOE_DEV_BAD_SLOT);
+          slot = -1;
+        }
+      }
+    }
+    int tot;
+    const int ex = base + block_exclusive_scan(c, tmp, &tot);
+    for (int i = 0; i < c && ex + i < most; ++i)
+      tab[ex + i] = W4Batch{slot, p0 + kW4Rows * i, min(kW4Rows, rows - kW4Rows * i)};
+    base += tot;
+  }
+  __syncthreads();
+  if (base > most && threadIdx.x == 0) set_status(a.status, MOE_DEV_BAD_GROUPS);
+  return min(base, most);
 }
 
-// Gate and up: unit = (listed expert, tile of 16 h features); eight warps split the inputs.
-template <int NB>
-__global__ void __launch_bounds__(kW4Threads) w4_gateup_kernel(const W4FfnArgs a) {
-  __shared__ float red[kW4Warps * 2 * NB * 4 * 32];
+// Gate and up: unit = (row batch, two tiles of gate with their neighbours of up); an expert's batches follow
+// each other, so that their weights come from memory once.
+constexpr int kGuTiles = 4;
+template <bool G32>
+__global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_gateup_kernel(const W4FfnArgs a, int most) {
+  extern __shared__ W4Batch tab[];
+  __shared__ float red[2 * kW4Warps * kGuTiles * 128];
+  __shared__ int tmp[33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const W4Dims& d = a.sl.gu;
-  const int nl = *a.f.n_list, FT = d.Mt / 2, I = d.N / 2;  // a tile of gate and its neighbour of up
-  for (int u = blockIdx.x; u < nl * FT; u += gridDim.x) {
-    int e, slot;
-    if (!w4_slot(a.f, u / FT, e, slot)) continue;
-    if (slot < 0 || slot >= a.f.S) {
-      if (threadIdx.x == 0) set_status(a.f.status, MOE_DEV_BAD_SLOT);
-      continue;
+  const int nbat = w4_batches(a.f, tab, most, tmp);
+  const int FT = (d.Mt + kGuTiles - 1) / kGuTiles, I = d.N / 2, units = nbat * FT;
+  const int ks = w4_split(units, d.Kb, gridDim.x), sub = kW4Warps / ks;
+  const int rounds = (units - (int)blockIdx.x * sub + (int)gridDim.x * sub - 1) / ((int)gridDim.x * sub);
+  if (rounds <= 0) return;
+  auto index = [&](int r, int g) { return (r * (int)gridDim.x + (int)blockIdx.x) * sub + g; };
+  auto slab = [&](int slot) { return reinterpret_cast<const uint8_t*>(a.f.pool) + (size_t)slot * a.sl.bytes; };
+  auto unit = [&](int r) {
+    W4Unit<1> u;
+    u.nm = 0;
+    const int i = index(r, warp / ks);
+    if (i >= units) return u;
+    const W4Batch b = tab[i / FT];
+    if (b.slot < 0) return u;
+    const int tile = i % FT * kGuTiles;
+    w4_at(u, slab(b.slot), d, tile, min(kGuTiles, d.Mt - tile), lane);
+    u.x[0] = a.f.x + (size_t)(a.f.rows[b.p0 + min(lane >> 2, b.n - 1)] / a.f.k) * a.f.H + 8 * (lane & 3);
+    return u;
+  };
+  w4_stream<kGuTiles, 1, false, G32>(d, ks, rounds, 0, red, unit, [&](int r, const float* buf) {
+    for (int i = threadIdx.x; i < sub * 32 * kW4Rows; i += kW4Threads) {
+      const int col = i & 31, row = (i >> 5) % kW4Rows, g = (i >> 5) / kW4Rows, u = index(r, g);
+      if (u >= units) continue;
+      const W4Batch b = tab[u / FT];
+      const int tile = u % FT * kGuTiles, m = 2 * (col >> 4), f = tile / 2 * 16 + col;
+      if (b.slot < 0 || row >= b.n || tile + m >= d.Mt) continue;
+      const float* mg = reinterpret_cast<const float*>(slab(b.slot) + d.mult) + (tile + m) * 16 + (col & 15);
+      const float gv = w4_sum_part<kGuTiles, 1>(buf, g * ks, ks, m, row, col & 15) * mg[0];
+      const float uv = w4_sum_part<kGuTiles, 1>(buf, g * ks, ks, m + 1, row, col & 15) * mg[16];
+      const float h = gv / (1.f + __expf(-gv)) * uv;
+      // h as the sum of two bf16: 16 significant bits reach the down product
+      const uint16_t hi = f32_to_bf16(h);
+      const size_t o = (size_t)(b.p0 + row) * I + f;
+      a.h[o] = hi;
+      a.h[a.n * I + o] = isfinite(bf16_to_f32(hi)) ? f32_to_bf16(h - bf16_to_f32(hi)) : 0;
     }
-    const int tile = u % FT, pe = a.f.offset[e + 1];
-    const uint8_t* base = reinterpret_cast<const uint8_t*>(a.f.pool) + (size_t)slot * a.sl.bytes;
-    const W4Tile t[2] = {w4_tile(base, d, 2 * tile, lane), w4_tile(base, d, 2 * tile + 1, lane)};
-    const float* mg = reinterpret_cast<const float*>(base + d.mult) + tile * 32;
-    const float* mu = mg + 16;
-    const int per = (d.Kb + kW4Warps - 1) / kW4Warps;
-    for (int p0 = a.f.offset[e]; p0 < pe; p0 += 8 * NB) {
-      const int nt = min(8 * NB, pe - p0);
-      const uint16_t* xr[NB];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-        xr[nb] = a.f.x + (size_t)(a.f.rows[p0 + min(8 * nb + (lane >> 2), nt - 1)] / a.f.k) * a.f.H + 8 * (lane & 3);
-      float acc[2][NB][4] = {};
-      w4_accumulate<2, NB, false>(t, xr, 0, d.K, d.G, min(warp * per, d.Kb), min((warp + 1) * per, d.Kb), lane & 3,
-                                  acc);
-      __syncthreads();
-      w4_store_part<2, NB>(red, warp, lane, acc);
-      __syncthreads();
-      for (int i = threadIdx.x; i < 16 * nt; i += kW4Threads) {
-        const int col = i & 15, row = i >> 4;
-        const float g = w4_sum_part<2, NB>(red, 0, kW4Warps, 0, row, col) * mg[col];
-        const float v = w4_sum_part<2, NB>(red, 0, kW4Warps, 1, row, col) * mu[col];
-        const float h = g / (1.f + __expf(-g)) * v;
-        // h as the sum of two bf16: 16 significant bits reach the down product
-        const uint16_t hi = f32_to_bf16(h);
-        const size_t o = (size_t)(p0 + row) * I + tile * 16 + col;
-        a.h[o] = hi;
-        a.h[a.n * I + o] = isfinite(bf16_to_f32(hi)) ? f32_to_bf16(h - bf16_to_f32(hi)) : 0;
-      }
-    }
-  }
+  });
 }
 
-// Down: unit = (listed expert, two tiles of 16 output columns); four warps split the inputs of a tile.
-template <int NB>
-__global__ void __launch_bounds__(kW4Threads) w4_down_kernel(const W4FfnArgs a) {
-  constexpr int KS = 4, TPC = kW4Warps / KS;
-  __shared__ float red[kW4Warps * NB * 4 * 32];
+// Down: unit = (row batch, four tiles of 16 output columns).
+constexpr int kDnTiles = 4;
+template <bool G32>
+__global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_down_kernel(const W4FfnArgs a, int most) {
+  extern __shared__ W4Batch tab[];
+  __shared__ float red[2 * kW4Warps * kDnTiles * 128];
+  __shared__ int tmp[33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const W4Dims& d = a.sl.dn;
-  const int nl = *a.f.n_list, FT = (d.Mt + TPC - 1) / TPC;
-  for (int u = blockIdx.x; u < nl * FT; u += gridDim.x) {
-    int e, slot;
-    if (!w4_slot(a.f, u / FT, e, slot)) continue;
-    const int tile0 = u % FT * TPC, tile = tile0 + warp / KS, part = warp % KS, pe = a.f.offset[e + 1];
-    const bool ok = slot >= 0 && slot < a.f.S;
-    const uint8_t* base =
-        reinterpret_cast<const uint8_t*>(a.f.pool) + (size_t)(ok ? slot : 0) * a.sl.bytes + a.sl.dn_at;
-    const float* mult = reinterpret_cast<const float*>(base + d.mult);
-    const int per = (d.Kb + KS - 1) / KS;
-    for (int p0 = a.f.offset[e]; p0 < pe; p0 += 8 * NB) {
-      const int nt = min(8 * NB, pe - p0);
-      float acc[1][NB][4] = {};
-      if (ok && tile < d.Mt) {
-        const W4Tile t[1] = {w4_tile(base, d, tile, lane)};
-        const uint16_t* xr[NB];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-          xr[nb] = a.h + (size_t)(p0 + min(8 * nb + (lane >> 2), nt - 1)) * d.K + 8 * (lane & 3);
-        w4_accumulate<1, NB, true>(t, xr, a.n * d.K, d.K, d.G, min(part * per, d.Kb), min((part + 1) * per, d.Kb),
-                                   lane & 3, acc);
-      }
-      __syncthreads();
-      w4_store_part<1, NB>(red, warp, lane, acc);
-      __syncthreads();
-      for (int i = threadIdx.x; i < TPC * 16 * nt; i += kW4Threads) {
-        const int col = i & 15, row = (i >> 4) % nt, tl = (i >> 4) / nt, n = (tile0 + tl) * 16 + col;
-        // an expert without a slot adds nothing: its rows are zero
-        if (n < d.N)
-          a.f.y[(size_t)(p0 + row) * d.N + n] = ok ? w4_sum_part<1, NB>(red, tl * KS, KS, 0, row, col) * mult[n] : 0.f;
-      }
+  const int nbat = w4_batches(a.f, tab, most, tmp);
+  const int FT = (d.Mt + kDnTiles - 1) / kDnTiles, units = nbat * FT;
+  const int ks = w4_split(units, d.Kb, gridDim.x), sub = kW4Warps / ks;
+  const int rounds = (units - (int)blockIdx.x * sub + (int)gridDim.x * sub - 1) / ((int)gridDim.x * sub);
+  if (rounds <= 0) return;
+  auto index = [&](int r, int g) { return (r * (int)gridDim.x + (int)blockIdx.x) * sub + g; };
+  auto down = [&](int slot) {
+    return reinterpret_cast<const uint8_t*>(a.f.pool) + (size_t)slot * a.sl.bytes + a.sl.dn_at;
+  };
+  auto unit = [&](int r) {
+    W4Unit<1> u;
+    u.nm = 0;
+    const int i = index(r, warp / ks);
+    if (i >= units) return u;
+    const W4Batch b = tab[i / FT];
+    if (b.slot < 0) return u;
+    const int tile = i % FT * kDnTiles;
+    w4_at(u, down(b.slot), d, tile, min(kDnTiles, d.Mt - tile), lane);
+    u.x[0] = a.h + (size_t)(b.p0 + min(lane >> 2, b.n - 1)) * d.K + 8 * (lane & 3);
+    return u;
+  };
+  w4_stream<kDnTiles, 1, true, G32>(d, ks, rounds, a.n * d.K, red, unit, [&](int r, const float* buf) {
+    for (int i = threadIdx.x; i < sub * 16 * kDnTiles * kW4Rows; i += kW4Threads) {
+      const int col = i % (16 * kDnTiles), row = i / (16 * kDnTiles) % kW4Rows, g = i / (16 * kDnTiles * kW4Rows);
+      const int u = index(r, g);
+      if (u >= units) continue;
+      const W4Batch b = tab[u / FT];
+      const int n = u % FT * (16 * kDnTiles) + col;
+      if (row >= b.n || n >= d.N) continue;
+      // an expert without a slot adds nothing: its rows are zero
+      float v = 0.f;
+      if (b.slot >= 0)
+        v = w4_sum_part<kDnTiles, 1>(buf, g * ks, ks, col >> 4, row, col & 15) *
+            reinterpret_cast<const float*>(down(b.slot) + d.mult)[n];
+      a.f.y[(size_t)(b.p0 + row) * d.N + n] = v;
     }
-  }
+  });
 }
 
 static int w4_sms(int* sms) {
@@ -271,16 +419,17 @@ int launch_ffn_w4(const FfnArgs& f, int group, void* ws, size_t ws_bytes, int ma
   int sms = 0;
   const int r = w4_sms(&sms);
   if (r != MOE_OK) return r;
-  W4FfnArgs a{f, w4_slab(f.H, f.I, group), (uint16_t*)ws, (size_t)n};
-  const int g1 = std::min(max_list * (a.sl.gu.Mt / 2), sms * 8), g2 = std::min(max_list * ((a.sl.dn.Mt + 1) / 2), sms * 8);
+  const W4FfnArgs a{f, w4_slab(f.H, f.I, group), (uint16_t*)ws, (size_t)n};
+  const int most = std::min(n, std::min(max_list, n) + n / kW4Rows);  // one per expert and one per full batch
+  const size_t smem = most * sizeof(W4Batch);
   if (prof) prof->begin(MOE_PROF_FFN_GATEUP, stream);
-  if (f.T <= 8) w4_gateup_kernel<1><<<g1, kW4Threads, 0, stream>>>(a);
-  else w4_gateup_kernel<2><<<g1, kW4Threads, 0, stream>>>(a);
+  if (group == 32) w4_gateup_kernel<true><<<sms * kW4Ctas, kW4Threads, smem, stream>>>(a, most);
+  else w4_gateup_kernel<false><<<sms * kW4Ctas, kW4Threads, smem, stream>>>(a, most);
   MOE_LAUNCH_CHECK();
   if (prof) prof->end(stream);
   if (prof) prof->begin(MOE_PROF_FFN_DOWN, stream);
-  if (f.T <= 8) w4_down_kernel<1><<<g2, kW4Threads, 0, stream>>>(a);
-  else w4_down_kernel<2><<<g2, kW4Threads, 0, stream>>>(a);
+  if (group == 32) w4_down_kernel<true><<<sms * kW4Ctas, kW4Threads, smem, stream>>>(a, most);
+  else w4_down_kernel<false><<<sms * kW4Ctas, kW4Threads, smem, stream>>>(a, most);
   MOE_LAUNCH_CHECK();
   if (prof) prof->end(stream);
   return MOE_OK;
@@ -350,18 +499,26 @@ extern "C" int moe_w4_linear(const void* x, long long ldx, int T, int K, int N, 
   const int r = w4_sms(&sms);
   if (r != MOE_OK) return r;
   W4LinArgs a{(const uint16_t*)x, (size_t)ldx, (size_t)ldo, T, 1, (const uint8_t*)w, w4_dims(K, N, group), out, out_f32};
-  while (a.ks < kW4Warps && a.d.Mt * a.ks < sms * 32) a.ks *= 2;
-  const int gx = (a.d.Mt + kW4Warps / a.ks - 1) / (kW4Warps / a.ks);
-  const int rows = T <= 8 ? 8 : T <= 16 ? 16 : 32;
+  // rows of a pass, and tiles of a warp: four where that leaves a unit for every other warp, as many rows need
+  // the registers for their sums
+  const int rows = T <= 8 ? 8 : T <= 16 ? 16 : 32, ctas = sms * kW4Ctas;
+  const int cm = rows == 32 ? 1 : rows == 16 ? 2 : a.d.Mt >= 8 * ctas ? 4 : a.d.Mt >= ctas ? 2 : 1;
+  const int groups = (a.d.Mt + cm - 1) / cm;
+  a.ks = w4_split(groups, a.d.Kb, ctas);
+  const int gx = std::min((groups + kW4Warps / a.ks - 1) / (kW4Warps / a.ks), ctas);
+  const bool g32 = group == 32;
   for (int t0 = 0; t0 < T; t0 += 65535 * rows) {  // the grid's y
     W4LinArgs b = a;
     b.x += (size_t)t0 * ldx;
     b.out = (char*)out + (size_t)t0 * ldo * (out_f32 ? 4 : 2);
     b.T = std::min(T - t0, 65535 * rows);
     const dim3 grid(gx, (b.T + rows - 1) / rows);
-    if (rows == 8) w4_linear_kernel<1><<<grid, kW4Threads, 0, (cudaStream_t)stream>>>(b);
-    else if (rows == 16) w4_linear_kernel<2><<<grid, kW4Threads, 0, (cudaStream_t)stream>>>(b);
-    else w4_linear_kernel<4><<<grid, kW4Threads, 0, (cudaStream_t)stream>>>(b);
+    auto go = [&](auto kernel, auto kernel32) { (g32 ? kernel32 : kernel)<<<grid, kW4Threads, 0, (cudaStream_t)stream>>>(b); };
+    if (rows == 32) go(w4_linear_kernel<1, 4, false>, w4_linear_kernel<1, 4, true>);
+    else if (rows == 16) go(w4_linear_kernel<2, 2, false>, w4_linear_kernel<2, 2, true>);
+    else if (cm == 4) go(w4_linear_kernel<4, 1, false>, w4_linear_kernel<4, 1, true>);
+    else if (cm == 2) go(w4_linear_kernel<2, 1, false>, w4_linear_kernel<2, 1, true>);
+    else go(w4_linear_kernel<1, 1, false>, w4_linear_kernel<1, 1, true>);
     MOE_LAUNCH_CHECK();
   }
   return MOE_OK;

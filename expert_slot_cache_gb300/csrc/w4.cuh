@@ -10,14 +10,15 @@
 //                            columns g and g + 8 (g = 0..7): chunk 4g + (q + g / 2) % 4 holds inputs
 //                            8q .. 8q + 7 and 32 + 8q .. 32 + 8q + 7 of column g, then the same of
 //                            column g + 8, one 32-bit word for eight inputs.  In a word, the codes of
-//                            inputs 0, 2, 4, 6 start at bits 6, 2, 10, 14, those of 1, 3, 5, 7 sixteen
-//                            bits further (bits 30, 31 wrap to 0, 1).
+//                            inputs 0, 2, 4, 6 start at bits 3, 7, 11, 15, those of 1, 3, 5, 7 sixteen
+//                            bits further (the last one's bits 32-34 wrap to 0-2).
 //   The two readers this serves: in a warp, lane 4g + q's chunk is its A fragment of four 16 x 16 MMAs
 //   (one coalesced 16-byte load each), whose B fragment is 16 consecutive bytes of a bf16 row; and a
 //   thread that owns one column reads its 64 inputs as four 8-byte pieces from shared memory, where the
-//   rotation by g / 2 spreads sixteen columns over all banks.  A code in bits 6-9 of a half is the top of
-//   an fp16 mantissa: 0x4c00 | code << 6 is 16 + code, so (code - 8) * scale is one fused multiply-add
-//   with -24 * scale, exact for a scale of 8 significant bits.
+//   rotation by g / 2 spreads sixteen columns over all banks.  A code in bits 3-6 of a half is the top of
+//   a bf16 mantissa (0x4180 | code << 3 is 16 + code), one in bits 6-9 the top of an fp16 mantissa
+//   (0x4c00 | code << 6 is 16 + code): there (code - 8) * scale is one fused multiply-add with -24 * scale,
+//   exact for a scale of 8 significant bits.
 //   scales  [Mt / 8][Kg][8][8 words] Kg groups, neighbours as for the codes; word g = (column g, column
 //                            g + 8) of the tile as two fp16, divided by the column's multiplier
 //   mult    [Mt * 16] fp32   power of two per column: 2^floor(log2(max |scale|)), 1 where that is 0 or
@@ -98,8 +99,7 @@ __host__ __device__ inline W4Slab w4_slab(int H, int I, int G) {
 
 // First bit of the code of input i (0..7) in a word.
 __host__ __device__ constexpr int w4_code_bit(int i) {
-  const int b[4] = {6, 2, 10, 14};
-  return b[i >> 1] + 16 * (i & 1);
+  return 3 + 4 * (i >> 1) + 16 * (i & 1);
 }
 __host__ __device__ inline uint32_t w4_put(int code, int bit) {
   const uint32_t c = (uint32_t)code;
@@ -109,32 +109,26 @@ __host__ __device__ inline uint32_t w4_put(int code, int bit) {
 // A lane's chunk within a tile block.
 __device__ __forceinline__ int w4_chunk(int g, int q) { return 4 * g + ((q + (g >> 1)) & 3); }
 
-// The words of columns g (w0) and g + 8 (w1) for one run of eight inputs -> the A fragments (bf16x2, as
-// code - 8) of two 16 x 16 MMAs, inputs 0-3 and 4-7 of the run: a code in mantissa bits 2-5 of 0x4300 is
-// 128 + 4 code, and a quarter of that minus 40 is exact.
+// The words of columns g (w0) and g + 8 (w1) for one run of eight inputs -> the A fragments (bf16x2) of two
+// 16 x 16 MMAs, inputs 0-3 and 4-7 of the run, as 16 + code (the caller takes 24 sum(x) off the products).
 __device__ __forceinline__ void w4_frag_bf16(uint32_t w0, uint32_t w1, uint32_t (&a0)[4], uint32_t (&a1)[4]) {
-  const uint32_t quarter = 0x3e803e80u, off = 0xc220c220u;  // 0.25, -40
-  auto conv = [&](uint32_t v) {
-    uint32_t r;
-    v = (v & 0x003c003cu) | 0x43004300u;
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(quarter), "r"(off));
-    return r;
-  };
-  a0[0] = conv(w0 >> 4);
-  a0[1] = conv(w1 >> 4);
-  a0[2] = conv(w0);
-  a0[3] = conv(w1);
+  auto conv = [](uint32_t v) { return (v & 0x00780078u) | 0x41804180u; };
+  a0[0] = conv(w0);
+  a0[1] = conv(w1);
+  a0[2] = conv(w0 >> 4);
+  a0[3] = conv(w1 >> 4);
   a1[0] = conv(w0 >> 8);
   a1[1] = conv(w1 >> 8);
   a1[2] = conv(__funnelshift_r(w0, w0, 12));
   a1[3] = conv(__funnelshift_r(w1, w1, 12));
 }
 
-// C += A(16 x 16, bf16) B(16 x 8, bf16), fp32 accumulators.
-__device__ __forceinline__ void mma_bf16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// D = A(16 x 16, bf16) B(16 x 8, bf16) + C, fp32.
+__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                               float c0, float c1, float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 // The tensor-core path (w4_gemm.cu).

@@ -226,14 +226,14 @@ __device__ __forceinline__ void w4_expand(uint32_t w, __half2 s, uint32_t* o) {
     const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&v), s, m24s);
     return *reinterpret_cast<const uint32_t*>(&r);
   };
-  o[0] = top(w);
-  // codes in bits 2-5: 256 + code; the shift is saved and one more half-precision operation spent,
-  // which keeps the integer and the floating-point pipe equally busy
-  const uint32_t v = (w & 0x003c003cu) | 0x5c005c00u;
-  const __half2 c = __hsub2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(264.f)), p = __hmul2(c, s);
-  o[1] = *reinterpret_cast<const uint32_t*>(&p);
-  o[2] = top(w >> 4);
-  o[3] = top(__funnelshift_r(w, w, 8));
+  // codes in bits 3-6: 128 + code; the shift is saved and one more half-precision operation spent, which
+  // keeps the integer and the floating-point pipe equally busy
+  const uint32_t v = (w & 0x00780078u) | 0x58005800u;
+  const __half2 c = __hsub2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(136.f)), p = __hmul2(c, s);
+  o[0] = *reinterpret_cast<const uint32_t*>(&p);
+  o[1] = top(w >> 1);
+  o[2] = top(w >> 5);
+  o[3] = top(__funnelshift_r(w, w, 9));
 }
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
