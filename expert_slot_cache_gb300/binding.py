@@ -96,7 +96,7 @@ _ffn_w4_ws = _sig("moe_ffn_w4_workspace_bytes", [I32, I32, I32, I32], c_size_t)
 _ffn_w4 = _sig("moe_expert_ffn_w4", [V, I32, I32, I32, I32, I32, I32, V, V, V, V, I32, V, I32, V, V, V, c_size_t, V, V])
 _experts_w4_ws = _sig("moe_experts_w4_workspace_bytes", [I32, I32, I32, I32, I32], c_size_t)
 _experts_w4 = _sig("moe_experts_w4", [V, V, V, I32, I32, I32, I32, I32, I32, V, I32, V, V, V, c_size_t, V, V])
-_balance_ws = _sig("moe_balance_workspace_bytes", [I32], c_size_t)
+_balance_ws = _sig("moe_balance_workspace_bytes", [I32, I32, I32], c_size_t)
 _balance = _sig("moe_balance_loss", [V, I32, V, V, V, I32, I32, I32, I32, I32, c_float, V, V, V, V, V, c_size_t, V, V])
 _layer = _sig("moe_layer_forward", [POINTER(LayerArgs), V, V])
 _layer_ws = _sig("moe_layer_workspace_bytes", [I32, I32, I32, I32, I32, I32], c_size_t)
@@ -128,6 +128,18 @@ def _ptr(t: Optional[torch.Tensor]) -> int:
 def _s(stream=None):
     s = torch.cuda.current_stream() if stream is None else stream
     return c_void_p(s.cuda_stream)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _here(t: torch.Tensor, stream=None) -> int:
+    """The stream handle for work on ``t``: ``stream``, or the current one of its device."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and t.is_cuda:
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
 
 
 # ---------------------------------------------------------------------------
@@ -360,6 +372,8 @@ class W4Linear:
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=packed.device)
         self.workspace = torch.empty(int(_w4_linear_ws(max_tokens, K, N, group)), dtype=torch.uint8,
                                      device=packed.device)
+        self._packed, self._status = packed.data_ptr(), self.dev_status.data_ptr()
+        self._ws, self._ws_bytes, self._f32 = self.workspace.data_ptr(), self.workspace.numel(), out_dtype == torch.float32
 
     def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         T, K = x.shape
@@ -371,10 +385,9 @@ class W4Linear:
             out = torch.empty(T, self.N, dtype=self.out_dtype, device=x.device)
         elif out.dtype != self.out_dtype or out.shape != (T, self.N) or out.stride(1) != 1:
             raise ValueError(f"out: need {self.out_dtype} ({T}, {self.N}) with a contiguous last dimension")
-        _ck(_w4_linear(x.data_ptr(), x.stride(0) if T > 1 else self.K, T, K, self.N, self.group,
-                       self.packed.data_ptr(), out.data_ptr(), out.stride(0) if T > 1 else self.N,
-                       int(self.out_dtype == torch.float32), self.workspace.data_ptr(), self.workspace.numel(),
-                       self.dev_status.data_ptr(), _s(stream)), "moe_w4_linear")
+        _ck(_w4_linear(x.data_ptr(), x.stride(0) if T > 1 else K, T, K, self.N, self.group, self._packed,
+                       out.data_ptr(), out.stride(0) if T > 1 else self.N, self._f32, self._ws, self._ws_bytes,
+                       self._status, _here(x, stream)), "moe_w4_linear")
         return out
 
 
@@ -410,23 +423,27 @@ class W4Experts:
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=pool.device)
         self.workspace = torch.empty(int(_experts_w4_ws(max_tokens, H, I, k, E)), dtype=torch.uint8,
                                      device=pool.device)
+        self._pool, self._e2s = pool.data_ptr(), None if e2s is None else e2s.data_ptr()
+        self._status, self._ws, self._ws_bytes = self.dev_status.data_ptr(), self.workspace.data_ptr(), self.workspace.numel()
 
     def forward(self, x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, out: Optional[torch.Tensor] = None,
                 stream=None) -> torch.Tensor:
         T = x.shape[0]
         if T > self.max_tokens:
             raise ValueError(f"T={T} > max_tokens={self.max_tokens}")
-        _want(x, "x", torch.bfloat16, (T, self.H))
-        _want(ids, "ids", torch.int32, (T, self.k))
-        _want(w, "w", torch.float32, (T, self.k))
+        if x.dtype != torch.bfloat16 or x.shape != (T, self.H) or not x.is_contiguous():
+            raise ValueError(f"x: need contiguous bf16 [{T}][{self.H}]")
+        if ids.dtype != torch.int32 or ids.shape != (T, self.k) or not ids.is_contiguous():
+            raise ValueError(f"ids: need contiguous int32 [{T}][{self.k}]")
+        if w.dtype != torch.float32 or w.shape != (T, self.k) or not w.is_contiguous():
+            raise ValueError(f"w: need contiguous fp32 [{T}][{self.k}]")
         if out is None:
             out = torch.empty(T, self.H, dtype=torch.bfloat16, device=x.device)
         else:
             _want(out, "out", torch.bfloat16, (T, self.H))
         _ck(_experts_w4(x.data_ptr(), ids.data_ptr(), w.data_ptr(), T, self.H, self.I, self.k, self.E, self.group,
-                        self.pool.data_ptr(), self.S, None if self.e2s is None else self.e2s.data_ptr(),
-                        out.data_ptr(), self.workspace.data_ptr(), self.workspace.numel(),
-                        self.dev_status.data_ptr(), _s(stream)), "moe_experts_w4")
+                        self._pool, self.S, self._e2s, out.data_ptr(), self._ws, self._ws_bytes, self._status,
+                        _here(x, stream)), "moe_experts_w4")
         return out
 
 
@@ -446,28 +463,31 @@ def balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float, seq_start
                  stream=None) -> Balance:
     """Loss, per-sequence expert counts and (with_grad) the gradient in the logits times ``grad_loss`` (1 if None)."""
     T, E = logits.shape
-    if logits.dtype != torch.float32:
-        _want(logits, "logits", torch.bfloat16, (T, E))
-    _want(logits, "logits", logits.dtype)
-    _want(ids, "ids", torch.int32, (T, ids.shape[1]))
-    if token_mask is not None and token_mask.dtype != torch.bool:
-        _want(token_mask, "token_mask", torch.uint8)
+    bf16 = logits.dtype == torch.bfloat16
+    if not (bf16 or logits.dtype == torch.float32) or not logits.is_contiguous():
+        raise ValueError(f"logits: need contiguous fp32 or bf16, got {logits.dtype}")
+    k = ids.shape[-1]
+    if ids.dtype != torch.int32 or ids.shape != (T, k) or not ids.is_contiguous():
+        raise ValueError(f"ids: need contiguous int32 [{T}][k], got {ids.dtype} {tuple(ids.shape)}")
     if token_mask is not None:
-        _want(token_mask, "token_mask", token_mask.dtype, (T,))
+        _want(token_mask, "token_mask", torch.bool if token_mask.dtype == torch.bool else torch.uint8, (T,))
+    n_seq = 1
     if seq_start is not None:
         _want(seq_start, "seq_start", torch.int32)
+        n_seq = seq_start.numel() - 1
     if grad_loss is not None and (grad_loss.dtype != torch.float32 or grad_loss.numel() != 1):
         raise ValueError("grad_loss: need one fp32 value")
-    n_seq = 1 if seq_start is None else seq_start.numel() - 1
     dev = logits.device
     loss = torch.empty((), dtype=torch.float32, device=dev) if with_loss else None
-    counts = torch.empty(max(n_seq, 0), E, dtype=torch.int32, device=dev)
+    counts = torch.empty((max(n_seq, 0), E), dtype=torch.int32, device=dev)
     grad = torch.empty_like(logits) if with_grad else None
-    ws = torch.empty(int(_balance_ws(n_seq)), dtype=torch.uint8, device=dev)
-    _ck(_balance(logits.data_ptr(), int(logits.dtype == torch.bfloat16), ids.data_ptr(), _ptr(token_mask) or None,
-                 _ptr(seq_start) or None, n_seq, T, E, ids.shape[1], ROUTE_SIGMOID if sigmoid else 0, coef,
-                 _ptr(grad_loss) or None, counts.data_ptr(), _ptr(loss) or None, _ptr(grad) or None, ws.data_ptr(),
-                 ws.numel(), _ptr(dev_status) or None, _s(stream)), "moe_balance_loss")
+    nws = _balance_ws(T, E, n_seq)
+    ws = torch.empty(nws, dtype=torch.uint8, device=dev)
+    _ck(_balance(logits.data_ptr(), bf16, ids.data_ptr(), None if token_mask is None else token_mask.data_ptr(),
+                 None if seq_start is None else seq_start.data_ptr(), n_seq, T, E, k, ROUTE_SIGMOID if sigmoid else 0,
+                 coef, None if grad_loss is None else grad_loss.data_ptr(), counts.data_ptr(),
+                 loss.data_ptr() if with_loss else None, grad.data_ptr() if with_grad else None, ws.data_ptr(), nws,
+                 None if dev_status is None else dev_status.data_ptr(), _here(logits, stream)), "moe_balance_loss")
     return Balance(loss, counts, grad)
 
 

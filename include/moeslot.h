@@ -506,12 +506,12 @@ int moe_experts_w4(const void* x, const int32_t* ids, const float* w, int T, int
  *   token_mask device uint8 [T], 0 = padding, or NULL
  *   seq_start  device int32 [n_seq + 1], ascending, sequence s is the tokens
  *              [seq_start[s], seq_start[s + 1]), empty ones allowed; NULL with
- *              n_seq = 1: one sequence of T tokens
+ *              n_seq = 1: one sequence of T tokens (T, n_seq <= 2^26)
  *   grad_loss  device fp32 [1] (the loss's own gradient) or NULL = 1
  *   counts     device int32 [n_seq][E] output
  *   loss       device fp32 [1] output, or NULL
  *   grad_logits device [T][E] output in the type of logits, or NULL
- *   workspace  device, moe_balance_workspace_bytes(n_seq), 256-byte aligned
+ *   workspace  device, moe_balance_workspace_bytes(T, E, n_seq), 256-byte aligned
  * Tokens masked or in no sequence add nothing, their logits are not read into
  * any result and their gradient is 0; with no valid token the loss is 0.  A row
  * of -inf has no probabilities: it adds 0 and gets a zero gradient.  The result
@@ -522,7 +522,7 @@ int moe_experts_w4(const void* x, const int32_t* ids, const float* w, int T, int
  * not in [1, 1024], k not in [1, min(16, E)], n_seq < 1 or unknown flags;
  * MOE_ERR_ALIGN for an unaligned or small workspace.
  */
-size_t moe_balance_workspace_bytes(int n_seq);
+size_t moe_balance_workspace_bytes(int T, int E, int n_seq);
 int moe_balance_loss(const void* logits, int bf16, const int32_t* ids, const uint8_t* token_mask,
                      const int32_t* seq_start, int n_seq, int T, int E, int k, int rflags, float coef,
                      const float* grad_loss, int32_t* counts, float* loss, void* grad_logits, void* workspace,

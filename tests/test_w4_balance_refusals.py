@@ -32,7 +32,7 @@ def test_sizes(b):
     for K, N, G in ((0, 8, 64), (12, 8, 64), (64, 0, 64), (64, 8, 16), (64, 8, 0), (1 << 21, 8, 64), (64, 1 << 25, 64)):
         assert b.w4_bytes(K, N, G) == 0
     assert b.w4_slab_bytes(100, 128, 64) == 0 and b.w4_slab_bytes(256, 100, 64) == 0
-    assert int(b._balance_ws(0)) == 0 and int(b._balance_ws(5)) > 0
+    assert int(b._balance_ws(8, 16, 0)) == 0 and int(b._balance_ws(8, 1025, 1)) == 0 and int(b._balance_ws(8, 16, 5)) > 0
     assert int(b._experts_w4_ws(0, 256, 128, 2, 16)) == 0 and int(b._experts_w4_ws(4, 256, 128, 17, 32)) == 0
 
 
