@@ -42,7 +42,7 @@ __device__ __forceinline__ int bal_seq_start(const BalArgs& a, int s) {
 
 constexpr int kCntThreads = 512;
 constexpr int kCntCluster = 16;  // CTAs of a cluster, at most
-constexpr int kCntIds = 4096;    // ids per CTA that a cluster size aims at
+constexpr int kCntIds = 1024;    // ids per CTA that a cluster size aims at
 
 __device__ __forceinline__ uint32_t bal_cluster_ctas() {
   uint32_t r;
@@ -57,13 +57,22 @@ __device__ __forceinline__ uint32_t bal_cluster_rank() {
 __device__ __forceinline__ void bal_cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The 32-bit word at shared::cta address p of CTA `rank` of the cluster.
-__device__ __forceinline__ int bal_peer(const int* p, uint32_t rank) {
-  uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), r;
-  int v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(r) : "memory");
-  return v;
+// The sum of the 32-bit words at shared::cta address p of the cluster's CTAs, all of them in flight at once.
+__device__ __forceinline__ int bal_cluster_sum(const int* p, uint32_t nc) {
+  const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+  int v[kCntCluster], sum = 0;
+#pragma unroll
+  for (uint32_t r = 0; r < kCntCluster; ++r) {
+    v[r] = 0;
+    if (r < nc) {
+      uint32_t at;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(a), "r"(r));
+      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v[r]) : "r"(at));
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kCntCluster; ++r) sum += v[r];
+  return sum;
 }
 
 // One cluster per sequence: its expert counts, f, valid tokens, and the tokens' sequence ids.  Integer sums:
@@ -116,12 +125,10 @@ __global__ void __launch_bounds__(kCntThreads) balance_count_kernel(const BalArg
   if (s == a.n_seq - 1)
     for (int t = b1 + (int)(rank * kCntThreads + threadIdx.x); t < a.T; t += (int)nc * kCntThreads) a.seqid[t] = -1;
   bal_cluster_sync();
-  int tok = 0;
-  for (uint32_t r = 0; r < nc; ++r) tok += bal_peer(&ntok, r);
+  const int tok = bal_cluster_sum(&ntok, nc);
   const float u = (float)a.E / ((float)a.k * (float)max(tok, 1));
   for (int e = (int)(rank * kCntThreads + threadIdx.x); e < a.E; e += (int)nc * kCntThreads) {
-    int c = 0;
-    for (uint32_t r = 0; r < nc; ++r) c += bal_peer(&cnt[e], r);
+    const int c = bal_cluster_sum(&cnt[e], nc);
     a.counts[(size_t)s * a.E + e] = c;
     a.f[(size_t)s * a.E + e] = (float)c * u;
   }
@@ -134,7 +141,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float bal_exp2(float x) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float bal_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -173,121 +185,140 @@ struct BalVec {
   }
 };
 
-// Groups of `lanes` lanes (a power of two) take a token each; a lane holds NC chunks of V values, chunk c of
-// lane l being the row's (c * lanes + l)-th.  CTA b takes `per` consecutive tokens.
-template <int V, int NC, bool BF16, bool SIG>
-__global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalArgs a, int lanes, int per) {
-  constexpr int W = kBalThreads / 32;
+// Groups of L lanes take a token each; a lane holds NC chunks of V values, chunk c of lane l being the row's
+// (c L + l)-th.  CTA b takes `per` consecutive tokens.
+//
+// What bounds the pass next to memory is its instructions, so the usual row costs few: exp of the logits as
+// they are (or 1 / (1 + exp(-l))), no maximum.  A row whose sum leaves [2^-20, 2^100] is done again with the
+// maximum taken off; for the others whatever underflows is below 2^-106 of the sum.
+template <int V, int NC, int L, bool BF16, bool SIG>
+__global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalArgs a, int per) {
+  constexpr int W = kBalThreads / 32, G = kBalThreads / L, N = NC * V;
   __shared__ int s_red[W];
   __shared__ double s_loss[W];
   __shared__ int s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gl = lane & (lanes - 1), groups = kBalThreads / lanes, g = threadIdx.x / lanes;
+  const int gl = threadIdx.x % L, g = threadIdx.x / L;
   const int t_end = min((int)(blockIdx.x + 1) * per, a.T);
-  auto fetch = [&](int t, BalVec<BF16, V> (&x)[NC]) {
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int e = (c * lanes + gl) * V;
-      if (t < t_end && e < a.E) x[c].load(a.logits, (size_t)t * a.E + e);
-    }
-  };
+  bool has[NC];
   BalVec<BF16, V> x[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    has[c] = (c * L + gl) * V < a.E;
+#pragma unroll
+    for (int j = 0; j < (V == 1 ? 1 : 4); ++j) x[c].r[j] = V > 1 && BF16 ? 0xff80ff80u : 0xff800000u;  // -inf past the row
+  }
   int t = blockIdx.x * per + g;
-  fetch(t, x);
+  size_t row = (size_t)t * a.E + gl * V;  // the lane's first value
+  auto fetch = [&](bool in, size_t at) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      if (in && has[c]) x[c].load(a.logits, at + c * (L * V));
+  };
+  fetch(t < t_end, row);
   pdl_wait();
   // valid tokens of all sequences
   int tv = 0;
   for (int s = threadIdx.x; s < a.n_seq; s += kBalThreads) tv += a.tokens[s];
   tv = __reduce_add_sync(MOE_FULL_MASK, tv);
   if (lane == 0) s_red[warp] = tv;
-  int sid = t < t_end ? a.seqid[t] : -1;
+  int sid = t < t_end ? a.seqid[t] : -1, sid_f = -1;
   __syncthreads();
   tv = 0;
   for (int w = 0; w < W; ++w) tv += s_red[w];
   const float gscale = a.coef / (float)max(tv, 1) * (a.grad && a.grad_out ? *a.grad_out : 1.f);
+  auto group_sum = [](float v) {
+#pragma unroll
+    for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(MOE_FULL_MASK, v, o);
+    return v;
+  };
 
-  float loss = 0.f;
-  for (; t - g < t_end; t += groups) {  // the same number of rounds for every lane
+  float loss = 0.f, f[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = 0.f;
+  for (; t - g < t_end; t += G, row += (size_t)G * a.E) {  // the same number of rounds for every lane
     const bool in = t < t_end, valid = in && sid >= 0 && sid < a.n_seq;
-    const float* fr = a.f + (size_t)(valid ? sid : 0) * a.E;
-    const int tn = t + groups;
-    const int sn = tn < t_end ? a.seqid[tn] : -1;
-    float mx = -INFINITY;
-    float q[NC * V], keep[SIG ? NC * V : 1];
+    const int sn = t + G < t_end ? a.seqid[t + G] : -1;
+    if (valid && sid != sid_f) {
+      sid_f = sid;
+      const float* fr = a.f + (size_t)sid * a.E + gl * V;
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+      for (int c = 0; c < NC; ++c)
+        if (has[c]) {
+          if constexpr (V == 1) {
+            f[c] = fr[c * L];
+          } else {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const bool has = valid && (c * lanes + gl) * V < a.E;
-        q[c * V + j] = has ? x[c].at(j) : -INFINITY;
-        mx = fmaxf(mx, q[c * V + j]);
-      }
-    fetch(tn, x);
-    for (int o = lanes >> 1; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(MOE_FULL_MASK, mx, o));
-    float sum = 0.f, dot = 0.f;
-    // softmax: exp(l - max).  sigmoid: sigma(l), or, where the largest logit is below -20, sigma(l) / exp(max):
-    // the sum takes the factor out, and nothing underflows that counts.
-    const float ref = SIG ? (mx < -20.f ? mx : 0.f) : mx;
-    const float shift = -(ref == -INFINITY ? 0.f : ref) * kLog2e;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int e0 = (c * lanes + gl) * V;
-      float f[V];
-      if constexpr (V == 1) {
-        f[0] = e0 < a.E ? __ldg(fr + e0) : 0.f;
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; j += 4) {
-          const float4 w = e0 < a.E ? __ldg(reinterpret_cast<const float4*>(fr + e0 + j)) : make_float4(0.f, 0.f, 0.f, 0.f);
-          f[j] = w.x, f[j + 1] = w.y, f[j + 2] = w.z, f[j + 3] = w.w;
+            for (int j = 0; j < V; j += 4) {
+              const float4 w = *reinterpret_cast<const float4*>(fr + c * (L * V) + j);
+              f[c * V + j] = w.x, f[c * V + j + 1] = w.y, f[c * V + j + 2] = w.z, f[c * V + j + 3] = w.w;
+            }
+          }
         }
-      }
+    }
+    float l[N], q[N], keep[SIG ? N : 1], sum = 0.f, dot = 0.f;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int i = c * V + j;
-        const float l = q[i];
+    for (int i = 0; i < N; ++i) {
+      l[i] = x[i / V].at(i % V);
+      q[i] = bal_exp2(SIG ? -kLog2e * l[i] : kLog2e * l[i]);
+      if (SIG) {
+        const float em = q[i];
+        q[i] = bal_rcp(1.f + em);
+        keep[i] = fminf(em, 3e38f) * q[i];  // 1 - sigma
+      }
+      sum += q[i];
+      dot = fmaf(q[i], f[i], dot);
+    }
+    sum = group_sum(sum);
+    dot = group_sum(dot);
+    const bool rare = valid && !(sum >= 0x1p-20f && sum <= 0x1p100f);
+    if (__any_sync(MOE_FULL_MASK, rare)) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < N; ++i) mx = fmaxf(mx, l[i]);
+#pragma unroll
+      for (int o = L / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(MOE_FULL_MASK, mx, o));
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      float sum2 = 0.f, dot2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float v;
         if (SIG) {
-          const float em = bal_exp2(-fabsf(l) * kLog2e);  // sigma = 1 / (1 + em) or em / (1 + em)
-          const float inv = __fdividef(1.f, 1.f + em);
-          const float lo = mx < -20.f ? bal_exp2(fmaf(l, kLog2e, shift)) : em;
-          keep[i] = (l >= 0.f ? em : 1.f) * inv;
-          q[i] = (l >= 0.f ? 1.f : lo) * inv;
+          // sigma(l) / exp(min(max, 0)) = exp(min(l, 0) - min(max, 0)) / (1 + exp(-|l|)); NaN stays NaN
+          const float em = expf(-fabsf(l[i])), r = 1.f / (1.f + em);
+          v = expf(fminf(l[i], 0.f) - fminf(ref, 0.f)) * r;
+          if (rare) keep[i] = (l[i] >= 0.f ? em : 1.f) * r;
         } else {
-          q[i] = bal_exp2(fmaf(l, kLog2e, shift));
+          v = expf(l[i] - ref);
         }
-        sum += q[i];
-        dot = fmaf(q[i], f[j], dot);
+        sum2 += v;
+        dot2 = fmaf(v, f[i], dot2);
+        if (rare) q[i] = v;
+      }
+      sum2 = group_sum(sum2);
+      dot2 = group_sum(dot2);
+      if (rare) {
+        sum = sum2;
+        dot = dot2;
       }
     }
-    for (int o = lanes >> 1; o; o >>= 1) {
-      sum += __shfl_xor_sync(MOE_FULL_MASK, sum, o);
-      dot += __shfl_xor_sync(MOE_FULL_MASK, dot, o);
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row of -inf has no probabilities, nor has one left out
+    fetch(t + G < t_end, row + (size_t)G * a.E);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row of -inf has no probabilities
     const float dt = dot * inv;
-    loss += dt;
-    if (a.grad && in) {
+    if (valid) loss += dt;
+    if (a.grad) {
       const float gs = gscale * inv;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int e0 = (c * lanes + gl) * V;
-        if (e0 >= a.E) continue;
         float v[V];
-        if constexpr (V == 1) {
-          v[0] = __ldg(fr + e0);
-        } else {
-#pragma unroll
-          for (int j = 0; j < V; j += 4) {
-            const float4 w = __ldg(reinterpret_cast<const float4*>(fr + e0 + j));
-            v[j] = w.x, v[j + 1] = w.y, v[j + 2] = w.z, v[j + 3] = w.w;
-          }
-        }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          v[j] = gs * q[c * V + j] * (v[j] - dt);
-          if (SIG) v[j] *= keep[c * V + j];
+          const int i = c * V + j;
+          v[j] = gs * q[i] * (f[i] - dt);
+          if (SIG) v[j] *= keep[i];
+          if (!valid) v[j] = 0.f;
         }
-        BalVec<BF16, V>::store(a.grad, (size_t)t * a.E + e0, v);
+        if (in && has[c]) BalVec<BF16, V>::store(a.grad, row + c * (L * V), v);
       }
     }
     sid = sn;
@@ -307,14 +338,20 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalArgs a, i
     s_last = atomicAdd(a.ticket, 1) == (int)gridDim.x - 1;
   }
   __syncthreads();
-  if (s_last && warp == 0) {
-    // the last CTA adds the parts: 32 strided sums, then their tree
+  if (s_last) {
+    // the last CTA adds the parts: strided sums, each warp's tree, the warps in order
     __threadfence();
     double v = 0.;
-    for (int i = lane; i < (int)gridDim.x; i += 32) v += *(volatile double*)(a.part + i);
+    for (int i = threadIdx.x; i < (int)gridDim.x; i += kBalThreads) v += __ldcg(a.part + i);
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(MOE_FULL_MASK, v, o);
-    if (lane == 0) *a.loss = (float)(v * ((double)a.coef / max(tv, 1)));
+    if (lane == 0) s_loss[warp] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      v = 0.;
+      for (int w = 0; w < W; ++w) v += s_loss[w];
+      *a.loss = (float)(v * ((double)a.coef / max(tv, 1)));
+    }
   }
 }
 
@@ -322,25 +359,26 @@ constexpr int kBalMaxGrid = 4096;
 
 static size_t bal256(size_t v) { return (v + 255) & ~size_t(255); }
 
-template <int V, int NC>
-static int launch_pass(const BalArgs& a, bool bf16, bool sig, int lanes, int sms, cudaStream_t s) {
-  // CTAs of whole rounds of tokens, up to six per SM
-  const int groups = kBalThreads / lanes, most = std::min(sms * 6, kBalMaxGrid);
-  const int rounds = (int)(((int64_t)a.T + (int64_t)most * groups - 1) / ((int64_t)most * groups));
-  const int per = rounds * groups;
-  const dim3 grid((a.T + per - 1) / per), block(kBalThreads);
-  cudaError_t e;
-  if (bf16) {
-    e = sig ? launch_pdl(balance_kernel<V, NC, true, true>, grid, block, 0, s, a, lanes, per)
-            : launch_pdl(balance_kernel<V, NC, true, false>, grid, block, 0, s, a, lanes, per);
-  } else if constexpr (V <= 4) {
-    e = sig ? launch_pdl(balance_kernel<V, NC, false, true>, grid, block, 0, s, a, lanes, per)
-            : launch_pdl(balance_kernel<V, NC, false, false>, grid, block, 0, s, a, lanes, per);
-  } else {
-    e = cudaErrorInvalidValue;
-  }
-  MOE_CUDA_TRY(e);
-  return MOE_OK;
+// CTAs of whole rounds of tokens, as many as are resident at once.
+template <int V, int NC, int L, bool BF16>
+static int launch_pass(const BalArgs& a, bool sig, int sms, cudaStream_t s) {
+  auto run = [&](auto kernel, int (&resident)[64]) -> int {
+    int dev = 0;
+    MOE_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= 64) return MOE_ERR_CUDA;
+    if (resident[dev] == 0) {
+      int n = 0;
+      MOE_CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kBalThreads, 0));
+      resident[dev] = std::max(n, 1);
+    }
+    constexpr int G = kBalThreads / L;
+    const int64_t most = std::min(sms * resident[dev], kBalMaxGrid);
+    const int per = (int)((a.T + most * G - 1) / (most * G)) * G;
+    MOE_CUDA_TRY(launch_pdl(kernel, dim3((a.T + per - 1) / per), dim3(kBalThreads), 0, s, a, per));
+    return MOE_OK;
+  };
+  static int r0[64] = {}, r1[64] = {};
+  return sig ? run(balance_kernel<V, NC, L, BF16, true>, r1) : run(balance_kernel<V, NC, L, BF16, false>, r0);
 }
 
 // Workspace: ticket, partial losses, valid tokens per sequence, sequence of each token, f.
@@ -411,24 +449,32 @@ extern "C" int moe_balance_loss(const void* logits, int bf16, const int32_t* ids
   cfg.numAttrs = 1;
   MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, balance_count_kernel, a));
   const bool sig = rflags & MOE_ROUTE_SIGMOID;
-  // 16-byte chunks where every row starts on one; lanes: about 16 values each, so that few reductions are
-  // needed and a warp has several rows in flight
+  // 16-byte chunks where every row starts on one; at most 16 values (bf16: 24) a lane, so that few sums cross
+  // lanes and a warp has several rows in flight
   const int v = bf16 ? 8 : 4;
   const bool vec = E % v == 0 && (uintptr_t)logits % 16 == 0 && (uintptr_t)grad_logits % 16 == 0;
-  const int chunks = vec ? E / v : E;
   if (!vec) {
-    if (E <= 128) return launch_pass<1, 4>(a, bf16, sig, 32, sms, s);
-    if (E <= 384) return launch_pass<1, 12>(a, bf16, sig, 32, sms, s);
-    return launch_pass<1, 32>(a, bf16, sig, 32, sms, s);
+    if (bf16) {
+      if (E <= 128) return launch_pass<1, 4, 32, true>(a, sig, sms, s);
+      if (E <= 384) return launch_pass<1, 12, 32, true>(a, sig, sms, s);
+      return launch_pass<1, 32, 32, true>(a, sig, sms, s);
+    }
+    if (E <= 128) return launch_pass<1, 4, 32, false>(a, sig, sms, s);
+    if (E <= 384) return launch_pass<1, 12, 32, false>(a, sig, sms, s);
+    return launch_pass<1, 32, 32, false>(a, sig, sms, s);
   }
-  int lanes = 1;
-  while (lanes < 32 && lanes * (bf16 ? 2 : 4) < chunks) lanes *= 2;
-  const int nc2 = (chunks + lanes - 1) / lanes;
+  const int chunks = E / v;
   if (bf16) {
-    if (nc2 <= 2) return launch_pass<8, 2>(a, bf16, sig, lanes, sms, s);
-    return launch_pass<8, 4>(a, bf16, sig, lanes, sms, s);
+    if (chunks <= 16) return launch_pass<8, 2, 8, true>(a, sig, sms, s);
+    if (chunks <= 32) return launch_pass<8, 2, 16, true>(a, sig, sms, s);
+    if (chunks <= 48) return launch_pass<8, 3, 16, true>(a, sig, sms, s);
+    if (chunks <= 64) return launch_pass<8, 2, 32, true>(a, sig, sms, s);
+    return launch_pass<8, 4, 32, true>(a, sig, sms, s);
   }
-  if (nc2 <= 3) return launch_pass<4, 3>(a, bf16, sig, lanes, sms, s);
-  if (nc2 <= 4) return launch_pass<4, 4>(a, bf16, sig, lanes, sms, s);
-  return launch_pass<4, 8>(a, bf16, sig, lanes, sms, s);
+  if (chunks <= 16) return launch_pass<4, 2, 8, false>(a, sig, sms, s);
+  if (chunks <= 32) return launch_pass<4, 4, 8, false>(a, sig, sms, s);
+  if (chunks <= 64) return launch_pass<4, 4, 16, false>(a, sig, sms, s);
+  if (chunks <= 96) return launch_pass<4, 3, 32, false>(a, sig, sms, s);
+  if (chunks <= 128) return launch_pass<4, 4, 32, false>(a, sig, sms, s);
+  return launch_pass<4, 8, 32, false>(a, sig, sms, s);
 }
