@@ -26,6 +26,10 @@ namespace moe {
 constexpr int kW4Warps = 8;
 constexpr int kW4Threads = 32 * kW4Warps;
 constexpr int kW4Ctas = 2;   // resident CTAs per SM that the registers allow
+// Routing slots up to which the down kernel adds the experts up itself: the sums then fall to the few CTAs that
+// finish last (one token 20.5 us against 24.6 us with a kernel for them, 32 tokens 142 against 133 us).
+constexpr int kW4Fuse = 16;
+constexpr int kGemmRows = 512;  // routing slots from which the experts' tensor-core path takes over
 
 // One block of 64 inputs in registers: a lane's codes of CM tiles, their columns' scales, and the lane's inputs
 // of NB groups of eight rows (LO: as the sum of two bf16).
@@ -54,8 +58,7 @@ __device__ __forceinline__ void w4_at(W4Unit<NB>& u, const uint8_t* m, const W4D
 }
 
 template <int CM, int NB, bool LO, bool G32>
-__device__ __forceinline__ void w4_load(W4Block<CM, NB, LO, G32>& b, const W4Unit<NB>& u, const W4Dims& d, int kb, int q,
-                                        size_t lo) {
+__device__ __forceinline__ void w4_load_codes(W4Block<CM, NB, LO, G32>& b, const W4Unit<NB>& u, const W4Dims& d, int kb) {
   const uint8_t* c = u.codes + (size_t)(uint32_t)(kb * u.mates) * 512;
   const int kg = G32 ? 2 * kb : d.G == 128 ? kb >> 1 : kb;
   const uint8_t* s = u.scales + (uint32_t)(kg * u.mates) * 32u;
@@ -66,15 +69,30 @@ __device__ __forceinline__ void w4_load(W4Block<CM, NB, LO, G32>& b, const W4Uni
       b.s[m][0] = __ldg(reinterpret_cast<const uint32_t*>(s + m * 32));
       if (G32) b.s[m][G32 ? 1 : 0] = __ldg(reinterpret_cast<const uint32_t*>(s + (u.mates + m) * 32));
     }
+}
+
+// Rows written by the kernel before (LO) are read by plain loads after the wait, x through the read-only path.
+template <int CM, int NB, bool LO, bool G32>
+__device__ __forceinline__ void w4_load_rows(W4Block<CM, NB, LO, G32>& b, const W4Unit<NB>& u, const W4Dims& d, int kb, int q,
+                                             size_t lo) {
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
     for (int p = 0; p < (LO ? 2 : 1); ++p) {
       const uint16_t* x = u.x[nb] + p * lo + kb * 64;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)  // K % 8 == 0: a lane's eight inputs are inside or outside together
-        b.x[nb][p][h] = kb * 64 + 32 * h + 8 * q < d.K ? __ldg(reinterpret_cast<const uint4*>(x + 32 * h)) : make_uint4(0, 0, 0, 0);
+      for (int h = 0; h < 2; ++h) {  // K % 8 == 0: a lane's eight inputs are inside or outside together
+        const uint4* at = reinterpret_cast<const uint4*>(x + 32 * h);
+        b.x[nb][p][h] = kb * 64 + 32 * h + 8 * q < d.K ? (LO ? *at : __ldg(at)) : make_uint4(0, 0, 0, 0);
+      }
     }
+}
+
+template <int CM, int NB, bool LO, bool G32>
+__device__ __forceinline__ void w4_load(W4Block<CM, NB, LO, G32>& b, const W4Unit<NB>& u, const W4Dims& d, int kb, int q,
+                                        size_t lo) {
+  w4_load_codes<CM, NB, LO, G32>(b, u, d, kb);
+  w4_load_rows<CM, NB, LO, G32>(b, u, d, kb, q, lo);
 }
 
 template <int CM, int NB, bool LO, bool G32>
@@ -170,7 +188,8 @@ __host__ __device__ inline int w4_split(int units, int Kb, int ctas) {
 }
 
 // The stream of one CTA: rounds 0 .. rounds - 1 of units; unit(round) gives this warp's unit (of its subgroup)
-// and done(round, red) is called by all threads once the subgroups' parts of a round are in red.
+// and done(round, red) is called by all threads once the subgroups' parts of a round are in red.  The first
+// blocks' codes are loaded before a programmatic dependent's wait, the rows after it.
 template <int CM, int NB, bool LO, bool G32, class Unit, class Done>
 __device__ __forceinline__ void w4_stream(const W4Dims& d, int ks, int rounds, size_t lo, float* red, Unit&& unit,
                                           Done&& done) {
@@ -180,7 +199,11 @@ __device__ __forceinline__ void w4_stream(const W4Dims& d, int ks, int rounds, s
   W4Unit<NB> cur, nxt = unit(0);
 #pragma unroll
   for (int j = 0; j < 2; ++j)
-    if (nxt.nm > 0 && part + j * ks < d.Kb) w4_load<CM, NB, LO, G32>(ring[j], nxt, d, part + j * ks, q, lo);
+    if (nxt.nm > 0 && part + j * ks < d.Kb) w4_load_codes<CM, NB, LO, G32>(ring[j], nxt, d, part + j * ks);
+  pdl_wait();
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (nxt.nm > 0 && part + j * ks < d.Kb) w4_load_rows<CM, NB, LO, G32>(ring[j], nxt, d, part + j * ks, q, lo);
   for (int r = 0; r < rounds; ++r) {
     cur = nxt;
     if (r + 1 < rounds) nxt = unit(r + 1);
@@ -251,21 +274,85 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_linear_kernel(const W4
 }
 
 struct W4FfnArgs {
-  FfnArgs f;      // f.pool: bytes of the 4-bit slot pool
+  FfnArgs f;              // f.pool: bytes of the 4-bit slot pool
   W4Slab sl;
-  uint16_t* h;    // bf16 [2][n][I]: h = h[0] + h[1]
-  size_t n;
+  uint16_t* h;            // bf16 [2][n][I]: h = h[0] + h[1]
+  int n;                  // routing slots
+  // Routed form: the groups come from the ids (row = flat routing slot), the combine follows in the down kernel.
+  const int32_t* ids;     // [n], or NULL: f.offset / f.rows / f.list_e / f.n_list (row = grouped position)
+  const float* w;         // [n]
+  uint16_t* out;          // bf16 [T][H]
+  int32_t* ready;         // [H / 64] row batches done per 64 output columns, or NULL: w4_sum_kernel follows
 };
 
-// A listed expert's batch of at most eight rows.
+// At most eight rows of one expert.
 constexpr int kW4Rows = 8;
 struct W4Batch {
-  int slot, p0, n;  // slot -1: no slot
+  int slot, n;            // slot -1: no slot
+  uint16_t row[kW4Rows];  // rows of h and y
 };
 
-// The listed experts' row batches, in shared memory: built by all threads, `most` entries at most.  Returns
-// their number.
-__device__ __forceinline__ int w4_batches(const FfnArgs& a, W4Batch* tab, int most, int* tmp) {
+// Dynamic shared memory of the expert kernels: the batches.
+static size_t w4_tab_bytes(int n) { return (size_t)n * sizeof(W4Batch); }
+
+// The row batches of the listed experts, or of the ids, by ascending expert, in shared memory: `tab` holds n
+// entries, `cnt` (2 kMaxE + n ints, free afterwards) is scratch.  Built by all threads; returns their number.
+// Every CTA builds the same batches, though the order of the rows inside one may vary: no row's result depends
+// on its neighbours.
+__device__ __forceinline__ int w4_batches(const W4FfnArgs& g, W4Batch* tab, int* cnt, int* tmp) {
+  const FfnArgs& a = g.f;
+  const int n = g.n;
+  if (g.ids) {
+    int *first = cnt + kMaxE, *ids = cnt + 2 * kMaxE;  // an expert's first batch; the ids
+    for (int e = threadIdx.x; e < a.E; e += kW4Threads) cnt[e] = 0;
+    __syncthreads();
+    constexpr int U = (kGemmRows + kW4Threads - 1) / kW4Threads;  // routing slots per thread
+    int id[U], rank[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = threadIdx.x + u * kW4Threads;
+      id[u] = i < n ? g.ids[i] : -1;
+      if (i < n && (id[u] < 0 || id[u] >= a.E)) {
+        set_status(a.status, MOE_DEV_BAD_EXPERT);
+        id[u] = -1;
+      }
+      if (i < n) ids[i] = id[u];
+      rank[u] = id[u] >= 0 ? atomicAdd(&cnt[id[u]], 1) : 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (id[u] >= 0 && cnt[id[u]] > kW4Rows) {  // several batches: the row's place is its place among the ids
+        rank[u] = 0;
+        for (int j = 0; j < (int)threadIdx.x + u * kW4Threads; ++j) rank[u] += ids[j] == id[u];
+      }
+    int base = 0;
+    for (int e0 = 0; e0 < a.E; e0 += kW4Threads) {
+      const int e = e0 + threadIdx.x, rows = e < a.E ? cnt[e] : 0, c = (rows + kW4Rows - 1) / kW4Rows;
+      int tot;
+      const int b = base + block_exclusive_scan(c, tmp, &tot);
+      if (c > 0) {
+        int slot = a.e2s ? a.e2s[e] : e;
+        if (slot < 0 || slot >= a.S) {
+          set_status(a.status, MOE_DEV_BAD_SLOT);
+          slot = -1;
+        }
+        first[e] = b;
+        for (int i = 0; i < c; ++i) {
+          tab[b + i].slot = slot;
+          tab[b + i].n = min(kW4Rows, rows - kW4Rows * i);
+        }
+      }
+      base += tot;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (id[u] >= 0)
+        tab[first[id[u]] + rank[u] / kW4Rows].row[rank[u] % kW4Rows] = (uint16_t)(threadIdx.x + u * kW4Threads);
+    __syncthreads();
+    return base;
+  }
   const int nl = min(*a.n_list, kMaxE);
   int base = 0;
   for (int l0 = 0; l0 < nl; l0 += kW4Threads) {
@@ -276,7 +363,7 @@ __device__ __forceinline__ int w4_batches(const FfnArgs& a, W4Batch* tab, int mo
       if (e >= 0 && e < a.E) {
         slot = a.list_s ? a.list_s[li] : a.e2s ? a.e2s[e] : e;
         p0 = a.offset[e];
-        rows = max(a.offset[e + 1] - p0, 0);
+        rows = min(max(a.offset[e + 1] - p0, 0), n);
         c = (rows + kW4Rows - 1) / kW4Rows;
         if (slot < 0 || slot >= a.S) {
           if (c > 0) set_status(a.status, MOE_DEV_BAD_SLOT);
@@ -286,26 +373,33 @@ __device__ __forceinline__ int w4_batches(const FfnArgs& a, W4Batch* tab, int mo
     }
     int tot;
     const int ex = base + block_exclusive_scan(c, tmp, &tot);
-    for (int i = 0; i < c && ex + i < most; ++i)
-      tab[ex + i] = W4Batch{slot, p0 + kW4Rows * i, min(kW4Rows, rows - kW4Rows * i)};
+    for (int i = 0; i < c && ex + i < n; ++i) {
+      W4Batch& b = tab[ex + i];
+      b.slot = slot;
+      b.n = min(kW4Rows, rows - kW4Rows * i);
+      for (int j = 0; j < b.n; ++j) b.row[j] = (uint16_t)(p0 + kW4Rows * i + j);
+    }
     base += tot;
   }
   __syncthreads();
-  if (base > most && threadIdx.x == 0) set_status(a.status, MOE_DEV_BAD_GROUPS);
-  return min(base, most);
+  if (base > n && threadIdx.x == 0) set_status(a.status, MOE_DEV_BAD_GROUPS);
+  return min(base, n);
 }
 
 // Gate and up: unit = (row batch, two tiles of gate with their neighbours of up); an expert's batches follow
 // each other, so that their weights come from memory once.
 constexpr int kGuTiles = 4;
 template <bool G32>
-__global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_gateup_kernel(const W4FfnArgs a, int most) {
+__global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_gateup_kernel(const W4FfnArgs a) {
   extern __shared__ W4Batch tab[];
   __shared__ float red[2 * kW4Warps * kGuTiles * 128];
   __shared__ int tmp[33];
+  pdl_trigger();  // the down kernel may start: it waits for this one before it reads h or the counters
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const W4Dims& d = a.sl.gu;
-  const int nbat = w4_batches(a.f, tab, most, tmp);
+  if (a.ready && blockIdx.x == 0)
+    for (int i = threadIdx.x; i < a.f.H / 64; i += kW4Threads) a.ready[i] = 0;
+  const int nbat = w4_batches(a, tab, reinterpret_cast<int*>(red), tmp);
   const int FT = (d.Mt + kGuTiles - 1) / kGuTiles, I = d.N / 2, units = nbat * FT;
   const int ks = w4_split(units, d.Kb, gridDim.x), sub = kW4Warps / ks;
   const int rounds = (units - (int)blockIdx.x * sub + (int)gridDim.x * sub - 1) / ((int)gridDim.x * sub);
@@ -317,18 +411,19 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_gateup_kernel(const W4
     u.nm = 0;
     const int i = index(r, warp / ks);
     if (i >= units) return u;
-    const W4Batch b = tab[i / FT];
+    const W4Batch& b = tab[i / FT];
     if (b.slot < 0) return u;
     const int tile = i % FT * kGuTiles;
     w4_at(u, slab(b.slot), d, tile, min(kGuTiles, d.Mt - tile), lane);
-    u.x[0] = a.f.x + (size_t)(a.f.rows[b.p0 + min(lane >> 2, b.n - 1)] / a.f.k) * a.f.H + 8 * (lane & 3);
+    const int row = b.row[min(lane >> 2, b.n - 1)];  // rows past the batch repeat its last one
+    u.x[0] = a.f.x + (size_t)((a.ids ? row : a.f.rows[row]) / a.f.k) * a.f.H + 8 * (lane & 3);
     return u;
   };
   w4_stream<kGuTiles, 1, false, G32>(d, ks, rounds, 0, red, unit, [&](int r, const float* buf) {
     for (int i = threadIdx.x; i < sub * 32 * kW4Rows; i += kW4Threads) {
       const int col = i & 31, row = (i >> 5) % kW4Rows, g = (i >> 5) / kW4Rows, u = index(r, g);
       if (u >= units) continue;
-      const W4Batch b = tab[u / FT];
+      const W4Batch& b = tab[u / FT];
       const int tile = u % FT * kGuTiles, m = 2 * (col >> 4), f = tile / 2 * 16 + col;
       if (b.slot < 0 || row >= b.n || tile + m >= d.Mt) continue;
       const float* mg = reinterpret_cast<const float*>(slab(b.slot) + d.mult) + (tile + m) * 16 + (col & 15);
@@ -337,27 +432,90 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_gateup_kernel(const W4
       const float h = gv / (1.f + __expf(-gv)) * uv;
       // h as the sum of two bf16: 16 significant bits reach the down product
       const uint16_t hi = f32_to_bf16(h);
-      const size_t o = (size_t)(b.p0 + row) * I + f;
+      const size_t o = (size_t)b.row[row] * I + f;
       a.h[o] = hi;
-      a.h[a.n * I + o] = isfinite(bf16_to_f32(hi)) ? f32_to_bf16(h - bf16_to_f32(hi)) : 0;
+      a.h[(size_t)a.n * I + o] = isfinite(bf16_to_f32(hi)) ? f32_to_bf16(h - bf16_to_f32(hi)) : 0;
     }
   });
 }
 
-// Down: unit = (row batch, four tiles of 16 output columns).
+// out[t] = bf16(sum_j w[t][j] y[t k + j]), fp32, j ascending, for the 64 columns of each of the `n` groups cg[].
+__device__ __forceinline__ void w4_combine_columns(const W4FfnArgs& a, const int* cg, int n) {
+  const int H = a.f.H, k = a.f.k;
+  for (int i = threadIdx.x; i < n * a.f.T * 16; i += kW4Threads) {
+    const int t = (i >> 4) % a.f.T, c = cg[(i >> 4) / a.f.T] * 64 + (i & 15) * 4;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < k; j0 += 4) {
+      float4 y[4];
+      float w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {  // four rows in flight
+        const int j = j0 + u, at = t * k + min(j, k - 1), e = a.ids[at];
+        const bool ok = j < k && e >= 0 && e < a.f.E;
+        w[u] = ok ? a.w[at] : 0.f;
+        y[u] = ok ? __ldcg(reinterpret_cast<const float4*>(a.f.y + (size_t)at * H + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        s.x = fmaf(w[u], y[u].x, s.x), s.y = fmaf(w[u], y[u].y, s.y);
+        s.z = fmaf(w[u], y[u].z, s.z), s.w = fmaf(w[u], y[u].w, s.w);
+      }
+    }
+    *reinterpret_cast<uint2*>(a.out + (size_t)t * H + c) =
+        make_uint2(uint32_t(f32_to_bf16(s.x)) | uint32_t(f32_to_bf16(s.y)) << 16,
+                   uint32_t(f32_to_bf16(s.z)) | uint32_t(f32_to_bf16(s.w)) << 16);
+  }
+}
+
+// The same for any number of rows, as a kernel of its own: grid (T, H / 512).
+__global__ void __launch_bounds__(128) w4_sum_kernel(const W4FfnArgs a) {
+  pdl_wait();
+  const int H = a.f.H, k = a.f.k, t = blockIdx.x, c = (blockIdx.y * 128 + threadIdx.x) * 4;
+  if (c >= H) return;
+  float4 y[kMaxK], s = make_float4(0.f, 0.f, 0.f, 0.f);
+  float w[kMaxK];
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j) {
+    y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    w[j] = 0.f;
+    const int at = t * k + j, e = j < k ? a.ids[at] : -1;
+    if (e >= 0 && e < a.f.E) {
+      w[j] = a.w[at];
+      y[j] = *reinterpret_cast<const float4*>(a.f.y + (size_t)at * H + c);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j) {
+    s.x = fmaf(w[j], y[j].x, s.x), s.y = fmaf(w[j], y[j].y, s.y);
+    s.z = fmaf(w[j], y[j].z, s.z), s.w = fmaf(w[j], y[j].w, s.w);
+  }
+  *reinterpret_cast<uint2*>(a.out + (size_t)t * H + c) =
+      make_uint2(uint32_t(f32_to_bf16(s.x)) | uint32_t(f32_to_bf16(s.y)) << 16,
+                 uint32_t(f32_to_bf16(s.z)) | uint32_t(f32_to_bf16(s.w)) << 16);
+}
+
+// Down: unit = (row batch, four tiles of 16 output columns).  In the routed form with few rows (a.ready) the
+// CTA that finishes the last batch of a column group adds the experts up: no further launch, and the sums'
+// order is fixed.
 constexpr int kDnTiles = 4;
 template <bool G32>
-__global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_down_kernel(const W4FfnArgs a, int most) {
+__global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_down_kernel(const W4FfnArgs a) {
   extern __shared__ W4Batch tab[];
   __shared__ float red[2 * kW4Warps * kDnTiles * 128];
   __shared__ int tmp[33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const W4Dims& d = a.sl.dn;
-  const int nbat = w4_batches(a.f, tab, most, tmp);
+  const int nbat = w4_batches(a, tab, reinterpret_cast<int*>(red), tmp);
   const int FT = (d.Mt + kDnTiles - 1) / kDnTiles, units = nbat * FT;
   const int ks = w4_split(units, d.Kb, gridDim.x), sub = kW4Warps / ks;
   const int rounds = (units - (int)blockIdx.x * sub + (int)gridDim.x * sub - 1) / ((int)gridDim.x * sub);
-  if (rounds <= 0) return;
+  if (rounds <= 0) {
+    pdl_wait();
+    if (a.ready && nbat == 0)  // no expert at all
+      for (int cg = blockIdx.x; cg < a.f.H / 64; cg += gridDim.x) w4_combine_columns(a, &cg, 1);
+    return;
+  }
+  int* s_mine = reinterpret_cast<int*>(red);  // after the rounds: per column group
   auto index = [&](int r, int g) { return (r * (int)gridDim.x + (int)blockIdx.x) * sub + g; };
   auto down = [&](int slot) {
     return reinterpret_cast<const uint8_t*>(a.f.pool) + (size_t)slot * a.sl.bytes + a.sl.dn_at;
@@ -367,19 +525,19 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_down_kernel(const W4Ff
     u.nm = 0;
     const int i = index(r, warp / ks);
     if (i >= units) return u;
-    const W4Batch b = tab[i / FT];
+    const W4Batch& b = tab[i / FT];
     if (b.slot < 0) return u;
     const int tile = i % FT * kDnTiles;
     w4_at(u, down(b.slot), d, tile, min(kDnTiles, d.Mt - tile), lane);
-    u.x[0] = a.h + (size_t)(b.p0 + min(lane >> 2, b.n - 1)) * d.K + 8 * (lane & 3);
+    u.x[0] = a.h + (size_t)b.row[min(lane >> 2, b.n - 1)] * d.K + 8 * (lane & 3);
     return u;
   };
-  w4_stream<kDnTiles, 1, true, G32>(d, ks, rounds, a.n * d.K, red, unit, [&](int r, const float* buf) {
+  w4_stream<kDnTiles, 1, true, G32>(d, ks, rounds, (size_t)a.n * d.K, red, unit, [&](int r, const float* buf) {
     for (int i = threadIdx.x; i < sub * 16 * kDnTiles * kW4Rows; i += kW4Threads) {
       const int col = i % (16 * kDnTiles), row = i / (16 * kDnTiles) % kW4Rows, g = i / (16 * kDnTiles * kW4Rows);
       const int u = index(r, g);
       if (u >= units) continue;
-      const W4Batch b = tab[u / FT];
+      const W4Batch& b = tab[u / FT];
       const int n = u % FT * (16 * kDnTiles) + col;
       if (row >= b.n || n >= d.N) continue;
       // an expert without a slot adds nothing: its rows are zero
@@ -387,9 +545,31 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_down_kernel(const W4Ff
       if (b.slot >= 0)
         v = w4_sum_part<kDnTiles, 1>(buf, g * ks, ks, col >> 4, row, col & 15) *
             reinterpret_cast<const float*>(down(b.slot) + d.mult)[n];
-      a.f.y[(size_t)(b.p0 + row) * d.N + n] = v;
+      a.f.y[(size_t)b.row[row] * d.N + n] = v;
     }
   });
+  if (!a.ready) return;
+  // count this CTA's units per column group; whoever brings a group's last one adds the experts up
+  __syncthreads();
+  for (int cg = threadIdx.x; cg < FT; cg += kW4Threads) s_mine[cg] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < rounds * sub; i += kW4Threads) {
+    const int u = index(i / sub, i % sub);
+    if (u < units) atomicAdd(&s_mine[u % FT], 1);
+  }
+  __syncthreads();
+  int* s_done = s_mine + FT;  // the groups that this CTA completed
+  if (threadIdx.x == 0) tmp[0] = 0;
+  __syncthreads();
+  for (int cg = threadIdx.x; cg < FT; cg += kW4Threads) {
+    const int mine = s_mine[cg];
+    if (mine == 0) continue;
+    __threadfence();
+    if (atomicAdd(&a.ready[cg], mine) + mine == nbat) s_done[atomicAdd(&tmp[0], 1)] = cg;
+  }
+  __syncthreads();
+  __threadfence();
+  w4_combine_columns(a, s_done, tmp[0]);
 }
 
 static int w4_sms(int* sms) {
@@ -399,14 +579,28 @@ static int w4_sms(int* sms) {
   return MOE_OK;
 }
 
-// Rows from which the tensor-core path takes over.
-constexpr int kGemmRows = 512;
-
 static bool w4_gemm_ffn(int n) { return n >= kGemmRows; }
 
 size_t w4_ws_bytes(int n, int H, int I) {
   const size_t h = ((size_t)n * I * 4 + 255) & ~size_t(255);
   return w4_gemm_ffn(n) ? std::max(h, w4_ffn_gemm_ws(n, H, I, false)) : h;
+}
+
+// The two weight streams; the second one's CTAs start as the first one's leave.
+static int launch_ffn_w4_stream(const W4FfnArgs& a, int group, int sms, cudaStream_t stream, Prof* prof) {
+  const size_t smem = w4_tab_bytes(a.n);
+  const dim3 grid(sms * kW4Ctas), block(kW4Threads);
+  if (prof) prof->begin(MOE_PROF_FFN_GATEUP, stream);
+  if (group == 32) w4_gateup_kernel<true><<<grid, block, smem, stream>>>(a);
+  else w4_gateup_kernel<false><<<grid, block, smem, stream>>>(a);
+  MOE_LAUNCH_CHECK();
+  if (prof) prof->end(stream);
+  if (prof) prof->begin(MOE_PROF_FFN_DOWN, stream);
+  MOE_CUDA_TRY(launch_pdl(group == 32 ? w4_down_kernel<true> : w4_down_kernel<false>, grid, block, smem, stream, a));
+  if (prof) prof->end(stream);
+  if (a.out && !a.ready)
+    MOE_CUDA_TRY(launch_pdl(w4_sum_kernel, dim3(a.f.T, (a.f.H + 511) / 512), dim3(128), 0, stream, a));
+  return MOE_OK;
 }
 
 // y rows of the listed experts; ws holds h (w4_ws_bytes).
@@ -419,20 +613,9 @@ int launch_ffn_w4(const FfnArgs& f, int group, void* ws, size_t ws_bytes, int ma
   int sms = 0;
   const int r = w4_sms(&sms);
   if (r != MOE_OK) return r;
-  const W4FfnArgs a{f, w4_slab(f.H, f.I, group), (uint16_t*)ws, (size_t)n};
-  const int most = std::min(n, std::min(max_list, n) + n / kW4Rows);  // one per expert and one per full batch
-  const size_t smem = most * sizeof(W4Batch);
-  if (prof) prof->begin(MOE_PROF_FFN_GATEUP, stream);
-  if (group == 32) w4_gateup_kernel<true><<<sms * kW4Ctas, kW4Threads, smem, stream>>>(a, most);
-  else w4_gateup_kernel<false><<<sms * kW4Ctas, kW4Threads, smem, stream>>>(a, most);
-  MOE_LAUNCH_CHECK();
-  if (prof) prof->end(stream);
-  if (prof) prof->begin(MOE_PROF_FFN_DOWN, stream);
-  if (group == 32) w4_down_kernel<true><<<sms * kW4Ctas, kW4Threads, smem, stream>>>(a, most);
-  else w4_down_kernel<false><<<sms * kW4Ctas, kW4Threads, smem, stream>>>(a, most);
-  MOE_LAUNCH_CHECK();
-  if (prof) prof->end(stream);
-  return MOE_OK;
+  W4FfnArgs a{};
+  a.f = f, a.sl = w4_slab(f.H, f.I, group), a.h = (uint16_t*)ws, a.n = n;
+  return launch_ffn_w4_stream(a, group, sms, stream, prof);
 }
 
 static size_t al256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -440,6 +623,7 @@ static size_t al256(size_t v) { return (v + 255) & ~size_t(255); }
 // Workspace of moe_experts_w4: the groups of the permute, then y and the FFN's own.
 struct W4ExpWs {
   int32_t *count, *offset, *rows, *pos, *act_e, *n_act, *perm;
+  int32_t* ready;
   float* y;
   void* ffn;
   size_t ffn_bytes, bytes;
@@ -461,6 +645,7 @@ static W4ExpWs w4_exp_ws(void* base, int T, int H, int I, int k, int E) {
   w.act_e = (int32_t*)take(4 * (size_t)E);
   w.n_act = (int32_t*)take(4);
   w.perm = (int32_t*)take(moe_permute_scratch_bytes(n, E) + 4);
+  w.ready = (int32_t*)take(4 * (size_t)(H / 64));
   const bool gemm = w4_gemm_ffn(n);  // its y is fp16 inside its own workspace
   w.y = gemm ? nullptr : (float*)take(4 * (size_t)n * H);
   w.ffn_bytes = gemm ? w4_ffn_gemm_ws(n, H, I, true) : w4_ws_bytes(n, H, I);
@@ -565,20 +750,25 @@ extern "C" int moe_experts_w4(const void* x, const int32_t* ids, const float* w,
   const W4ExpWs ws = w4_exp_ws(workspace, T, H, I, k, E);
   if (workspace_bytes < ws.bytes) return MOE_ERR_ALIGN;
   cudaStream_t s = (cudaStream_t)stream;
-  int r = launch_permute(ids, n, E, ws.count, ws.offset, ws.rows, ws.pos, ws.act_e, ws.n_act, dev_status, ws.perm, s);
-  if (r != MOE_OK) return r;
   FfnArgs f{};
   f.x = (const uint16_t*)x;
   f.T = T, f.H = H, f.I = I, f.k = k, f.E = E;
-  f.offset = ws.offset, f.rows = ws.rows, f.list_e = ws.act_e, f.n_list = ws.n_act;
   f.pool = (const uint16_t*)pool, f.e2s = e2s, f.S = S, f.pool_only = 1;
   f.y = ws.y, f.status = dev_status;
-  if (w4_gemm_ffn(n)) {
-    const uint16_t* yh = nullptr;
-    const int32_t* yexp = nullptr;
-    if ((r = launch_ffn_w4_gemm(f, group, ws.ffn, &yh, &yexp, s, nullptr)) != MOE_OK) return r;
-    return launch_w4_combine(yh, yexp, w, ws.pos, T, k, H, out, s);
+  if (!w4_gemm_ffn(n)) {
+    int sms = 0;
+    const int r = w4_sms(&sms);
+    if (r != MOE_OK) return r;
+    W4FfnArgs a{};
+    a.f = f, a.sl = w4_slab(H, I, group), a.h = (uint16_t*)ws.ffn, a.n = n;
+    a.ids = ids, a.w = w, a.out = (uint16_t*)out, a.ready = n <= kW4Fuse ? ws.ready : nullptr;
+    return launch_ffn_w4_stream(a, group, sms, s, nullptr);
   }
-  if ((r = launch_ffn_w4(f, group, ws.ffn, ws.ffn_bytes, std::min(n, E), s, nullptr)) != MOE_OK) return r;
-  return launch_combine(ws.y, w, ws.pos, ids, nullptr, T, k, H, E, 0, out, nullptr, nullptr, s);
+  int r = launch_permute(ids, n, E, ws.count, ws.offset, ws.rows, ws.pos, ws.act_e, ws.n_act, dev_status, ws.perm, s);
+  if (r != MOE_OK) return r;
+  f.offset = ws.offset, f.rows = ws.rows, f.list_e = ws.act_e, f.n_list = ws.n_act;
+  const uint16_t* yh = nullptr;
+  const int32_t* yexp = nullptr;
+  if ((r = launch_ffn_w4_gemm(f, group, ws.ffn, &yh, &yexp, s, nullptr)) != MOE_OK) return r;
+  return launch_w4_combine(yh, yexp, w, ws.pos, T, k, H, out, s);
 }
