@@ -36,7 +36,7 @@ constexpr int kGemmRows = 512;  // routing slots from which the experts' tensor-
 template <int CM, int NB, bool LO, bool G32>
 struct W4Block {
   uint4 w[CM];
-  uint32_t s[CM][G32 ? 2 : 1];
+  uint32_t s[G32 ? 2 : 1][CM];
   uint4 x[NB][LO ? 2 : 1][2];
 };
 
@@ -52,29 +52,52 @@ struct W4Unit {
 template <int NB>
 __device__ __forceinline__ void w4_at(W4Unit<NB>& u, const uint8_t* m, const W4Dims& d, int tile, int nm, int lane) {
   u.codes = m + w4_code_at(d, tile, 0) * 512 + 16 * w4_chunk(lane >> 2, lane & 3);
-  u.scales = m + d.scales + w4_scale_at(d, tile, 0) * 32 + 4 * (lane >> 2);
+  u.scales = m + d.scales + w4_scale_at(d, tile, 0, lane >> 2) * 4;
   u.mates = w4_mates(d, tile);
   u.nm = nm;
 }
 
-template <int CM, int NB, bool LO, bool G32>
+// FULL: every unit has its CM tiles and they start on a multiple of CM, so that a lane's scales are one load.
+template <int CM, int NB, bool LO, bool G32, bool FULL>
 __device__ __forceinline__ void w4_load_codes(W4Block<CM, NB, LO, G32>& b, const W4Unit<NB>& u, const W4Dims& d, int kb) {
   const uint8_t* c = u.codes + (size_t)(uint32_t)(kb * u.mates) * 512;
   const int kg = G32 ? 2 * kb : d.G == 128 ? kb >> 1 : kb;
   const uint8_t* s = u.scales + (uint32_t)(kg * u.mates) * 32u;
 #pragma unroll
   for (int m = 0; m < CM; ++m)
-    if (m == 0 || m < u.nm) {
-      b.w[m] = ldg_stream(c + m * 512);
-      b.s[m][0] = __ldg(reinterpret_cast<const uint32_t*>(s + m * 32));
-      if (G32) b.s[m][G32 ? 1 : 0] = __ldg(reinterpret_cast<const uint32_t*>(s + (u.mates + m) * 32));
+    if (FULL || m == 0 || m < u.nm) b.w[m] = ldg_stream(c + m * 512);
+#pragma unroll
+  for (int p = 0; p < (G32 ? 2 : 1); ++p) {
+    const uint32_t* sp = reinterpret_cast<const uint32_t*>(s + p * u.mates * 32);
+    if constexpr (FULL && CM == 4) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(sp));
+      b.s[p][0] = v.x, b.s[p][1] = v.y, b.s[p][2] = v.z, b.s[p][3] = v.w;
+    } else if constexpr (FULL && CM == 2) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(sp));
+      b.s[p][0] = v.x, b.s[p][1] = v.y;
+    } else {
+#pragma unroll
+      for (int m = 0; m < CM; ++m)
+        if (m == 0 || m < u.nm) b.s[p][m] = __ldg(sp + m);
     }
+  }
 }
 
 // Rows written by the kernel before (LO) are read by plain loads after the wait, x through the read-only path.
 template <int CM, int NB, bool LO, bool G32>
 __device__ __forceinline__ void w4_load_rows(W4Block<CM, NB, LO, G32>& b, const W4Unit<NB>& u, const W4Dims& d, int kb, int q,
                                              size_t lo) {
+  if (kb * 64 + 64 <= d.K) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int p = 0; p < (LO ? 2 : 1); ++p) {
+        const uint4* at = reinterpret_cast<const uint4*>(u.x[nb] + p * lo + kb * 64);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) b.x[nb][p][h] = LO ? at[4 * h] : __ldg(at + 4 * h);
+      }
+    return;
+  }
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -88,14 +111,14 @@ __device__ __forceinline__ void w4_load_rows(W4Block<CM, NB, LO, G32>& b, const 
     }
 }
 
-template <int CM, int NB, bool LO, bool G32>
+template <int CM, int NB, bool LO, bool G32, bool FULL>
 __device__ __forceinline__ void w4_load(W4Block<CM, NB, LO, G32>& b, const W4Unit<NB>& u, const W4Dims& d, int kb, int q,
                                         size_t lo) {
-  w4_load_codes<CM, NB, LO, G32>(b, u, d, kb);
+  w4_load_codes<CM, NB, LO, G32, FULL>(b, u, d, kb);
   w4_load_rows<CM, NB, LO, G32>(b, u, d, kb, q, lo);
 }
 
-template <int CM, int NB, bool LO, bool G32>
+template <int CM, int NB, bool LO, bool G32, bool FULL>
 __device__ __forceinline__ void w4_block(const W4Block<CM, NB, LO, G32>& b, int nm, float (&acc)[CM][NB][4]) {
   constexpr int P = LO ? 2 : 1;
   const uint32_t one = 0x3f803f80u;
@@ -120,7 +143,7 @@ __device__ __forceinline__ void w4_block(const W4Block<CM, NB, LO, G32>& b, int 
     }
 #pragma unroll
     for (int m = 0; m < CM; ++m) {
-      if (m > 0 && m >= nm) break;
+      if (!FULL && m > 0 && m >= nm) break;
       float c[NB][4];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -139,7 +162,7 @@ __device__ __forceinline__ void w4_block(const W4Block<CM, NB, LO, G32>& b, int 
             mma_bf16_16816(c[nb], a1, v.z, v.w, c[nb][0], c[nb][1], c[nb][2], c[nb][3]);
           }
       }
-      const uint32_t sw = b.s[m][part];
+      const uint32_t sw = b.s[part][m];
       const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&sw));
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
@@ -190,7 +213,7 @@ __host__ __device__ inline int w4_split(int units, int Kb, int ctas) {
 // The stream of one CTA: rounds 0 .. rounds - 1 of units; unit(round) gives this warp's unit (of its subgroup)
 // and done(round, red) is called by all threads once the subgroups' parts of a round are in red.  The first
 // blocks' codes are loaded before a programmatic dependent's wait, the rows after it.
-template <int CM, int NB, bool LO, bool G32, class Unit, class Done>
+template <int CM, int NB, bool LO, bool G32, bool FULL, class Unit, class Done>
 __device__ __forceinline__ void w4_stream(const W4Dims& d, int ks, int rounds, size_t lo, float* red, Unit&& unit,
                                           Done&& done) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, part = warp % ks;
@@ -199,7 +222,7 @@ __device__ __forceinline__ void w4_stream(const W4Dims& d, int ks, int rounds, s
   W4Unit<NB> cur, nxt = unit(0);
 #pragma unroll
   for (int j = 0; j < 2; ++j)
-    if (nxt.nm > 0 && part + j * ks < d.Kb) w4_load_codes<CM, NB, LO, G32>(ring[j], nxt, d, part + j * ks);
+    if (nxt.nm > 0 && part + j * ks < d.Kb) w4_load_codes<CM, NB, LO, G32, FULL>(ring[j], nxt, d, part + j * ks);
   pdl_wait();
 #pragma unroll
   for (int j = 0; j < 2; ++j)
@@ -213,14 +236,14 @@ __device__ __forceinline__ void w4_stream(const W4Dims& d, int ks, int rounds, s
     for (int s = 0; s + 1 < steps; ++s, kb += 2 * ks)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        if (cur.nm > 0) w4_block<CM, NB, LO, G32>(ring[j], cur.nm, acc);  // all but a share's last two blocks exist
+        if (cur.nm > 0) w4_block<CM, NB, LO, G32, FULL>(ring[j], cur.nm, acc);  // all but a share's last two blocks exist
         const int kn = kb + (2 + j) * ks;
-        if (cur.nm > 0 && kn < d.Kb) w4_load<CM, NB, LO, G32>(ring[j], cur, d, kn, q, lo);
+        if (cur.nm > 0 && kn < d.Kb) w4_load<CM, NB, LO, G32, FULL>(ring[j], cur, d, kn, q, lo);
       }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {  // the slots' next blocks are the next unit's
-      if (cur.nm > 0 && kb + j * ks < d.Kb) w4_block<CM, NB, LO, G32>(ring[j], cur.nm, acc);
-      if (nxt.nm > 0 && part + j * ks < d.Kb) w4_load<CM, NB, LO, G32>(ring[j], nxt, d, part + j * ks, q, lo);
+      if (cur.nm > 0 && kb + j * ks < d.Kb) w4_block<CM, NB, LO, G32, FULL>(ring[j], cur.nm, acc);
+      if (nxt.nm > 0 && part + j * ks < d.Kb) w4_load<CM, NB, LO, G32, FULL>(ring[j], nxt, d, part + j * ks, q, lo);
     }
     float* buf = red + (r & 1) * (kW4Warps * CM * NB * 128);  // two buffers: one barrier per round
     w4_put_part<CM, NB>(buf, warp, lane, acc);
@@ -240,7 +263,7 @@ struct W4LinArgs {
 };
 
 // grid (CTAs, ceil(T / (8 NB))).
-template <int CM, int NB, bool G32>
+template <int CM, int NB, bool G32, bool FULL>
 __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_linear_kernel(const W4LinArgs a) {
   __shared__ float red[2 * kW4Warps * CM * NB * 128];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -260,7 +283,7 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_linear_kernel(const W4
     return u;
   };
   if (rounds <= 0) return;
-  w4_stream<CM, NB, false, G32>(a.d, ks, rounds, 0, red, unit, [&](int r, const float* buf) {
+  w4_stream<CM, NB, false, G32, FULL>(a.d, ks, rounds, 0, red, unit, [&](int r, const float* buf) {
     for (int i = threadIdx.x; i < sub * CM * 16 * nt; i += kW4Threads) {
       const int col = i % (CM * 16), row = i / (CM * 16) % nt, g = i / (CM * 16 * nt);
       const int n = first(r, g) * 16 + col;
@@ -388,7 +411,7 @@ __device__ __forceinline__ int w4_batches(const W4FfnArgs& g, W4Batch* tab, int*
 
 // Gate and up: unit = (row batch, two tiles of gate with their neighbours of up); an expert's batches follow
 // each other, so that their weights come from memory once.
-constexpr int kGuTiles = 4;
+constexpr int kGuTiles = 4;  // (I % 32 == 0 and H % 64 == 0: both matrices have whole units)
 template <bool G32>
 __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_gateup_kernel(const W4FfnArgs a) {
   extern __shared__ W4Batch tab[];
@@ -419,7 +442,7 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_gateup_kernel(const W4
     u.x[0] = a.f.x + (size_t)((a.ids ? row : a.f.rows[row]) / a.f.k) * a.f.H + 8 * (lane & 3);
     return u;
   };
-  w4_stream<kGuTiles, 1, false, G32>(d, ks, rounds, 0, red, unit, [&](int r, const float* buf) {
+  w4_stream<kGuTiles, 1, false, G32, true>(d, ks, rounds, 0, red, unit, [&](int r, const float* buf) {
     for (int i = threadIdx.x; i < sub * 32 * kW4Rows; i += kW4Threads) {
       const int col = i & 31, row = (i >> 5) % kW4Rows, g = (i >> 5) / kW4Rows, u = index(r, g);
       if (u >= units) continue;
@@ -532,7 +555,7 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_down_kernel(const W4Ff
     u.x[0] = a.h + (size_t)b.row[min(lane >> 2, b.n - 1)] * d.K + 8 * (lane & 3);
     return u;
   };
-  w4_stream<kDnTiles, 1, true, G32>(d, ks, rounds, (size_t)a.n * d.K, red, unit, [&](int r, const float* buf) {
+  w4_stream<kDnTiles, 1, true, G32, true>(d, ks, rounds, (size_t)a.n * d.K, red, unit, [&](int r, const float* buf) {
     for (int i = threadIdx.x; i < sub * 16 * kDnTiles * kW4Rows; i += kW4Threads) {
       const int col = i % (16 * kDnTiles), row = i / (16 * kDnTiles) % kW4Rows, g = i / (16 * kDnTiles * kW4Rows);
       const int u = index(r, g);
@@ -699,11 +722,15 @@ extern "C" int moe_w4_linear(const void* x, long long ldx, int T, int K, int N, 
     b.T = std::min(T - t0, 65535 * rows);
     const dim3 grid(gx, (b.T + rows - 1) / rows);
     auto go = [&](auto kernel, auto kernel32) { (g32 ? kernel32 : kernel)<<<grid, kW4Threads, 0, (cudaStream_t)stream>>>(b); };
-    if (rows == 32) go(w4_linear_kernel<1, 4, false>, w4_linear_kernel<1, 4, true>);
-    else if (rows == 16) go(w4_linear_kernel<2, 2, false>, w4_linear_kernel<2, 2, true>);
-    else if (cm == 4) go(w4_linear_kernel<4, 1, false>, w4_linear_kernel<4, 1, true>);
-    else if (cm == 2) go(w4_linear_kernel<2, 1, false>, w4_linear_kernel<2, 1, true>);
-    else go(w4_linear_kernel<1, 1, false>, w4_linear_kernel<1, 1, true>);
+    const bool full = a.d.Mt % cm == 0;
+    if (rows == 32) go(w4_linear_kernel<1, 4, false, true>, w4_linear_kernel<1, 4, true, true>);
+    else if (rows == 16 && full) go(w4_linear_kernel<2, 2, false, true>, w4_linear_kernel<2, 2, true, true>);
+    else if (rows == 16) go(w4_linear_kernel<2, 2, false, false>, w4_linear_kernel<2, 2, true, false>);
+    else if (cm == 4 && full) go(w4_linear_kernel<4, 1, false, true>, w4_linear_kernel<4, 1, true, true>);
+    else if (cm == 4) go(w4_linear_kernel<4, 1, false, false>, w4_linear_kernel<4, 1, true, false>);
+    else if (cm == 2 && full) go(w4_linear_kernel<2, 1, false, true>, w4_linear_kernel<2, 1, true, true>);
+    else if (cm == 2) go(w4_linear_kernel<2, 1, false, false>, w4_linear_kernel<2, 1, true, false>);
+    else go(w4_linear_kernel<1, 1, false, true>, w4_linear_kernel<1, 1, true, true>);
     MOE_LAUNCH_CHECK();
   }
   return MOE_OK;

@@ -19,8 +19,9 @@
 //   a bf16 mantissa (0x4180 | code << 3 is 16 + code), one in bits 6-9 the top of an fp16 mantissa
 //   (0x4c00 | code << 6 is 16 + code): there (code - 8) * scale is one fused multiply-add with -24 * scale,
 //   exact for a scale of 8 significant bits.
-//   scales  [Mt / 8][Kg][8][8 words] Kg groups, neighbours as for the codes; word g = (column g, column
-//                            g + 8) of the tile as two fp16, divided by the column's multiplier
+//   scales  [Mt / 8][Kg][8 words][8] Kg groups, neighbours as for the codes (word g of all eight tiles, then
+//                            word g + 1); word g = (column g, column g + 8) of the tile as two fp16, divided
+//                            by the column's multiplier
 //   mult    [Mt * 16] fp32   power of two per column: 2^floor(log2(max |scale|)), 1 where that is 0 or
 //                            not finite.  fp16 scales below 2 then keep every bit of a bf16 scale down
 //                            to 2^-14 of the column's largest one, and (code - 8) * scale has at most 11
@@ -57,7 +58,8 @@ __host__ __device__ inline W4Dims w4_dims(int K, int N, int G) {
   return d;
 }
 
-// Tiles that lie together with tile mt, and the place of its block kb (512 B units) and group kg (32 B units).
+// Tiles that lie together with tile mt, and the place of its block kb (512 B units) and of word g of its group
+// kg (4 B units).
 __host__ __device__ __forceinline__ int w4_mates(const W4Dims& d, int mt) {
   const int left = d.Mt - (mt & ~7);
   return left < 8 ? left : 8;
@@ -65,8 +67,8 @@ __host__ __device__ __forceinline__ int w4_mates(const W4Dims& d, int mt) {
 __host__ __device__ __forceinline__ size_t w4_code_at(const W4Dims& d, int mt, int kb) {
   return (size_t)(mt & ~7) * d.Kb + (size_t)kb * w4_mates(d, mt) + (mt & 7);
 }
-__host__ __device__ __forceinline__ size_t w4_scale_at(const W4Dims& d, int mt, int kg) {
-  return (size_t)(mt & ~7) * d.Kg + (size_t)kg * w4_mates(d, mt) + (mt & 7);
+__host__ __device__ __forceinline__ size_t w4_scale_at(const W4Dims& d, int mt, int kg, int g) {
+  return ((size_t)(mt & ~7) * d.Kg + (size_t)kg * w4_mates(d, mt)) * 8 + g * w4_mates(d, mt) + (mt & 7);
 }
 
 inline bool w4_group_ok(int G) { return G == 32 || G == 64 || G == 128; }

@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
           if (nm > 0) {
             mbar_expect_tx(&wfull[s], nm * (512 * nb + 32 * ng));
             bulk_load(dst, ti.base + w4_code_at(d, 8 * blk, kb) * 512, nm * 512 * nb, &wfull[s]);
-            bulk_load(dst + kGCodeBytes, ti.base + d.scales + w4_scale_at(d, 8 * blk, kb * kGK / d.G) * 32, nm * 32 * ng,
+            bulk_load(dst + kGCodeBytes, ti.base + d.scales + w4_scale_at(d, 8 * blk, kb * kGK / d.G, 0) * 4, nm * 32 * ng,
                       &wfull[s]);
           } else {
             mbar_arrive(&wfull[s]);  // the pair's second CTA has no columns here: its results are dropped
@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
             const int j4 = kb % kGChunk + h;
             const unsigned char* code = wst + (j4 * nm + (r >> 4)) * 512 + g * 64 + hi * 8;
             const int gi = d.G == 128 ? j4 >> 1 : d.G == 64 ? j4 : 2 * j4;
-            const __half* sp = reinterpret_cast<const __half*>(wst + kGCodeBytes + (gi * nm + (r >> 4)) * 32 + g * 4) + hi;
+            const __half* sp = reinterpret_cast<const __half*>(wst + kGCodeBytes + (gi * nm * 8 + g * nm + (r >> 4)) * 4) + hi;
             uint2 w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint2*>(code + ((j + (g >> 1)) & 3) * 16);

@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const W4PackArgs a) {
     for (int i = threadIdx.x; i < gpc * kPackCols; i += 256) {
       const int g = k0 / d.G + i / kPackCols, n = n0 + i % kPackCols;
       if (g < d.Kg && n < d.Mt * 16)
-        dsc[w4_scale_at(d, n >> 4, g) * 16 + (n & 7) * 2 + ((n >> 3) & 1)] =
+        dsc[w4_scale_at(d, n >> 4, g, n & 7) * 2 + ((n >> 3) & 1)] =
             g < src_groups(d) && n < d.N ? ss[src_col(m, n, src_groups(d)) + (size_t)g * ld] : 0;
     }
   } else {
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const W4PackArgs a) {
         }
         sc[k - k0][c] = (uint8_t)code;
       }
-      if (n < d.Mt * 16) dsc[w4_scale_at(d, n >> 4, g) * 16 + (n & 7) * 2 + ((n >> 3) & 1)] = sb;
+      if (n < d.Mt * 16) dsc[w4_scale_at(d, n >> 4, g, n & 7) * 2 + ((n >> 3) & 1)] = sb;
     }
   }
   __syncthreads();
@@ -119,16 +119,16 @@ __global__ void __launch_bounds__(128) w4_scale_kernel(const W4PackArgs a) {
   if (n >= d.Mt * 16) return;
   uint8_t* dst = a.dst + item * a.dst_item + m.dst;
   const int tile = n >> 4, g = n & 7, h = (n >> 3) & 1;
-  uint16_t* sc = reinterpret_cast<uint16_t*>(dst + d.scales) + g * 2 + h;
+  uint16_t* sc = reinterpret_cast<uint16_t*>(dst + d.scales) + h;
   float amax = 0.f;
-  for (int i = 0; i < d.Kg; ++i) amax = fmaxf(amax, fabsf(bf16_to_f32(sc[w4_scale_at(d, tile, i) * 16])));
+  for (int i = 0; i < d.Kg; ++i) amax = fmaxf(amax, fabsf(bf16_to_f32(sc[w4_scale_at(d, tile, i, g) * 2])));
   const int e = amax > 0.f && amax < INFINITY ? ilogbf(amax) : 0;
   // 2^-e as two factors, so that a subnormal largest scale does not overflow it
   const float f0 = ldexpf(1.f, -e / 2), f1 = ldexpf(1.f, -(e - e / 2));
   const uint32_t* words = reinterpret_cast<const uint32_t*>(dst);
   float norm = 0.f;
   for (int i = 0; i < d.Kg; ++i) {
-    const size_t at = w4_scale_at(d, tile, i) * 16;
+    const size_t at = w4_scale_at(d, tile, i, g) * 2;
     const float raw = bf16_to_f32(sc[at]);
     int sq = 0;  // sum of (code - 8)^2 of the group: at most 128 * 64
     for (int b = i * d.G / 32; b < (i + 1) * d.G / 32 && b < d.Kb * 2; ++b)  // blocks of 32 inputs
