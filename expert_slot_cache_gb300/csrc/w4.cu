@@ -11,14 +11,16 @@
 // stream is bound by its instructions: 64 codes of 16 columns are 512 bytes, 21 cycles of an SM's share of
 // the memory bandwidth.)
 //
-// A warp streams CM neighbouring tiles of 16 columns (CM x 512 bytes a block of 64 inputs, one 16-byte load
-// per lane and tile), every ks-th block of the inputs, two blocks ahead and on across the end of a unit, so
-// that its loads never pause; the activations of a block travel with its codes.  The ks warps that share a
-// unit add up in shared memory, in warp order.  ks is the split that costs least for the unit count at hand
-// (w4_split): few long shares while there are units for every warp, short ones for a few small matrices.
+// A warp streams CM neighbouring tiles of 16 columns (CM x 512 bytes a block of 64 inputs), every ks-th block
+// of the inputs, through a ring of its own in shared memory: its first lane issues the bulk copies, kW4Stages
+// blocks ahead and on across the end of a unit, so that the copies never pause and cost no registers.  The ks
+// warps that share a unit add up in shared memory, in warp order.  ks is the split that costs least for the
+// unit count at hand (w4_split): few long shares while there are units for every warp, short ones for a few
+// small matrices.
 #include <algorithm>
 
 #include "internal.cuh"
+#include "tma.cuh"
 #include "w4.cuh"
 
 namespace moe {
@@ -31,102 +33,76 @@ constexpr int kW4Ctas = 2;   // resident CTAs per SM that the registers allow
 constexpr int kW4Fuse = 16;
 constexpr int kGemmRows = 512;  // routing slots from which the experts' tensor-core path takes over
 
-// One block of 64 inputs in registers: a lane's codes of CM tiles, their columns' scales, and the lane's inputs
-// of NB groups of eight rows (LO: as the sum of two bf16).
-template <int CM, int NB, bool LO, bool G32>
-struct W4Block {
-  uint4 w[CM];
-  uint32_t s[G32 ? 2 : 1][CM];
-  uint4 x[NB][LO ? 2 : 1][2];
-};
+constexpr int kW4Stages = 4; // blocks of a warp's ring
 
-// What a warp streams of one unit: its tiles' codes and scales, and the rows they meet.
+// What a warp streams of one unit.
 template <int NB>
 struct W4Unit {
-  const uint8_t* codes;   // the lane's chunk in block 0 of the first tile
-  const uint8_t* scales;  // the lane's columns in group 0
-  int mates;              // tiles that lie between one block and the next
-  int nm;                 // tiles that exist (0: nothing to do)
-  const uint16_t* x[NB];  // the lane's row of each group, at input 8 (lane & 3)
+  const uint8_t* m;       // the matrix
+  int tile, nm;           // first tile of 16 columns, tiles that exist (0: nothing to do)
+  const uint16_t* x[NB];  // the lane's row of each group of eight, at input 8 (lane & 3)
 };
-template <int NB>
-__device__ __forceinline__ void w4_at(W4Unit<NB>& u, const uint8_t* m, const W4Dims& d, int tile, int nm, int lane) {
-  u.codes = m + w4_code_at(d, tile, 0) * 512 + 16 * w4_chunk(lane >> 2, lane & 3);
-  u.scales = m + d.scales + w4_scale_at(d, tile, 0, lane >> 2) * 4;
-  u.mates = w4_mates(d, tile);
-  u.nm = nm;
-}
 
-// FULL: every unit has its CM tiles and they start on a multiple of CM, so that a lane's scales are one load.
-template <int CM, int NB, bool LO, bool G32, bool FULL>
-__device__ __forceinline__ void w4_load_codes(W4Block<CM, NB, LO, G32>& b, const W4Unit<NB>& u, const W4Dims& d, int kb) {
-  const uint8_t* c = u.codes + (size_t)(uint32_t)(kb * u.mates) * 512;
-  const int kg = G32 ? 2 * kb : d.G == 128 ? kb >> 1 : kb;
-  const uint8_t* s = u.scales + (uint32_t)(kg * u.mates) * 32u;
-#pragma unroll
-  for (int m = 0; m < CM; ++m)
-    if (FULL || m == 0 || m < u.nm) b.w[m] = ldg_stream(c + m * 512);
-#pragma unroll
-  for (int p = 0; p < (G32 ? 2 : 1); ++p) {
-    const uint32_t* sp = reinterpret_cast<const uint32_t*>(s + p * u.mates * 32);
-    if constexpr (FULL && CM == 4) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(sp));
-      b.s[p][0] = v.x, b.s[p][1] = v.y, b.s[p][2] = v.z, b.s[p][3] = v.w;
-    } else if constexpr (FULL && CM == 2) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(sp));
-      b.s[p][0] = v.x, b.s[p][1] = v.y;
-    } else {
-#pragma unroll
-      for (int m = 0; m < CM; ++m)
-        if (m == 0 || m < u.nm) b.s[p][m] = __ldg(sp + m);
-    }
+// A warp's ring.  A stage holds a block's codes of CM tiles and the scales of all tiles that lie with them.
+template <int CM, bool G32>
+struct W4Ring {
+  static constexpr int kScales = G32 ? 512 : 256, kStage = CM * 512 + kScales;
+  static constexpr int kBytes = kW4Warps * (kW4Stages * kStage + 8 * kW4Stages);  // of a CTA
+  unsigned char* st;
+  uint64_t* bar;
+  __device__ __forceinline__ void init(unsigned char* smem, int warp, int lane) {
+    st = smem + warp * kW4Stages * kStage;
+    bar = reinterpret_cast<uint64_t*>(smem + kW4Warps * kW4Stages * kStage) + warp * kW4Stages;
+    if (lane < kW4Stages) mbar_init(&bar[lane], 1);
+    mbar_fence_init();
+    __syncwarp();
   }
-}
+};
 
-// Rows written by the kernel before (LO) are read by plain loads after the wait, x through the read-only path.
-template <int CM, int NB, bool LO, bool G32>
-__device__ __forceinline__ void w4_load_rows(W4Block<CM, NB, LO, G32>& b, const W4Unit<NB>& u, const W4Dims& d, int kb, int q,
-                                             size_t lo) {
-  if (kb * 64 + 64 <= d.K) {
+// The inputs of one block: a lane's eight per half, of NB groups of eight rows (LO: as the sum of two bf16).
+template <int NB, bool LO>
+struct W4Rows {
+  uint4 x[NB][LO ? 2 : 1][2];
+  // Rows written by the kernel before (LO) are read by plain loads, x through the read-only path.
+  __device__ __forceinline__ void load(const uint16_t* const (&xr)[NB], int K, int kb, int q, size_t lo) {
+    if (kb * 64 + 64 <= K) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int p = 0; p < (LO ? 2 : 1); ++p) {
+          const uint4* at = reinterpret_cast<const uint4*>(xr[nb] + p * lo + kb * 64);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) x[nb][p][h] = LO ? at[4 * h] : __ldg(at + 4 * h);
+        }
+      return;
+    }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int p = 0; p < (LO ? 2 : 1); ++p) {
-        const uint4* at = reinterpret_cast<const uint4*>(u.x[nb] + p * lo + kb * 64);
+      for (int p = 0; p < (LO ? 2 : 1); ++p)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) b.x[nb][p][h] = LO ? at[4 * h] : __ldg(at + 4 * h);
-      }
-    return;
+        for (int h = 0; h < 2; ++h) {  // K % 8 == 0: a lane's eight inputs are inside or outside together
+          const uint4* at = reinterpret_cast<const uint4*>(xr[nb] + p * lo + kb * 64 + 32 * h);
+          x[nb][p][h] = kb * 64 + 32 * h + 8 * q < K ? (LO ? *at : __ldg(at)) : make_uint4(0, 0, 0, 0);
+        }
   }
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-    for (int p = 0; p < (LO ? 2 : 1); ++p) {
-      const uint16_t* x = u.x[nb] + p * lo + kb * 64;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {  // K % 8 == 0: a lane's eight inputs are inside or outside together
-        const uint4* at = reinterpret_cast<const uint4*>(x + 32 * h);
-        b.x[nb][p][h] = kb * 64 + 32 * h + 8 * q < d.K ? (LO ? *at : __ldg(at)) : make_uint4(0, 0, 0, 0);
-      }
-    }
-}
+};
 
-template <int CM, int NB, bool LO, bool G32, bool FULL>
-__device__ __forceinline__ void w4_load(W4Block<CM, NB, LO, G32>& b, const W4Unit<NB>& u, const W4Dims& d, int kb, int q,
-                                        size_t lo) {
-  w4_load_codes<CM, NB, LO, G32, FULL>(b, u, d, kb);
-  w4_load_rows<CM, NB, LO, G32>(b, u, d, kb, q, lo);
-}
-
-template <int CM, int NB, bool LO, bool G32, bool FULL>
-__device__ __forceinline__ void w4_block(const W4Block<CM, NB, LO, G32>& b, int nm, float (&acc)[CM][NB][4]) {
+// acc += the block in stage `st` times the rows.  All CM tiles are computed; what the stage holds of tiles that
+// do not exist is dropped with their sums.
+template <int CM, int NB, bool LO, bool G32>
+__device__ __forceinline__ void w4_block(const unsigned char* st, int tile, int mates, int lane, const W4Rows<NB, LO>& b,
+                                         float (&acc)[CM][NB][4]) {
   constexpr int P = LO ? 2 : 1;
   const uint32_t one = 0x3f803f80u;
   const uint32_t ones[4] = {one, one, one, one};
+  const int g = lane >> 2;
+  const uint4* codes = reinterpret_cast<const uint4*>(st) + w4_chunk(g, lane & 3);
+  const uint32_t* sc = reinterpret_cast<const uint32_t*>(st + CM * 512);
 #pragma unroll
   for (int part = 0; part < (G32 ? 2 : 1); ++part) {
     constexpr int H = G32 ? 1 : 2;  // halves of the block per scale
-    float off[NB][2];               // -24 sum of the rows' inputs
+    float off[NB][4];               // -24 sum of the rows' inputs, as an accumulator fragment
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       float d[4] = {0.f, 0.f, 0.f, 0.f};
@@ -138,32 +114,36 @@ __device__ __forceinline__ void w4_block(const W4Block<CM, NB, LO, G32>& b, int 
           mma_bf16_16816(d, ones, v.x, v.y, d[0], d[1], d[2], d[3]);
           mma_bf16_16816(d, ones, v.z, v.w, d[0], d[1], d[2], d[3]);
         }
-      off[nb][0] = -24.f * d[0];
-      off[nb][1] = -24.f * d[1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) off[nb][i] = -24.f * d[i];
+    }
+    uint32_t sw[CM];
+    if (CM == 4 && mates == 8) {
+      const uint4 v = *reinterpret_cast<const uint4*>(sc + part * 64 + g * 8 + (tile & 7));
+      sw[0] = v.x, sw[CM > 1 ? 1 : 0] = v.y, sw[CM > 2 ? 2 : 0] = v.z, sw[CM > 3 ? 3 : 0] = v.w;
+    } else {
+#pragma unroll
+      for (int m = 0; m < CM; ++m) sw[m] = sc[(part * 8 + g) * mates + min((tile & 7) + m, mates - 1)];
     }
 #pragma unroll
     for (int m = 0; m < CM; ++m) {
-      if (!FULL && m > 0 && m >= nm) break;
+      const uint4 w = codes[m * 32];
       float c[NB][4];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[nb][i] = off[nb][i & 1];
 #pragma unroll
       for (int h = 0; h < H; ++h) {
         uint32_t a0[4], a1[4];
-        w4_frag_bf16(part + h ? b.w[m].y : b.w[m].x, part + h ? b.w[m].w : b.w[m].z, a0, a1);
+        w4_frag_bf16(part + h ? w.y : w.x, part + h ? w.w : w.z, a0, a1);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int p = 0; p < P; ++p) {
             const uint4 v = b.x[nb][p][part + h];
-            mma_bf16_16816(c[nb], a0, v.x, v.y, c[nb][0], c[nb][1], c[nb][2], c[nb][3]);
+            if (h == 0 && p == 0) mma_bf16_16816(c[nb], a0, v.x, v.y, off[nb][0], off[nb][1], off[nb][2], off[nb][3]);
+            else mma_bf16_16816(c[nb], a0, v.x, v.y, c[nb][0], c[nb][1], c[nb][2], c[nb][3]);
             mma_bf16_16816(c[nb], a1, v.z, v.w, c[nb][0], c[nb][1], c[nb][2], c[nb][3]);
           }
       }
-      const uint32_t sw = b.s[part][m];
-      const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&sw));
+      const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&sw[m]));
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         acc[m][nb][0] = fmaf(s.x, c[nb][0], acc[m][nb][0]);
@@ -210,45 +190,89 @@ __host__ __device__ inline int w4_split(int units, int Kb, int ctas) {
   return best;
 }
 
-// The stream of one CTA: rounds 0 .. rounds - 1 of units; unit(round) gives this warp's unit (of its subgroup)
-// and done(round, red) is called by all threads once the subgroups' parts of a round are in red.  The first
-// blocks' codes are loaded before a programmatic dependent's wait, the rows after it.
-template <int CM, int NB, bool LO, bool G32, bool FULL, class Unit, class Done>
-__device__ __forceinline__ void w4_stream(const W4Dims& d, int ks, int rounds, size_t lo, float* red, Unit&& unit,
-                                          Done&& done) {
+// The stream of one CTA: rounds 0 .. rounds - 1 of units; unit(round, rows) gives this warp's unit (of its
+// subgroup; the rows' pointers only where asked for) and done(round, red) is called by all threads once the
+// subgroups' parts of a round are in red.  The first blocks are copied before a programmatic dependent's
+// wait, the rows are read after it.
+template <int CM, int NB, bool LO, bool G32, class Unit, class Done>
+__device__ __forceinline__ void w4_stream(const W4Dims& d, int ks, int rounds, size_t lo, unsigned char* smem, float* red,
+                                          int32_t* status, Unit&& unit, Done&& done) {
+  using Ring = W4Ring<CM, G32>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, part = warp % ks;
-  const int steps = ((d.Kb + ks - 1) / ks + 1) / 2;  // of two blocks
-  W4Block<CM, NB, LO, G32> ring[2];
-  W4Unit<NB> cur, nxt = unit(0);
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    if (nxt.nm > 0 && part + j * ks < d.Kb) w4_load_codes<CM, NB, LO, G32, FULL>(ring[j], nxt, d, part + j * ks);
-  pdl_wait();
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    if (nxt.nm > 0 && part + j * ks < d.Kb) w4_load_rows<CM, NB, LO, G32>(ring[j], nxt, d, part + j * ks, q, lo);
-  for (int r = 0; r < rounds; ++r) {
-    cur = nxt;
-    if (r + 1 < rounds) nxt = unit(r + 1);
-    else nxt.nm = 0;
-    float acc[CM][NB][4] = {};
-    int kb = part;
-    for (int s = 0; s + 1 < steps; ++s, kb += 2 * ks)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (cur.nm > 0) w4_block<CM, NB, LO, G32, FULL>(ring[j], cur.nm, acc);  // all but a share's last two blocks exist
-        const int kn = kb + (2 + j) * ks;
-        if (cur.nm > 0 && kn < d.Kb) w4_load<CM, NB, LO, G32, FULL>(ring[j], cur, d, kn, q, lo);
-      }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {  // the slots' next blocks are the next unit's
-      if (cur.nm > 0 && kb + j * ks < d.Kb) w4_block<CM, NB, LO, G32, FULL>(ring[j], cur.nm, acc);
-      if (nxt.nm > 0 && part + j * ks < d.Kb) w4_load<CM, NB, LO, G32, FULL>(ring[j], nxt, d, part + j * ks, q, lo);
+  Ring ring;
+  ring.init(smem, warp, lane);
+  // where the copies are: block pk of round pr's unit, into stage ps
+  int pr = 0, pk = part, ps = 0, flying = 0;
+  const uint8_t *pc, *psc;       // the unit's block 0 and group 0
+  uint32_t nc = 0, mates = 0;    // bytes of a block's codes (0: nothing to do), tiles that lie together
+  auto open = [&] {
+    const W4Unit<NB> u = unit(pr, false);
+    nc = 512u * u.nm;
+    mates = w4_mates(d, u.tile);
+    pc = u.m + w4_code_at(d, u.tile, 0) * 512;
+    psc = u.m + d.scales + w4_scale_at(d, u.tile & ~7, 0, 0) * 4;
+  };
+  open();
+  auto issue = [&] {
+    while (nc == 0 || pk >= d.Kb) {
+      if (pr + 1 >= rounds) return;
+      pk = part;
+      ++pr;
+      open();
     }
-    float* buf = red + (r & 1) * (kW4Warps * CM * NB * 128);  // two buffers: one barrier per round
-    w4_put_part<CM, NB>(buf, warp, lane, acc);
+    if (lane == 0) {
+      const uint32_t kg = G32 ? 2 * pk : d.G == 128 ? pk >> 1 : pk, ns = mates * (G32 ? 64u : 32u);
+      unsigned char* dst = ring.st + ps * Ring::kStage;
+      mbar_expect_tx(&ring.bar[ps], nc + ns);
+      bulk_load(dst, pc + (size_t)((uint32_t)pk * mates) * 512, nc, &ring.bar[ps]);
+      bulk_load(dst + CM * 512, psc + (size_t)(kg * mates) * 32, ns, &ring.bar[ps]);
+    }
+    pk += ks;
+    ++flying;
+    ps = ps + 1 == kW4Stages ? 0 : ps + 1;
+  };
+#pragma unroll 1
+  for (int i = 0; i < kW4Stages; ++i) issue();
+  pdl_wait();
+  int cs = 0;
+  uint32_t parity = 0;
+  bool dead = false;
+#pragma unroll 1
+  for (int r = 0; r < rounds; ++r) {
+    const W4Unit<NB> u = unit(r, true);
+    float acc[CM][NB][4] = {};
+    if (u.nm > 0) {
+      const int um = w4_mates(d, u.tile);
+      W4Rows<NB, LO> rows[2];  // a block's inputs and the next one's
+      if (part < d.Kb) rows[0].load(u.x, d.K, part, q, lo);
+#pragma unroll 1
+      for (int k0 = part; k0 < d.Kb; k0 += 2 * ks)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int kb = k0 + j * ks;
+          if (kb >= d.Kb) break;
+          if (kb + ks < d.Kb) rows[j ^ 1].load(u.x, d.K, kb + ks, q, lo);
+          if (!dead && !mbar_try_wait(&ring.bar[cs], parity) && !mbar_wait(&ring.bar[cs], parity)) {
+            // give up: no more copies, and those under way land before the CTA can exit
+            dead = true;
+            set_status(status, MOE_DEV_TIMEOUT);
+            for (int i = 1; i < flying; ++i)
+              mbar_wait(&ring.bar[(cs + i) % kW4Stages], parity ^ (cs + i >= kW4Stages ? 1u : 0u));
+          }
+          w4_block<CM, NB, LO, G32>(ring.st + cs * Ring::kStage, u.tile, um, lane, rows[j], acc);
+          __syncwarp();
+          --flying;
+          if (!dead) issue();
+          if (++cs == kW4Stages) {
+            cs = 0;
+            parity ^= 1u;
+          }
+        }
+    }
+    if (r > 0) __syncthreads();  // the last round's sums have been read
+    w4_put_part<CM, NB>(red, warp, lane, acc);
     __syncthreads();
-    done(r, buf);
+    done(r, red);
   }
 }
 
@@ -260,12 +284,14 @@ struct W4LinArgs {
   W4Dims d;
   void* out;
   int out_f32;
+  int32_t* status;
 };
 
 // grid (CTAs, ceil(T / (8 NB))).
-template <int CM, int NB, bool G32, bool FULL>
+template <int CM, int NB, bool G32>
 __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_linear_kernel(const W4LinArgs a) {
-  __shared__ float red[2 * kW4Warps * CM * NB * 128];
+  extern __shared__ __align__(16) unsigned char w4_smem[];
+  float* red = reinterpret_cast<float*>(w4_smem + W4Ring<CM, G32>::kBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ks = a.ks, sub = kW4Warps / ks;  // subgroups of the CTA
   const int groups = (a.d.Mt + CM - 1) / CM;
@@ -273,17 +299,18 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_linear_kernel(const W4
   const int t0 = blockIdx.y * 8 * NB, nt = min(8 * NB, a.T - t0);
   const float* mult = reinterpret_cast<const float*>(a.w + a.d.mult);
   auto first = [&](int r, int g) { return ((r * (int)gridDim.x + (int)blockIdx.x) * sub + g) * CM; };  // tile
-  auto unit = [&](int r) {
+  auto unit = [&](int r, bool) {
     W4Unit<NB> u;
-    const int tile = first(r, warp / ks);
-    w4_at(u, a.w, a.d, min(tile, a.d.Mt - 1), max(0, min(CM, a.d.Mt - tile)), lane);
+    u.m = a.w;
+    u.tile = first(r, warp / ks);
+    u.nm = max(0, min(CM, a.d.Mt - u.tile));
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)  // rows past the batch repeat its last one; their results are dropped
       u.x[nb] = a.x + (size_t)(t0 + min(8 * nb + (lane >> 2), nt - 1)) * a.ldx + 8 * (lane & 3);
     return u;
   };
   if (rounds <= 0) return;
-  w4_stream<CM, NB, false, G32, FULL>(a.d, ks, rounds, 0, red, unit, [&](int r, const float* buf) {
+  w4_stream<CM, NB, false, G32>(a.d, ks, rounds, 0, w4_smem, red, a.status, unit, [&](int r, const float* buf) {
     for (int i = threadIdx.x; i < sub * CM * 16 * nt; i += kW4Threads) {
       const int col = i % (CM * 16), row = i / (CM * 16) % nt, g = i / (CM * 16 * nt);
       const int n = first(r, g) * 16 + col;
@@ -314,9 +341,6 @@ struct W4Batch {
   int slot, n;            // slot -1: no slot
   uint16_t row[kW4Rows];  // rows of h and y
 };
-
-// Dynamic shared memory of the expert kernels: the batches.
-static size_t w4_tab_bytes(int n) { return (size_t)n * sizeof(W4Batch); }
 
 // The row batches of the listed experts, or of the ids, by ascending expert, in shared memory: `tab` holds n
 // entries, `cnt` (2 kMaxE + n ints, free afterwards) is scratch.  Built by all threads; returns their number.
@@ -414,8 +438,9 @@ __device__ __forceinline__ int w4_batches(const W4FfnArgs& g, W4Batch* tab, int*
 constexpr int kGuTiles = 4;  // (I % 32 == 0 and H % 64 == 0: both matrices have whole units)
 template <bool G32>
 __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_gateup_kernel(const W4FfnArgs a) {
-  extern __shared__ W4Batch tab[];
-  __shared__ float red[2 * kW4Warps * kGuTiles * 128];
+  extern __shared__ __align__(16) unsigned char w4_smem[];
+  float* red = reinterpret_cast<float*>(w4_smem + W4Ring<kGuTiles, G32>::kBytes);
+  W4Batch* tab = reinterpret_cast<W4Batch*>(red + kW4Warps * kGuTiles * 128);
   __shared__ int tmp[33];
   pdl_trigger();  // the down kernel may start: it waits for this one before it reads h or the counters
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -429,20 +454,22 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_gateup_kernel(const W4
   if (rounds <= 0) return;
   auto index = [&](int r, int g) { return (r * (int)gridDim.x + (int)blockIdx.x) * sub + g; };
   auto slab = [&](int slot) { return reinterpret_cast<const uint8_t*>(a.f.pool) + (size_t)slot * a.sl.bytes; };
-  auto unit = [&](int r) {
+  auto unit = [&](int r, bool rows) {
     W4Unit<1> u;
     u.nm = 0;
     const int i = index(r, warp / ks);
     if (i >= units) return u;
     const W4Batch& b = tab[i / FT];
     if (b.slot < 0) return u;
-    const int tile = i % FT * kGuTiles;
-    w4_at(u, slab(b.slot), d, tile, min(kGuTiles, d.Mt - tile), lane);
+    u.m = slab(b.slot);
+    u.tile = i % FT * kGuTiles;
+    u.nm = min(kGuTiles, d.Mt - u.tile);
+    if (!rows) return u;
     const int row = b.row[min(lane >> 2, b.n - 1)];  // rows past the batch repeat its last one
     u.x[0] = a.f.x + (size_t)((a.ids ? row : a.f.rows[row]) / a.f.k) * a.f.H + 8 * (lane & 3);
     return u;
   };
-  w4_stream<kGuTiles, 1, false, G32, true>(d, ks, rounds, 0, red, unit, [&](int r, const float* buf) {
+  w4_stream<kGuTiles, 1, false, G32>(d, ks, rounds, 0, w4_smem, red, a.f.status, unit, [&](int r, const float* buf) {
     for (int i = threadIdx.x; i < sub * 32 * kW4Rows; i += kW4Threads) {
       const int col = i & 31, row = (i >> 5) % kW4Rows, g = (i >> 5) / kW4Rows, u = index(r, g);
       if (u >= units) continue;
@@ -523,8 +550,9 @@ __global__ void __launch_bounds__(128) w4_sum_kernel(const W4FfnArgs a) {
 constexpr int kDnTiles = 4;
 template <bool G32>
 __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_down_kernel(const W4FfnArgs a) {
-  extern __shared__ W4Batch tab[];
-  __shared__ float red[2 * kW4Warps * kDnTiles * 128];
+  extern __shared__ __align__(16) unsigned char w4_smem[];
+  float* red = reinterpret_cast<float*>(w4_smem + W4Ring<kDnTiles, G32>::kBytes);
+  W4Batch* tab = reinterpret_cast<W4Batch*>(red + kW4Warps * kDnTiles * 128);
   __shared__ int tmp[33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const W4Dims& d = a.sl.dn;
@@ -543,19 +571,20 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_down_kernel(const W4Ff
   auto down = [&](int slot) {
     return reinterpret_cast<const uint8_t*>(a.f.pool) + (size_t)slot * a.sl.bytes + a.sl.dn_at;
   };
-  auto unit = [&](int r) {
+  auto unit = [&](int r, bool rows) {
     W4Unit<1> u;
     u.nm = 0;
     const int i = index(r, warp / ks);
     if (i >= units) return u;
     const W4Batch& b = tab[i / FT];
     if (b.slot < 0) return u;
-    const int tile = i % FT * kDnTiles;
-    w4_at(u, down(b.slot), d, tile, min(kDnTiles, d.Mt - tile), lane);
-    u.x[0] = a.h + (size_t)b.row[min(lane >> 2, b.n - 1)] * d.K + 8 * (lane & 3);
+    u.m = down(b.slot);
+    u.tile = i % FT * kDnTiles;
+    u.nm = min(kDnTiles, d.Mt - u.tile);
+    if (rows) u.x[0] = a.h + (size_t)b.row[min(lane >> 2, b.n - 1)] * d.K + 8 * (lane & 3);
     return u;
   };
-  w4_stream<kDnTiles, 1, true, G32, true>(d, ks, rounds, (size_t)a.n * d.K, red, unit, [&](int r, const float* buf) {
+  w4_stream<kDnTiles, 1, true, G32>(d, ks, rounds, (size_t)a.n * d.K, w4_smem, red, a.f.status, unit, [&](int r, const float* buf) {
     for (int i = threadIdx.x; i < sub * 16 * kDnTiles * kW4Rows; i += kW4Threads) {
       const int col = i % (16 * kDnTiles), row = i / (16 * kDnTiles) % kW4Rows, g = i / (16 * kDnTiles * kW4Rows);
       const int u = index(r, g);
@@ -609,21 +638,33 @@ size_t w4_ws_bytes(int n, int H, int I) {
   return w4_gemm_ffn(n) ? std::max(h, w4_ffn_gemm_ws(n, H, I, false)) : h;
 }
 
+// Dynamic shared memory of a stream kernel: the rings, the reduction buffer, the row batches.
+template <int CM, int NB, bool G32>
+static constexpr size_t w4_smem_bytes(int batches) {
+  return W4Ring<CM, G32>::kBytes + kW4Warps * CM * NB * 128 * sizeof(float) + batches * sizeof(W4Batch);
+}
+
 // The two weight streams; the second one's CTAs start as the first one's leave.
-static int launch_ffn_w4_stream(const W4FfnArgs& a, int group, int sms, cudaStream_t stream, Prof* prof) {
-  const size_t smem = w4_tab_bytes(a.n);
+template <bool G32>
+static int launch_ffn_w4_streams(const W4FfnArgs& a, int sms, cudaStream_t stream, Prof* prof) {
+  static bool done_gu[64] = {}, done_dn[64] = {};
+  MOE_CUDA_TRY(ensure_smem(w4_gateup_kernel<G32>, (int)w4_smem_bytes<kGuTiles, 1, G32>(kGemmRows), done_gu));
+  MOE_CUDA_TRY(ensure_smem(w4_down_kernel<G32>, (int)w4_smem_bytes<kDnTiles, 1, G32>(kGemmRows), done_dn));
   const dim3 grid(sms * kW4Ctas), block(kW4Threads);
   if (prof) prof->begin(MOE_PROF_FFN_GATEUP, stream);
-  if (group == 32) w4_gateup_kernel<true><<<grid, block, smem, stream>>>(a);
-  else w4_gateup_kernel<false><<<grid, block, smem, stream>>>(a);
+  w4_gateup_kernel<G32><<<grid, block, w4_smem_bytes<kGuTiles, 1, G32>(a.n), stream>>>(a);
   MOE_LAUNCH_CHECK();
   if (prof) prof->end(stream);
   if (prof) prof->begin(MOE_PROF_FFN_DOWN, stream);
-  MOE_CUDA_TRY(launch_pdl(group == 32 ? w4_down_kernel<true> : w4_down_kernel<false>, grid, block, smem, stream, a));
+  MOE_CUDA_TRY(launch_pdl(w4_down_kernel<G32>, grid, block, w4_smem_bytes<kDnTiles, 1, G32>(a.n), stream, a));
   if (prof) prof->end(stream);
   if (a.out && !a.ready)
     MOE_CUDA_TRY(launch_pdl(w4_sum_kernel, dim3(a.f.T, (a.f.H + 511) / 512), dim3(128), 0, stream, a));
   return MOE_OK;
+}
+
+static int launch_ffn_w4_stream(const W4FfnArgs& a, int group, int sms, cudaStream_t stream, Prof* prof) {
+  return group == 32 ? launch_ffn_w4_streams<true>(a, sms, stream, prof) : launch_ffn_w4_streams<false>(a, sms, stream, prof);
 }
 
 // y rows of the listed experts; ws holds h (w4_ws_bytes).
@@ -679,6 +720,16 @@ static W4ExpWs w4_exp_ws(void* base, int T, int H, int I, int k, int E) {
 
 static bool w4_gemm_linear(int T) { return T >= 64; }
 
+template <int CM, int NB, bool G32>
+static int launch_linear(const W4LinArgs& a, dim3 grid, cudaStream_t s) {
+  static bool done[64] = {};
+  constexpr size_t smem = w4_smem_bytes<CM, NB, G32>(0);
+  MOE_CUDA_TRY(ensure_smem(w4_linear_kernel<CM, NB, G32>, (int)smem, done));
+  w4_linear_kernel<CM, NB, G32><<<grid, kW4Threads, smem, s>>>(a);
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
+}
+
 // Routing slots and hidden sizes whose products the kernels index with 32 bits.
 static bool w4_rows_ok(int T, int k) { return (int64_t)T * k <= (1 << 24); }
 
@@ -706,7 +757,7 @@ extern "C" int moe_w4_linear(const void* x, long long ldx, int T, int K, int N, 
   int sms = 0;
   const int r = w4_sms(&sms);
   if (r != MOE_OK) return r;
-  W4LinArgs a{(const uint16_t*)x, (size_t)ldx, (size_t)ldo, T, 1, (const uint8_t*)w, w4_dims(K, N, group), out, out_f32};
+  W4LinArgs a{(const uint16_t*)x, (size_t)ldx, (size_t)ldo, T, 1, (const uint8_t*)w, w4_dims(K, N, group), out, out_f32, dev_status};
   // rows of a pass, and tiles of a warp: four where that leaves a unit for every other warp, as many rows need
   // the registers for their sums
   const int rows = T <= 8 ? 8 : T <= 16 ? 16 : 32, ctas = sms * kW4Ctas;
@@ -715,23 +766,20 @@ extern "C" int moe_w4_linear(const void* x, long long ldx, int T, int K, int N, 
   a.ks = w4_split(groups, a.d.Kb, ctas);
   const int gx = std::min((groups + kW4Warps / a.ks - 1) / (kW4Warps / a.ks), ctas);
   const bool g32 = group == 32;
+  cudaStream_t s = (cudaStream_t)stream;
   for (int t0 = 0; t0 < T; t0 += 65535 * rows) {  // the grid's y
     W4LinArgs b = a;
     b.x += (size_t)t0 * ldx;
     b.out = (char*)out + (size_t)t0 * ldo * (out_f32 ? 4 : 2);
     b.T = std::min(T - t0, 65535 * rows);
     const dim3 grid(gx, (b.T + rows - 1) / rows);
-    auto go = [&](auto kernel, auto kernel32) { (g32 ? kernel32 : kernel)<<<grid, kW4Threads, 0, (cudaStream_t)stream>>>(b); };
-    const bool full = a.d.Mt % cm == 0;
-    if (rows == 32) go(w4_linear_kernel<1, 4, false, true>, w4_linear_kernel<1, 4, true, true>);
-    else if (rows == 16 && full) go(w4_linear_kernel<2, 2, false, true>, w4_linear_kernel<2, 2, true, true>);
-    else if (rows == 16) go(w4_linear_kernel<2, 2, false, false>, w4_linear_kernel<2, 2, true, false>);
-    else if (cm == 4 && full) go(w4_linear_kernel<4, 1, false, true>, w4_linear_kernel<4, 1, true, true>);
-    else if (cm == 4) go(w4_linear_kernel<4, 1, false, false>, w4_linear_kernel<4, 1, true, false>);
-    else if (cm == 2 && full) go(w4_linear_kernel<2, 1, false, true>, w4_linear_kernel<2, 1, true, true>);
-    else if (cm == 2) go(w4_linear_kernel<2, 1, false, false>, w4_linear_kernel<2, 1, true, false>);
-    else go(w4_linear_kernel<1, 1, false, true>, w4_linear_kernel<1, 1, true, true>);
-    MOE_LAUNCH_CHECK();
+    int rc;
+    if (rows == 32) rc = g32 ? launch_linear<1, 4, true>(b, grid, s) : launch_linear<1, 4, false>(b, grid, s);
+    else if (rows == 16) rc = g32 ? launch_linear<2, 2, true>(b, grid, s) : launch_linear<2, 2, false>(b, grid, s);
+    else if (cm == 4) rc = g32 ? launch_linear<4, 1, true>(b, grid, s) : launch_linear<4, 1, false>(b, grid, s);
+    else if (cm == 2) rc = g32 ? launch_linear<2, 1, true>(b, grid, s) : launch_linear<2, 1, false>(b, grid, s);
+    else rc = g32 ? launch_linear<1, 1, true>(b, grid, s) : launch_linear<1, 1, false>(b, grid, s);
+    if (rc != MOE_OK) return rc;
   }
   return MOE_OK;
 }

@@ -222,13 +222,14 @@ __device__ __forceinline__ int w4g_half(int ntok) { return ((ntok + 31) & ~31) >
 __device__ __forceinline__ void w4_expand(uint32_t w, __half2 s, uint32_t* o) {
   const __half2 m24s = __hmul2(s, __float2half2_rn(-24.f));
   auto top = [&](uint32_t v) {  // codes in bits 6-9: 16 + code; (16 + code) s - 24 s is exact
-    v = (v & 0x03c003c0u) | 0x4c004c00u;
+    asm("lop3.b32 %0, %0, %1, %2, 0xEA;" : "+r"(v) : "r"(0x03c003c0u), "r"(0x4c004c00u));
     const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&v), s, m24s);
     return *reinterpret_cast<const uint32_t*>(&r);
   };
   // codes in bits 3-6: 128 + code; the shift is saved and one more half-precision operation spent, which
   // keeps the integer and the floating-point pipe equally busy
-  const uint32_t v = (w & 0x00780078u) | 0x58005800u;
+  uint32_t v;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "r"(0x00780078u), "r"(0x58005800u));
   const __half2 c = __hsub2(*reinterpret_cast<const __half2*>(&v), __float2half2_rn(136.f)), p = __hmul2(c, s);
   o[0] = *reinterpret_cast<const uint32_t*>(&p);
   o[1] = top(w >> 1);
