@@ -12,15 +12,14 @@
 // the memory bandwidth.)
 //
 // A warp streams CM neighbouring tiles of 16 columns (CM x 512 bytes a block of 64 inputs), every ks-th block
-// of the inputs, through a ring of its own in shared memory: its first lane issues the bulk copies, kW4Stages
-// blocks ahead and on across the end of a unit, so that the copies never pause and cost no registers.  The ks
-// warps that share a unit add up in shared memory, in warp order.  ks is the split that costs least for the
-// unit count at hand (w4_split): few long shares while there are units for every warp, short ones for a few
-// small matrices.
+// of the inputs, through a ring in shared memory: each lane copies the 16-byte chunks that it will itself read
+// (cp.async, kW4Stages blocks ahead and on across the end of a unit), so that the copies never pause, cost no
+// registers and need no barrier.  The ks warps that share a unit add up in shared memory, in warp order.  ks
+// is the split that costs least for the unit count at hand (w4_split): few long shares while there are units
+// for every warp, short ones for a few small matrices.
 #include <algorithm>
 
 #include "internal.cuh"
-#include "tma.cuh"
 #include "w4.cuh"
 
 namespace moe {
@@ -43,21 +42,24 @@ struct W4Unit {
   const uint16_t* x[NB];  // the lane's row of each group of eight, at input 8 (lane & 3)
 };
 
-// A warp's ring.  A stage holds a block's codes of CM tiles and the scales of all tiles that lie with them.
+// A warp's ring.  A stage holds, per lane, its chunk of each of the CM tiles and its columns' scales of them
+// (of one group, or two where G = 32).
 template <int CM, bool G32>
 struct W4Ring {
-  static constexpr int kScales = G32 ? 512 : 256, kStage = CM * 512 + kScales;
-  static constexpr int kBytes = kW4Warps * (kW4Stages * kStage + 8 * kW4Stages);  // of a CTA
-  unsigned char* st;
-  uint64_t* bar;
-  __device__ __forceinline__ void init(unsigned char* smem, int warp, int lane) {
-    st = smem + warp * kW4Stages * kStage;
-    bar = reinterpret_cast<uint64_t*>(smem + kW4Warps * kW4Stages * kStage) + warp * kW4Stages;
-    if (lane < kW4Stages) mbar_init(&bar[lane], 1);
-    mbar_fence_init();
-    __syncwarp();
-  }
+  static constexpr int kStage = CM * 512 + (G32 ? 2 : 1) * CM * 128;
+  static constexpr int kBytes = kW4Warps * kW4Stages * kStage;  // of a CTA
 };
+
+__device__ __forceinline__ uint32_t w4_shared(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void w4_copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void w4_copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void w4_copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest kW4Stages - 1 groups of this thread have landed.
+__device__ __forceinline__ void w4_copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kW4Stages - 1) : "memory"); }
 
 // The inputs of one block: a lane's eight per half, of NB groups of eight rows (LO: as the sum of two bf16).
 template <int NB, bool LO>
@@ -91,14 +93,13 @@ struct W4Rows {
 // acc += the block in stage `st` times the rows.  All CM tiles are computed; what the stage holds of tiles that
 // do not exist is dropped with their sums.
 template <int CM, int NB, bool LO, bool G32>
-__device__ __forceinline__ void w4_block(const unsigned char* st, int tile, int mates, int lane, const W4Rows<NB, LO>& b,
+__device__ __forceinline__ void w4_block(const unsigned char* st, int lane, const W4Rows<NB, LO>& b,
                                          float (&acc)[CM][NB][4]) {
   constexpr int P = LO ? 2 : 1;
   const uint32_t one = 0x3f803f80u;
   const uint32_t ones[4] = {one, one, one, one};
-  const int g = lane >> 2;
-  const uint4* codes = reinterpret_cast<const uint4*>(st) + w4_chunk(g, lane & 3);
-  const uint32_t* sc = reinterpret_cast<const uint32_t*>(st + CM * 512);
+  const uint4* codes = reinterpret_cast<const uint4*>(st) + lane;
+  const uint32_t* sc = reinterpret_cast<const uint32_t*>(st + CM * 512) + lane * CM;
 #pragma unroll
   for (int part = 0; part < (G32 ? 2 : 1); ++part) {
     constexpr int H = G32 ? 1 : 2;  // halves of the block per scale
@@ -118,12 +119,12 @@ __device__ __forceinline__ void w4_block(const unsigned char* st, int tile, int 
       for (int i = 0; i < 4; ++i) off[nb][i] = -24.f * d[i];
     }
     uint32_t sw[CM];
-    if (CM == 4 && mates == 8) {
-      const uint4 v = *reinterpret_cast<const uint4*>(sc + part * 64 + g * 8 + (tile & 7));
-      sw[0] = v.x, sw[CM > 1 ? 1 : 0] = v.y, sw[CM > 2 ? 2 : 0] = v.z, sw[CM > 3 ? 3 : 0] = v.w;
+    if constexpr (CM == 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(sc + part * CM * 32);
+      sw[0] = v.x, sw[1] = v.y, sw[2] = v.z, sw[3] = v.w;
     } else {
 #pragma unroll
-      for (int m = 0; m < CM; ++m) sw[m] = sc[(part * 8 + g) * mates + min((tile & 7) + m, mates - 1)];
+      for (int m = 0; m < CM; ++m) sw[m] = sc[part * CM * 32 + m];
     }
 #pragma unroll
     for (int m = 0; m < CM; ++m) {
@@ -196,53 +197,68 @@ __host__ __device__ inline int w4_split(int units, int Kb, int ctas) {
 // wait, the rows are read after it.
 template <int CM, int NB, bool LO, bool G32, class Unit, class Done>
 __device__ __forceinline__ void w4_stream(const W4Dims& d, int ks, int rounds, size_t lo, unsigned char* smem, float* red,
-                                          int32_t* status, Unit&& unit, Done&& done) {
-  using Ring = W4Ring<CM, G32>;
+                                          Unit&& unit, Done&& done) {
+  constexpr int kStage = W4Ring<CM, G32>::kStage;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, part = warp % ks;
-  Ring ring;
-  ring.init(smem, warp, lane);
+  unsigned char* ring = smem + warp * (kW4Stages * kStage);
+  const uint32_t ring_at = w4_shared(ring) + lane * 16, scale_at = w4_shared(ring) + CM * 512 + lane * CM * 4;
   // where the copies are: block pk of round pr's unit, into stage ps
-  int pr = 0, pk = part, ps = 0, flying = 0;
-  const uint8_t *pc, *psc;       // the unit's block 0 and group 0
-  uint32_t nc = 0, mates = 0;    // bytes of a block's codes (0: nothing to do), tiles that lie together
+  int pr = 0, pk = part, ps = 0, nm = 0;  // nm: tiles of the unit (0: nothing to do)
+  const uint8_t *pc, *psc;                // the lane's chunk in block 0, its columns' scales in group 0
+  uint32_t mates = 0;                     // tiles that lie together
   auto open = [&] {
     const W4Unit<NB> u = unit(pr, false);
-    nc = 512u * u.nm;
+    nm = u.nm;
     mates = w4_mates(d, u.tile);
-    pc = u.m + w4_code_at(d, u.tile, 0) * 512;
-    psc = u.m + d.scales + w4_scale_at(d, u.tile & ~7, 0, 0) * 4;
+    pc = u.m + w4_code_at(d, u.tile, 0) * 512 + 16 * w4_chunk(lane >> 2, q);
+    psc = u.m + d.scales + w4_scale_at(d, u.tile, 0, lane >> 2) * 4;
   };
   open();
   auto issue = [&] {
-    while (nc == 0 || pk >= d.Kb) {
-      if (pr + 1 >= rounds) return;
+    while (nm == 0 || pk >= d.Kb) {
+      if (pr + 1 >= rounds) {
+        w4_copy_commit();  // (an empty group: the waits count groups)
+        return;
+      }
       pk = part;
       ++pr;
       open();
     }
-    if (lane == 0) {
-      const uint32_t kg = G32 ? 2 * pk : d.G == 128 ? pk >> 1 : pk, ns = mates * (G32 ? 64u : 32u);
-      unsigned char* dst = ring.st + ps * Ring::kStage;
-      mbar_expect_tx(&ring.bar[ps], nc + ns);
-      bulk_load(dst, pc + (size_t)((uint32_t)pk * mates) * 512, nc, &ring.bar[ps]);
-      bulk_load(dst + CM * 512, psc + (size_t)(kg * mates) * 32, ns, &ring.bar[ps]);
+    const uint8_t* c = pc + (size_t)((uint32_t)pk * mates) * 512;
+    const uint32_t kg = G32 ? 2 * pk : d.G == 128 ? pk >> 1 : pk;
+    const uint8_t* s = psc + (size_t)(kg * mates) * 32;
+    const uint32_t cd = ring_at + ps * kStage, sd = scale_at + ps * kStage;
+    if (nm == CM && (CM != 4 || mates == 8)) {
+#pragma unroll
+      for (int m = 0; m < CM; ++m) w4_copy16(cd + m * 512, c + m * 512);
+#pragma unroll
+      for (int p = 0; p < (G32 ? 2 : 1); ++p) {
+        if constexpr (CM == 4) {
+          w4_copy16(sd + p * CM * 128, s + p * 256);
+        } else {
+#pragma unroll
+          for (int m = 0; m < CM; ++m) w4_copy4(sd + p * CM * 128 + m * 4, s + p * mates * 32 + m * 4);
+        }
+      }
+    } else {  // the last tiles
+      for (int m = 0; m < nm; ++m) {
+        w4_copy16(cd + m * 512, c + m * 512);
+        for (int p = 0; p < (G32 ? 2 : 1); ++p) w4_copy4(sd + p * CM * 128 + m * 4, s + p * mates * 32 + m * 4);
+      }
     }
+    w4_copy_commit();
     pk += ks;
-    ++flying;
     ps = ps + 1 == kW4Stages ? 0 : ps + 1;
   };
 #pragma unroll 1
   for (int i = 0; i < kW4Stages; ++i) issue();
   pdl_wait();
   int cs = 0;
-  uint32_t parity = 0;
-  bool dead = false;
 #pragma unroll 1
   for (int r = 0; r < rounds; ++r) {
     const W4Unit<NB> u = unit(r, true);
     float acc[CM][NB][4] = {};
     if (u.nm > 0) {
-      const int um = w4_mates(d, u.tile);
       W4Rows<NB, LO> rows[2];  // a block's inputs and the next one's
       if (part < d.Kb) rows[0].load(u.x, d.K, part, q, lo);
 #pragma unroll 1
@@ -252,21 +268,10 @@ __device__ __forceinline__ void w4_stream(const W4Dims& d, int ks, int rounds, s
           const int kb = k0 + j * ks;
           if (kb >= d.Kb) break;
           if (kb + ks < d.Kb) rows[j ^ 1].load(u.x, d.K, kb + ks, q, lo);
-          if (!dead && !mbar_try_wait(&ring.bar[cs], parity) && !mbar_wait(&ring.bar[cs], parity)) {
-            // give up: no more copies, and those under way land before the CTA can exit
-            dead = true;
-            set_status(status, MOE_DEV_TIMEOUT);
-            for (int i = 1; i < flying; ++i)
-              mbar_wait(&ring.bar[(cs + i) % kW4Stages], parity ^ (cs + i >= kW4Stages ? 1u : 0u));
-          }
-          w4_block<CM, NB, LO, G32>(ring.st + cs * Ring::kStage, u.tile, um, lane, rows[j], acc);
-          __syncwarp();
-          --flying;
-          if (!dead) issue();
-          if (++cs == kW4Stages) {
-            cs = 0;
-            parity ^= 1u;
-          }
+          w4_copy_wait();
+          w4_block<CM, NB, LO, G32>(ring + cs * kStage, lane, rows[j], acc);
+          issue();
+          if (++cs == kW4Stages) cs = 0;
         }
     }
     if (r > 0) __syncthreads();  // the last round's sums have been read
@@ -284,7 +289,6 @@ struct W4LinArgs {
   W4Dims d;
   void* out;
   int out_f32;
-  int32_t* status;
 };
 
 // grid (CTAs, ceil(T / (8 NB))).
@@ -310,7 +314,7 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_linear_kernel(const W4
     return u;
   };
   if (rounds <= 0) return;
-  w4_stream<CM, NB, false, G32>(a.d, ks, rounds, 0, w4_smem, red, a.status, unit, [&](int r, const float* buf) {
+  w4_stream<CM, NB, false, G32>(a.d, ks, rounds, 0, w4_smem, red, unit, [&](int r, const float* buf) {
     for (int i = threadIdx.x; i < sub * CM * 16 * nt; i += kW4Threads) {
       const int col = i % (CM * 16), row = i / (CM * 16) % nt, g = i / (CM * 16 * nt);
       const int n = first(r, g) * 16 + col;
@@ -469,7 +473,7 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_gateup_kernel(const W4
     u.x[0] = a.f.x + (size_t)((a.ids ? row : a.f.rows[row]) / a.f.k) * a.f.H + 8 * (lane & 3);
     return u;
   };
-  w4_stream<kGuTiles, 1, false, G32>(d, ks, rounds, 0, w4_smem, red, a.f.status, unit, [&](int r, const float* buf) {
+  w4_stream<kGuTiles, 1, false, G32>(d, ks, rounds, 0, w4_smem, red, unit, [&](int r, const float* buf) {
     for (int i = threadIdx.x; i < sub * 32 * kW4Rows; i += kW4Threads) {
       const int col = i & 31, row = (i >> 5) % kW4Rows, g = (i >> 5) / kW4Rows, u = index(r, g);
       if (u >= units) continue;
@@ -584,7 +588,7 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_down_kernel(const W4Ff
     if (rows) u.x[0] = a.h + (size_t)b.row[min(lane >> 2, b.n - 1)] * d.K + 8 * (lane & 3);
     return u;
   };
-  w4_stream<kDnTiles, 1, true, G32>(d, ks, rounds, (size_t)a.n * d.K, w4_smem, red, a.f.status, unit, [&](int r, const float* buf) {
+  w4_stream<kDnTiles, 1, true, G32>(d, ks, rounds, (size_t)a.n * d.K, w4_smem, red, unit, [&](int r, const float* buf) {
     for (int i = threadIdx.x; i < sub * 16 * kDnTiles * kW4Rows; i += kW4Threads) {
       const int col = i % (16 * kDnTiles), row = i / (16 * kDnTiles) % kW4Rows, g = i / (16 * kDnTiles * kW4Rows);
       const int u = index(r, g);
@@ -757,7 +761,7 @@ extern "C" int moe_w4_linear(const void* x, long long ldx, int T, int K, int N, 
   int sms = 0;
   const int r = w4_sms(&sms);
   if (r != MOE_OK) return r;
-  W4LinArgs a{(const uint16_t*)x, (size_t)ldx, (size_t)ldo, T, 1, (const uint8_t*)w, w4_dims(K, N, group), out, out_f32, dev_status};
+  W4LinArgs a{(const uint16_t*)x, (size_t)ldx, (size_t)ldo, T, 1, (const uint8_t*)w, w4_dims(K, N, group), out, out_f32};
   // rows of a pass, and tiles of a warp: four where that leaves a unit for every other warp, as many rows need
   // the registers for their sums
   const int rows = T <= 8 ? 8 : T <= 16 ? 16 : 32, ctas = sms * kW4Ctas;
