@@ -11,12 +11,14 @@
 // stream is bound by its instructions: 64 codes of 16 columns are 512 bytes, 21 cycles of an SM's share of
 // the memory bandwidth.)
 //
-// A warp streams CM neighbouring tiles of 16 columns (CM x 512 bytes a block of 64 inputs), every ks-th block
-// of the inputs, through a ring in shared memory: each lane copies the 16-byte chunks that it will itself read
-// (cp.async, kW4Stages blocks ahead and on across the end of a unit), so that the copies never pause, cost no
-// registers and need no barrier.  The ks warps that share a unit add up in shared memory, in warp order.  ks
-// is the split that costs least for the unit count at hand (w4_split): few long shares while there are units
-// for every warp, short ones for a few small matrices.
+// A warp streams CM neighbouring tiles of 16 columns (CM x 512 bytes a block of 64 inputs, one 16-byte load
+// per lane and tile), every ks-th block of the inputs, two blocks ahead and on across the end of a unit, so
+// that its loads do not pause; the activations of a block travel with its codes.  (A ring in shared memory,
+// filled by bulk copies or by cp.async, hid the latency better but cost instructions, which are what bounds
+// the stream: about 265 for 2 KB; 8 tokens took 58 and 59 us with those, 51 us with registers.)  The ks warps
+// that share a unit add up in shared memory, in warp order.  ks is the split that costs least for the unit
+// count at hand (w4_split): few long shares while there are units for every warp, short ones for a few small
+// matrices.
 #include <algorithm>
 
 #include "internal.cuh"
@@ -32,74 +34,105 @@ constexpr int kW4Ctas = 2;   // resident CTAs per SM that the registers allow
 constexpr int kW4Fuse = 16;
 constexpr int kGemmRows = 512;  // routing slots from which the experts' tensor-core path takes over
 
-constexpr int kW4Stages = 4; // blocks of a warp's ring
+// One block of 64 inputs in registers: a lane's codes of CM tiles, their columns' scales, and the lane's inputs
+// of NB groups of eight rows (LO: as the sum of two bf16).
+template <int CM, int NB, bool LO, bool G32>
+struct W4Block {
+  uint4 w[CM];
+  uint32_t s[G32 ? 2 : 1][CM];
+  uint4 x[NB][LO ? 2 : 1][2];
+};
 
-// What a warp streams of one unit.
+// What a warp streams of one unit: its tiles' codes and scales, and the rows they meet.
 template <int NB>
 struct W4Unit {
-  const uint8_t* m;       // the matrix
-  int tile, nm;           // first tile of 16 columns, tiles that exist (0: nothing to do)
-  const uint16_t* x[NB];  // the lane's row of each group of eight, at input 8 (lane & 3)
+  const uint8_t* codes;   // the lane's chunk in block 0 of the first tile
+  const uint8_t* scales;  // the lane's columns in group 0
+  int mates;              // tiles that lie between one block and the next
+  int nm;                 // tiles that exist (0: nothing to do)
+  const uint16_t* x[NB];  // the lane's row of each group, at input 8 (lane & 3)
 };
-
-// A warp's ring.  A stage holds, per lane, its chunk of each of the CM tiles and its columns' scales of them
-// (of one group, or two where G = 32).
-template <int CM, bool G32>
-struct W4Ring {
-  static constexpr int kStage = CM * 512 + (G32 ? 2 : 1) * CM * 128;
-  static constexpr int kBytes = kW4Warps * kW4Stages * kStage;  // of a CTA
-};
-
-__device__ __forceinline__ uint32_t w4_shared(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-__device__ __forceinline__ void w4_copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+template <int NB>
+__device__ __forceinline__ void w4_at(W4Unit<NB>& u, const uint8_t* m, const W4Dims& d, int tile, int nm, int lane) {
+  u.codes = m + w4_code_at(d, tile, 0) * 512 + 16 * w4_chunk(lane >> 2, lane & 3);
+  u.scales = m + d.scales + w4_scale_at(d, tile, 0, lane >> 2) * 4;
+  u.mates = w4_mates(d, tile);
+  u.nm = nm;
 }
-__device__ __forceinline__ void w4_copy4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void w4_copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All but the newest kW4Stages - 1 groups of this thread have landed.
-__device__ __forceinline__ void w4_copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kW4Stages - 1) : "memory"); }
 
-// The inputs of one block: a lane's eight per half, of NB groups of eight rows (LO: as the sum of two bf16).
-template <int NB, bool LO>
-struct W4Rows {
-  uint4 x[NB][LO ? 2 : 1][2];
-  // Rows written by the kernel before (LO) are read by plain loads, x through the read-only path.
-  __device__ __forceinline__ void load(const uint16_t* const (&xr)[NB], int K, int kb, int q, size_t lo) {
-    if (kb * 64 + 64 <= K) {
+template <int CM, int NB, bool LO, bool G32>
+__device__ __forceinline__ void w4_load_codes(W4Block<CM, NB, LO, G32>& b, const W4Unit<NB>& u, const W4Dims& d, int kb) {
+  const uint8_t* c = u.codes + (size_t)(uint32_t)(kb * u.mates) * 512;
+  const int kg = G32 ? 2 * kb : d.G == 128 ? kb >> 1 : kb;
+  const uint8_t* s = u.scales + (uint32_t)(kg * u.mates) * 32u;
+  if (u.nm == CM && (CM == 1 || u.mates == 8)) {  // (units start on a multiple of CM: a lane's scales are one load)
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+    for (int m = 0; m < CM; ++m) b.w[m] = ldg_stream(c + m * 512);
 #pragma unroll
-        for (int p = 0; p < (LO ? 2 : 1); ++p) {
-          const uint4* at = reinterpret_cast<const uint4*>(xr[nb] + p * lo + kb * 64);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) x[nb][p][h] = LO ? at[4 * h] : __ldg(at + 4 * h);
-        }
-      return;
+    for (int p = 0; p < (G32 ? 2 : 1); ++p) {
+      const uint8_t* sp = s + p * u.mates * 32;
+      if constexpr (CM == 4) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(sp));
+        b.s[p][0] = v.x, b.s[p][1] = v.y, b.s[p][2] = v.z, b.s[p][3] = v.w;
+      } else if constexpr (CM == 2) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(sp));
+        b.s[p][0] = v.x, b.s[p][1] = v.y;
+      } else {
+        b.s[p][0] = __ldg(reinterpret_cast<const uint32_t*>(sp));
+      }
     }
+    return;
+  }
+#pragma unroll
+  for (int m = 0; m < CM; ++m) {  // the last tiles; those that do not exist repeat the last one
+    const int mm = min(m, u.nm - 1);
+    b.w[m] = ldg_stream(c + mm * 512);
+#pragma unroll
+    for (int p = 0; p < (G32 ? 2 : 1); ++p)
+      b.s[p][m] = __ldg(reinterpret_cast<const uint32_t*>(s + p * u.mates * 32) + mm);
+  }
+}
+
+// Rows written by the kernel before (LO) are read by plain loads after the wait, x through the read-only path.
+template <int CM, int NB, bool LO, bool G32>
+__device__ __forceinline__ void w4_load_rows(W4Block<CM, NB, LO, G32>& b, const W4Unit<NB>& u, const W4Dims& d, int kb, int q,
+                                             size_t lo) {
+  if (kb * 64 + 64 <= d.K) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int p = 0; p < (LO ? 2 : 1); ++p)
+      for (int p = 0; p < (LO ? 2 : 1); ++p) {
+        const uint4* at = reinterpret_cast<const uint4*>(u.x[nb] + p * lo + kb * 64);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {  // K % 8 == 0: a lane's eight inputs are inside or outside together
-          const uint4* at = reinterpret_cast<const uint4*>(xr[nb] + p * lo + kb * 64 + 32 * h);
-          x[nb][p][h] = kb * 64 + 32 * h + 8 * q < K ? (LO ? *at : __ldg(at)) : make_uint4(0, 0, 0, 0);
-        }
+        for (int h = 0; h < 2; ++h) b.x[nb][p][h] = LO ? at[4 * h] : __ldg(at + 4 * h);
+      }
+    return;
   }
-};
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int p = 0; p < (LO ? 2 : 1); ++p) {
+      const uint16_t* x = u.x[nb] + p * lo + kb * 64;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // K % 8 == 0: a lane's eight inputs are inside or outside together
+        const uint4* at = reinterpret_cast<const uint4*>(x + 32 * h);
+        b.x[nb][p][h] = kb * 64 + 32 * h + 8 * q < d.K ? (LO ? *at : __ldg(at)) : make_uint4(0, 0, 0, 0);
+      }
+    }
+}
 
-// acc += the block in stage `st` times the rows.  All CM tiles are computed; what the stage holds of tiles that
-// do not exist is dropped with their sums.
 template <int CM, int NB, bool LO, bool G32>
-__device__ __forceinline__ void w4_block(const unsigned char* st, int lane, const W4Rows<NB, LO>& b,
-                                         float (&acc)[CM][NB][4]) {
+__device__ __forceinline__ void w4_load(W4Block<CM, NB, LO, G32>& b, const W4Unit<NB>& u, const W4Dims& d, int kb, int q,
+                                        size_t lo) {
+  w4_load_codes<CM, NB, LO, G32>(b, u, d, kb);
+  w4_load_rows<CM, NB, LO, G32>(b, u, d, kb, q, lo);
+}
+
+template <int CM, int NB, bool LO, bool G32>
+__device__ __forceinline__ void w4_block(const W4Block<CM, NB, LO, G32>& b, float (&acc)[CM][NB][4]) {
   constexpr int P = LO ? 2 : 1;
   const uint32_t one = 0x3f803f80u;
   const uint32_t ones[4] = {one, one, one, one};
-  const uint4* codes = reinterpret_cast<const uint4*>(st) + lane;
-  const uint32_t* sc = reinterpret_cast<const uint32_t*>(st + CM * 512) + lane * CM;
 #pragma unroll
   for (int part = 0; part < (G32 ? 2 : 1); ++part) {
     constexpr int H = G32 ? 1 : 2;  // halves of the block per scale
@@ -118,22 +151,13 @@ __device__ __forceinline__ void w4_block(const unsigned char* st, int lane, cons
 #pragma unroll
       for (int i = 0; i < 4; ++i) off[nb][i] = -24.f * d[i];
     }
-    uint32_t sw[CM];
-    if constexpr (CM == 4) {
-      const uint4 v = *reinterpret_cast<const uint4*>(sc + part * CM * 32);
-      sw[0] = v.x, sw[1] = v.y, sw[2] = v.z, sw[3] = v.w;
-    } else {
-#pragma unroll
-      for (int m = 0; m < CM; ++m) sw[m] = sc[part * CM * 32 + m];
-    }
 #pragma unroll
     for (int m = 0; m < CM; ++m) {
-      const uint4 w = codes[m * 32];
       float c[NB][4];
 #pragma unroll
       for (int h = 0; h < H; ++h) {
         uint32_t a0[4], a1[4];
-        w4_frag_bf16(part + h ? w.y : w.x, part + h ? w.w : w.z, a0, a1);
+        w4_frag_bf16(part + h ? b.w[m].y : b.w[m].x, part + h ? b.w[m].w : b.w[m].z, a0, a1);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -144,7 +168,8 @@ __device__ __forceinline__ void w4_block(const unsigned char* st, int lane, cons
             mma_bf16_16816(c[nb], a1, v.z, v.w, c[nb][0], c[nb][1], c[nb][2], c[nb][3]);
           }
       }
-      const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&sw[m]));
+      const uint32_t sw = b.s[part][m];
+      const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&sw));
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         acc[m][nb][0] = fmaf(s.x, c[nb][0], acc[m][nb][0]);
@@ -175,14 +200,14 @@ __device__ __forceinline__ float w4_sum_part(const float* red, int w0, int ks, i
   return s;
 }
 
-// Warps per unit: the power of two with the least rounds x (blocks of a share + the cost of ending a round,
-// about three blocks).
+// Warps per unit: the power of two with the least rounds x (blocks of a share + the cost of ending a round, about
+// one block: with 3 in its place 8 tokens took 51 us, with 1 46 us; 32 tokens over 288 experts 108 and 101 us).
 __host__ __device__ inline int w4_split(int units, int Kb, int ctas) {
   int best = 1;
   int64_t least = 0;
   for (int ks = 1; ks <= kW4Warps; ks *= 2) {
     const int64_t sub = (int64_t)ctas * (kW4Warps / ks), rounds = (units + sub - 1) / sub;
-    const int64_t cost = rounds * ((Kb + ks - 1) / ks + 3);
+    const int64_t cost = rounds * ((Kb + ks - 1) / ks + 1);
     if (ks == 1 || cost < least) {
       best = ks;
       least = cost;
@@ -191,93 +216,45 @@ __host__ __device__ inline int w4_split(int units, int Kb, int ctas) {
   return best;
 }
 
-// The stream of one CTA: rounds 0 .. rounds - 1 of units; unit(round, rows) gives this warp's unit (of its
-// subgroup; the rows' pointers only where asked for) and done(round, red) is called by all threads once the
-// subgroups' parts of a round are in red.  The first blocks are copied before a programmatic dependent's
-// wait, the rows are read after it.
+// The stream of one CTA: rounds 0 .. rounds - 1 of units; unit(round) gives this warp's unit (of its subgroup)
+// and done(round, red) is called by all threads once the subgroups' parts of a round are in red.  The first
+// blocks' codes are loaded before a programmatic dependent's wait, the rows after it.
 template <int CM, int NB, bool LO, bool G32, class Unit, class Done>
-__device__ __forceinline__ void w4_stream(const W4Dims& d, int ks, int rounds, size_t lo, unsigned char* smem, float* red,
-                                          Unit&& unit, Done&& done) {
-  constexpr int kStage = W4Ring<CM, G32>::kStage;
+__device__ __forceinline__ void w4_stream(const W4Dims& d, int ks, int rounds, size_t lo, float* red, Unit&& unit,
+                                          Done&& done) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, part = warp % ks;
-  unsigned char* ring = smem + warp * (kW4Stages * kStage);
-  const uint32_t ring_at = w4_shared(ring) + lane * 16, scale_at = w4_shared(ring) + CM * 512 + lane * CM * 4;
-  // where the copies are: block pk of round pr's unit, into stage ps
-  int pr = 0, pk = part, ps = 0, nm = 0;  // nm: tiles of the unit (0: nothing to do)
-  const uint8_t *pc, *psc;                // the lane's chunk in block 0, its columns' scales in group 0
-  uint32_t mates = 0;                     // tiles that lie together
-  auto open = [&] {
-    const W4Unit<NB> u = unit(pr, false);
-    nm = u.nm;
-    mates = w4_mates(d, u.tile);
-    pc = u.m + w4_code_at(d, u.tile, 0) * 512 + 16 * w4_chunk(lane >> 2, q);
-    psc = u.m + d.scales + w4_scale_at(d, u.tile, 0, lane >> 2) * 4;
-  };
-  open();
-  auto issue = [&] {
-    while (nm == 0 || pk >= d.Kb) {
-      if (pr + 1 >= rounds) {
-        w4_copy_commit();  // (an empty group: the waits count groups)
-        return;
-      }
-      pk = part;
-      ++pr;
-      open();
-    }
-    const uint8_t* c = pc + (size_t)((uint32_t)pk * mates) * 512;
-    const uint32_t kg = G32 ? 2 * pk : d.G == 128 ? pk >> 1 : pk;
-    const uint8_t* s = psc + (size_t)(kg * mates) * 32;
-    const uint32_t cd = ring_at + ps * kStage, sd = scale_at + ps * kStage;
-    if (nm == CM && (CM != 4 || mates == 8)) {
+  const int steps = ((d.Kb + ks - 1) / ks + 1) / 2;  // of two blocks
+  W4Block<CM, NB, LO, G32> ring[2];
+  W4Unit<NB> cur, nxt = unit(0);
 #pragma unroll
-      for (int m = 0; m < CM; ++m) w4_copy16(cd + m * 512, c + m * 512);
-#pragma unroll
-      for (int p = 0; p < (G32 ? 2 : 1); ++p) {
-        if constexpr (CM == 4) {
-          w4_copy16(sd + p * CM * 128, s + p * 256);
-        } else {
-#pragma unroll
-          for (int m = 0; m < CM; ++m) w4_copy4(sd + p * CM * 128 + m * 4, s + p * mates * 32 + m * 4);
-        }
-      }
-    } else {  // the last tiles
-      for (int m = 0; m < nm; ++m) {
-        w4_copy16(cd + m * 512, c + m * 512);
-        for (int p = 0; p < (G32 ? 2 : 1); ++p) w4_copy4(sd + p * CM * 128 + m * 4, s + p * mates * 32 + m * 4);
-      }
-    }
-    w4_copy_commit();
-    pk += ks;
-    ps = ps + 1 == kW4Stages ? 0 : ps + 1;
-  };
-#pragma unroll 1
-  for (int i = 0; i < kW4Stages; ++i) issue();
+  for (int j = 0; j < 2; ++j)
+    if (nxt.nm > 0 && part + j * ks < d.Kb) w4_load_codes<CM, NB, LO, G32>(ring[j], nxt, d, part + j * ks);
   pdl_wait();
-  int cs = 0;
-#pragma unroll 1
-  for (int r = 0; r < rounds; ++r) {
-    const W4Unit<NB> u = unit(r, true);
-    float acc[CM][NB][4] = {};
-    if (u.nm > 0) {
-      W4Rows<NB, LO> rows[2];  // a block's inputs and the next one's
-      if (part < d.Kb) rows[0].load(u.x, d.K, part, q, lo);
-#pragma unroll 1
-      for (int k0 = part; k0 < d.Kb; k0 += 2 * ks)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int kb = k0 + j * ks;
-          if (kb >= d.Kb) break;
-          if (kb + ks < d.Kb) rows[j ^ 1].load(u.x, d.K, kb + ks, q, lo);
-          w4_copy_wait();
-          w4_block<CM, NB, LO, G32>(ring + cs * kStage, lane, rows[j], acc);
-          issue();
-          if (++cs == kW4Stages) cs = 0;
-        }
+  for (int j = 0; j < 2; ++j)
+    if (nxt.nm > 0 && part + j * ks < d.Kb) w4_load_rows<CM, NB, LO, G32>(ring[j], nxt, d, part + j * ks, q, lo);
+  for (int r = 0; r < rounds; ++r) {
+    cur = nxt;
+    if (r + 1 < rounds) nxt = unit(r + 1);
+    else nxt.nm = 0;
+    float acc[CM][NB][4] = {};
+    int kb = part;
+    for (int s = 0; s + 1 < steps; ++s, kb += 2 * ks)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (cur.nm > 0) w4_block<CM, NB, LO, G32>(ring[j], acc);  // all but a share's last two blocks exist
+        const int kn = kb + (2 + j) * ks;
+        if (cur.nm > 0 && kn < d.Kb) w4_load<CM, NB, LO, G32>(ring[j], cur, d, kn, q, lo);
+      }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {  // the slots' next blocks are the next unit's
+      if (cur.nm > 0 && kb + j * ks < d.Kb) w4_block<CM, NB, LO, G32>(ring[j], acc);
+      if (nxt.nm > 0 && part + j * ks < d.Kb) w4_load<CM, NB, LO, G32>(ring[j], nxt, d, part + j * ks, q, lo);
     }
-    if (r > 0) __syncthreads();  // the last round's sums have been read
-    w4_put_part<CM, NB>(red, warp, lane, acc);
+    float* buf = red + (r & 1) * (kW4Warps * CM * NB * 128);  // two buffers: one barrier per round
+    w4_put_part<CM, NB>(buf, warp, lane, acc);
     __syncthreads();
-    done(r, red);
+    done(r, buf);
   }
 }
 
@@ -294,8 +271,7 @@ struct W4LinArgs {
 // grid (CTAs, ceil(T / (8 NB))).
 template <int CM, int NB, bool G32>
 __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_linear_kernel(const W4LinArgs a) {
-  extern __shared__ __align__(16) unsigned char w4_smem[];
-  float* red = reinterpret_cast<float*>(w4_smem + W4Ring<CM, G32>::kBytes);
+  __shared__ float red[2 * kW4Warps * CM * NB * 128];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ks = a.ks, sub = kW4Warps / ks;  // subgroups of the CTA
   const int groups = (a.d.Mt + CM - 1) / CM;
@@ -303,18 +279,17 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_linear_kernel(const W4
   const int t0 = blockIdx.y * 8 * NB, nt = min(8 * NB, a.T - t0);
   const float* mult = reinterpret_cast<const float*>(a.w + a.d.mult);
   auto first = [&](int r, int g) { return ((r * (int)gridDim.x + (int)blockIdx.x) * sub + g) * CM; };  // tile
-  auto unit = [&](int r, bool) {
+  auto unit = [&](int r) {
     W4Unit<NB> u;
-    u.m = a.w;
-    u.tile = first(r, warp / ks);
-    u.nm = max(0, min(CM, a.d.Mt - u.tile));
+    const int tile = first(r, warp / ks);
+    w4_at(u, a.w, a.d, min(tile, a.d.Mt - 1), max(0, min(CM, a.d.Mt - tile)), lane);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)  // rows past the batch repeat its last one; their results are dropped
       u.x[nb] = a.x + (size_t)(t0 + min(8 * nb + (lane >> 2), nt - 1)) * a.ldx + 8 * (lane & 3);
     return u;
   };
   if (rounds <= 0) return;
-  w4_stream<CM, NB, false, G32>(a.d, ks, rounds, 0, w4_smem, red, unit, [&](int r, const float* buf) {
+  w4_stream<CM, NB, false, G32>(a.d, ks, rounds, 0, red, unit, [&](int r, const float* buf) {
     for (int i = threadIdx.x; i < sub * CM * 16 * nt; i += kW4Threads) {
       const int col = i % (CM * 16), row = i / (CM * 16) % nt, g = i / (CM * 16 * nt);
       const int n = first(r, g) * 16 + col;
@@ -345,6 +320,9 @@ struct W4Batch {
   int slot, n;            // slot -1: no slot
   uint16_t row[kW4Rows];  // rows of h and y
 };
+
+// Dynamic shared memory of the expert kernels: the batches.
+static size_t w4_tab_bytes(int n) { return (size_t)n * sizeof(W4Batch); }
 
 // The row batches of the listed experts, or of the ids, by ascending expert, in shared memory: `tab` holds n
 // entries, `cnt` (2 kMaxE + n ints, free afterwards) is scratch.  Built by all threads; returns their number.
@@ -442,9 +420,8 @@ __device__ __forceinline__ int w4_batches(const W4FfnArgs& g, W4Batch* tab, int*
 constexpr int kGuTiles = 4;  // (I % 32 == 0 and H % 64 == 0: both matrices have whole units)
 template <bool G32>
 __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_gateup_kernel(const W4FfnArgs a) {
-  extern __shared__ __align__(16) unsigned char w4_smem[];
-  float* red = reinterpret_cast<float*>(w4_smem + W4Ring<kGuTiles, G32>::kBytes);
-  W4Batch* tab = reinterpret_cast<W4Batch*>(red + kW4Warps * kGuTiles * 128);
+  extern __shared__ W4Batch tab[];
+  __shared__ float red[2 * kW4Warps * kGuTiles * 128];
   __shared__ int tmp[33];
   pdl_trigger();  // the down kernel may start: it waits for this one before it reads h or the counters
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -458,22 +435,20 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_gateup_kernel(const W4
   if (rounds <= 0) return;
   auto index = [&](int r, int g) { return (r * (int)gridDim.x + (int)blockIdx.x) * sub + g; };
   auto slab = [&](int slot) { return reinterpret_cast<const uint8_t*>(a.f.pool) + (size_t)slot * a.sl.bytes; };
-  auto unit = [&](int r, bool rows) {
+  auto unit = [&](int r) {
     W4Unit<1> u;
     u.nm = 0;
     const int i = index(r, warp / ks);
     if (i >= units) return u;
     const W4Batch& b = tab[i / FT];
     if (b.slot < 0) return u;
-    u.m = slab(b.slot);
-    u.tile = i % FT * kGuTiles;
-    u.nm = min(kGuTiles, d.Mt - u.tile);
-    if (!rows) return u;
+    const int tile = i % FT * kGuTiles;
+    w4_at(u, slab(b.slot), d, tile, min(kGuTiles, d.Mt - tile), lane);
     const int row = b.row[min(lane >> 2, b.n - 1)];  // rows past the batch repeat its last one
     u.x[0] = a.f.x + (size_t)((a.ids ? row : a.f.rows[row]) / a.f.k) * a.f.H + 8 * (lane & 3);
     return u;
   };
-  w4_stream<kGuTiles, 1, false, G32>(d, ks, rounds, 0, w4_smem, red, unit, [&](int r, const float* buf) {
+  w4_stream<kGuTiles, 1, false, G32>(d, ks, rounds, 0, red, unit, [&](int r, const float* buf) {
     for (int i = threadIdx.x; i < sub * 32 * kW4Rows; i += kW4Threads) {
       const int col = i & 31, row = (i >> 5) % kW4Rows, g = (i >> 5) / kW4Rows, u = index(r, g);
       if (u >= units) continue;
@@ -554,9 +529,8 @@ __global__ void __launch_bounds__(128) w4_sum_kernel(const W4FfnArgs a) {
 constexpr int kDnTiles = 4;
 template <bool G32>
 __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_down_kernel(const W4FfnArgs a) {
-  extern __shared__ __align__(16) unsigned char w4_smem[];
-  float* red = reinterpret_cast<float*>(w4_smem + W4Ring<kDnTiles, G32>::kBytes);
-  W4Batch* tab = reinterpret_cast<W4Batch*>(red + kW4Warps * kDnTiles * 128);
+  extern __shared__ W4Batch tab[];
+  __shared__ float red[2 * kW4Warps * kDnTiles * 128];
   __shared__ int tmp[33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const W4Dims& d = a.sl.dn;
@@ -575,20 +549,19 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_down_kernel(const W4Ff
   auto down = [&](int slot) {
     return reinterpret_cast<const uint8_t*>(a.f.pool) + (size_t)slot * a.sl.bytes + a.sl.dn_at;
   };
-  auto unit = [&](int r, bool rows) {
+  auto unit = [&](int r) {
     W4Unit<1> u;
     u.nm = 0;
     const int i = index(r, warp / ks);
     if (i >= units) return u;
     const W4Batch& b = tab[i / FT];
     if (b.slot < 0) return u;
-    u.m = down(b.slot);
-    u.tile = i % FT * kDnTiles;
-    u.nm = min(kDnTiles, d.Mt - u.tile);
-    if (rows) u.x[0] = a.h + (size_t)b.row[min(lane >> 2, b.n - 1)] * d.K + 8 * (lane & 3);
+    const int tile = i % FT * kDnTiles;
+    w4_at(u, down(b.slot), d, tile, min(kDnTiles, d.Mt - tile), lane);
+    u.x[0] = a.h + (size_t)b.row[min(lane >> 2, b.n - 1)] * d.K + 8 * (lane & 3);
     return u;
   };
-  w4_stream<kDnTiles, 1, true, G32>(d, ks, rounds, (size_t)a.n * d.K, w4_smem, red, unit, [&](int r, const float* buf) {
+  w4_stream<kDnTiles, 1, true, G32>(d, ks, rounds, (size_t)a.n * d.K, red, unit, [&](int r, const float* buf) {
     for (int i = threadIdx.x; i < sub * 16 * kDnTiles * kW4Rows; i += kW4Threads) {
       const int col = i % (16 * kDnTiles), row = i / (16 * kDnTiles) % kW4Rows, g = i / (16 * kDnTiles * kW4Rows);
       const int u = index(r, g);
@@ -642,33 +615,21 @@ size_t w4_ws_bytes(int n, int H, int I) {
   return w4_gemm_ffn(n) ? std::max(h, w4_ffn_gemm_ws(n, H, I, false)) : h;
 }
 
-// Dynamic shared memory of a stream kernel: the rings, the reduction buffer, the row batches.
-template <int CM, int NB, bool G32>
-static constexpr size_t w4_smem_bytes(int batches) {
-  return W4Ring<CM, G32>::kBytes + kW4Warps * CM * NB * 128 * sizeof(float) + batches * sizeof(W4Batch);
-}
-
 // The two weight streams; the second one's CTAs start as the first one's leave.
-template <bool G32>
-static int launch_ffn_w4_streams(const W4FfnArgs& a, int sms, cudaStream_t stream, Prof* prof) {
-  static bool done_gu[64] = {}, done_dn[64] = {};
-  MOE_CUDA_TRY(ensure_smem(w4_gateup_kernel<G32>, (int)w4_smem_bytes<kGuTiles, 1, G32>(kGemmRows), done_gu));
-  MOE_CUDA_TRY(ensure_smem(w4_down_kernel<G32>, (int)w4_smem_bytes<kDnTiles, 1, G32>(kGemmRows), done_dn));
+static int launch_ffn_w4_stream(const W4FfnArgs& a, int group, int sms, cudaStream_t stream, Prof* prof) {
+  const size_t smem = w4_tab_bytes(a.n);
   const dim3 grid(sms * kW4Ctas), block(kW4Threads);
   if (prof) prof->begin(MOE_PROF_FFN_GATEUP, stream);
-  w4_gateup_kernel<G32><<<grid, block, w4_smem_bytes<kGuTiles, 1, G32>(a.n), stream>>>(a);
+  if (group == 32) w4_gateup_kernel<true><<<grid, block, smem, stream>>>(a);
+  else w4_gateup_kernel<false><<<grid, block, smem, stream>>>(a);
   MOE_LAUNCH_CHECK();
   if (prof) prof->end(stream);
   if (prof) prof->begin(MOE_PROF_FFN_DOWN, stream);
-  MOE_CUDA_TRY(launch_pdl(w4_down_kernel<G32>, grid, block, w4_smem_bytes<kDnTiles, 1, G32>(a.n), stream, a));
+  MOE_CUDA_TRY(launch_pdl(group == 32 ? w4_down_kernel<true> : w4_down_kernel<false>, grid, block, smem, stream, a));
   if (prof) prof->end(stream);
   if (a.out && !a.ready)
     MOE_CUDA_TRY(launch_pdl(w4_sum_kernel, dim3(a.f.T, (a.f.H + 511) / 512), dim3(128), 0, stream, a));
   return MOE_OK;
-}
-
-static int launch_ffn_w4_stream(const W4FfnArgs& a, int group, int sms, cudaStream_t stream, Prof* prof) {
-  return group == 32 ? launch_ffn_w4_streams<true>(a, sms, stream, prof) : launch_ffn_w4_streams<false>(a, sms, stream, prof);
 }
 
 // y rows of the listed experts; ws holds h (w4_ws_bytes).
@@ -724,16 +685,6 @@ static W4ExpWs w4_exp_ws(void* base, int T, int H, int I, int k, int E) {
 
 static bool w4_gemm_linear(int T) { return T >= 64; }
 
-template <int CM, int NB, bool G32>
-static int launch_linear(const W4LinArgs& a, dim3 grid, cudaStream_t s) {
-  static bool done[64] = {};
-  constexpr size_t smem = w4_smem_bytes<CM, NB, G32>(0);
-  MOE_CUDA_TRY(ensure_smem(w4_linear_kernel<CM, NB, G32>, (int)smem, done));
-  w4_linear_kernel<CM, NB, G32><<<grid, kW4Threads, smem, s>>>(a);
-  MOE_LAUNCH_CHECK();
-  return MOE_OK;
-}
-
 // Routing slots and hidden sizes whose products the kernels index with 32 bits.
 static bool w4_rows_ok(int T, int k) { return (int64_t)T * k <= (1 << 24); }
 
@@ -770,20 +721,19 @@ extern "C" int moe_w4_linear(const void* x, long long ldx, int T, int K, int N, 
   a.ks = w4_split(groups, a.d.Kb, ctas);
   const int gx = std::min((groups + kW4Warps / a.ks - 1) / (kW4Warps / a.ks), ctas);
   const bool g32 = group == 32;
-  cudaStream_t s = (cudaStream_t)stream;
   for (int t0 = 0; t0 < T; t0 += 65535 * rows) {  // the grid's y
     W4LinArgs b = a;
     b.x += (size_t)t0 * ldx;
     b.out = (char*)out + (size_t)t0 * ldo * (out_f32 ? 4 : 2);
     b.T = std::min(T - t0, 65535 * rows);
     const dim3 grid(gx, (b.T + rows - 1) / rows);
-    int rc;
-    if (rows == 32) rc = g32 ? launch_linear<1, 4, true>(b, grid, s) : launch_linear<1, 4, false>(b, grid, s);
-    else if (rows == 16) rc = g32 ? launch_linear<2, 2, true>(b, grid, s) : launch_linear<2, 2, false>(b, grid, s);
-    else if (cm == 4) rc = g32 ? launch_linear<4, 1, true>(b, grid, s) : launch_linear<4, 1, false>(b, grid, s);
-    else if (cm == 2) rc = g32 ? launch_linear<2, 1, true>(b, grid, s) : launch_linear<2, 1, false>(b, grid, s);
-    else rc = g32 ? launch_linear<1, 1, true>(b, grid, s) : launch_linear<1, 1, false>(b, grid, s);
-    if (rc != MOE_OK) return rc;
+    auto go = [&](auto kernel, auto kernel32) { (g32 ? kernel32 : kernel)<<<grid, kW4Threads, 0, (cudaStream_t)stream>>>(b); };
+    if (rows == 32) go(w4_linear_kernel<1, 4, false>, w4_linear_kernel<1, 4, true>);
+    else if (rows == 16) go(w4_linear_kernel<2, 2, false>, w4_linear_kernel<2, 2, true>);
+    else if (cm == 4) go(w4_linear_kernel<4, 1, false>, w4_linear_kernel<4, 1, true>);
+    else if (cm == 2) go(w4_linear_kernel<2, 1, false>, w4_linear_kernel<2, 1, true>);
+    else go(w4_linear_kernel<1, 1, false>, w4_linear_kernel<1, 1, true>);
+    MOE_LAUNCH_CHECK();
   }
   return MOE_OK;
 }
