@@ -38,19 +38,19 @@ constexpr int kGM = 128;       // packed columns per CTA
 constexpr int kGN = 256;       // rows per tile
 constexpr int kGRows = 128;    // of them in one CTA's shared memory, at most
 constexpr int kGK = 64;        // inputs per stage
-constexpr int kGXRing = 4;     // stages of rows in shared memory
 constexpr int kGChunk = 4;     // stages of codes that are copied together
-constexpr int kGWRing = 4;     // chunks of codes in shared memory
-constexpr int kGVisit = 2;     // stages that a worker dequantises at a time
-constexpr int kGSets = 4;      // sets of four worker warps, taking visits in turn
+constexpr int kGWRing = 2;     // chunks of codes in shared memory
+constexpr int kGVisit = 2;     // stages that a worker dequantises, and the MMA warp issues, at a time
+constexpr int kGSets = 4;      // sets of four worker warps, taking visits in turn; visits of rows in shared memory
 constexpr int kGWorkers = 4 * kGSets;
 constexpr int kGThreads = 96 + 32 * kGWorkers;
-constexpr int kGXBytes = kGRows * kGK * 2;
+constexpr int kGXBytes = kGRows * kGK * 2;      // a stage's rows
 constexpr int kGCodeBytes = kGChunk * 4096;     // a chunk's codes of 128 columns
 constexpr int kGScaleBytes = kGChunk * 2 * 256; // its fp16 scales (two groups a stage at most)
 constexpr int kGWBytes = kGCodeBytes + kGScaleBytes;
+constexpr int kGEpiRows = 16;                   // rows that a worker warp stores at a time
 constexpr int kGLd = 36;                        // staging: floats per row of 32 (padded against bank conflicts)
-constexpr int kGEpiBytes = 32 * kGLd * 4;       // per worker warp
+constexpr int kGEpiBytes = kGEpiRows * kGLd * 4;  // per worker warp
 constexpr uint32_t kGTmemCols = 512;
 constexpr uint32_t kGACol = kGN;                // first weight column
 static_assert(kGChunk == 2 * kGVisit, "a chunk is two visits, of different sets");
@@ -248,10 +248,10 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-// 32 rows x 32 packed columns of a warp (v[row], a column per lane, without the rows' powers of two) through
-// shared memory (st) to their place.  fac[row] is the row's power of two (kGateUp: of x, then of 1 / h).
+// 16 rows x 32 packed columns of a warp (v[row], a column per lane, without the rows' powers of two) through
+// shared memory (st) to their place.  fac[row] is the row's power of two (kGateUp: of x, and of 1 / h 64 on).
 template <int kMode>
-__device__ __forceinline__ void w4g_store(const W4GemmArgs& a, const float (&v)[32], float cm, float* st,
+__device__ __forceinline__ void w4g_store(const W4GemmArgs& a, const float* v, float cm, float* st,
                                           const float* fac, size_t row0, int nrow, int c0, int lane) {
   const W4Dims& d = a.d;
   const bool f32 = kMode == kGateUp || (kMode == kLinear ? a.out_f32 != 0 : a.yh == nullptr);
@@ -262,60 +262,52 @@ __device__ __forceinline__ void w4g_store(const W4GemmArgs& a, const float (&v)[
     // after the rounding too (a bf16 has fp32's range; y's fp16 rows carry none)
     uint32_t* s2 = reinterpret_cast<uint32_t*>(st);
 #pragma unroll
-    for (int j = 0; j < 32; j += 2)
+    for (int j = 0; j < kGEpiRows; j += 2)
       s2[j / 2 * kGLd + lane] = kMode == kLinear ? pack_bf16(v[j] * cm, v[j + 1] * cm) : pack_f16(v[j] * cm, v[j + 1] * cm);
     __syncwarp();
     uint16_t* out = kMode == kLinear ? reinterpret_cast<uint16_t*>(a.out) : a.yh;
+    const int rp = lane >> 2, seg = (lane & 3) * 8;  // 8 row pairs x 4 runs of 8 columns
+    const uint4 w0 = *reinterpret_cast<const uint4*>(s2 + rp * kGLd + seg);
+    const uint4 w1 = *reinterpret_cast<const uint4*>(s2 + rp * kGLd + seg + 4);
+    const float2 f = *reinterpret_cast<const float2*>(fac + 2 * rp);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {  // 16 row pairs x 4 runs of 8 columns
-      const int idx = i * 32 + lane, rp = idx >> 2, seg = (idx & 3) * 8;
-      const uint4 w0 = *reinterpret_cast<const uint4*>(s2 + rp * kGLd + seg);
-      const uint4 w1 = *reinterpret_cast<const uint4*>(s2 + rp * kGLd + seg + 4);
-      const float2 f = *reinterpret_cast<const float2*>(fac + 2 * rp);
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t sel = h ? 0x7632 : 0x5410;
+      uint32_t o[4] = {__byte_perm(w0.x, w0.y, sel), __byte_perm(w0.z, w0.w, sel), __byte_perm(w1.x, w1.y, sel),
+                       __byte_perm(w1.z, w1.w, sel)};
+      if (kMode == kLinear) {
+        const __nv_bfloat162 m = __float2bfloat162_rn(h ? f.y : f.x);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t sel = h ? 0x7632 : 0x5410;
-        uint32_t o[4] = {__byte_perm(w0.x, w0.y, sel), __byte_perm(w0.z, w0.w, sel), __byte_perm(w1.x, w1.y, sel),
-                         __byte_perm(w1.z, w1.w, sel)};
-        if (kMode == kLinear) {
-          const __nv_bfloat162 m = __float2bfloat162_rn(h ? f.y : f.x);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&o[j]), m);
-            o[j] = *reinterpret_cast<const uint32_t*>(&p);
-          }
+        for (int j = 0; j < 4; ++j) {
+          const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&o[j]), m);
+          o[j] = *reinterpret_cast<const uint32_t*>(&p);
         }
-        if (2 * rp + h < nrow)
-          *reinterpret_cast<uint4*>(out + (row0 + 2 * rp + h) * ld + c0 + seg) = make_uint4(o[0], o[1], o[2], o[3]);
       }
+      if (2 * rp + h < nrow)
+        *reinterpret_cast<uint4*>(out + (row0 + 2 * rp + h) * ld + c0 + seg) = make_uint4(o[0], o[1], o[2], o[3]);
     }
     __syncwarp();
     return;
   }
 #pragma unroll
-  for (int j = 0; j < 32; ++j) st[j * kGLd + lane] = v[j] * cm;
+  for (int j = 0; j < kGEpiRows; ++j) st[j * kGLd + lane] = v[j] * cm;
   __syncwarp();
   if (kMode == kGateUp) {  // columns 0-15: gate, 16-31: up of the same 16 features
-    const int f0 = c0 / 2, I = d.N / 2;
+    const int f0 = c0 / 2, I = d.N / 2, row = lane >> 1, seg = (lane & 1) * 8;
+    const float x = fac[row], xh = x * fac[64 + row];
+    uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int idx = i * 32 + lane, row = idx >> 1, seg = (idx & 1) * 8;
-      const float x = fac[row], xh = x * fac[32 + row];
-      uint32_t o[4];
-#pragma unroll
-      for (int j = 0; j < 8; j += 4) {
-        const float4 g = *reinterpret_cast<const float4*>(st + row * kGLd + seg + j);
-        const float4 u = *reinterpret_cast<const float4*>(st + row * kGLd + 16 + seg + j);
-        auto h = [&](float gv, float uv) {
-          gv *= x;
-          return __fdividef(gv, 1.f + __expf(-gv)) * (uv * xh);
-        };
-        o[j / 2] = pack_f16(h(g.x, u.x), h(g.y, u.y));
-        o[j / 2 + 1] = pack_f16(h(g.z, u.z), h(g.w, u.w));
-      }
-      if (row < nrow)
-        *reinterpret_cast<uint4*>(a.h + (row0 + row) * I + f0 + seg) = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int j = 0; j < 8; j += 4) {
+      const float4 g = *reinterpret_cast<const float4*>(st + row * kGLd + seg + j);
+      const float4 u = *reinterpret_cast<const float4*>(st + row * kGLd + 16 + seg + j);
+      auto h = [&](float gv, float uv) {
+        gv *= x;
+        return __fdividef(gv, 1.f + __expf(-gv)) * (uv * xh);
+      };
+      o[j / 2] = pack_f16(h(g.x, u.x), h(g.y, u.y));
+      o[j / 2 + 1] = pack_f16(h(g.z, u.z), h(g.w, u.w));
     }
+    if (row < nrow) *reinterpret_cast<uint4*>(a.h + (row0 + row) * I + f0 + seg) = make_uint4(o[0], o[1], o[2], o[3]);
   } else if (ragged) {
     // unaligned or ragged rows of out: element stores, 32 consecutive columns per row
     if (c0 + lane < d.N)
@@ -328,7 +320,7 @@ __device__ __forceinline__ void w4g_store(const W4GemmArgs& a, const float (&v)[
   } else {
     float* out = kMode == kLinear ? reinterpret_cast<float*>(a.out) : a.y;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {  // 32 rows x 128 B
+    for (int i = 0; i < kGEpiRows / 4; ++i) {  // rows of 128 B
       const int idx = i * 32 + lane, row = idx >> 3, seg = (idx & 7) * 4;
       float4 o = *reinterpret_cast<const float4*>(st + row * kGLd + seg);
       const float m = fac[row];
@@ -352,8 +344,8 @@ __device__ __forceinline__ float w4g_factors(const W4GemmArgs& a, const W4GTile&
     const bool mine = row < nrow;
     const size_t p = (size_t)ti.row0 + tok0 + row;
     // scaled rows of y keep the row's own power of two apart
-    fac[64 * i + lane] = !mine ? 0.f : kMode == kDown && a.yh ? 1.f : pow2(a.rexp[p]);
-    if (kMode == kGateUp) fac[64 * i + 32 + lane] = mine ? pow2(-a.oexp[p]) : 0.f;
+    fac[row] = !mine ? 0.f : kMode == kDown && a.yh ? 1.f : pow2(a.rexp[p]);
+    if (kMode == kGateUp) fac[64 + row] = mine ? pow2(-a.oexp[p]) : 0.f;
   }
   float cm = 0.f;
   if (c < d.N) cm = reinterpret_cast<const float*>(ti.base + d.mult)[c];
@@ -362,7 +354,7 @@ __device__ __forceinline__ float w4g_factors(const W4GemmArgs& a, const W4GTile&
 }
 
 // Drains 64 rows (of set `set`) x this warp's 32 columns: to registers, the accumulators are handed back
-// (tempty of the pair's first CTA), then 32 rows at a time through shared memory to their place.
+// (tempty of the pair's first CTA), then 16 rows at a time through shared memory to their place.
 template <int kMode, class Wait>
 __device__ __forceinline__ void w4g_drain(const W4GemmArgs& a, const W4GTile& ti, int blk, uint32_t taddr, int q, int set,
                                           int lane, float* st, const float* fac, float cm, uint64_t* tfull,
@@ -384,25 +376,28 @@ __device__ __forceinline__ void w4g_drain(const W4GemmArgs& a, const W4GTile& ti
   __syncwarp();
   if (lane == 0) mbar_arrive_pair(tempty0);
   if (!any || dead) return;
-  w4g_store<kMode>(a, v0, cm, st, fac, row0, min(nrow, 32), c0, lane);
-  if (nrow > 32) w4g_store<kMode>(a, v1, cm, st, fac + 64, row0 + 32, min(nrow - 32, 32), c0, lane);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (nrow > 16 * i)
+      w4g_store<kMode>(a, (i < 2 ? v0 : v1) + 16 * (i & 1), cm, st, fac + 16 * i, row0 + 16 * i, min(nrow - 16 * i, 16), c0,
+                       lane);
 }
 
 template <int kMode>
 __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs a, const __grid_constant__ W4RowMaps mapX) {
   extern __shared__ __align__(16) unsigned char gsm_raw[];
   unsigned char* sm = gsm_raw + ((0u - smem_u32(gsm_raw)) & 1023u);  // (an offset: the accesses stay shared ones)
-  unsigned char* xs = sm;                             // [ring][16 KB]
-  unsigned char* wsm = sm + kGXRing * kGXBytes;       // [ring][codes | scales]
-  float* epi = reinterpret_cast<float*>(wsm + kGWRing * kGWBytes);   // [workers][32][kGLd]
+  unsigned char* xs = sm;                             // [ring][stages of a visit][16 KB]
+  unsigned char* wsm = sm + kGSets * kGVisit * kGXBytes;  // [ring][codes | scales]
+  float* epi = reinterpret_cast<float*>(wsm + kGWRing * kGWBytes);   // [workers][kGEpiRows][kGLd]
   float* facs = epi + kGWorkers * (kGEpiBytes / 4);   // [workers][128]
-  uint64_t* xfull = reinterpret_cast<uint64_t*>(facs + kGWorkers * 128);
-  uint64_t* xempty = xfull + kGXRing;
-  uint64_t* wfull = xempty + kGXRing;
+  // of a visit: its rows have landed and its weights are in TMEM, in both CTAs (the first one's barrier counts);
+  // its MMAs have read both
+  uint64_t* full = reinterpret_cast<uint64_t*>(facs + kGWorkers * 128);
+  uint64_t* empty = full + kGSets;
+  uint64_t* wfull = empty + kGSets;
   uint64_t* wempty = wfull + kGWRing;
-  uint64_t* afull = wempty + kGWRing;
-  uint64_t* aempty = afull + kGSets;
-  uint64_t* tfull = aempty + kGSets;
+  uint64_t* tfull = wempty + kGWRing;
   uint64_t* tempty = tfull + 1;
   uint64_t* done = tempty + 1;
   __shared__ uint32_t s_tmem;
@@ -417,17 +412,13 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   int nl = 0, total;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kGXRing; ++s) {
-      mbar_init(&xfull[s], 1);
-      mbar_init(&xempty[s], 1);
-    }
     for (int s = 0; s < kGWRing; ++s) {
       mbar_init(&wfull[s], 1);
       mbar_init(&wempty[s], 8);  // two visits of four warps
     }
     for (int s = 0; s < kGSets; ++s) {
-      mbar_init(&afull[s], 8);  // a set's four warps in each CTA
-      mbar_init(&aempty[s], 1);
+      mbar_init(&full[s], 9);  // a set's four warps in each CTA, and the bytes
+      mbar_init(&empty[s], 1);
     }
     mbar_init(tfull, 1);
     mbar_init(tempty, 2 * kGWorkers);
@@ -478,41 +469,47 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   };
 
   if (warp == 0) {
-    uint32_t xi = 0;  // stages issued
+    uint32_t vi = 0;  // visits issued
     const bool lead = elect_one();
     for (int t = cl; t < total && !dead; t += ncl) {
       const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
       const int r = w4g_half(ti.ntok), row = ti.row0 + (int)rank * r;
-      for (int kb = 0; kb < nkb; ++kb, ++xi) {
-        const uint32_t s = xi % kGXRing, use = xi / kGXRing;
-        if (use > 0) wait(&xempty[s], (use - 1) & 1u);
+      for (int kb = 0; kb < nkb; kb += kGVisit, ++vi) {
+        const uint32_t s = vi % kGSets, use = vi / kGSets, nb = min(kGVisit, nkb - kb);
+        if (use > 0) wait(&empty[s], (use - 1) & 1u);
         if (dead) break;
         if (lead) {
           // the first CTA's barrier counts the bytes of both
-          if (rank == 0) mbar_expect_tx(&xfull[s], 2u * (uint32_t)r * (kGK * 2));
-          const uint32_t fb = mapa_shared(smem_u32(&xfull[s]), 0);
-          unsigned char* dst = xs + s * kGXBytes;
-          if (r == kGRows) {
-            tma_load_3d_pair(dst, &mapX.m[0], fb, kb * kGK, row, 0);
-          } else {
-            int o = 0;
-            if (r & 64) {
-              tma_load_3d_pair(dst, &mapX.m[1], fb, kb * kGK, row, 0);
-              o = 64;
+          if (rank == 0) mbar_expect_tx(&full[s], 2u * nb * (uint32_t)r * (kGK * 2));
+          const uint32_t fb = mapa_shared(smem_u32(&full[s]), 0);
+          for (uint32_t h = 0; h < nb; ++h) {
+            unsigned char* dst = xs + (s * kGVisit + h) * kGXBytes;
+            const int c = (kb + (int)h) * kGK;
+            if (r == kGRows) {
+              tma_load_3d_pair(dst, &mapX.m[0], fb, c, row, 0);
+            } else {
+              int o = 0;
+              if (r & 64) {
+                tma_load_3d_pair(dst, &mapX.m[1], fb, c, row, 0);
+                o = 64;
+              }
+              if (r & 32) {
+                tma_load_3d_pair(dst + o * 128, &mapX.m[2], fb, c, row + o, 0);
+                o += 32;
+              }
+              if (r & 16) tma_load_3d_pair(dst + o * 128, &mapX.m[3], fb, c, row + o, 0);
             }
-            if (r & 32) {
-              tma_load_3d_pair(dst + o * 128, &mapX.m[2], fb, kb * kGK, row + o, 0);
-              o += 32;
-            }
-            if (r & 16) tma_load_3d_pair(dst + o * 128, &mapX.m[3], fb, kb * kGK, row + o, 0);
           }
         }
         __syncwarp();
       }
     }
-    // after a timeout: let every copy land before the CTAs can exit
+    // after a timeout: let every copy land before the CTAs can exit (the workers' arrivals may be missing, so
+    // that the barriers can only show it where they complete: the wait is short and bounded)
     if (dead && rank == 0)
-      for (uint32_t j = xi > kGXRing ? xi - kGXRing : 0; j < xi; ++j) mbar_wait(&xfull[j % kGXRing], (j / kGXRing) & 1u);
+      for (uint32_t j = vi > kGSets ? vi - kGSets : 0; j < vi; ++j)
+        for (int i = 0; i < 1024 && !mbar_poll(&full[j % kGSets], (j / kGSets) & 1u); ++i) {
+        }
   } else if (warp == kGWorkers + 2) {
     uint32_t wi = 0;  // chunks issued
     const bool lead = elect_one();
@@ -545,28 +542,22 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     if (rank == 0) {
       const uint64_t bd0 = smem_desc_l(smem_u32(xs), 16, 1024, kLayoutSw128);
       const bool lead = elect_one();
-      uint32_t xi = 0, vi = 0, tc = 0;  // stages of rows, visits, tiles
+      uint32_t vi = 0, tc = 0;  // visits, tiles
       for (int t = cl; t < total && !dead; t += ncl, ++tc) {
         const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
         const uint32_t idesc = idesc_f16(2 * kGM, 2 * w4g_half(ti.ntok));
         if (tc > 0) wait(tempty, (tc - 1) & 1u);
-        for (int kb = 0; kb < nkb; ++vi) {
-          const uint32_t as = vi % kGSets;
-          wait(&afull[as], (vi / kGSets) & 1u);
-#pragma unroll
-          for (int h = 0; h < kGVisit; ++h, ++kb, ++xi) {
-            if (kb >= nkb) break;
-            const uint32_t s = xi % kGXRing;
-            wait(&xfull[s], (xi / kGXRing) & 1u);
-            tc_fence_after();
-            if (lead && !dead) {
-              umma_f16_ts_pair_k64(tmem, tmem + kGACol + as * 64 + h * 32, bd0 + (uint64_t)(s * (kGXBytes >> 4)), idesc,
-                                   kb > 0);
-              umma_commit_pair(&xempty[s]);
-            }
-            __syncwarp();
+        for (int kb = 0; kb < nkb; kb += kGVisit, ++vi) {
+          const uint32_t s = vi % kGSets;
+          wait(&full[s], (vi / kGSets) & 1u);
+          tc_fence_after();
+          if (lead && !dead) {
+            const uint32_t at = tmem + kGACol + s * 64;
+            const uint64_t bd = bd0 + (uint64_t)(s * kGVisit * (kGXBytes >> 4));
+            umma_f16_ts_pair_k64(tmem, at, bd, idesc, kb > 0);
+            if (kb + 1 < nkb) umma_f16_ts_pair_k64(tmem, at + 32, bd + (kGXBytes >> 4), idesc, 1);
           }
-          if (lead) umma_commit_pair(&aempty[as]);
+          if (lead) umma_commit_pair(&empty[s]);
           __syncwarp();
         }
         if (lead) umma_commit_pair(tfull);
@@ -583,7 +574,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     const uint32_t a_addr = lane_addr + kGACol + set * 64;
     float* st = epi + (warp - 2) * (kGEpiBytes / 4);
     float* fac = facs + (warp - 2) * 128;
-    const uint32_t afull0 = mapa_shared(smem_u32(&afull[set]), 0), tempty0 = mapa_shared(smem_u32(tempty), 0);
+    const uint32_t full0 = mapa_shared(smem_u32(&full[set]), 0), tempty0 = mapa_shared(smem_u32(tempty), 0);
     uint32_t vi = 0, wi = 0, tc = 0;  // visits and chunks before this tile, tiles drained
     uint32_t uses = 0;                // this set's visits
     W4GTile prev = {};
@@ -623,7 +614,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
               w4_expand(w[j].x, s0, &o[4 * j]);
               w4_expand(w[j].y, s1, &o[16 + 4 * j]);
             }
-            if (h == 0 && uses > 0) wait(&aempty[set], (uses - 1) & 1u);
+            if (h == 0 && uses > 0) wait(&empty[set], (uses - 1) & 1u);
             tc_fence_after();
             tmem_st32(a_addr + 32 * h, o);
           }
@@ -631,7 +622,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive_pair(afull0);
+            mbar_arrive_pair(full0);
             // a last chunk of one visit counts it twice
             mbar_arrive_n(&wempty[ws], kb % kGChunk == 0 && kb + kGVisit >= nkb ? 2 : 1);
           }
@@ -804,7 +795,7 @@ __global__ void __launch_bounds__(128) w4_combine_kernel(const uint16_t* __restr
   *reinterpret_cast<uint4*>(out + (size_t)t * H + c) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-constexpr size_t kGSmem = 1024 + (size_t)kGXRing * kGXBytes + (size_t)kGWRing * kGWBytes +
+constexpr size_t kGSmem = 1024 + (size_t)kGSets * kGVisit * kGXBytes + (size_t)kGWRing * kGWBytes +
                           (size_t)kGWorkers * (kGEpiBytes + 128 * 4) + 64 * sizeof(uint64_t);
 static_assert(kGSmem <= 222 * 1024, "shared memory of a CTA, with the 4.3 KB of static arrays");
 
