@@ -19,10 +19,13 @@
 // an SM gets; and each code is dequantised once per 256 rows.  (One CTA, 2 x 128 columns x 128 rows, took
 // 87 us for 4096 rows through 2048 x 4096: its MMAs of 64 cycles could not be issued fast enough.)
 //
-// Warps: 0 loads the rows, the last one the codes (which run further ahead), 1 allocates TMEM and, in the
-// pair's first CTA, issues the MMAs (one lane); 2-17 are workers: four sets of four warps (one per TMEM lane quarter) that dequantise 128 inputs in turn, each
-// set into TMEM columns of its own; all drain the accumulators.  Before a tile is drained three sets
-// have dequantised inputs of the next one, so the MMAs go on while the drained values are stored.
+// Warps: 0-15 are workers: four sets of four warps (one per TMEM lane quarter) that dequantise 128 inputs (a
+// visit) in turn, each set into TMEM columns of its own; all drain the accumulators.  16 loads the rows, 18 the
+// codes (which run further ahead), 17 allocates TMEM and, in the pair's first CTA, issues the MMAs (one lane).
+// A visit has one barrier for its rows' bytes and its workers' arrivals, and one commit gives both rings back:
+// with a barrier and a commit per stage and ring the issuing warp needed 390 cycles a stage, and 4096 rows
+// through 2048 x 4096 took 73 us, now 66.  Before a tile is drained three sets have dequantised inputs of the
+// next one, so the MMAs go on while the drained values are stored.
 // TMEM: 256 accumulator columns, 4 x 64 columns of weights.
 #include <limits.h>
 
@@ -43,7 +46,10 @@ constexpr int kGWRing = 2;     // chunks of codes in shared memory
 constexpr int kGVisit = 2;     // stages that a worker dequantises, and the MMA warp issues, at a time
 constexpr int kGSets = 4;      // sets of four worker warps, taking visits in turn; visits of rows in shared memory
 constexpr int kGWorkers = 4 * kGSets;
-constexpr int kGThreads = 96 + 32 * kGWorkers;
+constexpr int kGThreads = 128 + 32 * kGWorkers;  // the workers, then four warps (one idle): whole warpgroups
+// Registers per thread after the split: what is live while 64 accumulators per lane are drained needs more than
+// the 96 of an even split.  512 x 112 + 128 x 32 = 640 x 96.
+constexpr int kGWorkerRegs = 112, kGHelperRegs = 32;
 constexpr int kGXBytes = kGRows * kGK * 2;      // a stage's rows
 constexpr int kGCodeBytes = kGChunk * 4096;     // a chunk's codes of 128 columns
 constexpr int kGScaleBytes = kGChunk * 2 * 256; // its fp16 scales (two groups a stage at most)
@@ -248,47 +254,54 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-// 16 rows x 32 packed columns of a warp (v[row], a column per lane, without the rows' powers of two) through
-// shared memory (st) to their place.  fac[row] is the row's power of two (kGateUp: of x, and of 1 / h 64 on).
+// 16 rows x 32 packed columns of a warp, as 16-bit values times the column's power of two (v[row pair], a
+// column per lane), through shared memory (st) to their place.  fac[row] is the row's power of two.
 template <int kMode>
-__device__ __forceinline__ void w4g_store(const W4GemmArgs& a, const float* v, float cm, float* st,
-                                          const float* fac, size_t row0, int nrow, int c0, int lane) {
+__device__ __forceinline__ void w4g_store16(const W4GemmArgs& a, const uint32_t* v, uint32_t* st, const float* fac,
+                                            size_t row0, int nrow, int c0, int lane) {
   const W4Dims& d = a.d;
-  const bool f32 = kMode == kGateUp || (kMode == kLinear ? a.out_f32 != 0 : a.yh == nullptr);
   const size_t ld = kMode == kLinear ? a.ldo : (size_t)d.N;
-  const bool ragged = kMode == kLinear && !(ld % 8 == 0 && (uintptr_t)a.out % 16 == 0 && c0 + 32 <= d.N);
-  if (!f32 && !ragged) {
-    // 16-bit rows: two rows of a column in a word, [row pair][kGLd columns]; the powers of two are exact
-    // after the rounding too (a bf16 has fp32's range; y's fp16 rows carry none)
-    uint32_t* s2 = reinterpret_cast<uint32_t*>(st);
 #pragma unroll
-    for (int j = 0; j < kGEpiRows; j += 2)
-      s2[j / 2 * kGLd + lane] = kMode == kLinear ? pack_bf16(v[j] * cm, v[j + 1] * cm) : pack_f16(v[j] * cm, v[j + 1] * cm);
-    __syncwarp();
-    uint16_t* out = kMode == kLinear ? reinterpret_cast<uint16_t*>(a.out) : a.yh;
+  for (int j = 0; j < kGEpiRows / 2; ++j) st[j * kGLd + lane] = v[j];
+  __syncwarp();
+  uint16_t* out = kMode == kLinear ? reinterpret_cast<uint16_t*>(a.out) : a.yh;
+  auto scaled = [](uint32_t w, float m) {
+    const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), __float2bfloat162_rn(m));
+    return *reinterpret_cast<const uint32_t*>(&p);
+  };
+  if (kMode == kLinear && !(ld % 8 == 0 && (uintptr_t)a.out % 16 == 0 && c0 + 32 <= d.N)) {
+    // unaligned or ragged rows of out: element stores, 32 consecutive columns per row
+    if (c0 + lane < d.N)
+      for (int j = 0; j < nrow; ++j) {
+        const uint32_t w = scaled(st[j / 2 * kGLd + lane], fac[j]);
+        out[(row0 + j) * ld + c0 + lane] = uint16_t(j & 1 ? w >> 16 : w);
+      }
+  } else {
     const int rp = lane >> 2, seg = (lane & 3) * 8;  // 8 row pairs x 4 runs of 8 columns
-    const uint4 w0 = *reinterpret_cast<const uint4*>(s2 + rp * kGLd + seg);
-    const uint4 w1 = *reinterpret_cast<const uint4*>(s2 + rp * kGLd + seg + 4);
+    const uint4 w0 = *reinterpret_cast<const uint4*>(st + rp * kGLd + seg);
+    const uint4 w1 = *reinterpret_cast<const uint4*>(st + rp * kGLd + seg + 4);
     const float2 f = *reinterpret_cast<const float2*>(fac + 2 * rp);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t sel = h ? 0x7632 : 0x5410;
       uint32_t o[4] = {__byte_perm(w0.x, w0.y, sel), __byte_perm(w0.z, w0.w, sel), __byte_perm(w1.x, w1.y, sel),
                        __byte_perm(w1.z, w1.w, sel)};
-      if (kMode == kLinear) {
-        const __nv_bfloat162 m = __float2bfloat162_rn(h ? f.y : f.x);
+      if (kMode == kLinear)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&o[j]), m);
-          o[j] = *reinterpret_cast<const uint32_t*>(&p);
-        }
-      }
+        for (int j = 0; j < 4; ++j) o[j] = scaled(o[j], h ? f.y : f.x);
       if (2 * rp + h < nrow)
         *reinterpret_cast<uint4*>(out + (row0 + 2 * rp + h) * ld + c0 + seg) = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    __syncwarp();
-    return;
   }
+  __syncwarp();
+}
+
+// The same of fp32 values (v[row], without the column's power of two cm): to fp32 results, or (kGateUp) to h, with
+// fac[64 + row] the power of two of 1 / h.
+template <int kMode>
+__device__ __forceinline__ void w4g_store32(const W4GemmArgs& a, const float* v, float cm, float* st, const float* fac,
+                                            size_t row0, int nrow, int c0, int lane) {
+  const W4Dims& d = a.d;
 #pragma unroll
   for (int j = 0; j < kGEpiRows; ++j) st[j * kGLd + lane] = v[j] * cm;
   __syncwarp();
@@ -308,79 +321,114 @@ __device__ __forceinline__ void w4g_store(const W4GemmArgs& a, const float* v, f
       o[j / 2 + 1] = pack_f16(h(g.z, u.z), h(g.w, u.w));
     }
     if (row < nrow) *reinterpret_cast<uint4*>(a.h + (row0 + row) * I + f0 + seg) = make_uint4(o[0], o[1], o[2], o[3]);
-  } else if (ragged) {
-    // unaligned or ragged rows of out: element stores, 32 consecutive columns per row
-    if (c0 + lane < d.N)
-      for (int row = 0; row < nrow; ++row) {
-        const float o = st[row * kGLd + lane] * fac[row];
-        const size_t at = (row0 + row) * ld + c0 + lane;
-        if (f32) reinterpret_cast<float*>(a.out)[at] = o;
-        else reinterpret_cast<uint16_t*>(a.out)[at] = f32_to_bf16(o);
-      }
   } else {
     float* out = kMode == kLinear ? reinterpret_cast<float*>(a.out) : a.y;
+    const size_t ld = kMode == kLinear ? a.ldo : (size_t)d.N;
+    if (kMode == kLinear && !(ld % 4 == 0 && (uintptr_t)a.out % 16 == 0 && c0 + 32 <= d.N)) {
+      if (c0 + lane < d.N)
+        for (int row = 0; row < nrow; ++row) out[(row0 + row) * ld + c0 + lane] = st[row * kGLd + lane] * fac[row];
+    } else {
 #pragma unroll
-    for (int i = 0; i < kGEpiRows / 4; ++i) {  // rows of 128 B
-      const int idx = i * 32 + lane, row = idx >> 3, seg = (idx & 7) * 4;
-      float4 o = *reinterpret_cast<const float4*>(st + row * kGLd + seg);
-      const float m = fac[row];
-      o.x *= m, o.y *= m, o.z *= m, o.w *= m;
-      if (row < nrow) *reinterpret_cast<float4*>(out + (row0 + row) * ld + c0 + seg) = o;
+      for (int i = 0; i < kGEpiRows / 4; ++i) {  // rows of 128 B
+        const int idx = i * 32 + lane, row = idx >> 3, seg = (idx & 7) * 4;
+        float4 o = *reinterpret_cast<const float4*>(st + row * kGLd + seg);
+        const float m = fac[row];
+        o.x *= m, o.y *= m, o.z *= m, o.w *= m;
+        if (row < nrow) *reinterpret_cast<float4*>(out + (row0 + row) * ld + c0 + seg) = o;
+      }
     }
   }
   __syncwarp();
 }
 
-// What the drain of 64 rows (of set `set`) multiplies with: the rows' powers of two, into fac, and the
-// lane's column's, returned.
+// What the drain of 64 rows (of set `set`) multiplies with: the rows' exponents (two rows a lane) and the
+// lane's column's power of two.  Loaded a visit before they are needed.
+struct W4GFactors {
+  int r[2], o[2];
+  float cm;
+};
 template <int kMode>
-__device__ __forceinline__ float w4g_factors(const W4GemmArgs& a, const W4GTile& ti, int blk, int q, int set, int lane,
-                                             float* fac) {
+__device__ __forceinline__ W4GFactors w4g_factors(const W4GemmArgs& a, const W4GTile& ti, int blk, int q, int set,
+                                                  int lane) {
   const W4Dims& d = a.d;
   const int tok0 = 64 * set, nrow = ti.ntok - tok0, c = blk * kGM + 32 * q + lane;
+  W4GFactors f = {};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int row = 32 * i + lane;
-    const bool mine = row < nrow;
-    const size_t p = (size_t)ti.row0 + tok0 + row;
-    // scaled rows of y keep the row's own power of two apart
-    fac[row] = !mine ? 0.f : kMode == kDown && a.yh ? 1.f : pow2(a.rexp[p]);
-    if (kMode == kGateUp) fac[64 + row] = mine ? pow2(-a.oexp[p]) : 0.f;
+    const size_t p = (size_t)ti.row0 + tok0 + 32 * i + lane;
+    if (32 * i + lane < nrow) {
+      // scaled rows of y keep the row's own power of two apart
+      if (!(kMode == kDown && a.yh)) f.r[i] = a.rexp[p];
+      if (kMode == kGateUp) f.o[i] = a.oexp[p];
+    }
   }
-  float cm = 0.f;
-  if (c < d.N) cm = reinterpret_cast<const float*>(ti.base + d.mult)[c];
-  if (kMode == kDown && a.yh) cm = ldexpf(cm, -w4_y_exp(ti.base, d));
-  return cm;
+  if (c < d.N) f.cm = reinterpret_cast<const float*>(ti.base + d.mult)[c];
+  if (kMode == kDown && a.yh) f.cm = ldexpf(f.cm, -w4_y_exp(ti.base, d));
+  return f;
 }
 
 // Drains 64 rows (of set `set`) x this warp's 32 columns: to registers, the accumulators are handed back
-// (tempty of the pair's first CTA), then 16 rows at a time through shared memory to their place.
+// (tempty of the pair's first CTA), then 16 rows at a time through shared memory to their place.  16-bit results
+// are rounded on their way to the registers, which takes half as many.
 template <int kMode, class Wait>
 __device__ __forceinline__ void w4g_drain(const W4GemmArgs& a, const W4GTile& ti, int blk, uint32_t taddr, int q, int set,
-                                          int lane, float* st, const float* fac, float cm, uint64_t* tfull,
+                                          int lane, float* st, float* fac, const W4GFactors& f, uint64_t* tfull,
                                           uint32_t tempty0, uint32_t parity, Wait&& wait, const bool& dead) {
   const W4Dims& d = a.d;
   const int tok0 = 64 * set, nrow = ti.ntok - tok0, c0 = blk * kGM + 32 * q;
   const bool any = nrow > 0 && c0 < d.N;
+  const bool half = kMode != kGateUp && (kMode == kLinear ? !a.out_f32 : a.yh != nullptr);
   const size_t row0 = (size_t)ti.row0 + tok0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    fac[32 * i + lane] = pow2(f.r[i]);
+    if (kMode == kGateUp) fac[64 + 32 * i + lane] = pow2(-f.o[i]);
+  }
   __syncwarp();
   wait(tfull, parity);
   tc_fence_after();
-  float v0[32], v1[32];
-  if (any) {
+  auto hand_back = [&] {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_pair(tempty0);
+  };
+  if (!any) {
+    hand_back();
+    return;
+  }
+  if (half) {
+    // two rows of a column in a word; the rows' powers of two are exact after the rounding too (a bf16 has
+    // fp32's range; y's fp16 rows carry none)
+    uint32_t v[32];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float t[32];
+      tmem_ld32(taddr + tok0 + 32 * i, t);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 32; j += 2)
+        v[16 * i + j / 2] = kMode == kLinear ? pack_bf16(t[j] * f.cm, t[j + 1] * f.cm) : pack_f16(t[j] * f.cm, t[j + 1] * f.cm);
+    }
+    hand_back();
+    if (dead) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (nrow > 16 * i)
+        w4g_store16<kMode>(a, v + 8 * i, reinterpret_cast<uint32_t*>(st), fac + 16 * i, row0 + 16 * i,
+                           min(nrow - 16 * i, 16), c0, lane);
+  } else {
+    float v0[32], v1[32];
     tmem_ld32(taddr + tok0, v0);
     tmem_ld32(taddr + tok0 + 32, v1);
     tmem_ld_wait();
-  }
-  tc_fence_before();
-  __syncwarp();
-  if (lane == 0) mbar_arrive_pair(tempty0);
-  if (!any || dead) return;
+    hand_back();
+    if (dead) return;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (nrow > 16 * i)
-      w4g_store<kMode>(a, (i < 2 ? v0 : v1) + 16 * (i & 1), cm, st, fac + 16 * i, row0 + 16 * i, min(nrow - 16 * i, 16), c0,
-                       lane);
+    for (int i = 0; i < 4; ++i)
+      if (nrow > 16 * i)
+        w4g_store32<kMode>(a, (i < 2 ? v0 : v1) + 16 * (i & 1), f.cm, st, fac + 16 * i, row0 + 16 * i,
+                           min(nrow - 16 * i, 16), c0, lane);
+  }
 }
 
 template <int kMode>
@@ -426,7 +474,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     s_abort = 0;
     mbar_fence_init();
   }
-  if (warp == 1) {
+  if (warp == kGWorkers + 1) {
     tmem_alloc_pair(&s_tmem, kGTmemCols);
     tmem_relinquish_pair();
   }
@@ -468,7 +516,8 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     dead = __any_sync(MOE_FULL_MASK, !ok);
   };
 
-  if (warp == 0) {
+  if (warp >= kGWorkers) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGHelperRegs));
+  if (warp == kGWorkers) {
     uint32_t vi = 0;  // visits issued
     const bool lead = elect_one();
     for (int t = cl; t < total && !dead; t += ncl) {
@@ -538,7 +587,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     }
     if (dead)
       for (uint32_t j = wi > kGWRing ? wi - kGWRing : 0; j < wi; ++j) mbar_wait(&wfull[j % kGWRing], (j / kGWRing) & 1u);
-  } else if (warp == 1) {
+  } else if (warp == kGWorkers + 1) {
     if (rank == 0) {
       const uint64_t bd0 = smem_desc_l(smem_u32(xs), 16, 1024, kLayoutSw128);
       const bool lead = elect_one();
@@ -567,19 +616,20 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
       __syncwarp();
     }
     mbar_wait(done, 0);
-  } else {
-    const int q = warp & 3, set = (warp - 2) >> 2;  // TMEM lane quarter; visits (dequantising) and rows (draining)
+  } else if (warp < kGWorkers) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGWorkerRegs));
+    const int q = warp & 3, set = warp >> 2;  // TMEM lane quarter; visits (dequantising) and rows (draining)
     const int r = 32 * q + lane, g = r & 7, hi = (r >> 3) & 1;
     const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
     const uint32_t a_addr = lane_addr + kGACol + set * 64;
-    float* st = epi + (warp - 2) * (kGEpiBytes / 4);
-    float* fac = facs + (warp - 2) * 128;
+    float* st = epi + warp * (kGEpiBytes / 4);
+    float* fac = facs + warp * 128;
     const uint32_t full0 = mapa_shared(smem_u32(&full[set]), 0), tempty0 = mapa_shared(smem_u32(tempty), 0);
     uint32_t vi = 0, wi = 0, tc = 0;  // visits and chunks before this tile, tiles drained
     uint32_t uses = 0;                // this set's visits
     W4GTile prev = {};
     bool pending = false;  // prev has not been drained
-    float cm = 0.f;
+    W4GFactors f = {};
     for (int t = cl;; t += ncl) {
       const bool real = t < total && !dead;
       W4GTile ti = {};
@@ -629,7 +679,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
           ++uses;
         }
         if (phase == 0 && pending) {
-          w4g_drain<kMode>(a, prev, 2 * prev.ft + (int)rank, lane_addr, q, set, lane, st, fac, cm, tfull, tempty0, tc & 1u,
+          w4g_drain<kMode>(a, prev, 2 * prev.ft + (int)rank, lane_addr, q, set, lane, st, fac, f, tfull, tempty0, tc & 1u,
                            wait, dead);
           ++tc;
         }
@@ -637,7 +687,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
       if (!real) break;
       prev = ti;
       pending = true;
-      cm = w4g_factors<kMode>(a, ti, 2 * ti.ft + (int)rank, q, set, lane, fac);
+      f = w4g_factors<kMode>(a, ti, 2 * ti.ft + (int)rank, q, set, lane);
       vi += (nkb + kGVisit - 1) / kGVisit;
       wi += (nkb + kGChunk - 1) / kGChunk;
     }
@@ -647,7 +697,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   __syncwarp();
   tc_fence_before();
   cluster_sync();
-  if (warp == 1) {
+  if (warp == kGWorkers + 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kGTmemCols);
   }
