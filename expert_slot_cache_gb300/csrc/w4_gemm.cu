@@ -41,25 +41,23 @@ constexpr int kGM = 128;       // packed columns per CTA
 constexpr int kGN = 256;       // rows per tile
 constexpr int kGRows = 128;    // of them in one CTA's shared memory, at most
 constexpr int kGK = 64;        // inputs per stage
-constexpr int kGChunk = 4;     // stages of codes that are copied together
-constexpr int kGWRing = 2;     // chunks of codes in shared memory
-constexpr int kGVisit = 2;     // stages that a worker dequantises, and the MMA warp issues, at a time
+constexpr int kGVisit = 2;     // stages that are copied, dequantised and multiplied at a time
 constexpr int kGSets = 4;      // sets of four worker warps, taking visits in turn; visits of rows in shared memory
+constexpr int kGWRing = 6;     // visits of codes in shared memory: four in the workers' hands, two on their way
 constexpr int kGWorkers = 4 * kGSets;
 constexpr int kGThreads = 128 + 32 * kGWorkers;  // the workers, then four warps (one idle): whole warpgroups
 // Registers per thread after the split: what is live while 64 accumulators per lane are drained needs more than
 // the 96 of an even split.  512 x 112 + 128 x 32 = 640 x 96.
 constexpr int kGWorkerRegs = 112, kGHelperRegs = 32;
 constexpr int kGXBytes = kGRows * kGK * 2;      // a stage's rows
-constexpr int kGCodeBytes = kGChunk * 4096;     // a chunk's codes of 128 columns
-constexpr int kGScaleBytes = kGChunk * 2 * 256; // its fp16 scales (two groups a stage at most)
+constexpr int kGCodeBytes = kGVisit * 4096;     // a visit's codes of 128 columns
+constexpr int kGScaleBytes = kGVisit * 2 * 256; // its fp16 scales (two groups a stage at most)
 constexpr int kGWBytes = kGCodeBytes + kGScaleBytes;
 constexpr int kGEpiRows = 16;                   // rows that a worker warp stores at a time
 constexpr int kGLd = 36;                        // staging: floats per row of 32 (padded against bank conflicts)
 constexpr int kGEpiBytes = kGEpiRows * kGLd * 4;  // per worker warp
 constexpr uint32_t kGTmemCols = 512;
 constexpr uint32_t kGACol = kGN;                // first weight column
-static_assert(kGChunk == 2 * kGVisit, "a chunk is two visits, of different sets");
 static_assert(kGN == 64 * kGSets, "each set drains 64 rows");
 
 enum { kGateUp = 0, kDown = 1, kLinear = 2 };
@@ -148,10 +146,6 @@ __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
       : "r"(smem_u32(bar)), "r"(parity), "n"(kGPolls)
       : "memory");
   return ok != 0;
-}
-
-__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
 
 // 2^e >= 1.001 |column|_2 of every column (0 for a matrix of zeros or a norm that is not finite).
@@ -254,93 +248,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-// 16 rows x 32 packed columns of a warp, as 16-bit values times the column's power of two (v[row pair], a
-// column per lane), through shared memory (st) to their place.  fac[row] is the row's power of two.
-template <int kMode>
-__device__ __forceinline__ void w4g_store16(const W4GemmArgs& a, const uint32_t* v, uint32_t* st, const float* fac,
-                                            size_t row0, int nrow, int c0, int lane) {
-  const W4Dims& d = a.d;
-  const size_t ld = kMode == kLinear ? a.ldo : (size_t)d.N;
-#pragma unroll
-  for (int j = 0; j < kGEpiRows / 2; ++j) st[j * kGLd + lane] = v[j];
-  __syncwarp();
-  uint16_t* out = kMode == kLinear ? reinterpret_cast<uint16_t*>(a.out) : a.yh;
-  auto scaled = [](uint32_t w, float m) {
-    const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), __float2bfloat162_rn(m));
-    return *reinterpret_cast<const uint32_t*>(&p);
-  };
-  if (kMode == kLinear && !(ld % 8 == 0 && (uintptr_t)a.out % 16 == 0 && c0 + 32 <= d.N)) {
-    // unaligned or ragged rows of out: element stores, 32 consecutive columns per row
-    if (c0 + lane < d.N)
-      for (int j = 0; j < nrow; ++j) {
-        const uint32_t w = scaled(st[j / 2 * kGLd + lane], fac[j]);
-        out[(row0 + j) * ld + c0 + lane] = uint16_t(j & 1 ? w >> 16 : w);
-      }
-  } else {
-    const int rp = lane >> 2, seg = (lane & 3) * 8;  // 8 row pairs x 4 runs of 8 columns
-    const uint4 w0 = *reinterpret_cast<const uint4*>(st + rp * kGLd + seg);
-    const uint4 w1 = *reinterpret_cast<const uint4*>(st + rp * kGLd + seg + 4);
-    const float2 f = *reinterpret_cast<const float2*>(fac + 2 * rp);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t sel = h ? 0x7632 : 0x5410;
-      uint32_t o[4] = {__byte_perm(w0.x, w0.y, sel), __byte_perm(w0.z, w0.w, sel), __byte_perm(w1.x, w1.y, sel),
-                       __byte_perm(w1.z, w1.w, sel)};
-      if (kMode == kLinear)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = scaled(o[j], h ? f.y : f.x);
-      if (2 * rp + h < nrow)
-        *reinterpret_cast<uint4*>(out + (row0 + 2 * rp + h) * ld + c0 + seg) = make_uint4(o[0], o[1], o[2], o[3]);
-    }
-  }
-  __syncwarp();
-}
-
-// The same of fp32 values (v[row], without the column's power of two cm): to fp32 results, or (kGateUp) to h, with
-// fac[64 + row] the power of two of 1 / h.
-template <int kMode>
-__device__ __forceinline__ void w4g_store32(const W4GemmArgs& a, const float* v, float cm, float* st, const float* fac,
-                                            size_t row0, int nrow, int c0, int lane) {
-  const W4Dims& d = a.d;
-#pragma unroll
-  for (int j = 0; j < kGEpiRows; ++j) st[j * kGLd + lane] = v[j] * cm;
-  __syncwarp();
-  if (kMode == kGateUp) {  // columns 0-15: gate, 16-31: up of the same 16 features
-    const int f0 = c0 / 2, I = d.N / 2, row = lane >> 1, seg = (lane & 1) * 8;
-    const float x = fac[row], xh = x * fac[64 + row];
-    uint32_t o[4];
-#pragma unroll
-    for (int j = 0; j < 8; j += 4) {
-      const float4 g = *reinterpret_cast<const float4*>(st + row * kGLd + seg + j);
-      const float4 u = *reinterpret_cast<const float4*>(st + row * kGLd + 16 + seg + j);
-      auto h = [&](float gv, float uv) {
-        gv *= x;
-        return __fdividef(gv, 1.f + __expf(-gv)) * (uv * xh);
-      };
-      o[j / 2] = pack_f16(h(g.x, u.x), h(g.y, u.y));
-      o[j / 2 + 1] = pack_f16(h(g.z, u.z), h(g.w, u.w));
-    }
-    if (row < nrow) *reinterpret_cast<uint4*>(a.h + (row0 + row) * I + f0 + seg) = make_uint4(o[0], o[1], o[2], o[3]);
-  } else {
-    float* out = kMode == kLinear ? reinterpret_cast<float*>(a.out) : a.y;
-    const size_t ld = kMode == kLinear ? a.ldo : (size_t)d.N;
-    if (kMode == kLinear && !(ld % 4 == 0 && (uintptr_t)a.out % 16 == 0 && c0 + 32 <= d.N)) {
-      if (c0 + lane < d.N)
-        for (int row = 0; row < nrow; ++row) out[(row0 + row) * ld + c0 + lane] = st[row * kGLd + lane] * fac[row];
-    } else {
-#pragma unroll
-      for (int i = 0; i < kGEpiRows / 4; ++i) {  // rows of 128 B
-        const int idx = i * 32 + lane, row = idx >> 3, seg = (idx & 7) * 4;
-        float4 o = *reinterpret_cast<const float4*>(st + row * kGLd + seg);
-        const float m = fac[row];
-        o.x *= m, o.y *= m, o.z *= m, o.w *= m;
-        if (row < nrow) *reinterpret_cast<float4*>(out + (row0 + row) * ld + c0 + seg) = o;
-      }
-    }
-  }
-  __syncwarp();
-}
-
 // What the drain of 64 rows (of set `set`) multiplies with: the rows' exponents (two rows a lane) and the
 // lane's column's power of two.  Loaded a visit before they are needed.
 struct W4GFactors {
@@ -367,23 +274,112 @@ __device__ __forceinline__ W4GFactors w4g_factors(const W4GemmArgs& a, const W4G
   return f;
 }
 
+// 16 rows x 32 packed columns of a warp, as 16-bit values times the column's power of two (v[row pair], a
+// column per lane), through shared memory (st) to their place: the rows 16 i, ... of the 64 of f.
+template <int kMode>
+__device__ __forceinline__ void w4g_store16(const W4GemmArgs& a, const uint32_t* v, uint32_t* st, const W4GFactors& f,
+                                            int i, size_t row0, int nrow, int c0, int lane) {
+  const W4Dims& d = a.d;
+  const size_t ld = kMode == kLinear ? a.ldo : (size_t)d.N;
+#pragma unroll
+  for (int j = 0; j < kGEpiRows / 2; ++j) st[j * kGLd + lane] = v[j];
+  __syncwarp();
+  uint16_t* out = kMode == kLinear ? reinterpret_cast<uint16_t*>(a.out) : a.yh;
+  auto row_fac = [&](int row) { return pow2(__shfl_sync(MOE_FULL_MASK, f.r[i >> 1], 16 * (i & 1) + row)); };
+  auto scaled = [](uint32_t w, float m) {
+    const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), __float2bfloat162_rn(m));
+    return *reinterpret_cast<const uint32_t*>(&p);
+  };
+  if (kMode == kLinear && !(ld % 8 == 0 && (uintptr_t)a.out % 16 == 0 && c0 + 32 <= d.N)) {
+    // unaligned or ragged rows of out: element stores, 32 consecutive columns per row
+    for (int j = 0; j < nrow; ++j) {
+      const float m = row_fac(j);
+      if (c0 + lane < d.N) {
+        const uint32_t w = scaled(st[j / 2 * kGLd + lane], m);
+        out[(row0 + j) * ld + c0 + lane] = uint16_t(j & 1 ? w >> 16 : w);
+      }
+    }
+  } else {
+    const int rp = lane >> 2, seg = (lane & 3) * 8;  // 8 row pairs x 4 runs of 8 columns
+    const uint4 w0 = *reinterpret_cast<const uint4*>(st + rp * kGLd + seg);
+    const uint4 w1 = *reinterpret_cast<const uint4*>(st + rp * kGLd + seg + 4);
+    float m[2] = {1.f, 1.f};
+    if (kMode == kLinear) m[0] = row_fac(2 * rp), m[1] = row_fac(2 * rp + 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t sel = h ? 0x7632 : 0x5410;
+      uint32_t o[4] = {__byte_perm(w0.x, w0.y, sel), __byte_perm(w0.z, w0.w, sel), __byte_perm(w1.x, w1.y, sel),
+                       __byte_perm(w1.z, w1.w, sel)};
+      if (kMode == kLinear)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = scaled(o[j], m[h]);
+      if (2 * rp + h < nrow)
+        *reinterpret_cast<uint4*>(out + (row0 + 2 * rp + h) * ld + c0 + seg) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  __syncwarp();
+}
+
+// The same of fp32 values (v[row], without the column's power of two): to fp32 results, or (kGateUp) to h.
+template <int kMode>
+__device__ __forceinline__ void w4g_store32(const W4GemmArgs& a, const float* v, float* st, const W4GFactors& f, int i,
+                                            size_t row0, int nrow, int c0, int lane) {
+  const W4Dims& d = a.d;
+  auto row_fac = [&](int row) { return pow2(__shfl_sync(MOE_FULL_MASK, f.r[i >> 1], 16 * (i & 1) + row)); };
+#pragma unroll
+  for (int j = 0; j < kGEpiRows; ++j) st[j * kGLd + lane] = v[j] * f.cm;
+  __syncwarp();
+  if (kMode == kGateUp) {  // columns 0-15: gate, 16-31: up of the same 16 features
+    const int f0 = c0 / 2, I = d.N / 2, row = lane >> 1, seg = (lane & 1) * 8;
+    const float x = row_fac(row),
+                xh = x * pow2(-__shfl_sync(MOE_FULL_MASK, f.o[i >> 1], 16 * (i & 1) + row));
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 8; j += 4) {
+      const float4 g = *reinterpret_cast<const float4*>(st + row * kGLd + seg + j);
+      const float4 u = *reinterpret_cast<const float4*>(st + row * kGLd + 16 + seg + j);
+      auto h = [&](float gv, float uv) {
+        gv *= x;
+        return __fdividef(gv, 1.f + __expf(-gv)) * (uv * xh);
+      };
+      o[j / 2] = pack_f16(h(g.x, u.x), h(g.y, u.y));
+      o[j / 2 + 1] = pack_f16(h(g.z, u.z), h(g.w, u.w));
+    }
+    if (row < nrow) *reinterpret_cast<uint4*>(a.h + (row0 + row) * I + f0 + seg) = make_uint4(o[0], o[1], o[2], o[3]);
+  } else {
+    float* out = kMode == kLinear ? reinterpret_cast<float*>(a.out) : a.y;
+    const size_t ld = kMode == kLinear ? a.ldo : (size_t)d.N;
+    if (kMode == kLinear && !(ld % 4 == 0 && (uintptr_t)a.out % 16 == 0 && c0 + 32 <= d.N)) {
+      for (int row = 0; row < nrow; ++row) {
+        const float m = row_fac(row);
+        if (c0 + lane < d.N) out[(row0 + row) * ld + c0 + lane] = st[row * kGLd + lane] * m;
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < kGEpiRows / 4; ++n) {  // rows of 128 B
+        const int idx = n * 32 + lane, row = idx >> 3, seg = (idx & 7) * 4;
+        float4 o = *reinterpret_cast<const float4*>(st + row * kGLd + seg);
+        const float m = row_fac(row);
+        o.x *= m, o.y *= m, o.z *= m, o.w *= m;
+        if (row < nrow) *reinterpret_cast<float4*>(out + (row0 + row) * ld + c0 + seg) = o;
+      }
+    }
+  }
+  __syncwarp();
+}
+
 // Drains 64 rows (of set `set`) x this warp's 32 columns: to registers, the accumulators are handed back
 // (tempty of the pair's first CTA), then 16 rows at a time through shared memory to their place.  16-bit results
 // are rounded on their way to the registers, which takes half as many.
 template <int kMode, class Wait>
 __device__ __forceinline__ void w4g_drain(const W4GemmArgs& a, const W4GTile& ti, int blk, uint32_t taddr, int q, int set,
-                                          int lane, float* st, float* fac, const W4GFactors& f, uint64_t* tfull,
+                                          int lane, float* st, const W4GFactors& f, uint64_t* tfull,
                                           uint32_t tempty0, uint32_t parity, Wait&& wait, const bool& dead) {
   const W4Dims& d = a.d;
   const int tok0 = 64 * set, nrow = ti.ntok - tok0, c0 = blk * kGM + 32 * q;
   const bool any = nrow > 0 && c0 < d.N;
   const bool half = kMode != kGateUp && (kMode == kLinear ? !a.out_f32 : a.yh != nullptr);
   const size_t row0 = (size_t)ti.row0 + tok0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    fac[32 * i + lane] = pow2(f.r[i]);
-    if (kMode == kGateUp) fac[64 + 32 * i + lane] = pow2(-f.o[i]);
-  }
   __syncwarp();
   wait(tfull, parity);
   tc_fence_after();
@@ -414,7 +410,7 @@ __device__ __forceinline__ void w4g_drain(const W4GemmArgs& a, const W4GTile& ti
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (nrow > 16 * i)
-        w4g_store16<kMode>(a, v + 8 * i, reinterpret_cast<uint32_t*>(st), fac + 16 * i, row0 + 16 * i,
+        w4g_store16<kMode>(a, v + 8 * i, reinterpret_cast<uint32_t*>(st), f, i, row0 + 16 * i,
                            min(nrow - 16 * i, 16), c0, lane);
   } else {
     float v0[32], v1[32];
@@ -426,7 +422,7 @@ __device__ __forceinline__ void w4g_drain(const W4GemmArgs& a, const W4GTile& ti
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (nrow > 16 * i)
-        w4g_store32<kMode>(a, (i < 2 ? v0 : v1) + 16 * (i & 1), f.cm, st, fac + 16 * i, row0 + 16 * i,
+        w4g_store32<kMode>(a, (i < 2 ? v0 : v1) + 16 * (i & 1), st, f, i, row0 + 16 * i,
                            min(nrow - 16 * i, 16), c0, lane);
   }
 }
@@ -438,10 +434,9 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   unsigned char* xs = sm;                             // [ring][stages of a visit][16 KB]
   unsigned char* wsm = sm + kGSets * kGVisit * kGXBytes;  // [ring][codes | scales]
   float* epi = reinterpret_cast<float*>(wsm + kGWRing * kGWBytes);   // [workers][kGEpiRows][kGLd]
-  float* facs = epi + kGWorkers * (kGEpiBytes / 4);   // [workers][128]
   // of a visit: its rows have landed and its weights are in TMEM, in both CTAs (the first one's barrier counts);
   // its MMAs have read both
-  uint64_t* full = reinterpret_cast<uint64_t*>(facs + kGWorkers * 128);
+  uint64_t* full = reinterpret_cast<uint64_t*>(epi + kGWorkers * (kGEpiBytes / 4));
   uint64_t* empty = full + kGSets;
   uint64_t* wfull = empty + kGSets;
   uint64_t* wempty = wfull + kGWRing;
@@ -462,7 +457,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kGWRing; ++s) {
       mbar_init(&wfull[s], 1);
-      mbar_init(&wempty[s], 8);  // two visits of four warps
+      mbar_init(&wempty[s], 4);  // a set's four warps
     }
     for (int s = 0; s < kGSets; ++s) {
       mbar_init(&full[s], 9);  // a set's four warps in each CTA, and the bytes
@@ -560,14 +555,14 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
         for (int i = 0; i < 1024 && !mbar_poll(&full[j % kGSets], (j / kGSets) & 1u); ++i) {
         }
   } else if (warp == kGWorkers + 2) {
-    uint32_t wi = 0;  // chunks issued
+    uint32_t wi = 0;  // visits issued
     const bool lead = elect_one();
     for (int t = cl; t < total && !dead; t += ncl) {
       const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
       const int blk = 2 * ti.ft + (int)rank;
       const uint32_t nm = max(0, min(8, d.Mt - 8 * blk));  // the tiles of 16 columns that exist
-      for (int kb = 0; kb < nkb; kb += kGChunk, ++wi) {
-        const uint32_t s = wi % kGWRing, use = wi / kGWRing, nb = min(kGChunk, nkb - kb);
+      for (int kb = 0; kb < nkb; kb += kGVisit, ++wi) {
+        const uint32_t s = wi % kGWRing, use = wi / kGWRing, nb = min(kGVisit, nkb - kb);
         const uint32_t ng = d.G == 128 ? (nb + 1) / 2 : d.G == 64 ? nb : 2 * nb;
         if (use > 0) wait(&wempty[s], (use - 1) & 1u);
         if (dead) break;
@@ -623,9 +618,8 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
     const uint32_t a_addr = lane_addr + kGACol + set * 64;
     float* st = epi + warp * (kGEpiBytes / 4);
-    float* fac = facs + warp * 128;
     const uint32_t full0 = mapa_shared(smem_u32(&full[set]), 0), tempty0 = mapa_shared(smem_u32(tempty), 0);
-    uint32_t vi = 0, wi = 0, tc = 0;  // visits and chunks before this tile, tiles drained
+    uint32_t vi = 0, tc = 0;          // visits before this tile, tiles drained
     uint32_t uses = 0;                // this set's visits
     W4GTile prev = {};
     bool pending = false;  // prev has not been drained
@@ -643,17 +637,15 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
         const int end = phase ? nk : min(nk, (kGSets - 1) * kGVisit);
 #pragma unroll 1
         for (; kb < end; kb += kGSets * kGVisit) {
-          // a chunk of codes holds two visits; a tile starts a chunk of its own
-          const uint32_t c = wi + kb / kGChunk, ws = c % kGWRing;
-          wait(&wfull[ws], (c / kGWRing) & 1u);
+          const uint32_t v = vi + kb / kGVisit, ws = v % kGWRing;
+          wait(&wfull[ws], (v / kGWRing) & 1u);
           const unsigned char* wst = wsm + ws * kGWBytes;
           uint32_t o[32];
 #pragma unroll
           for (int h = 0; h < kGVisit; ++h) {
             if (kb + h >= nkb) break;
-            const int j4 = kb % kGChunk + h;
-            const unsigned char* code = wst + (j4 * nm + (r >> 4)) * 512 + g * 64 + hi * 8;
-            const int gi = d.G == 128 ? j4 >> 1 : d.G == 64 ? j4 : 2 * j4;
+            const unsigned char* code = wst + (h * nm + (r >> 4)) * 512 + g * 64 + hi * 8;
+            const int gi = d.G == 128 ? 0 : d.G == 64 ? h : 2 * h;
             const __half* sp = reinterpret_cast<const __half*>(wst + kGCodeBytes + (gi * nm * 8 + g * nm + (r >> 4)) * 4) + hi;
             uint2 w[4];
 #pragma unroll
@@ -673,13 +665,12 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
           __syncwarp();
           if (lane == 0) {
             mbar_arrive_pair(full0);
-            // a last chunk of one visit counts it twice
-            mbar_arrive_n(&wempty[ws], kb % kGChunk == 0 && kb + kGVisit >= nkb ? 2 : 1);
+            mbar_arrive(&wempty[ws]);
           }
           ++uses;
         }
         if (phase == 0 && pending) {
-          w4g_drain<kMode>(a, prev, 2 * prev.ft + (int)rank, lane_addr, q, set, lane, st, fac, f, tfull, tempty0, tc & 1u,
+          w4g_drain<kMode>(a, prev, 2 * prev.ft + (int)rank, lane_addr, q, set, lane, st, f, tfull, tempty0, tc & 1u,
                            wait, dead);
           ++tc;
         }
@@ -689,7 +680,6 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
       pending = true;
       f = w4g_factors<kMode>(a, ti, 2 * ti.ft + (int)rank, q, set, lane);
       vi += (nkb + kGVisit - 1) / kGVisit;
-      wi += (nkb + kGChunk - 1) / kGChunk;
     }
   }
   // reconverge before the cluster barrier, which also keeps each CTA's shared memory alive while its peer
@@ -846,7 +836,7 @@ __global__ void __launch_bounds__(128) w4_combine_kernel(const uint16_t* __restr
 }
 
 constexpr size_t kGSmem = 1024 + (size_t)kGSets * kGVisit * kGXBytes + (size_t)kGWRing * kGWBytes +
-                          (size_t)kGWorkers * (kGEpiBytes + 128 * 4) + 64 * sizeof(uint64_t);
+                          (size_t)kGWorkers * kGEpiBytes + 64 * sizeof(uint64_t);
 static_assert(kGSmem <= 222 * 1024, "shared memory of a CTA, with the 4.3 KB of static arrays");
 
 // [n][K] 16-bit rows; boxes of 128, 64, 32 and 16 rows x one stage (what lies outside reads as 0).
