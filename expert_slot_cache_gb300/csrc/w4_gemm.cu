@@ -473,6 +473,8 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     tmem_alloc_pair(&s_tmem, kGTmemCols);
     tmem_relinquish_pair();
   }
+  // (the kernels before this one trigger after their own waits: the grouping of the rows, which is older than
+  // the kernel before, may be read already)
   if (kMode == kLinear) {
     total = (a.n + kGN - 1) / kGN * a.NF;
   } else {
@@ -494,6 +496,8 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   __syncwarp();
   tc_fence_before();
   cluster_sync();  // barriers of both CTAs initialised, TMEM allocated on both, prefix complete
+  pdl_wait();
+  pdl_trigger();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* abort_flag = &s_abort;
@@ -714,52 +718,72 @@ struct W4RowArgs {
   float* y;                // rows of experts without a slot are zeroed, or NULL (yexp says so)
 };
 
-// One row: returns its exponent and ceil(log2 |x'|^2) (x' = the scaled row).
+// One row: its exponent and, with kNorm, ceil(log2 |x'|^2) (x' = the scaled row).  The row is read once, all of it
+// in flight at a time, up to 256 NC inputs; what is beyond them is read again.
+template <int NC, bool kNorm>
 __device__ __forceinline__ void w4_scale_row(const uint16_t* x, uint16_t* xp, int K, int lane, int& xe, int& ln) {
-  float amax = 0.f;
-  auto take = [&](uint32_t v) {
-    const float lo = fabsf(bf16_lo(v)), hi = fabsf(bf16_hi(v));
-    amax = fmaxf(amax, lo < INFINITY ? lo : 0.f);  // infinities and NaN do not set the scale
-    amax = fmaxf(amax, hi < INFINITY ? hi : 0.f);
-  };
-  for (int c = lane; c < K / 8; c += 32) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(x) + c);
-    take(v.x), take(v.y), take(v.z), take(v.w);
-  }
+  const uint4* xv = reinterpret_cast<const uint4*>(x);
+  uint4 v[NC];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(MOE_FULL_MASK, amax, o));
-  xe = amax > 0.f ? max(ilogbf(amax) - 14, -126) : 0;
+  for (int i = 0; i < NC; ++i) v[i] = 32 * i + lane < K / 8 ? __ldg(xv + 32 * i + lane) : make_uint4(0, 0, 0, 0);
+  uint32_t amax = 0;  // of the bits: bf16 magnitudes are ordered like integers
+  auto take = [&](uint32_t u) {
+    const uint32_t lo = u & 0x7fffu, hi = (u >> 16) & 0x7fffu;
+    amax = max(amax, lo < 0x7f80u ? lo : 0u);  // infinities and NaN do not set the scale
+    amax = max(amax, hi < 0x7f80u ? hi : 0u);
+  };
+#pragma unroll
+  for (int i = 0; i < NC; ++i) take(v[i].x), take(v[i].y), take(v[i].z), take(v[i].w);
+  for (int c = 32 * NC + lane; c < K / 8; c += 32) {
+    const uint4 u = __ldg(xv + c);
+    take(u.x), take(u.y), take(u.z), take(u.w);
+  }
+  amax = __reduce_max_sync(MOE_FULL_MASK, amax);
+  xe = amax ? max(ilogbf(__uint_as_float(amax << 16)) - 14, -126) : 0;
   const float f0 = ldexpf(1.f, -xe / 2), f1 = ldexpf(1.f, -xe - (-xe / 2));  // 2^-xe may overflow by itself
   float nrm = 0.f;
-  auto conv = [&](uint32_t v) {
-    const float lo = bf16_lo(v) * f0 * f1, hi = bf16_hi(v) * f0 * f1;
-    nrm += fabsf(lo) < INFINITY ? lo * lo : 0.f;
-    nrm += fabsf(hi) < INFINITY ? hi * hi : 0.f;
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
+  auto conv = [&](uint32_t u) {
+    const float lo = bf16_lo(u) * f0 * f1, hi = bf16_hi(u) * f0 * f1;
+    if (kNorm) {
+      nrm += fabsf(lo) < INFINITY ? lo * lo : 0.f;
+      nrm += fabsf(hi) < INFINITY ? hi * hi : 0.f;
+    }
+    return pack_f16(lo, hi);
   };
-  for (int c = lane; c < K / 8; c += 32) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(x) + c);
-    reinterpret_cast<uint4*>(xp)[c] = make_uint4(conv(v.x), conv(v.y), conv(v.z), conv(v.w));
-  }
+  uint4* xo = reinterpret_cast<uint4*>(xp);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) nrm += __shfl_xor_sync(MOE_FULL_MASK, nrm, o);
-  ln = nrm > 0.f ? ilogbf(nrm * 1.001f) + 1 : 0;
+  for (int i = 0; i < NC; ++i)
+    if (32 * i + lane < K / 8) xo[32 * i + lane] = make_uint4(conv(v[i].x), conv(v[i].y), conv(v[i].z), conv(v[i].w));
+  for (int c = 32 * NC + lane; c < K / 8; c += 32) {
+    const uint4 u = __ldg(xv + c);
+    xo[c] = make_uint4(conv(u.x), conv(u.y), conv(u.z), conv(u.w));
+  }
+  if (kNorm) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) nrm += __shfl_xor_sync(MOE_FULL_MASK, nrm, o);
+    ln = nrm > 0.f ? ilogbf(nrm * 1.001f) + 1 : 0;
+  }
 }
 
+template <int NC>
 __global__ void __launch_bounds__(kRowThreads) w4_rows_kernel(const W4RowArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = gridDim.x * (kRowThreads / 32);
+  pdl_wait();
+  pdl_trigger();
   for (int p = blockIdx.x * (kRowThreads / 32) + warp; p < a.n; p += nw) {
     int xe, ln;
-    w4_scale_row(a.x + (size_t)p * a.ldx, a.xp + (size_t)p * a.K, a.K, lane, xe, ln);
+    w4_scale_row<NC, false>(a.x + (size_t)p * a.ldx, a.xp + (size_t)p * a.K, a.K, lane, xe, ln);
     if (lane == 0) a.xexp[p] = xe;
   }
 }
 
+template <int NC>
 __global__ void __launch_bounds__(kRowThreads) w4_group_rows_kernel(const W4RowArgs a) {
   __shared__ int s_pre[kMaxE + 1];
   __shared__ int s_tmp[33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = gridDim.x * (kRowThreads / 32);
+  pdl_wait();
+  pdl_trigger();
   const int nl = min(*a.g.n_list, kMaxE);
   int carry = 0;
   for (int l0 = 0; l0 < nl; l0 += kRowThreads) {
@@ -793,7 +817,7 @@ __global__ void __launch_bounds__(kRowThreads) w4_group_rows_kernel(const W4RowA
       continue;
     }
     int xe, ln;
-    w4_scale_row(a.x + (size_t)(a.rows[p] / a.k) * a.ldx, a.xp + (size_t)p * a.K, a.K, lane, xe, ln);
+    w4_scale_row<NC, true>(a.x + (size_t)(a.rows[p] / a.k) * a.ldx, a.xp + (size_t)p * a.K, a.K, lane, xe, ln);
     if (lane == 0) {
       const uint8_t* base = a.g.w + (size_t)slot * a.g.slab;
       // |h| <= |g| |u| <= |x|^2 |Wg| |Wu|; h 2^-hexp stays below 2^15
@@ -812,21 +836,32 @@ __global__ void __launch_bounds__(128) w4_combine_kernel(const uint16_t* __restr
                                                          const float* __restrict__ w, const int32_t* __restrict__ pos,
                                                          int k, int H, uint16_t* __restrict__ out) {
   const int t = blockIdx.x, c = (blockIdx.y * 128 + threadIdx.x) * 8;
+  pdl_wait();
   if (c >= H) return;
   float acc[8] = {};
-  for (int j = 0; j < k; ++j) {
-    const int p = pos[(size_t)t * k + j];
-    if (p < 0) continue;
-    const int e = yexp[p];
-    if (e == kNoRow) continue;
-    const uint4 v = *reinterpret_cast<const uint4*>(yh + (size_t)p * H + c);
-    const float wj = ldexpf(w[(size_t)t * k + j], e / 2), m = ldexpf(1.f, e - e / 2);  // 2^e may overflow by itself
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  for (int j0 = 0; j0 < k; j0 += 4) {  // four rows in flight
+    int p[4], e[4];
+    float wj[4];
+    uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-      acc[2 * i] = fmaf(wj, f.x * m, acc[2 * i]);
-      acc[2 * i + 1] = fmaf(wj, f.y * m, acc[2 * i + 1]);
+    for (int j = 0; j < 4; ++j) p[j] = j0 + j < k ? pos[(size_t)t * k + j0 + j] : -1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      e[j] = p[j] >= 0 ? yexp[p[j]] : kNoRow;
+      wj[j] = p[j] >= 0 ? w[(size_t)t * k + j0 + j] : 0.f;
+      if (p[j] >= 0) v[j] = __ldcs(reinterpret_cast<const uint4*>(yh + (size_t)p[j] * H + c));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (e[j] == kNoRow) continue;
+      const float we = ldexpf(wj[j], e[j] / 2), m = ldexpf(1.f, e[j] - e[j] / 2);  // 2^e may overflow by itself
+      const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+        acc[2 * i] = fmaf(we, f.x * m, acc[2 * i]);
+        acc[2 * i + 1] = fmaf(we, f.y * m, acc[2 * i + 1]);
+      }
     }
   }
   uint32_t o[4];
@@ -861,17 +896,19 @@ static int launch_gemm(const W4GemmArgs& g, const void* rows, cudaStream_t s) {
   MOE_CUDA_TRY(cudaGetDevice(&dev));
   W4RowMaps m;
   if (row_maps(&m, rows, g.n, g.K) != MOE_OK) return MOE_ERR_CUDA;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kGThreads);
   cfg.dynamicSmemBytes = kGSmem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   if (clusters[dev] == 0) {
     int sms = 0, n = 0;
     MOE_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
@@ -895,8 +932,8 @@ int launch_w4_linear_gemm(const uint16_t* x, size_t ldx, int T, const uint8_t* w
   r.x = x, r.ldx = ldx, r.n = T, r.K = d.K;
   r.xp = (uint16_t*)ws;
   r.xexp = (int32_t*)((char*)ws + g256(2 * (size_t)T * d.K));
-  w4_rows_kernel<<<std::min((T + 7) / 8, 1216), kRowThreads, 0, s>>>(r);
-  MOE_LAUNCH_CHECK();
+  MOE_CUDA_TRY(launch_pdl(d.K <= 2048 ? w4_rows_kernel<8> : w4_rows_kernel<16>, dim3(std::min((T + 7) / 8, 1216)),
+                          dim3(kRowThreads), 0, s, r));
   W4GemmArgs g{};
   g.w = w, g.d = d, g.K = d.K, g.n = T;
   g.NF = (d.N + 2 * kGM - 1) / (2 * kGM);
@@ -937,8 +974,8 @@ int launch_ffn_w4_gemm(const FfnArgs& f, int group, void* ws, const uint16_t** y
   r.g = g, r.rows = f.rows, r.k = f.k, r.sl = sl;
   r.y = yh ? nullptr : f.y;
   if (prof) prof->begin(MOE_PROF_FFN_ROWS, s);
-  w4_group_rows_kernel<<<(int)std::min((n + 7) / 8, (size_t)1216), kRowThreads, 0, s>>>(r);
-  MOE_LAUNCH_CHECK();
+  MOE_CUDA_TRY(launch_pdl(f.H <= 2048 ? w4_group_rows_kernel<8> : w4_group_rows_kernel<16>,
+                          dim3((unsigned)std::min((n + 7) / 8, (size_t)1216)), dim3(kRowThreads), 0, s, r));
   if (prof) prof->end(s);
   if (prof) prof->begin(MOE_PROF_FFN_GATEUP, s);
   int rc = launch_gemm<kGateUp>(g, r.xp, s);
@@ -962,8 +999,8 @@ int launch_ffn_w4_gemm(const FfnArgs& f, int group, void* ws, const uint16_t** y
 
 int launch_w4_combine(const uint16_t* yh, const int32_t* yexp, const float* w, const int32_t* pos, int T, int k, int H,
                       void* out, cudaStream_t s) {
-  w4_combine_kernel<<<dim3(T, (H / 8 + 127) / 128), 128, 0, s>>>(yh, yexp, w, pos, k, H, (uint16_t*)out);
-  MOE_LAUNCH_CHECK();
+  MOE_CUDA_TRY(launch_pdl(w4_combine_kernel, dim3(T, (H / 8 + 127) / 128), dim3(128), 0, s, yh, yexp, w, pos, k, H,
+                          (uint16_t*)out));
   return MOE_OK;
 }
 
