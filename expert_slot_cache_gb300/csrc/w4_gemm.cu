@@ -45,10 +45,7 @@ constexpr int kGVisit = 2;     // stages that are copied, dequantised and multip
 constexpr int kGSets = 4;      // sets of four worker warps, taking visits in turn; visits of rows in shared memory
 constexpr int kGWRing = 6;     // visits of codes in shared memory: four in the workers' hands, two on their way
 constexpr int kGWorkers = 4 * kGSets;
-constexpr int kGThreads = 128 + 32 * kGWorkers;  // the workers, then four warps (one idle): whole warpgroups
-// Registers per thread after the split: what is live while 64 accumulators per lane are drained needs more than
-// the 96 of an even split.  512 x 112 + 128 x 32 = 640 x 96.
-constexpr int kGWorkerRegs = 112, kGHelperRegs = 32;
+constexpr int kGThreads = 96 + 32 * kGWorkers;
 constexpr int kGXBytes = kGRows * kGK * 2;      // a stage's rows
 constexpr int kGCodeBytes = kGVisit * 4096;     // a visit's codes of 128 columns
 constexpr int kGScaleBytes = kGVisit * 2 * 256; // its fp16 scales (two groups a stage at most)
@@ -473,8 +470,8 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     tmem_alloc_pair(&s_tmem, kGTmemCols);
     tmem_relinquish_pair();
   }
-  // (the kernels before this one trigger after their own waits: the grouping of the rows, which is older than
-  // the kernel before, may be read already)
+  pdl_wait();
+  pdl_trigger();
   if (kMode == kLinear) {
     total = (a.n + kGN - 1) / kGN * a.NF;
   } else {
@@ -496,8 +493,6 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   __syncwarp();
   tc_fence_before();
   cluster_sync();  // barriers of both CTAs initialised, TMEM allocated on both, prefix complete
-  pdl_wait();
-  pdl_trigger();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* abort_flag = &s_abort;
@@ -515,7 +510,6 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     dead = __any_sync(MOE_FULL_MASK, !ok);
   };
 
-  if (warp >= kGWorkers) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kGHelperRegs));
   if (warp == kGWorkers) {
     uint32_t vi = 0;  // visits issued
     const bool lead = elect_one();
@@ -616,7 +610,6 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     }
     mbar_wait(done, 0);
   } else if (warp < kGWorkers) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGWorkerRegs));
     const int q = warp & 3, set = warp >> 2;  // TMEM lane quarter; visits (dequantising) and rows (draining)
     const int r = 32 * q + lane, g = r & 7, hi = (r >> 3) & 1;
     const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
