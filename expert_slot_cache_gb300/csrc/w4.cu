@@ -638,7 +638,7 @@ int launch_ffn_w4(const FfnArgs& f, int group, void* ws, size_t ws_bytes, int ma
   const int n = f.T * f.k;
   if (ws_bytes < w4_ws_bytes(n, f.H, f.I)) return MOE_ERR_ALIGN;
   if (max_list <= 0) return MOE_OK;
-  if (w4_gemm_ffn(n)) return launch_ffn_w4_gemm(f, group, ws, nullptr, nullptr, stream, prof);
+  if (w4_gemm_ffn(n)) return launch_ffn_w4_gemm(f, nullptr, nullptr, group, ws, nullptr, nullptr, stream, prof);
   int sms = 0;
   const int r = w4_sms(&sms);
   if (r != MOE_OK) return r;
@@ -798,6 +798,6 @@ extern "C" int moe_experts_w4(const void* x, const int32_t* ids, const float* w,
   f.offset = ws.offset, f.rows = ws.rows, f.list_e = ws.act_e, f.n_list = ws.n_act;
   const uint16_t* yh = nullptr;
   const int32_t* yexp = nullptr;
-  if ((r = launch_ffn_w4_gemm(f, group, ws.ffn, &yh, &yexp, s, nullptr)) != MOE_OK) return r;
+  if ((r = launch_ffn_w4_gemm(f, ids, ws.pos, group, ws.ffn, &yh, &yexp, s, nullptr)) != MOE_OK) return r;
   return launch_w4_combine(yh, yexp, w, ws.pos, T, k, H, out, s);
 }

@@ -142,8 +142,8 @@ size_t w4_linear_gemm_ws(int T, int K);
 int launch_w4_linear_gemm(const uint16_t* x, size_t ldx, int T, const uint8_t* w, const W4Dims& d, void* out,
                           size_t ldo, int out_f32, void* ws, int32_t* status, cudaStream_t s);
 size_t w4_ffn_gemm_ws(size_t n, int H, int I, bool yh);
-int launch_ffn_w4_gemm(const FfnArgs& f, int group, void* ws, const uint16_t** yh, const int32_t** yexp,
-                       cudaStream_t s, Prof* prof);
+int launch_ffn_w4_gemm(const FfnArgs& f, const int32_t* ids, const int32_t* pos, int group, void* ws,
+                       const uint16_t** yh, const int32_t** yexp, cudaStream_t s, Prof* prof);
 int launch_w4_combine(const uint16_t* yh, const int32_t* yexp, const float* w, const int32_t* pos, int T, int k, int H,
                       void* out, cudaStream_t s);
 

@@ -693,70 +693,86 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
 // ---------------------------------------------------------------------------
 // Rows: x -> fp16 times a power of two per row, in grouped order; one warp per row.
 // ---------------------------------------------------------------------------
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 256, kTokenThreads = 128;
 constexpr int kNoRow = INT_MIN;  // yexp of a row whose expert has no slot
 
 struct W4RowArgs {
   const uint16_t* x;
   size_t ldx;
-  int n, K;
+  int n, K;                // rows of xp, or of x with ids and pos
   uint16_t* xp;            // fp16 [n][K]
   int32_t* xexp;           // [n]
   // grouped rows (list_e != NULL)
   W4GemmArgs g;
   const int32_t* rows;
+  const int32_t *ids, *pos;  // every slot is grouped: rows by token (w4_token_rows_kernel)
   int k;
   W4Slab sl;
   int32_t *hexp, *yexp;    // [n]
   float* y;                // rows of experts without a slot are zeroed, or NULL (yexp says so)
 };
 
-// One row: its exponent and, with kNorm, ceil(log2 |x'|^2) (x' = the scaled row).  The row is read once, all of it
-// in flight at a time, up to 256 NC inputs; what is beyond them is read again.
-template <int NC, bool kNorm>
-__device__ __forceinline__ void w4_scale_row(const uint16_t* x, uint16_t* xp, int K, int lane, int& xe, int& ln) {
-  const uint4* xv = reinterpret_cast<const uint4*>(x);
-  uint4 v[NC];
+// One row x of K inputs, its exponent and, with kNorm, ceil(log2 |x'|^2) (x' = the scaled row).  The row is read
+// once, all of it in flight at a time, up to 256 NC inputs; what is beyond them is read again.
+template <int NC>
+struct W4Row {
+  const uint4* x;
+  int K, lane, xe;
+  float f0, f1;
+  uint4 v[NC];  // scaled, after scale()
+
+  __device__ __forceinline__ uint32_t conv(uint32_t u) const { return pack_f16(bf16_lo(u) * f0 * f1, bf16_hi(u) * f0 * f1); }
+  __device__ __forceinline__ uint4 conv(uint4 u) const { return make_uint4(conv(u.x), conv(u.y), conv(u.z), conv(u.w)); }
+  __device__ __forceinline__ uint4 at(int c) const { return __ldg(x + c); }
+
+  template <bool kNorm>
+  __device__ __forceinline__ int scale(const uint16_t* row, int K_, int lane_) {
+    x = reinterpret_cast<const uint4*>(row), K = K_, lane = lane_;
 #pragma unroll
-  for (int i = 0; i < NC; ++i) v[i] = 32 * i + lane < K / 8 ? __ldg(xv + 32 * i + lane) : make_uint4(0, 0, 0, 0);
-  uint32_t amax = 0;  // of the bits: bf16 magnitudes are ordered like integers
-  auto take = [&](uint32_t u) {
-    const uint32_t lo = u & 0x7fffu, hi = (u >> 16) & 0x7fffu;
-    amax = max(amax, lo < 0x7f80u ? lo : 0u);  // infinities and NaN do not set the scale
-    amax = max(amax, hi < 0x7f80u ? hi : 0u);
-  };
+    for (int i = 0; i < NC; ++i) v[i] = 32 * i + lane < K / 8 ? at(32 * i + lane) : make_uint4(0, 0, 0, 0);
+    uint32_t amax = 0;  // of the bits: bf16 magnitudes are ordered like integers
+    auto take = [&](uint32_t u) {
+      const uint32_t lo = u & 0x7fffu, hi = (u >> 16) & 0x7fffu;
+      amax = max(amax, lo < 0x7f80u ? lo : 0u);  // infinities and NaN do not set the scale
+      amax = max(amax, hi < 0x7f80u ? hi : 0u);
+    };
 #pragma unroll
-  for (int i = 0; i < NC; ++i) take(v[i].x), take(v[i].y), take(v[i].z), take(v[i].w);
-  for (int c = 32 * NC + lane; c < K / 8; c += 32) {
-    const uint4 u = __ldg(xv + c);
-    take(u.x), take(u.y), take(u.z), take(u.w);
-  }
-  amax = __reduce_max_sync(MOE_FULL_MASK, amax);
-  xe = amax ? max(ilogbf(__uint_as_float(amax << 16)) - 14, -126) : 0;
-  const float f0 = ldexpf(1.f, -xe / 2), f1 = ldexpf(1.f, -xe - (-xe / 2));  // 2^-xe may overflow by itself
-  float nrm = 0.f;
-  auto conv = [&](uint32_t u) {
-    const float lo = bf16_lo(u) * f0 * f1, hi = bf16_hi(u) * f0 * f1;
-    if (kNorm) {
+    for (int i = 0; i < NC; ++i) take(v[i].x), take(v[i].y), take(v[i].z), take(v[i].w);
+    for (int c = 32 * NC + lane; c < K / 8; c += 32) {
+      const uint4 u = at(c);
+      take(u.x), take(u.y), take(u.z), take(u.w);
+    }
+    amax = __reduce_max_sync(MOE_FULL_MASK, amax);
+    xe = amax ? max(ilogbf(__uint_as_float(amax << 16)) - 14, -126) : 0;
+    f0 = ldexpf(1.f, -xe / 2), f1 = ldexpf(1.f, -xe - (-xe / 2));  // 2^-xe may overflow by itself
+    float nrm = 0.f;
+    auto square = [&](uint32_t u) {
+      const float lo = bf16_lo(u) * f0 * f1, hi = bf16_hi(u) * f0 * f1;
       nrm += fabsf(lo) < INFINITY ? lo * lo : 0.f;
       nrm += fabsf(hi) < INFINITY ? hi * hi : 0.f;
-    }
-    return pack_f16(lo, hi);
-  };
-  uint4* xo = reinterpret_cast<uint4*>(xp);
+    };
 #pragma unroll
-  for (int i = 0; i < NC; ++i)
-    if (32 * i + lane < K / 8) xo[32 * i + lane] = make_uint4(conv(v[i].x), conv(v[i].y), conv(v[i].z), conv(v[i].w));
-  for (int c = 32 * NC + lane; c < K / 8; c += 32) {
-    const uint4 u = __ldg(xv + c);
-    xo[c] = make_uint4(conv(u.x), conv(u.y), conv(u.z), conv(u.w));
-  }
-  if (kNorm) {
+    for (int i = 0; i < NC; ++i) {
+      if (kNorm) square(v[i].x), square(v[i].y), square(v[i].z), square(v[i].w);
+      v[i] = conv(v[i]);
+    }
+    if (!kNorm) return 0;
+    for (int c = 32 * NC + lane; c < K / 8; c += 32) {
+      const uint4 u = at(c);
+      square(u.x), square(u.y), square(u.z), square(u.w);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) nrm += __shfl_xor_sync(MOE_FULL_MASK, nrm, o);
-    ln = nrm > 0.f ? ilogbf(nrm * 1.001f) + 1 : 0;
+    return nrm > 0.f ? ilogbf(nrm * 1.001f) + 1 : 0;
   }
-}
+  __device__ __forceinline__ void store(uint16_t* row) const {
+    uint4* o = reinterpret_cast<uint4*>(row);
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (32 * i + lane < K / 8) o[32 * i + lane] = v[i];
+    for (int c = 32 * NC + lane; c < K / 8; c += 32) o[c] = conv(at(c));
+  }
+};
 
 template <int NC>
 __global__ void __launch_bounds__(kRowThreads) w4_rows_kernel(const W4RowArgs a) {
@@ -764,10 +780,22 @@ __global__ void __launch_bounds__(kRowThreads) w4_rows_kernel(const W4RowArgs a)
   pdl_wait();
   pdl_trigger();
   for (int p = blockIdx.x * (kRowThreads / 32) + warp; p < a.n; p += nw) {
-    int xe, ln;
-    w4_scale_row<NC, false>(a.x + (size_t)p * a.ldx, a.xp + (size_t)p * a.K, a.K, lane, xe, ln);
-    if (lane == 0) a.xexp[p] = xe;
+    W4Row<NC> r;
+    r.template scale<false>(a.x + (size_t)p * a.ldx, a.K, lane);
+    r.store(a.xp + (size_t)p * a.K);
+    if (lane == 0) a.xexp[p] = r.xe;
   }
+}
+
+// The exponents of row p: of x, of h, of y.
+__device__ __forceinline__ void w4_row_exps(const W4RowArgs& a, int slot, int p, int xe, int ln) {
+  const uint8_t* base = a.g.w + (size_t)slot * a.g.slab;
+  // |h| <= |g| |u| <= |x|^2 |Wg| |Wu|; h 2^-hexp stays below 2^15
+  const int b = ln + 2 * xe + w4_norm_exp(base + a.sl.gu.meta) + w4_norm_exp(base + a.sl.up_meta);
+  const int he = min(max(b - 15, -126), 126);
+  a.xexp[p] = xe;
+  a.hexp[p] = he;
+  a.yexp[p] = he + w4_y_exp(base + a.sl.dn_at, a.sl.dn);
 }
 
 template <int NC>
@@ -809,16 +837,37 @@ __global__ void __launch_bounds__(kRowThreads) w4_group_rows_kernel(const W4RowA
           reinterpret_cast<float4*>(a.y + (size_t)p * a.sl.dn.N)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
       continue;
     }
-    int xe, ln;
-    w4_scale_row<NC, true>(a.x + (size_t)(a.rows[p] / a.k) * a.ldx, a.xp + (size_t)p * a.K, a.K, lane, xe, ln);
-    if (lane == 0) {
-      const uint8_t* base = a.g.w + (size_t)slot * a.g.slab;
-      // |h| <= |g| |u| <= |x|^2 |Wg| |Wu|; h 2^-hexp stays below 2^15
-      const int b = ln + 2 * xe + w4_norm_exp(base + a.sl.gu.meta) + w4_norm_exp(base + a.sl.up_meta);
-      const int he = min(max(b - 15, -126), 126);
-      a.xexp[p] = xe;
-      a.hexp[p] = he;
-      a.yexp[p] = he + w4_y_exp(base + a.sl.dn_at, a.sl.dn);
+    W4Row<NC> r;
+    const int ln = r.template scale<true>(a.x + (size_t)(a.rows[p] / a.k) * a.ldx, a.K, lane);
+    r.store(a.xp + (size_t)p * a.K);
+    if (lane == 0) w4_row_exps(a, slot, p, r.xe, ln);
+  }
+}
+
+// The same by token, where every slot is grouped: a row is read and scaled once and stored k times, its slots'
+// exponents found by a lane each.
+template <int NC>
+__global__ void __launch_bounds__(kTokenThreads) w4_token_rows_kernel(const W4RowArgs a) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = gridDim.x * (kTokenThreads / 32);
+  pdl_wait();
+  pdl_trigger();
+  for (int t = blockIdx.x * (kTokenThreads / 32) + warp; t < a.n; t += nw) {
+    W4Row<NC> r;
+    const int ln = r.template scale<true>(a.x + (size_t)t * a.ldx, a.K, lane);
+    for (int j0 = 0; j0 < a.k; j0 += 32) {
+      int p = j0 + lane < a.k ? a.pos[(size_t)t * a.k + j0 + lane] : -1;  // -1: not an expert
+      if (p >= 0) {
+        const int e = a.ids[(size_t)t * a.k + j0 + lane], slot = a.g.e2s ? a.g.e2s[e] : e;
+        if (slot >= 0 && slot < a.g.S) {
+          w4_row_exps(a, slot, p, r.xe, ln);
+        } else {
+          set_status(a.g.status, MOE_DEV_BAD_SLOT);
+          a.yexp[p] = kNoRow;
+          p = -1;
+        }
+      }
+      for (unsigned m = __ballot_sync(MOE_FULL_MASK, p >= 0); m; m &= m - 1)
+        r.store(a.xp + (size_t)__shfl_sync(MOE_FULL_MASK, p, __ffs(m) - 1) * a.K);
     }
   }
 }
@@ -832,20 +881,20 @@ __global__ void __launch_bounds__(128) w4_combine_kernel(const uint16_t* __restr
   pdl_wait();
   if (c >= H) return;
   float acc[8] = {};
-  for (int j0 = 0; j0 < k; j0 += 4) {  // four rows in flight
-    int p[4], e[4];
-    float wj[4];
-    uint4 v[4];
+  for (int j0 = 0; j0 < k; j0 += 8) {  // eight rows in flight
+    int p[8], e[8];
+    float wj[8];
+    uint4 v[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) p[j] = j0 + j < k ? pos[(size_t)t * k + j0 + j] : -1;
+    for (int j = 0; j < 8; ++j) p[j] = j0 + j < k ? pos[(size_t)t * k + j0 + j] : -1;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
       e[j] = p[j] >= 0 ? yexp[p[j]] : kNoRow;
       wj[j] = p[j] >= 0 ? w[(size_t)t * k + j0 + j] : 0.f;
       if (p[j] >= 0) v[j] = __ldcs(reinterpret_cast<const uint4*>(yh + (size_t)p[j] * H + c));
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
       if (e[j] == kNoRow) continue;
       const float we = ldexpf(wj[j], e[j] / 2), m = ldexpf(1.f, e[j] - e[j] / 2);  // 2^e may overflow by itself
       const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
@@ -940,9 +989,10 @@ size_t w4_ffn_gemm_ws(size_t n, int H, int I, bool yh) {
   return g256(2 * n * H) + g256(2 * n * I) + 3 * g256(4 * n) + (yh ? g256(2 * n * H) : 0);
 }
 
-// y rows of the listed experts (fp32 f.y, or scaled fp16 with *yh / *yexp set for launch_w4_combine).
-int launch_ffn_w4_gemm(const FfnArgs& f, int group, void* ws, const uint16_t** yh, const int32_t** yexp,
-                       cudaStream_t s, Prof* prof) {
+// y rows of the listed experts (fp32 f.y, or scaled fp16 with *yh / *yexp set for launch_w4_combine).  ids and pos:
+// every slot's expert and row, where the list holds every expert with rows (else NULL).
+int launch_ffn_w4_gemm(const FfnArgs& f, const int32_t* ids, const int32_t* pos, int group, void* ws,
+                       const uint16_t** yh, const int32_t** yexp, cudaStream_t s, Prof* prof) {
   const size_t n = (size_t)f.T * f.k;
   const W4Slab sl = w4_slab(f.H, f.I, group);
   char* b = (char*)ws;
@@ -967,8 +1017,14 @@ int launch_ffn_w4_gemm(const FfnArgs& f, int group, void* ws, const uint16_t** y
   r.g = g, r.rows = f.rows, r.k = f.k, r.sl = sl;
   r.y = yh ? nullptr : f.y;
   if (prof) prof->begin(MOE_PROF_FFN_ROWS, s);
-  MOE_CUDA_TRY(launch_pdl(f.H <= 2048 ? w4_group_rows_kernel<8> : w4_group_rows_kernel<16>,
-                          dim3((unsigned)std::min((n + 7) / 8, (size_t)1216)), dim3(kRowThreads), 0, s, r));
+  if (ids) {
+    r.ids = ids, r.pos = pos, r.n = f.T;
+    MOE_CUDA_TRY(launch_pdl(f.H <= 2048 ? w4_token_rows_kernel<8> : w4_token_rows_kernel<16>,
+                            dim3((unsigned)std::min((f.T + 3) / 4, 2432)), dim3(kTokenThreads), 0, s, r));
+  } else {
+    MOE_CUDA_TRY(launch_pdl(f.H <= 2048 ? w4_group_rows_kernel<8> : w4_group_rows_kernel<16>,
+                            dim3((unsigned)std::min((n + 7) / 8, (size_t)1216)), dim3(kRowThreads), 0, s, r));
+  }
   if (prof) prof->end(s);
   if (prof) prof->begin(MOE_PROF_FFN_GATEUP, s);
   int rc = launch_gemm<kGateUp>(g, r.xp, s);
