@@ -683,7 +683,14 @@ static W4ExpWs w4_exp_ws(void* base, int T, int H, int I, int k, int E) {
   return w;
 }
 
-static bool w4_gemm_linear(int T) { return T >= 64; }
+// Streams take a pass over the weights per 32 rows, about 0.55 us for 10^6 of them; the tensor-core path costs 8 us
+// and more (rows, launches, the pipeline's start) and then little.  us, streams / tensor cores: 17 rows, 4096 x 4096
+// 10.9 / 12.1, x 16384 33.8 / 21.9; 33 rows, 4096 x 4096 19.9 / 12.8, 1024 x 8192 13.3 / 10.3; 128 rows, 2048 x 2048
+// 15.1 / 11.5, 1024 x 1024 6.3 / 10.5; 512 rows, 1024 x 1024 18.7 / 12.2, 512 x 512 8.4 / 11.0.
+static bool w4_gemm_linear(int T, int K, int N) {
+  const double work = (double)((T + 31) / 32) * K * N;
+  return T > 16 && work >= (T > 32 ? 1 << 24 : 1 << 25);
+}
 
 // Routing slots and hidden sizes whose products the kernels index with 32 bits.
 static bool w4_rows_ok(int T, int k) { return (int64_t)T * k <= (1 << 24); }
@@ -694,7 +701,7 @@ using namespace moe;
 
 extern "C" size_t moe_w4_linear_workspace_bytes(int T, int K, int N, int group) {
   if (T < 1 || !w4_shape_ok(K, N, group)) return 0;
-  return w4_gemm_linear(T) ? w4_linear_gemm_ws(T, K) : 0;
+  return w4_gemm_linear(T, K, N) ? w4_linear_gemm_ws(T, w4_dims(K, N, group)) : 0;
 }
 
 extern "C" int moe_w4_linear(const void* x, long long ldx, int T, int K, int N, int group, const void* w, void* out,
@@ -706,7 +713,7 @@ extern "C" int moe_w4_linear(const void* x, long long ldx, int T, int K, int N, 
   if ((uintptr_t)x % 16 || ldx % 8 || (uintptr_t)w % 16 || (uintptr_t)out % (out_f32 ? 4 : 2)) return MOE_ERR_ALIGN;
   if (workspace_bytes < moe_w4_linear_workspace_bytes(T, K, N, group) || (uintptr_t)workspace % 256)
     return MOE_ERR_ALIGN;
-  if (w4_gemm_linear(T))
+  if (w4_gemm_linear(T, K, N))
     return launch_w4_linear_gemm((const uint16_t*)x, (size_t)ldx, T, (const uint8_t*)w, w4_dims(K, N, group), out,
                                  (size_t)ldo, out_f32, workspace, dev_status, (cudaStream_t)stream);
   int sms = 0;

@@ -138,7 +138,7 @@ __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a
 }
 
 // The tensor-core path (w4_gemm.cu).
-size_t w4_linear_gemm_ws(int T, int K);
+size_t w4_linear_gemm_ws(int T, const W4Dims& d);
 int launch_w4_linear_gemm(const uint16_t* x, size_t ldx, int T, const uint8_t* w, const W4Dims& d, void* out,
                           size_t ldo, int out_f32, void* ws, int32_t* status, cudaStream_t s);
 size_t w4_ffn_gemm_ws(size_t n, int H, int I, bool yh);

@@ -66,6 +66,7 @@ struct W4GemmArgs {
   size_t mat;              // offset of the matrix in a slab
   int K, NF;               // K of the rows; column tiles of 256
   int n;                   // rows
+  int parts, stages;       // kLinear: parts of the inputs, stages in one (even); 1 and d.Kb elsewhere
   // grouped rows
   const int32_t *offset, *list_e, *n_list, *e2s, *list_s;
   int E, S;
@@ -184,17 +185,24 @@ __device__ __forceinline__ bool w4g_slot(const W4GemmArgs& a, int li, int& e, in
 struct W4GTile {
   const uint8_t* base;  // the matrix
   int ft, row0, ntok;
+  int k0, nk;           // first stage, stages
+  int part;
 };
 
-// Tile t: row tile t / NF (by the prefix of row tiles over the list), column tile t % NF.
+// Tile t: column tile t % NF, row tile t / NF (by the prefix of row tiles over the list); kLinear: of part
+// t / (NF x row tiles) of the inputs.
 template <int kMode>
 __device__ __forceinline__ W4GTile w4g_tile(const W4GemmArgs& a, const int* pre, int nl, int t) {
   W4GTile r;
   const int i = t / a.NF;
   r.ft = t - i * a.NF;
+  r.k0 = r.part = 0, r.nk = a.d.Kb;
   if (kMode == kLinear) {
+    const int rt = (a.n + kGN - 1) / kGN;
+    r.part = i / rt;
+    r.k0 = r.part * a.stages, r.nk = min(a.stages, a.d.Kb - r.k0);
     r.base = a.w;
-    r.row0 = i * kGN;
+    r.row0 = (i - r.part * rt) * kGN;
     r.ntok = min(kGN, a.n - r.row0);
   } else {
     int lo = 0, hi = nl;  // pre[lo] <= i < pre[hi]
@@ -320,7 +328,7 @@ __device__ __forceinline__ void w4g_store16(const W4GemmArgs& a, const uint32_t*
 // The same of fp32 values (v[row], without the column's power of two): to fp32 results, or (kGateUp) to h.
 template <int kMode>
 __device__ __forceinline__ void w4g_store32(const W4GemmArgs& a, const float* v, float* st, const W4GFactors& f, int i,
-                                            size_t row0, int nrow, int c0, int lane) {
+                                            int part, size_t row0, int nrow, int c0, int lane) {
   const W4Dims& d = a.d;
   auto row_fac = [&](int row) { return pow2(__shfl_sync(MOE_FULL_MASK, f.r[i >> 1], 16 * (i & 1) + row)); };
 #pragma unroll
@@ -344,7 +352,8 @@ __device__ __forceinline__ void w4g_store32(const W4GemmArgs& a, const float* v,
     }
     if (row < nrow) *reinterpret_cast<uint4*>(a.h + (row0 + row) * I + f0 + seg) = make_uint4(o[0], o[1], o[2], o[3]);
   } else {
-    float* out = kMode == kLinear ? reinterpret_cast<float*>(a.out) : a.y;
+    // (a part of the inputs writes sums of its own)
+    float* out = kMode == kLinear ? reinterpret_cast<float*>(a.out) + (size_t)part * a.n * a.ldo : a.y;
     const size_t ld = kMode == kLinear ? a.ldo : (size_t)d.N;
     if (kMode == kLinear && !(ld % 4 == 0 && (uintptr_t)a.out % 16 == 0 && c0 + 32 <= d.N)) {
       for (int row = 0; row < nrow; ++row) {
@@ -419,7 +428,7 @@ __device__ __forceinline__ void w4g_drain(const W4GemmArgs& a, const W4GTile& ti
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (nrow > 16 * i)
-        w4g_store32<kMode>(a, (i < 2 ? v0 : v1) + 16 * (i & 1), st, f, i, row0 + 16 * i,
+        w4g_store32<kMode>(a, (i < 2 ? v0 : v1) + 16 * (i & 1), st, f, i, ti.part, row0 + 16 * i,
                            min(nrow - 16 * i, 16), c0, lane);
   }
 }
@@ -448,7 +457,6 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   const uint32_t rank = cluster_rank();
   const int cl = (int)cluster_index(), ncl = (int)cluster_count();
   const W4Dims& d = a.d;
-  const int nkb = d.Kb;
   int nl = 0, total;
 
   if (threadIdx.x == 0) {
@@ -473,7 +481,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   pdl_wait();
   pdl_trigger();
   if (kMode == kLinear) {
-    total = (a.n + kGN - 1) / kGN * a.NF;
+    total = (a.n + kGN - 1) / kGN * a.NF * a.parts;
   } else {
     // prefix of the listed experts' row tiles
     nl = min(*a.n_list, kMaxE);
@@ -516,8 +524,8 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     for (int t = cl; t < total && !dead; t += ncl) {
       const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
       const int r = w4g_half(ti.ntok), row = ti.row0 + (int)rank * r;
-      for (int kb = 0; kb < nkb; kb += kGVisit, ++vi) {
-        const uint32_t s = vi % kGSets, use = vi / kGSets, nb = min(kGVisit, nkb - kb);
+      for (int kb = 0; kb < ti.nk; kb += kGVisit, ++vi) {
+        const uint32_t s = vi % kGSets, use = vi / kGSets, nb = min(kGVisit, ti.nk - kb);
         if (use > 0) wait(&empty[s], (use - 1) & 1u);
         if (dead) break;
         if (lead) {
@@ -526,7 +534,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
           const uint32_t fb = mapa_shared(smem_u32(&full[s]), 0);
           for (uint32_t h = 0; h < nb; ++h) {
             unsigned char* dst = xs + (s * kGVisit + h) * kGXBytes;
-            const int c = (kb + (int)h) * kGK;
+            const int c = (ti.k0 + kb + (int)h) * kGK;
             if (r == kGRows) {
               tma_load_3d_pair(dst, &mapX.m[0], fb, c, row, 0);
             } else {
@@ -559,8 +567,8 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
       const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
       const int blk = 2 * ti.ft + (int)rank;
       const uint32_t nm = max(0, min(8, d.Mt - 8 * blk));  // the tiles of 16 columns that exist
-      for (int kb = 0; kb < nkb; kb += kGVisit, ++wi) {
-        const uint32_t s = wi % kGWRing, use = wi / kGWRing, nb = min(kGVisit, nkb - kb);
+      for (int kb = ti.k0; kb < ti.k0 + ti.nk; kb += kGVisit, ++wi) {
+        const uint32_t s = wi % kGWRing, use = wi / kGWRing, nb = min(kGVisit, ti.k0 + ti.nk - kb);
         const uint32_t ng = d.G == 128 ? (nb + 1) / 2 : d.G == 64 ? nb : 2 * nb;
         if (use > 0) wait(&wempty[s], (use - 1) & 1u);
         if (dead) break;
@@ -589,7 +597,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
         const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
         const uint32_t idesc = idesc_f16(2 * kGM, 2 * w4g_half(ti.ntok));
         if (tc > 0) wait(tempty, (tc - 1) & 1u);
-        for (int kb = 0; kb < nkb; kb += kGVisit, ++vi) {
+        for (int kb = 0; kb < ti.nk; kb += kGVisit, ++vi) {
           const uint32_t s = vi % kGSets;
           wait(&full[s], (vi / kGSets) & 1u);
           tc_fence_after();
@@ -597,7 +605,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
             const uint32_t at = tmem + kGACol + s * 64;
             const uint64_t bd = bd0 + (uint64_t)(s * kGVisit * (kGXBytes >> 4));
             umma_f16_ts_pair_k64(tmem, at, bd, idesc, kb > 0);
-            if (kb + 1 < nkb) umma_f16_ts_pair_k64(tmem, at + 32, bd + (kGXBytes >> 4), idesc, 1);
+            if (kb + 1 < ti.nk) umma_f16_ts_pair_k64(tmem, at + 32, bd + (kGXBytes >> 4), idesc, 1);
           }
           if (lead) umma_commit_pair(&empty[s]);
           __syncwarp();
@@ -625,7 +633,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
       const bool real = t < total && !dead;
       W4GTile ti = {};
       if (real) ti = w4g_tile<kMode>(a, s_pre, nl, t);
-      const int nm = max(1, min(8, d.Mt - 8 * (2 * ti.ft + (int)rank))), nk = real ? nkb : 0;
+      const int nm = max(1, min(8, d.Mt - 8 * (2 * ti.ft + (int)rank))), nk = real ? ti.nk : 0;
       // a visit of every set but one (whose columns the last tile's final MMAs still read), the last tile's
       // drain, the other visits; this set's are every fourth one of the CTA's sequence
       int kb = (int)((set - vi) % kGSets) * kGVisit;
@@ -640,7 +648,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
           uint32_t o[32];
 #pragma unroll
           for (int h = 0; h < kGVisit; ++h) {
-            if (kb + h >= nkb) break;
+            if (kb + h >= nk) break;
             const unsigned char* code = wst + (h * nm + (r >> 4)) * 512 + g * 64 + hi * 8;
             const int gi = d.G == 128 ? 0 : d.G == 64 ? h : 2 * h;
             const __half* sp = reinterpret_cast<const __half*>(wst + kGCodeBytes + (gi * nm * 8 + g * nm + (r >> 4)) * 4) + hi;
@@ -676,7 +684,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
       prev = ti;
       pending = true;
       f = w4g_factors<kMode>(a, ti, 2 * ti.ft + (int)rank, q, set, lane);
-      vi += (nkb + kGVisit - 1) / kGVisit;
+      vi += (nk + kGVisit - 1) / kGVisit;
     }
   }
   // reconverge before the cluster barrier, which also keeps each CTA's shared memory alive while its peer
@@ -712,37 +720,40 @@ struct W4RowArgs {
   float* y;                // rows of experts without a slot are zeroed, or NULL (yexp says so)
 };
 
-// One row x of K inputs, its exponent and, with kNorm, ceil(log2 |x'|^2) (x' = the scaled row).  The row is read
-// once, all of it in flight at a time, up to 256 NC inputs; what is beyond them is read again.
+// The share of a row x of K inputs that one of `step` threads (the i0-th) has: 16 bytes of every 16 step.  It is
+// read once, all of it in flight at a time, up to NC loads; what is beyond them is read again.
 template <int NC>
 struct W4Row {
   const uint4* x;
-  int K, lane, xe;
+  int n, i0, step, xe;
   float f0, f1;
   uint4 v[NC];  // scaled, after scale()
 
   __device__ __forceinline__ uint32_t conv(uint32_t u) const { return pack_f16(bf16_lo(u) * f0 * f1, bf16_hi(u) * f0 * f1); }
   __device__ __forceinline__ uint4 conv(uint4 u) const { return make_uint4(conv(u.x), conv(u.y), conv(u.z), conv(u.w)); }
-  __device__ __forceinline__ uint4 at(int c) const { return __ldg(x + c); }
 
-  template <bool kNorm>
-  __device__ __forceinline__ int scale(const uint16_t* row, int K_, int lane_) {
-    x = reinterpret_cast<const uint4*>(row), K = K_, lane = lane_;
+  // The largest magnitude, as bits (bf16 magnitudes are ordered like integers); infinities and NaN do not count.
+  __device__ __forceinline__ uint32_t load(const uint16_t* row, int K, int i0_, int step_) {
+    x = reinterpret_cast<const uint4*>(row), n = K / 8, i0 = i0_, step = step_;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) v[i] = 32 * i + lane < K / 8 ? at(32 * i + lane) : make_uint4(0, 0, 0, 0);
-    uint32_t amax = 0;  // of the bits: bf16 magnitudes are ordered like integers
+    for (int i = 0; i < NC; ++i) v[i] = step * i + i0 < n ? __ldg(x + step * i + i0) : make_uint4(0, 0, 0, 0);
+    uint32_t amax = 0;
     auto take = [&](uint32_t u) {
       const uint32_t lo = u & 0x7fffu, hi = (u >> 16) & 0x7fffu;
-      amax = max(amax, lo < 0x7f80u ? lo : 0u);  // infinities and NaN do not set the scale
+      amax = max(amax, lo < 0x7f80u ? lo : 0u);
       amax = max(amax, hi < 0x7f80u ? hi : 0u);
     };
 #pragma unroll
     for (int i = 0; i < NC; ++i) take(v[i].x), take(v[i].y), take(v[i].z), take(v[i].w);
-    for (int c = 32 * NC + lane; c < K / 8; c += 32) {
-      const uint4 u = at(c);
+    for (int c = step * NC + i0; c < n; c += step) {
+      const uint4 u = __ldg(x + c);
       take(u.x), take(u.y), take(u.z), take(u.w);
     }
-    amax = __reduce_max_sync(MOE_FULL_MASK, amax);
+    return amax;
+  }
+  // With the whole row's largest: xe, and this share times 2^-xe; with kNorm its sum of squares.
+  template <bool kNorm>
+  __device__ __forceinline__ float scale(uint32_t amax) {
     xe = amax ? max(ilogbf(__uint_as_float(amax << 16)) - 14, -126) : 0;
     f0 = ldexpf(1.f, -xe / 2), f1 = ldexpf(1.f, -xe - (-xe / 2));  // 2^-xe may overflow by itself
     float nrm = 0.f;
@@ -756,24 +767,33 @@ struct W4Row {
       if (kNorm) square(v[i].x), square(v[i].y), square(v[i].z), square(v[i].w);
       v[i] = conv(v[i]);
     }
-    if (!kNorm) return 0;
-    for (int c = 32 * NC + lane; c < K / 8; c += 32) {
-      const uint4 u = at(c);
-      square(u.x), square(u.y), square(u.z), square(u.w);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) nrm += __shfl_xor_sync(MOE_FULL_MASK, nrm, o);
-    return nrm > 0.f ? ilogbf(nrm * 1.001f) + 1 : 0;
+    if (kNorm)
+      for (int c = step * NC + i0; c < n; c += step) {
+        const uint4 u = __ldg(x + c);
+        square(u.x), square(u.y), square(u.z), square(u.w);
+      }
+    return nrm;
   }
   __device__ __forceinline__ void store(uint16_t* row) const {
     uint4* o = reinterpret_cast<uint4*>(row);
 #pragma unroll
     for (int i = 0; i < NC; ++i)
-      if (32 * i + lane < K / 8) o[32 * i + lane] = v[i];
-    for (int c = 32 * NC + lane; c < K / 8; c += 32) o[c] = conv(at(c));
+      if (step * i + i0 < n) o[step * i + i0] = v[i];
+    for (int c = step * NC + i0; c < n; c += step) o[c] = conv(__ldg(x + c));
   }
 };
 
+// A row by one warp: loaded and scaled; with kNorm, returns ceil(log2 |x'|^2) (x' = the scaled row).
+template <bool kNorm, int NC>
+__device__ __forceinline__ int w4_warp_row(W4Row<NC>& r, const uint16_t* row, int K, int lane) {
+  float nrm = r.template scale<kNorm>(__reduce_max_sync(MOE_FULL_MASK, r.load(row, K, lane, 32)));
+  if (kNorm)
+#pragma unroll
+    for (int o = 16; o; o >>= 1) nrm += __shfl_xor_sync(MOE_FULL_MASK, nrm, o);
+  return nrm > 0.f ? ilogbf(nrm * 1.001f) + 1 : 0;
+}
+
+// Rows of a linear layer, a warp to a row.
 template <int NC>
 __global__ void __launch_bounds__(kRowThreads) w4_rows_kernel(const W4RowArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = gridDim.x * (kRowThreads / 32);
@@ -781,9 +801,30 @@ __global__ void __launch_bounds__(kRowThreads) w4_rows_kernel(const W4RowArgs a)
   pdl_trigger();
   for (int p = blockIdx.x * (kRowThreads / 32) + warp; p < a.n; p += nw) {
     W4Row<NC> r;
-    r.template scale<false>(a.x + (size_t)p * a.ldx, a.K, lane);
+    w4_warp_row<false>(r, a.x + (size_t)p * a.ldx, a.K, lane);
     r.store(a.xp + (size_t)p * a.K);
     if (lane == 0) a.xexp[p] = r.xe;
+  }
+}
+
+// The same of few rows: `per` warps (a power of two) to a row, four loads a thread.
+__global__ void __launch_bounds__(kRowThreads) w4_few_rows_kernel(const W4RowArgs a, int per) {
+  constexpr int kWarps = kRowThreads / 32;
+  __shared__ uint32_t s_max[2][kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp & (per - 1), rows = kWarps / per;
+  pdl_wait();
+  pdl_trigger();
+  int buf = 0;
+  for (int p0 = blockIdx.x * rows; p0 < a.n; p0 += gridDim.x * rows, buf ^= 1) {
+    const int p = min(p0 + warp / per, a.n - 1);  // (a last row may be done twice, with the same result)
+    W4Row<4> r;
+    uint32_t amax = __reduce_max_sync(MOE_FULL_MASK, r.load(a.x + (size_t)p * a.ldx, a.K, 32 * sub + lane, 32 * per));
+    if (lane == 0) s_max[buf][warp] = amax;
+    __syncthreads();
+    for (int i = 0; i < per; ++i) amax = max(amax, s_max[buf][warp - sub + i]);
+    r.scale<false>(amax);
+    r.store(a.xp + (size_t)p * a.K);
+    if (sub == 0 && lane == 0) a.xexp[p] = r.xe;
   }
 }
 
@@ -838,7 +879,7 @@ __global__ void __launch_bounds__(kRowThreads) w4_group_rows_kernel(const W4RowA
       continue;
     }
     W4Row<NC> r;
-    const int ln = r.template scale<true>(a.x + (size_t)(a.rows[p] / a.k) * a.ldx, a.K, lane);
+    const int ln = w4_warp_row<true>(r, a.x + (size_t)(a.rows[p] / a.k) * a.ldx, a.K, lane);
     r.store(a.xp + (size_t)p * a.K);
     if (lane == 0) w4_row_exps(a, slot, p, r.xe, ln);
   }
@@ -853,7 +894,7 @@ __global__ void __launch_bounds__(kTokenThreads) w4_token_rows_kernel(const W4Ro
   pdl_trigger();
   for (int t = blockIdx.x * (kTokenThreads / 32) + warp; t < a.n; t += nw) {
     W4Row<NC> r;
-    const int ln = r.template scale<true>(a.x + (size_t)t * a.ldx, a.K, lane);
+    const int ln = w4_warp_row<true>(r, a.x + (size_t)t * a.ldx, a.K, lane);
     for (int j0 = 0; j0 < a.k; j0 += 32) {
       int p = j0 + lane < a.k ? a.pos[(size_t)t * a.k + j0 + lane] : -1;  // -1: not an expert
       if (p >= 0) {
@@ -881,20 +922,20 @@ __global__ void __launch_bounds__(128) w4_combine_kernel(const uint16_t* __restr
   pdl_wait();
   if (c >= H) return;
   float acc[8] = {};
-  for (int j0 = 0; j0 < k; j0 += 8) {  // eight rows in flight
-    int p[8], e[8];
-    float wj[8];
-    uint4 v[8];
+  for (int j0 = 0; j0 < k; j0 += 4) {  // four rows in flight
+    int p[4], e[4];
+    float wj[4];
+    uint4 v[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) p[j] = j0 + j < k ? pos[(size_t)t * k + j0 + j] : -1;
+    for (int j = 0; j < 4; ++j) p[j] = j0 + j < k ? pos[(size_t)t * k + j0 + j] : -1;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
       e[j] = p[j] >= 0 ? yexp[p[j]] : kNoRow;
       wj[j] = p[j] >= 0 ? w[(size_t)t * k + j0 + j] : 0.f;
       if (p[j] >= 0) v[j] = __ldcs(reinterpret_cast<const uint4*>(yh + (size_t)p[j] * H + c));
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
       if (e[j] == kNoRow) continue;
       const float we = ldexpf(wj[j], e[j] / 2), m = ldexpf(1.f, e[j] - e[j] / 2);  // 2^e may overflow by itself
       const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
@@ -966,7 +1007,60 @@ static int launch_gemm(const W4GemmArgs& g, const void* rows, cudaStream_t s) {
 
 static size_t g256(size_t v) { return (v + 255) & ~size_t(255); }
 
-size_t w4_linear_gemm_ws(int T, int K) { return g256(2 * (size_t)T * K) + g256(4 * (size_t)T); }
+// Parts of the inputs: where there are fewer tiles than pairs of SMs, as many as there are pairs for, of kGPart
+// stages or more.  (256 rows through 4096 x 4096, four parts: 16.7 us, undivided 28; through 8192 x 1024, 16 parts:
+// 19 and 52.  Parts of 8 stages against 16: 2048 x 2048 13.3 and 14.4 us, 8192 x 1024 19.2 and 17.2.)
+constexpr int kGPairs = 76, kGPart = 8;
+static void w4_parts(int T, const W4Dims& d, int& parts, int& stages) {
+  const int64_t tiles = (int64_t)((T + kGN - 1) / kGN) * ((d.N + 2 * kGM - 1) / (2 * kGM));
+  parts = (int)std::min<int64_t>(kGPairs / tiles, d.Kb / kGPart);
+  stages = parts < 2 ? d.Kb : ((d.Kb + parts - 1) / parts + kGVisit - 1) / kGVisit * kGVisit;
+  parts = (d.Kb + stages - 1) / stages;
+}
+static int w4_part_ld(int N) { return (N + 3) & ~3; }
+
+// Enough for any number of rows up to T: parts x rows <= kGPairs / (column tiles) x min(T, kGN).
+size_t w4_linear_gemm_ws(int T, const W4Dims& d) {
+  const size_t nf = (d.N + 2 * kGM - 1) / (2 * kGM);
+  return g256(2 * (size_t)T * d.K) + g256(4 * (size_t)T) +
+         (2 * nf > kGPairs ? 0 : 4 * (kGPairs / nf) * std::min(T, kGN) * w4_part_ld(d.N));
+}
+
+// out = the sums of the parts, in order; four columns a thread.
+__global__ void __launch_bounds__(256) w4_parts_kernel(const float* __restrict__ part, int parts, int T, int N, int ldp,
+                                                       void* out, size_t ldo, int out_f32) {
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, per = ldp / 4, t = i / per, c = (i - t * per) * 4;
+  pdl_wait();
+  if (t >= (size_t)T) return;
+  const float* p = part + t * ldp + c;
+  float4 s = __ldcs(reinterpret_cast<const float4*>(p));
+#pragma unroll 4
+  for (int j = 1; j < parts; ++j) {
+    const float4 v = __ldcs(reinterpret_cast<const float4*>(p + (size_t)j * T * ldp));
+    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+  }
+  const float v[4] = {s.x, s.y, s.z, s.w};
+  const size_t at = t * ldo + c;
+  if (out_f32) {
+    float* o = reinterpret_cast<float*>(out) + at;
+    if ((uintptr_t)o % 16 == 0 && c + 4 <= (size_t)N) {
+      *reinterpret_cast<float4*>(o) = s;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j < (size_t)N) o[j] = v[j];
+    }
+  } else {
+    uint16_t* o = reinterpret_cast<uint16_t*>(out) + at;
+    if ((uintptr_t)o % 8 == 0 && c + 4 <= (size_t)N) {
+      *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j < (size_t)N) o[j] = f32_to_bf16(v[j]);
+    }
+  }
+}
 
 int launch_w4_linear_gemm(const uint16_t* x, size_t ldx, int T, const uint8_t* w, const W4Dims& d, void* out,
                           size_t ldo, int out_f32, void* ws, int32_t* status, cudaStream_t s) {
@@ -974,14 +1068,30 @@ int launch_w4_linear_gemm(const uint16_t* x, size_t ldx, int T, const uint8_t* w
   r.x = x, r.ldx = ldx, r.n = T, r.K = d.K;
   r.xp = (uint16_t*)ws;
   r.xexp = (int32_t*)((char*)ws + g256(2 * (size_t)T * d.K));
-  MOE_CUDA_TRY(launch_pdl(d.K <= 2048 ? w4_rows_kernel<8> : w4_rows_kernel<16>, dim3(std::min((T + 7) / 8, 1216)),
-                          dim3(kRowThreads), 0, s, r));
+  // a warp to a row while there is a row for every scheduler twice; several warps where a row's latency is what
+  // counts (33 rows of 4096: 15.6 us with one, 12.7 with four; 4096 rows of 2048: 53.5 with one, 55 with two)
+  if (T >= 1216) {
+    MOE_CUDA_TRY(launch_pdl(d.K <= 2048 ? w4_rows_kernel<8> : w4_rows_kernel<16>, dim3(std::min((T + 7) / 8, 1216)),
+                            dim3(kRowThreads), 0, s, r));
+  } else {
+    const int per = d.K <= 1024 ? 1 : d.K <= 2048 ? 2 : d.K <= 4096 ? 4 : 8, rows = kRowThreads / 32 / per;
+    MOE_CUDA_TRY(launch_pdl(w4_few_rows_kernel, dim3((T + rows - 1) / rows), dim3(kRowThreads), 0, s, r, per));
+  }
   W4GemmArgs g{};
   g.w = w, g.d = d, g.K = d.K, g.n = T;
   g.NF = (d.N + 2 * kGM - 1) / (2 * kGM);
   g.status = status, g.rexp = r.xexp;
   g.out = out, g.ldo = ldo, g.out_f32 = out_f32;
-  return launch_gemm<kLinear>(g, r.xp, s);
+  w4_parts(T, d, g.parts, g.stages);
+  if (g.parts == 1) return launch_gemm<kLinear>(g, r.xp, s);
+  float* part = (float*)((char*)r.xexp + g256(4 * (size_t)T));
+  const int ldp = w4_part_ld(d.N);
+  g.out = part, g.ldo = ldp, g.out_f32 = 1;
+  const int rc = launch_gemm<kLinear>(g, r.xp, s);
+  if (rc != MOE_OK) return rc;
+  MOE_CUDA_TRY(launch_pdl(w4_parts_kernel, dim3((unsigned)(((size_t)T * (ldp / 4) + 255) / 256)), dim3(256), 0, s,
+                          (const float*)part, g.parts, T, d.N, ldp, out, ldo, out_f32));
+  return MOE_OK;
 }
 
 // Workspace: x' [n][H] fp16, h [n][I] fp16, exponents, and y [n][H] fp16 where the caller combines.

@@ -1,0 +1,81 @@
+"""The 4-bit linear layer where it runs on the tensor cores' large tiles: from 17 rows, by rows x weights.
+
+Compared with fp64 products of the unpacked weights, with the tolerance of the small sizes: (K / 32 + 40) fp32
+roundings of 2^-23 of the sum of |x w| at most (parts of the inputs that are summed apart add one rounding each,
+of the 40), and half a unit in the last place of a bf16 output.
+"""
+import pytest
+import torch
+
+from tests.test_gpu_w4 import check_linear, draw_w4, dequant
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+# K, N, group, T: many parts of few columns; ragged columns; one, two and several row tiles; an odd number of
+# stages, and a last stage that is mostly past K; one row more than a pass of the small kernel
+CASES = [(16392, 520, 64, 40), (4104, 4097, 32, 33), (8200, 4160, 128, 17), (2064, 3000, 64, 300),
+         (1032, 1001, 128, 600), (136, 100003, 32, 65), (520, 2049, 128, 513), (4096, 2112, 64, 257)]
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K,N,group,T", CASES)
+def test_linear(K, N, group, T, out_dtype):
+    import expert_slot_cache_gb300 as M
+    codes, scales = draw_w4(K, N, group, T)
+    x = torch.randn(T, K, generator=torch.Generator().manual_seed(T + 1)).to(torch.bfloat16)
+    x[:, :: 97] *= 30
+    op = M.W4Linear(M.w4_pack(codes.to(DEV), scales.to(DEV), group), K, N, group, max_tokens=T, out_dtype=out_dtype)
+    y = op.forward(x.to(DEV))
+    assert int(op.dev_status.item()) == 0
+    check_linear(y, x, dequant(codes, scales, group), out_dtype)
+
+
+@pytest.mark.parametrize("K,N,T", [(4104, 1100, 130), (2056, 5000, 70)])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_strided_rows(K, N, T, out_dtype):
+    """Rows of x and out inside wider tensors, fewer of them than the operator was made for."""
+    import expert_slot_cache_gb300 as M
+    codes, scales = draw_w4(K, N, 64, 5)
+    wide = torch.full((T, K + 24), float("nan"), dtype=torch.bfloat16, device=DEV)
+    x = torch.randn(T, K, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    wide[:, 8:8 + K] = x.to(DEV)
+    out = torch.full((T, N + 5), 7.0, dtype=out_dtype, device=DEV)
+    op = M.W4Linear(M.w4_pack(codes.to(DEV), scales.to(DEV), 64), K, N, 64, max_tokens=3000, out_dtype=out_dtype)
+    op.forward(wide[:, 8:8 + K], out=out[:, 2:2 + N])
+    check_linear(out[:, 2:2 + N].contiguous(), x, dequant(codes, scales, 64), out_dtype)
+    assert bool((out[:, :2] == 7).all()) and bool((out[:, 2 + N:] == 7).all())
+
+
+def test_extreme_rows():
+    """Rows of very large and very small values and of zeros; infinities and NaN stay in their rows."""
+    import expert_slot_cache_gb300 as M
+    T, K, N, group = 90, 4096, 1536, 128
+    codes, scales = draw_w4(K, N, group, 9)
+    x = torch.randn(T, K, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    x[0] = 0
+    x[1] *= 2.0 ** 90
+    x[2] *= 2.0 ** -90
+    op = M.W4Linear(M.w4_pack(codes.to(DEV), scales.to(DEV), group), K, N, group, max_tokens=T, out_dtype=torch.float32)
+    w = dequant(codes, scales, group)
+    check_linear(op.forward(x.to(DEV)), x, w, torch.float32)
+    x[3, 5] = float("nan")
+    x[1, 7] = float("inf")
+    y = op.forward(x.to(DEV)).cpu()
+    assert bool(y[3].isnan().all()) and not bool(y[1].isfinite().any())
+    keep = [0, 2] + list(range(4, T))
+    check_linear(y[keep], x[keep], w, torch.float32)
+
+
+def test_same_result_every_time():
+    import expert_slot_cache_gb300 as M
+    T, K, N, group = 200, 4096, 1024, 64
+    codes, scales = draw_w4(K, N, group, 1)
+    op = M.W4Linear(M.w4_pack(codes.to(DEV), scales.to(DEV), group), K, N, group, max_tokens=T)
+    x = torch.randn(T, K, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).to(DEV)
+    want = op.forward(x).clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(20):
+            assert torch.equal(op.forward(x), want)
