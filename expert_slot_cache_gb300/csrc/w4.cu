@@ -32,7 +32,12 @@ constexpr int kW4Ctas = 2;   // resident CTAs per SM that the registers allow
 // Routing slots up to which the down kernel adds the experts up itself: the sums then fall to the few CTAs that
 // finish last (one token 20.5 us against 24.6 us with a kernel for them, 32 tokens 142 against 133 us).
 constexpr int kW4Fuse = 16;
-constexpr int kGemmRows = 512;  // routing slots from which the experts' tensor-core path takes over
+constexpr int kW4Slots = 512;  // routing slots that the stream kernels group themselves; more are grouped before them
+// Rows of an expert, on average, from which the tensor-core path takes over: a stream pays for every eight rows of an
+// expert, a large tile hardly for any of its 256.  us, streams / tensor cores: 8 experts, 12 rows each 24.9 / 32.6, 16
+// rows 34.1 / 33.3, 48 rows 62.8 / 34.0; 32 experts, 8 rows 29.0 / 37.5, 12 rows 36.2 / 36.6; 128 experts, 3 rows
+// 104 / 167.
+constexpr int kGemmRows = 10;
 
 // One block of 64 inputs in registers: a lane's codes of CM tiles, their columns' scales, and the lane's inputs
 // of NB groups of eight rows (LO: as the sum of two bf16).
@@ -309,6 +314,8 @@ struct W4FfnArgs {
   int n;                  // routing slots
   // Routed form: the groups come from the ids (row = flat routing slot), the combine follows in the down kernel.
   const int32_t* ids;     // [n], or NULL: f.offset / f.rows / f.list_e / f.n_list (row = grouped position)
+  const int32_t* pos;     // [n] row of y of every slot, where the groups are given and the combine follows
+  int cap;                // row batches that there can be
   const float* w;         // [n]
   uint16_t* out;          // bf16 [T][H]
   int32_t* ready;         // [H / 64] row batches done per 64 output columns, or NULL: w4_sum_kernel follows
@@ -321,11 +328,9 @@ struct W4Batch {
   uint16_t row[kW4Rows];  // rows of h and y
 };
 
-// Dynamic shared memory of the expert kernels: the batches.
-static size_t w4_tab_bytes(int n) { return (size_t)n * sizeof(W4Batch); }
 
-// The row batches of the listed experts, or of the ids, by ascending expert, in shared memory: `tab` holds n
-// entries, `cnt` (2 kMaxE + n ints, free afterwards) is scratch.  Built by all threads; returns their number.
+// The row batches of the listed experts, or of the ids, by ascending expert, in shared memory: `tab` holds
+// cap entries, `cnt` (2 kMaxE + n ints, free afterwards) is scratch.  Built by all threads; returns their number.
 // Every CTA builds the same batches, though the order of the rows inside one may vary: no row's result depends
 // on its neighbours.
 __device__ __forceinline__ int w4_batches(const W4FfnArgs& g, W4Batch* tab, int* cnt, int* tmp) {
@@ -335,7 +340,7 @@ __device__ __forceinline__ int w4_batches(const W4FfnArgs& g, W4Batch* tab, int*
     int *first = cnt + kMaxE, *ids = cnt + 2 * kMaxE;  // an expert's first batch; the ids
     for (int e = threadIdx.x; e < a.E; e += kW4Threads) cnt[e] = 0;
     __syncthreads();
-    constexpr int U = (kGemmRows + kW4Threads - 1) / kW4Threads;  // routing slots per thread
+    constexpr int U = kW4Slots / kW4Threads;  // routing slots per thread
     int id[U], rank[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -402,7 +407,7 @@ __device__ __forceinline__ int w4_batches(const W4FfnArgs& g, W4Batch* tab, int*
     }
     int tot;
     const int ex = base + block_exclusive_scan(c, tmp, &tot);
-    for (int i = 0; i < c && ex + i < n; ++i) {
+    for (int i = 0; i < c && ex + i < g.cap; ++i) {
       W4Batch& b = tab[ex + i];
       b.slot = slot;
       b.n = min(kW4Rows, rows - kW4Rows * i);
@@ -411,8 +416,8 @@ __device__ __forceinline__ int w4_batches(const W4FfnArgs& g, W4Batch* tab, int*
     base += tot;
   }
   __syncthreads();
-  if (base > n && threadIdx.x == 0) set_status(a.status, MOE_DEV_BAD_GROUPS);
-  return min(base, n);
+  if (base > g.cap && threadIdx.x == 0) set_status(a.status, MOE_DEV_BAD_GROUPS);
+  return min(base, g.cap);
 }
 
 // Gate and up: unit = (row batch, two tiles of gate with their neighbours of up); an expert's batches follow
@@ -507,10 +512,12 @@ __global__ void __launch_bounds__(128) w4_sum_kernel(const W4FfnArgs a) {
   for (int j = 0; j < kMaxK; ++j) {
     y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
     w[j] = 0.f;
-    const int at = t * k + j, e = j < k ? a.ids[at] : -1;
-    if (e >= 0 && e < a.f.E) {
+    const int at = t * k + j;
+    int p = -1;  // the slot's row of y; none for an id that is not an expert
+    if (j < k) p = a.pos ? a.pos[at] : a.ids[at] >= 0 && a.ids[at] < a.f.E ? at : -1;
+    if (p >= 0) {
       w[j] = a.w[at];
-      y[j] = *reinterpret_cast<const float4*>(a.f.y + (size_t)at * H + c);
+      y[j] = *reinterpret_cast<const float4*>(a.f.y + (size_t)p * H + c);
     }
   }
 #pragma unroll
@@ -608,16 +615,26 @@ static int w4_sms(int* sms) {
   return MOE_OK;
 }
 
-static bool w4_gemm_ffn(int n) { return n >= kGemmRows; }
+static bool w4_gemm_ffn(int n, int E) { return n > 128 && n >= kGemmRows * E; }
 
 size_t w4_ws_bytes(int n, int H, int I) {
   const size_t h = ((size_t)n * I * 4 + 255) & ~size_t(255);
-  return w4_gemm_ffn(n) ? std::max(h, w4_ffn_gemm_ws(n, H, I, false)) : h;
+  return w4_gemm_ffn(n, 0) ? std::max(h, w4_ffn_gemm_ws(n, H, I, false)) : h;  // (enough for any number of experts)
 }
 
 // The two weight streams; the second one's CTAs start as the first one's leave.
-static int launch_ffn_w4_stream(const W4FfnArgs& a, int group, int sms, cudaStream_t stream, Prof* prof) {
-  const size_t smem = w4_tab_bytes(a.n);
+static int launch_ffn_w4_stream(W4FfnArgs a, int group, int sms, cudaStream_t stream, Prof* prof) {
+  static bool d0[64] = {}, d1[64] = {}, d2[64] = {}, d3[64] = {};
+  a.cap = std::min(a.n, a.f.E + a.n / kW4Rows);  // a batch that is not full is an expert's last
+  const size_t smem = (size_t)a.cap * sizeof(W4Batch);
+  constexpr int most = (kMaxE + kMaxE * kGemmRows / kW4Rows) * (int)sizeof(W4Batch);
+  if (group == 32) {
+    MOE_CUDA_TRY(ensure_smem(w4_gateup_kernel<true>, most, d0));
+    MOE_CUDA_TRY(ensure_smem(w4_down_kernel<true>, most, d1));
+  } else {
+    MOE_CUDA_TRY(ensure_smem(w4_gateup_kernel<false>, most, d2));
+    MOE_CUDA_TRY(ensure_smem(w4_down_kernel<false>, most, d3));
+  }
   const dim3 grid(sms * kW4Ctas), block(kW4Threads);
   if (prof) prof->begin(MOE_PROF_FFN_GATEUP, stream);
   if (group == 32) w4_gateup_kernel<true><<<grid, block, smem, stream>>>(a);
@@ -638,7 +655,7 @@ int launch_ffn_w4(const FfnArgs& f, int group, void* ws, size_t ws_bytes, int ma
   const int n = f.T * f.k;
   if (ws_bytes < w4_ws_bytes(n, f.H, f.I)) return MOE_ERR_ALIGN;
   if (max_list <= 0) return MOE_OK;
-  if (w4_gemm_ffn(n)) return launch_ffn_w4_gemm(f, nullptr, nullptr, group, ws, nullptr, nullptr, stream, prof);
+  if (w4_gemm_ffn(n, f.E)) return launch_ffn_w4_gemm(f, nullptr, nullptr, group, ws, nullptr, nullptr, stream, prof);
   int sms = 0;
   const int r = w4_sms(&sms);
   if (r != MOE_OK) return r;
@@ -675,9 +692,9 @@ static W4ExpWs w4_exp_ws(void* base, int T, int H, int I, int k, int E) {
   w.n_act = (int32_t*)take(4);
   w.perm = (int32_t*)take(moe_permute_scratch_bytes(n, E) + 4);
   w.ready = (int32_t*)take(4 * (size_t)(H / 64));
-  const bool gemm = w4_gemm_ffn(n);  // its y is fp16 inside its own workspace
+  const bool gemm = w4_gemm_ffn(n, E);  // its y is fp16 inside its own workspace
   w.y = gemm ? nullptr : (float*)take(4 * (size_t)n * H);
-  w.ffn_bytes = gemm ? w4_ffn_gemm_ws(n, H, I, true) : w4_ws_bytes(n, H, I);
+  w.ffn_bytes = gemm ? w4_ffn_gemm_ws(n, H, I, true) : 4 * (size_t)n * I;
   w.ffn = take(w.ffn_bytes);
   w.bytes = off;
   return w;
@@ -771,7 +788,9 @@ extern "C" int moe_expert_ffn_w4(const void* x, int T, int H, int I, int k, int 
 
 extern "C" size_t moe_experts_w4_workspace_bytes(int T, int H, int I, int k, int E) {
   if (!shape_ok(T, H, I, k, E) || !w4_rows_ok(T, k)) return 0;
-  return w4_exp_ws(nullptr, T, H, I, k, E).bytes;
+  // fewer tokens may need more: the streams' y is fp32
+  const int most = std::min((std::max(kGemmRows * E, 129) - 1) / k, T);
+  return std::max(w4_exp_ws(nullptr, T, H, I, k, E).bytes, most > 0 ? w4_exp_ws(nullptr, most, H, I, k, E).bytes : 0);
 }
 
 extern "C" int moe_experts_w4(const void* x, const int32_t* ids, const float* w, int T, int H, int I, int k, int E,
@@ -791,18 +810,23 @@ extern "C" int moe_experts_w4(const void* x, const int32_t* ids, const float* w,
   f.T = T, f.H = H, f.I = I, f.k = k, f.E = E;
   f.pool = (const uint16_t*)pool, f.e2s = e2s, f.S = S, f.pool_only = 1;
   f.y = ws.y, f.status = dev_status;
-  if (!w4_gemm_ffn(n)) {
-    int sms = 0;
-    const int r = w4_sms(&sms);
-    if (r != MOE_OK) return r;
-    W4FfnArgs a{};
-    a.f = f, a.sl = w4_slab(H, I, group), a.h = (uint16_t*)ws.ffn, a.n = n;
-    a.ids = ids, a.w = w, a.out = (uint16_t*)out, a.ready = n <= kW4Fuse ? ws.ready : nullptr;
+  const bool gemm = w4_gemm_ffn(n, E);
+  int sms = 0, r = w4_sms(&sms);
+  if (r != MOE_OK) return r;
+  W4FfnArgs a{};
+  a.f = f, a.sl = w4_slab(H, I, group), a.h = (uint16_t*)ws.ffn, a.n = n;
+  a.w = w, a.out = (uint16_t*)out;
+  if (!gemm && n <= kW4Slots) {
+    a.ids = ids, a.ready = n <= kW4Fuse ? ws.ready : nullptr;
     return launch_ffn_w4_stream(a, group, sms, s, nullptr);
   }
-  int r = launch_permute(ids, n, E, ws.count, ws.offset, ws.rows, ws.pos, ws.act_e, ws.n_act, dev_status, ws.perm, s);
+  r = launch_permute(ids, n, E, ws.count, ws.offset, ws.rows, ws.pos, ws.act_e, ws.n_act, dev_status, ws.perm, s);
   if (r != MOE_OK) return r;
   f.offset = ws.offset, f.rows = ws.rows, f.list_e = ws.act_e, f.n_list = ws.n_act;
+  if (!gemm) {
+    a.f = f, a.pos = ws.pos;
+    return launch_ffn_w4_stream(a, group, sms, s, nullptr);
+  }
   const uint16_t* yh = nullptr;
   const int32_t* yexp = nullptr;
   if ((r = launch_ffn_w4_gemm(f, ids, ws.pos, group, ws.ffn, &yh, &yexp, s, nullptr)) != MOE_OK) return r;

@@ -1,4 +1,5 @@
-"""The 4-bit linear layer where it runs on the tensor cores' large tiles: from 17 rows, by rows x weights.
+"""The 4-bit operators at larger sizes: the linear layer on the large tensor-core tiles (from 17 rows, by rows x
+weights), and many experts of few rows.
 
 Compared with fp64 products of the unpacked weights, with the tolerance of the small sizes: (K / 32 + 40) fp32
 roundings of 2^-23 of the sum of |x w| at most (parts of the inputs that are summed apart add one rounding each,
@@ -7,7 +8,10 @@ of the 40), and half a unit in the last place of a bf16 output.
 import pytest
 import torch
 
-from tests.test_gpu_w4 import check_linear, draw_w4, dequant
+from tests._setup import rel_l2
+from tests.test_gpu_w4 import (RL2_OUT_BF16, check_linear, dequant, draw_experts, draw_routing, draw_w4,
+                               experts_plain)
+from tests import test_gpu_w4 as small
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -79,3 +83,45 @@ def test_same_result_every_time():
     with torch.cuda.stream(s):
         for _ in range(20):
             assert torch.equal(op.forward(x), want)
+
+
+# more routing slots than the stream kernels group themselves, few of them for each expert
+MANY_EXPERTS = [("qwen_T100", 2048, 768, 128, 8, 100, 128, 0.5), ("many_T600", 256, 128, 300, 4, 600, 64, 0.3),
+                ("most_T1100", 128, 64, 1024, 9, 1100, 32, 0.1), ("edge_T64", 448, 96, 100, 8, 64, 64, 0.0),
+                ("edge_T65", 448, 96, 100, 8, 65, 64, 0.0)]
+
+
+@pytest.mark.parametrize("name,H,I,E,k,T,group,skew", MANY_EXPERTS, ids=[c[0] for c in MANY_EXPERTS])
+def test_experts_of_few_rows(name, H, I, E, k, T, group, skew):
+    small.test_experts(name, H, I, E, k, T, group, skew)
+
+
+def test_experts_missing_slots_in_groups():
+    import expert_slot_cache_gb300 as M
+    H, I, E, k, group, S, T = 128, 64, 100, 6, 64, 90, 160
+    codes, scales = draw_experts(H, I, E, group, 3)
+    pool = M.w4_pack_slabs(codes[:S].contiguous(), scales[:S].contiguous(), H, I, group)
+    e2s = torch.full((E,), -1, dtype=torch.int32, device=DEV)
+    e2s[:S] = torch.arange(S, dtype=torch.int32, device=DEV)
+    x = torch.randn(T, H, device=DEV).to(torch.bfloat16)
+    ids, w = draw_routing(T, S, k, 5)
+    ids[3, 2], ids[5, 0], ids[7, 1] = -1, E, 95  # not experts; an expert without a slot
+    op = M.W4Experts(pool, H, I, k, E, group, e2s=e2s, max_tokens=T)
+    want = experts_plain(x, ids, w, codes, scales, H, I, group, skip=range(S, E))
+    assert rel_l2(op.forward(x, ids, w).double().cpu(), want.cpu()) <= RL2_OUT_BF16
+    assert int(op.dev_status.item()) != 0
+
+
+def test_experts_any_batch_up_to_the_largest():
+    """An operator made for many tokens takes every smaller batch, whichever way it is computed."""
+    import expert_slot_cache_gb300 as M
+    H, I, E, k, group = 128, 256, 20, 4, 64
+    codes, scales = draw_experts(H, I, E, group, 8)
+    pool = M.w4_pack_slabs(codes, scales, H, I, group)
+    for most in (50, 51, 600):
+        op = M.W4Experts(pool, H, I, k, E, group, max_tokens=most)
+        for T in sorted({1, 4, 5, 31, 32, 33, 49, 50, most}):
+            x = torch.randn(T, H, device=DEV).to(torch.bfloat16)
+            ids, w = draw_routing(T, E, k, T)
+            want = experts_plain(x, ids, w, codes, scales, H, I, group)
+            assert rel_l2(op.forward(x, ids, w).double().cpu(), want.cpu()) <= RL2_OUT_BF16, (most, T)
