@@ -21,10 +21,11 @@
 //
 // Warps: 0-15 are workers: four sets of four warps (one per TMEM lane quarter) that dequantise 128 inputs (a
 // visit) in turn, each set into TMEM columns of its own; all drain the accumulators.  16 loads the rows, 18 the
-// codes (which run further ahead), 17 allocates TMEM and, in the pair's first CTA, issues the MMAs (one lane).
+// codes, 17 allocates TMEM and, in the pair's first CTA, issues the MMAs (one lane).
 // A visit has one barrier for its rows' bytes and its workers' arrivals, and one commit gives both rings back:
 // with a barrier and a commit per stage and ring the issuing warp needed 390 cycles a stage, and 4096 rows
-// through 2048 x 4096 took 73 us, now 66.  Before a tile is drained three sets have dequantised inputs of the
+// through 2048 x 4096 took 73 us instead of 66 (54 since the drain spills no registers and launches overlap; its
+// MMAs alone would take 34).  Before a tile is drained three sets have dequantised inputs of the
 // next one, so the MMAs go on while the drained values are stored.
 // TMEM: 256 accumulator columns, 4 x 64 columns of weights.
 #include <limits.h>
@@ -43,7 +44,10 @@ constexpr int kGRows = 128;    // of them in one CTA's shared memory, at most
 constexpr int kGK = 64;        // inputs per stage
 constexpr int kGVisit = 2;     // stages that are copied, dequantised and multiplied at a time
 constexpr int kGSets = 4;      // sets of four worker warps, taking visits in turn; visits of rows in shared memory
-constexpr int kGWRing = 6;     // visits of codes in shared memory: four in the workers' hands, two on their way
+// Visits of codes in shared memory.  A multiple of the sets, so that a slot always belongs to the same set: copies
+// can land out of order, and a set that met another set's slot could take a phase that is still open, by its
+// parity, for the one after it.
+constexpr int kGWRing = kGSets;
 constexpr int kGWorkers = 4 * kGSets;
 constexpr int kGThreads = 96 + 32 * kGWorkers;
 constexpr int kGXBytes = kGRows * kGK * 2;      // a stage's rows
@@ -56,6 +60,7 @@ constexpr int kGEpiBytes = kGEpiRows * kGLd * 4;  // per worker warp
 constexpr uint32_t kGTmemCols = 512;
 constexpr uint32_t kGACol = kGN;                // first weight column
 static_assert(kGN == 64 * kGSets, "each set drains 64 rows");
+static_assert(kGWRing % kGSets == 0, "a slot of codes belongs to one set");
 
 enum { kGateUp = 0, kDown = 1, kLinear = 2 };
 

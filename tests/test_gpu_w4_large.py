@@ -125,3 +125,23 @@ def test_experts_any_batch_up_to_the_largest():
             ids, w = draw_routing(T, E, k, T)
             want = experts_plain(x, ids, w, codes, scales, H, I, group)
             assert rel_l2(op.forward(x, ids, w).double().cpu(), want.cpu()) <= RL2_OUT_BF16, (most, T)
+
+
+@pytest.mark.parametrize("H,I,E,k,T,group", [(2048, 768, 128, 8, 717, 32), (1024, 256, 64, 8, 500, 128)])
+def test_experts_same_result_every_time(H, I, E, k, T, group):
+    """Weights read from memory and from the caches, in turn: copies that land in any order."""
+    import expert_slot_cache_gb300 as M
+    codes, scales = draw_experts(H, I, E, group, T)
+    pool = M.w4_pack_slabs(codes, scales, H, I, group)
+    x = torch.randn(T, H, device=DEV).to(torch.bfloat16)
+    ids, w = draw_routing(T, E, k, T, 0.4)
+    op = M.W4Experts(pool, H, I, k, E, group, max_tokens=T)
+    want = op.forward(x, ids, w).clone()
+    assert rel_l2(want.double().cpu(), experts_plain(x, ids, w, codes, scales, H, I, group).cpu()) <= RL2_OUT_BF16
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device=DEV)
+    same = torch.ones((), dtype=torch.bool, device=DEV)
+    for i in range(400):
+        if i % 4 == 0:
+            flush.fill_(i % 256)
+        same &= (op.forward(x, ids, w) == want).all()
+    assert bool(same) and int(op.dev_status.item()) == 0
