@@ -126,7 +126,7 @@ __device__ __forceinline__ void mbar_arrive_pair(uint32_t caddr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
 
-// Waits for a barrier's phase, `polls` tests at most, in as few instructions as there can be: waiting warps
+// Waits for a barrier's phase, kGPolls tests at most, in as few instructions as there can be: waiting warps
 // share their schedulers with the workers.
 constexpr uint32_t kGPolls = 64;  // between looks at the abort flag
 __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
@@ -509,11 +509,12 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   volatile int* abort_flag = &s_abort;
-  // Waits as a whole warp.  A wait that gives up (or sees that another one did) ends the work of its role:
-  // `dead`, the same in every lane; a role that is dead waits no more.
+  // Waits as a whole warp, first with one test (the loops that issue copies are short of instructions: 4096 tokens
+  // 358 us, 350 with it).  A wait that gives up (or sees that another one did) ends the work of its role: `dead`,
+  // the same in every lane; a role that is dead waits no more.
   bool dead = false;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (dead || __all_sync(MOE_FULL_MASK, mbar_poll(bar, parity))) return;
+    if (__all_sync(MOE_FULL_MASK, mbar_try_wait(bar, parity)) || dead) return;
     bool ok = false;
     for (int i = 0; i < int(kWaitPolls / kGPolls) && !ok && !*abort_flag; ++i) ok = mbar_poll(bar, parity);
     if (!ok && !*abort_flag) {
@@ -891,7 +892,8 @@ __global__ void __launch_bounds__(kRowThreads) w4_group_rows_kernel(const W4RowA
 }
 
 // The same by token, where every slot is grouped: a row is read and scaled once and stored k times, its slots'
-// exponents found by a lane each.
+// exponents found by a lane each.  (4096 tokens of 2048, top 8: 26 us for the 128 MB it stores, 5.2 TB/s; by slot,
+// with the same arithmetic eight times, 50 us.)
 template <int NC>
 __global__ void __launch_bounds__(kTokenThreads) w4_token_rows_kernel(const W4RowArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = gridDim.x * (kTokenThreads / 32);
@@ -919,6 +921,7 @@ __global__ void __launch_bounds__(kTokenThreads) w4_token_rows_kernel(const W4Ro
 }
 
 // out[t] = bf16(sum_j w[t][j] y[pos[t][j]]) from the scaled fp16 rows, fp32, j ascending; 8 columns a thread.
+// Bound by memory: 144 MB for 4096 tokens of 2048, top 8, in 31 us (4.7 TB/s; with eight rows in flight 35 us).
 __global__ void __launch_bounds__(128) w4_combine_kernel(const uint16_t* __restrict__ yh,
                                                          const int32_t* __restrict__ yexp,
                                                          const float* __restrict__ w, const int32_t* __restrict__ pos,
