@@ -525,25 +525,27 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   };
 
   if (warp == kGWorkers) {
-    uint32_t vi = 0;  // visits issued
     const bool lead = elect_one();
+    uint32_t s = 0, ph = 1, issued = 0;
     for (int t = cl; t < total && !dead; t += ncl) {
       const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
       const int r = w4g_half(ti.ntok), row = ti.row0 + (int)rank * r;
-      for (int kb = 0; kb < ti.nk; kb += kGVisit, ++vi) {
-        const uint32_t s = vi % kGSets, use = vi / kGSets, nb = min(kGVisit, ti.nk - kb);
-        if (use > 0) wait(&empty[s], (use - 1) & 1u);
+      const uint32_t bytes = 2u * (uint32_t)r * (kGK * 2);  // of a stage, in both CTAs
+      for (int kb = ti.k0; kb < ti.k0 + ti.nk; kb += kGVisit) {
+        wait(&empty[s], ph);
         if (dead) break;
         if (lead) {
+          const uint32_t nb = min(kGVisit, ti.k0 + ti.nk - kb);
           // the first CTA's barrier counts the bytes of both
-          if (rank == 0) mbar_expect_tx(&full[s], 2u * nb * (uint32_t)r * (kGK * 2));
+          if (rank == 0) mbar_expect_tx(&full[s], nb * bytes);
           const uint32_t fb = mapa_shared(smem_u32(&full[s]), 0);
-          for (uint32_t h = 0; h < nb; ++h) {
-            unsigned char* dst = xs + (s * kGVisit + h) * kGXBytes;
-            const int c = (ti.k0 + kb + (int)h) * kGK;
-            if (r == kGRows) {
-              tma_load_3d_pair(dst, &mapX.m[0], fb, c, row, 0);
-            } else {
+          unsigned char* dst = xs + s * (kGVisit * kGXBytes);
+          if (r == kGRows) {
+            tma_load_3d_pair(dst, &mapX.m[0], fb, kb * kGK, row, 0);
+            if (nb > 1) tma_load_3d_pair(dst + kGXBytes, &mapX.m[0], fb, kb * kGK + kGK, row, 0);
+          } else {
+            for (uint32_t h = 0; h < nb; ++h, dst += kGXBytes) {
+              const int c = (kb + (int)h) * kGK;
               int o = 0;
               if (r & 64) {
                 tma_load_3d_pair(dst, &mapX.m[1], fb, c, row, 0);
@@ -558,54 +560,64 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
           }
         }
         __syncwarp();
+        ++issued;
+        s = (s + 1) % kGSets;
+        ph ^= s == 0;
       }
     }
     // after a timeout: let every copy land before the CTAs can exit (the workers' arrivals may be missing, so
     // that the barriers can only show it where they complete: the wait is short and bounded)
     if (dead && rank == 0)
-      for (uint32_t j = vi > kGSets ? vi - kGSets : 0; j < vi; ++j)
+      for (uint32_t j = issued > kGSets ? issued - kGSets : 0; j < issued; ++j)
         for (int i = 0; i < 1024 && !mbar_poll(&full[j % kGSets], (j / kGSets) & 1u); ++i) {
         }
   } else if (warp == kGWorkers + 2) {
-    uint32_t wi = 0;  // visits issued
     const bool lead = elect_one();
+    uint32_t s = 0, ph = 1, issued = 0;
     for (int t = cl; t < total && !dead; t += ncl) {
       const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
       const int blk = 2 * ti.ft + (int)rank;
       const uint32_t nm = max(0, min(8, d.Mt - 8 * blk));  // the tiles of 16 columns that exist
-      for (int kb = ti.k0; kb < ti.k0 + ti.nk; kb += kGVisit, ++wi) {
-        const uint32_t s = wi % kGWRing, use = wi / kGWRing, nb = min(kGVisit, ti.k0 + ti.nk - kb);
-        const uint32_t ng = d.G == 128 ? (nb + 1) / 2 : d.G == 64 ? nb : 2 * nb;
-        if (use > 0) wait(&wempty[s], (use - 1) & 1u);
+      const uint8_t* code = ti.base + w4_code_at(d, 8 * blk, ti.k0) * 512;
+      const uint8_t* scale = ti.base + d.scales + w4_scale_at(d, 8 * blk, ti.k0 * kGK / d.G, 0) * 4;
+      const uint32_t cb = nm * 512 * kGVisit, sb = nm * 32 * (kGVisit * kGK / d.G);  // of a whole visit
+      for (int kb = 0; kb < ti.nk; kb += kGVisit) {
+        wait(&wempty[s], ph);
         if (dead) break;
-        unsigned char* dst = wsm + s * kGWBytes;
         if (lead) {
+          unsigned char* dst = wsm + s * kGWBytes;
+          const bool whole = kb + kGVisit <= ti.nk;  // else one stage
+          const uint32_t c1 = whole ? cb : cb / 2, s1 = whole || d.G == 128 ? sb : sb / 2;
           if (nm > 0) {
-            mbar_expect_tx(&wfull[s], nm * (512 * nb + 32 * ng));
-            bulk_load(dst, ti.base + w4_code_at(d, 8 * blk, kb) * 512, nm * 512 * nb, &wfull[s]);
-            bulk_load(dst + kGCodeBytes, ti.base + d.scales + w4_scale_at(d, 8 * blk, kb * kGK / d.G, 0) * 4, nm * 32 * ng,
-                      &wfull[s]);
+            mbar_expect_tx(&wfull[s], c1 + s1);
+            bulk_load(dst, code, c1, &wfull[s]);
+            bulk_load(dst + kGCodeBytes, scale, s1, &wfull[s]);
           } else {
             mbar_arrive(&wfull[s]);  // the pair's second CTA has no columns here: its results are dropped
           }
         }
         __syncwarp();
+        code += cb, scale += sb;
+        ++issued;
+        s = (s + 1) % kGWRing;
+        ph ^= s == 0;
       }
     }
     if (dead)
-      for (uint32_t j = wi > kGWRing ? wi - kGWRing : 0; j < wi; ++j) mbar_wait(&wfull[j % kGWRing], (j / kGWRing) & 1u);
+      for (uint32_t j = issued > kGWRing ? issued - kGWRing : 0; j < issued; ++j)
+        mbar_wait(&wfull[j % kGWRing], (j / kGWRing) & 1u);
   } else if (warp == kGWorkers + 1) {
     if (rank == 0) {
       const uint64_t bd0 = smem_desc_l(smem_u32(xs), 16, 1024, kLayoutSw128);
       const bool lead = elect_one();
-      uint32_t vi = 0, tc = 0;  // visits, tiles
-      for (int t = cl; t < total && !dead; t += ncl, ++tc) {
+      uint32_t s = 0, ph = 0, tp = 1;  // of the ring, of the accumulators
+      for (int t = cl; t < total && !dead; t += ncl) {
         const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
         const uint32_t idesc = idesc_f16(2 * kGM, 2 * w4g_half(ti.ntok));
-        if (tc > 0) wait(tempty, (tc - 1) & 1u);
-        for (int kb = 0; kb < ti.nk; kb += kGVisit, ++vi) {
-          const uint32_t s = vi % kGSets;
-          wait(&full[s], (vi / kGSets) & 1u);
+        wait(tempty, tp);
+        tp ^= 1;
+        for (int kb = 0; kb < ti.nk; kb += kGVisit) {
+          wait(&full[s], ph);
           tc_fence_after();
           if (lead && !dead) {
             const uint32_t at = tmem + kGACol + s * 64;
@@ -615,6 +627,8 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
           }
           if (lead) umma_commit_pair(&empty[s]);
           __syncwarp();
+          s = (s + 1) % kGSets;
+          ph ^= s == 0;
         }
         if (lead) umma_commit_pair(tfull);
         __syncwarp();
@@ -667,7 +681,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
               w4_expand(w[j].x, s0, &o[4 * j]);
               w4_expand(w[j].y, s1, &o[16 + 4 * j]);
             }
-            if (h == 0 && uses > 0) wait(&empty[set], (uses - 1) & 1u);
+            if (h == 0) wait(&empty[set], (uses & 1u) ^ 1u);
             tc_fence_after();
             tmem_st32(a_addr + 32 * h, o);
           }
