@@ -79,7 +79,8 @@ struct W4GemmArgs {
   const int32_t* rexp;     // [n] the B operand's row p is 2^-rexp[p] times the true one
   const int32_t* oexp;     // [n] kGateUp: the same of h
   // outputs
-  uint16_t* h;             // kGateUp: fp16 [n][N / 2]
+  uint16_t* h;             // kGateUp: fp16 [n][ldh]
+  int ldh;
   uint16_t* yh;            // kDown: fp16 [n][N], 2^-(rexp + w4_y_exp) times y, or NULL
   float* y;                // kDown: fp32 [n][N]
   void* out;               // kLinear
@@ -87,10 +88,13 @@ struct W4GemmArgs {
   int out_f32;
 };
 
-// The rows as tensor maps with boxes of 128, 64, 32 and 16 rows x 64 inputs.
+// The rows as tensor maps with boxes of 16, 32, ... 128 rows x two stages: one copy a visit.
+constexpr int kGBoxes = kGRows / 16;
 struct W4RowMaps {
-  CUtensorMap m[4];
+  CUtensorMap m[kGBoxes];
 };
+// Rows are kept in whole stages, the rest zeros.
+__host__ __device__ inline int w4g_ld(int K) { return (K + kGK - 1) / kGK * kGK; }
 
 // One lane of the (converged) warp.  The loops that issue copies and MMAs are run by whole warps, so that
 // their operands stay in uniform registers; only the issue itself is one lane's.
@@ -226,7 +230,7 @@ __device__ __forceinline__ W4GTile w4g_tile(const W4GemmArgs& a, const int* pre,
 }
 
 // Rows of a tile in each CTA: half the MMA's N, which is a multiple of 32.
-__device__ __forceinline__ int w4g_half(int ntok) { return ((ntok + 31) & ~31) >> 1; }
+__host__ __device__ __forceinline__ int w4g_half(int ntok) { return ((ntok + 31) & ~31) >> 1; }
 
 // Eight codes of a word (w4.cuh) times their scale, fp16, inputs in order.
 __device__ __forceinline__ void w4_expand(uint32_t w, __half2 s, uint32_t* o) {
@@ -340,7 +344,7 @@ __device__ __forceinline__ void w4g_store32(const W4GemmArgs& a, const float* v,
   for (int j = 0; j < kGEpiRows; ++j) st[j * kGLd + lane] = v[j] * f.cm;
   __syncwarp();
   if (kMode == kGateUp) {  // columns 0-15: gate, 16-31: up of the same 16 features
-    const int f0 = c0 / 2, I = d.N / 2, row = lane >> 1, seg = (lane & 1) * 8;
+    const int f0 = c0 / 2, row = lane >> 1, seg = (lane & 1) * 8;
     const float x = row_fac(row),
                 xh = x * pow2(-__shfl_sync(MOE_FULL_MASK, f.o[i >> 1], 16 * (i & 1) + row));
     uint32_t o[4];
@@ -355,7 +359,7 @@ __device__ __forceinline__ void w4g_store32(const W4GemmArgs& a, const float* v,
       o[j / 2] = pack_f16(h(g.x, u.x), h(g.y, u.y));
       o[j / 2 + 1] = pack_f16(h(g.z, u.z), h(g.w, u.w));
     }
-    if (row < nrow) *reinterpret_cast<uint4*>(a.h + (row0 + row) * I + f0 + seg) = make_uint4(o[0], o[1], o[2], o[3]);
+    if (row < nrow) *reinterpret_cast<uint4*>(a.h + (row0 + row) * a.ldh + f0 + seg) = make_uint4(o[0], o[1], o[2], o[3]);
   } else {
     // (a part of the inputs writes sums of its own)
     float* out = kMode == kLinear ? reinterpret_cast<float*>(a.out) + (size_t)part * a.n * a.ldo : a.y;
@@ -530,34 +534,14 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     for (int t = cl; t < total && !dead; t += ncl) {
       const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
       const int r = w4g_half(ti.ntok), row = ti.row0 + (int)rank * r;
-      const uint32_t bytes = 2u * (uint32_t)r * (kGK * 2);  // of a stage, in both CTAs
+      const CUtensorMap* map = &mapX.m[r / 16 - 1];
       for (int kb = ti.k0; kb < ti.k0 + ti.nk; kb += kGVisit) {
         wait(&empty[s], ph);
         if (dead) break;
         if (lead) {
-          const uint32_t nb = min(kGVisit, ti.k0 + ti.nk - kb);
-          // the first CTA's barrier counts the bytes of both
-          if (rank == 0) mbar_expect_tx(&full[s], nb * bytes);
-          const uint32_t fb = mapa_shared(smem_u32(&full[s]), 0);
-          unsigned char* dst = xs + s * (kGVisit * kGXBytes);
-          if (r == kGRows) {
-            tma_load_3d_pair(dst, &mapX.m[0], fb, kb * kGK, row, 0);
-            if (nb > 1) tma_load_3d_pair(dst + kGXBytes, &mapX.m[0], fb, kb * kGK + kGK, row, 0);
-          } else {
-            for (uint32_t h = 0; h < nb; ++h, dst += kGXBytes) {
-              const int c = (kb + (int)h) * kGK;
-              int o = 0;
-              if (r & 64) {
-                tma_load_3d_pair(dst, &mapX.m[1], fb, c, row, 0);
-                o = 64;
-              }
-              if (r & 32) {
-                tma_load_3d_pair(dst + o * 128, &mapX.m[2], fb, c, row + o, 0);
-                o += 32;
-              }
-              if (r & 16) tma_load_3d_pair(dst + o * 128, &mapX.m[3], fb, c, row + o, 0);
-            }
-          }
+          // the first CTA's barrier counts the bytes of both (of two stages: past the last one zeros are read)
+          if (rank == 0) mbar_expect_tx(&full[s], 2u * kGVisit * (uint32_t)r * (kGK * 2));
+          tma_load_3d_pair(xs + s * (kGVisit * kGXBytes), map, mapa_shared(smem_u32(&full[s]), 0), 0, row, kb);
         }
         __syncwarp();
         ++issued;
@@ -613,7 +597,8 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
       uint32_t s = 0, ph = 0, tp = 1;  // of the ring, of the accumulators
       for (int t = cl; t < total && !dead; t += ncl) {
         const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
-        const uint32_t idesc = idesc_f16(2 * kGM, 2 * w4g_half(ti.ntok));
+        const int r = w4g_half(ti.ntok);
+        const uint32_t idesc = idesc_f16(2 * kGM, 2 * r);
         wait(tempty, tp);
         tp ^= 1;
         for (int kb = 0; kb < ti.nk; kb += kGVisit) {
@@ -623,7 +608,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
             const uint32_t at = tmem + kGACol + s * 64;
             const uint64_t bd = bd0 + (uint64_t)(s * kGVisit * (kGXBytes >> 4));
             umma_f16_ts_pair_k64(tmem, at, bd, idesc, kb > 0);
-            if (kb + 1 < ti.nk) umma_f16_ts_pair_k64(tmem, at + 32, bd + (kGXBytes >> 4), idesc, 1);
+            if (kb + 1 < ti.nk) umma_f16_ts_pair_k64(tmem, at + 32, bd + (uint64_t)(r * (kGK * 2 >> 4)), idesc, 1);
           }
           if (lead) umma_commit_pair(&empty[s]);
           __syncwarp();
@@ -728,7 +713,8 @@ struct W4RowArgs {
   const uint16_t* x;
   size_t ldx;
   int n, K;                // rows of xp, or of x with ids and pos
-  uint16_t* xp;            // fp16 [n][K]
+  uint16_t* xp;            // fp16 [n][ld], zeros past K
+  int ld;
   int32_t* xexp;           // [n]
   // grouped rows (list_e != NULL)
   W4GemmArgs g;
@@ -794,12 +780,13 @@ struct W4Row {
       }
     return nrm;
   }
-  __device__ __forceinline__ void store(uint16_t* row) const {
+  // To ld values, zeros past the row's own.
+  __device__ __forceinline__ void store(uint16_t* row, int ld) const {
     uint4* o = reinterpret_cast<uint4*>(row);
 #pragma unroll
     for (int i = 0; i < NC; ++i)
-      if (step * i + i0 < n) o[step * i + i0] = v[i];
-    for (int c = step * NC + i0; c < n; c += step) o[c] = conv(__ldg(x + c));
+      if (step * i + i0 < ld / 8) o[step * i + i0] = v[i];
+    for (int c = step * NC + i0; c < ld / 8; c += step) o[c] = c < n ? conv(__ldg(x + c)) : make_uint4(0, 0, 0, 0);
   }
 };
 
@@ -822,7 +809,7 @@ __global__ void __launch_bounds__(kRowThreads) w4_rows_kernel(const W4RowArgs a)
   for (int p = blockIdx.x * (kRowThreads / 32) + warp; p < a.n; p += nw) {
     W4Row<NC> r;
     w4_warp_row<false>(r, a.x + (size_t)p * a.ldx, a.K, lane);
-    r.store(a.xp + (size_t)p * a.K);
+    r.store(a.xp + (size_t)p * a.ld, a.ld);
     if (lane == 0) a.xexp[p] = r.xe;
   }
 }
@@ -843,7 +830,7 @@ __global__ void __launch_bounds__(kRowThreads) w4_few_rows_kernel(const W4RowArg
     __syncthreads();
     for (int i = 0; i < per; ++i) amax = max(amax, s_max[buf][warp - sub + i]);
     r.scale<false>(amax);
-    r.store(a.xp + (size_t)p * a.K);
+    r.store(a.xp + (size_t)p * a.ld, a.ld);
     if (sub == 0 && lane == 0) a.xexp[p] = r.xe;
   }
 }
@@ -857,6 +844,12 @@ __device__ __forceinline__ void w4_row_exps(const W4RowArgs& a, int slot, int p,
   a.xexp[p] = xe;
   a.hexp[p] = he;
   a.yexp[p] = he + w4_y_exp(base + a.sl.dn_at, a.sl.dn);
+}
+
+// Zeros past a row of h.
+__device__ __forceinline__ void w4_pad_h(const W4RowArgs& a, size_t p, int lane) {
+  for (int c = a.sl.dn.K / 8 + lane; c < a.g.ldh / 8; c += 32)
+    reinterpret_cast<uint4*>(a.g.h + p * a.g.ldh)[c] = make_uint4(0, 0, 0, 0);
 }
 
 template <int NC>
@@ -900,7 +893,8 @@ __global__ void __launch_bounds__(kRowThreads) w4_group_rows_kernel(const W4RowA
     }
     W4Row<NC> r;
     const int ln = w4_warp_row<true>(r, a.x + (size_t)(a.rows[p] / a.k) * a.ldx, a.K, lane);
-    r.store(a.xp + (size_t)p * a.K);
+    r.store(a.xp + (size_t)p * a.ld, a.ld);
+    w4_pad_h(a, p, lane);
     if (lane == 0) w4_row_exps(a, slot, p, r.xe, ln);
   }
 }
@@ -928,8 +922,11 @@ __global__ void __launch_bounds__(kTokenThreads) w4_token_rows_kernel(const W4Ro
           p = -1;
         }
       }
-      for (unsigned m = __ballot_sync(MOE_FULL_MASK, p >= 0); m; m &= m - 1)
-        r.store(a.xp + (size_t)__shfl_sync(MOE_FULL_MASK, p, __ffs(m) - 1) * a.K);
+      for (unsigned m = __ballot_sync(MOE_FULL_MASK, p >= 0); m; m &= m - 1) {
+        const size_t at = __shfl_sync(MOE_FULL_MASK, p, __ffs(m) - 1);
+        r.store(a.xp + at * a.ld, a.ld);
+        w4_pad_h(a, at, lane);
+      }
     }
   }
 }
@@ -979,12 +976,12 @@ constexpr size_t kGSmem = 1024 + (size_t)kGSets * kGVisit * kGXBytes + (size_t)k
                           (size_t)kGWorkers * kGEpiBytes + 64 * sizeof(uint64_t);
 static_assert(kGSmem <= 222 * 1024, "shared memory of a CTA, with the 4.3 KB of static arrays");
 
-// [n][K] 16-bit rows; boxes of 128, 64, 32 and 16 rows x one stage (what lies outside reads as 0).
-static int row_maps(W4RowMaps* rm, const void* base, int n, int K) {
-  const uint64_t d[3] = {(uint64_t)K, (uint64_t)n, 1};
-  const uint64_t s[2] = {(uint64_t)K * 2, (uint64_t)n * K * 2};
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t b[3] = {kGK, (uint32_t)(kGRows >> i), 1};
+// [n][ld] 16-bit rows as [stages][n][64]; what lies outside reads as 0.
+static int row_maps(W4RowMaps* rm, const void* base, int n, int K, unsigned boxes) {
+  const uint64_t ld = w4g_ld(K), d[3] = {kGK, (uint64_t)n, ld / kGK}, s[2] = {ld * 2, kGK * 2};
+  for (int i = 0; i < kGBoxes; ++i) {
+    if (!(boxes >> i & 1)) continue;
+    const uint32_t b[3] = {kGK, 16u * (i + 1), kGVisit};
     const int r = encode_tmap_3d_bf16(&rm->m[i], base, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B);
     if (r != MOE_OK) return r;
   }
@@ -999,8 +996,14 @@ static int launch_gemm(const W4GemmArgs& g, const void* rows, cudaStream_t s) {
   MOE_CUDA_TRY(ensure_smem(w4_gemm_kernel<kMode>, (int)kGSmem, done));
   int dev = 0;
   MOE_CUDA_TRY(cudaGetDevice(&dev));
-  W4RowMaps m;
-  if (row_maps(&m, rows, g.n, g.K) != MOE_OK) return MOE_ERR_CUDA;
+  // one matrix has full row tiles and a last one; groups have any
+  unsigned boxes = (1u << kGBoxes) - 1;
+  if (kMode == kLinear) {
+    boxes = g.n >= kGN ? 1u << (kGBoxes - 1) : 0;
+    if (g.n % kGN) boxes |= 1u << (w4g_half(g.n % kGN) / 16 - 1);
+  }
+  W4RowMaps m = {};
+  if (row_maps(&m, rows, g.n, g.K, boxes) != MOE_OK) return MOE_ERR_CUDA;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -1044,7 +1047,7 @@ static int w4_part_ld(int N) { return (N + 3) & ~3; }
 // Enough for any number of rows up to T: parts x rows <= kGPairs / (column tiles) x min(T, kGN).
 size_t w4_linear_gemm_ws(int T, const W4Dims& d) {
   const size_t nf = (d.N + 2 * kGM - 1) / (2 * kGM);
-  return g256(2 * (size_t)T * d.K) + g256(4 * (size_t)T) +
+  return g256(2 * (size_t)T * w4g_ld(d.K)) + g256(4 * (size_t)T) +
          (2 * nf > kGPairs ? 0 : 4 * (kGPairs / nf) * std::min(T, kGN) * w4_part_ld(d.N));
 }
 
@@ -1088,8 +1091,8 @@ int launch_w4_linear_gemm(const uint16_t* x, size_t ldx, int T, const uint8_t* w
                           size_t ldo, int out_f32, void* ws, int32_t* status, cudaStream_t s) {
   W4RowArgs r{};
   r.x = x, r.ldx = ldx, r.n = T, r.K = d.K;
-  r.xp = (uint16_t*)ws;
-  r.xexp = (int32_t*)((char*)ws + g256(2 * (size_t)T * d.K));
+  r.xp = (uint16_t*)ws, r.ld = w4g_ld(d.K);
+  r.xexp = (int32_t*)((char*)ws + g256(2 * (size_t)T * r.ld));
   // a warp to a row while there is a row for every scheduler twice; several warps where a row's latency is what
   // counts (33 rows of 4096: 15.6 us with one, 12.7 with four; 4096 rows of 2048: 53.5 with one, 55 with two)
   if (T >= 1216) {
@@ -1116,9 +1119,9 @@ int launch_w4_linear_gemm(const uint16_t* x, size_t ldx, int T, const uint8_t* w
   return MOE_OK;
 }
 
-// Workspace: x' [n][H] fp16, h [n][I] fp16, exponents, and y [n][H] fp16 where the caller combines.
+// Workspace: x' [n][H] and h [n][I] fp16 in whole stages, exponents, and y [n][H] fp16 where the caller combines.
 size_t w4_ffn_gemm_ws(size_t n, int H, int I, bool yh) {
-  return g256(2 * n * H) + g256(2 * n * I) + 3 * g256(4 * n) + (yh ? g256(2 * n * H) : 0);
+  return g256(2 * n * w4g_ld(H)) + g256(2 * n * w4g_ld(I)) + 3 * g256(4 * n) + (yh ? g256(2 * n * H) : 0);
 }
 
 // y rows of the listed experts (fp32 f.y, or scaled fp16 with *yh / *yexp set for launch_w4_combine).  ids and pos:
@@ -1135,8 +1138,9 @@ int launch_ffn_w4_gemm(const FfnArgs& f, const int32_t* ids, const int32_t* pos,
   };
   W4RowArgs r{};
   r.x = f.x, r.ldx = f.H, r.n = (int)n, r.K = f.H;
-  r.xp = (uint16_t*)take(2 * n * f.H);
-  uint16_t* h = (uint16_t*)take(2 * n * f.I);
+  r.ld = w4g_ld(f.H);
+  r.xp = (uint16_t*)take(2 * n * r.ld);
+  uint16_t* h = (uint16_t*)take(2 * n * w4g_ld(f.I));
   r.xexp = (int32_t*)take(4 * n);
   r.hexp = (int32_t*)take(4 * n);
   r.yexp = (int32_t*)take(4 * n);
@@ -1145,7 +1149,7 @@ int launch_ffn_w4_gemm(const FfnArgs& f, const int32_t* ids, const int32_t* pos,
   g.K = f.H, g.n = (int)n, g.NF = (2 * f.I + 2 * kGM - 1) / (2 * kGM);
   g.offset = f.offset, g.list_e = f.list_e, g.n_list = f.n_list, g.e2s = f.e2s, g.list_s = f.list_s;
   g.E = f.E, g.S = f.S, g.status = f.status;
-  g.rexp = r.xexp, g.oexp = r.hexp, g.h = h;
+  g.rexp = r.xexp, g.oexp = r.hexp, g.h = h, g.ldh = w4g_ld(f.I);
   r.g = g, r.rows = f.rows, r.k = f.k, r.sl = sl;
   r.y = yh ? nullptr : f.y;
   if (prof) prof->begin(MOE_PROF_FFN_ROWS, s);
