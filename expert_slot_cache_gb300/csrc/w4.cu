@@ -34,9 +34,9 @@ constexpr int kW4Ctas = 2;   // resident CTAs per SM that the registers allow
 constexpr int kW4Fuse = 16;
 constexpr int kW4Slots = 512;  // routing slots that the stream kernels group themselves; more are grouped before them
 // Rows of an expert, on average, from which the tensor-core path takes over: a stream pays for every eight rows of an
-// expert, a large tile hardly for any of its 256.  us, streams / tensor cores: 8 experts, 12 rows each 24.9 / 32.6, 16
-// rows 34.1 / 33.3, 48 rows 62.8 / 34.0; 32 experts, 8 rows 29.0 / 37.5, 12 rows 36.2 / 36.6; 128 experts, 3 rows
-// 104 / 167.
+// expert, a large tile hardly for any of its 256.  us, streams / tensor cores: 8 experts, 12 rows each 25.1 / 30.1, 24
+// rows 39.2 / 32.0, 48 rows 62.8 / 32.9; 32 experts, 8 rows 29.5 / 36.0, 12 rows 36.4 / 34.2; 128 experts, 6 rows
+// 122 / 154, 8 rows 153 / 154, 12 rows 195 / 157.
 constexpr int kGemmRows = 10;
 
 // One block of 64 inputs in registers: a lane's codes of CM tiles, their columns' scales, and the lane's inputs
@@ -702,8 +702,8 @@ static W4ExpWs w4_exp_ws(void* base, int T, int H, int I, int k, int E) {
 
 // Streams take a pass over the weights per 32 rows, about 0.55 us for 10^6 of them; the tensor-core path costs 8 us
 // and more (rows, launches, the pipeline's start) and then little.  us, streams / tensor cores: 17 rows, 4096 x 4096
-// 10.9 / 12.1, x 16384 33.8 / 21.9; 33 rows, 4096 x 4096 19.9 / 12.8, 1024 x 8192 13.3 / 10.3; 128 rows, 2048 x 2048
-// 15.1 / 11.5, 1024 x 1024 6.3 / 10.5; 512 rows, 1024 x 1024 18.7 / 12.2, 512 x 512 8.4 / 11.0.
+// 11.3 / 11.9, x 16384 35.2 / 19.1; 33 rows, 4096 x 4096 20.3 / 12.6, 1024 x 8192 13.3 / 10.4; 128 rows, 2048 x 2048
+// 15.2 / 11.7, 1024 x 1024 6.2 / 10.7; 512 rows, 1024 x 1024 18.7 / 12.7, 512 x 512 8.4 / 11.2.
 static bool w4_gemm_linear(int T, int K, int N) {
   const double work = (double)((T + 31) / 32) * K * N;
   return T > 16 && work >= (T > 32 ? 1 << 24 : 1 << 25);

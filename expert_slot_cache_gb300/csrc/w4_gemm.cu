@@ -1033,12 +1033,13 @@ static int launch_gemm(const W4GemmArgs& g, const void* rows, cudaStream_t s) {
 static size_t g256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // Parts of the inputs: where there are fewer tiles than pairs of SMs, as many as there are pairs for, of kGPart
-// stages or more.  (256 rows through 4096 x 4096, four parts: 16.7 us, undivided 28; through 8192 x 1024, 16 parts:
-// 19 and 52.  Parts of 8 stages against 16: 2048 x 2048 13.3 and 14.4 us, 8192 x 1024 19.2 and 17.2.)
-constexpr int kGPairs = 76, kGPart = 8;
+// stages or more, kGMostParts at most: each adds its sums to write and read.  (256 rows through 4096 x 4096, four
+// parts: 17.2 us, undivided 26.4; 8192 x 1024, eight parts of 16 stages 17.7, sixteen of 8 20.0, undivided 42.9;
+// 2048 x 2048, four parts of 8 stages 13.7, two of 16 15.0, undivided 17.9.)
+constexpr int kGPairs = 76, kGPart = 8, kGMostParts = 8;
 static void w4_parts(int T, const W4Dims& d, int& parts, int& stages) {
   const int64_t tiles = (int64_t)((T + kGN - 1) / kGN) * ((d.N + 2 * kGM - 1) / (2 * kGM));
-  parts = (int)std::min<int64_t>(kGPairs / tiles, d.Kb / kGPart);
+  parts = (int)std::min<int64_t>(kGPairs / tiles, std::min(d.Kb / kGPart, kGMostParts));
   stages = parts < 2 ? d.Kb : ((d.Kb + parts - 1) / parts + kGVisit - 1) / kGVisit * kGVisit;
   parts = (d.Kb + stages - 1) / stages;
 }
