@@ -29,9 +29,6 @@ namespace moe {
 constexpr int kW4Warps = 8;
 constexpr int kW4Threads = 32 * kW4Warps;
 constexpr int kW4Ctas = 2;   // resident CTAs per SM that the registers allow
-// Routing slots up to which the down kernel adds the experts up itself: the sums then fall to the few CTAs that
-// finish last (one token 20.5 us against 24.6 us with a kernel for them, 32 tokens 142 against 133 us).
-constexpr int kW4Fuse = 16;
 constexpr int kW4Slots = 512;  // routing slots that the stream kernels group themselves; more are grouped before them
 // Rows of an expert, on average, from which the tensor-core path takes over: a stream pays for every eight rows of an
 // expert, a large tile hardly for any of its 256.  us, streams / tensor cores: 8 experts, 12 rows each 25.1 / 30.1, 24
@@ -312,13 +309,12 @@ struct W4FfnArgs {
   W4Slab sl;
   uint16_t* h;            // bf16 [2][n][I]: h = h[0] + h[1]
   int n;                  // routing slots
-  // Routed form: the groups come from the ids (row = flat routing slot), the combine follows in the down kernel.
+  // Routed form: the groups come from the ids (row = flat routing slot), the combine follows in w4_sum_kernel.
   const int32_t* ids;     // [n], or NULL: f.offset / f.rows / f.list_e / f.n_list (row = grouped position)
   const int32_t* pos;     // [n] row of y of every slot, where the groups are given and the combine follows
   int cap;                // row batches that there can be
   const float* w;         // [n]
   uint16_t* out;          // bf16 [T][H]
-  int32_t* ready;         // [H / 64] row batches done per 64 output columns, or NULL: w4_sum_kernel follows
 };
 
 // At most eight rows of one expert.
@@ -428,11 +424,9 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_gateup_kernel(const W4
   extern __shared__ W4Batch tab[];
   __shared__ float red[2 * kW4Warps * kGuTiles * 128];
   __shared__ int tmp[33];
-  pdl_trigger();  // the down kernel may start: it waits for this one before it reads h or the counters
+  pdl_trigger();  // the down kernel may start: it waits for this one before it reads h
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const W4Dims& d = a.sl.gu;
-  if (a.ready && blockIdx.x == 0)
-    for (int i = threadIdx.x; i < a.f.H / 64; i += kW4Threads) a.ready[i] = 0;
   const int nbat = w4_batches(a, tab, reinterpret_cast<int*>(red), tmp);
   const int FT = (d.Mt + kGuTiles - 1) / kGuTiles, I = d.N / 2, units = nbat * FT;
   const int ks = w4_split(units, d.Kb, gridDim.x), sub = kW4Warps / ks;
@@ -473,35 +467,9 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_gateup_kernel(const W4
   });
 }
 
-// out[t] = bf16(sum_j w[t][j] y[t k + j]), fp32, j ascending, for the 64 columns of each of the `n` groups cg[].
-__device__ __forceinline__ void w4_combine_columns(const W4FfnArgs& a, const int* cg, int n) {
-  const int H = a.f.H, k = a.f.k;
-  for (int i = threadIdx.x; i < n * a.f.T * 16; i += kW4Threads) {
-    const int t = (i >> 4) % a.f.T, c = cg[(i >> 4) / a.f.T] * 64 + (i & 15) * 4;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j0 = 0; j0 < k; j0 += 4) {
-      float4 y[4];
-      float w[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {  // four rows in flight
-        const int j = j0 + u, at = t * k + min(j, k - 1), e = a.ids[at];
-        const bool ok = j < k && e >= 0 && e < a.f.E;
-        w[u] = ok ? a.w[at] : 0.f;
-        y[u] = ok ? __ldcg(reinterpret_cast<const float4*>(a.f.y + (size_t)at * H + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        s.x = fmaf(w[u], y[u].x, s.x), s.y = fmaf(w[u], y[u].y, s.y);
-        s.z = fmaf(w[u], y[u].z, s.z), s.w = fmaf(w[u], y[u].w, s.w);
-      }
-    }
-    *reinterpret_cast<uint2*>(a.out + (size_t)t * H + c) =
-        make_uint2(uint32_t(f32_to_bf16(s.x)) | uint32_t(f32_to_bf16(s.y)) << 16,
-                   uint32_t(f32_to_bf16(s.z)) | uint32_t(f32_to_bf16(s.w)) << 16);
-  }
-}
-
-// The same for any number of rows, as a kernel of its own: grid (T, H / 512).
+// out[t] = bf16(sum_j w[t][j] y[slot]), fp32, j ascending: grid (T, H / 512).  (Sums by the CTAs of the down kernel
+// that finish last save this launch, which overlaps, and cost as much: one token 16.6 us with them, 16.1 without;
+// 8 tokens 45.4 and 46.0.)
 __global__ void __launch_bounds__(128) w4_sum_kernel(const W4FfnArgs a) {
   pdl_wait();
   const int H = a.f.H, k = a.f.k, t = blockIdx.x, c = (blockIdx.y * 128 + threadIdx.x) * 4;
@@ -530,9 +498,7 @@ __global__ void __launch_bounds__(128) w4_sum_kernel(const W4FfnArgs a) {
                  uint32_t(f32_to_bf16(s.z)) | uint32_t(f32_to_bf16(s.w)) << 16);
 }
 
-// Down: unit = (row batch, four tiles of 16 output columns).  In the routed form with few rows (a.ready) the
-// CTA that finishes the last batch of a column group adds the experts up: no further launch, and the sums'
-// order is fixed.
+// Down: unit = (row batch, four tiles of 16 output columns).
 constexpr int kDnTiles = 4;
 template <bool G32>
 __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_down_kernel(const W4FfnArgs a) {
@@ -547,11 +513,8 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_down_kernel(const W4Ff
   const int rounds = (units - (int)blockIdx.x * sub + (int)gridDim.x * sub - 1) / ((int)gridDim.x * sub);
   if (rounds <= 0) {
     pdl_wait();
-    if (a.ready && nbat == 0)  // no expert at all
-      for (int cg = blockIdx.x; cg < a.f.H / 64; cg += gridDim.x) w4_combine_columns(a, &cg, 1);
     return;
   }
-  int* s_mine = reinterpret_cast<int*>(red);  // after the rounds: per column group
   auto index = [&](int r, int g) { return (r * (int)gridDim.x + (int)blockIdx.x) * sub + g; };
   auto down = [&](int slot) {
     return reinterpret_cast<const uint8_t*>(a.f.pool) + (size_t)slot * a.sl.bytes + a.sl.dn_at;
@@ -584,28 +547,6 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_down_kernel(const W4Ff
       a.f.y[(size_t)b.row[row] * d.N + n] = v;
     }
   });
-  if (!a.ready) return;
-  // count this CTA's units per column group; whoever brings a group's last one adds the experts up
-  __syncthreads();
-  for (int cg = threadIdx.x; cg < FT; cg += kW4Threads) s_mine[cg] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < rounds * sub; i += kW4Threads) {
-    const int u = index(i / sub, i % sub);
-    if (u < units) atomicAdd(&s_mine[u % FT], 1);
-  }
-  __syncthreads();
-  int* s_done = s_mine + FT;  // the groups that this CTA completed
-  if (threadIdx.x == 0) tmp[0] = 0;
-  __syncthreads();
-  for (int cg = threadIdx.x; cg < FT; cg += kW4Threads) {
-    const int mine = s_mine[cg];
-    if (mine == 0) continue;
-    __threadfence();
-    if (atomicAdd(&a.ready[cg], mine) + mine == nbat) s_done[atomicAdd(&tmp[0], 1)] = cg;
-  }
-  __syncthreads();
-  __threadfence();
-  w4_combine_columns(a, s_done, tmp[0]);
 }
 
 static int w4_sms(int* sms) {
@@ -644,7 +585,7 @@ static int launch_ffn_w4_stream(W4FfnArgs a, int group, int sms, cudaStream_t st
   if (prof) prof->begin(MOE_PROF_FFN_DOWN, stream);
   MOE_CUDA_TRY(launch_pdl(group == 32 ? w4_down_kernel<true> : w4_down_kernel<false>, grid, block, smem, stream, a));
   if (prof) prof->end(stream);
-  if (a.out && !a.ready)
+  if (a.out)
     MOE_CUDA_TRY(launch_pdl(w4_sum_kernel, dim3(a.f.T, (a.f.H + 511) / 512), dim3(128), 0, stream, a));
   return MOE_OK;
 }
@@ -669,7 +610,6 @@ static size_t al256(size_t v) { return (v + 255) & ~size_t(255); }
 // Workspace of moe_experts_w4: the groups of the permute, then y and the FFN's own.
 struct W4ExpWs {
   int32_t *count, *offset, *rows, *pos, *act_e, *n_act, *perm;
-  int32_t* ready;
   float* y;
   void* ffn;
   size_t ffn_bytes, bytes;
@@ -691,7 +631,6 @@ static W4ExpWs w4_exp_ws(void* base, int T, int H, int I, int k, int E) {
   w.act_e = (int32_t*)take(4 * (size_t)E);
   w.n_act = (int32_t*)take(4);
   w.perm = (int32_t*)take(moe_permute_scratch_bytes(n, E) + 4);
-  w.ready = (int32_t*)take(4 * (size_t)(H / 64));
   const bool gemm = w4_gemm_ffn(n, E);  // its y is fp16 inside its own workspace
   w.y = gemm ? nullptr : (float*)take(4 * (size_t)n * H);
   w.ffn_bytes = gemm ? w4_ffn_gemm_ws(n, H, I, true) : 4 * (size_t)n * I;
@@ -817,7 +756,7 @@ extern "C" int moe_experts_w4(const void* x, const int32_t* ids, const float* w,
   a.f = f, a.sl = w4_slab(H, I, group), a.h = (uint16_t*)ws.ffn, a.n = n;
   a.w = w, a.out = (uint16_t*)out;
   if (!gemm && n <= kW4Slots) {
-    a.ids = ids, a.ready = n <= kW4Fuse ? ws.ready : nullptr;
+    a.ids = ids;
     return launch_ffn_w4_stream(a, group, sms, s, nullptr);
   }
   r = launch_permute(ids, n, E, ws.count, ws.offset, ws.rows, ws.pos, ws.act_e, ws.n_act, dev_status, ws.perm, s);
