@@ -448,7 +448,9 @@ int moe_w4_quantize_slabs(const void* w, int n, int H, int I, int group, void* d
  *        with out_f32 = 1
  *   workspace  device, moe_w4_linear_workspace_bytes(T, K, N, group) bytes,
  *        256-byte aligned (may be NULL where that is 0)
- * Sums are fp32; the result does not depend on thread timing.
+ *        (a workspace for T rows is enough for fewer)
+ * Sums are fp32; the result does not depend on thread timing.  A row of x that
+ * holds an infinity or a NaN gives a row without finite values, no other.
  * Errors: MOE_ERR_ARG on NULL pointers, T < 1 or shapes out of range;
  * MOE_ERR_ALIGN if x or w is not 16-byte aligned, ldx % 8 != 0, or the
  * workspace is unaligned or too small.
@@ -478,7 +480,7 @@ int moe_expert_ffn_w4(const void* x, int T, int H, int I, int k, int E, int grou
  *   x device bf16 [T][H]; ids device int32 [T][k]; w device fp32 [T][k]
  *   out device bf16 [T][H]
  *   workspace device, moe_experts_w4_workspace_bytes(T, H, I, k, E) bytes,
- *        256-byte aligned
+ *        256-byte aligned (enough for fewer tokens, too)
  * An id outside [0, E) sets MOE_DEV_BAD_EXPERT, an expert without a slot
  * MOE_DEV_BAD_SLOT; either adds nothing to the sum.
  * Errors: as moe_expert_ffn_w4.
