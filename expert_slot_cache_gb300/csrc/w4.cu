@@ -16,10 +16,9 @@
 // that its loads do not pause; the activations of a block travel with its codes.  (A ring in shared memory,
 // filled by bulk copies or by cp.async, hid the latency better but cost instructions, which are what bounds
 // the stream: about 265 for 2 KB; 8 tokens took 58 and 59 us with those, 51 us with registers, 46 since the
-// shares are finer.)  The ks warps
-// that share a unit add up in shared memory, in warp order.  ks is the split that costs least for the unit
-// count at hand (w4_split): few long shares while there are units for every warp, short ones for a few small
-// matrices.
+// shares are finer.)  The ks warps that share a unit add up in shared memory, in warp order.  ks is the split
+// that costs least for the unit count at hand (w4_split): few long shares while there are units for every
+// warp, short ones for a few small matrices.
 #include <algorithm>
 
 #include "internal.cuh"
