@@ -8,6 +8,7 @@ of the 40), and half a unit in the last place of a bf16 output.
 import pytest
 import torch
 
+from harness import configs as C
 from tests._setup import rel_l2
 from tests.test_gpu_w4 import (RL2_OUT_BF16, check_linear, dequant, draw_experts, draw_routing, draw_w4,
                                experts_plain)
@@ -145,3 +146,11 @@ def test_experts_same_result_every_time(H, I, E, k, T, group):
             flush.fill_(i % 256)
         same &= (op.forward(x, ids, w) == want).all()
     assert bool(same) and int(op.dev_status.item()) == 0
+
+
+@pytest.mark.parametrize("mode,T,S,sched", [(C.MODE_RESIDENT, 120, 16, 0), (C.MODE_GATHER, 120, 8, C.SCHED_CHUNKS),
+                                            (C.MODE_GATHER, 120, 8, C.SCHED_WAVES)],
+                         ids=["resident", "gather_chunks", "gather_waves"])
+def test_layer_with_4bit_slabs(mode, T, S, sched):
+    """The layer's larger steps: experts of many rows, hits and misses as lists of their own."""
+    small.test_layer_with_4bit_slabs(mode, T, S, sched)
