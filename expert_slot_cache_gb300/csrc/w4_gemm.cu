@@ -969,7 +969,13 @@ __global__ void __launch_bounds__(128) w4_combine_kernel(const uint16_t* __restr
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) o[i] = uint32_t(f32_to_bf16(acc[2 * i])) | (uint32_t(f32_to_bf16(acc[2 * i + 1])) << 16);
-  *reinterpret_cast<uint4*>(out + (size_t)t * H + c) = make_uint4(o[0], o[1], o[2], o[3]);
+  uint16_t* at = out + (size_t)t * H + c;
+  if ((uintptr_t)at % 16 == 0) {
+    *reinterpret_cast<uint4*>(at) = make_uint4(o[0], o[1], o[2], o[3]);
+  } else {  // out is 8-byte aligned
+    *reinterpret_cast<uint2*>(at) = make_uint2(o[0], o[1]);
+    *reinterpret_cast<uint2*>(at + 4) = make_uint2(o[2], o[3]);
+  }
 }
 
 constexpr size_t kGSmem = 1024 + (size_t)kGSets * kGVisit * kGXBytes + (size_t)kGWRing * kGWBytes +

@@ -478,7 +478,7 @@ int moe_expert_ffn_w4(const void* x, int T, int H, int I, int k, int E, int grou
  *   out[t] = bf16( sum_{j=0..k-1} w[t][j] * FFN_{ids[t][j]}(x[t]) ), j ascending, fp32,
  * over a pool of packed 4-bit slabs (S slots; e2s as in moe_expert_ffn).
  *   x device bf16 [T][H]; ids device int32 [T][k]; w device fp32 [T][k]
- *   out device bf16 [T][H]
+ *   out device bf16 [T][H], 8-byte aligned
  *   workspace device, moe_experts_w4_workspace_bytes(T, H, I, k, E) bytes,
  *        256-byte aligned (enough for fewer tokens, too)
  * An id outside [0, E) sets MOE_DEV_BAD_EXPERT, an expert without a slot
