@@ -142,6 +142,30 @@ def _here(t: torch.Tensor, stream=None) -> int:
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
+def _on(dev: torch.device, **tensors) -> None:
+    """Refuses tensors that are not all on the CUDA device ``dev``: the kernels get their addresses as they are."""
+    if dev.type != "cuda":
+        raise ValueError(f"need tensors on a CUDA device, got {dev}")
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: on {t.device}, the call runs on {dev}")
+
+
+class _Current:
+    """Makes a device the current one, where it is not: the library launches on the current device."""
+
+    def __init__(self, dev: torch.device):
+        self.dev = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
+
+    def __enter__(self):
+        if self.dev is not None:
+            self.dev.__enter__()
+
+    def __exit__(self, *e):
+        if self.dev is not None:
+            self.dev.__exit__(*e)
+
+
 # ---------------------------------------------------------------------------
 # Single calls
 # ---------------------------------------------------------------------------
@@ -320,8 +344,10 @@ def w4_pack(codes: torch.Tensor, scales: torch.Tensor, group: int, stream=None) 
     K, N = codes.shape[-2:]
     _want(codes, "codes", torch.uint8)
     _want(scales, "scales", torch.bfloat16, (*codes.shape[:-2], -(-K // group) if group > 0 else 0, N))
-    out = torch.empty(*codes.shape[:-2], w4_bytes(K, N, group), dtype=torch.uint8, device=codes.device)
-    _ck(_w4_pack(_p(codes), _p(scales), codes[..., 0, 0].numel(), K, N, group, _p(out), _s(stream)), "moe_w4_pack")
+    _on(codes.device, scales=scales)
+    with _Current(codes.device):
+        out = torch.empty(*codes.shape[:-2], w4_bytes(K, N, group), dtype=torch.uint8, device=codes.device)
+        _ck(_w4_pack(_p(codes), _p(scales), codes[..., 0, 0].numel(), K, N, group, _p(out), _s(stream)), "moe_w4_pack")
     return out
 
 
@@ -329,8 +355,10 @@ def w4_quantize(w: torch.Tensor, group: int, stream=None) -> torch.Tensor:
     """bf16 [..., K, N] -> packed uint8 [..., w4_bytes]."""
     K, N = w.shape[-2:]
     _want(w, "w", torch.bfloat16)
-    out = torch.empty(*w.shape[:-2], w4_bytes(K, N, group), dtype=torch.uint8, device=w.device)
-    _ck(_w4_quantize(_p(w), w[..., 0, 0].numel(), K, N, group, _p(out), _s(stream)), "moe_w4_quantize")
+    _on(w.device)
+    with _Current(w.device):
+        out = torch.empty(*w.shape[:-2], w4_bytes(K, N, group), dtype=torch.uint8, device=w.device)
+        _ck(_w4_quantize(_p(w), w[..., 0, 0].numel(), K, N, group, _p(out), _s(stream)), "moe_w4_quantize")
     return out
 
 
@@ -340,8 +368,10 @@ def w4_pack_slabs(codes: torch.Tensor, scales: torch.Tensor, H: int, I: int, gro
     _want(codes, "codes", torch.uint8, (n, 3 * H * I))
     if group > 0:
         _want(scales, "scales", torch.bfloat16, (n, 2 * -(-H // group) * I + -(-I // group) * H))
-    out = torch.empty(n, w4_slab_bytes(H, I, group), dtype=torch.uint8, device=codes.device)
-    _ck(_w4_pack_slabs(_p(codes), _p(scales), n, H, I, group, _p(out), _s(stream)), "moe_w4_pack_slabs")
+    _on(codes.device, scales=scales)
+    with _Current(codes.device):
+        out = torch.empty(n, w4_slab_bytes(H, I, group), dtype=torch.uint8, device=codes.device)
+        _ck(_w4_pack_slabs(_p(codes), _p(scales), n, H, I, group, _p(out), _s(stream)), "moe_w4_pack_slabs")
     return out
 
 
@@ -349,8 +379,10 @@ def w4_quantize_slabs(slabs: torch.Tensor, H: int, I: int, group: int, stream=No
     """bf16 slabs [n][3HI] (device) -> packed 4-bit slabs uint8 [n][w4_slab_bytes] (device)."""
     n = slabs.shape[0]
     _want(slabs, "slabs", torch.bfloat16, (n, 3 * H * I))
-    out = torch.empty(n, w4_slab_bytes(H, I, group), dtype=torch.uint8, device=slabs.device)
-    _ck(_w4_quantize_slabs(_p(slabs), n, H, I, group, _p(out), _s(stream)), "moe_w4_quantize_slabs")
+    _on(slabs.device)
+    with _Current(slabs.device):
+        out = torch.empty(n, w4_slab_bytes(H, I, group), dtype=torch.uint8, device=slabs.device)
+        _ck(_w4_quantize_slabs(_p(slabs), n, H, I, group, _p(out), _s(stream)), "moe_w4_quantize_slabs")
     return out
 
 
@@ -381,26 +413,31 @@ class W4Linear:
             raise ValueError(f"x is {T} x {K}; the layer takes up to {self.max_tokens} rows of {self.K}")
         if x.dtype != torch.bfloat16 or x.stride(1) != 1:
             raise ValueError("x: need bf16 rows with a contiguous last dimension")
-        if out is None:
-            out = torch.empty(T, self.N, dtype=self.out_dtype, device=x.device)
-        elif out.dtype != self.out_dtype or out.shape != (T, self.N) or out.stride(1) != 1:
+        if out is not None and (out.dtype != self.out_dtype or out.shape != (T, self.N) or out.stride(1) != 1):
             raise ValueError(f"out: need {self.out_dtype} ({T}, {self.N}) with a contiguous last dimension")
-        _ck(_w4_linear(x.data_ptr(), x.stride(0) if T > 1 else K, T, K, self.N, self.group, self._packed,
-                       out.data_ptr(), out.stride(0) if T > 1 else self.N, self._f32, self._ws, self._ws_bytes,
-                       self._status, _here(x, stream)), "moe_w4_linear")
+        _on(self.packed.device, x=x, out=out)
+        with _Current(x.device):
+            if out is None:
+                out = torch.empty(T, self.N, dtype=self.out_dtype, device=x.device)
+            _ck(_w4_linear(x.data_ptr(), x.stride(0) if T > 1 else K, T, K, self.N, self.group, self._packed,
+                           out.data_ptr(), out.stride(0) if T > 1 else self.N, self._f32, self._ws, self._ws_bytes,
+                           self._status, _here(x, stream)), "moe_w4_linear")
         return out
 
 
 def expert_ffn_w4(x, k, I, E, group, offset, rows, list_e, n_list, max_list, pool, e2s=None, y=None, workspace=None,
                   dev_status=None, stream=None) -> torch.Tensor:
     T, H = x.shape
-    if y is None:
-        y = torch.zeros(T * k, H, dtype=torch.float32, device=x.device)
-    if workspace is None:
-        workspace = torch.empty(int(_ffn_w4_ws(T, H, k, I)), dtype=torch.uint8, device=x.device)
-    _ck(_ffn_w4(_p(x), T, H, I, k, E, group, _p(offset), _p(rows), _p(list_e), _p(n_list), max_list, _p(pool),
-                pool.shape[0], _p(e2s), _p(y), _p(workspace), workspace.numel(), _p(dev_status), _s(stream)),
-        "moe_expert_ffn_w4")
+    _on(x.device, offset=offset, rows=rows, list_e=list_e, n_list=n_list, pool=pool, e2s=e2s, y=y, workspace=workspace,
+        dev_status=dev_status)
+    with _Current(x.device):
+        if y is None:
+            y = torch.zeros(T * k, H, dtype=torch.float32, device=x.device)
+        if workspace is None:
+            workspace = torch.empty(int(_ffn_w4_ws(T, H, k, I)), dtype=torch.uint8, device=x.device)
+        _ck(_ffn_w4(_p(x), T, H, I, k, E, group, _p(offset), _p(rows), _p(list_e), _p(n_list), max_list, _p(pool),
+                    pool.shape[0], _p(e2s), _p(y), _p(workspace), workspace.numel(), _p(dev_status), _s(stream)),
+            "moe_expert_ffn_w4")
     return y
 
 
@@ -437,13 +474,15 @@ class W4Experts:
             raise ValueError(f"ids: need contiguous int32 [{T}][{self.k}]")
         if w.dtype != torch.float32 or w.shape != (T, self.k) or not w.is_contiguous():
             raise ValueError(f"w: need contiguous fp32 [{T}][{self.k}]")
-        if out is None:
-            out = torch.empty(T, self.H, dtype=torch.bfloat16, device=x.device)
-        else:
+        if out is not None:
             _want(out, "out", torch.bfloat16, (T, self.H))
-        _ck(_experts_w4(x.data_ptr(), ids.data_ptr(), w.data_ptr(), T, self.H, self.I, self.k, self.E, self.group,
-                        self._pool, self.S, self._e2s, out.data_ptr(), self._ws, self._ws_bytes, self._status,
-                        _here(x, stream)), "moe_experts_w4")
+        _on(self.pool.device, x=x, ids=ids, w=w, e2s=self.e2s, out=out)
+        with _Current(x.device):
+            if out is None:
+                out = torch.empty(T, self.H, dtype=torch.bfloat16, device=x.device)
+            _ck(_experts_w4(x.data_ptr(), ids.data_ptr(), w.data_ptr(), T, self.H, self.I, self.k, self.E, self.group,
+                            self._pool, self.S, self._e2s, out.data_ptr(), self._ws, self._ws_bytes, self._status,
+                            _here(x, stream)), "moe_experts_w4")
         return out
 
 
@@ -478,16 +517,18 @@ def balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float, seq_start
     if grad_loss is not None and (grad_loss.dtype != torch.float32 or grad_loss.numel() != 1):
         raise ValueError("grad_loss: need one fp32 value")
     dev = logits.device
-    loss = torch.empty((), dtype=torch.float32, device=dev) if with_loss else None
-    counts = torch.empty((max(n_seq, 0), E), dtype=torch.int32, device=dev)
-    grad = torch.empty_like(logits) if with_grad else None
-    nws = _balance_ws(T, E, n_seq)
-    ws = torch.empty(nws, dtype=torch.uint8, device=dev)
-    _ck(_balance(logits.data_ptr(), bf16, ids.data_ptr(), None if token_mask is None else token_mask.data_ptr(),
-                 None if seq_start is None else seq_start.data_ptr(), n_seq, T, E, k, ROUTE_SIGMOID if sigmoid else 0,
-                 coef, None if grad_loss is None else grad_loss.data_ptr(), counts.data_ptr(),
-                 loss.data_ptr() if with_loss else None, grad.data_ptr() if with_grad else None, ws.data_ptr(), nws,
-                 None if dev_status is None else dev_status.data_ptr(), _here(logits, stream)), "moe_balance_loss")
+    _on(dev, ids=ids, seq_start=seq_start, token_mask=token_mask, grad_loss=grad_loss, dev_status=dev_status)
+    with _Current(dev):
+        loss = torch.empty((), dtype=torch.float32, device=dev) if with_loss else None
+        counts = torch.empty((max(n_seq, 0), E), dtype=torch.int32, device=dev)
+        grad = torch.empty_like(logits) if with_grad else None
+        nws = _balance_ws(T, E, n_seq)
+        ws = torch.empty(nws, dtype=torch.uint8, device=dev)
+        _ck(_balance(logits.data_ptr(), bf16, ids.data_ptr(), None if token_mask is None else token_mask.data_ptr(),
+                     None if seq_start is None else seq_start.data_ptr(), n_seq, T, E, k, ROUTE_SIGMOID if sigmoid else 0,
+                     coef, None if grad_loss is None else grad_loss.data_ptr(), counts.data_ptr(),
+                     loss.data_ptr() if with_loss else None, grad.data_ptr() if with_grad else None, ws.data_ptr(), nws,
+                     None if dev_status is None else dev_status.data_ptr(), _here(logits, stream)), "moe_balance_loss")
     return Balance(loss, counts, grad)
 
 
