@@ -8,6 +8,8 @@ library is missing, importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 from ctypes import POINTER, c_float, c_int, c_int32, c_size_t, c_void_p
 from dataclasses import dataclass
@@ -151,6 +153,21 @@ def _on(dev: torch.device, **tensors) -> None:
             raise ValueError(f"{name}: on {t.device}, the call runs on {dev}")
 
 
+def _for_its_stream(call):
+    """A call given a ``stream`` allocates its temporaries and results for that stream.  From the current stream's pool
+    a temporary, free again on return, could go to the current stream's next work while the kernels still use it."""
+    at = list(inspect.signature(call).parameters).index("stream")
+
+    @functools.wraps(call)
+    def on(*args, **kwargs):
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        if stream is None:
+            return call(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return call(*args, **kwargs)
+    return on
+
+
 class _Current:
     """Makes a device the current one, where it is not: the library launches on the current device."""
 
@@ -170,6 +187,7 @@ class _Current:
 # Single calls
 # ---------------------------------------------------------------------------
 
+@_for_its_stream
 def bias_table(b: torch.Tensor, n_hot: int, cap: float, stream=None, mode: int = BIAS_GRADED) -> torch.Tensor:
     out = torch.empty_like(b)
     if mode == BIAS_GRADED:
@@ -179,6 +197,7 @@ def bias_table(b: torch.Tensor, n_hot: int, cap: float, stream=None, mode: int =
     return out
 
 
+@_for_its_stream
 def route(x, w_router, k, logit_offset=None, sel_bias=None, return_logits=False, stream=None, blocked=True,
           e2s=None, affinity=0.0, rflags=0):
     T, H = x.shape
@@ -207,6 +226,7 @@ class Groups:
     n_act: torch.Tensor
 
 
+@_for_its_stream
 def permute(ids: torch.Tensor, E: int, dev_status: Optional[torch.Tensor] = None, stream=None,
             chunked: bool = True) -> Groups:
     n = ids.numel()
@@ -252,6 +272,7 @@ class ManageOut:
     sid: torch.Tensor
 
 
+@_for_its_stream
 def cache_manage(ids: torch.Tensor, state: CacheState, policy: int, dev_status=None, stream=None) -> ManageOut:
     n = ids.numel()
     E, S = state.e2s.numel(), state.s2e.numel()
@@ -285,6 +306,7 @@ class RepickResult:
     n_miss: torch.Tensor
 
 
+@_for_its_stream
 def cache_repick(counts, state: "CacheState", stream=None) -> RepickResult:
     """Re-pick a STATIC pool's resident set from the window counts (clears them)."""
     E, S = state.e2s.numel(), state.s2e.numel()
@@ -299,6 +321,7 @@ def q8_slab_bytes(H: int, I: int) -> int:
     return int(_q8_slab(H, I))
 
 
+@_for_its_stream
 def quantize_slabs(slabs: torch.Tensor, H: int, I: int, stream=None) -> torch.Tensor:
     """bf16 slabs [n][3HI] (device) -> W8A8 slabs uint8 [n][q8_slab_bytes] (device)."""
     n = slabs.shape[0]
@@ -307,6 +330,7 @@ def quantize_slabs(slabs: torch.Tensor, H: int, I: int, stream=None) -> torch.Te
     return out
 
 
+@_for_its_stream
 def expert_ffn_q8(x, k, I, E, offset, rows, list_e, n_list, max_list, pool_q, e2s=None, y=None, workspace=None,
                   dev_status=None, stream=None) -> torch.Tensor:
     T, H = x.shape
@@ -339,6 +363,7 @@ def _want(t: torch.Tensor, what: str, dtype, shape=None) -> None:
                          + f", got {t.dtype} {tuple(t.shape)}")
 
 
+@_for_its_stream
 def w4_pack(codes: torch.Tensor, scales: torch.Tensor, group: int, stream=None) -> torch.Tensor:
     """codes uint8 [..., K, N] (0..15), scales bf16 [..., ceil(K / group), N] -> packed uint8 [..., w4_bytes]."""
     K, N = codes.shape[-2:]
@@ -351,6 +376,7 @@ def w4_pack(codes: torch.Tensor, scales: torch.Tensor, group: int, stream=None) 
     return out
 
 
+@_for_its_stream
 def w4_quantize(w: torch.Tensor, group: int, stream=None) -> torch.Tensor:
     """bf16 [..., K, N] -> packed uint8 [..., w4_bytes]."""
     K, N = w.shape[-2:]
@@ -362,6 +388,7 @@ def w4_quantize(w: torch.Tensor, group: int, stream=None) -> torch.Tensor:
     return out
 
 
+@_for_its_stream
 def w4_pack_slabs(codes: torch.Tensor, scales: torch.Tensor, H: int, I: int, group: int, stream=None) -> torch.Tensor:
     """Expert slabs: codes uint8 [n][3HI], scales bf16 [n][2 ceil(H/group) I + ceil(I/group) H] -> [n][w4_slab_bytes]."""
     n = codes.shape[0]
@@ -375,6 +402,7 @@ def w4_pack_slabs(codes: torch.Tensor, scales: torch.Tensor, H: int, I: int, gro
     return out
 
 
+@_for_its_stream
 def w4_quantize_slabs(slabs: torch.Tensor, H: int, I: int, group: int, stream=None) -> torch.Tensor:
     """bf16 slabs [n][3HI] (device) -> packed 4-bit slabs uint8 [n][w4_slab_bytes] (device)."""
     n = slabs.shape[0]
@@ -407,6 +435,7 @@ class W4Linear:
         self._packed, self._status = packed.data_ptr(), self.dev_status.data_ptr()
         self._ws, self._ws_bytes, self._f32 = self.workspace.data_ptr(), self.workspace.numel(), out_dtype == torch.float32
 
+    @_for_its_stream
     def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         T, K = x.shape
         if T > self.max_tokens or K != self.K:
@@ -425,6 +454,7 @@ class W4Linear:
         return out
 
 
+@_for_its_stream
 def expert_ffn_w4(x, k, I, E, group, offset, rows, list_e, n_list, max_list, pool, e2s=None, y=None, workspace=None,
                   dev_status=None, stream=None) -> torch.Tensor:
     T, H = x.shape
@@ -463,6 +493,7 @@ class W4Experts:
         self._pool, self._e2s = pool.data_ptr(), None if e2s is None else e2s.data_ptr()
         self._status, self._ws, self._ws_bytes = self.dev_status.data_ptr(), self.workspace.data_ptr(), self.workspace.numel()
 
+    @_for_its_stream
     def forward(self, x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, out: Optional[torch.Tensor] = None,
                 stream=None) -> torch.Tensor:
         T = x.shape[0]
@@ -496,6 +527,7 @@ class Balance(NamedTuple):
     grad: Optional[torch.Tensor]   # [T][E], the type of the logits
 
 
+@_for_its_stream
 def balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float, seq_start: Optional[torch.Tensor] = None,
                  token_mask: Optional[torch.Tensor] = None, sigmoid: bool = False, with_loss: bool = True,
                  with_grad: bool = False, grad_loss: Optional[torch.Tensor] = None, dev_status=None,
@@ -555,6 +587,7 @@ def ffn_workspace_bytes(T: int, H: int, k: int, I: int) -> int:
     return int(_ffn_ws(T, H, k, I))
 
 
+@_for_its_stream
 def expert_ffn(x, k, I, E, offset, rows, list_e, n_list, max_list, pool, e2s=None, host_slabs=None,
                y=None, workspace=None, dev_status=None, stream=None) -> torch.Tensor:
     T, H = x.shape
@@ -569,6 +602,7 @@ def expert_ffn(x, k, I, E, offset, rows, list_e, n_list, max_list, pool, e2s=Non
     return y
 
 
+@_for_its_stream
 def combine(y, w, pos, T, k, E, ids=None, e2s=None, split=False, stream=None):
     H = y.shape[1]
     out = torch.empty(T, H, dtype=torch.bfloat16, device=y.device)
@@ -620,6 +654,7 @@ class SlotCachedMoELayer:
                                      dtype=torch.uint8, device=dev)
         self.side = torch.cuda.Stream(device=dev) if side_stream else None
 
+    @_for_its_stream
     def forward(self, x, out=None, ids=None, w=None, out_res=None, out_miss=None, stream=None, prof=None):
         T = x.shape[0]
         if T > self.max_tokens:
