@@ -11,8 +11,13 @@
 // by powers of two: scales are stored relative to their column's largest (w4.cuh), each row of x is
 // scaled so that its largest element is in [2^14, 2^15), h by the bound |h| <= |x|^2 |Wg| |Wu| (column
 // 2-norms), y by the bound that follows.  A value keeps all 11 bits while it is above 2^-29 of its row's
-// bound; typical values are 2^-11 (h) and 2^-16 (y) of it.  So x (8 bits) is exact and only h and, on its
-// way to the combine, y are rounded, to 11 bits.
+// bound; typical values are 2^-11 (h) and 2^-16 (y) of it.  So x (8 bits) is exact, down to 2^-29 of the
+// row's largest, and only h and, on its way to the combine, y are rounded, to 11 bits.
+// The bound can be far too large: for a row with a few inputs far above the rest whose weights are small.  A row
+// all of whose h are below 2^-17 of the bound is noticed on the way (w4g_small), its tile's gate / up product
+// done again in a second launch (kRedo), scaled by the row's largest |h|, and y by what follows from that.
+// (Inputs of 10^4 and 10^5 times the rest with zero weights, 2048 inputs: y off by 3% and 100% without that, as
+// for ordinary rows with it.  Where no row needs it: 4096 tokens 346 -> 350 us, 1.4 of them the launch.)
 //
 // Why pairs and 256 rows: an MMA over 256 x 256 x 16 runs 128 cycles in each SM and one thread can issue
 // it in that time; a pair's SM needs 32 B of rows and 8 B of codes a cycle from L2, near the 40 B that
@@ -62,7 +67,9 @@ constexpr uint32_t kGACol = kGN;                // first weight column
 static_assert(kGN == 64 * kGSets, "each set drains 64 rows");
 static_assert(kGWRing % kGSets == 0, "a slot of codes belongs to one set");
 
-enum { kGateUp = 0, kDown = 1, kLinear = 2 };
+constexpr int kNoRow = INT_MIN;  // yexp of a row whose expert has no slot
+
+enum { kGateUp = 0, kDown = 1, kLinear = 2, kRedo = 3 };  // kRedo: kGateUp of the tiles that hold a row to scale anew
 
 struct W4GemmArgs {
   const uint8_t* w;        // slab pool, or the packed matrix
@@ -77,7 +84,10 @@ struct W4GemmArgs {
   int E, S;
   int32_t* status;
   const int32_t* rexp;     // [n] the B operand's row p is 2^-rexp[p] times the true one
-  const int32_t* oexp;     // [n] kGateUp: the same of h
+  const int32_t* oexp;     // [n] kGateUp: the same of h, by its bound
+  // grouped rows: of a row's runs of 16 h, how many are small, their largest |h 2^-oexp| (its bits), and whether
+  // there is a row all of whose runs are; yexp of such rows is corrected by kRedo
+  int32_t *hcnt, *hmax, *redo, *yexp;
   // outputs
   uint16_t* h;             // kGateUp: fp16 [n][ldh]
   int ldh;
@@ -163,6 +173,14 @@ __device__ __forceinline__ int w4_norm_exp(const uint8_t* meta) {
 // |y| <= |h|_2 |column|_2 <= sqrt(I) 2^15 2^hexp 2^norm_exp: the exponent that takes y / 2^hexp below 2^15.
 __device__ __forceinline__ int w4_y_exp(const uint8_t* m, const W4Dims& d) {
   return (32 - __clz(d.K) + 1) / 2 + w4_norm_exp(m + d.meta);
+}
+
+// Of a row all of whose h are small: the exponent, <= 0, that takes 2^he times it to the row's largest |h| (in
+// [2^14, 2^15) of it).  0 for other rows, and for rows of zeros.
+constexpr float kGSmall = 0.25f;  // |h 2^-he| below it is small: 2^-25, which fp16 rounds by, is 2^-23 of it
+__device__ __forceinline__ int w4_h_shift(const W4GemmArgs& a, int runs, size_t p, int he) {
+  const float m = __int_as_float(a.hmax[p]);
+  return a.hcnt[p] == runs && m > 0.f ? max(ilogbf(m) - 14, -126 - he) : 0;
 }
 
 // 32 lanes x 32 consecutive 32-bit columns from registers.
@@ -280,7 +298,9 @@ __device__ __forceinline__ W4GFactors w4g_factors(const W4GemmArgs& a, const W4G
     if (32 * i + lane < nrow) {
       // scaled rows of y keep the row's own power of two apart
       if (!(kMode == kDown && a.yh)) f.r[i] = a.rexp[p];
-      if (kMode == kGateUp) f.o[i] = a.oexp[p];
+      if (kMode == kDown && !a.yh) f.r[i] += w4_h_shift(a, d.K / 16, p, f.r[i]);
+      if (kMode == kGateUp || kMode == kRedo) f.o[i] = a.oexp[p];
+      if (kMode == kRedo) f.o[i] += w4_h_shift(a, d.N / 32, p, f.o[i]);
     }
   }
   if (c < d.N) f.cm = reinterpret_cast<const float*>(ti.base + d.mult)[c];
@@ -334,7 +354,19 @@ __device__ __forceinline__ void w4g_store16(const W4GemmArgs& a, const uint32_t*
   __syncwarp();
 }
 
-// The same of fp32 values (v[row], without the column's power of two): to fp32 results, or (kGateUp) to h.
+// Notes the rows of a warp's 16 rows x 16 h whose run is small.  most: the largest |h| of a lane's half of a run.
+__device__ __forceinline__ void w4g_small(const W4GemmArgs& a, float most, size_t row0, int nrow, int lane) {
+  const unsigned big = __ballot_sync(MOE_FULL_MASK, most >= kGSmall);
+  if (((big | big >> 1) & 0x55555555u) == 0x55555555u) return;  // as usual
+  most = fmaxf(most, __shfl_xor_sync(MOE_FULL_MASK, most, 1));
+  if ((lane & 1) || (lane >> 1) >= nrow || most >= kGSmall) return;
+  const size_t p = row0 + (lane >> 1);
+  atomicMax(a.hmax + p, __float_as_int(most));
+  __threadfence();
+  if (atomicAdd(a.hcnt + p, 1) == a.d.N / 32 - 1 && atomicMax(a.hmax + p, 0) > 0) *a.redo = 1;
+}
+
+// The same of fp32 values (v[row], without the column's power of two): to fp32 results, or (kGateUp, kRedo) to h.
 template <int kMode>
 __device__ __forceinline__ void w4g_store32(const W4GemmArgs& a, const float* v, float* st, const W4GFactors& f, int i,
                                             int part, size_t row0, int nrow, int c0, int lane) {
@@ -343,23 +375,27 @@ __device__ __forceinline__ void w4g_store32(const W4GemmArgs& a, const float* v,
 #pragma unroll
   for (int j = 0; j < kGEpiRows; ++j) st[j * kGLd + lane] = v[j] * f.cm;
   __syncwarp();
-  if (kMode == kGateUp) {  // columns 0-15: gate, 16-31: up of the same 16 features
+  if (kMode == kGateUp || kMode == kRedo) {  // columns 0-15: gate, 16-31: up of the same 16 features
     const int f0 = c0 / 2, row = lane >> 1, seg = (lane & 1) * 8;
     const float x = row_fac(row),
                 xh = x * pow2(-__shfl_sync(MOE_FULL_MASK, f.o[i >> 1], 16 * (i & 1) + row));
     uint32_t o[4];
+    float most = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; j += 4) {
       const float4 g = *reinterpret_cast<const float4*>(st + row * kGLd + seg + j);
       const float4 u = *reinterpret_cast<const float4*>(st + row * kGLd + 16 + seg + j);
       auto h = [&](float gv, float uv) {
         gv *= x;
-        return __fdividef(gv, 1.f + __expf(-gv)) * (uv * xh);
+        const float hv = __fdividef(gv, 1.f + __expf(-gv)) * (uv * xh);
+        if (kMode == kGateUp) most = fmaxf(most, fabsf(hv));
+        return hv;
       };
       o[j / 2] = pack_f16(h(g.x, u.x), h(g.y, u.y));
       o[j / 2 + 1] = pack_f16(h(g.z, u.z), h(g.w, u.w));
     }
     if (row < nrow) *reinterpret_cast<uint4*>(a.h + (row0 + row) * a.ldh + f0 + seg) = make_uint4(o[0], o[1], o[2], o[3]);
+    if (kMode == kGateUp) w4g_small(a, most, row0, nrow, lane);
   } else {
     // (a part of the inputs writes sums of its own)
     float* out = kMode == kLinear ? reinterpret_cast<float*>(a.out) + (size_t)part * a.n * a.ldo : a.y;
@@ -393,7 +429,7 @@ __device__ __forceinline__ void w4g_drain(const W4GemmArgs& a, const W4GTile& ti
   const W4Dims& d = a.d;
   const int tok0 = 64 * set, nrow = ti.ntok - tok0, c0 = blk * kGM + 32 * q;
   const bool any = nrow > 0 && c0 < d.N;
-  const bool half = kMode != kGateUp && (kMode == kLinear ? !a.out_f32 : a.yh != nullptr);
+  const bool half = kMode == kLinear ? !a.out_f32 : kMode == kDown && a.yh != nullptr;
   const size_t row0 = (size_t)ti.row0 + tok0;
   __syncwarp();
   wait(tfull, parity);
@@ -468,6 +504,13 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   const W4Dims& d = a.d;
   int nl = 0, total;
 
+  if (kMode == kRedo) {
+    pdl_wait();
+    pdl_trigger();
+    if (*a.redo == 0) return;  // in every CTA
+    for (int p = blockIdx.x * kGThreads + threadIdx.x; p < a.n; p += gridDim.x * kGThreads)
+      if (a.yexp[p] != kNoRow) a.yexp[p] += w4_h_shift(a, d.N / 32, p, a.oexp[p]);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kGWRing; ++s) {
       mbar_init(&wfull[s], 1);
@@ -487,8 +530,10 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     tmem_alloc_pair(&s_tmem, kGTmemCols);
     tmem_relinquish_pair();
   }
-  pdl_wait();
-  pdl_trigger();
+  if (kMode != kRedo) {
+    pdl_wait();
+    pdl_trigger();
+  }
   if (kMode == kLinear) {
     total = (a.n + kGN - 1) / kGN * a.NF * a.parts;
   } else {
@@ -528,10 +573,25 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     dead = __any_sync(MOE_FULL_MASK, !ok);
   };
 
+  // the first tile from t on that there is work in
+  auto next = [&](int t) {
+    if (kMode == kRedo)
+      for (; t < total; t += ncl) {
+        const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
+        bool any = false;
+        for (int i = lane; i < ti.ntok; i += 32) {
+          const size_t p = (size_t)ti.row0 + i;
+          any |= w4_h_shift(a, d.N / 32, p, a.oexp[p]) != 0;
+        }
+        if (__any_sync(MOE_FULL_MASK, any)) break;
+      }
+    return t;
+  };
+
   if (warp == kGWorkers) {
     const bool lead = elect_one();
     uint32_t s = 0, ph = 1, issued = 0;
-    for (int t = cl; t < total && !dead; t += ncl) {
+    for (int t = next(cl); t < total && !dead; t = next(t + ncl)) {
       const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
       const int r = w4g_half(ti.ntok), row = ti.row0 + (int)rank * r;
       const CUtensorMap* map = &mapX.m[r / 16 - 1];
@@ -558,7 +618,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
   } else if (warp == kGWorkers + 2) {
     const bool lead = elect_one();
     uint32_t s = 0, ph = 1, issued = 0;
-    for (int t = cl; t < total && !dead; t += ncl) {
+    for (int t = next(cl); t < total && !dead; t = next(t + ncl)) {
       const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
       const int blk = 2 * ti.ft + (int)rank;
       const uint32_t nm = max(0, min(8, d.Mt - 8 * blk));  // the tiles of 16 columns that exist
@@ -595,7 +655,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
       const uint64_t bd0 = smem_desc_l(smem_u32(xs), 16, 1024, kLayoutSw128);
       const bool lead = elect_one();
       uint32_t s = 0, ph = 0, tp = 1;  // of the ring, of the accumulators
-      for (int t = cl; t < total && !dead; t += ncl) {
+      for (int t = next(cl); t < total && !dead; t = next(t + ncl)) {
         const W4GTile ti = w4g_tile<kMode>(a, s_pre, nl, t);
         const int r = w4g_half(ti.ntok);
         const uint32_t idesc = idesc_f16(2 * kGM, 2 * r);
@@ -634,7 +694,7 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
     W4GTile prev = {};
     bool pending = false;  // prev has not been drained
     W4GFactors f = {};
-    for (int t = cl;; t += ncl) {
+    for (int t = next(cl);; t = next(t + ncl)) {
       const bool real = t < total && !dead;
       W4GTile ti = {};
       if (real) ti = w4g_tile<kMode>(a, s_pre, nl, t);
@@ -707,7 +767,6 @@ __global__ void __launch_bounds__(kGThreads, 1) w4_gemm_kernel(const W4GemmArgs 
 // Rows: x -> fp16 times a power of two per row, in grouped order; one warp per row.
 // ---------------------------------------------------------------------------
 constexpr int kRowThreads = 256, kTokenThreads = 128;
-constexpr int kNoRow = INT_MIN;  // yexp of a row whose expert has no slot
 
 struct W4RowArgs {
   const uint16_t* x;
@@ -844,6 +903,7 @@ __device__ __forceinline__ void w4_row_exps(const W4RowArgs& a, int slot, int p,
   a.xexp[p] = xe;
   a.hexp[p] = he;
   a.yexp[p] = he + w4_y_exp(base + a.sl.dn_at, a.sl.dn);
+  a.g.hcnt[p] = a.g.hmax[p] = 0;
 }
 
 // Zeros past a row of h.
@@ -859,6 +919,7 @@ __global__ void __launch_bounds__(kRowThreads) w4_group_rows_kernel(const W4RowA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = gridDim.x * (kRowThreads / 32);
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.g.redo = 0;
   const int nl = min(*a.g.n_list, kMaxE);
   int carry = 0;
   for (int l0 = 0; l0 < nl; l0 += kRowThreads) {
@@ -907,6 +968,7 @@ __global__ void __launch_bounds__(kTokenThreads) w4_token_rows_kernel(const W4Ro
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = gridDim.x * (kTokenThreads / 32);
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.g.redo = 0;
   for (int t = blockIdx.x * (kTokenThreads / 32) + warp; t < a.n; t += nw) {
     W4Row<NC> r;
     const int ln = w4_warp_row<true>(r, a.x + (size_t)t * a.ldx, a.K, lane);
@@ -1126,9 +1188,9 @@ int launch_w4_linear_gemm(const uint16_t* x, size_t ldx, int T, const uint8_t* w
   return MOE_OK;
 }
 
-// Workspace: x' [n][H] and h [n][I] fp16 in whole stages, exponents, and y [n][H] fp16 where the caller combines.
+// Workspace: x' [n][H] and h [n][I] fp16 in whole stages, exponents, what tells of small h, and y [n][H] fp16 where the caller combines.
 size_t w4_ffn_gemm_ws(size_t n, int H, int I, bool yh) {
-  return g256(2 * n * w4g_ld(H)) + g256(2 * n * w4g_ld(I)) + 3 * g256(4 * n) + (yh ? g256(2 * n * H) : 0);
+  return g256(2 * n * w4g_ld(H)) + g256(2 * n * w4g_ld(I)) + 5 * g256(4 * n) + 256 + (yh ? g256(2 * n * H) : 0);
 }
 
 // y rows of the listed experts (fp32 f.y, or scaled fp16 with *yh / *yexp set for launch_w4_combine).  ids and pos:
@@ -1151,12 +1213,14 @@ int launch_ffn_w4_gemm(const FfnArgs& f, const int32_t* ids, const int32_t* pos,
   r.xexp = (int32_t*)take(4 * n);
   r.hexp = (int32_t*)take(4 * n);
   r.yexp = (int32_t*)take(4 * n);
+  int32_t *hcnt = (int32_t*)take(4 * n), *hmax = (int32_t*)take(4 * n), *redo = (int32_t*)take(4);
   W4GemmArgs g{};
   g.w = (const uint8_t*)f.pool, g.slab = sl.bytes, g.d = sl.gu, g.mat = 0;
   g.K = f.H, g.n = (int)n, g.NF = (2 * f.I + 2 * kGM - 1) / (2 * kGM);
   g.offset = f.offset, g.list_e = f.list_e, g.n_list = f.n_list, g.e2s = f.e2s, g.list_s = f.list_s;
   g.E = f.E, g.S = f.S, g.status = f.status;
   g.rexp = r.xexp, g.oexp = r.hexp, g.h = h, g.ldh = w4g_ld(f.I);
+  g.hcnt = hcnt, g.hmax = hmax, g.redo = redo, g.yexp = r.yexp;
   r.g = g, r.rows = f.rows, r.k = f.k, r.sl = sl;
   r.y = yh ? nullptr : f.y;
   if (prof) prof->begin(MOE_PROF_FFN_ROWS, s);
@@ -1171,6 +1235,7 @@ int launch_ffn_w4_gemm(const FfnArgs& f, const int32_t* ids, const int32_t* pos,
   if (prof) prof->end(s);
   if (prof) prof->begin(MOE_PROF_FFN_GATEUP, s);
   int rc = launch_gemm<kGateUp>(g, r.xp, s);
+  if (rc == MOE_OK) rc = launch_gemm<kRedo>(g, r.xp, s);
   if (rc != MOE_OK) return rc;
   if (prof) prof->end(s);
   W4GemmArgs gd = g;
