@@ -7,6 +7,7 @@ library is missing, importing this module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import inspect
@@ -133,23 +134,25 @@ def _s(stream=None):
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _here(t: torch.Tensor, stream=None) -> int:
-    """The stream handle for work on ``t``: ``stream``, or the current one of its device."""
+def _here(index: int, stream=None) -> int:
+    """The handle of ``stream``, or of the current stream of CUDA device ``index``."""
     if stream is not None:
         return stream.cuda_stream
-    if _raw_stream is not None and t.is_cuda:
-        return _raw_stream(t.get_device())
-    return torch.cuda.current_stream(t.device).cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(index)
+    return torch.cuda.current_stream(index).cuda_stream
 
 
 def _on(dev: torch.device, **tensors) -> None:
     """Refuses tensors that are not all on the CUDA device ``dev``: the kernels get their addresses as they are."""
     if dev.type != "cuda":
         raise ValueError(f"need tensors on a CUDA device, got {dev}")
+    index = dev.index
     for name, t in tensors.items():
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"{name}: on {t.device}, the call runs on {dev}")
 
 
@@ -168,19 +171,20 @@ def _for_its_stream(call):
     return on
 
 
-class _Current:
+_AS_IT_IS = contextlib.nullcontext()
+
+
+def _current(dev: torch.device):
     """Makes a device the current one, where it is not: the library launches on the current device."""
+    return _AS_IT_IS if dev.index == _current_device() else torch.cuda.device(dev)
 
-    def __init__(self, dev: torch.device):
-        self.dev = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
 
-    def __enter__(self):
-        if self.dev is not None:
-            self.dev.__enter__()
-
-    def __exit__(self, *e):
-        if self.dev is not None:
-            self.dev.__exit__(*e)
+def _result(stream, *shape, dtype, device) -> torch.Tensor:
+    """A result of a call on ``stream`` (None: the current one), allocated for it."""
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(*shape, dtype=dtype, device=device)
 
 
 # ---------------------------------------------------------------------------
@@ -370,7 +374,7 @@ def w4_pack(codes: torch.Tensor, scales: torch.Tensor, group: int, stream=None) 
     _want(codes, "codes", torch.uint8)
     _want(scales, "scales", torch.bfloat16, (*codes.shape[:-2], -(-K // group) if group > 0 else 0, N))
     _on(codes.device, scales=scales)
-    with _Current(codes.device):
+    with _current(codes.device):
         out = torch.empty(*codes.shape[:-2], w4_bytes(K, N, group), dtype=torch.uint8, device=codes.device)
         _ck(_w4_pack(_p(codes), _p(scales), codes[..., 0, 0].numel(), K, N, group, _p(out), _s(stream)), "moe_w4_pack")
     return out
@@ -382,7 +386,7 @@ def w4_quantize(w: torch.Tensor, group: int, stream=None) -> torch.Tensor:
     K, N = w.shape[-2:]
     _want(w, "w", torch.bfloat16)
     _on(w.device)
-    with _Current(w.device):
+    with _current(w.device):
         out = torch.empty(*w.shape[:-2], w4_bytes(K, N, group), dtype=torch.uint8, device=w.device)
         _ck(_w4_quantize(_p(w), w[..., 0, 0].numel(), K, N, group, _p(out), _s(stream)), "moe_w4_quantize")
     return out
@@ -396,7 +400,7 @@ def w4_pack_slabs(codes: torch.Tensor, scales: torch.Tensor, H: int, I: int, gro
     if group > 0:
         _want(scales, "scales", torch.bfloat16, (n, 2 * -(-H // group) * I + -(-I // group) * H))
     _on(codes.device, scales=scales)
-    with _Current(codes.device):
+    with _current(codes.device):
         out = torch.empty(n, w4_slab_bytes(H, I, group), dtype=torch.uint8, device=codes.device)
         _ck(_w4_pack_slabs(_p(codes), _p(scales), n, H, I, group, _p(out), _s(stream)), "moe_w4_pack_slabs")
     return out
@@ -408,7 +412,7 @@ def w4_quantize_slabs(slabs: torch.Tensor, H: int, I: int, group: int, stream=No
     n = slabs.shape[0]
     _want(slabs, "slabs", torch.bfloat16, (n, 3 * H * I))
     _on(slabs.device)
-    with _Current(slabs.device):
+    with _current(slabs.device):
         out = torch.empty(n, w4_slab_bytes(H, I, group), dtype=torch.uint8, device=slabs.device)
         _ck(_w4_quantize_slabs(_p(slabs), n, H, I, group, _p(out), _s(stream)), "moe_w4_quantize_slabs")
     return out
@@ -429,13 +433,13 @@ class W4Linear:
             raise ValueError(f"out_dtype: bfloat16 or float32, got {out_dtype}")
         self.packed, self.K, self.N, self.group = packed, K, N, group
         self.max_tokens, self.out_dtype = max_tokens, out_dtype
+        self.device, self._index = packed.device, packed.get_device()
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=packed.device)
         self.workspace = torch.empty(int(_w4_linear_ws(max_tokens, K, N, group)), dtype=torch.uint8,
                                      device=packed.device)
         self._packed, self._status = packed.data_ptr(), self.dev_status.data_ptr()
         self._ws, self._ws_bytes, self._f32 = self.workspace.data_ptr(), self.workspace.numel(), out_dtype == torch.float32
 
-    @_for_its_stream
     def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         T, K = x.shape
         if T > self.max_tokens or K != self.K:
@@ -444,13 +448,17 @@ class W4Linear:
             raise ValueError("x: need bf16 rows with a contiguous last dimension")
         if out is not None and (out.dtype != self.out_dtype or out.shape != (T, self.N) or out.stride(1) != 1):
             raise ValueError(f"out: need {self.out_dtype} ({T}, {self.N}) with a contiguous last dimension")
-        _on(self.packed.device, x=x, out=out)
-        with _Current(x.device):
-            if out is None:
-                out = torch.empty(T, self.N, dtype=self.out_dtype, device=x.device)
-            _ck(_w4_linear(x.data_ptr(), x.stride(0) if T > 1 else K, T, K, self.N, self.group, self._packed,
-                           out.data_ptr(), out.stride(0) if T > 1 else self.N, self._f32, self._ws, self._ws_bytes,
-                           self._status, _here(x, stream)), "moe_w4_linear")
+        dev = self._index
+        if dev < 0 or x.get_device() != dev or (out is not None and out.get_device() != dev):
+            _on(self.device, x=x, out=out)
+        if _current_device() != dev:
+            with torch.cuda.device(self.device):
+                return self.forward(x, out, stream)
+        if out is None:
+            out = _result(stream, T, self.N, dtype=self.out_dtype, device=self.device)
+        _ck(_w4_linear(x.data_ptr(), x.stride(0) if T > 1 else K, T, K, self.N, self.group, self._packed,
+                       out.data_ptr(), out.stride(0) if T > 1 else self.N, self._f32, self._ws, self._ws_bytes,
+                       self._status, _here(dev, stream)), "moe_w4_linear")
         return out
 
 
@@ -460,7 +468,7 @@ def expert_ffn_w4(x, k, I, E, group, offset, rows, list_e, n_list, max_list, poo
     T, H = x.shape
     _on(x.device, offset=offset, rows=rows, list_e=list_e, n_list=n_list, pool=pool, e2s=e2s, y=y, workspace=workspace,
         dev_status=dev_status)
-    with _Current(x.device):
+    with _current(x.device):
         if y is None:
             y = torch.zeros(T * k, H, dtype=torch.float32, device=x.device)
         if workspace is None:
@@ -487,13 +495,15 @@ class W4Experts:
             _want(e2s, "e2s", torch.int32, (E,))
         self.pool, self.H, self.I, self.k, self.E, self.group, self.e2s = pool, H, I, k, E, group, e2s
         self.S, self.max_tokens = pool.shape[0], max_tokens
+        self.device, self._index = pool.device, pool.get_device()
+        if e2s is not None and e2s.device != pool.device:
+            raise ValueError(f"e2s: on {e2s.device}, the pool is on {pool.device}")
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=pool.device)
         self.workspace = torch.empty(int(_experts_w4_ws(max_tokens, H, I, k, E)), dtype=torch.uint8,
                                      device=pool.device)
         self._pool, self._e2s = pool.data_ptr(), None if e2s is None else e2s.data_ptr()
         self._status, self._ws, self._ws_bytes = self.dev_status.data_ptr(), self.workspace.data_ptr(), self.workspace.numel()
 
-    @_for_its_stream
     def forward(self, x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, out: Optional[torch.Tensor] = None,
                 stream=None) -> torch.Tensor:
         T = x.shape[0]
@@ -507,13 +517,18 @@ class W4Experts:
             raise ValueError(f"w: need contiguous fp32 [{T}][{self.k}]")
         if out is not None:
             _want(out, "out", torch.bfloat16, (T, self.H))
-        _on(self.pool.device, x=x, ids=ids, w=w, e2s=self.e2s, out=out)
-        with _Current(x.device):
-            if out is None:
-                out = torch.empty(T, self.H, dtype=torch.bfloat16, device=x.device)
-            _ck(_experts_w4(x.data_ptr(), ids.data_ptr(), w.data_ptr(), T, self.H, self.I, self.k, self.E, self.group,
-                            self._pool, self.S, self._e2s, out.data_ptr(), self._ws, self._ws_bytes, self._status,
-                            _here(x, stream)), "moe_experts_w4")
+        dev = self._index
+        if (dev < 0 or x.get_device() != dev or ids.get_device() != dev or w.get_device() != dev
+                or (out is not None and out.get_device() != dev)):
+            _on(self.device, x=x, ids=ids, w=w, out=out)
+        if _current_device() != dev:
+            with torch.cuda.device(self.device):
+                return self.forward(x, ids, w, out, stream)
+        if out is None:
+            out = _result(stream, T, self.H, dtype=torch.bfloat16, device=self.device)
+        _ck(_experts_w4(x.data_ptr(), ids.data_ptr(), w.data_ptr(), T, self.H, self.I, self.k, self.E, self.group,
+                        self._pool, self.S, self._e2s, out.data_ptr(), self._ws, self._ws_bytes, self._status,
+                        _here(dev, stream)), "moe_experts_w4")
         return out
 
 
@@ -527,7 +542,6 @@ class Balance(NamedTuple):
     grad: Optional[torch.Tensor]   # [T][E], the type of the logits
 
 
-@_for_its_stream
 def balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float, seq_start: Optional[torch.Tensor] = None,
                  token_mask: Optional[torch.Tensor] = None, sigmoid: bool = False, with_loss: bool = True,
                  with_grad: bool = False, grad_loss: Optional[torch.Tensor] = None, dev_status=None,
@@ -548,19 +562,22 @@ def balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float, seq_start
         n_seq = seq_start.numel() - 1
     if grad_loss is not None and (grad_loss.dtype != torch.float32 or grad_loss.numel() != 1):
         raise ValueError("grad_loss: need one fp32 value")
-    dev = logits.device
-    _on(dev, ids=ids, seq_start=seq_start, token_mask=token_mask, grad_loss=grad_loss, dev_status=dev_status)
-    with _Current(dev):
-        loss = torch.empty((), dtype=torch.float32, device=dev) if with_loss else None
-        counts = torch.empty((max(n_seq, 0), E), dtype=torch.int32, device=dev)
-        grad = torch.empty_like(logits) if with_grad else None
-        nws = _balance_ws(T, E, n_seq)
-        ws = torch.empty(nws, dtype=torch.uint8, device=dev)
-        _ck(_balance(logits.data_ptr(), bf16, ids.data_ptr(), None if token_mask is None else token_mask.data_ptr(),
-                     None if seq_start is None else seq_start.data_ptr(), n_seq, T, E, k, ROUTE_SIGMOID if sigmoid else 0,
-                     coef, None if grad_loss is None else grad_loss.data_ptr(), counts.data_ptr(),
-                     loss.data_ptr() if with_loss else None, grad.data_ptr() if with_grad else None, ws.data_ptr(), nws,
-                     None if dev_status is None else dev_status.data_ptr(), _here(logits, stream)), "moe_balance_loss")
+    dev, index = logits.device, logits.get_device()
+    if index < 0 or any(t is not None and t.get_device() != index for t in (ids, seq_start, token_mask, grad_loss, dev_status)):
+        _on(dev, ids=ids, seq_start=seq_start, token_mask=token_mask, grad_loss=grad_loss, dev_status=dev_status)
+    if stream is not None or _current_device() != index:  # temporaries and results for the stream that the kernels run on
+        with torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream):
+            return balance_loss(logits, ids, coef, seq_start, token_mask, sigmoid, with_loss, with_grad, grad_loss, dev_status)
+    loss = torch.empty((), dtype=torch.float32, device=dev) if with_loss else None
+    counts = torch.empty((max(n_seq, 0), E), dtype=torch.int32, device=dev)
+    grad = torch.empty_like(logits) if with_grad else None
+    nws = _balance_ws(T, E, n_seq)
+    ws = torch.empty(nws, dtype=torch.uint8, device=dev)
+    _ck(_balance(logits.data_ptr(), bf16, ids.data_ptr(), None if token_mask is None else token_mask.data_ptr(),
+                 None if seq_start is None else seq_start.data_ptr(), n_seq, T, E, k, ROUTE_SIGMOID if sigmoid else 0,
+                 coef, None if grad_loss is None else grad_loss.data_ptr(), counts.data_ptr(),
+                 loss.data_ptr() if with_loss else None, grad.data_ptr() if with_grad else None, ws.data_ptr(), nws,
+                 None if dev_status is None else dev_status.data_ptr(), _here(index)), "moe_balance_loss")
     return Balance(loss, counts, grad)
 
 

@@ -35,7 +35,9 @@ def b(monkeypatch):
         monkeypatch.setattr(b, name, lambda *a: 0)
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(b, "_on", lambda *a, **k: None)
-    monkeypatch.setattr(b, "_Current", lambda dev: contextlib.nullcontext())
+    monkeypatch.setattr(b, "_current", lambda dev: contextlib.nullcontext())
+    monkeypatch.setattr(b, "_current_device", lambda: -1)
+    monkeypatch.setattr(b, "_here", lambda *a: 0)
     b.seen = seen
     lin = b.W4Linear(torch.zeros(b.w4_bytes(64, 16, 64), dtype=torch.uint8), 64, 16, 64, max_tokens=2)
     ex = b.W4Experts(torch.zeros(16, b.w4_slab_bytes(256, 128, 64), dtype=torch.uint8), 256, 128, 2, 16, 64, max_tokens=2)
