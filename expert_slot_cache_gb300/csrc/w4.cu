@@ -3,22 +3,21 @@
 //
 //   y[t][n] = sum_k x[t][k] (code[k][n] - 8) scale[k / G][n]
 //
-// The codes become the A operand of 16 x 16 x 8 MMAs as the exact bf16 integers 16 + code, the bf16
-// activations the B operand; a 64-input block's products (32 inputs where G = 32) are summed in fp32 by the
-// tensor core, 24 times the block's sum of activations (an MMA with ones, shared by all columns) is taken
-// off, the rest multiplied by its fp32 scale and added in fp32.  No weight and no activation is rounded.
-// (16 + code needs a mask and at most a shift; code - 8 would need a third operation for every pair, and the
-// stream is bound by its instructions: 64 codes of 16 columns are 512 bytes, 21 cycles of an SM's share of
-// the memory bandwidth.)
+// The codes become the A operand of 16 x 16 x 8 MMAs as the exact bf16 integers code - 8, the bf16 activations
+// the B operand; a 64-input block's products (32 inputs where G = 32) are summed in fp32 by the tensor core,
+// multiplied by their fp32 scale and added in fp32.  No weight and no activation is rounded.
+// (16 + code needs one operation less for every pair of codes, but its surplus, 24 times the block's sum of
+// activations, has to come off again: an input far above the rest then costs accuracy in columns where its weight
+// is 0, infinities become NaN, and sums overflow early.  The extra MMAs for the surplus cost as much as they save:
+// us, with it / as it is, 8 tokens through the experts 46.6 / 45.4, 32 tokens 101.7 / 99.3, head 28.8 / 29.1.)
 //
 // A warp streams CM neighbouring tiles of 16 columns (CM x 512 bytes a block of 64 inputs, one 16-byte load
 // per lane and tile), every ks-th block of the inputs, two blocks ahead and on across the end of a unit, so
-// that its loads do not pause; the activations of a block travel with its codes.  (A ring in shared memory,
-// filled by bulk copies or by cp.async, hid the latency better but cost instructions, which are what bounds
-// the stream: about 265 for 2 KB; 8 tokens took 58 and 59 us with those, 51 us with registers, 46 since the
-// shares are finer.)  The ks warps that share a unit add up in shared memory, in warp order.  ks is the split
-// that costs least for the unit count at hand (w4_split): few long shares while there are units for every
-// warp, short ones for a few small matrices.
+// that its loads do not pause; the activations of a block travel with its codes.  (A ring in shared memory, filled
+// by bulk copies or by cp.async, took 8 tokens 58 and 59 us when registers took 51; 45 since the shares are finer and
+// the products exact.)  The ks warps that share a unit add up in shared memory, in warp order.  ks is the split that
+// costs least for the unit count at hand (w4_split): few long shares while there are units for every warp, short ones
+// for a few small matrices.
 #include <algorithm>
 
 #include "internal.cuh"
@@ -133,26 +132,9 @@ __device__ __forceinline__ void w4_load(W4Block<CM, NB, LO, G32>& b, const W4Uni
 template <int CM, int NB, bool LO, bool G32>
 __device__ __forceinline__ void w4_block(const W4Block<CM, NB, LO, G32>& b, float (&acc)[CM][NB][4]) {
   constexpr int P = LO ? 2 : 1;
-  const uint32_t one = 0x3f803f80u;
-  const uint32_t ones[4] = {one, one, one, one};
 #pragma unroll
   for (int part = 0; part < (G32 ? 2 : 1); ++part) {
     constexpr int H = G32 ? 1 : 2;  // halves of the block per scale
-    float off[NB][4];               // -24 sum of the rows' inputs, as an accumulator fragment
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int h = 0; h < H; ++h)
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const uint4 v = b.x[nb][p][part + h];
-          mma_bf16_16816(d, ones, v.x, v.y, d[0], d[1], d[2], d[3]);
-          mma_bf16_16816(d, ones, v.z, v.w, d[0], d[1], d[2], d[3]);
-        }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) off[nb][i] = -24.f * d[i];
-    }
 #pragma unroll
     for (int m = 0; m < CM; ++m) {
       float c[NB][4];
@@ -165,7 +147,7 @@ __device__ __forceinline__ void w4_block(const W4Block<CM, NB, LO, G32>& b, floa
 #pragma unroll
           for (int p = 0; p < P; ++p) {
             const uint4 v = b.x[nb][p][part + h];
-            if (h == 0 && p == 0) mma_bf16_16816(c[nb], a0, v.x, v.y, off[nb][0], off[nb][1], off[nb][2], off[nb][3]);
+            if (h == 0 && p == 0) mma_bf16_16816(c[nb], a0, v.x, v.y, 0.f, 0.f, 0.f, 0.f);
             else mma_bf16_16816(c[nb], a0, v.x, v.y, c[nb][0], c[nb][1], c[nb][2], c[nb][3]);
             mma_bf16_16816(c[nb], a1, v.z, v.w, c[nb][0], c[nb][1], c[nb][2], c[nb][3]);
           }

@@ -112,11 +112,12 @@ __host__ __device__ inline uint32_t w4_put(int code, int bit) {
 __device__ __forceinline__ int w4_chunk(int g, int q) { return 4 * g + ((q + (g >> 1)) & 3); }
 
 // The words of columns g (w0) and g + 8 (w1) for one run of eight inputs -> the A fragments (bf16x2) of two
-// 16 x 16 MMAs, inputs 0-3 and 4-7 of the run, as 16 + code (the caller takes 24 sum(x) off the products).
+// 16 x 16 MMAs, inputs 0-3 and 4-7 of the run, as code - 8: 16 + code, then 24 off, both exact.
 __device__ __forceinline__ void w4_frag_bf16(uint32_t w0, uint32_t w1, uint32_t (&a0)[4], uint32_t (&a1)[4]) {
-  auto conv = [](uint32_t v) {  // one operation: both constants in registers
+  auto conv = [](uint32_t v) {  // two operations: the constants in registers
     uint32_t r;
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(0x00780078u), "r"(0x41804180u));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0x41c041c0u));
     return r;
   };
   a0[0] = conv(w0);

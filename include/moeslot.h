@@ -449,8 +449,11 @@ int moe_w4_quantize_slabs(const void* w, int n, int H, int I, int group, void* d
  *   workspace  device, moe_w4_linear_workspace_bytes(T, K, N, group) bytes,
  *        256-byte aligned (may be NULL where that is 0)
  *        (a workspace for T rows is enough for fewer)
- * Sums are fp32; the result does not depend on thread timing.  A row of x that
- * holds an infinity or a NaN gives a row without finite values, no other.
+ * Sums are fp32; the result does not depend on thread timing.  Infinities and
+ * NaN of a row of x give what the formula gives (inf * 0 is NaN), in no other
+ * row.  From 17 rows on, by rows x weights, the products are taken on the
+ * tensor cores from fp16 rows that are scaled by a power of two each: values of
+ * a row below 2^-29 of its largest lose bits there, below 2^-40 they count as 0.
  * Errors: MOE_ERR_ARG on NULL pointers, T < 1 or shapes out of range;
  * MOE_ERR_ALIGN if x or w is not 16-byte aligned, ldx % 8 != 0, or the
  * workspace is unaligned or too small.
