@@ -184,6 +184,35 @@ __device__ __forceinline__ float w4_sum_part(const float* red, int w0, int ks, i
   return s;
 }
 
+// One result in 64 bits, for a sum that left fp32's range on its way: inputs above some 2^100, infinities, NaN.
+// Reached by such results alone, and in a pass of its own after a kernel's stream (called from the stream's rounds it
+// took registers from them: 32 tokens 98.3 / 101.5 us), so in no hurry; what is NaN stays NaN.  codes: the packed column's words in its tile's
+// block 0 (g: its place among the tile's first or second eight), sc: its scale of group 0, mates: w4_mates.
+template <bool LO>
+__device__ __noinline__ float w4_dot_at(const uint32_t* codes, const __half* sc, int mates, int g, float mult, int K, int G,
+                                        const uint16_t* x, size_t lo) {
+  double sum = 0.;
+  for (int k = 0; k < K && sum == sum; k += 8) {
+    const int b = k >> 5, q = (k >> 3) & 3;
+    const uint32_t v = codes[(size_t)(b >> 1) * mates * 128 + w4_chunk(g, q) * 4 + (b & 1)];
+    const double s = __half2float(sc[(size_t)(k / G) * mates * 16]);
+    for (int j = 0; j < 8; ++j) {
+      double xv = bf16_to_f32(x[k + j]);
+      if (LO) xv += bf16_to_f32(x[lo + k + j]);
+      sum += xv * (((int)(__funnelshift_r(v, v, w4_code_bit(j)) & 15) - 8) * s);
+    }
+  }
+  return (float)(sum * mult);
+}
+// Of packed column n of the matrix at w, for the inputs at x (LO: as the sum with those at x + lo).
+template <bool LO>
+__device__ __forceinline__ float w4_dot(const uint8_t* w, const W4Dims& d, int n, const uint16_t* x, size_t lo) {
+  const int tile = n >> 4, g = n & 7, h = (n >> 3) & 1;
+  return w4_dot_at<LO>(reinterpret_cast<const uint32_t*>(w) + w4_code_at(d, tile, 0) * 128 + 2 * h,
+                       reinterpret_cast<const __half*>(w + d.scales) + w4_scale_at(d, tile, 0, g) * 2 + h, w4_mates(d, tile), g,
+                       reinterpret_cast<const float*>(w + d.mult)[n], d.K, d.G, x, lo);
+}
+
 // Warps per unit: the power of two with the least rounds x (blocks of a share + the cost of ending a round, about
 // one block: with 3 in its place 8 tokens took 51 us, with 1 46 us; 32 tokens over 288 experts 108 and 101 us).
 __host__ __device__ inline int w4_split(int units, int Kb, int ctas) {
@@ -273,17 +302,28 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_linear_kernel(const W4
     return u;
   };
   if (rounds <= 0) return;
-  w4_stream<CM, NB, false, G32>(a.d, ks, rounds, 0, red, unit, [&](int r, const float* buf) {
+  bool lost = false;  // a result of this thread is not finite
+  auto put = [&](int r, const float* buf, bool again) {
     for (int i = threadIdx.x; i < sub * CM * 16 * nt; i += kW4Threads) {
       const int col = i % (CM * 16), row = i / (CM * 16) % nt, g = i / (CM * 16 * nt);
       const int n = first(r, g) * 16 + col;
       if (n >= a.d.N) continue;
-      const float v = w4_sum_part<CM, NB>(buf, g * ks, ks, col >> 4, row, col & 15) * mult[n];
       const size_t o = (size_t)(t0 + row) * a.ldo + n;
+      float v;
+      if (again) {
+        if (isfinite(a.out_f32 ? reinterpret_cast<float*>(a.out)[o] : bf16_to_f32(reinterpret_cast<uint16_t*>(a.out)[o]))) continue;
+        v = w4_dot<false>(a.w, a.d, n, a.x + (size_t)(t0 + row) * a.ldx, 0);
+      } else {
+        v = w4_sum_part<CM, NB>(buf, g * ks, ks, col >> 4, row, col & 15) * mult[n];
+        lost |= !isfinite(v);
+      }
       if (a.out_f32) reinterpret_cast<float*>(a.out)[o] = v;
       else reinterpret_cast<uint16_t*>(a.out)[o] = f32_to_bf16(v);
     }
-  });
+  };
+  w4_stream<CM, NB, false, G32>(a.d, ks, rounds, 0, red, unit, [&](int r, const float* buf) { put(r, buf, false); });
+  if (lost)
+    for (int r = 0; r < rounds; ++r) put(r, nullptr, true);
 }
 
 struct W4FfnArgs {
@@ -429,7 +469,8 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_gateup_kernel(const W4
     u.x[0] = a.f.x + (size_t)((a.ids ? row : a.f.rows[row]) / a.f.k) * a.f.H + 8 * (lane & 3);
     return u;
   };
-  w4_stream<kGuTiles, 1, false, G32>(d, ks, rounds, 0, red, unit, [&](int r, const float* buf) {
+  bool lost = false;  // a gate or up value, or h, of this thread is not finite (h is not wherever one of the others is not)
+  auto put = [&](int r, const float* buf, bool again) {
     for (int i = threadIdx.x; i < sub * 32 * kW4Rows; i += kW4Threads) {
       const int col = i & 31, row = (i >> 5) % kW4Rows, g = (i >> 5) / kW4Rows, u = index(r, g);
       if (u >= units) continue;
@@ -437,16 +478,30 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_gateup_kernel(const W4
       const int tile = u % FT * kGuTiles, m = 2 * (col >> 4), f = tile / 2 * 16 + col;
       if (b.slot < 0 || row >= b.n || tile + m >= d.Mt) continue;
       const float* mg = reinterpret_cast<const float*>(slab(b.slot) + d.mult) + (tile + m) * 16 + (col & 15);
-      const float gv = w4_sum_part<kGuTiles, 1>(buf, g * ks, ks, m, row, col & 15) * mg[0];
-      const float uv = w4_sum_part<kGuTiles, 1>(buf, g * ks, ks, m + 1, row, col & 15) * mg[16];
+      const size_t o = (size_t)b.row[row] * I + f;
+      float gv, uv;
+      if (again) {
+        if (isfinite(bf16_to_f32(a.h[o]))) continue;
+        const uint16_t* x = a.f.x + (size_t)((a.ids ? b.row[row] : a.f.rows[b.row[row]]) / a.f.k) * a.f.H;
+        const int n = (tile + m) * 16 + (col & 15);
+        gv = w4_dot<false>(slab(b.slot), d, n, x, 0);
+        uv = w4_dot<false>(slab(b.slot), d, n + 16, x, 0);
+      } else {
+        gv = w4_sum_part<kGuTiles, 1>(buf, g * ks, ks, m, row, col & 15) * mg[0];
+        uv = w4_sum_part<kGuTiles, 1>(buf, g * ks, ks, m + 1, row, col & 15) * mg[16];
+      }
       const float h = gv / (1.f + __expf(-gv)) * uv;
       // h as the sum of two bf16: 16 significant bits reach the down product
       const uint16_t hi = f32_to_bf16(h);
-      const size_t o = (size_t)b.row[row] * I + f;
+      const bool fin = isfinite(bf16_to_f32(hi));
+      lost |= !fin;
       a.h[o] = hi;
-      a.h[(size_t)a.n * I + o] = isfinite(bf16_to_f32(hi)) ? f32_to_bf16(h - bf16_to_f32(hi)) : 0;
+      a.h[(size_t)a.n * I + o] = fin ? f32_to_bf16(h - bf16_to_f32(hi)) : 0;
     }
-  });
+  };
+  w4_stream<kGuTiles, 1, false, G32>(d, ks, rounds, 0, red, unit, [&](int r, const float* buf) { put(r, buf, false); });
+  if (lost)
+    for (int r = 0; r < rounds; ++r) put(r, nullptr, true);
 }
 
 // out[t] = bf16(sum_j w[t][j] y[slot]), fp32, j ascending: grid (T, H / 512).  (Sums by the CTAs of the down kernel
@@ -513,7 +568,8 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_down_kernel(const W4Ff
     u.x[0] = a.h + (size_t)b.row[min(lane >> 2, b.n - 1)] * d.K + 8 * (lane & 3);
     return u;
   };
-  w4_stream<kDnTiles, 1, true, G32>(d, ks, rounds, (size_t)a.n * d.K, red, unit, [&](int r, const float* buf) {
+  bool lost = false;  // a result of this thread is not finite
+  auto put = [&](int r, const float* buf, bool again) {
     for (int i = threadIdx.x; i < sub * 16 * kDnTiles * kW4Rows; i += kW4Threads) {
       const int col = i % (16 * kDnTiles), row = i / (16 * kDnTiles) % kW4Rows, g = i / (16 * kDnTiles * kW4Rows);
       const int u = index(r, g);
@@ -522,13 +578,23 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_down_kernel(const W4Ff
       const int n = u % FT * (16 * kDnTiles) + col;
       if (row >= b.n || n >= d.N) continue;
       // an expert without a slot adds nothing: its rows are zero
+      float* y = a.f.y + (size_t)b.row[row] * d.N + n;
       float v = 0.f;
-      if (b.slot >= 0)
+      if (again) {
+        if (isfinite(*y)) continue;
+        v = w4_dot<true>(down(b.slot), d, n, a.h + (size_t)b.row[row] * d.K, (size_t)a.n * d.K);
+      } else if (b.slot >= 0) {
         v = w4_sum_part<kDnTiles, 1>(buf, g * ks, ks, col >> 4, row, col & 15) *
             reinterpret_cast<const float*>(down(b.slot) + d.mult)[n];
-      a.f.y[(size_t)b.row[row] * d.N + n] = v;
+        lost |= !isfinite(v);
+      }
+      *y = v;
     }
-  });
+  };
+  w4_stream<kDnTiles, 1, true, G32>(d, ks, rounds, (size_t)a.n * d.K, red, unit,
+                                    [&](int r, const float* buf) { put(r, buf, false); });
+  if (lost)
+    for (int r = 0; r < rounds; ++r) put(r, nullptr, true);
 }
 
 static int w4_sms(int* sms) {

@@ -296,8 +296,8 @@ __device__ __forceinline__ W4GFactors w4g_factors(const W4GemmArgs& a, const W4G
   for (int i = 0; i < 2; ++i) {
     const size_t p = (size_t)ti.row0 + tok0 + 32 * i + lane;
     if (32 * i + lane < nrow) {
-      // scaled rows of y keep the row's own power of two apart
-      if (!(kMode == kDown && a.yh)) f.r[i] = a.rexp[p];
+      // scaled rows of y keep the row's own power of two apart, and parts of the inputs theirs, up to their sum
+      if (!(kMode == kDown && a.yh) && !(kMode == kLinear && a.parts > 1)) f.r[i] = a.rexp[p];
       if (kMode == kDown && !a.yh) f.r[i] += w4_h_shift(a, d.K / 16, p, f.r[i]);
       if (kMode == kGateUp || kMode == kRedo) f.o[i] = a.oexp[p];
       if (kMode == kRedo) f.o[i] += w4_h_shift(a, d.N / 32, p, f.o[i]);
@@ -1120,9 +1120,10 @@ size_t w4_linear_gemm_ws(int T, const W4Dims& d) {
          (2 * nf > kGPairs ? 0 : 4 * (kGPairs / nf) * std::min(T, kGN) * w4_part_ld(d.N));
 }
 
-// out = the sums of the parts, in order; four columns a thread.
-__global__ void __launch_bounds__(256) w4_parts_kernel(const float* __restrict__ part, int parts, int T, int N, int ldp,
-                                                       void* out, size_t ldo, int out_f32) {
+// out = the sums of the parts, in order, times the row's power of two; four columns a thread.
+__global__ void __launch_bounds__(256) w4_parts_kernel(const float* __restrict__ part, const int32_t* __restrict__ rexp,
+                                                       int parts, int T, int N, int ldp, void* out, size_t ldo,
+                                                       int out_f32) {
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, per = ldp / 4, t = i / per, c = (i - t * per) * 4;
   pdl_wait();
   if (t >= (size_t)T) return;
@@ -1133,6 +1134,8 @@ __global__ void __launch_bounds__(256) w4_parts_kernel(const float* __restrict__
     const float4 v = __ldcs(reinterpret_cast<const float4*>(p + (size_t)j * T * ldp));
     s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
   }
+  const float m = pow2(rexp[t]);
+  s.x *= m, s.y *= m, s.z *= m, s.w *= m;
   const float v[4] = {s.x, s.y, s.z, s.w};
   const size_t at = t * ldo + c;
   if (out_f32) {
@@ -1184,7 +1187,7 @@ int launch_w4_linear_gemm(const uint16_t* x, size_t ldx, int T, const uint8_t* w
   const int rc = launch_gemm<kLinear>(g, r.xp, s);
   if (rc != MOE_OK) return rc;
   MOE_CUDA_TRY(launch_pdl(w4_parts_kernel, dim3((unsigned)(((size_t)T * (ldp / 4) + 255) / 256)), dim3(256), 0, s,
-                          (const float*)part, g.parts, T, d.N, ldp, out, ldo, out_f32));
+                          (const float*)part, (const int32_t*)r.xexp, g.parts, T, d.N, ldp, out, ldo, out_f32));
   return MOE_OK;
 }
 
