@@ -307,14 +307,13 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalArgs a, i
     const float dt = dot * inv;
     if (valid) loss += dt;
     if (a.grad) {
-      const float gs = gscale * inv;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         float v[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const int i = c * V + j;
-          v[j] = gs * q[i] * (f[i] - dt);
+          v[j] = gscale * (q[i] * inv * (f[i] - dt));  // gscale * inv alone could leave fp32's range
           if (SIG) v[j] *= keep[i];
           if (!valid) v[j] = 0.f;
         }
