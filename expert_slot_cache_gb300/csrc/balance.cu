@@ -233,7 +233,8 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalArgs a, i
     return v;
   };
 
-  float loss = 0.f, f[N];
+  double loss = 0.;  // (in 32 bits the roundings add up: 2^24 equal tokens were 2e-5 off)
+  float f[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) f[i] = 0.f;
   for (; t - g < t_end; t += G, row += (size_t)G * a.E) {  // the same number of rounds for every lane
@@ -324,9 +325,8 @@ __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalArgs a, i
   }
   if (!a.loss) return;
   // one value per token group, then the groups of a warp, the warps, the CTAs: a fixed order
-  if (gl != 0) loss = 0.f;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) loss += __shfl_xor_sync(MOE_FULL_MASK, loss, o);
+  for (int o = 16; o >= L; o >>= 1) loss += __shfl_xor_sync(MOE_FULL_MASK, loss, o);  // (a group's lanes hold the same)
   if (lane == 0) s_loss[warp] = loss;
   __syncthreads();
   if (threadIdx.x == 0) {
