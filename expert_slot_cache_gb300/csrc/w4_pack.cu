@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const W4PackArgs a) {
   const W4PackMat& m = a.m[blockIdx.z % a.mats];
   const size_t item = blockIdx.z / a.mats;
   const W4Dims& d = m.d;
-  const int k0 = blockIdx.x * kPackRows, n0 = blockIdx.y * kPackCols, ld = src_ld(m);
+  const int k0 = blockIdx.y * kPackRows, n0 = blockIdx.x * kPackCols, ld = src_ld(m);
   if (k0 >= d.Kb * 64 || n0 >= d.Mt * 16) return;
   uint8_t* dst = a.dst + item * a.dst_item + m.dst;
   uint16_t* dsc = reinterpret_cast<uint16_t*>(dst + d.scales);
@@ -167,7 +167,6 @@ static int launch_pack(const W4PackArgs& a, int count, cudaStream_t s) {
     nc = std::max(nc, (d.Mt * 16 + kPackCols - 1) / kPackCols);
     sc = std::max(sc, (d.Mt * 16 + 127) / 128);
   }
-  if (nc > 65535) return MOE_ERR_ARG;
   const int per = 65535 / a.mats;  // items per launch: the grid's z
   for (int i0 = 0; i0 < count; i0 += per) {
     const int n = std::min(per, count - i0);
@@ -176,7 +175,7 @@ static int launch_pack(const W4PackArgs& a, int count, cudaStream_t s) {
     if (b.w) b.w += i0 * a.src_item;
     b.dst += i0 * a.dst_item;
     w4_meta_kernel<<<(n * a.mats + 127) / 128, 128, 0, s>>>(b, n * a.mats);
-    w4_pack_kernel<<<dim3(kc, nc, n * a.mats), 256, 0, s>>>(b);
+    w4_pack_kernel<<<dim3(nc, kc, n * a.mats), 256, 0, s>>>(b);  // (kc <= 8192, nc up to 2^17: the grid's x)
     w4_scale_kernel<<<dim3(sc, n * a.mats), 128, 0, s>>>(b);
     MOE_LAUNCH_CHECK();
   }
