@@ -48,6 +48,8 @@ struct LayerWs {
   int32_t* perm;
   float* skp;
   size_t skp_bytes;
+  void* w4;  // 4-bit slabs: all of the FFN's buffers
+  size_t w4_bytes;
   size_t bytes;
 };
 
@@ -83,18 +85,23 @@ static LayerWs carve(void* base, int n, int H, int E, int I, int T) {
   w.ev_e = (int32_t*)take(4 * (size_t)lmax);
   w.kept_e = (int32_t*)take(4 * (size_t)lmax);
   w.n_kept = (int32_t*)take(4);
-  w.hbuf = (float*)take(4 * (size_t)n * I);
   w.y = (float*)take(4 * (size_t)n * H);
   w.logits = (float*)take(4 * (size_t)T * E);
   w.route = (float*)take(moe_route_scratch_bytes(T, H, E) + 4);
   w.perm = (int32_t*)take(moe_permute_scratch_bytes(n, E) + 4);
+  // The FFN's own buffers, one after the other.  4-bit slabs need none of them and use the whole stretch: it holds
+  // 4nI + 2nH + 2nI bytes or more (the second and third as xp and hb from 4096 rows on, in skp below), and w4_ws_bytes
+  // is 4nI, or from 129 rows on 2nH + 2n (I + 32) + 20n and eight paddings.
+  const size_t ffn = off;
+  w.hbuf = (float*)take(4 * (size_t)n * I);
   if (prefill_extra_bytes(n, H, I) > 0) {
     w.xp = (uint16_t*)take(2 * (size_t)n * H);
     w.hb = (uint16_t*)take(2 * (size_t)n * I);
   }
-  // bf16 stream, W8A8 or 4-bit buffers
-  w.skp_bytes = std::max(std::max(sk_part_bytes(n, H, I), q8_ws_bytes(n, H, I)), w4_ws_bytes(n, H, I));
+  w.skp_bytes = std::max(sk_part_bytes(n, H, I), q8_ws_bytes(n, H, I));  // bf16 stream or W8A8 buffers
   if (w.skp_bytes) w.skp = (float*)take(w.skp_bytes);
+  w.w4 = b ? b + ffn : nullptr;
+  w.w4_bytes = off - ffn;
   w.bytes = off;
   return w;
 }
@@ -246,7 +253,7 @@ extern "C" int moe_layer_forward(const moe_layer_args* a, moe_stream_t main_s, m
 
   const int C = chunk_tokens(T, k, S, E, mode, policy, a->schedule);
   LayerWs ws = carve(a->workspace, C * k, H, E, I, T);
-  if (a->workspace_bytes < ws.bytes) return MOE_ERR_ALIGN;
+  if (a->workspace_bytes < ws.bytes || (w4_slabs && ws.w4_bytes < w4_ws_bytes(C * k, H, I))) return MOE_ERR_ALIGN;
 
   cudaStream_t ms = (cudaStream_t)main_s;
   cudaStream_t ss = (cudaStream_t)side_s;
@@ -327,7 +334,7 @@ extern "C" int moe_layer_forward(const moe_layer_args* a, moe_stream_t main_s, m
     // the FFN of one expert list: bf16 slabs (stream / prefill / CUDA-core paths), W8A8 or 4-bit slabs
     auto ffn_of = [&](const FfnArgs& fa, int maxl, cudaStream_t st) {
       return q8_slabs   ? launch_ffn_q8(fa, ws.skp, ws.skp_bytes, maxl, st, &prof)
-             : w4_slabs ? launch_ffn_w4(fa, a->quant_group, ws.skp, ws.skp_bytes, maxl, st, &prof)
+             : w4_slabs ? launch_ffn_w4(fa, a->quant_group, ws.w4, ws.w4_bytes, maxl, st, &prof)
                         : launch_ffn(fa, maxl, st, &prof);
     };
     auto ffn = [&](const FfnArgs& fa, cudaStream_t st) { return ffn_of(fa, lmax, st); };
