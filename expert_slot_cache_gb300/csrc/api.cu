@@ -54,6 +54,7 @@ struct LayerWs {
 };
 
 // n = routing slots per chunk, T = tokens of the whole step (router logits).
+constexpr int kMaxSplitRows = 4096;  // routing slots up to which sk_part_bytes and q8_ws_bytes are not 0
 static LayerWs carve(void* base, int n, int H, int E, int I, int T) {
   LayerWs w{};
   size_t off = 0;
@@ -212,8 +213,11 @@ extern "C" int moe_combine(const float* y, const float* w, const int32_t* pos, c
 
 extern "C" size_t moe_layer_workspace_bytes(int T, int H, int E, int k, int I, int S) {
   if (T < 1 || k < 1 || E < 1 || S < 1) return 0;
-  // Worst case over modes: the largest chunk is all T tokens.
-  return carve(nullptr, T * k, H, E, I, T).bytes;
+  // Worst case over modes, chunks and smaller steps: up to 4096 routing slots the split sums of the weight streams need
+  // a size that does not grow with the slots alone.
+  size_t most = carve(nullptr, T * k, H, E, I, T).bytes;
+  for (int c = 1; c <= std::min(T, kMaxSplitRows / k); ++c) most = std::max(most, carve(nullptr, c * k, H, E, I, T).bytes);
+  return most;
 }
 
 extern "C" size_t moe_workspace_bytes(int T, int H, int I, int E, int k) {
