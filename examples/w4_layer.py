@@ -76,7 +76,8 @@ def main(argv=None):
     resident = torch.arange(slots, dtype=torch.int32).numpy()
     host = torch.empty(packed.shape, dtype=torch.uint8, pin_memory=True)
     host.copy_(packed)
-    layer = M.SlotCachedMoELayer(wr.contiguous(), packed[:slots].clone(), K, I, M.MODE_GATHER, M.POLICY_LRU,
+    router = wr.to(torch.bfloat16).contiguous()  # the layer's router is bf16
+    layer = M.SlotCachedMoELayer(router, packed[:slots].clone(), K, I, M.MODE_GATHER, M.POLICY_LRU,
                                  host_slabs=host, state=M.CacheState.from_slots(resident, E), max_tokens=1, quant=2,
                                  quant_group=GROUP)
     token, text = torch.zeros(1, dtype=torch.int64, device=dev), []
@@ -92,7 +93,8 @@ def main(argv=None):
     misses = int(layer.stats[0])
     print(f"{a.tokens} tokens in {(time.perf_counter() - t0) * 1e3:.2f} ms; {misses} of {(a.tokens + 1) * K} experts gathered")
     assert int(layer.dev_status.item()) == 0 and int(op_head.dev_status.item()) == 0
-    return dict(before=before, after=after, text=text, packed=packed, slabs=slabs, head=head, op_head=op_head)
+    return dict(before=before, after=after, text=text, packed=packed, slabs=slabs, head=head, op_head=op_head, layer=layer,
+                router=router, embed=embed)
 
 
 if __name__ == "__main__":

@@ -649,6 +649,8 @@ class SlotCachedMoELayer:
     def __init__(self, w_router, pool, k, I, mode, policy=POLICY_LRU, host_slabs=None, state=None,
                  logit_offset=None, sel_bias=None, max_tokens=64, side_stream=True, affinity=0.0,
                  route_flags=0, window_counts=None, quant=0, schedule=0, decode_kernels=0, quant_group=0):
+        if w_router.dtype != torch.bfloat16:
+            raise ValueError(f"w_router: need bfloat16 [H][E], got {w_router.dtype}")
         self.w_router, self.pool, self.k, self.I = w_router, pool, k, I
         self.H, self.E = w_router.shape
         self.S = pool.shape[0]
