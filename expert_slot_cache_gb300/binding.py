@@ -581,6 +581,18 @@ def balance_loss(logits: torch.Tensor, ids: torch.Tensor, coef: float, seq_start
     return Balance(loss, counts, grad)
 
 
+class _BalanceGrad(torch.autograd.Function):
+    """The gradient as a function of what it came from: to differentiate it again is an error, it is not a constant."""
+
+    @staticmethod
+    def forward(ctx, grad, logits, grad_loss):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("BalanceLoss has no second derivative")
+
+
 class BalanceLoss(torch.autograd.Function):
     """balance_loss for autograd: ``loss, counts = BalanceLoss.apply(logits, ids, coef, seq_start, token_mask, sigmoid)``."""
 
@@ -596,8 +608,9 @@ class BalanceLoss(torch.autograd.Function):
     def backward(ctx, grad_loss, _):
         logits, ids, seq_start, token_mask = ctx.saved_tensors
         r = balance_loss(logits, ids, ctx.coef, seq_start, token_mask, ctx.sigmoid, with_loss=False, with_grad=True,
-                         grad_loss=grad_loss.float().contiguous())
-        return r.grad, None, None, None, None, None
+                         grad_loss=grad_loss.detach().float().contiguous())
+        grad = _BalanceGrad.apply(r.grad, logits, grad_loss) if torch.is_grad_enabled() else r.grad
+        return grad, None, None, None, None, None
 
 
 def ffn_workspace_bytes(T: int, H: int, k: int, I: int) -> int:
