@@ -333,6 +333,7 @@ struct W4FfnArgs {
   int n;                  // routing slots
   // Routed form: the groups come from the ids (row = flat routing slot), the combine follows in w4_sum_kernel.
   const int32_t* ids;     // [n], or NULL: f.offset / f.rows / f.list_e / f.n_list (row = grouped position)
+  const int32_t* sum_ids; // [n] where the combine follows: the ids, whichever form the groups come in
   const int32_t* pos;     // [n] row of y of every slot, where the groups are given and the combine follows
   int cap;                // row batches that there can be
   const float* w;         // [n]
@@ -513,18 +514,22 @@ __global__ void __launch_bounds__(128) w4_sum_kernel(const W4FfnArgs a) {
   if (c >= H) return;
   float4 y[kMaxK], s = make_float4(0.f, 0.f, 0.f, 0.f);
   float w[kMaxK];
+  int e[kMaxK];
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j) {
+    e[j] = j < k ? a.sum_ids[t * k + j] : -1;
+    w[j] = j < k ? a.w[t * k + j] : 0.f;
+  }
 #pragma unroll
   for (int j = 0; j < kMaxK; ++j) {
     y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-    w[j] = 0.f;
-    const int at = t * k + j;
-    int p = -1;  // the slot's row of y; none for an id that is not an expert
-    if (j < k) p = a.pos ? a.pos[at] : a.ids[at] >= 0 && a.ids[at] < a.f.E ? at : -1;
-    if (p >= 0) {
-      w[j] = a.w[at];
-      y[j] = *reinterpret_cast<const float4*>(a.f.y + (size_t)p * H + c);
-    }
+    const bool expert = e[j] >= 0 && e[j] < a.f.E;  // others have no row
+    if (expert) y[j] = *reinterpret_cast<const float4*>(a.f.y + (size_t)(a.pos ? a.pos[t * k + j] : t * k + j) * H + c);
+    e[j] = !expert ? -1 : a.f.e2s ? a.f.e2s[e[j]] : e[j];  // its slot
   }
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j)  // an expert without a slot has a row of zeros; its weight may be anything
+    if (e[j] < 0 || e[j] >= a.f.S) w[j] = 0.f;
 #pragma unroll
   for (int j = 0; j < kMaxK; ++j) {
     s.x = fmaf(w[j], y[j].x, s.x), s.y = fmaf(w[j], y[j].y, s.y);
@@ -802,7 +807,7 @@ extern "C" int moe_experts_w4(const void* x, const int32_t* ids, const float* w,
   if (r != MOE_OK) return r;
   W4FfnArgs a{};
   a.f = f, a.sl = w4_slab(H, I, group), a.h = (uint16_t*)ws.ffn, a.n = n;
-  a.w = w, a.out = (uint16_t*)out;
+  a.w = w, a.sum_ids = ids, a.out = (uint16_t*)out;
   if (!gemm && n <= kW4Slots) {
     a.ids = ids;
     return launch_ffn_w4_stream(a, group, sms, s, nullptr);

@@ -1,0 +1,45 @@
+"""The routed 4-bit experts beside weights and scales that are not finite."""
+import pytest
+import torch
+
+from tests._setup import rel_l2
+from tests.test_gpu_w4 import RL2_OUT_BF16, draw_experts, draw_routing, experts_plain
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.mark.parametrize("weight", [float("inf"), float("nan")])
+@pytest.mark.parametrize("T", [1, 9, 60, 300])  # the kernels' own groups, given groups, large tiles
+def test_missing_experts_add_nothing_whatever_their_weight(T, weight):
+    import expert_slot_cache_gb300 as M
+    H, I, E, k, group, S = 128, 64, 60, 9, 64, 50
+    codes, scales = draw_experts(H, I, E, group, 3)
+    pool = M.w4_pack_slabs(codes[:S].contiguous(), scales[:S].contiguous(), H, I, group)
+    e2s = torch.full((E,), -1, dtype=torch.int32, device=DEV)
+    e2s[:S] = torch.arange(S, dtype=torch.int32, device=DEV)
+    e2s[E - 1] = S  # outside the pool
+    x = torch.randn(T, H, generator=torch.Generator(device=DEV).manual_seed(T), device=DEV).to(torch.bfloat16)
+    ids, w = draw_routing(T, S, k, 5)
+    for t, j, e in ((0, 2, E - 2), (T // 2, 3, E - 1), (T - 1, 1, -1), (T - 1, 0, E)):
+        ids[t, j], w[t, j] = e, weight
+    op = M.W4Experts(pool, H, I, k, E, group, e2s=e2s, max_tokens=T)
+    want = experts_plain(x, ids, w, codes, scales, H, I, group, skip=range(S, E))
+    assert bool(want.isfinite().all())
+    assert rel_l2(op.forward(x, ids, w).double().cpu(), want.cpu()) <= RL2_OUT_BF16
+    assert int(op.dev_status.item()) != 0
+
+
+@pytest.mark.parametrize("T", [1, 60])
+def test_ids_past_the_experts_add_nothing_in_a_larger_pool(T):
+    import expert_slot_cache_gb300 as M
+    H, I, E, k, group, S = 128, 64, 60, 9, 64, 70
+    codes, scales = draw_experts(H, I, S, group, 3)
+    pool = M.w4_pack_slabs(codes, scales, H, I, group)
+    x = torch.randn(T, H, generator=torch.Generator(device=DEV).manual_seed(T), device=DEV).to(torch.bfloat16)
+    ids, w = draw_routing(T, E, k, 5)
+    ids[0, 2], w[0, 2] = E + 3, float("inf")
+    op = M.W4Experts(pool, H, I, k, E, group, max_tokens=T)
+    want = experts_plain(x, ids, w, codes[:E], scales[:E], H, I, group)
+    assert bool(want.isfinite().all())
+    assert rel_l2(op.forward(x, ids, w).double().cpu(), want.cpu()) <= RL2_OUT_BF16
