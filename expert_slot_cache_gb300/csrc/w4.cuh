@@ -26,7 +26,8 @@
 //                            not finite.  fp16 scales below 2 then keep every bit of a bf16 scale down
 //                            to 2^-14 of the column's largest one, and (code - 8) * scale has at most 11
 //                            significant bits: exact in fp16.
-//   meta    [4] fp32         [0] the largest column 2-norm of W (bounds |x W| by |x| times it), 0 0 0
+//   meta    [4] fp32         [0] the largest column 2-norm of W (bounds |x W| by |x| times it; columns whose norm
+//                            is not finite are left out), 0 0 0
 //
 // Inputs beyond K and columns beyond N have code 8 (weight 0) and scale 0.
 #pragma once

@@ -165,10 +165,10 @@ __device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// 2^e >= 1.001 |column|_2 of every column (0 for a matrix of zeros or a norm that is not finite).
+// 2^e >= 1.001 |column|_2 of every column whose norm is finite (0 for a matrix of zeros).
 __device__ __forceinline__ int w4_norm_exp(const uint8_t* meta) {
   const float c = *reinterpret_cast<const float*>(meta);
-  return c > 0.f && c < INFINITY ? ilogbf(c) + 1 : 0;
+  return c > 0.f ? ilogbf(c) + 1 : 0;
 }
 // |y| <= |h|_2 |column|_2 <= sqrt(I) 2^15 2^hexp 2^norm_exp: the exponent that takes y / 2^hexp below 2^15.
 __device__ __forceinline__ int w4_y_exp(const uint8_t* m, const W4Dims& d) {

@@ -145,9 +145,11 @@ __global__ void __launch_bounds__(128) w4_scale_kernel(const W4PackArgs a) {
     sc[at] = __half_as_ushort(__float2half_rn(r));
   }
   reinterpret_cast<float*>(dst + d.mult)[n] = ldexpf(1.f, e);
-  // 1e-3 up: the sum above is rounded, the bound must not be below the norm
+  // 1e-3 up: the sum above is rounded, the bound must not be below the norm.  A column with a scale that is not finite
+  // has no results to bound; the others keep theirs.
   uint8_t* meta = m.paired && (tile & 1) ? a.dst + item * a.dst_item + m.meta : dst + d.meta;
-  atomicMax(reinterpret_cast<int*>(meta), __float_as_int(ldexpf(sqrtf(norm) * 1.001f, e)));
+  const float bound = ldexpf(sqrtf(norm) * 1.001f, e);
+  if (bound < INFINITY) atomicMax(reinterpret_cast<int*>(meta), __float_as_int(bound));
 }
 
 __global__ void w4_meta_kernel(const W4PackArgs a, int n) {

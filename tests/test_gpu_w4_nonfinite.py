@@ -43,3 +43,22 @@ def test_ids_past_the_experts_add_nothing_in_a_larger_pool(T):
     want = experts_plain(x, ids, w, codes[:E], scales[:E], H, I, group)
     assert bool(want.isfinite().all())
     assert rel_l2(op.forward(x, ids, w).double().cpu(), want.cpu()) <= RL2_OUT_BF16
+
+
+@pytest.mark.parametrize("scale", [float("inf"), float("nan")])
+@pytest.mark.parametrize("T", [3, 200])
+def test_a_column_without_finite_values_leaves_the_others(T, scale):
+    """One output column of every expert has a scale that is not finite; the others are large."""
+    import expert_slot_cache_gb300 as M
+    H, I, E, k, group = 128, 64, 6, 3, 64
+    codes, scales = draw_experts(H, I, E, group, 3)
+    down = scales[:, 2 * (H // group) * I:].view(E, I // group, H)
+    down *= 2.0 ** 24
+    down[:, 0, 5] = scale
+    op = M.W4Experts(M.w4_pack_slabs(codes, scales, H, I, group), H, I, k, E, group, max_tokens=T)
+    x = torch.randn(T, H, generator=torch.Generator(device=DEV).manual_seed(T), device=DEV).to(torch.bfloat16)
+    ids, w = draw_routing(T, E, k, 5)
+    out, want = op.forward(x, ids, w).double().cpu(), experts_plain(x, ids, w, codes, scales, H, I, group).cpu()
+    others = [n for n in range(H) if n != 5]
+    assert not bool(out[:, 5].isfinite().any()) and bool(want[:, others].isfinite().all())
+    assert rel_l2(out[:, others], want[:, others]) <= RL2_OUT_BF16
