@@ -184,15 +184,27 @@ __device__ __forceinline__ float w4_sum_part(const float* red, int w0, int ks, i
   return s;
 }
 
-// One result in 64 bits, for a sum that left fp32's range on its way: inputs above some 2^100, infinities, NaN.
+// Whether a row has neither infinities nor NaN (those have given the formula's result already); by a whole warp.
+__device__ __noinline__ bool w4_finite(const uint16_t* x, int K) {
+  const uint4* at = reinterpret_cast<const uint4*>(x);
+  uint32_t bad = 0;
+#pragma unroll 4
+  for (int k = threadIdx.x & 31; k < K / 8; k += 32) {
+    const uint4 v = at[k];
+    for (uint32_t u : {v.x, v.y, v.z, v.w}) bad |= __vcmpeq2(u & 0x7f807f80u, 0x7f807f80u);
+  }
+  return !__any_sync(MOE_FULL_MASK, bad);
+}
+
+// One result in 64 bits, for a sum of finite inputs that left fp32's range on its way: inputs above some 2^100.
 // Reached by such results alone, and in a pass of its own after a kernel's stream (called from the stream's rounds it
-// took registers from them: 32 tokens 98.3 / 101.5 us), so in no hurry; what is NaN stays NaN.  codes: the packed column's words in its tile's
+// took registers from them: 32 tokens 98.3 / 101.5 us), so in no hurry.  codes: the packed column's words in its tile's
 // block 0 (g: its place among the tile's first or second eight), sc: its scale of group 0, mates: w4_mates.
 template <bool LO>
 __device__ __noinline__ float w4_dot_at(const uint32_t* codes, const __half* sc, int mates, int g, float mult, int K, int G,
                                         const uint16_t* x, size_t lo) {
   double sum = 0.;
-  for (int k = 0; k < K && sum == sum; k += 8) {
+  for (int k = 0; k < K; k += 8) {
     const int b = k >> 5, q = (k >> 3) & 3;
     const uint32_t v = codes[(size_t)(b >> 1) * mates * 128 + w4_chunk(g, q) * 4 + (b & 1)];
     const double s = __half2float(sc[(size_t)(k / G) * mates * 16]);
@@ -291,6 +303,7 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_linear_kernel(const W4
   const int rounds = (groups - (int)blockIdx.x * sub + (int)gridDim.x * sub - 1) / ((int)gridDim.x * sub);
   const int t0 = blockIdx.y * 8 * NB, nt = min(8 * NB, a.T - t0);
   const float* mult = reinterpret_cast<const float*>(a.w + a.d.mult);
+  __shared__ bool fin[8 * NB];  // rows without infinities and NaN; only where a result was lost
   auto first = [&](int r, int g) { return ((r * (int)gridDim.x + (int)blockIdx.x) * sub + g) * CM; };  // tile
   auto unit = [&](int r) {
     W4Unit<NB> u;
@@ -311,6 +324,7 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_linear_kernel(const W4
       const size_t o = (size_t)(t0 + row) * a.ldo + n;
       float v;
       if (again) {
+        if (!fin[row]) continue;
         if (isfinite(a.out_f32 ? reinterpret_cast<float*>(a.out)[o] : bf16_to_f32(reinterpret_cast<uint16_t*>(a.out)[o]))) continue;
         v = w4_dot<false>(a.w, a.d, n, a.x + (size_t)(t0 + row) * a.ldx, 0);
       } else {
@@ -322,6 +336,12 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_linear_kernel(const W4
     }
   };
   w4_stream<CM, NB, false, G32>(a.d, ks, rounds, 0, red, unit, [&](int r, const float* buf) { put(r, buf, false); });
+  if (!__syncthreads_or(lost)) return;
+  for (int row = warp; row < nt; row += kW4Warps) {
+    const bool f = w4_finite(a.x + (size_t)(t0 + row) * a.ldx, a.d.K);
+    if (lane == 0) fin[row] = f;
+  }
+  __syncthreads();
   if (lost)
     for (int r = 0; r < rounds; ++r) put(r, nullptr, true);
 }
@@ -482,8 +502,10 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_gateup_kernel(const W4
       const size_t o = (size_t)b.row[row] * I + f;
       float gv, uv;
       if (again) {
-        if (isfinite(bf16_to_f32(a.h[o]))) continue;
+        // (a warp has 32 columns of one row, and gets here as a whole)
+        const bool bad = !isfinite(bf16_to_f32(a.h[o]));
         const uint16_t* x = a.f.x + (size_t)((a.ids ? b.row[row] : a.f.rows[b.row[row]]) / a.f.k) * a.f.H;
+        if (!__any_sync(MOE_FULL_MASK, bad) || !w4_finite(x, d.K) || !bad) continue;
         const int n = (tile + m) * 16 + (col & 15);
         gv = w4_dot<false>(slab(b.slot), d, n, x, 0);
         uv = w4_dot<false>(slab(b.slot), d, n + 16, x, 0);
@@ -501,7 +523,7 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_gateup_kernel(const W4
     }
   };
   w4_stream<kGuTiles, 1, false, G32>(d, ks, rounds, 0, red, unit, [&](int r, const float* buf) { put(r, buf, false); });
-  if (lost)
+  if (__any_sync(MOE_FULL_MASK, lost))
     for (int r = 0; r < rounds; ++r) put(r, nullptr, true);
 }
 
@@ -586,8 +608,11 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_down_kernel(const W4Ff
       float* y = a.f.y + (size_t)b.row[row] * d.N + n;
       float v = 0.f;
       if (again) {
-        if (isfinite(*y)) continue;
-        v = w4_dot<true>(down(b.slot), d, n, a.h + (size_t)b.row[row] * d.K, (size_t)a.n * d.K);
+        // (a warp has 32 columns of one row, and gets here as a whole)
+        const bool bad = !isfinite(*y);
+        const uint16_t* h = a.h + (size_t)b.row[row] * d.K;
+        if (!__any_sync(MOE_FULL_MASK, bad) || !w4_finite(h, d.K) || !bad) continue;
+        v = w4_dot<true>(down(b.slot), d, n, h, (size_t)a.n * d.K);
       } else if (b.slot >= 0) {
         v = w4_sum_part<kDnTiles, 1>(buf, g * ks, ks, col >> 4, row, col & 15) *
             reinterpret_cast<const float*>(down(b.slot) + d.mult)[n];
@@ -598,7 +623,7 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_down_kernel(const W4Ff
   };
   w4_stream<kDnTiles, 1, true, G32>(d, ks, rounds, (size_t)a.n * d.K, red, unit,
                                     [&](int r, const float* buf) { put(r, buf, false); });
-  if (lost)
+  if (__any_sync(MOE_FULL_MASK, lost))
     for (int r = 0; r < rounds; ++r) put(r, nullptr, true);
 }
 
