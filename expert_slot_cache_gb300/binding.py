@@ -421,7 +421,8 @@ def w4_quantize_slabs(slabs: torch.Tensor, H: int, I: int, group: int, stream=No
 class W4Linear:
     """y = x W with a packed 4-bit matrix (w4_pack, w4_quantize) of K inputs and N outputs, for up to max_tokens rows.
 
-    x may be a row-strided view (last dimension contiguous).  One call at a time: calls share the workspace.
+    x may be a row-strided view (last dimension contiguous).  One call at a time: calls share the workspace.  Forward
+    only: the result carries no gradient.
     """
 
     def __init__(self, packed: torch.Tensor, K: int, N: int, group: int, max_tokens: int = 1,
@@ -483,7 +484,7 @@ class W4Experts:
     """The routed experts of one layer over a pool of packed 4-bit slabs ([S][w4_slab_bytes] uint8, device).
 
     forward(x, ids, w) -> bf16 [T][H]: sum_j w[t][j] * FFN_{ids[t][j]}(x[t]).  One call at a time: calls share the
-    workspace.
+    workspace.  Forward only: the result carries no gradient.
     """
 
     def __init__(self, pool: torch.Tensor, H: int, I: int, k: int, E: int, group: int,
@@ -594,7 +595,10 @@ class _BalanceGrad(torch.autograd.Function):
 
 
 class BalanceLoss(torch.autograd.Function):
-    """balance_loss for autograd: ``loss, counts = BalanceLoss.apply(logits, ids, coef, seq_start, token_mask, sigmoid)``."""
+    """balance_loss for autograd: ``loss, counts = BalanceLoss.apply(logits, ids, coef, seq_start, token_mask, sigmoid)``.
+
+    It has no second derivative: differentiating the gradient again raises.
+    """
 
     @staticmethod
     def forward(ctx, logits, ids, coef, seq_start=None, token_mask=None, sigmoid=False):

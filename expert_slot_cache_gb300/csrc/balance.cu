@@ -188,9 +188,12 @@ struct BalVec {
 // Groups of L lanes take a token each; a lane holds NC chunks of V values, chunk c of lane l being the row's
 // (c L + l)-th.  CTA b takes `per` consecutive tokens.
 //
-// What bounds the pass next to memory is its instructions, so the usual row costs few: exp of the logits as
-// they are (or 1 / (1 + exp(-l))), no maximum.  A row whose sum leaves [2^-20, 2^100] is done again with the
-// maximum taken off; for the others whatever underflows is below 2^-106 of the sum.
+// The usual row costs few instructions: exp of the logits as they are (or 1 / (1 + exp(-l))), no maximum.  A row whose
+// sum leaves [2^-20, 2^100] is done again with the maximum taken off; for the others whatever underflows is below
+// 2^-106 of the sum.  The price is the rounding of the larger argument, 2^-24 of it: the gradient's largest error is
+// 2e-7 of p (f + d) for logits around 0, 4e-7 around 30, 7e-7 around 62.
+// Issue slots are 44 to 49% busy and the memory 14 to 24%: the pass waits for its loads and, between a row's two
+// reductions, for itself.  (16,384 x 512 bf16 with gradient 17.1 us with the counts, 30,011 x 288 sigmoid 19.8.)
 template <int V, int NC, int L, bool BF16, bool SIG>
 __global__ void __launch_bounds__(kBalThreads) balance_kernel(const BalArgs a, int per) {
   constexpr int W = kBalThreads / 32, G = kBalThreads / L, N = NC * V;

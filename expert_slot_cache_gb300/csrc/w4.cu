@@ -30,9 +30,11 @@ constexpr int kW4Threads = 32 * kW4Warps;
 constexpr int kW4Ctas = 2;   // resident CTAs per SM that the registers allow
 constexpr int kW4Slots = 512;  // routing slots that the stream kernels group themselves; more are grouped before them
 // Rows of an expert, on average, from which the tensor-core path takes over: a stream pays for every eight rows of an
-// expert, a large tile hardly for any of its 256.  us, streams / tensor cores: 8 experts, 12 rows each 25.1 / 30.1, 24
-// rows 39.2 / 32.0, 48 rows 62.8 / 32.9; 32 experts, 8 rows 29.5 / 36.0, 12 rows 36.4 / 34.2; 128 experts, 6 rows
-// 122 / 154, 8 rows 153 / 154, 12 rows 195 / 157.
+// expert, a large tile hardly for any of its 256.  us, streams / tensor cores: 8 experts, 12 rows each 25.0 / 32.3, 24
+// rows 39.3 / 34.1, 48 rows 64.8 / 34.2; 32 experts, 8 rows 29.0 / 37.3, 12 rows 35.7 / 36.2, 16 rows 41.5 / 36.6; 128
+// experts, 6 rows 120 / 156, 8 rows 142 / 157, 10 rows 172 / 159; 288 experts, 8 rows 233 / 238, 10 rows 274 / 240.
+// The average counts all experts and the figures are for even loads: how many rows the experts in use have is known on
+// the device alone.
 constexpr int kGemmRows = 10;
 
 // One block of 64 inputs in registers: a lane's codes of CM tiles, their columns' scales, and the lane's inputs
@@ -717,10 +719,10 @@ static W4ExpWs w4_exp_ws(void* base, int T, int H, int I, int k, int E) {
   return w;
 }
 
-// Streams take a pass over the weights per 32 rows, about 0.55 us for 10^6 of them; the tensor-core path costs 8 us
+// Streams take a pass over the weights per 32 rows, about 0.4 us for 10^6 of them; the tensor-core path costs 8 us
 // and more (rows, launches, the pipeline's start) and then little.  us, streams / tensor cores: 17 rows, 4096 x 4096
-// 11.3 / 11.9, x 16384 35.2 / 19.1; 33 rows, 4096 x 4096 20.3 / 12.6, 1024 x 8192 13.3 / 10.4; 128 rows, 2048 x 2048
-// 15.2 / 11.7, 1024 x 1024 6.2 / 10.7; 512 rows, 1024 x 1024 18.7 / 12.7, 512 x 512 8.4 / 11.2.
+// 8.8 / 12.0, x 16384 25.5 / 19.0; 33 rows, 4096 x 4096 16.0 / 12.5, 1024 x 8192 11.2 / 10.5; 128 rows, 2048 x 2048
+// 12.4 / 11.7, 1024 x 1024 5.5 / 10.6; 512 rows, 1024 x 1024 16.2 / 12.7, 512 x 512 7.6 / 11.3.
 static bool w4_gemm_linear(int T, int K, int N) {
   const double work = (double)((T + 31) / 32) * K * N;
   return T > 16 && work >= (T > 32 ? 1 << 24 : 1 << 25);

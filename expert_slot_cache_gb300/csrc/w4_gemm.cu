@@ -29,7 +29,7 @@
 // codes, 17 allocates TMEM and, in the pair's first CTA, issues the MMAs (one lane).
 // A visit has one barrier for its rows' bytes and its workers' arrivals, and one commit gives both rings back:
 // with a barrier and a commit per stage and ring the issuing warp needed 390 cycles a stage, and 4096 rows
-// through 2048 x 4096 took 73 us instead of 66 (54 since the drain spills no registers and launches overlap; its
+// through 2048 x 4096 took 73 us instead of 66 (53 since the drain spills no registers and launches overlap; its
 // MMAs alone would take 34).  Before a tile is drained three sets have dequantised inputs of the
 // next one, so the MMAs go on while the drained values are stored.
 // TMEM: 256 accumulator columns, 4 x 64 columns of weights.
