@@ -71,16 +71,18 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const W4PackArgs a) {
       const int lg = i / kPackCols, c = i % kPackCols, g = k0 / d.G + lg, n = n0 + c;
       if (g >= d.Kg) continue;
       const int kb = k0 + lg * d.G, ke = min(kb + d.G, d.K);
-      // the weight furthest from zero gets code 0: scale = w / -8, rounded to bf16
-      float hi = 0.f, lo = 0.f;
+      // the weight furthest from zero gets code 0: scale = w / -8, rounded to bf16; NaN where a weight is, as no code can
+      // say so
+      float hi = 0.f, lo = 0.f, nan = 0.f;
       const uint16_t* col = src + src_col(m, min(n, d.N - 1), d.K);
       if (n < d.N)
         for (int k = kb; k < ke; ++k) {
           const float v = bf16_to_f32(col[(size_t)k * ld]);
           hi = fmaxf(hi, v);
           lo = fminf(lo, v);
+          if (v != v) nan = v;
         }
-      const uint16_t sb = f32_to_bf16((hi > -lo ? hi : lo) * -0.125f);
+      const uint16_t sb = f32_to_bf16((hi > -lo ? hi : lo) * -0.125f + nan);
       const float s = bf16_to_f32(sb);
       for (int k = kb; k < min(kb + d.G, d.Kb * 64); ++k) {
         int code = 8;

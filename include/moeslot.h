@@ -424,7 +424,7 @@ int moe_expert_ffn_q8(const void* x, int T, int H, int I, int k, int E, const in
  * moe_w4_quantize: w device bf16 [n][K][N] -> dst.  Per group and column: m =
  * the element furthest from zero (the positive one of equal ones is taken only
  * if it is larger), scale = bf16(m / -8), code = clamp(rint(w / scale), -8, 7)
- * + 8 in fp32 (scale 0: code 8).
+ * + 8 in fp32 (scale 0: code 8).  A group with a NaN gets scale NaN.
  * The _slabs forms take the slab layout of moe_expert_ffn (codes or bf16
  * weights [n][3HI]) with scales [n][2 ceil(H / group) I + ceil(I / group) H]
  * (gate, up, down).

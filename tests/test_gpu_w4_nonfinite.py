@@ -62,3 +62,19 @@ def test_a_column_without_finite_values_leaves_the_others(T, scale):
     others = [n for n in range(H) if n != 5]
     assert not bool(out[:, 5].isfinite().any()) and bool(want[:, others].isfinite().all())
     assert rel_l2(out[:, others], want[:, others]) <= RL2_OUT_BF16
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_quantising_does_not_hide_values_that_are_not_finite(value):
+    """A weight without a finite value: its column gives none where its group is met, other columns and groups are as before."""
+    import expert_slot_cache_gb300 as M
+    K, N, group = 192, 40, 64
+    w = (torch.randn(K, N, generator=torch.Generator().manual_seed(1)) * 0.02).to(torch.bfloat16).to(DEV)
+    op = lambda w: M.W4Linear(M.w4_quantize(w, group), K, N, group, max_tokens=2, out_dtype=torch.float32)  # noqa: E731
+    x = torch.randn(2, K, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).to(DEV)
+    want = op(w).forward(x)
+    w[70, 7] = value
+    y = op(w).forward(x)
+    others = [n for n in range(N) if n != 7]
+    assert torch.equal(y[:, others], want[:, others])
+    assert not bool(y[:, 7].isfinite().any())
