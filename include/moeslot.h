@@ -455,6 +455,7 @@ int moe_w4_quantize_slabs(const void* w, int n, int H, int I, int group, void* d
  * row.  From 17 rows on, by rows x weights, the products are taken on the
  * tensor cores from fp16 rows that are scaled by a power of two each: values of
  * a row below 2^-29 of its largest lose bits there, below 2^-40 they count as 0.
+ * (Scales above 2^88 could overflow there on the way to a finite result.)
  * Errors: MOE_ERR_ARG on NULL pointers, T < 1 or shapes out of range;
  * MOE_ERR_ALIGN if x or w is not 16-byte aligned, ldx % 8 != 0, or the
  * workspace is unaligned or too small.
