@@ -228,7 +228,7 @@ __device__ __forceinline__ float w4_dot(const uint8_t* w, const W4Dims& d, int n
 }
 
 // Warps per unit: the power of two with the least rounds x (blocks of a share + the cost of ending a round, about
-// one block: with 3 in its place 8 tokens took 51 us, with 1 46 us; 32 tokens over 288 experts 108 and 101 us).
+// one block: with 3 in its place 8 tokens took 51 us, with 1 46; 32 tokens over 288 experts 108 and 101; now 44.5 and 99).
 __host__ __device__ inline int w4_split(int units, int Kb, int ctas) {
   int best = 1;
   int64_t least = 0;
@@ -530,8 +530,8 @@ __global__ void __launch_bounds__(kW4Threads, kW4Ctas) w4_gateup_kernel(const W4
 }
 
 // out[t] = bf16(sum_j w[t][j] y[slot]), fp32, j ascending: grid (T, H / 512).  (Sums by the CTAs of the down kernel
-// that finish last save this launch, which overlaps, and cost as much: one token 16.6 us with them, 16.1 without;
-// 8 tokens 45.4 and 46.0.)
+// that finish last save this launch, which overlaps, and cost as much: one token 16.6 us with them and 16.1
+// without when that was measured, 8 tokens 45.4 and 46.0; 15.7 and 44.5 now.)
 __global__ void __launch_bounds__(128) w4_sum_kernel(const W4FfnArgs a) {
   pdl_wait();
   const int H = a.f.H, k = a.f.k, t = blockIdx.x, c = (blockIdx.y * 128 + threadIdx.x) * 4;
