@@ -71,7 +71,7 @@ _route_ex = _sig("moe_route_ex", [V, V, V, V, V, c_float, I32, I32, I32, I32, I3
 
 BIAS_GRADED, BIAS_FLAT, BIAS_HARD = 0, 1, 2
 SCHED_CHUNKS, SCHED_WAVES = 0, 1
-ROUTE_SIGMOID, ROUTE_DAMPED = 1, 2
+ROUTE_SIGMOID, ROUTE_DAMPED, ROUTE_GROUP_MAX, ROUTE_RAW = 1, 2, 4, 8
 _route_scratch = _sig("moe_route_scratch_bytes", [I32, I32, I32], c_size_t)
 _permute = _sig("moe_permute", [V, I32, I32, V, V, V, V, V, V, V, V, V])
 _permute_scratch = _sig("moe_permute_scratch_bytes", [I32, I32], c_size_t)
@@ -101,6 +101,8 @@ _experts_w4_ws = _sig("moe_experts_w4_workspace_bytes", [I32, I32, I32, I32, I32
 _experts_w4 = _sig("moe_experts_w4", [V, V, V, I32, I32, I32, I32, I32, I32, V, I32, V, V, V, c_size_t, V, V])
 _balance_ws = _sig("moe_balance_workspace_bytes", [I32, I32, I32], c_size_t)
 _balance = _sig("moe_balance_loss", [V, I32, V, V, V, I32, I32, I32, I32, I32, c_float, V, V, V, V, V, c_size_t, V, V])
+_route_groups = _sig("moe_route_groups", [V, I32, V, V, I32, I32, I32, I32, I32, I32, c_float, V, V, V])
+_route_groups_grad = _sig("moe_route_groups_grad", [V, I32, V, V, I32, I32, I32, I32, c_float, V, V, V])
 _layer = _sig("moe_layer_forward", [POINTER(LayerArgs), V, V])
 _layer_ws = _sig("moe_layer_workspace_bytes", [I32, I32, I32, I32, I32, I32], c_size_t)
 
@@ -615,6 +617,115 @@ class BalanceLoss(torch.autograd.Function):
                          grad_loss=grad_loss.detach().float().contiguous())
         grad = _BalanceGrad.apply(r.grad, logits, grad_loss) if torch.is_grad_enabled() else r.grad
         return grad, None, None, None, None, None
+
+
+# ---------------------------------------------------------------------------
+# Group-limited routing
+# ---------------------------------------------------------------------------
+
+class GroupRoute(NamedTuple):
+    ids: torch.Tensor  # int32 [T][k]
+    w: torch.Tensor    # fp32 [T][k]
+
+
+def _logits_ok(logits: torch.Tensor) -> bool:
+    """Whether the logits are bf16; refuses what is neither bf16 nor fp32."""
+    bf16 = logits.dtype == torch.bfloat16
+    if not (bf16 or logits.dtype == torch.float32) or logits.dim() != 2 or not logits.is_contiguous():
+        raise ValueError(f"logits: need contiguous fp32 or bf16 [T][E], got {logits.dtype} {tuple(logits.shape)}")
+    return bf16
+
+
+def route_groups(logits: torch.Tensor, k: int, n_group: int = 1, topk_group: int = 1,
+                 sel_bias: Optional[torch.Tensor] = None, token_mask: Optional[torch.Tensor] = None,
+                 sigmoid: bool = False, group_max: bool = False, renormalise: bool = True, scale: float = 1.0,
+                 stream=None) -> GroupRoute:
+    """Picks and weights of each token from its ``topk_group`` best of ``n_group`` groups of experts.
+
+    Forward only; ``RouteGroups`` carries the gradient of the weights.
+    """
+    bf16 = _logits_ok(logits)
+    T, E = logits.shape
+    if sel_bias is not None:
+        _want(sel_bias, "sel_bias", torch.float32, (E,))
+    if token_mask is not None:
+        _want(token_mask, "token_mask", torch.bool if token_mask.dtype == torch.bool else torch.uint8, (T,))
+    dev, index = logits.device, logits.get_device()
+    if index < 0 or any(t is not None and t.get_device() != index for t in (sel_bias, token_mask)):
+        _on(dev, sel_bias=sel_bias, token_mask=token_mask)
+    if stream is not None or _current_device() != index:  # results for the stream that the kernel runs on
+        with torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream):
+            return route_groups(logits, k, n_group, topk_group, sel_bias, token_mask, sigmoid, group_max, renormalise,
+                                scale)
+    ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
+    w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+    flags = (ROUTE_SIGMOID if sigmoid else 0) | (ROUTE_GROUP_MAX if group_max else 0) | (0 if renormalise else ROUTE_RAW)
+    _ck(_route_groups(logits.data_ptr(), bf16, None if sel_bias is None else sel_bias.data_ptr(),
+                      None if token_mask is None else token_mask.data_ptr(), T, E, k, n_group, topk_group, flags, scale,
+                      ids.data_ptr(), w.data_ptr(), _here(index)), "moe_route_groups")
+    return GroupRoute(ids, w)
+
+
+def route_groups_grad(logits: torch.Tensor, ids: torch.Tensor, grad_w: torch.Tensor, sigmoid: bool = False,
+                      renormalise: bool = True, scale: float = 1.0, dev_status=None, stream=None) -> torch.Tensor:
+    """The gradient in the logits of the weights of ``route_groups``, for the picks ``ids``."""
+    bf16 = _logits_ok(logits)
+    T, E = logits.shape
+    k = ids.shape[-1]
+    if ids.dtype != torch.int32 or ids.shape != (T, k) or not ids.is_contiguous():
+        raise ValueError(f"ids: need contiguous int32 [{T}][k], got {ids.dtype} {tuple(ids.shape)}")
+    _want(grad_w, "grad_w", torch.float32, (T, k))
+    dev, index = logits.device, logits.get_device()
+    if index < 0 or any(t is not None and t.get_device() != index for t in (ids, grad_w, dev_status)):
+        _on(dev, ids=ids, grad_w=grad_w, dev_status=dev_status)
+    if stream is not None or _current_device() != index:
+        with torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream):
+            return route_groups_grad(logits, ids, grad_w, sigmoid, renormalise, scale, dev_status)
+    grad = torch.empty_like(logits)
+    flags = (ROUTE_SIGMOID if sigmoid else 0) | (0 if renormalise else ROUTE_RAW)
+    _ck(_route_groups_grad(logits.data_ptr(), bf16, ids.data_ptr(), grad_w.data_ptr(), T, E, k, flags, scale,
+                           grad.data_ptr(), None if dev_status is None else dev_status.data_ptr(), _here(index)),
+        "moe_route_groups_grad")
+    return grad
+
+
+class _FirstGrad(torch.autograd.Function):
+    """Gradients as a function of what they came from: to differentiate them again is an error, they are no constants."""
+
+    @staticmethod
+    def forward(ctx, name, n, *args):
+        ctx.name = name
+        return tuple(None if g is None else g.view_as(g) for g in args[:n])
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.name} has no second derivative")
+
+
+class RouteGroups(torch.autograd.Function):
+    """route_groups for autograd: ``ids, w = RouteGroups.apply(logits, k, n_group, topk_group, sel_bias, token_mask,
+    sigmoid, group_max, renormalise, scale)``.
+
+    The weights have a gradient in the logits, the picks none (nor has the bias).  There is no second derivative:
+    differentiating the gradient again raises.
+    """
+
+    @staticmethod
+    def forward(ctx, logits, k, n_group=1, topk_group=1, sel_bias=None, token_mask=None, sigmoid=False, group_max=False,
+                renormalise=True, scale=1.0):
+        r = route_groups(logits, k, n_group, topk_group, sel_bias, token_mask, sigmoid, group_max, renormalise, scale)
+        ctx.save_for_backward(logits, r.ids)
+        ctx.args = sigmoid, renormalise, scale
+        ctx.mark_non_differentiable(r.ids)
+        return r.ids, r.w
+
+    @staticmethod
+    def backward(ctx, _, grad_w):
+        logits, ids = ctx.saved_tensors
+        grad = route_groups_grad(logits, ids, grad_w.detach().float().contiguous(), *ctx.args)
+        if torch.is_grad_enabled():
+            grad = _FirstGrad.apply("RouteGroups", 1, grad, logits, grad_w)[0]
+        return (grad,) + (None,) * 9
 
 
 def ffn_workspace_bytes(T: int, H: int, k: int, I: int) -> int:

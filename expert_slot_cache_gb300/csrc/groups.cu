@@ -1,0 +1,550 @@
+// Group-limited routing from given logits, and the gradient of its weights.
+//
+// The E experts are n_group groups of E / n_group neighbours.  With s = softmax(l) or sigmoid(l) and c = s + bias (no
+// bias: c is ordered as l is), a group's score is the sum of its two best c (or its best one), the topk_group best
+// groups stay, and the k best c among their experts are picked; w_j = scale s_j (/ sum_j s_j).  Equal values: the lower
+// index first.
+//
+// The picks are whole numbers, so they are those of 64-bit arithmetic: c is formed in fp32, and a token for which two
+// neighbours in the order are closer than the fp32 error bound (and not the same logit with the same bias) is picked
+// again in fp64 by its warp.  That is one token in some thousands.
+//
+// The bytes of the logits, read once, bound a large batch; what a warp does for a token (k reductions one after the
+// other) bounds it in practice, and the launch a small one.
+#include <algorithm>
+
+#include "internal.cuh"
+
+namespace moe {
+
+struct GroupArgs {
+  const void* logits;   // [T][E], fp32 or bf16
+  const float* bias;    // [E] or NULL
+  const uint8_t* mask;  // [T] or NULL
+  int T, E, k;
+  int n_group, group, topk_group;  // group = E / n_group experts
+  int lanes;                       // lanes of a group: a power of two
+  int flags;
+  float scale;
+  int32_t* ids;
+  float* w;
+};
+
+constexpr int kGrpThreads = 256;
+
+// Order of 32-bit floats as unsigned integers: absent 0, NaN 1, -inf, ..., +inf; -0 counts as 0.
+__device__ __forceinline__ uint32_t grp_key(float v) {
+  const uint32_t b = __float_as_uint(v + 0.f);
+  return v != v ? 1u : b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float grp_value(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+__device__ __forceinline__ uint64_t grp_key64(double v) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v + 0.);
+  return v != v ? 1ull : b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double grp_value64(uint64_t key) {
+  return __longlong_as_double((long long)(key >> 63 ? key ^ 0x8000000000000000ull : ~key));
+}
+__device__ __forceinline__ uint64_t grp_max64(uint64_t v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = max(v, __shfl_xor_sync(MOE_FULL_MASK, v, o));
+  return v;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float grp_logit(const void* p, size_t i) {
+  return BF16 ? bf16_to_f32(reinterpret_cast<const uint16_t*>(p)[i]) : reinterpret_cast<const float*>(p)[i];
+}
+
+// Whether fp32 does not tell the order of two scores of these keys (m at most ml).
+__device__ __forceinline__ bool grp_close(uint32_t ml, uint32_t m, float rel, float bmax) {
+  if (m <= 1u) return false;  // nothing, or a NaN
+  const float a = grp_value(ml), b = grp_value(m);
+  return !(a - b > rel * (fabsf(a) + bmax) + 1e-30f) && !(isinf(a) && a == b);
+}
+
+// V consecutive logits (16 bytes, or one).
+template <bool BF16, int V>
+__device__ __forceinline__ void grp_load(const void* p, size_t i, float* v) {
+  if constexpr (V == 1) {
+    v[0] = grp_logit<BF16>(p, i);
+  } else {
+    const uint4 r = ldg_stream(reinterpret_cast<const uint8_t*>(p) + i * (BF16 ? 2 : 4));
+    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      v[j] = BF16 ? (j & 1 ? bf16_hi(u[j / 2]) : bf16_lo(u[j / 2])) : __uint_as_float(u[j & 3]);
+  }
+}
+
+// The picks of one token in fp64, by the whole warp; lane j returns pick j.  A lane holds the experts it holds in
+// the kernel below: group lane / lanes, vectors lane % lanes + q lanes of V.
+template <int V, int NQ, bool BF16>
+__device__ __noinline__ int grp_pick64(const GroupArgs& a, size_t row) {
+  const int lane = threadIdx.x & 31, g = lane / a.lanes, i0 = lane % a.lanes;
+  const bool sig = a.flags & MOE_ROUTE_SIGMOID;
+  uint64_t key[NQ * V];
+  double mx = -INFINITY, sum = 0.;
+  auto at = [&](int u) {  // the lane's u-th expert, or -1
+    const int i = (u / V * a.lanes + i0) * V + u % V;
+    return g < a.n_group && i < a.group ? g * a.group + i : -1;
+  };
+  if (!sig) {
+    for (int u = 0; u < NQ * V; ++u)
+      if (at(u) >= 0) mx = fmax(mx, (double)grp_logit<BF16>(a.logits, row + at(u)));
+    for (int o = 16; o; o >>= 1) mx = fmax(mx, __shfl_xor_sync(MOE_FULL_MASK, mx, o));
+    for (int u = 0; u < NQ * V; ++u)
+      if (at(u) >= 0) sum += exp((double)grp_logit<BF16>(a.logits, row + at(u)) - mx);
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(MOE_FULL_MASK, sum, o);
+  }
+  double b1 = -INFINITY, b2 = -INFINITY;
+  for (int u = 0; u < NQ * V; ++u) {
+    const int e = at(u);
+    key[u] = 0;
+    if (e < 0) continue;
+    const double l = (double)grp_logit<BF16>(a.logits, row + e);
+    const double s = sig ? 1. / (1. + exp(-l)) : exp(l - mx) / sum;
+    const double c = a.bias ? s + (double)a.bias[e] : s;
+    b2 = fmax(b2, fmin(b1, c));
+    b1 = fmax(b1, c);
+    key[u] = grp_key64(a.bias ? c : l);
+  }
+  if (a.topk_group < a.n_group) {
+    for (int o = a.lanes / 2; o; o >>= 1) {
+      const double o1 = __shfl_xor_sync(MOE_FULL_MASK, b1, o), o2 = __shfl_xor_sync(MOE_FULL_MASK, b2, o);
+      b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+      b1 = fmax(b1, o1);
+    }
+    uint64_t gk;
+    if (a.flags & MOE_ROUTE_GROUP_MAX) {
+      gk = 0;
+      for (int u = 0; u < NQ * V; ++u) gk = max(gk, key[u]);
+      for (int o = a.lanes / 2; o; o >>= 1) gk = max(gk, __shfl_xor_sync(MOE_FULL_MASK, gk, o));
+    } else {
+      gk = grp_key64(a.group == 1 ? b1 : b1 + b2);
+    }
+    int before = 0;
+    for (int h = 0; h < a.n_group; ++h) {
+      const uint64_t ok = __shfl_sync(MOE_FULL_MASK, gk, h * a.lanes);
+      before += ok > gk || (ok == gk && h < g);
+    }
+    if (before >= a.topk_group)
+      for (int u = 0; u < NQ * V; ++u) key[u] = 0;
+  }
+  int mine = -1;
+  for (int j = 0; j < a.k; ++j) {
+    uint64_t best = 0;
+    for (int u = 0; u < NQ * V; ++u) best = max(best, key[u]);
+    const uint64_t m = grp_max64(best);
+    int e = INT_MAX;
+    for (int u = NQ * V - 1; u >= 0; --u)
+      if (key[u] == m && at(u) >= 0) e = at(u);
+    e = __reduce_min_sync(MOE_FULL_MASK, e);
+    for (int u = 0; u < NQ * V; ++u)
+      if (at(u) == e) key[u] = 0;
+    if (lane == j) mine = e;
+  }
+  return mine;
+}
+
+// One warp routes a token.  Lane (g, i) holds the vectors i, i + lanes, ... of V experts of group g, so that a group's
+// score takes log2(lanes) shuffles.
+template <int V, int NQ, bool BF16>
+__global__ void __launch_bounds__(kGrpThreads) group_route_kernel(const GroupArgs a) {
+  constexpr int NE = NQ * V;
+  pdl_wait();
+  const int lane = threadIdx.x & 31, g = lane / a.lanes, i0 = lane % a.lanes;
+  const bool sig = a.flags & MOE_ROUTE_SIGMOID, raw = a.flags & MOE_ROUTE_RAW, gmax = a.flags & MOE_ROUTE_GROUP_MAX;
+  const bool limited = a.topk_group < a.n_group;
+  const bool sums = limited && !gmax;         // groups are chosen by sums of scores
+  const bool scores = a.bias || sums;         // scores are needed for the choice
+  const bool total = !sig && (scores || raw);  // the softmax over all experts is
+  const int e0 = g * a.group + i0 * V;        // vector q starts at expert e0 + q lanes V
+  const int step = a.lanes * V;
+  const int held = g < a.n_group ? max(0, a.group - i0 * V + step - 1) / step : 0;  // vectors of this lane
+  float bmax = 0.f;
+  if (a.bias) {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (q < held) {
+          const float b = fabsf(a.bias[e0 + q * step + j]);
+          if (b < INFINITY) bmax = fmaxf(bmax, b);
+        }
+    bmax = __uint_as_float(__reduce_max_sync(MOE_FULL_MASK, __float_as_uint(bmax)));
+  }
+  const int warps = gridDim.x * (kGrpThreads / 32);
+  for (int t = blockIdx.x * (kGrpThreads / 32) + (threadIdx.x >> 5); t < a.T; t += warps) {
+    const size_t row = (size_t)t * a.E;
+    if (a.mask && !a.mask[t]) {
+      if (lane < a.k) {
+        a.ids[(size_t)t * a.k + lane] = -1;
+        a.w[(size_t)t * a.k + lane] = 0.f;
+      }
+      continue;
+    }
+    float l[NE];
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      if (q < held) {
+        grp_load<BF16, V>(a.logits, row + e0 + q * step, l + q * V);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) l[q * V + j] = -INFINITY;
+      }
+    }
+    float mx = 0.f, sum = 1.f;
+    if (total) {
+      mx = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < NE; ++u) mx = fmaxf(mx, l[u]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(MOE_FULL_MASK, mx, o));
+      sum = 0.f;
+#pragma unroll
+      for (int u = 0; u < NE; ++u)
+        if (u / V < held) sum += expf(l[u] - mx);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(MOE_FULL_MASK, sum, o);
+    }
+    const float inv = 1.f / sum;
+    uint32_t key[NE];
+    float b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int u = q * V + j;
+        float c = l[u];
+        if (scores) {
+          const float s = sig ? __fdividef(1.f, 1.f + expf(-c)) : expf(c - mx) * inv;
+          const float v = a.bias && q < held ? s + a.bias[e0 + q * step + j] : s;
+          if (a.bias) c = v;
+          if (q < held) {
+            b2 = fmaxf(b2, fminf(b1, v));
+            b1 = fmaxf(b1, v);
+          }
+        }
+        key[u] = q < held ? grp_key(c) : 0u;
+      }
+    // Error bound of a difference of two scores, relative to them: exp, a reciprocal and two roundings each (2^-21),
+    // and for a softmax the rounding of an argument below 64 and the sum's (2^-18).
+    const float rel = sig ? 0x1p-19f : 0x1p-17f;
+    bool close = false;
+    if (limited) {
+      uint32_t gk = 0;
+      if (gmax) {
+#pragma unroll
+        for (int u = 0; u < NE; ++u) gk = max(gk, key[u]);
+        for (int o = a.lanes / 2; o; o >>= 1) gk = max(gk, __shfl_xor_sync(MOE_FULL_MASK, gk, o));
+      } else {
+        for (int o = a.lanes / 2; o; o >>= 1) {
+          const float o1 = __shfl_xor_sync(MOE_FULL_MASK, b1, o), o2 = __shfl_xor_sync(MOE_FULL_MASK, b2, o);
+          b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+          b1 = fmaxf(b1, o1);
+        }
+        gk = grp_key(a.group == 1 ? b1 : b1 + b2);
+      }
+      int before = 0;
+      for (int h = 0; h < a.n_group; ++h) {
+        const uint32_t ok = __shfl_sync(MOE_FULL_MASK, gk, h * a.lanes);
+        before += ok > gk || (ok == gk && h < g);
+      }
+      const bool in = before < a.topk_group && g < a.n_group;
+      if (!in) {
+#pragma unroll
+        for (int u = 0; u < NE; ++u) key[u] = 0u;
+      }
+      if (sums || a.bias) {
+        const float lo = grp_value(__reduce_min_sync(MOE_FULL_MASK, in ? gk : 0xffffffffu));
+        const float hi = grp_value(__reduce_max_sync(MOE_FULL_MASK, !in && g < a.n_group ? gk : 0u));
+        close = !(lo - hi > 2.f * rel * (fabsf(lo) + 2.f * bmax) + 1e-30f);
+      }
+    }
+    // the k best, one after the other
+    int mine = -1, last = -1;
+    uint32_t ml = 0;
+    for (int j = 0; j < a.k && !close; ++j) {
+      uint32_t best = 0;
+#pragma unroll
+      for (int u = 0; u < NE; ++u) best = max(best, key[u]);
+      const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, best);
+      int e = INT_MAX;
+#pragma unroll
+      for (int q = NQ - 1; q >= 0; --q)
+#pragma unroll
+        for (int v = V - 1; v >= 0; --v)
+          if (key[q * V + v] == m) e = e0 + q * step + v;
+      e = __reduce_min_sync(MOE_FULL_MASK, best == m ? e : INT_MAX);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (e0 + q * step + v == e) key[q * V + v] = 0u;
+      if (a.bias) {
+        if (j > 0 && grp_close(ml, m, rel, bmax))
+          close = grp_logit<BF16>(a.logits, row + e) != grp_logit<BF16>(a.logits, row + last) || a.bias[e] != a.bias[last];
+        ml = m;
+        last = e;
+      }
+      if (lane == j) mine = e;
+    }
+    if (a.bias && !close && ml > 1) {
+      // the last pick and what is left
+      const float ll = grp_logit<BF16>(a.logits, row + last), lb = a.bias[last];
+      const bool finite = fabsf(grp_value(ml)) < INFINITY;
+      uint32_t next = 0;
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const uint32_t m = key[q * V + v];
+          if (m == ml) close |= finite && (l[q * V + v] != ll || a.bias[e0 + q * step + v] != lb);
+          else next = max(next, m);
+        }
+      next = __reduce_max_sync(MOE_FULL_MASK, next);
+      close = __any_sync(MOE_FULL_MASK, close) || grp_close(ml, next, rel, bmax);
+    }
+    if (close) mine = grp_pick64<V, NQ, BF16>(a, row);
+    // weights: lane j has pick j
+    const bool on = lane < a.k;
+    const float z = on ? grp_logit<BF16>(a.logits, row + mine) : -INFINITY;
+    float w = 0.f;
+    if (raw) {
+      if (on) w = sig ? 1.f / (1.f + expf(-z)) : expf(z - mx) / sum;
+    } else {
+      float top = z;
+#pragma unroll
+      for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(MOE_FULL_MASK, top, o));
+      if (on) {
+        if (sig) {
+          // sigmoid(z) / exp(min(top, 0)): a row of large negative logits keeps its proportions
+          const float em = expf(-fabsf(z));
+          w = expf(fminf(z, 0.f) - (top == -INFINITY ? 0.f : fminf(top, 0.f))) / (1.f + em);
+        } else {
+          w = expf(z - (top == -INFINITY ? 0.f : top));
+        }
+      }
+      float all = w;
+#pragma unroll
+      for (int o = 8; o; o >>= 1) all += __shfl_xor_sync(MOE_FULL_MASK, all, o);
+      w = all == 0.f ? 0.f : w / all;  // picks of -inf alone have no weight
+    }
+    if (on) {
+      a.ids[(size_t)t * a.k + lane] = mine;
+      a.w[(size_t)t * a.k + lane] = w * a.scale;
+    }
+  }
+}
+
+struct GroupGradArgs {
+  const void* logits;
+  const int32_t* ids;
+  const float* gw;  // [T][k]
+  int T, E, k, flags;
+  float scale;
+  void* grad;
+  int32_t* status;
+};
+
+template <bool BF16>
+__device__ __forceinline__ void grp_put(void* p, size_t i, float v) {
+  if (BF16) reinterpret_cast<uint16_t*>(p)[i] = f32_to_bf16(v);
+  else reinterpret_cast<float*>(p)[i] = v;
+}
+
+// The gradient of a token's weights, one warp a token.  With W = sum_i g_i w_i / scale over its picks:
+//   renormalised      w_j (g_j - W)   [sigmoid: (1 - s_j)]         in the picks alone
+//   not, sigmoid      scale g_j s_j (1 - s_j)                      in the picks alone
+//   not, softmax      s_e (scale G_e - sum_i scale g_i s_i)        everywhere; G_e: the g of the picks of e
+// The row is written in whole vectors first and the picks' values over it by the same warp.  A pick that is there
+// twice adds up, in the order of the picks.
+template <int V, bool BF16>
+__global__ void __launch_bounds__(kGrpThreads) group_grad_kernel(const GroupGradArgs a) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const bool sig = a.flags & MOE_ROUTE_SIGMOID, raw = a.flags & MOE_ROUTE_RAW, dense = raw && !sig;
+  const int warps = gridDim.x * (kGrpThreads / 32);
+  for (int t = blockIdx.x * (kGrpThreads / 32) + (threadIdx.x >> 5); t < a.T; t += warps) {
+    const size_t row = (size_t)t * a.E;
+    int e = -1;
+    if (lane < a.k) {
+      e = a.ids[(size_t)t * a.k + lane];
+      if (e < -1 || e >= a.E) set_status(a.status, MOE_DEV_BAD_EXPERT);
+      if (e >= a.E) e = -1;
+    }
+    const bool on = e >= 0;
+    const bool any = __any_sync(MOE_FULL_MASK, on);
+    const float gj = on ? a.gw[(size_t)t * a.k + lane] * a.scale : 0.f;
+    const float z = on ? grp_logit<BF16>(a.logits, row + e) : -INFINITY;
+    float mx = 0.f, inv = 0.f;
+    float p = 0.f, jac = 1.f;  // the pick's share of the sum that its weight is over
+    if (!raw || dense) {
+      mx = z;
+      if (dense && any)
+        for (int i = lane; i < a.E; i += 32) mx = fmaxf(mx, grp_logit<BF16>(a.logits, row + i));
+#pragma unroll
+      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(MOE_FULL_MASK, mx, o));
+      if (mx == -INFINITY) mx = 0.f;
+    }
+    if (on) {
+      const float em = expf(-fabsf(z));
+      if (sig) jac = (z >= 0.f ? em : 1.f) / (1.f + em);
+      if (sig && raw) p = (z >= 0.f ? 1.f : em) / (1.f + em);
+      else p = sig ? expf(fminf(z, 0.f) - fminf(mx, 0.f)) / (1.f + em) : expf(z - mx);
+    }
+    float dot = 0.f;
+    if (!raw || dense) {
+      float sum = 0.f;
+      if (dense) {
+        if (any)
+          for (int i = lane; i < a.E; i += 32) sum += expf(grp_logit<BF16>(a.logits, row + i) - mx);
+      } else {
+        sum = p;
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(MOE_FULL_MASK, sum, o);
+      inv = sum == 0.f ? 0.f : 1.f / sum;
+      p *= inv;
+      dot = on ? p * gj : 0.f;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(MOE_FULL_MASK, dot, o);
+    }
+    // the row without its picks
+    for (int i = lane * V; i < a.E; i += 32 * V) {
+      float v[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = 0.f;
+      if (dense && any) {
+        grp_load<BF16, V>(a.logits, row + i, v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = expf(v[j] - mx) * inv * -dot;
+      }
+      if constexpr (V == 1) {
+        grp_put<BF16>(a.grad, row + i, v[0]);
+      } else {
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (BF16) {
+            const __nv_bfloat162 q = __floats2bfloat162_rn(v[(2 * j) % V], v[(2 * j + 1) % V]);
+            o[j] = *reinterpret_cast<const uint32_t*>(&q);
+          } else {
+            o[j] = __float_as_uint(v[j]);
+          }
+        }
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.grad) + (row + i) * (BF16 ? 2 : 4)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+    __syncwarp();
+    // the picks: the first lane of a repeated one adds all of them
+    const unsigned same = __match_any_sync(MOE_FULL_MASK, on ? e : -1 - lane);
+    const bool twice = __any_sync(MOE_FULL_MASK, on && (same & (same - 1)));
+    float v;
+    if (dense) {
+      float all = gj;
+      if (twice) {
+        all = 0.f;
+        for (int j = 0; j < a.k; ++j) {
+          const float o = __shfl_sync(MOE_FULL_MASK, gj, j);
+          if (same >> j & 1) all += o;
+        }
+      }
+      v = p * (all - dot);
+    } else {
+      const float own = raw ? p * gj * jac : p * (gj - dot) * jac;
+      v = own;
+      if (twice) {
+        v = 0.f;
+        for (int j = 0; j < a.k; ++j) {
+          const float o = __shfl_sync(MOE_FULL_MASK, own, j);
+          if (same >> j & 1) v += o;
+        }
+      }
+    }
+    if (on && (same & lanemask_lt()) == 0) grp_put<BF16>(a.grad, row + e, v);
+  }
+}
+
+static int grp_sms(int* sms) {
+  int dev = 0;
+  MOE_CUDA_TRY(cudaGetDevice(&dev));
+  MOE_CUDA_TRY(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
+  return MOE_OK;
+}
+
+template <int V, int NQ, bool BF16>
+static int launch_groups(const GroupArgs& a, int sms, cudaStream_t s) {
+  const int grid = std::min((a.T + 7) / 8, sms * 4);
+  MOE_CUDA_TRY(launch_pdl(group_route_kernel<V, NQ, BF16>, dim3(grid), dim3(kGrpThreads), 0, s, a));
+  return MOE_OK;
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_route_groups(const void* logits, int bf16, const float* sel_bias, const uint8_t* token_mask, int T,
+                                int E, int k, int n_group, int topk_group, int rflags, float scale, int32_t* ids,
+                                float* w, moe_stream_t stream) {
+  if (!logits || !ids || !w || (bf16 != 0 && bf16 != 1)) return MOE_ERR_ARG;
+  if (T < 1 || T > (1 << 26) || E < 1 || E > kMaxE || n_group < 1 || n_group > 32 || E % n_group || topk_group < 1 ||
+      topk_group > n_group || k < 1 || k > kMaxK || k > topk_group * (E / n_group))
+    return MOE_ERR_ARG;
+  if (rflags & ~(MOE_ROUTE_SIGMOID | MOE_ROUTE_RAW | MOE_ROUTE_GROUP_MAX)) return MOE_ERR_ARG;
+  if ((uintptr_t)logits % (bf16 ? 2 : 4)) return MOE_ERR_ALIGN;
+  int sms = 0;
+  if (int rc = grp_sms(&sms)) return rc;
+  int lanes = 32;
+  while (lanes * n_group > 32) lanes /= 2;
+  const int group = E / n_group;
+  const GroupArgs a{logits, sel_bias, token_mask, T, E, k, n_group, group, topk_group, lanes, rflags, scale, ids, w};
+  cudaStream_t s = (cudaStream_t)stream;
+  const int v = bf16 ? 8 : 4;
+  const int each = (group + lanes - 1) / lanes;  // experts of a lane
+  const int quads = (group + lanes * v - 1) / (lanes * v);
+  if (group % v == 0 && (uintptr_t)logits % 16 == 0 && quads * v <= 32) {
+    if (bf16) {
+      if (quads <= 1) return launch_groups<8, 1, true>(a, sms, s);
+      if (quads <= 2) return launch_groups<8, 2, true>(a, sms, s);
+      return launch_groups<8, 4, true>(a, sms, s);
+    }
+    if (quads <= 1) return launch_groups<4, 1, false>(a, sms, s);
+    if (quads <= 2) return launch_groups<4, 2, false>(a, sms, s);
+    if (quads <= 4) return launch_groups<4, 4, false>(a, sms, s);
+    return launch_groups<4, 8, false>(a, sms, s);
+  }
+  if (bf16) {
+    if (each <= 4) return launch_groups<1, 4, true>(a, sms, s);
+    if (each <= 16) return launch_groups<1, 16, true>(a, sms, s);
+    return launch_groups<1, 64, true>(a, sms, s);
+  }
+  if (each <= 4) return launch_groups<1, 4, false>(a, sms, s);
+  if (each <= 16) return launch_groups<1, 16, false>(a, sms, s);
+  return launch_groups<1, 64, false>(a, sms, s);
+}
+
+extern "C" int moe_route_groups_grad(const void* logits, int bf16, const int32_t* ids, const float* grad_w, int T, int E,
+                                     int k, int rflags, float scale, void* grad_logits, int32_t* dev_status,
+                                     moe_stream_t stream) {
+  if (!logits || !ids || !grad_w || !grad_logits || (bf16 != 0 && bf16 != 1)) return MOE_ERR_ARG;
+  if (T < 1 || T > (1 << 26) || E < 1 || E > kMaxE || k < 1 || k > kMaxK) return MOE_ERR_ARG;
+  if (rflags & ~(MOE_ROUTE_SIGMOID | MOE_ROUTE_RAW)) return MOE_ERR_ARG;
+  if ((uintptr_t)logits % (bf16 ? 2 : 4) || (uintptr_t)grad_logits % (bf16 ? 2 : 4)) return MOE_ERR_ALIGN;
+  int sms = 0;
+  if (int rc = grp_sms(&sms)) return rc;
+  const GroupGradArgs a{logits, ids, grad_w, T, E, k, rflags, scale, grad_logits, dev_status};
+  const int v = bf16 ? 8 : 4;
+  const bool vec = E % v == 0 && (uintptr_t)logits % 16 == 0 && (uintptr_t)grad_logits % 16 == 0;
+  const dim3 grid(std::min((T + 7) / 8, sms * 8)), block(kGrpThreads);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (vec && bf16) MOE_CUDA_TRY(launch_pdl(group_grad_kernel<8, true>, grid, block, 0, s, a));
+  else if (vec) MOE_CUDA_TRY(launch_pdl(group_grad_kernel<4, false>, grid, block, 0, s, a));
+  else if (bf16) MOE_CUDA_TRY(launch_pdl(group_grad_kernel<1, true>, grid, block, 0, s, a));
+  else MOE_CUDA_TRY(launch_pdl(group_grad_kernel<1, false>, grid, block, 0, s, a));
+  return MOE_OK;
+}

@@ -539,6 +539,59 @@ int moe_balance_loss(const void* logits, int bf16, const int32_t* ids, const uin
                      const float* grad_loss, int32_t* counts, float* loss, void* grad_logits, void* workspace,
                      size_t workspace_bytes, int32_t* dev_status, moe_stream_t stream);
 
+/* Further flags of moe_route_groups (with MOE_ROUTE_SIGMOID). */
+#define MOE_ROUTE_GROUP_MAX 4 /* a group's score is its best choice, not the sum of its two best */
+#define MOE_ROUTE_RAW 8       /* weights are the scores as they are, not over the sum of the picks */
+
+/*
+ * Group-limited routing from given logits: the picks and weights that
+ * moe_experts_w4, moe_permute and moe_combine take.  ("Nudge, don't cut" keeps
+ * a bias in the selection alone; the groups keep a token's experts together.)
+ * The experts are n_group groups of E / n_group consecutive ones.  With
+ *   s = softmax(logits[t]) over all E, or with MOE_ROUTE_SIGMOID sigmoid(logits[t]),
+ *   c = s + sel_bias          (no bias: the order of c is that of the logits)
+ *   a group's score = the sum of its two best c (its one c, if it has one
+ *       expert; without a bias c = s here), or its best c with MOE_ROUTE_GROUP_MAX,
+ * the topk_group groups of highest score stay, the k highest c of their experts
+ * are picked, in descending order, and
+ *   w[t][j] = scale * s_j / sum_i s_i   over the picks, with MOE_ROUTE_RAW scale * s_j.
+ * Equal values: the lower index first.  NaN ranks behind everything else.  The
+ * picks are those of 64-bit arithmetic; they do not depend on thread timing.
+ * Renormalised picks that are all -inf have weight 0.
+ *   logits     device [T][E], fp32 or bf16 (bf16 = 1)
+ *   sel_bias   device fp32 [E] or NULL; -inf: never picked while k others stay
+ *   token_mask device uint8 [T], 0 = padding, or NULL; padding gets ids -1 and
+ *              weights 0, its logits are not read into any result
+ *   ids        device int32 [T][k] output
+ *   w          device fp32 [T][k] output
+ * Errors: MOE_ERR_ARG on NULL pointers, T not in [1, 2^26], E not in [1, 1024],
+ * n_group not in [1, 32] or no divisor of E, topk_group not in [1, n_group],
+ * k not in [1, min(16, topk_group * E / n_group)], or unknown flags;
+ * MOE_ERR_ALIGN for logits that are not aligned to their type.
+ */
+int moe_route_groups(const void* logits, int bf16, const float* sel_bias, const uint8_t* token_mask, int T, int E, int k,
+                     int n_group, int topk_group, int rflags, float scale, int32_t* ids, float* w,
+                     moe_stream_t stream);
+
+/*
+ * The gradient of these weights in the logits, the picks held fixed.  With
+ * s as above, W = sum_i grad_w[t][i] w[t][i] / scale over the token's picks:
+ *   renormalised            grad[t][ids_j] += w_j (grad_w_j - W)  [* (1 - s_j)]
+ *   MOE_ROUTE_RAW, sigmoid  grad[t][ids_j] += scale grad_w_j s_j (1 - s_j)
+ *   MOE_ROUTE_RAW, softmax  grad[t][e] = scale s_e (sum_{j: ids_j = e} grad_w_j - sum_i grad_w_i s_i)
+ * and 0 elsewhere.  grad_logits is written whole.
+ *   ids     device int32 [T][k]; -1: no pick (a token without any gets a zero
+ *           gradient; its logits are not read); a pick may be there twice
+ *   grad_w  device fp32 [T][k]
+ *   grad_logits  device [T][E] output in the type of logits
+ * An id outside [-1, E) sets MOE_DEV_BAD_EXPERT and counts as -1.  Picks of
+ * -inf alone get a zero gradient.
+ * Errors: MOE_ERR_ARG on NULL pointers, shapes out of range (k not in [1, 16])
+ * or flags other than MOE_ROUTE_SIGMOID and MOE_ROUTE_RAW; MOE_ERR_ALIGN as above.
+ */
+int moe_route_groups_grad(const void* logits, int bf16, const int32_t* ids, const float* grad_w, int T, int E, int k,
+                          int rflags, float scale, void* grad_logits, int32_t* dev_status, moe_stream_t stream);
+
 /*
  * How GATHER mode serves a step that needs more experts than the pool holds
  * ("Porting vllm-expert-cache to NVIDIA GPUs", "Measuring, without fooling
