@@ -14,4 +14,4 @@ from .binding import (MODE_GATHER, MODE_RESIDENT, MODE_ZERO_RETURN, POLICY_LFU, 
                       q8_slab_bytes, quantize_slabs, expert_ffn_q8, SCHED_CHUNKS, SCHED_WAVES,
                       w4_bytes, w4_slab_bytes, w4_pack, w4_quantize, w4_pack_slabs, w4_quantize_slabs, W4Linear,
                       expert_ffn_w4, W4Experts, Balance, BalanceLoss, balance_loss,
-                      GroupRoute, RouteGroups, route_groups, route_groups_grad)
+                      GroupRoute, RouteGroups, route_groups, route_groups_grad, Adapters, AdapterAdd, AdapterGrads)

@@ -103,6 +103,10 @@ _balance_ws = _sig("moe_balance_workspace_bytes", [I32, I32, I32], c_size_t)
 _balance = _sig("moe_balance_loss", [V, I32, V, V, V, I32, I32, I32, I32, I32, c_float, V, V, V, V, V, c_size_t, V, V])
 _route_groups = _sig("moe_route_groups", [V, I32, V, V, I32, I32, I32, I32, I32, I32, c_float, V, V, V])
 _route_groups_grad = _sig("moe_route_groups_grad", [V, I32, V, V, I32, I32, I32, I32, c_float, V, V, V])
+_adapters = _sig("moe_adapters", [V, LL, V, LL, I32, I32, I32, I32, I32, V, V, V, V, V, I32, V, LL, I32, V, V, V])
+_adapters_grad_ws = _sig("moe_adapters_grad_workspace_bytes", [I32, I32], c_size_t)
+_adapters_grad = _sig("moe_adapters_grad", [V, LL, V, LL, V, V, LL, I32, I32, I32, I32, I32, V, V, V, V, V, I32, V, LL, V, V,
+                                            V, c_size_t, V, V])
 _layer = _sig("moe_layer_forward", [POINTER(LayerArgs), V, V])
 _layer_ws = _sig("moe_layer_workspace_bytes", [I32, I32, I32, I32, I32, I32], c_size_t)
 
@@ -425,6 +429,9 @@ class W4Linear:
 
     x may be a row-strided view (last dimension contiguous).  One call at a time: calls share the workspace.  Forward
     only: the result carries no gradient.
+
+    ``forward(x, adapters=, adapter_ids=, seq_start=)`` adds the low-rank part of each request's adapter (``Adapters``)
+    to the result, in place.
     """
 
     def __init__(self, packed: torch.Tensor, K: int, N: int, group: int, max_tokens: int = 1,
@@ -443,7 +450,15 @@ class W4Linear:
         self._packed, self._status = packed.data_ptr(), self.dev_status.data_ptr()
         self._ws, self._ws_bytes, self._f32 = self.workspace.data_ptr(), self.workspace.numel(), out_dtype == torch.float32
 
-    def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None,
+                adapters: Optional["Adapters"] = None, adapter_ids: Optional[torch.Tensor] = None,
+                seq_start: Optional[torch.Tensor] = None) -> torch.Tensor:
+        if adapters is not None:
+            if (adapters.K, adapters.N) != (self.K, self.N) or adapter_ids is None:
+                raise ValueError(f"adapters: need {self.K} inputs, {self.N} outputs and adapter_ids")
+            adapters.check(x, adapter_ids, seq_start, self.out_dtype, out)  # nothing is written where the second call refuses
+            out = self.forward(x, out, stream)
+            return adapters.forward(x, adapter_ids, out, seq_start, out, stream=stream)
         T, K = x.shape
         if T > self.max_tokens or K != self.K:
             raise ValueError(f"x is {T} x {K}; the layer takes up to {self.max_tokens} rows of {self.K}")
@@ -463,6 +478,173 @@ class W4Linear:
                        out.data_ptr(), out.stride(0) if T > 1 else self.N, self._f32, self._ws, self._ws_bytes,
                        self._status, _here(dev, stream)), "moe_w4_linear")
         return out
+
+
+# ---------------------------------------------------------------------------
+# Low-rank adapters beside a projection
+# ---------------------------------------------------------------------------
+
+class AdapterGrads(NamedTuple):
+    dx: Optional[torch.Tensor]  # bf16 [T][K]
+    da: Optional[torch.Tensor]  # fp32 [L][R][K]
+    db: Optional[torch.Tensor]  # fp32 [L][R][N]
+
+
+class Adapters:
+    """L low-rank adapters of rank R for a projection of K inputs and N outputs: out = base + scale_l (x A_l^T) B_l.
+
+    ``a`` bf16 [L][R][K], ``b`` bf16 [L][R][N] and ``scale`` fp32 [L] are read where they are: what is written into them
+    counts from the next call on.  Sequence q of a batch is the rows [seq_start[q], seq_start[q + 1]) with the adapter
+    ids[q] (int32, -1: none); without ``seq_start`` every row is a sequence of its own.  Rows may be row-strided views
+    on 16 bytes.  ``AdapterAdd`` is the form for autograd; forward and grad carry no gradient themselves.
+    """
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor):
+        if a.dim() != 3 or b.dim() != 3 or a.shape[:2] != b.shape[:2]:
+            raise ValueError(f"a, b: need [L][R][K] and [L][R][N], got {tuple(a.shape)} and {tuple(b.shape)}")
+        _want(a, "a", torch.bfloat16)
+        _want(b, "b", torch.bfloat16)
+        _want(scale, "scale", torch.float32, (a.shape[0],))
+        self.a, self.b, self.scale = a, b, scale
+        (self.L, self.R, self.K), self.N = a.shape, b.shape[2]
+        if not (1 <= self.L <= 65535 and 1 <= self.R <= 128) or any(n % 8 or not 8 <= n <= 1 << 17 for n in (self.K, self.N)):
+            raise ValueError(f"a, b: 1..65535 adapters of rank 1..128, 8..131072 features in eights, got "
+                             f"{tuple(a.shape)} and {tuple(b.shape)}")
+        self.device, self._index = a.device, a.get_device()
+        if b.device != a.device or scale.device != a.device:
+            raise ValueError(f"a, b, scale: on {a.device}, {b.device} and {scale.device}")
+        self.dev_status = torch.zeros(1, dtype=torch.int32, device=a.device)
+        self._a, self._b, self._scale, self._status = (t.data_ptr() for t in (a, b, scale, self.dev_status))
+
+    def _sequences(self, T, ids, seq_start):
+        n = T if seq_start is None else seq_start.numel() - 1
+        if ids.dtype != torch.int32 or ids.shape != (n,) or not ids.is_contiguous():
+            raise ValueError(f"ids: need contiguous int32 [{n}], got {ids.dtype} {tuple(ids.shape)}")
+        if seq_start is not None:
+            _want(seq_start, "seq_start", torch.int32, (n + 1,))
+        return n
+
+    @staticmethod
+    def _rows(t, what, T, n, dtype):
+        if t.dtype != dtype or t.shape != (T, n) or (t.stride(1) != 1 and n > 1):
+            raise ValueError(f"{what}: need {dtype} ({T}, {n}) with a contiguous last dimension, got {t.dtype} "
+                             f"{tuple(t.shape)}")
+        return t.data_ptr(), t.stride(0) if T > 1 else n
+
+    def check(self, x, ids, seq_start, dtype, out) -> None:
+        """Refuses what forward would refuse."""
+        T = x.shape[0]
+        self._sequences(T, ids, seq_start)
+        for what, t, n, kind in (("x", x, self.K, torch.bfloat16), ("out", out, self.N, dtype)):
+            if t is not None:
+                at, ld = self._rows(t, what, T, n, kind)
+                if at % 16 or ld * t.element_size() % 16:
+                    raise MoeError(-3, f"Adapters ({what})")
+        _on(self.device, x=x, ids=ids, seq_start=seq_start, out=out)
+
+    def forward(self, x: torch.Tensor, ids: torch.Tensor, base: Optional[torch.Tensor] = None,
+                seq_start: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                out_dtype=torch.bfloat16, kept: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """base + the adapters' part, in a new tensor or in ``out`` (base itself, if need be), of the type of base or
+        out (neither: ``out_dtype``).  ``kept`` (fp32 [T][R]) receives scale_l x A_l^T for the gradient."""
+        T = x.shape[0]
+        px, ldx = self._rows(x, "x", T, self.K, torch.bfloat16)
+        n = self._sequences(T, ids, seq_start)
+        dtype = base.dtype if base is not None else out.dtype if out is not None else out_dtype
+        f32 = dtype == torch.float32
+        if not f32 and dtype != torch.bfloat16:
+            raise ValueError(f"base, out: bfloat16 or float32, got {dtype}")
+        pb, ldb = (None, 0) if base is None else self._rows(base, "base", T, self.N, dtype)
+        if kept is not None:
+            _want(kept, "kept", torch.float32, (T, self.R))
+        dev = self._index
+        if (dev < 0 or x.get_device() != dev or ids.get_device() != dev
+                or any(t is not None and t.get_device() != dev for t in (base, seq_start, out, kept))):
+            _on(self.device, x=x, ids=ids, base=base, seq_start=seq_start, out=out, kept=kept)
+        if _current_device() != dev:
+            with torch.cuda.device(self.device):
+                return self.forward(x, ids, base, seq_start, out, out_dtype, kept, stream)
+        if out is None:
+            out = _result(stream, T, self.N, dtype=dtype, device=self.device)
+        po, ldo = self._rows(out, "out", T, self.N, dtype)
+        _ck(_adapters(px, ldx, pb, ldb, T, self.K, self.N, self.R, self.L, self._a, self._b, self._scale, ids.data_ptr(),
+                      None if seq_start is None else seq_start.data_ptr(), n, po, ldo, f32,
+                      None if kept is None else kept.data_ptr(), self._status, _here(dev, stream)), "moe_adapters")
+        return out
+
+    def grad(self, dy: torch.Tensor, x: Optional[torch.Tensor], kept: Optional[torch.Tensor], ids: torch.Tensor,
+             base: Optional[torch.Tensor] = None, seq_start: Optional[torch.Tensor] = None, with_dx: bool = True,
+             with_weights: bool = True, stream=None) -> AdapterGrads:
+        """The gradients in x (plus ``base``), a and b, from that in out; ``kept`` as the forward pass left it."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.grad(dy, x, kept, ids, base, seq_start, with_dx, with_weights)
+        T = dy.shape[0]
+        pdy, ldy = self._rows(dy, "dy", T, self.N, torch.bfloat16)
+        n = self._sequences(T, ids, seq_start)
+        px = ldx = pk = None
+        if with_weights:
+            if x is None or kept is None:
+                raise ValueError("x, kept: needed for the gradients in a and b")
+            px, ldx = self._rows(x, "x", T, self.K, torch.bfloat16)
+            _want(kept, "kept", torch.float32, (T, self.R))
+            pk = kept.data_ptr()
+        pb, ldb = (None, 0) if base is None else self._rows(base, "base", T, self.K, torch.bfloat16)
+        dev = self._index
+        if (dev < 0 or dy.get_device() != dev or ids.get_device() != dev
+                or any(t is not None and t.get_device() != dev for t in (x, kept, base, seq_start))):
+            _on(self.device, dy=dy, x=x, kept=kept, ids=ids, base=base, seq_start=seq_start)
+        if _current_device() != dev:
+            with torch.cuda.device(self.device):
+                return self.grad(dy, x, kept, ids, base, seq_start, with_dx, with_weights)
+        dx = torch.empty((T, self.K), dtype=torch.bfloat16, device=self.device) if with_dx else None
+        da = torch.empty(self.a.shape, dtype=torch.float32, device=self.device) if with_weights else None
+        db = torch.empty(self.b.shape, dtype=torch.float32, device=self.device) if with_weights else None
+        nws = _adapters_grad_ws(T, self.R)
+        ws = torch.empty(nws, dtype=torch.uint8, device=self.device)
+        _ck(_adapters_grad(pdy, ldy, px, ldx or 0, pk, pb, ldb, T, self.K, self.N, self.R, self.L, self._a, self._b,
+                           self._scale, ids.data_ptr(), None if seq_start is None else seq_start.data_ptr(), n,
+                           None if dx is None else dx.data_ptr(), self.K, None if da is None else da.data_ptr(),
+                           None if db is None else db.data_ptr(), ws.data_ptr(), nws, self._status, _here(dev)),
+            "moe_adapters_grad")
+        return AdapterGrads(dx, da, db)
+
+
+class AdapterAdd(torch.autograd.Function):
+    """Adapters for autograd: ``out = AdapterAdd.apply(x, a, b, scale, ids, base, seq_start)``, bf16.
+
+    Gradients in x, a, b and base (none in scale).  There is no second derivative: differentiating the gradient again
+    raises.
+    """
+
+    @staticmethod
+    def forward(ctx, x, a, b, scale, ids, base=None, seq_start=None):
+        if base is not None and base.dtype != torch.bfloat16:
+            raise ValueError(f"base: bfloat16 where a gradient is wanted, got {base.dtype}")
+        need = any(ctx.needs_input_grad[1:3])
+        op = Adapters(a, b, scale)
+        kept = torch.empty((x.shape[0], op.R), dtype=torch.float32, device=x.device) if need else None
+        out = op.forward(x, ids, base, seq_start, kept=kept)
+        ctx.save_for_backward(x if need else None, a, b, scale, ids, seq_start, kept)
+        return out
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, a, b, scale, ids, seq_start, kept = ctx.saved_tensors
+        op = Adapters(a.detach(), b.detach(), scale.detach())
+        need_x, need_a, need_b = ctx.needs_input_grad[:3]
+        rows = dy.detach()
+        if rows.stride(1) != 1 or rows.stride(0) % 8 or rows.stride(0) < op.N or rows.data_ptr() % 16:
+            rows = rows.contiguous()
+        dx = da = db = None
+        if need_x or need_a or need_b:
+            g = op.grad(rows, x, kept, ids, None, seq_start, need_x, need_a or need_b)
+            dx = g.dx
+            da = g.da.to(a.dtype) if need_a else None
+            db = g.db.to(b.dtype) if need_b else None
+            if torch.is_grad_enabled():
+                dx, da, db = _FirstGrad.apply("AdapterAdd", 3, dx, da, db, dy, x, a, b)
+        return dx, da, db, None, None, dy if ctx.needs_input_grad[5] else None, None
 
 
 @_for_its_stream

@@ -1,0 +1,252 @@
+// Low-rank adapters of many requests beside a shared projection, and their gradients.
+//
+// Sequence q of a batch is the rows [seq[q], seq[q + 1]) and has the adapter l = ids[q], or none:
+//   v = s_l x A_l^T  (R values a row),   out = base + v B_l;
+//   dv = s_l dy B_l^T,   dx = base + dv A_l,   dA_l = sum_t dv_t x_t^T,   dB_l = sum_t v_t dy_t^T.
+// A [L][R][K] and B [L][R][N] both run along the features, so the gradient's dx is the forward pass with A and B
+// exchanged, and dA and dB are one kernel.
+#include <algorithm>
+
+#include "adapters.cuh"
+
+namespace moe {
+
+constexpr int kRowThreads = 256;
+constexpr int kRowCluster = 8;
+
+__device__ __forceinline__ uint32_t ad_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void ad_cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void ad_cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void ad_store_remote(float* p, uint32_t rank, float v) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(at)
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ float ad_dot8(uint4 x, uint4 w, float s) {
+  const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s = fmaf(bf16_lo(a[i]), bf16_lo(b[i]), s);
+    s = fmaf(bf16_hi(a[i]), bf16_hi(b[i]), s);
+  }
+  return s;
+}
+__device__ __forceinline__ void ad_axpy8(float v, uint4 w, float (&acc)[8]) {
+  const uint32_t b[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    acc[2 * i] = fmaf(v, bf16_lo(b[i]), acc[2 * i]);
+    acc[2 * i + 1] = fmaf(v, bf16_hi(b[i]), acc[2 * i + 1]);
+  }
+}
+
+// out = base + acc over 8 values, one rounding.
+template <bool F32>
+__device__ __forceinline__ void ad_add8(const void* base, void* out, long long ib, long long io, const float (&acc)[8]) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = acc[i];
+  if (F32) {
+    if (base) {
+      const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + ib);
+      const float4 b0 = p[0], b1 = p[1];
+      v[0] += b0.x, v[1] += b0.y, v[2] += b0.z, v[3] += b0.w, v[4] += b1.x, v[5] += b1.y, v[6] += b1.z, v[7] += b1.w;
+    }
+    float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + io);
+    q[0] = make_float4(v[0], v[1], v[2], v[3]);
+    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    if (base) {
+      const uint4 b = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + ib);
+      const uint32_t u[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[2 * i] += bf16_lo(u[i]), v[2 * i + 1] += bf16_hi(u[i]);
+    }
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 q = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      o[i] = *reinterpret_cast<const uint32_t*>(&q);
+    }
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(out) + io) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// One cluster of CTAs per row: CTA c takes its share of the K inputs for all R products, the partial sums meet in every
+// CTA's shared memory, and CTA c computes its share of the N outputs.  One launch, no workspace.
+template <bool F32>
+__global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(const AdArgs a) {
+  extern __shared__ __align__(16) unsigned char ad_smem[];
+  __shared__ float s_part[kRowCluster][kAdMaxR];
+  __shared__ float s_v[kAdMaxR];
+  pdl_wait();
+  const int c = (int)ad_rank(), t = blockIdx.x / kRowCluster;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int s = ad_sequence(a, t);
+  const int l = s < 0 ? -1 : ad_adapter(a, s);
+  const int nv = a.N / 8, n0 = nv * c / kRowCluster, n1 = nv * (c + 1) / kRowCluster;
+  if (t == 0 && a.seq)
+    for (int q = c * kRowThreads + tid; q < a.n_seq; q += kRowCluster * kRowThreads)
+      if (a.seq[q + 1] < a.seq[q]) set_status(a.status, MOE_DEV_BAD_GROUPS);
+  if (l < 0) {
+    if (a.kept && c == 0)
+      for (int r = tid; r < a.R; r += kRowThreads) a.kept[(size_t)t * a.R + r] = 0.f;
+    const float none[8] = {};
+    if (a.out && (a.out != a.base || a.ldo != a.ldb))
+      for (int j = n0 + tid; j < n1; j += kRowThreads)
+        ad_add8<F32>(a.base, a.out, t * a.ldb + 8 * j, t * a.ldo + 8 * j, none);
+    return;
+  }
+  ad_cluster_arrive();
+  const int kv = a.K / 8, k0 = kv * c / kRowCluster, k1 = kv * (c + 1) / kRowCluster;
+  uint4* xs = reinterpret_cast<uint4*>(ad_smem);
+  const uint4* xr = reinterpret_cast<const uint4*>(a.x + t * a.ldx) + k0;
+  for (int i = tid; i < k1 - k0; i += kRowThreads) xs[i] = xr[i];
+  __syncthreads();
+  ad_cluster_wait();  // the other CTAs have started
+  const uint4* w1 = reinterpret_cast<const uint4*>(a.w1 + (size_t)l * a.R * a.K) + k0;
+  for (int r = warp; r < a.R; r += kRowThreads / 32) {
+    float sum = 0.f;
+    for (int i = lane; i < k1 - k0; i += 32) sum = ad_dot8(xs[i], w1[(size_t)r * kv + i], sum);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(MOE_FULL_MASK, sum, o);
+    if (lane < kRowCluster) ad_store_remote(&s_part[c][r], lane, sum);
+  }
+  ad_cluster_arrive();
+  ad_cluster_wait();
+  for (int r = tid; r < a.R; r += kRowThreads) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRowCluster; ++i) sum += s_part[i][r];
+    sum *= a.scale[l];
+    s_v[r] = sum;
+    if (a.kept && c == 0) a.kept[(size_t)t * a.R + r] = sum;
+  }
+  __syncthreads();
+  if (!a.out) return;
+  const uint4* w2 = reinterpret_cast<const uint4*>(a.w2 + (size_t)l * a.R * a.N);
+  for (int j = n0 + tid; j < n1; j += kRowThreads) {
+    float acc[8] = {};
+    for (int r = 0; r < a.R; ++r) ad_axpy8(s_v[r], w2[(size_t)r * nv + j], acc);
+    ad_add8<F32>(a.base, a.out, t * a.ldb + 8 * j, t * a.ldo + 8 * j, acc);
+  }
+}
+
+// dA and dB: a thread has one feature and 16 ranks, and goes over the rows of one adapter.
+constexpr int kOutThreads = 128;
+constexpr int kOutRanks = 16;
+__global__ void __launch_bounds__(kOutThreads) adapters_outer_kernel(const AdGradArgs a) {
+  pdl_wait();
+  const int ka = (a.K + kOutThreads - 1) / kOutThreads;
+  const bool first = (int)blockIdx.x < ka;
+  const int F = first ? a.K : a.N, f = ((int)blockIdx.x - (first ? 0 : ka)) * kOutThreads + threadIdx.x;
+  const int l = blockIdx.y, r0 = blockIdx.z * kOutRanks;
+  const uint16_t* x = first ? a.x : a.dy;
+  const long long ld = first ? a.ldx : a.ldy;
+  const float* v = first ? a.dv : a.v;
+  float acc[kOutRanks] = {};
+  for (int s = 0; s < a.n_seq; ++s) {
+    if (a.ids[s] != l) continue;
+    const int t0 = a.seq ? max(a.seq[s], 0) : s, t1 = a.seq ? min(a.seq[s + 1], a.T) : s + 1;
+    for (int t = t0; t < t1; ++t) {
+      const float xv = f < F ? bf16_to_f32(x[t * ld + f]) : 0.f;
+#pragma unroll
+      for (int i = 0; i < kOutRanks; ++i)
+        if (r0 + i < a.R) acc[i] = fmaf(v[(size_t)t * a.R + r0 + i], xv, acc[i]);
+    }
+  }
+  if (f >= F) return;
+  float* o = (first ? a.da : a.db) + ((size_t)l * a.R + r0) * F + f;
+#pragma unroll
+  for (int i = 0; i < kOutRanks; ++i)
+    if (r0 + i < a.R) o[(size_t)i * F] = acc[i];
+}
+
+static int ad_launch_rows(const AdArgs& a, bool f32, cudaStream_t s) {
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = kRowCluster;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.T * kRowCluster);
+  cfg.blockDim = dim3(kRowThreads);
+  cfg.dynamicSmemBytes = (size_t)(a.K / 8 / kRowCluster + 1) * 16;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  if (f32) MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, adapters_row_kernel<true>, a));
+  else MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, adapters_row_kernel<false>, a));
+  return MOE_OK;
+}
+
+static bool ad_shape(int T, int K, int N, int R, int L, const int32_t* seq, int n_seq) {
+  return T >= 1 && T <= (1 << 24) && K >= 8 && K <= (1 << 17) && N >= 8 && N <= (1 << 17) && R >= 1 && R <= kAdMaxR &&
+         L >= 1 && L <= 65535 && n_seq >= 1 && n_seq <= (1 << 24) && (seq || n_seq == T);
+}
+// Rows of `ld` elements of `size` bytes that hold n: on 16 bytes, one behind the other.
+static bool ad_rows_ok(const void* p, long long ld, int n, int size) {
+  return (uintptr_t)p % 16 == 0 && ld * size % 16 == 0 && ld < (1ll << 31);
+}
+static size_t ad256(size_t v) { return (v + 255) & ~size_t(255); }
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_adapters(const void* x, long long ldx, const void* base, long long ldb, int T, int K, int N, int R,
+                            int L, const void* a, const void* b, const float* scale, const int32_t* ids,
+                            const int32_t* seq_start, int n_seq, void* out, long long ldo, int out_f32, float* kept,
+                            int32_t* dev_status, moe_stream_t stream) {
+  if (!x || !a || !b || !scale || !ids || !out || (out_f32 != 0 && out_f32 != 1)) return MOE_ERR_ARG;
+  if (!ad_shape(T, K, N, R, L, seq_start, n_seq)) return MOE_ERR_ARG;
+  if (ldx < K || ldo < N || (base && ldb < N)) return MOE_ERR_ARG;
+  const int size = out_f32 ? 4 : 2;
+  if (K % 8 || N % 8 || !ad_rows_ok(x, ldx, K, 2) || !ad_rows_ok(out, ldo, N, size) ||
+      (base && !ad_rows_ok(base, ldb, N, size)) || (uintptr_t)a % 16 || (uintptr_t)b % 16)
+    return MOE_ERR_ALIGN;
+  const AdArgs g{(const uint16_t*)x, (const uint16_t*)a, (const uint16_t*)b, scale, ids, seq_start, base, out, kept,
+                 dev_status, ldx, base ? ldb : 0, ldo, T, K, N, R, L, n_seq};
+  return ad_launch_rows(g, out_f32 != 0, (cudaStream_t)stream);
+}
+
+extern "C" size_t moe_adapters_grad_workspace_bytes(int T, int R) {
+  if (T < 1 || R < 1 || R > kAdMaxR) return 0;
+  return ad256((size_t)T * R * 4);
+}
+
+extern "C" int moe_adapters_grad(const void* dy, long long ldy, const void* x, long long ldx, const float* kept,
+                                 const void* base, long long ldb, int T, int K, int N, int R, int L, const void* a,
+                                 const void* b, const float* scale, const int32_t* ids, const int32_t* seq_start,
+                                 int n_seq, void* dx, long long lddx, float* da, float* db, void* workspace,
+                                 size_t workspace_bytes, int32_t* dev_status, moe_stream_t stream) {
+  if (!dy || !a || !b || !scale || !ids || !workspace || (!dx && !da) || (!da != !db) || (da && (!x || !kept)))
+    return MOE_ERR_ARG;
+  if (!ad_shape(T, K, N, R, L, seq_start, n_seq)) return MOE_ERR_ARG;
+  if (ldy < N || (da && ldx < K) || (dx && lddx < K) || (dx && base && ldb < K)) return MOE_ERR_ARG;
+  if (K % 8 || N % 8 || !ad_rows_ok(dy, ldy, N, 2) || (da && !ad_rows_ok(x, ldx, K, 2)) ||
+      (dx && !ad_rows_ok(dx, lddx, K, 2)) || (dx && base && !ad_rows_ok(base, ldb, K, 2)) || (uintptr_t)a % 16 ||
+      (uintptr_t)b % 16 || (uintptr_t)da % 16 || (uintptr_t)db % 16 || (uintptr_t)workspace % 256 ||
+      workspace_bytes < moe_adapters_grad_workspace_bytes(T, R))
+    return MOE_ERR_ALIGN;
+  cudaStream_t s = (cudaStream_t)stream;
+  float* dv = (float*)workspace;
+  const AdArgs g{(const uint16_t*)dy, (const uint16_t*)b, (const uint16_t*)a, scale, ids, seq_start, dx ? base : nullptr,
+                 dx, dv, dev_status, ldy, dx && base ? ldb : 0, lddx, T, N, K, R, L, n_seq};
+  if (int rc = ad_launch_rows(g, false, s)) return rc;
+  if (!da) return MOE_OK;
+  const AdGradArgs o{(const uint16_t*)x, (const uint16_t*)dy, dv, kept, ids, seq_start, da, db, dev_status, ldx, ldy, T,
+                     K, N, R, L, n_seq};
+  const int blocks = (K + kOutThreads - 1) / kOutThreads + (N + kOutThreads - 1) / kOutThreads;
+  MOE_CUDA_TRY(launch_pdl(adapters_outer_kernel, dim3(blocks, L, (R + kOutRanks - 1) / kOutRanks), dim3(kOutThreads), 0, s, o));
+  return MOE_OK;
+}

@@ -1,0 +1,60 @@
+// Low-rank adapters beside a shared projection: arguments and launchers shared by adapters.cu and its kernels.
+#pragma once
+
+#include "internal.cuh"
+
+namespace moe {
+
+constexpr int kAdMaxR = 128;
+
+// out = base + (scale_l x W1_l^T) W2_l over the rows of each sequence; the gradient's dx is the same with dy for x, W1
+// and W2 exchanged.
+struct AdArgs {
+  const uint16_t* x;   // [T] rows of K, ldx apart
+  const uint16_t* w1;  // [L][R][K]
+  const uint16_t* w2;  // [L][R][N]
+  const float* scale;  // [L]
+  const int32_t* ids;  // [n_seq], -1: no adapter
+  const int32_t* seq;  // [n_seq + 1] or NULL: row t is sequence t
+  const void* base;    // [T] rows of N, ldb apart, or NULL
+  void* out;           // [T] rows of N, ldo apart, or NULL: the product x W1^T alone
+  float* kept;         // [T][R] scale_l x W1_l^T, or NULL
+  int32_t* status;
+  long long ldx, ldb, ldo;
+  int T, K, N, R, L, n_seq;
+};
+
+// The adapter of sequence s, or -1 (flagged, where it is neither one nor -1).
+__device__ __forceinline__ int ad_adapter(const AdArgs& a, int s) {
+  const int l = a.ids[s];
+  if (l < -1 || l >= a.L) set_status(a.status, MOE_DEV_BAD_EXPERT);
+  return l < a.L ? l : -1;
+}
+
+// The sequence of row t: the last s with seq[s] <= t < seq[s + 1]; -1 for a row in none.
+__device__ __forceinline__ int ad_sequence(const AdArgs& a, int t) {
+  if (!a.seq) return t;
+  int lo = 0, hi = a.n_seq + 1;  // the first s with seq[s] > t lies in [lo, hi]
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (a.seq[mid] > t) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo >= 1 && lo <= a.n_seq ? lo - 1 : -1;
+}
+
+struct AdGradArgs {
+  const uint16_t* x;   // [T] rows of K
+  const uint16_t* dy;  // [T] rows of N
+  const float* dv;     // [T][R]
+  const float* v;      // [T][R]
+  const int32_t* ids;
+  const int32_t* seq;
+  float* da;           // [L][R][K]
+  float* db;           // [L][R][N]
+  int32_t* status;
+  long long ldx, ldy;
+  int T, K, N, R, L, n_seq;
+};
+
+}  // namespace moe

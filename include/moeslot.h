@@ -593,6 +593,66 @@ int moe_route_groups_grad(const void* logits, int bf16, const int32_t* ids, cons
                           int rflags, float scale, void* grad_logits, int32_t* dev_status, moe_stream_t stream);
 
 /*
+ * Low-rank adapters of many requests beside a shared projection (moe_w4_linear,
+ * a bf16 product): base is the projection's result.  The pages have one model
+ * for all requests; an adapter is a request's own small correction to it.
+ * Sequence q is the rows [seq_start[q], seq_start[q + 1]) and has adapter
+ * l = ids[q]:
+ *   v[t] = scale[l] * x[t] A_l^T           (R values, kept in fp32)
+ *   out[t] = base[t] + v[t] B_l            (base NULL: 0), rounded once
+ *   x       device bf16 [T] rows of K, ldx elements apart (ldx >= K)
+ *   base    device [T] rows of N, ldb apart, of the type of out, or NULL; it may
+ *           be out itself (then ldb = ldo)
+ *   a, b    device bf16 [L][R][K] and [L][R][N]: rank r of A reads, rank r of B
+ *           writes one run of features.  Smaller ranks: zero rows.
+ *   scale   device fp32 [L]
+ *   ids     device int32 [n_seq], -1: no adapter (out = base)
+ *   seq_start  device int32 [n_seq + 1], ascending, empty sequences allowed, or
+ *           NULL with n_seq = T: every row is a sequence of its own (decoding).
+ *           Rows before the first and behind the last sequence have no adapter.
+ *   out     device [T] rows of N, ldo apart: bf16, or fp32 with out_f32 = 1
+ *   kept    device fp32 [T][R] output, v (0 without an adapter), for the gradient,
+ *           or NULL
+ * Sums are fp32; the result does not depend on thread timing.  x of a row
+ * reaches no other row.
+ * An id outside [-1, L) sets MOE_DEV_BAD_EXPERT and counts as -1; a descending
+ * seq_start sets MOE_DEV_BAD_GROUPS.
+ * Errors: MOE_ERR_ARG on NULL pointers, T not in [1, 2^24], K or N not in
+ * [8, 2^17], R not in [1, 128], L not in [1, 65535], n_seq < 1 or leading
+ * dimensions too small; MOE_ERR_ALIGN if K or N is no multiple of 8, or a matrix
+ * or a row of one does not start on 16 bytes.
+ */
+int moe_adapters(const void* x, long long ldx, const void* base, long long ldb, int T, int K, int N, int R, int L,
+                 const void* a, const void* b, const float* scale, const int32_t* ids, const int32_t* seq_start,
+                 int n_seq, void* out, long long ldo, int out_f32, float* kept, int32_t* dev_status,
+                 moe_stream_t stream);
+
+/*
+ * The gradients of moe_adapters, of dy = the gradient in out (in base it is dy
+ * itself):
+ *   dv[t] = scale[l] * dy[t] B_l^T,   dx[t] = base[t] + dv[t] A_l,
+ *   da_l = sum_t dv[t] x[t]^T,        db_l = sum_t kept[t] dy[t]^T
+ * over the rows of the sequences with adapter l.
+ *   dy      device bf16 [T] rows of N, ldy apart
+ *   x, kept as in and from moe_adapters (not needed without da and db)
+ *   base    device bf16 [T] rows of K, ldb apart, or NULL: the gradient in x of
+ *           the projection itself; it may be dx
+ *   dx      device bf16 [T] rows of K, lddx apart, or NULL
+ *   da, db  device fp32 [L][R][K] and [L][R][N], written whole (0 for adapters
+ *           without rows), or both NULL
+ *   workspace  device, moe_adapters_grad_workspace_bytes(T, R), 256-byte aligned
+ * Sums are fp32, in an order that does not depend on thread timing.
+ * Errors: as moe_adapters; MOE_ERR_ARG without dx, da and db; MOE_ERR_ALIGN for
+ * an unaligned or small workspace.
+ */
+size_t moe_adapters_grad_workspace_bytes(int T, int R);
+int moe_adapters_grad(const void* dy, long long ldy, const void* x, long long ldx, const float* kept, const void* base,
+                      long long ldb, int T, int K, int N, int R, int L, const void* a, const void* b,
+                      const float* scale, const int32_t* ids, const int32_t* seq_start, int n_seq, void* dx,
+                      long long lddx, float* da, float* db, void* workspace, size_t workspace_bytes,
+                      int32_t* dev_status, moe_stream_t stream);
+
+/*
  * How GATHER mode serves a step that needs more experts than the pool holds
  * ("Porting vllm-expert-cache to NVIDIA GPUs", "Measuring, without fooling
  * yourself": a step is served from slots only when tokens x top_k <= slots;
