@@ -79,63 +79,76 @@ __device__ __forceinline__ void ad_add8(const void* base, void* out, long long i
   }
 }
 
-// One cluster of CTAs per row: CTA c takes its share of the K inputs for all R products, the partial sums meet in every
-// CTA's shared memory, and CTA c computes its share of the N outputs.  One launch, no workspace.
+// One cluster of CTAs per row, or per sequence of up to max_rows rows: CTA c takes its share of the K inputs for all R
+// products, the partial sums meet in every CTA's shared memory, and CTA c computes its share of the N outputs.  One
+// launch, no workspace.
 template <bool F32>
-__global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(const AdArgs a) {
+__global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(const AdArgs a, int max_rows) {
   extern __shared__ __align__(16) unsigned char ad_smem[];
-  __shared__ float s_part[kRowCluster][kAdMaxR];
+  __shared__ float s_part[2][kRowCluster][kAdMaxR];
   __shared__ float s_v[kAdMaxR];
   pdl_wait();
-  const int c = (int)ad_rank(), t = blockIdx.x / kRowCluster;
+  const int c = (int)ad_rank(), unit = blockIdx.x / kRowCluster;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int s = ad_sequence(a, t);
+  int s = unit, t0 = unit, t1 = unit + 1;
+  if (max_rows) {
+    t0 = min(max(a.seq[s], 0), a.T);
+    t1 = min(max(a.seq[s + 1], 0), a.T);
+    if (t1 - t0 > max_rows || t1 <= t0) return;
+  } else {
+    s = ad_sequence(a, unit);
+    if (unit == 0 && a.seq)
+      for (int q = c * kRowThreads + tid; q < a.n_seq; q += kRowCluster * kRowThreads)
+        if (a.seq[q + 1] < a.seq[q]) set_status(a.status, MOE_DEV_BAD_GROUPS);
+  }
   const int l = s < 0 ? -1 : ad_adapter(a, s);
   const int nv = a.N / 8, n0 = nv * c / kRowCluster, n1 = nv * (c + 1) / kRowCluster;
-  if (t == 0 && a.seq)
-    for (int q = c * kRowThreads + tid; q < a.n_seq; q += kRowCluster * kRowThreads)
-      if (a.seq[q + 1] < a.seq[q]) set_status(a.status, MOE_DEV_BAD_GROUPS);
   if (l < 0) {
-    if (a.kept && c == 0)
-      for (int r = tid; r < a.R; r += kRowThreads) a.kept[(size_t)t * a.R + r] = 0.f;
     const float none[8] = {};
-    if (a.out && (a.out != a.base || a.ldo != a.ldb))
-      for (int j = n0 + tid; j < n1; j += kRowThreads)
-        ad_add8<F32>(a.base, a.out, t * a.ldb + 8 * j, t * a.ldo + 8 * j, none);
+    for (int t = t0; t < t1; ++t) {
+      if (a.kept && c == 0)
+        for (int r = tid; r < a.R; r += kRowThreads) a.kept[(size_t)t * a.R + r] = 0.f;
+      if (a.out && (a.out != a.base || a.ldo != a.ldb))
+        for (int j = n0 + tid; j < n1; j += kRowThreads)
+          ad_add8<F32>(a.base, a.out, t * a.ldb + 8 * j, t * a.ldo + 8 * j, none);
+    }
     return;
   }
   ad_cluster_arrive();
   const int kv = a.K / 8, k0 = kv * c / kRowCluster, k1 = kv * (c + 1) / kRowCluster;
   uint4* xs = reinterpret_cast<uint4*>(ad_smem);
-  const uint4* xr = reinterpret_cast<const uint4*>(a.x + t * a.ldx) + k0;
-  for (int i = tid; i < k1 - k0; i += kRowThreads) xs[i] = xr[i];
-  __syncthreads();
-  ad_cluster_wait();  // the other CTAs have started
   const uint4* w1 = reinterpret_cast<const uint4*>(a.w1 + (size_t)l * a.R * a.K) + k0;
-  for (int r = warp; r < a.R; r += kRowThreads / 32) {
-    float sum = 0.f;
-    for (int i = lane; i < k1 - k0; i += 32) sum = ad_dot8(xs[i], w1[(size_t)r * kv + i], sum);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(MOE_FULL_MASK, sum, o);
-    if (lane < kRowCluster) ad_store_remote(&s_part[c][r], lane, sum);
-  }
-  ad_cluster_arrive();
-  ad_cluster_wait();
-  for (int r = tid; r < a.R; r += kRowThreads) {
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kRowCluster; ++i) sum += s_part[i][r];
-    sum *= a.scale[l];
-    s_v[r] = sum;
-    if (a.kept && c == 0) a.kept[(size_t)t * a.R + r] = sum;
-  }
-  __syncthreads();
-  if (!a.out) return;
   const uint4* w2 = reinterpret_cast<const uint4*>(a.w2 + (size_t)l * a.R * a.N);
-  for (int j = n0 + tid; j < n1; j += kRowThreads) {
-    float acc[8] = {};
-    for (int r = 0; r < a.R; ++r) ad_axpy8(s_v[r], w2[(size_t)r * nv + j], acc);
-    ad_add8<F32>(a.base, a.out, t * a.ldb + 8 * j, t * a.ldo + 8 * j, acc);
+  ad_cluster_wait();  // the other CTAs have started
+  for (int t = t0; t < t1; ++t) {
+    float(*part)[kAdMaxR] = s_part[t & 1];
+    const uint4* xr = reinterpret_cast<const uint4*>(a.x + t * a.ldx) + k0;
+    for (int i = tid; i < k1 - k0; i += kRowThreads) xs[i] = xr[i];
+    __syncthreads();
+    for (int r = warp; r < a.R; r += kRowThreads / 32) {
+      float sum = 0.f;
+      for (int i = lane; i < k1 - k0; i += 32) sum = ad_dot8(xs[i], w1[(size_t)r * kv + i], sum);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(MOE_FULL_MASK, sum, o);
+      if (lane < kRowCluster) ad_store_remote(&part[c][r], lane, sum);
+    }
+    ad_cluster_arrive();
+    ad_cluster_wait();
+    for (int r = tid; r < a.R; r += kRowThreads) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kRowCluster; ++i) sum += part[i][r];
+      sum *= a.scale[l];
+      s_v[r] = sum;
+      if (a.kept && c == 0) a.kept[(size_t)t * a.R + r] = sum;
+    }
+    __syncthreads();
+    if (!a.out) continue;
+    for (int j = n0 + tid; j < n1; j += kRowThreads) {
+      float acc[8] = {};
+      for (int r = 0; r < a.R; ++r) ad_axpy8(s_v[r], w2[(size_t)r * nv + j], acc);
+      ad_add8<F32>(a.base, a.out, t * a.ldb + 8 * j, t * a.ldo + 8 * j, acc);
+    }
   }
 }
 
@@ -169,7 +182,7 @@ __global__ void __launch_bounds__(kOutThreads) adapters_outer_kernel(const AdGra
     if (r0 + i < a.R) o[(size_t)i * F] = acc[i];
 }
 
-static int ad_launch_rows(const AdArgs& a, bool f32, cudaStream_t s) {
+static int ad_launch_rows(const AdArgs& a, bool f32, int units, int max_rows, cudaStream_t s) {
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = kRowCluster;
@@ -178,15 +191,24 @@ static int ad_launch_rows(const AdArgs& a, bool f32, cudaStream_t s) {
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.T * kRowCluster);
+  cfg.gridDim = dim3((unsigned)units * kRowCluster);
   cfg.blockDim = dim3(kRowThreads);
   cfg.dynamicSmemBytes = (size_t)(a.K / 8 / kRowCluster + 1) * 16;
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  if (f32) MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, adapters_row_kernel<true>, a));
-  else MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, adapters_row_kernel<false>, a));
+  if (f32) MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, adapters_row_kernel<true>, a, max_rows));
+  else MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, adapters_row_kernel<false>, a, max_rows));
   return MOE_OK;
+}
+
+constexpr int kShortRows = 4;  // sequences of up to so many rows take the row kernel in a batch of short and long ones
+
+static int ad_run(const AdArgs& a, bool f32, cudaStream_t s) {
+  if (!a.seq || a.T <= kShortRows) return ad_launch_rows(a, f32, a.T, 0, s);
+  if (a.n_seq == 1 || a.T >= 64ll * a.n_seq) return ad_launch_tiles(a, f32, 0, s);
+  if (int rc = ad_launch_rows(a, f32, a.n_seq, kShortRows, s)) return rc;
+  return ad_launch_tiles(a, f32, kShortRows, s);
 }
 
 static bool ad_shape(int T, int K, int N, int R, int L, const int32_t* seq, int n_seq) {
@@ -216,7 +238,7 @@ extern "C" int moe_adapters(const void* x, long long ldx, const void* base, long
     return MOE_ERR_ALIGN;
   const AdArgs g{(const uint16_t*)x, (const uint16_t*)a, (const uint16_t*)b, scale, ids, seq_start, base, out, kept,
                  dev_status, ldx, base ? ldb : 0, ldo, T, K, N, R, L, n_seq};
-  return ad_launch_rows(g, out_f32 != 0, (cudaStream_t)stream);
+  return ad_run(g, out_f32 != 0, (cudaStream_t)stream);
 }
 
 extern "C" size_t moe_adapters_grad_workspace_bytes(int T, int R) {
@@ -242,7 +264,7 @@ extern "C" int moe_adapters_grad(const void* dy, long long ldy, const void* x, l
   float* dv = (float*)workspace;
   const AdArgs g{(const uint16_t*)dy, (const uint16_t*)b, (const uint16_t*)a, scale, ids, seq_start, dx ? base : nullptr,
                  dx, dv, dev_status, ldy, dx && base ? ldb : 0, lddx, T, N, K, R, L, n_seq};
-  if (int rc = ad_launch_rows(g, false, s)) return rc;
+  if (int rc = ad_run(g, false, s)) return rc;
   if (!da) return MOE_OK;
   const AdGradArgs o{(const uint16_t*)x, (const uint16_t*)dy, dv, kept, ids, seq_start, da, db, dev_status, ldx, ldy, T,
                      K, N, R, L, n_seq};

@@ -43,6 +43,9 @@ __device__ __forceinline__ int ad_sequence(const AdArgs& a, int t) {
   return lo >= 1 && lo <= a.n_seq ? lo - 1 : -1;
 }
 
+// The sequences of more than short_rows rows (and the rows of none), by tiles.
+int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, cudaStream_t s);
+
 struct AdGradArgs {
   const uint16_t* x;   // [T] rows of K
   const uint16_t* dy;  // [T] rows of N
