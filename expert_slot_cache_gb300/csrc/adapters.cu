@@ -152,36 +152,6 @@ __global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(const AdArgs 
   }
 }
 
-// dA and dB: a thread has one feature and 16 ranks, and goes over the rows of one adapter.
-constexpr int kOutThreads = 128;
-constexpr int kOutRanks = 16;
-__global__ void __launch_bounds__(kOutThreads) adapters_outer_kernel(const AdGradArgs a) {
-  pdl_wait();
-  const int ka = (a.K + kOutThreads - 1) / kOutThreads;
-  const bool first = (int)blockIdx.x < ka;
-  const int F = first ? a.K : a.N, f = ((int)blockIdx.x - (first ? 0 : ka)) * kOutThreads + threadIdx.x;
-  const int l = blockIdx.y, r0 = blockIdx.z * kOutRanks;
-  const uint16_t* x = first ? a.x : a.dy;
-  const long long ld = first ? a.ldx : a.ldy;
-  const float* v = first ? a.dv : a.v;
-  float acc[kOutRanks] = {};
-  for (int s = 0; s < a.n_seq; ++s) {
-    if (a.ids[s] != l) continue;
-    const int t0 = a.seq ? max(a.seq[s], 0) : s, t1 = a.seq ? min(a.seq[s + 1], a.T) : s + 1;
-    for (int t = t0; t < t1; ++t) {
-      const float xv = f < F ? bf16_to_f32(x[t * ld + f]) : 0.f;
-#pragma unroll
-      for (int i = 0; i < kOutRanks; ++i)
-        if (r0 + i < a.R) acc[i] = fmaf(v[(size_t)t * a.R + r0 + i], xv, acc[i]);
-    }
-  }
-  if (f >= F) return;
-  float* o = (first ? a.da : a.db) + ((size_t)l * a.R + r0) * F + f;
-#pragma unroll
-  for (int i = 0; i < kOutRanks; ++i)
-    if (r0 + i < a.R) o[(size_t)i * F] = acc[i];
-}
-
 static int ad_launch_rows(const AdArgs& a, bool f32, int units, int max_rows, cudaStream_t s) {
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -268,7 +238,8 @@ extern "C" int moe_adapters_grad(const void* dy, long long ldy, const void* x, l
   if (!da) return MOE_OK;
   const AdGradArgs o{(const uint16_t*)x, (const uint16_t*)dy, dv, kept, ids, seq_start, da, db, dev_status, ldx, ldy, T,
                      K, N, R, L, n_seq};
-  const int blocks = (K + kOutThreads - 1) / kOutThreads + (N + kOutThreads - 1) / kOutThreads;
-  MOE_CUDA_TRY(launch_pdl(adapters_outer_kernel, dim3(blocks, L, (R + kOutRanks - 1) / kOutRanks), dim3(kOutThreads), 0, s, o));
-  return MOE_OK;
+  int dev = 0, sms = 0;
+  MOE_CUDA_TRY(cudaGetDevice(&dev));
+  MOE_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  return ad_launch_outer(o, sms, s);
 }

@@ -46,6 +46,31 @@ __device__ __forceinline__ int ad_sequence(const AdArgs& a, int t) {
 // The sequences of more than short_rows rows (and the rows of none), by tiles.
 int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, cudaStream_t s);
 
+// v as a sum of NS bf16 numbers, eight values at once (packed pairs): truncation leaves an exact rest, so three of them
+// are all 24 bits; the last of two is rounded.  A rest of an infinity or a NaN counts as 0.
+template <int NS>
+__device__ __forceinline__ void ad_split8(const float (&v)[8], uint4 (&o)[NS]) {
+  uint32_t w[NS][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x = v[2 * i], y = v[2 * i + 1];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      if (s == NS - 1) {
+        const __nv_bfloat162 q = __floats2bfloat162_rn(x, y);
+        w[s][i] = *reinterpret_cast<const uint32_t*>(&q);
+      } else {
+        const uint32_t xb = __float_as_uint(x) & 0xffff0000u, yb = __float_as_uint(y) & 0xffff0000u;
+        w[s][i] = (xb >> 16) | yb;
+        x = fabsf(x) < INFINITY ? x - __uint_as_float(xb) : 0.f;
+        y = fabsf(y) < INFINITY ? y - __uint_as_float(yb) : 0.f;
+      }
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < NS; ++s) o[s] = make_uint4(w[s][0], w[s][1], w[s][2], w[s][3]);
+}
+
 struct AdGradArgs {
   const uint16_t* x;   // [T] rows of K
   const uint16_t* dy;  // [T] rows of N
@@ -59,5 +84,8 @@ struct AdGradArgs {
   long long ldx, ldy;
   int T, K, N, R, L, n_seq;
 };
+
+// dA and dB.
+int ad_launch_outer(const AdGradArgs& a, int sms, cudaStream_t s);
 
 }  // namespace moe

@@ -1,0 +1,372 @@
+// The weights' gradients of the adapters: dA_l = sum_t dv_t x_t^T and dB_l = sum_t v_t dy_t^T over the rows of the
+// sequences with adapter l, in one launch.
+//
+// Longer sequences: tcgen05.  D [128 features][R] of one adapter and one block of 128 features of x or dy, summed over
+// tiles of 64 rows: x by TMA as it lies (features run along, so it is MN-major), v MN-major too, written by four warps
+// that split its fp32 values into three bf16 numbers (24 bits, nothing is rounded); the three stand next to each other
+// as columns of one product and are added at the end.  A cluster of CTAs divides the rows of an adapter where blocks
+// are few; their sums meet in distributed shared memory in a fixed order.  x and dy are read once, which is what bounds
+// it.  Many short sequences: a thread per two features, on the CUDA cores (the tiles would be mostly empty).
+#include <algorithm>
+
+#include "adapters.cuh"
+#include "tc05.cuh"
+
+namespace moe {
+
+constexpr int kAoThreads = 192;  // TMA warp, MMA warp, four warps that split v and write the result
+constexpr int kAoFeat = 128;     // features of a block (MMA M)
+constexpr int kAoRows = 64;      // rows of a tile
+constexpr int kAoXBytes = kAoRows * kAoFeat * 2;
+constexpr int kAoAtom = kAoRows * 128;  // 64 columns of a tile
+
+struct AoGeo {
+  int S, Rk, atoms, stages, tmem;  // CTAs of a cluster, R in sixteens, 64-column atoms of v, ring slots, TMEM columns
+  int off_bar, blocks_a;           // blocks of features of x
+};
+
+// The tiles [lo, hi) of the rows of one adapter, by a whole warp: sequence after sequence, 64 rows at a time.
+struct AoTiles {
+  const AdGradArgs& a;
+  int l, lo, hi;
+  int s = 0, at = 0, t = 0, left = 0, t0 = 0, n = 0;
+  unsigned m = 0;
+  __device__ __forceinline__ bool next(int& row0, int& rows) {
+    for (;;) {
+      if (at >= hi) return false;
+      if (left > 0) {
+        row0 = t;
+        rows = min(kAoRows, left);
+        t += kAoRows;
+        left -= kAoRows;
+        ++at;
+        return true;
+      }
+      if (m == 0) {
+        if (s >= a.n_seq) return false;
+        const int q = s + (threadIdx.x & 31);
+        s += 32;
+        t0 = n = 0;
+        if (q < a.n_seq && a.ids[q] == l) {
+          t0 = a.seq ? min(max(a.seq[q], 0), a.T) : q;
+          n = a.seq ? max(min(max(a.seq[q + 1], 0), a.T) - t0, 0) : 1;
+        }
+        m = __ballot_sync(MOE_FULL_MASK, n > 0);
+        continue;
+      }
+      const int j = __ffs(m) - 1;
+      m &= m - 1;
+      t = __shfl_sync(MOE_FULL_MASK, t0, j);
+      left = __shfl_sync(MOE_FULL_MASK, n, j);
+      const int skip = min((left + kAoRows - 1) / kAoRows, max(lo - at, 0));  // tiles of other CTAs
+      at += skip;
+      t += skip * kAoRows;
+      left -= skip * kAoRows;
+    }
+  }
+};
+
+__device__ __forceinline__ float ao_remote(const float* p, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(p), rank)));
+  return v;
+}
+
+__global__ void __launch_bounds__(kAoThreads)
+    adapters_outer_tile_kernel(const AdGradArgs a, const AoGeo g, const __grid_constant__ CUtensorMap mapX,
+                               const __grid_constant__ CUtensorMap mapY) {
+  extern __shared__ __align__(16) unsigned char ao_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(ao_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_total, s_abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank(), S = g.S;
+  const int block = blockIdx.x / S, l = blockIdx.y;
+  const bool first = block < g.blocks_a;
+  const int F = first ? a.K : a.N, f0 = (block - (first ? 0 : g.blocks_a)) * kAoFeat;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + g.off_bar);  // x has landed
+  uint64_t* ready = full + 8;                                    // v is written
+  uint64_t* empty = ready + 8;
+  uint64_t* done = empty + 8;
+  const int stage = kAoXBytes + g.atoms * kAoAtom;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < g.stages; ++i) mbar_init(&full[i], 1), mbar_init(&ready[i], 4), mbar_init(&empty[i], 1);
+    mbar_init(done, 1);
+    s_abort = 0;
+    s_total = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&s_tmem, g.tmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();
+  int mine = 0;
+  for (int q = threadIdx.x; q < a.n_seq; q += kAoThreads)
+    if (a.ids[q] == l) {
+      const int n = a.seq ? min(max(a.seq[q + 1], 0), a.T) - min(max(a.seq[q], 0), a.T) : 1;
+      if (n > 0) mine += (n + kAoRows - 1) / kAoRows;
+    }
+  __syncwarp();
+  mine = __reduce_add_sync(MOE_FULL_MASK, mine);
+  if (lane == 0 && mine) atomicAdd(&s_total, mine);
+  __syncthreads();
+  const uint32_t tmem = s_tmem;
+  const int total = s_total;
+  AoTiles tiles{a, l, (int)((long long)total * rank / S), (int)((long long)total * (rank + 1) / S)};
+  const int nt = tiles.hi - tiles.lo;
+  volatile int* abort_flag = &s_abort;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {  // bounded; nothing is waited for after a timeout
+    if (!*abort_flag && !mbar_wait(bar, parity)) {
+      *abort_flag = 1;
+      set_status(a.status, MOE_DEV_TIMEOUT);
+    }
+  };
+  int row0 = 0, rows = 0;
+  if (warp == 0) {
+    int issued = 0;
+    for (int i = 0; tiles.next(row0, rows); ++i) {
+      if (lane == 0) {
+        const int s = i % g.stages, use = i / g.stages;
+        if (use > 0) wait(&empty[s], (use - 1) & 1);
+        if (!*abort_flag) {
+          unsigned char* st = sm + s * stage;
+          mbar_expect_tx(&full[s], kAoXBytes);
+          tma_load_3d(st, first ? &mapX : &mapY, &full[s], f0, row0, 0);
+          tma_load_3d(st + kAoAtom, first ? &mapX : &mapY, &full[s], f0 + 64, row0, 0);
+          issued = i + 1;
+        }
+      }
+      __syncwarp();
+    }
+    // after a timeout every copy lands before the CTA may go
+    if (lane == 0 && *abort_flag)
+      for (int s = 0; s < g.stages && s < issued; ++s) mbar_wait(&full[s], ((issued - 1 - s) / g.stages) & 1);
+    __syncwarp();
+  } else if (warp == 1) {
+    const int cols = 3 * g.Rk, n1 = cols <= 256 ? cols : 192;
+    const uint32_t id1 = idesc_bf16(kAoFeat, n1, 1, 1), id2 = idesc_bf16(kAoFeat, max(cols - n1, 16), 1, 1);
+    const uint32_t base = smem_u32(sm);
+    for (int i = 0; tiles.next(row0, rows); ++i) {
+      if (lane == 0) {
+        const int s = i % g.stages, use = i / g.stages;
+        wait(&full[s], use & 1);
+        wait(&ready[s], use & 1);
+        tc_fence_after();
+        if (!*abort_flag) {
+          const uint64_t ad = smem_desc_l(base + s * stage, kAoAtom, 1024, kLayoutSw128);
+          const uint64_t bd = smem_desc_l(base + s * stage + kAoXBytes, kAoAtom, 1024, kLayoutSw128);
+          for (int k = 0; k * 16 < rows; ++k) {  // 16 rows at a time
+            umma_f16(tmem, ad + k * (2048 >> 4), bd + k * (2048 >> 4), id1, i + k != 0);
+            if (cols > n1) umma_f16(tmem + n1, ad + k * (2048 >> 4), bd + (3 * kAoAtom >> 4) + k * (2048 >> 4), id2, i + k != 0);
+          }
+        }
+        umma_commit(&empty[s]);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) umma_commit(done);
+    __syncwarp();
+  } else {
+    // split v: unit = (row, 8 ranks); 3 x 16 bytes of the tile's columns [first | second | third part]
+    const float* src = first ? a.dv : a.v;
+    const int g8 = g.Rk / 8, tid = threadIdx.x - 64;
+    const bool vec = a.R % 4 == 0;
+    for (int i = 0; tiles.next(row0, rows); ++i) {
+      const int s = i % g.stages, use = i / g.stages;
+      unsigned char* vs = sm + s * stage + kAoXBytes;
+      const int rows16 = (rows + 15) & ~15;
+      if (use > 0) wait(&empty[s], (use - 1) & 1);
+      for (int u = tid; u < rows16 * g8; u += 128) {
+        const int r = u / g8, c = (u % g8) * 8;
+        float v[8] = {};
+        if (r < rows) {
+          const float* p = src + (size_t)(row0 + r) * a.R + c;
+          if (vec && c + 8 <= a.R) {
+            const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
+            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (c + j < a.R) v[j] = p[j];
+          }
+        }
+        uint4 o[3];
+        ad_split8<3>(v, o);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const int n = k * g.Rk + c;
+          *reinterpret_cast<uint4*>(vs + (n / 64) * kAoAtom + r * 128 + (((n % 64) / 8) ^ (r & 7)) * 16) = o[k];
+        }
+      }
+      if (rows16 != rows) {
+        // the rest of the last 16 rows belongs to others, whatever it is
+        wait(&full[s], use & 1);
+        for (int u = tid; u < (rows16 - rows) * 16; u += 128) {
+          const int r = rows + u / 16, p = u % 16;
+          *reinterpret_cast<uint4*>(sm + s * stage + (p / 8) * kAoAtom + r * 128 + (p % 8) * 16) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      asm volatile("fence.proxy.async;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ready[s]);
+    }
+    // the result: lane = feature; the parts of a rank are Rk columns apart
+    wait(done, 0);
+    __syncwarp();
+    tc_fence_after();
+    const int q = warp & 3, f = q * 32 + lane;
+    float* part = reinterpret_cast<float*>(sm);  // [Rk][128] (every product is done)
+    float* out = (first ? a.da : a.db) + (size_t)l * a.R * F + f0 + f;
+    for (int c = 0; c < g.Rk; c += 16) {
+      float v[16], w[16], x[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = w[j] = x[j] = 0.f;
+      if (nt > 0) {
+        const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + c;
+        tmem_ld_w<16>(at, v);
+        tmem_ld_w<16>(at + g.Rk, w);
+        tmem_ld_w<16>(at + 2 * g.Rk, x);
+        tmem_ld_wait();
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        v[j] += w[j] + x[j];
+        if (S > 1) part[(c + j) * kAoFeat + f] = v[j];
+        else if (c + j < a.R && f0 + f < F) out[(size_t)(c + j) * F] = v[j];
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+  }
+  if (S > 1) {
+    cluster_sync();
+    const int r0 = a.R * rank / S, r1 = a.R * (rank + 1) / S;
+    const float* part = reinterpret_cast<const float*>(sm);
+    float* out = (first ? a.da : a.db) + (size_t)l * a.R * F + f0;
+    for (int i = threadIdx.x; i < (r1 - r0) * kAoFeat; i += kAoThreads) {
+      const int r = r0 + i / kAoFeat, f = i % kAoFeat;
+      float v = 0.f;
+      for (int p = 0; p < S; ++p) v += ao_remote(part + r * kAoFeat + f, p);
+      if (f0 + f < F) out[(size_t)r * F + f] = v;
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while another one reads its shared memory
+  } else {
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, g.tmem);
+  }
+}
+
+// Short sequences: a thread has two features and 16 ranks; the rows of the adapter are listed in shared memory.
+constexpr int kAsThreads = 128;
+constexpr int kAsRanks = 16;
+constexpr int kAsList = 1024;
+__global__ void __launch_bounds__(kAsThreads) adapters_outer_short_kernel(const AdGradArgs a, int blocks_a) {
+  __shared__ int s_row[kAsList], s_scan[33];
+  pdl_wait();
+  const bool first = (int)blockIdx.x < blocks_a;
+  const int F = first ? a.K : a.N, f = (((int)blockIdx.x - (first ? 0 : blocks_a)) * kAsThreads + threadIdx.x) * 2;
+  const int l = blockIdx.y, r0 = blockIdx.z * kAsRanks, nr = min(kAsRanks, a.R - r0);
+  const uint16_t* x = (first ? a.x : a.dy) + (f < F ? f : 0);
+  const long long ld = first ? a.ldx : a.ldy;
+  const float* v = (first ? a.dv : a.v) + r0;
+  float acc[2 * kAsRanks] = {};
+  // sequences 128 at a time; their rows listed in order, up to kAsList of them at a time
+  for (int q0 = 0; q0 < a.n_seq; q0 += kAsThreads) {
+    const int q = q0 + (int)threadIdx.x;
+    int t = 0, n = 0;
+    if (q < a.n_seq && a.ids[q] == l) {
+      t = a.seq ? min(max(a.seq[q], 0), a.T) : q;
+      n = a.seq ? max(min(max(a.seq[q + 1], 0), a.T) - t, 0) : 1;
+    }
+    int total;
+    const int at = block_exclusive_scan(n, s_scan, &total);
+    for (int base = 0; base < total; base += kAsList) {
+      for (int i = max(base - at, 0); i < min(n, base + kAsList - at); ++i) s_row[at + i - base] = t + i;
+      __syncthreads();
+      const int m = min(kAsList, total - base);
+      for (int i = 0; i < m; i += 4) {
+        uint32_t xv[4];
+        float vv[4][kAsRanks];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int row = s_row[min(i + u, m - 1)];
+          xv[u] = i + u < m ? *reinterpret_cast<const uint32_t*>(x + row * ld) : 0u;
+#pragma unroll
+          for (int j = 0; j < kAsRanks; ++j) vv[u][j] = j < nr && i + u < m ? v[(size_t)row * a.R + j] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int j = 0; j < kAsRanks; ++j) {
+            acc[2 * j] = fmaf(vv[u][j], bf16_lo(xv[u]), acc[2 * j]);
+            acc[2 * j + 1] = fmaf(vv[u][j], bf16_hi(xv[u]), acc[2 * j + 1]);
+          }
+      }
+      __syncthreads();
+    }
+  }
+  if (f >= F) return;
+  float* o = (first ? a.da : a.db) + ((size_t)l * a.R + r0) * F + f;
+#pragma unroll
+  for (int j = 0; j < kAsRanks; ++j)
+    if (j < nr) *reinterpret_cast<float2*>(o + (size_t)j * F) = make_float2(acc[2 * j], acc[2 * j + 1]);
+}
+
+int ad_launch_outer(const AdGradArgs& a, int sms, cudaStream_t s) {
+  if (!a.seq || a.T < 16ll * a.n_seq) {
+    const int per = 2 * kAsThreads, blocks_a = (a.K + per - 1) / per, blocks = blocks_a + (a.N + per - 1) / per;
+    MOE_CUDA_TRY(launch_pdl(adapters_outer_short_kernel, dim3(blocks, a.L, (a.R + kAsRanks - 1) / kAsRanks), dim3(kAsThreads),
+                            0, s, a, blocks_a));
+    return MOE_OK;
+  }
+  AoGeo g = {};
+  g.Rk = (a.R + 15) / 16 * 16;
+  g.atoms = (3 * g.Rk + 63) / 64;
+  g.tmem = 32;
+  while (g.tmem < 3 * g.Rk) g.tmem *= 2;
+  const int stage = kAoXBytes + g.atoms * kAoAtom;
+  g.stages = 3;
+  g.off_bar = std::max(g.stages * stage, g.Rk * kAoFeat * 4);
+  g.blocks_a = (a.K + kAoFeat - 1) / kAoFeat;
+  const int blocks = g.blocks_a + (a.N + kAoFeat - 1) / kAoFeat;
+  const int bytes = g.off_bar + 256 + 1024;
+  // CTAs for about two a SM; the adapters in use are at most the sequences
+  const long long busy = (long long)blocks * std::min(a.L, a.n_seq);
+  g.S = 1;
+  while (g.S < 8 && busy * g.S * 2 <= 2ll * sms && a.T >= 128 * g.S) g.S *= 2;
+  CUtensorMap mx, my;
+  for (int w = 0; w < 2; ++w) {
+    const uint64_t ld = (uint64_t)(w ? a.ldy : a.ldx) * 2;
+    const uint64_t dims[3] = {(uint64_t)(w ? a.N : a.K), (uint64_t)a.T, 1}, st[2] = {ld, ld};
+    const uint32_t box[3] = {64, kAoRows, 1};
+    if (int rc = encode_tmap_3d_bf16(w ? &my : &mx, w ? a.dy : a.x, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B)) return rc;
+  }
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = g.S;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(blocks * g.S), (unsigned)a.L);
+  cfg.blockDim = dim3(kAoThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  static bool done[64] = {};
+  MOE_CUDA_TRY(ensure_smem(adapters_outer_tile_kernel, 227 * 1024 - 512, done));
+  MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, adapters_outer_tile_kernel, a, g, mx, my));
+  return MOE_OK;
+}
+
+}  // namespace moe

@@ -82,31 +82,6 @@ __device__ void at_find(const AdArgs& a, const AtGeo& g, int ti, int* tmp, int* 
   __syncthreads();
 }
 
-// v as a sum of NS bf16 numbers, eight values at once (packed pairs): truncation leaves an exact rest, so three of them
-// are all 24 bits; the last of two is rounded.  A rest of an infinity or a NaN counts as 0.
-template <int NS>
-__device__ __forceinline__ void at_split8(const float (&v)[8], uint4 (&o)[NS]) {
-  uint32_t w[NS][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float x = v[2 * i], y = v[2 * i + 1];
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      if (s == NS - 1) {
-        const __nv_bfloat162 q = __floats2bfloat162_rn(x, y);
-        w[s][i] = *reinterpret_cast<const uint32_t*>(&q);
-      } else {
-        const uint32_t xb = __float_as_uint(x) & 0xffff0000u, yb = __float_as_uint(y) & 0xffff0000u;
-        w[s][i] = (xb >> 16) | yb;
-        x = fabsf(x) < INFINITY ? x - __uint_as_float(xb) : 0.f;
-        y = fabsf(y) < INFINITY ? y - __uint_as_float(yb) : 0.f;
-      }
-    }
-  }
-#pragma unroll
-  for (int s = 0; s < NS; ++s) o[s] = make_uint4(w[s][0], w[s][1], w[s][2], w[s][3]);
-}
-
 template <bool F32>
 __global__ void __launch_bounds__(kAtThreads, 1)
     adapters_tile_kernel(const AdArgs a, const AtGeo g, const __grid_constant__ CUtensorMap mapX,
@@ -223,6 +198,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   if (warp >= 2) {
     if (nk > 0) {
       wait(d1full, 0);
+      __syncwarp();
       tc_fence_after();
     }
     const uint32_t dst = mapa_shared(smem_u32(part), (uint32_t)min(row / per, C - 1)) +
@@ -260,7 +236,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (a.kept && c + j < a.R) a.kept[(size_t)(row0 + t) * a.R + c + j] = v[j];
       }
       uint4 o[NS];
-      at_split8<NS>(v, o);
+      ad_split8<NS>(v, o);
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
         const int k = s * g.Rk + c;
@@ -333,6 +309,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       fetch(ch + 1);
       if (ch % kPer == 0) {
         wait(&tfull[b], (i / 2) & 1);
+        __syncwarp();
         tc_fence_after();
       }
       float v[kChunk];
