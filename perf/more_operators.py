@@ -255,7 +255,9 @@ def run(state):
             return M.route_groups_grad(state["logits"], state["ids"], state["grad_w"], sigmoid=state["sigmoid"],
                                        renormalise=state["renorm"], scale=state["scale"])
         if op == "adapters":
-            return state["adapters"].forward(state["x"], state["ids"], base=state["base"], seq_start=state["starts"])
+            # fp32 results of sequences are added in place, as the plain form adds them
+            place = state["base"] if state["starts"] is not None and state["base"].dtype == torch.float32 else None
+            return state["adapters"].forward(state["x"], state["ids"], base=state["base"], seq_start=state["starts"], out=place)
         return state["adapters"].grad(state["dy"], state["x"], state["kept"], state["ids"], base=state["base"],
                                       seq_start=state["starts"])._asdict()
     if op == "route":
