@@ -4,9 +4,10 @@
 // Longer sequences: tcgen05.  D [128 features][R] of one adapter and one block of 128 features of x or dy, summed over
 // tiles of 64 rows: x by TMA as it lies (features run along, so it is MN-major), v MN-major too, written by four warps
 // that split its fp32 values into three bf16 numbers (24 bits, nothing is rounded); the three stand next to each other
-// as columns of one product and are added at the end.  A cluster of CTAs divides the rows of an adapter where blocks
-// are few; their sums meet in distributed shared memory in a fixed order.  x and dy are read once, which is what bounds
-// it.  Many short sequences: a thread per two features, on the CUDA cores (the tiles would be mostly empty).
+// as columns of one product and are added in the end.  The tensor cores truncate what they add, so that an error grows
+// with every step in one direction: after four tiles the sums are taken over into shared memory by additions that round.
+// A cluster of CTAs divides the rows of an adapter where blocks are few; their sums meet in distributed shared memory in
+// a fixed order.  x and dy are read once, which is what bounds it.  Many short sequences: a thread per two features, on the CUDA cores (the tiles would be mostly empty).
 #include <algorithm>
 
 #include "adapters.cuh"
@@ -19,10 +20,13 @@ constexpr int kAoFeat = 128;     // features of a block (MMA M)
 constexpr int kAoRows = 64;      // rows of a tile
 constexpr int kAoXBytes = kAoRows * kAoFeat * 2;
 constexpr int kAoAtom = kAoRows * 128;  // 64 columns of a tile
+constexpr int kAoDrain = 4;             // tiles between two drains of an accumulator
 
 struct AoGeo {
-  int S, Rk, atoms, stages, tmem;  // CTAs of a cluster, R in sixteens, 64-column atoms of v, ring slots, TMEM columns
-  int off_bar, blocks_a;           // blocks of features of x
+  int S, Rk, atoms, stages;       // CTAs of a cluster, R in sixteens, 64-column atoms of v, ring slots
+  int acc, tmem;                  // accumulators, TMEM columns
+  int off_part, off_bar;          // sums, barriers
+  int blocks_a;                   // blocks of features of x
 };
 
 // The tiles [lo, hi) of the rows of one adapter, by a whole warp: sequence after sequence, 64 rows at a time.
@@ -87,11 +91,13 @@ __global__ void __launch_bounds__(kAoThreads)
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + g.off_bar);  // x has landed
   uint64_t* ready = full + 8;                                    // v is written
   uint64_t* empty = ready + 8;
-  uint64_t* done = empty + 8;
+  uint64_t* tfull = empty + 8;   // an accumulator's tiles are done
+  uint64_t* tempty = tfull + 2;  // and taken over
+  float* part = reinterpret_cast<float*>(sm + g.off_part);  // [Rk][128]
   const int stage = kAoXBytes + g.atoms * kAoAtom;
   if (threadIdx.x == 0) {
     for (int i = 0; i < g.stages; ++i) mbar_init(&full[i], 1), mbar_init(&ready[i], 4), mbar_init(&empty[i], 1);
-    mbar_init(done, 1);
+    for (int i = 0; i < g.acc; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 4);
     s_abort = 0;
     s_total = 0;
     mbar_fence_init();
@@ -153,28 +159,56 @@ __global__ void __launch_bounds__(kAoThreads)
     for (int i = 0; tiles.next(row0, rows); ++i) {
       if (lane == 0) {
         const int s = i % g.stages, use = i / g.stages;
+        const int j = i / kAoDrain, b = j % g.acc;
+        if (i % kAoDrain == 0 && j >= g.acc) wait(&tempty[b], (j / g.acc - 1) & 1);
         wait(&full[s], use & 1);
         wait(&ready[s], use & 1);
         tc_fence_after();
         if (!*abort_flag) {
+          const uint32_t d = tmem + b * cols;
           const uint64_t ad = smem_desc_l(base + s * stage, kAoAtom, 1024, kLayoutSw128);
           const uint64_t bd = smem_desc_l(base + s * stage + kAoXBytes, kAoAtom, 1024, kLayoutSw128);
           for (int k = 0; k * 16 < rows; ++k) {  // 16 rows at a time
-            umma_f16(tmem, ad + k * (2048 >> 4), bd + k * (2048 >> 4), id1, i + k != 0);
-            if (cols > n1) umma_f16(tmem + n1, ad + k * (2048 >> 4), bd + (3 * kAoAtom >> 4) + k * (2048 >> 4), id2, i + k != 0);
+            const uint32_t on = i % kAoDrain + k != 0;
+            umma_f16(d, ad + k * (2048 >> 4), bd + k * (2048 >> 4), id1, on);
+            if (cols > n1) umma_f16(d + n1, ad + k * (2048 >> 4), bd + (3 * kAoAtom >> 4) + k * (2048 >> 4), id2, on);
           }
         }
         umma_commit(&empty[s]);
+        if (i % kAoDrain == kAoDrain - 1 || i == nt - 1) umma_commit(&tfull[b]);
       }
       __syncwarp();
     }
-    if (lane == 0) umma_commit(done);
-    __syncwarp();
   } else {
     // split v: unit = (row, 8 ranks); 3 x 16 bytes of the tile's columns [first | second | third part]
     const float* src = first ? a.dv : a.v;
     const int g8 = g.Rk / 8, tid = threadIdx.x - 64;
     const bool vec = a.R % 4 == 0;
+    const int q = warp & 3, f = q * 32 + lane;  // of the sums: lane = feature
+    int drained = 0;
+    auto drain = [&] {  // the parts of a rank are Rk columns apart
+      const int j = drained++, b = j % g.acc;
+      wait(&tfull[b], (j / g.acc) & 1);
+      __syncwarp();
+      tc_fence_after();
+      for (int c = 0; c < g.Rk; c += 16) {
+        float v[16], w[16], x[16];
+        const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + b * 3 * g.Rk + c;
+        tmem_ld_w<16>(at, v);
+        tmem_ld_w<16>(at + g.Rk, w);
+        tmem_ld_w<16>(at + 2 * g.Rk, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          float* p = part + (c + k) * kAoFeat + f;
+          const float sum = v[k] + (w[k] + x[k]);
+          *p = j ? *p + sum : sum;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[b]);
+    };
     for (int i = 0; tiles.next(row0, rows); ++i) {
       const int s = i % g.stages, use = i / g.stages;
       unsigned char* vs = sm + s * stage + kAoXBytes;
@@ -213,39 +247,18 @@ __global__ void __launch_bounds__(kAoThreads)
       asm volatile("fence.proxy.async;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(&ready[s]);
+      // with two accumulators the one before last's sums are taken over while the products of the last one run
+      if (i % kAoDrain == kAoDrain - 1 && i / kAoDrain >= g.acc - 1) drain();
     }
-    // the result: lane = feature; the parts of a rank are Rk columns apart
-    wait(done, 0);
-    __syncwarp();
-    tc_fence_after();
-    const int q = warp & 3, f = q * 32 + lane;
-    float* part = reinterpret_cast<float*>(sm);  // [Rk][128] (every product is done)
-    float* out = (first ? a.da : a.db) + (size_t)l * a.R * F + f0 + f;
-    for (int c = 0; c < g.Rk; c += 16) {
-      float v[16], w[16], x[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = w[j] = x[j] = 0.f;
-      if (nt > 0) {
-        const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + c;
-        tmem_ld_w<16>(at, v);
-        tmem_ld_w<16>(at + g.Rk, w);
-        tmem_ld_w<16>(at + 2 * g.Rk, x);
-        tmem_ld_wait();
-      }
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        v[j] += w[j] + x[j];
-        if (S > 1) part[(c + j) * kAoFeat + f] = v[j];
-        else if (c + j < a.R && f0 + f < F) out[(size_t)(c + j) * F] = v[j];
-      }
-    }
-    tc_fence_before();
+    while (drained * kAoDrain < nt) drain();
+    if (nt == 0)
+      for (int r = 0; r < g.Rk; ++r) part[r * kAoFeat + f] = 0.f;
     __syncwarp();
   }
-  if (S > 1) {
-    cluster_sync();
+  if (S > 1) cluster_sync();
+  else __syncthreads();
+  {
     const int r0 = a.R * rank / S, r1 = a.R * (rank + 1) / S;
-    const float* part = reinterpret_cast<const float*>(sm);
     float* out = (first ? a.da : a.db) + (size_t)l * a.R * F + f0;
     for (int i = threadIdx.x; i < (r1 - r0) * kAoFeat; i += kAoThreads) {
       const int r = r0 + i / kAoFeat, f = i % kAoFeat;
@@ -254,10 +267,8 @@ __global__ void __launch_bounds__(kAoThreads)
       if (f0 + f < F) out[(size_t)r * F + f] = v;
     }
     __syncwarp();
-    cluster_sync();  // no CTA leaves while another one reads its shared memory
-  } else {
-    __syncthreads();
   }
+  if (S > 1) cluster_sync();  // no CTA leaves while another one reads its shared memory
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, g.tmem);
@@ -330,11 +341,13 @@ int ad_launch_outer(const AdGradArgs& a, int sms, cudaStream_t s) {
   AoGeo g = {};
   g.Rk = (a.R + 15) / 16 * 16;
   g.atoms = (3 * g.Rk + 63) / 64;
+  g.acc = 6 * g.Rk <= 512 ? 2 : 1;
   g.tmem = 32;
-  while (g.tmem < 3 * g.Rk) g.tmem *= 2;
+  while (g.tmem < g.acc * 3 * g.Rk) g.tmem *= 2;
   const int stage = kAoXBytes + g.atoms * kAoAtom;
-  g.stages = 3;
-  g.off_bar = std::max(g.stages * stage, g.Rk * kAoFeat * 4);
+  g.stages = g.Rk <= 64 ? 3 : 2;  // (of more, three and the sums do not fit)
+  g.off_part = g.stages * stage;
+  g.off_bar = g.off_part + g.Rk * kAoFeat * 4;
   g.blocks_a = (a.K + kAoFeat - 1) / kAoFeat;
   const int blocks = g.blocks_a + (a.N + kAoFeat - 1) / kAoFeat;
   const int bytes = g.off_bar + 256 + 1024;
