@@ -172,13 +172,22 @@ static int ad_launch_rows(const AdArgs& a, bool f32, int units, int max_rows, cu
   return MOE_OK;
 }
 
+static int ad_sms(int* sms) {
+  int dev = 0;
+  MOE_CUDA_TRY(cudaGetDevice(&dev));
+  MOE_CUDA_TRY(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
+  return MOE_OK;
+}
+
 constexpr int kShortRows = 4;  // sequences of up to so many rows take the row kernel in a batch of short and long ones
 
 static int ad_run(const AdArgs& a, bool f32, cudaStream_t s) {
   if (!a.seq || a.T <= kShortRows) return ad_launch_rows(a, f32, a.T, 0, s);
-  if (a.n_seq == 1 || a.T >= 64ll * a.n_seq) return ad_launch_tiles(a, f32, 0, s);
+  int sms = 0;
+  if (int rc = ad_sms(&sms)) return rc;
+  if (a.n_seq == 1 || a.T >= 64ll * a.n_seq) return ad_launch_tiles(a, f32, 0, sms, s);
   if (int rc = ad_launch_rows(a, f32, a.n_seq, kShortRows, s)) return rc;
-  return ad_launch_tiles(a, f32, kShortRows, s);
+  return ad_launch_tiles(a, f32, kShortRows, sms, s);
 }
 
 static bool ad_shape(int T, int K, int N, int R, int L, const int32_t* seq, int n_seq) {
@@ -238,8 +247,7 @@ extern "C" int moe_adapters_grad(const void* dy, long long ldy, const void* x, l
   if (!da) return MOE_OK;
   const AdGradArgs o{(const uint16_t*)x, (const uint16_t*)dy, dv, kept, ids, seq_start, da, db, dev_status, ldx, ldy, T,
                      K, N, R, L, n_seq};
-  int dev = 0, sms = 0;
-  MOE_CUDA_TRY(cudaGetDevice(&dev));
-  MOE_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  int sms = 0;
+  if (int rc = ad_sms(&sms)) return rc;
   return ad_launch_outer(o, sms, s);
 }

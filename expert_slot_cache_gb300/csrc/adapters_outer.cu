@@ -79,10 +79,7 @@ __device__ __forceinline__ float ao_remote(const float* p, uint32_t rank) {
 __global__ void __launch_bounds__(kAoThreads)
     adapters_outer_tile_kernel(const AdGradArgs a, const AoGeo g, const __grid_constant__ CUtensorMap mapX,
                                const __grid_constant__ CUtensorMap mapY) {
-  extern __shared__ __align__(16) unsigned char ao_raw[];
-  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(ao_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_total, s_abort;
+  extern __shared__ __align__(1024) unsigned char sm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), S = g.S;
   const int block = blockIdx.x / S, l = blockIdx.y;
@@ -93,17 +90,20 @@ __global__ void __launch_bounds__(kAoThreads)
   uint64_t* empty = ready + 8;
   uint64_t* tfull = empty + 8;   // an accumulator's tiles are done
   uint64_t* tempty = tfull + 2;  // and taken over
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tempty + 2);
+  int* s_total = reinterpret_cast<int*>(s_tmem + 1);
+  volatile int* abort_flag = s_total + 1;
   float* part = reinterpret_cast<float*>(sm + g.off_part);  // [Rk][128]
   const int stage = kAoXBytes + g.atoms * kAoAtom;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < g.stages; ++i) mbar_init(&full[i], 1), mbar_init(&ready[i], 4), mbar_init(&empty[i], 1);
+    for (int i = 0; i < g.stages; ++i) mbar_init(&full[i], 1), mbar_init(&ready[i], 1), mbar_init(&empty[i], 1);
     for (int i = 0; i < g.acc; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 4);
-    s_abort = 0;
-    s_total = 0;
+    *abort_flag = 0;
+    *s_total = 0;
     mbar_fence_init();
   }
   if (warp == 1) {
-    tmem_alloc(&s_tmem, g.tmem);
+    tmem_alloc(s_tmem, g.tmem);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -118,13 +118,12 @@ __global__ void __launch_bounds__(kAoThreads)
     }
   __syncwarp();
   mine = __reduce_add_sync(MOE_FULL_MASK, mine);
-  if (lane == 0 && mine) atomicAdd(&s_total, mine);
+  if (lane == 0 && mine) atomicAdd(s_total, mine);
   __syncthreads();
-  const uint32_t tmem = s_tmem;
-  const int total = s_total;
+  const uint32_t tmem = *s_tmem;
+  const int total = *s_total;
   AoTiles tiles{a, l, (int)((long long)total * rank / S), (int)((long long)total * (rank + 1) / S)};
   const int nt = tiles.hi - tiles.lo;
-  volatile int* abort_flag = &s_abort;
   auto wait = [&](uint64_t* bar, uint32_t parity) {  // bounded; nothing is waited for after a timeout
     if (!*abort_flag && !mbar_wait(bar, parity)) {
       *abort_flag = 1;
@@ -180,9 +179,12 @@ __global__ void __launch_bounds__(kAoThreads)
       __syncwarp();
     }
   } else {
-    // split v: unit = (row, 8 ranks); 3 x 16 bytes of the tile's columns [first | second | third part]
+    // split v: each slot of the ring has a warp of its own (which is never more than one use of its slot ahead);
+    // unit = (row, 8 ranks); 3 x 16 bytes of the tile's columns [first | second | third part].  A batch of loads is on
+    // its way while the slot is waited for.
+    constexpr int U = 8;
     const float* src = first ? a.dv : a.v;
-    const int g8 = g.Rk / 8, tid = threadIdx.x - 64;
+    const int g8 = g.Rk / 8;
     const bool vec = a.R % 4 == 0;
     const int q = warp & 3, f = q * 32 + lane;  // of the sums: lane = feature
     int drained = 0;
@@ -211,42 +213,56 @@ __global__ void __launch_bounds__(kAoThreads)
     };
     for (int i = 0; tiles.next(row0, rows); ++i) {
       const int s = i % g.stages, use = i / g.stages;
-      unsigned char* vs = sm + s * stage + kAoXBytes;
-      const int rows16 = (rows + 15) & ~15;
-      if (use > 0) wait(&empty[s], (use - 1) & 1);
-      for (int u = tid; u < rows16 * g8; u += 128) {
-        const int r = u / g8, c = (u % g8) * 8;
-        float v[8] = {};
-        if (r < rows) {
-          const float* p = src + (size_t)(row0 + r) * a.R + c;
-          if (vec && c + 8 <= a.R) {
-            const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
-            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-          } else {
+      if (s == warp - 2) {
+        unsigned char* vs = sm + s * stage + kAoXBytes;
+        const int rows16 = (rows + 15) & ~15, units = rows16 * g8;
+        for (int u0 = lane; u0 - lane < units; u0 += 32 * U) {
+          float v[U][8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (c + j < a.R) v[j] = p[j];
+          for (int k = 0; k < U; ++k) {
+            const int u = u0 + 32 * k, r = u / g8, c = (u % g8) * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[k][j] = 0.f;
+            if (r < rows) {
+              const float* p = src + (size_t)(row0 + r) * a.R + c;
+              if (vec && c + 8 <= a.R) {
+                const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
+                v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
+                v[k][4] = y.x, v[k][5] = y.y, v[k][6] = y.z, v[k][7] = y.w;
+              } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  if (c + j < a.R) v[k][j] = p[j];
+              }
+            }
+          }
+          if (u0 == lane && use > 0) wait(&empty[s], (use - 1) & 1);
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            const int u = u0 + 32 * k, r = u / g8, c = (u % g8) * 8;
+            uint4 o[3];
+            ad_split8<3>(v[k], o);
+            if (u < units) {
+#pragma unroll
+              for (int h = 0; h < 3; ++h) {
+                const int n = h * g.Rk + c;
+                *reinterpret_cast<uint4*>(vs + (n / 64) * kAoAtom + r * 128 + (((n % 64) / 8) ^ (r & 7)) * 16) = o[h];
+              }
+            }
           }
         }
-        uint4 o[3];
-        ad_split8<3>(v, o);
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const int n = k * g.Rk + c;
-          *reinterpret_cast<uint4*>(vs + (n / 64) * kAoAtom + r * 128 + (((n % 64) / 8) ^ (r & 7)) * 16) = o[k];
+        if (rows16 != rows) {
+          // the rest of the last 16 rows belongs to others, whatever it is
+          wait(&full[s], use & 1);
+          for (int u = lane; u < (rows16 - rows) * 16; u += 32) {
+            const int r = rows + u / 16, p = u % 16;
+            *reinterpret_cast<uint4*>(sm + s * stage + (p / 8) * kAoAtom + r * 128 + (p % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
         }
+        asm volatile("fence.proxy.async;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ready[s]);
       }
-      if (rows16 != rows) {
-        // the rest of the last 16 rows belongs to others, whatever it is
-        wait(&full[s], use & 1);
-        for (int u = tid; u < (rows16 - rows) * 16; u += 128) {
-          const int r = rows + u / 16, p = u % 16;
-          *reinterpret_cast<uint4*>(sm + s * stage + (p / 8) * kAoAtom + r * 128 + (p % 8) * 16) = make_uint4(0, 0, 0, 0);
-        }
-      }
-      asm volatile("fence.proxy.async;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ready[s]);
       // with two accumulators the one before last's sums are taken over while the products of the last one run
       if (i % kAoDrain == kAoDrain - 1 && i / kAoDrain >= g.acc - 1) drain();
     }
@@ -345,12 +361,13 @@ int ad_launch_outer(const AdGradArgs& a, int sms, cudaStream_t s) {
   g.tmem = 32;
   while (g.tmem < g.acc * 3 * g.Rk) g.tmem *= 2;
   const int stage = kAoXBytes + g.atoms * kAoAtom;
-  g.stages = g.Rk <= 64 ? 3 : 2;  // (of more, three and the sums do not fit)
+  // two CTAs a SM up to 32 ranks, else one; a slot for each of the four warps that split v at most
+  g.stages = std::min(4, ((g.Rk <= 32 ? 112 : 224) * 1024 - g.Rk * kAoFeat * 4) / stage);
   g.off_part = g.stages * stage;
   g.off_bar = g.off_part + g.Rk * kAoFeat * 4;
   g.blocks_a = (a.K + kAoFeat - 1) / kAoFeat;
   const int blocks = g.blocks_a + (a.N + kAoFeat - 1) / kAoFeat;
-  const int bytes = g.off_bar + 256 + 1024;
+  const int bytes = g.off_bar + 512;
   // CTAs for about two a SM; the adapters in use are at most the sequences
   const long long busy = (long long)blocks * std::min(a.L, a.n_seq);
   g.S = 1;

@@ -1,10 +1,14 @@
 // Adapters of longer sequences on the tcgen05 tensor cores: out = base + (scale_l x A_l^T) B_l in one launch.
 //
-// A cluster of C CTAs has a tile of up to 128 rows of one sequence.  CTA c multiplies its share of the K inputs by all R
-// ranks (D1 [rows][R] in TMEM: x by TMA, K-major; A_l K-major); the shares meet in distributed shared memory, where each
-// CTA adds up some of the rows in a fixed order, scales them and hands them to all; then CTA c multiplies them by its
-// share of the N outputs (D2 [rows][128], double-buffered; B_l as it lies, MN-major) and adds base on the way out.
+// A cluster of 8 CTAs has a tile of 32, 64 or 128 rows of one sequence.  CTA c multiplies its share of the K inputs by
+// all R ranks (D1 [rows][R] in TMEM: x by TMA, K-major; A_l K-major); the shares meet in distributed shared memory, where
+// each CTA adds up some of the rows in a fixed order, scales them and hands them to all; then CTA c multiplies them by
+// its share of the N outputs (D2 [rows][128], double-buffered; B_l as it lies, MN-major) and adds base on the way out.
 // Nothing but x, A, B, base and out crosses the memory, so those bytes bound it.
+//
+// The rows of a tile of 32 or 64 stand in the 128 lanes of D several times, so that all four epilogue warps (each reads
+// 32 lanes) have columns to store.  The tensor cores truncate what they add: D1 is several accumulators in turn, added
+// by additions that round.
 //
 // v = scale x A^T enters the second product as a sum of two (bf16 results) or three (fp32 results) bf16 numbers: 16 or
 // 24 significant bits.  The products cost little beside the bytes: 2 R flops a byte of x.
@@ -16,6 +20,7 @@
 namespace moe {
 
 constexpr int kAtThreads = 192;  // TMA warp, MMA warp, four epilogue warps
+constexpr int kAtCluster = 8;
 constexpr int kAtRows = 128;     // rows of a tile, at most (MMA M)
 constexpr int kAtCols = 128;     // outputs of a step of the second product
 constexpr uint32_t kAtTmem = 256;
@@ -24,7 +29,7 @@ constexpr int kAtStage = 4096;            // 32 rows x 128 bytes of results
 constexpr int kAtStages2 = 2;
 
 struct AtGeo {
-  int C, tile, Rk, stages1;     // CTAs, rows of a tile, R in sixteens, slots of the first ring
+  int tile, Rk, stages1;        // rows of a tile, R in sixteens, slots of the first ring
   int off2, off_part, off_bar;  // second ring, partial sums / staging, barriers
   int short_rows;               // sequences of up to so many rows are the row kernel's
 };
@@ -82,23 +87,34 @@ __device__ void at_find(const AdArgs& a, const AtGeo& g, int ti, int* tmp, int* 
   __syncthreads();
 }
 
+// Where 16-byte piece i of the partial sums lies: rows a power of two apart meet no bank twice.
+__device__ __forceinline__ uint32_t at_piece(uint32_t i) { return (i ^ ((i >> 3) & 7)) * 16; }
+
 template <bool F32>
 __global__ void __launch_bounds__(kAtThreads, 1)
     adapters_tile_kernel(const AdArgs a, const AtGeo g, const __grid_constant__ CUtensorMap mapX,
                          const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB) {
-  constexpr int NS = F32 ? 3 : 2;
-  extern __shared__ __align__(16) unsigned char at_raw[];
-  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(at_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ int s_tile[3], s_scan[33], s_abort;
-  __shared__ uint32_t s_tmem;
+  constexpr int NS = F32 ? 3 : 2, C = kAtCluster;
+  constexpr int kSize = F32 ? 4 : 2;
+  extern __shared__ __align__(1024) unsigned char sm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)cluster_rank(), C = g.C;
+  const int rank = (int)cluster_rank();
+  uint64_t* full1 = reinterpret_cast<uint64_t*>(sm + g.off_bar);
+  uint64_t* empty1 = full1 + 4;
+  uint64_t* full2 = empty1 + 4;
+  uint64_t* empty2 = full2 + kAtStages2;
+  uint64_t* tfull = empty2 + kAtStages2;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* d1full = tempty + 2;
+  int* s_tile = reinterpret_cast<int*>(d1full + 1);  // [4]
+  int* s_scan = s_tile + 4;                          // [33]
+  volatile int* abort_flag = s_scan + 33;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_scan + 34);
   pdl_wait();
   at_find(a, g, (int)cluster_index(), s_scan, s_tile);
   const int row0 = s_tile[0], rows = s_tile[1], l = s_tile[2];
   if (rows == 0) return;  // (the whole cluster)
   const int NT = (a.N + kAtCols - 1) / kAtCols, nt0 = NT * rank / C, nt1 = NT * (rank + 1) / C;
-  constexpr int kSize = F32 ? 4 : 2;
   if (l < 0) {
     if (a.kept && rank == 0)
       for (int i = threadIdx.x; i < rows * a.R; i += kAtThreads) a.kept[(size_t)row0 * a.R + i] = 0.f;
@@ -112,44 +128,47 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     }
     return;
   }
-  uint64_t* full1 = reinterpret_cast<uint64_t*>(sm + g.off_bar);
-  uint64_t* empty1 = full1 + 8;
-  uint64_t* full2 = empty1 + 8;
-  uint64_t* empty2 = full2 + kAtStages2;
-  uint64_t* tfull = empty2 + kAtStages2;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* d1full = tempty + 2;
   unsigned char* ring2 = sm + g.off2;
   unsigned char* part = sm + g.off_part;
   const int stage1 = kAtXBytes + g.Rk * 128, stage2 = g.Rk * 256;
+  const int nt = a.out ? nt1 - nt0 : 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < g.stages1; ++i) mbar_init(&full1[i], 1), mbar_init(&empty1[i], 1);
     for (int i = 0; i < kAtStages2; ++i) mbar_init(&full2[i], 1), mbar_init(&empty2[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 4);
     mbar_init(d1full, 1);
-    s_abort = 0;
+    *abort_flag = 0;
     mbar_fence_init();
   }
   if (warp == 1) {
-    tmem_alloc(&s_tmem, kAtTmem);
+    tmem_alloc(s_tmem, kAtTmem);
     tmem_relinquish();
+  }
+  if (warp >= 2 && nt > 0 && a.base) {
+    // base on its way to L2 while the first product runs
+    const int t = (int)threadIdx.x - 64;
+    if (t < rows) {
+      const int n0 = nt0 * kAtCols, n = min(nt1 * kAtCols, a.N) - n0;
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<const uint8_t*>(a.base) +
+                                                                     ((row0 + t) * a.ldb + n0) * kSize),
+                   "r"(n * kSize)
+                   : "memory");
+    }
   }
   __syncthreads();
   tc_fence_before();
   cluster_sync();  // every CTA of the cluster has started: its shared memory may be written
   tc_fence_after();
-  const uint32_t tmem = s_tmem, d1 = tmem + 128;
-  volatile int* abort_flag = &s_abort;
-  auto give_up = [&] {
-    *abort_flag = 1;
-    set_status(a.status, MOE_DEV_TIMEOUT);
-  };
+  const uint32_t tmem = *s_tmem;
   auto wait = [&](uint64_t* bar, uint32_t parity) {  // bounded; nothing is waited for after a timeout
-    if (!*abort_flag && !mbar_wait(bar, parity)) give_up();
+    if (!*abort_flag && !mbar_wait(bar, parity)) {
+      *abort_flag = 1;
+      set_status(a.status, MOE_DEV_TIMEOUT);
+    }
   };
   const int kc = (a.K + 63) / 64, kc0 = kc * rank / C, kc1 = kc * (rank + 1) / C, nk = kc1 - kc0;
-  const int boxes = (rows + 31) / 32;
-  const int nt = a.out ? nt1 - nt0 : 0;
+  const int nacc = min(min(nk, 8), (int)kAtTmem / g.Rk);  // accumulators of D1, taken in turn
+  const int copies = kAtRows / g.tile;                    // of a tile's rows in the 128 lanes
   int loaded2 = 0;
   auto load2 = [&](int i) {  // step i of the second product
     unsigned char* st = ring2 + (i % kAtStages2) * stage2;
@@ -161,13 +180,16 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   // ---- the first product
   if (warp == 0) {
     if (lane == 0) {
+      const int boxes = (rows + 31) / 32;
       for (int i = 0; i < nk && !*abort_flag; ++i) {
         const int s = i % g.stages1, use = i / g.stages1;
         if (use > 0) wait(&empty1[s], (use - 1) & 1);
         if (*abort_flag) break;
         unsigned char* st = sm + s * stage1;
-        mbar_expect_tx(&full1[s], (uint32_t)(boxes * 4096 + g.Rk * 128));
-        for (int b = 0; b < boxes; ++b) tma_load_3d(st + b * 4096, &mapX, &full1[s], (kc0 + i) * 64, row0 + 32 * b, 0);
+        mbar_expect_tx(&full1[s], (uint32_t)(copies * boxes * 4096 + g.Rk * 128));
+        for (int c = 0; c < copies; ++c)
+          for (int b = 0; b < boxes; ++b)
+            tma_load_3d(st + c * g.tile * 128 + b * 4096, &mapX, &full1[s], (kc0 + i) * 64, row0 + 32 * b, 0);
         tma_load_3d(st + kAtXBytes, &mapA, &full1[s], (kc0 + i) * 64, 0, l);
       }
       for (; loaded2 < min(nt, kAtStages2) && !*abort_flag; ++loaded2) load2(loaded2);
@@ -183,8 +205,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         tc_fence_after();
         if (!*abort_flag) {
           const uint64_t ad = at_desc(base + s * stage1, 16, 1024), bd = at_desc(base + s * stage1 + kAtXBytes, 16, 1024);
+          const uint32_t d = tmem + (i % nacc) * g.Rk;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) umma_f16(d1, ad + 2 * q, bd + 2 * q, idesc, i + q != 0);
+          for (int q = 0; q < 4; ++q) umma_f16(d, ad + 2 * q, bd + 2 * q, idesc, q != 0 || i >= nacc);
         }
         umma_commit(&empty1[s]);
       }
@@ -192,31 +215,35 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     }
     __syncwarp();
   }
-  const int per = g.tile / C;            // rows that a CTA adds up
-  const int pitch = g.Rk + 4;            // floats of a row of partial sums
-  const int q = warp & 3, row = q * 32 + lane;
+  const int per = g.tile / C;  // rows that a CTA adds up
+  const int q = warp & 3, row = (q * 32 + lane) % g.tile, copy = q * 32 / g.tile;
+  const uint32_t lanes = (uint32_t)(q * 32) << 16;
   if (warp >= 2) {
     if (nk > 0) {
       wait(d1full, 0);
       __syncwarp();
       tc_fence_after();
     }
-    const uint32_t dst = mapa_shared(smem_u32(part), (uint32_t)min(row / per, C - 1)) +
-                         (uint32_t)((rank * per + row % per) * pitch) * 4;
-    for (int c = 0; c < g.Rk; c += 16) {
+    const uint32_t dst = mapa_shared(smem_u32(part), (uint32_t)(row / per));
+    const int first = (rank * per + row % per) * (g.Rk / 4);
+    for (int c = copy * 16; c < g.Rk; c += 16 * copies) {
       float v[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = 0.f;
-      if (nk > 0) {
-        tmem_ld_w<16>(d1 + ((uint32_t)(q * 32) << 16) + c, v);
+      for (int n = 0; n < nacc; ++n) {
+        float w[16];
+        tmem_ld_w<16>(tmem + lanes + n * g.Rk + c, w);
         tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] += w[i];
       }
       if (row < rows) {
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) at_store4(dst + (c + i) * 4, v[i], v[i + 1], v[i + 2], v[i + 3]);
+        for (int i = 0; i < 16; i += 4) at_store4(dst + at_piece(first + (c + i) / 4), v[i], v[i + 1], v[i + 2], v[i + 3]);
       }
     }
     tc_fence_before();
+    __syncwarp();
   }
   cluster_sync();  // partial sums are there; the first ring is free in every CTA (its products are done)
   if (warp >= 2) {
@@ -225,9 +252,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     for (int i = threadIdx.x - 64; i < mine * g8; i += 128) {
       const int r = i / g8, c = (i % g8) * 8, t = rank * per + r;
       float v[8] = {};
+#pragma unroll
       for (int p = 0; p < C; ++p) {
-        const float4* src = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(part) + (p * per + r) * pitch + c);
-        const float4 x = src[0], y = src[1];
+        const uint32_t at = (p * per + r) * (g.Rk / 4) + c / 4;
+        const float4 x = *reinterpret_cast<const float4*>(part + at_piece(at));
+        const float4 y = *reinterpret_cast<const float4*>(part + at_piece(at + 1));
         v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
       }
 #pragma unroll
@@ -241,10 +270,15 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       for (int s = 0; s < NS; ++s) {
         const int k = s * g.Rk + c;
         const uint32_t off = smem_u32(sm) + (uint32_t)((k / 64) * kAtXBytes + t * 128 + (((k % 64) / 8) ^ (t & 7)) * 16);
-        for (int p = 0; p < C; ++p) at_store16(mapa_shared(off, p), o[s]);
+#pragma unroll
+        for (int p = 0; p < C; ++p) {
+          const uint32_t at = mapa_shared(off, p);
+          for (int n = 0; n < copies; ++n) at_store16(at + n * g.tile * 128, o[s]);
+        }
       }
     }
     at_fence_async();
+    __syncwarp();
   }
   cluster_sync();  // v of all rows is there
   // ---- the second product
@@ -287,72 +321,84 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   } else {
     constexpr int kChunk = F32 ? 32 : 64, kPer = kAtCols / kChunk;  // outputs of a chunk (128 bytes); chunks of a step
     unsigned char* buf = part + (warp - 2) * 2 * kAtStage;
-    const int nch = nt * kPer;
+    const int nch = nt * kPer;              // this warp's chunks: copy, copy + copies, ...
     const int pr = lane >> 3, pc = lane & 7;  // of a 4-row copy: row, 16-byte piece
+    const int r0 = q * 32 % g.tile;         // first row of this warp
+    const int have = min(32, rows - r0);    // (none: it waits and arrives only)
     auto col = [&](int ch) { return (nt0 + ch / kPer) * kAtCols + ch % kPer * kChunk; };
-    auto fetch = [&](int ch) {
+    int slot = 0;
+    auto fetch = [&](int ch, int to) {
       if (ch < nch && a.base) {
         const int n = col(ch) + pc * (16 / kSize);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int r = i * 4 + pr;
-          if (q * 32 + r < rows && n < a.N)
-            at_copy16(buf + (ch & 1) * kAtStage + r * 128 + ((pc ^ (r & 7)) * 16),
-                      reinterpret_cast<const uint8_t*>(a.base) + ((row0 + q * 32 + r) * a.ldb + n) * kSize);
+          if (r < have && n < a.N)
+            at_copy16(buf + to * kAtStage + r * 128 + ((pc ^ (r & 7)) * 16),
+                      reinterpret_cast<const uint8_t*>(a.base) + ((row0 + r0 + r) * a.ldb + n) * kSize);
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    fetch(0);
-    for (int ch = 0; ch < nch; ++ch) {
-      const int i = ch / kPer, b = i & 1;
-      fetch(ch + 1);
-      if (ch % kPer == 0) {
+    fetch(copy, 0);
+    for (int i = 0; i < nt; ++i) {
+      const int b = i & 1;
+      const int c0 = i * kPer, from = c0 + (copy - c0 % copies + copies) % copies;  // the step's first chunk of this warp
+      bool waited = false;
+      for (int ch = from; ch < c0 + kPer; ch += copies) {
+        fetch(ch + copies, slot ^ 1);
+        if (!waited) {
+          wait(&tfull[b], (i / 2) & 1);
+          __syncwarp();
+          tc_fence_after();
+          waited = true;
+        }
+        float v[kChunk];
+        const uint32_t at = tmem + lanes + b * kAtCols + ch % kPer * kChunk;
+#pragma unroll
+        for (int j = 0; j < kChunk; j += 32) tmem_ld32(at + j, *reinterpret_cast<float(*)[32]>(v + j));
+        tmem_ld_wait();
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+        unsigned char* st = buf + slot * kAtStage;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint4* p = reinterpret_cast<uint4*>(st + lane * 128 + ((j ^ (lane & 7)) * 16));
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (a.base) x = *p;
+          uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (F32) {
+              u[k] = __float_as_uint(__uint_as_float(u[k]) + v[j * 4 + k]);
+            } else {
+              const __nv_bfloat162 z = __floats2bfloat162_rn(bf16_lo(u[k]) + v[(j * 8 + 2 * k) % kChunk],
+                                                             bf16_hi(u[k]) + v[(j * 8 + 2 * k + 1) % kChunk]);
+              u[k] = *reinterpret_cast<const uint32_t*>(&z);
+            }
+          }
+          *p = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+        __syncwarp();
+        const int n = col(ch) + pc * (16 / kSize);
+        const bool store = n < a.N && !*abort_flag;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = k * 4 + pr;
+          if (store && r < have)
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.out) + ((row0 + r0 + r) * a.ldo + n) * kSize) =
+                *reinterpret_cast<const uint4*>(st + r * 128 + ((pc ^ (r & 7)) * 16));
+        }
+        __syncwarp();
+        slot ^= 1;
+      }
+      if (!waited) {  // nothing of this step: in step with the others all the same
         wait(&tfull[b], (i / 2) & 1);
         __syncwarp();
-        tc_fence_after();
       }
-      float v[kChunk];
-      const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + b * kAtCols + ch % kPer * kChunk;
-#pragma unroll
-      for (int j = 0; j < kChunk; j += 32) tmem_ld32(at + j, *reinterpret_cast<float(*)[32]>(v + j));
-      tmem_ld_wait();
-      if (ch % kPer == kPer - 1) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty[b]);
-      }
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      tc_fence_before();
       __syncwarp();
-      unsigned char* st = buf + (ch & 1) * kAtStage;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint4* p = reinterpret_cast<uint4*>(st + lane * 128 + ((j ^ (lane & 7)) * 16));
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (a.base) x = *p;
-        uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (F32) {
-            u[k] = __float_as_uint(__uint_as_float(u[k]) + v[j * 4 + k]);
-          } else {
-            const __nv_bfloat162 z = __floats2bfloat162_rn(bf16_lo(u[k]) + v[(j * 8 + 2 * k) % kChunk], bf16_hi(u[k]) + v[(j * 8 + 2 * k + 1) % kChunk]);
-            u[k] = *reinterpret_cast<const uint32_t*>(&z);
-          }
-        }
-        *p = make_uint4(u[0], u[1], u[2], u[3]);
-      }
-      __syncwarp();
-      const int n = col(ch) + pc * (16 / kSize);
-      const bool store = n < a.N && !*abort_flag;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int r = k * 4 + pr;
-        if (store && q * 32 + r < rows)
-          *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.out) + ((row0 + q * 32 + r) * a.ldo + n) * kSize) =
-              *reinterpret_cast<const uint4*>(st + r * 128 + ((pc ^ (r & 7)) * 16));
-      }
-      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[b]);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     tc_fence_before();
@@ -364,20 +410,22 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   }
 }
 
-int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, cudaStream_t s) {
+int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, int sms, cudaStream_t s) {
   AtGeo g = {};
   const int NS = f32 ? 3 : 2;
   g.Rk = (a.R + 15) / 16 * 16;
-  g.C = 4;
-  g.tile = g.Rk > 64 ? 64 : kAtRows;  // (the partial sums of 128 rows of more ranks do not fit beside the rings)
+  // rows of a tile: fewer where that gives the SMs something to do
+  g.tile = kAtRows;
+  while (g.tile > 32 && ((long long)a.T / g.tile + 1) * kAtCluster <= sms) g.tile /= 2;
   g.short_rows = short_rows;
   const int stage1 = kAtXBytes + g.Rk * 128;
-  g.stages1 = g.Rk > 64 ? 3 : 4;
+  // two CTAs a SM up to 64 ranks
+  g.stages1 = g.Rk <= 16 ? 4 : g.Rk <= 32 ? 3 : g.Rk <= 64 ? 2 : 3;
   const int ring1 = std::max(g.stages1 * stage1, (NS * g.Rk + 63) / 64 * kAtXBytes);
   g.off2 = ring1;
   g.off_part = g.off2 + kAtStages2 * g.Rk * 256;
-  g.off_bar = g.off_part + std::max(8 * kAtStage, (g.tile * (g.Rk + 4) * 4 + 1023) / 1024 * 1024);
-  const int bytes = g.off_bar + 256 + 1024;
+  g.off_bar = g.off_part + std::max(8 * kAtStage, g.tile * g.Rk * 4);
+  const int bytes = g.off_bar + 512;
   CUtensorMap mx, ma, mb;
   {
     const uint64_t dims[3] = {(uint64_t)a.K, (uint64_t)a.T, 1}, st[2] = {(uint64_t)a.ldx * 2, (uint64_t)a.ldx * 2};
@@ -391,16 +439,16 @@ int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, cudaStream_t s) {
     if (int rc = encode_tmap_3d_bf16(w ? &mb : &ma, w ? a.w2 : a.w1, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B)) return rc;
   }
   const long long tiles = std::min<long long>(a.T, a.T / g.tile + a.n_seq + 2ll);
-  if (tiles * g.C > 0x7fffffffll) return MOE_ERR_ARG;
+  if (tiles * kAtCluster > 0x7fffffffll) return MOE_ERR_ARG;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = g.C;
+  at[0].val.clusterDim.x = kAtCluster;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * g.C));
+  cfg.gridDim = dim3((unsigned)(tiles * kAtCluster));
   cfg.blockDim = dim3(kAtThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;

@@ -153,6 +153,23 @@ def test_many_sequences_and_adapters():
     check(2500, 64, 72, 8, 2, 9, lengths=[0] * 1200 + [1] * 500 + [2000] + [0] * 900, none=0.3)
 
 
+@pytest.mark.parametrize("R", [16, 32, 64, 80, 128])
+def test_many_passes_over_long_sequences(R):
+    """Rings of every number of slots, many rounds, passes one behind the other: the same bits each time, no timeout."""
+    import expert_slot_cache_gb300 as M
+    lengths = [1900, 70, 3000, 1030]
+    x, a, b, scale, ids, starts = case(6000, 512, 264, R, 2, R, lengths, none=0.0)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    dy, base = normal(6000, 264, g=g), normal(6000, 264, g=g)
+    op = M.Adapters(a, b, scale)
+    kept = torch.empty(6000, R, device=DEV)
+    out = op.forward(x, ids, base, starts, kept=kept)
+    want = op.grad(dy, x, kept, ids, None, starts)
+    passes = [(op.forward(x, ids, base, starts), op.grad(dy, x, kept, ids, None, starts)) for _ in range(40)]
+    assert all(torch.equal(o, out) and all(torch.equal(p, q) for p, q in zip(r, want)) for o, r in passes)
+    assert int(op.dev_status.item()) == 0
+
+
 def test_large_values_and_other_rows_nan():
     """NaN and infinities stay in their rows, whatever the tile; rows of no sequence are not read into anything."""
     import expert_slot_cache_gb300 as M
