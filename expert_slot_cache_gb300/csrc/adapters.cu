@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(const AdArgs 
   __shared__ float s_part[2][kRowCluster][kAdMaxR];
   __shared__ float s_v[kAdMaxR];
   pdl_wait();
+  pdl_trigger();  // what follows waits for this kernel, or has other rows
   const int c = (int)ad_rank(), unit = blockIdx.x / kRowCluster;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int s = unit, t0 = unit, t1 = unit + 1;
@@ -185,9 +186,9 @@ static int ad_run(const AdArgs& a, bool f32, cudaStream_t s) {
   if (!a.seq || a.T <= kShortRows) return ad_launch_rows(a, f32, a.T, 0, s);
   int sms = 0;
   if (int rc = ad_sms(&sms)) return rc;
-  if (a.n_seq == 1 || a.T >= 64ll * a.n_seq) return ad_launch_tiles(a, f32, 0, sms, s);
+  if (a.n_seq == 1 || a.T >= 64ll * a.n_seq) return ad_launch_tiles(a, f32, 0, false, sms, s);
   if (int rc = ad_launch_rows(a, f32, a.n_seq, kShortRows, s)) return rc;
-  return ad_launch_tiles(a, f32, kShortRows, sms, s);
+  return ad_launch_tiles(a, f32, kShortRows, true, sms, s);
 }
 
 static bool ad_shape(int T, int K, int N, int R, int L, const int32_t* seq, int n_seq) {

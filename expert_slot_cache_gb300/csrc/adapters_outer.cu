@@ -96,20 +96,22 @@ __global__ void __launch_bounds__(kAoThreads)
   float* part = reinterpret_cast<float*>(sm + g.off_part);  // [Rk][128]
   const int stage = kAoXBytes + g.atoms * kAoAtom;
   if (threadIdx.x == 0) {
+    prefetch_tmap(first ? &mapX : &mapY);
     for (int i = 0; i < g.stages; ++i) mbar_init(&full[i], 1), mbar_init(&ready[i], 1), mbar_init(&empty[i], 1);
     for (int i = 0; i < g.acc; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 4);
     *abort_flag = 0;
     *s_total = 0;
     mbar_fence_init();
   }
-  if (warp == 1) {
+  pdl_wait();
+  if (warp == 1) {  // (after the wait: a kernel before this one may have tensor memory to allocate yet)
     tmem_alloc(s_tmem, g.tmem);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  pdl_wait();
+  pdl_trigger();
   int mine = 0;
   for (int q = threadIdx.x; q < a.n_seq; q += kAoThreads)
     if (a.ids[q] == l) {

@@ -27,16 +27,20 @@ constexpr uint32_t kAtTmem = 256;
 constexpr int kAtXBytes = kAtRows * 128;  // 64 inputs of a tile's rows
 constexpr int kAtStage = 4096;            // 32 rows x 128 bytes of results
 constexpr int kAtStages2 = 2;
+constexpr int kAtAcc = 4;
 
 struct AtGeo {
   int tile, Rk, stages1;        // rows of a tile, R in sixteens, slots of the first ring
   int off2, off_part, off_bar;  // second ring, partial sums / staging, barriers
-  int short_rows;               // sequences of up to so many rows are the row kernel's
+  int short_rows;               // sequences of up to so many rows are the row kernel's,
+  int beside;                   // which has been launched before this one and may still run
 };
 
 __device__ __forceinline__ uint64_t at_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
   return smem_desc_l(saddr, lbo, sbo, kLayoutSw128);
 }
+__device__ __forceinline__ void at_cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void at_cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void at_fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ void at_store4(uint32_t caddr, float a, float b, float c, float d) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(caddr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
@@ -110,14 +114,30 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   int* s_scan = s_tile + 4;                          // [33]
   volatile int* abort_flag = s_scan + 33;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_scan + 34);
-  pdl_wait();
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&mapX);
+    prefetch_tmap(&mapA);
+    prefetch_tmap(&mapB);
+    for (int i = 0; i < g.stages1; ++i) mbar_init(&full1[i], 1), mbar_init(&empty1[i], 1);
+    for (int i = 0; i < kAtStages2; ++i) mbar_init(&full2[i], 1), mbar_init(&empty2[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 4);
+    mbar_init(d1full, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  // The row kernel waited for what came before it and reads and writes other rows: only the end has to be in order.
+  if (!g.beside) pdl_wait();
   at_find(a, g, (int)cluster_index(), s_scan, s_tile);
   const int row0 = s_tile[0], rows = s_tile[1], l = s_tile[2];
-  if (rows == 0) return;  // (the whole cluster)
+  if (rows == 0) {  // (the whole cluster)
+    if (g.beside) pdl_wait();
+    return;
+  }
   const int NT = (a.N + kAtCols - 1) / kAtCols, nt0 = NT * rank / C, nt1 = NT * (rank + 1) / C;
   if (l < 0) {
     if (a.kept && rank == 0)
       for (int i = threadIdx.x; i < rows * a.R; i += kAtThreads) a.kept[(size_t)row0 * a.R + i] = 0.f;
+    if (g.beside) pdl_wait();
     if (!a.out || (a.out == a.base && a.ldo == a.ldb)) return;
     const int p0 = nt0 * kAtCols * kSize / 16, np = min(nt1 * kAtCols, a.N) * kSize / 16 - p0;
     for (int i = threadIdx.x; i < rows * np; i += kAtThreads) {
@@ -132,15 +152,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   unsigned char* part = sm + g.off_part;
   const int stage1 = kAtXBytes + g.Rk * 128, stage2 = g.Rk * 256;
   const int nt = a.out ? nt1 - nt0 : 0;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < g.stages1; ++i) mbar_init(&full1[i], 1), mbar_init(&empty1[i], 1);
-    for (int i = 0; i < kAtStages2; ++i) mbar_init(&full2[i], 1), mbar_init(&empty2[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 4);
-    mbar_init(d1full, 1);
-    *abort_flag = 0;
-    mbar_fence_init();
-  }
-  if (warp == 1) {
+  if (warp == 1) {  // (after the wait: a kernel before this one may have tensor memory to allocate yet)
     tmem_alloc(s_tmem, kAtTmem);
     tmem_relinquish();
   }
@@ -155,10 +167,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                    : "memory");
     }
   }
-  __syncthreads();
   tc_fence_before();
-  cluster_sync();  // every CTA of the cluster has started: its shared memory may be written
+  __syncthreads();
   tc_fence_after();
+  at_cluster_arrive();  // waited for where another CTA's shared memory is written first
+  if (!g.beside) pdl_trigger();  // (after the allocation: a kernel that starts now may allocate, too)
   const uint32_t tmem = *s_tmem;
   auto wait = [&](uint64_t* bar, uint32_t parity) {  // bounded; nothing is waited for after a timeout
     if (!*abort_flag && !mbar_wait(bar, parity)) {
@@ -167,7 +180,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     }
   };
   const int kc = (a.K + 63) / 64, kc0 = kc * rank / C, kc1 = kc * (rank + 1) / C, nk = kc1 - kc0;
-  const int nacc = min(min(nk, 8), (int)kAtTmem / g.Rk);  // accumulators of D1, taken in turn
+  const int nacc = min(min(nk, kAtAcc), (int)kAtTmem / g.Rk);  // accumulators of D1, taken in turn
   const int copies = kAtRows / g.tile;                    // of a tile's rows in the 128 lanes
   int loaded2 = 0;
   auto load2 = [&](int i) {  // step i of the second product
@@ -226,16 +239,20 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     }
     const uint32_t dst = mapa_shared(smem_u32(part), (uint32_t)(row / per));
     const int first = (rank * per + row % per) * (g.Rk / 4);
+    at_cluster_wait();  // every CTA of the cluster has started
     for (int c = copy * 16; c < g.Rk; c += 16 * copies) {
+      float w[kAtAcc][16];
+#pragma unroll
+      for (int n = 0; n < kAtAcc; ++n)
+        if (n < nacc) tmem_ld_w<16>(tmem + lanes + n * g.Rk + c, w[n]);
+      tmem_ld_wait();
       float v[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = 0.f;
-      for (int n = 0; n < nacc; ++n) {
-        float w[16];
-        tmem_ld_w<16>(tmem + lanes + n * g.Rk + c, w);
-        tmem_ld_wait();
+      for (int i = 0; i < 16; ++i) {
+        v[i] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] += w[i];
+        for (int n = 0; n < kAtAcc; ++n)
+          if (n < nacc) v[i] += w[n][i];
       }
       if (row < rows) {
 #pragma unroll
@@ -244,10 +261,14 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     }
     tc_fence_before();
     __syncwarp();
+  } else {
+    at_cluster_wait();
   }
   cluster_sync();  // partial sums are there; the first ring is free in every CTA (its products are done)
   if (warp >= 2) {
     const float scale = a.scale[l];
+    // piece p (8 of the NS Rk values) of row t
+    auto v_at = [&](int t, int p) { return (uint32_t)((p / 8) * kAtXBytes + t * 128 + ((p % 8) ^ (t & 7)) * 16); };
     const int g8 = g.Rk / 8, mine = max(0, min(per, rows - rank * per));
     for (int i = threadIdx.x - 64; i < mine * g8; i += 128) {
       const int r = i / g8, c = (i % g8) * 8, t = rank * per + r;
@@ -267,15 +288,16 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       uint4 o[NS];
       ad_split8<NS>(v, o);
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        const int k = s * g.Rk + c;
-        const uint32_t off = smem_u32(sm) + (uint32_t)((k / 64) * kAtXBytes + t * 128 + (((k % 64) / 8) ^ (t & 7)) * 16);
-#pragma unroll
-        for (int p = 0; p < C; ++p) {
-          const uint32_t at = mapa_shared(off, p);
-          for (int n = 0; n < copies; ++n) at_store16(at + n * g.tile * 128, o[s]);
-        }
-      }
+      for (int s = 0; s < NS; ++s) *reinterpret_cast<uint4*>(sm + v_at(t, s * g8 + c / 8)) = o[s];
+    }
+    // to the other CTAs and the other copies, 16 bytes at a time
+    named_sync(1, 128);
+    const int pieces = NS * g8, places = C * copies;
+    for (int i = threadIdx.x - 64; i < mine * pieces * places; i += 128) {
+      const int at = i / places, to = i % places, t = rank * per + at / pieces;
+      const uint32_t off = v_at(t, at % pieces);
+      const uint4 v = *reinterpret_cast<const uint4*>(sm + off);
+      if (to != rank) at_store16(mapa_shared(smem_u32(sm) + off + (to / C) * g.tile * 128, to % C), v);
     }
     at_fence_async();
     __syncwarp();
@@ -408,9 +430,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kAtTmem);
   }
+  if (g.beside) pdl_wait();
 }
 
-int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, int sms, cudaStream_t s) {
+int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, bool beside, int sms, cudaStream_t s) {
   AtGeo g = {};
   const int NS = f32 ? 3 : 2;
   g.Rk = (a.R + 15) / 16 * 16;
@@ -418,6 +441,7 @@ int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, int sms, cudaStre
   g.tile = kAtRows;
   while (g.tile > 32 && ((long long)a.T / g.tile + 1) * kAtCluster <= sms) g.tile /= 2;
   g.short_rows = short_rows;
+  g.beside = beside;
   const int stage1 = kAtXBytes + g.Rk * 128;
   // two CTAs a SM up to 64 ranks
   g.stages1 = g.Rk <= 16 ? 4 : g.Rk <= 32 ? 3 : g.Rk <= 64 ? 2 : 3;
