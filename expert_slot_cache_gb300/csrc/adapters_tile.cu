@@ -39,14 +39,17 @@ struct AtGeo {
 __device__ __forceinline__ uint64_t at_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
   return smem_desc_l(saddr, lbo, sbo, kLayoutSw128);
 }
+__device__ __forceinline__ void at_cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void at_cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void at_cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void at_fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void at_fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void at_store4(uint32_t caddr, float a, float b, float c, float d) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(caddr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
-__device__ __forceinline__ void at_store16(uint32_t caddr, uint4 v) {
-  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(caddr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+// Shared memory of this CTA to another one's; the bytes count on an mbarrier there.
+__device__ __forceinline__ void at_send(uint32_t to, uint32_t from, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+               "r"(from), "r"(bytes), "r"(bar)
                : "memory");
 }
 __device__ __forceinline__ void at_copy16(void* dst, const void* src) {
@@ -110,7 +113,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   uint64_t* tfull = empty2 + kAtStages2;
   uint64_t* tempty = tfull + 2;
   uint64_t* d1full = tempty + 2;
-  int* s_tile = reinterpret_cast<int*>(d1full + 1);  // [4]
+  uint64_t* vfull = d1full + 1;                    // v of all rows is there,
+  uint64_t* vrep = vfull + 1;                      // in all the lanes
+  int* s_tile = reinterpret_cast<int*>(vrep + 1);  // [4]
   int* s_scan = s_tile + 4;                          // [33]
   volatile int* abort_flag = s_scan + 33;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_scan + 34);
@@ -122,22 +127,31 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     for (int i = 0; i < kAtStages2; ++i) mbar_init(&full2[i], 1), mbar_init(&empty2[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 4);
     mbar_init(d1full, 1);
+    mbar_init(vfull, 2);
+    mbar_init(vrep, 4);
     *abort_flag = 0;
     mbar_fence_init();
   }
   // The row kernel waited for what came before it and reads and writes other rows: only the end has to be in order.
   if (!g.beside) pdl_wait();
+  if (warp == 1) {  // (after the wait: a kernel before this one may have tensor memory to allocate yet)
+    tmem_alloc(s_tmem, kAtTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
   at_find(a, g, (int)cluster_index(), s_scan, s_tile);
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
   const int row0 = s_tile[0], rows = s_tile[1], l = s_tile[2];
-  if (rows == 0) {  // (the whole cluster)
+  if (rows == 0 || l < 0) {  // (the whole cluster)
+    if (warp == 1) tmem_dealloc(tmem, kAtTmem);
     if (g.beside) pdl_wait();
-    return;
+    if (rows == 0) return;
   }
   const int NT = (a.N + kAtCols - 1) / kAtCols, nt0 = NT * rank / C, nt1 = NT * (rank + 1) / C;
   if (l < 0) {
     if (a.kept && rank == 0)
       for (int i = threadIdx.x; i < rows * a.R; i += kAtThreads) a.kept[(size_t)row0 * a.R + i] = 0.f;
-    if (g.beside) pdl_wait();
     if (!a.out || (a.out == a.base && a.ldo == a.ldb)) return;
     const int p0 = nt0 * kAtCols * kSize / 16, np = min(nt1 * kAtCols, a.N) * kSize / 16 - p0;
     for (int i = threadIdx.x; i < rows * np; i += kAtThreads) {
@@ -152,10 +166,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   unsigned char* part = sm + g.off_part;
   const int stage1 = kAtXBytes + g.Rk * 128, stage2 = g.Rk * 256;
   const int nt = a.out ? nt1 - nt0 : 0;
-  if (warp == 1) {  // (after the wait: a kernel before this one may have tensor memory to allocate yet)
-    tmem_alloc(s_tmem, kAtTmem);
-    tmem_relinquish();
-  }
+  at_cluster_arrive_relaxed();    // waited for where another CTA's shared memory is written first
+  if (!g.beside) pdl_trigger();  // (after the allocation: a kernel that starts now may allocate, too)
   if (warp >= 2 && nt > 0 && a.base) {
     // base on its way to L2 while the first product runs
     const int t = (int)threadIdx.x - 64;
@@ -167,12 +179,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                    : "memory");
     }
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  at_cluster_arrive();  // waited for where another CTA's shared memory is written first
-  if (!g.beside) pdl_trigger();  // (after the allocation: a kernel that starts now may allocate, too)
-  const uint32_t tmem = *s_tmem;
   auto wait = [&](uint64_t* bar, uint32_t parity) {  // bounded; nothing is waited for after a timeout
     if (!*abort_flag && !mbar_wait(bar, parity)) {
       *abort_flag = 1;
@@ -180,8 +186,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     }
   };
   const int kc = (a.K + 63) / 64, kc0 = kc * rank / C, kc1 = kc * (rank + 1) / C, nk = kc1 - kc0;
-  const int nacc = min(min(nk, kAtAcc), (int)kAtTmem / g.Rk);  // accumulators of D1, taken in turn
+  const int nacc = min(min((nk + 3) / 4, kAtAcc), (int)kAtTmem / g.Rk);  // accumulators of D1, taken in turn
   const int copies = kAtRows / g.tile;                    // of a tile's rows in the 128 lanes
+  const int per = g.tile / C;                             // rows that a CTA adds up
+  const int mine = max(0, min(per, rows - rank * per));
+  const int atoms = (NS * g.Rk + 63) / 64;                // of v: 128 lanes x 128 bytes
   int loaded2 = 0;
   auto load2 = [&](int i) {  // step i of the second product
     unsigned char* st = ring2 + (i % kAtStages2) * stage2;
@@ -193,19 +202,17 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   // ---- the first product
   if (warp == 0) {
     if (lane == 0) {
-      const int boxes = (rows + 31) / 32;
       for (int i = 0; i < nk && !*abort_flag; ++i) {
         const int s = i % g.stages1, use = i / g.stages1;
         if (use > 0) wait(&empty1[s], (use - 1) & 1);
         if (*abort_flag) break;
         unsigned char* st = sm + s * stage1;
-        mbar_expect_tx(&full1[s], (uint32_t)(copies * boxes * 4096 + g.Rk * 128));
-        for (int c = 0; c < copies; ++c)
-          for (int b = 0; b < boxes; ++b)
-            tma_load_3d(st + c * g.tile * 128 + b * 4096, &mapX, &full1[s], (kc0 + i) * 64, row0 + 32 * b, 0);
+        mbar_expect_tx(&full1[s], (uint32_t)(g.tile + g.Rk) * 128);
+        tma_load_3d(st, &mapX, &full1[s], (kc0 + i) * 64, row0, 0);
         tma_load_3d(st + kAtXBytes, &mapA, &full1[s], (kc0 + i) * 64, 0, l);
       }
       for (; loaded2 < min(nt, kAtStages2) && !*abort_flag; ++loaded2) load2(loaded2);
+      mbar_expect_tx(vfull, (uint32_t)(atoms * 128 * (rows - mine)));
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -228,10 +235,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     }
     __syncwarp();
   }
-  const int per = g.tile / C;  // rows that a CTA adds up
   const int q = warp & 3, row = (q * 32 + lane) % g.tile, copy = q * 32 / g.tile;
   const uint32_t lanes = (uint32_t)(q * 32) << 16;
+  float scale = 0.f;
   if (warp >= 2) {
+    scale = a.scale[l];
     if (nk > 0) {
       wait(d1full, 0);
       __syncwarp();
@@ -240,7 +248,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const uint32_t dst = mapa_shared(smem_u32(part), (uint32_t)(row / per));
     const int first = (rank * per + row % per) * (g.Rk / 4);
     at_cluster_wait();  // every CTA of the cluster has started
-    for (int c = copy * 16; c < g.Rk; c += 16 * copies) {
+    for (int c = 0; c < g.Rk && copy == 0; c += 16) {
       float w[kAtAcc][16];
 #pragma unroll
       for (int n = 0; n < kAtAcc; ++n)
@@ -266,10 +274,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   }
   cluster_sync();  // partial sums are there; the first ring is free in every CTA (its products are done)
   if (warp >= 2) {
-    const float scale = a.scale[l];
     // piece p (8 of the NS Rk values) of row t
     auto v_at = [&](int t, int p) { return (uint32_t)((p / 8) * kAtXBytes + t * 128 + ((p % 8) ^ (t & 7)) * 16); };
-    const int g8 = g.Rk / 8, mine = max(0, min(per, rows - rank * per));
+    const int g8 = g.Rk / 8;
     for (int i = threadIdx.x - 64; i < mine * g8; i += 128) {
       const int r = i / g8, c = (i % g8) * 8, t = rank * per + r;
       float v[8] = {};
@@ -290,21 +297,36 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
       for (int s = 0; s < NS; ++s) *reinterpret_cast<uint4*>(sm + v_at(t, s * g8 + c / 8)) = o[s];
     }
-    // to the other CTAs and the other copies, 16 bytes at a time
-    named_sync(1, 128);
-    const int pieces = NS * g8, places = C * copies;
-    for (int i = threadIdx.x - 64; i < mine * pieces * places; i += 128) {
-      const int at = i / places, to = i % places, t = rank * per + at / pieces;
-      const uint32_t off = v_at(t, at % pieces);
-      const uint4 v = *reinterpret_cast<const uint4*>(sm + off);
-      if (to != rank) at_store16(mapa_shared(smem_u32(sm) + off + (to / C) * g.tile * 128, to % C), v);
-    }
     at_fence_async();
-    __syncwarp();
+    named_sync(1, 128);
+    if (a.out && warp == 2) {
+      // this CTA's rows to the other CTAs: rows are 128 bytes, one behind the other
+      for (int i = lane; i < atoms * C && mine > 0; i += 32)
+        if (i % C != rank) {
+          const uint32_t from = smem_u32(sm) + (uint32_t)(i / C * kAtXBytes + rank * per * 128);
+          at_send(mapa_shared(from, i % C), from, mine * 128, mapa_shared(smem_u32(vfull), i % C));
+        }
+      if (lane == 0) mbar_arrive(vfull);
+      __syncwarp();
+    }
+    if (a.out && copies > 1) {
+      wait(vfull, 0);
+      __syncwarp();
+      for (int i = threadIdx.x - 64; i < rows * NS * g8; i += 128) {
+        const uint32_t at = v_at(i / (NS * g8), i % (NS * g8));
+        const uint4 v = *reinterpret_cast<const uint4*>(sm + at);
+        for (int n = 1; n < copies; ++n) *reinterpret_cast<uint4*>(sm + at + n * g.tile * 128) = v;
+      }
+      at_fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(vrep);
+    }
+    at_cluster_arrive();
   }
-  cluster_sync();  // v of all rows is there
+  // (a CTA goes when all have their v: until then its shared memory is read)
   // ---- the second product
   if (warp == 0) {
+    at_cluster_arrive();
     if (lane == 0) {
       for (; loaded2 < nt && !*abort_flag; ++loaded2) {
         wait(&empty2[loaded2 % kAtStages2], (loaded2 / kAtStages2 - 1) & 1);
@@ -319,8 +341,14 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && nt > 0) {
+    if (lane == 0 && a.out) {
+      wait(vfull, 0);
+      if (copies > 1) wait(vrep, 0);
       at_fence_async();
+    }
+    __syncwarp();
+    at_cluster_arrive();
+    if (lane == 0 && nt > 0) {
       const uint32_t idesc = idesc_bf16(kAtRows, kAtCols, 0, 1);
       const uint32_t base = smem_u32(sm);
       for (int i = 0; i < nt; ++i) {
@@ -429,7 +457,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kAtTmem);
+    __syncwarp();
   }
+  at_cluster_wait();
   if (g.beside) pdl_wait();
 }
 
@@ -453,7 +483,7 @@ int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, bool beside, int 
   CUtensorMap mx, ma, mb;
   {
     const uint64_t dims[3] = {(uint64_t)a.K, (uint64_t)a.T, 1}, st[2] = {(uint64_t)a.ldx * 2, (uint64_t)a.ldx * 2};
-    const uint32_t box[3] = {64, 32, 1};
+    const uint32_t box[3] = {64, (uint32_t)g.tile, 1};
     if (int rc = encode_tmap_3d_bf16(&mx, a.x, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B)) return rc;
   }
   for (int w = 0; w < 2; ++w) {
