@@ -184,11 +184,9 @@ constexpr int kShortRows = 4;  // sequences of up to so many rows take the row k
 
 static int ad_run(const AdArgs& a, bool f32, cudaStream_t s) {
   if (!a.seq || a.T <= kShortRows) return ad_launch_rows(a, f32, a.T, 0, s);
-  int sms = 0;
-  if (int rc = ad_sms(&sms)) return rc;
-  if (a.n_seq == 1 || a.T >= 64ll * a.n_seq) return ad_launch_tiles(a, f32, 0, false, sms, s);
+  if (a.n_seq == 1 || a.T >= 64ll * a.n_seq) return ad_launch_tiles(a, f32, 0, false, s);
   if (int rc = ad_launch_rows(a, f32, a.n_seq, kShortRows, s)) return rc;
-  return ad_launch_tiles(a, f32, kShortRows, true, sms, s);
+  return ad_launch_tiles(a, f32, kShortRows, true, s);
 }
 
 static bool ad_shape(int T, int K, int N, int R, int L, const int32_t* seq, int n_seq) {
@@ -223,7 +221,7 @@ extern "C" int moe_adapters(const void* x, long long ldx, const void* base, long
 
 extern "C" size_t moe_adapters_grad_workspace_bytes(int T, int R) {
   if (T < 1 || R < 1 || R > kAdMaxR) return 0;
-  return ad256((size_t)T * R * 4);
+  return ad256((size_t)T * R * 4) + (size_t)T * ((R + 15) / 16 * 16) * 12;
 }
 
 extern "C" int moe_adapters_grad(const void* dy, long long ldy, const void* x, long long ldx, const float* kept,
@@ -246,7 +244,8 @@ extern "C" int moe_adapters_grad(const void* dy, long long ldy, const void* x, l
                  dx, dv, dev_status, ldy, dx && base ? ldb : 0, lddx, T, N, K, R, L, n_seq};
   if (int rc = ad_run(g, false, s)) return rc;
   if (!da) return MOE_OK;
-  const AdGradArgs o{(const uint16_t*)x, (const uint16_t*)dy, dv, kept, ids, seq_start, da, db, dev_status, ldx, ldy, T,
+  const AdGradArgs o{(const uint16_t*)x, (const uint16_t*)dy, dv, kept, ids, seq_start, da, db,
+                     (uint16_t*)((char*)workspace + ad256((size_t)T * R * 4)), dev_status, ldx, ldy, T,
                      K, N, R, L, n_seq};
   int sms = 0;
   if (int rc = ad_sms(&sms)) return rc;

@@ -44,7 +44,7 @@ __device__ __forceinline__ int ad_sequence(const AdArgs& a, int t) {
 }
 
 // The sequences of more than short_rows rows (and the rows of none), by tiles.
-int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, bool beside, int sms, cudaStream_t s);
+int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, bool beside, cudaStream_t s);
 
 // v as a sum of NS bf16 numbers, eight values at once (packed pairs): truncation leaves an exact rest, so three of them
 // are all 24 bits; the last of two is rounded.  A rest of an infinity or a NaN counts as 0.
@@ -80,6 +80,7 @@ struct AdGradArgs {
   const int32_t* seq;
   float* da;           // [L][R][K]
   float* db;           // [L][R][N]
+  uint16_t* parts;     // bf16 [2][T][3 Rk]: dv and v as three numbers each (workspace)
   int32_t* status;
   long long ldx, ldy;
   int T, K, N, R, L, n_seq;

@@ -2,10 +2,11 @@
 // sequences with adapter l, in one launch.
 //
 // Longer sequences: tcgen05.  D [128 features][R] of one adapter and one block of 128 features of x or dy, summed over
-// tiles of 64 rows: x by TMA as it lies (features run along, so it is MN-major), v MN-major too, written by four warps
-// that split its fp32 values into three bf16 numbers (24 bits, nothing is rounded); the three stand next to each other
-// as columns of one product and are added in the end.  The tensor cores truncate what they add, so that an error grows
-// with every step in one direction: after four tiles the sums are taken over into shared memory by additions that round.
+// tiles of 64 rows by TMA as they lie (features run along, so x is MN-major, and v is too).  A kernel before writes each
+// fp32 value of v and dv as three bf16 numbers (24 bits, nothing is rounded) next to each other, as columns of one
+// product that are added in the end: done in the product's kernel by its own warps, once for every block of features, it
+// took three times as long as the product.  The tensor cores truncate what they add, so that an error grows with every
+// step in one direction: after four tiles the sums are taken over into shared memory by additions that round.
 // A cluster of CTAs divides the rows of an adapter where blocks are few; their sums meet in distributed shared memory in
 // a fixed order.  x and dy are read once, which is what bounds it.  Many short sequences: a thread per two features, on the CUDA cores (the tiles would be mostly empty).
 #include <algorithm>
@@ -15,7 +16,7 @@
 
 namespace moe {
 
-constexpr int kAoThreads = 192;  // TMA warp, MMA warp, four warps that split v and write the result
+constexpr int kAoThreads = 192;  // TMA warp, MMA warp, four warps that take the sums over
 constexpr int kAoFeat = 128;     // features of a block (MMA M)
 constexpr int kAoRows = 64;      // rows of a tile
 constexpr int kAoXBytes = kAoRows * kAoFeat * 2;
@@ -76,19 +77,49 @@ __device__ __forceinline__ float ao_remote(const float* p, uint32_t rank) {
   return v;
 }
 
+// dv and v as three bf16 numbers each: [row][first | second | third part][Rk]; a thread has 8 ranks of a row.
+constexpr int kApThreads = 256;
+__global__ void __launch_bounds__(kApThreads) adapters_parts_kernel(const AdGradArgs a, int Rk) {
+  pdl_wait();
+  pdl_trigger();
+  const int g8 = Rk / 8;
+  const long long units = (long long)a.T * g8;
+  const bool vec = a.R % 4 == 0;
+  for (long long i = (long long)blockIdx.x * kApThreads + threadIdx.x; i < 2 * units; i += (long long)gridDim.x * kApThreads) {
+    const int which = i >= units;
+    const long long u = i - which * units, t = u / g8;
+    const int c = (int)(u - t * g8) * 8;
+    const float* p = (which ? a.v : a.dv) + t * a.R + c;
+    float v[8] = {};
+    if (vec && c + 8 <= a.R) {
+      const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j < a.R) v[j] = p[j];
+    }
+    uint4 o[3];
+    ad_split8<3>(v, o);
+    uint16_t* q = a.parts + ((size_t)which * a.T + t) * (3 * Rk) + c;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(q + k * Rk) = o[k];
+  }
+}
+
 __global__ void __launch_bounds__(kAoThreads)
     adapters_outer_tile_kernel(const AdGradArgs a, const AoGeo g, const __grid_constant__ CUtensorMap mapX,
-                               const __grid_constant__ CUtensorMap mapY) {
+                               const __grid_constant__ CUtensorMap mapY, const __grid_constant__ CUtensorMap mapV) {
   extern __shared__ __align__(1024) unsigned char sm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), S = g.S;
   const int block = blockIdx.x / S, l = blockIdx.y;
   const bool first = block < g.blocks_a;
   const int F = first ? a.K : a.N, f0 = (block - (first ? 0 : g.blocks_a)) * kAoFeat;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + g.off_bar);  // x has landed
-  uint64_t* ready = full + 8;                                    // v is written
-  uint64_t* empty = ready + 8;
-  uint64_t* tfull = empty + 8;   // an accumulator's tiles are done
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + g.off_bar);  // x and v have landed
+  uint64_t* clean = full + 4;                                    // rows of others are zeroed
+  uint64_t* empty = clean + 4;
+  uint64_t* tfull = empty + 4;   // an accumulator's tiles are done
   uint64_t* tempty = tfull + 2;  // and taken over
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tempty + 2);
   int* s_total = reinterpret_cast<int*>(s_tmem + 1);
@@ -97,7 +128,8 @@ __global__ void __launch_bounds__(kAoThreads)
   const int stage = kAoXBytes + g.atoms * kAoAtom;
   if (threadIdx.x == 0) {
     prefetch_tmap(first ? &mapX : &mapY);
-    for (int i = 0; i < g.stages; ++i) mbar_init(&full[i], 1), mbar_init(&ready[i], 1), mbar_init(&empty[i], 1);
+    prefetch_tmap(&mapV);
+    for (int i = 0; i < g.stages; ++i) mbar_init(&full[i], 1), mbar_init(&clean[i], 1), mbar_init(&empty[i], 1);
     for (int i = 0; i < g.acc; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 4);
     *abort_flag = 0;
     *s_total = 0;
@@ -141,9 +173,11 @@ __global__ void __launch_bounds__(kAoThreads)
         if (use > 0) wait(&empty[s], (use - 1) & 1);
         if (!*abort_flag) {
           unsigned char* st = sm + s * stage;
-          mbar_expect_tx(&full[s], kAoXBytes);
+          mbar_expect_tx(&full[s], (uint32_t)stage);
           tma_load_3d(st, first ? &mapX : &mapY, &full[s], f0, row0, 0);
           tma_load_3d(st + kAoAtom, first ? &mapX : &mapY, &full[s], f0 + 64, row0, 0);
+          for (int n = 0; n < g.atoms; ++n)
+            tma_load_3d(st + kAoXBytes + n * kAoAtom, &mapV, &full[s], n * 64, row0, first ? 0 : 1);
           issued = i + 1;
         }
       }
@@ -157,13 +191,17 @@ __global__ void __launch_bounds__(kAoThreads)
     const int cols = 3 * g.Rk, n1 = cols <= 256 ? cols : 192;
     const uint32_t id1 = idesc_bf16(kAoFeat, n1, 1, 1), id2 = idesc_bf16(kAoFeat, max(cols - n1, 16), 1, 1);
     const uint32_t base = smem_u32(sm);
+    uint32_t cleaned = 0;  // parity of a slot's `clean`
     for (int i = 0; tiles.next(row0, rows); ++i) {
       if (lane == 0) {
         const int s = i % g.stages, use = i / g.stages;
         const int j = i / kAoDrain, b = j % g.acc;
         if (i % kAoDrain == 0 && j >= g.acc) wait(&tempty[b], (j / g.acc - 1) & 1);
         wait(&full[s], use & 1);
-        wait(&ready[s], use & 1);
+        if (rows % 16) {
+          wait(&clean[s], (cleaned >> s) & 1);
+          cleaned ^= 1u << s;
+        }
         tc_fence_after();
         if (!*abort_flag) {
           const uint32_t d = tmem + b * cols;
@@ -181,13 +219,6 @@ __global__ void __launch_bounds__(kAoThreads)
       __syncwarp();
     }
   } else {
-    // split v: each slot of the ring has a warp of its own (which is never more than one use of its slot ahead);
-    // unit = (row, 8 ranks); 3 x 16 bytes of the tile's columns [first | second | third part].  A batch of loads is on
-    // its way while the slot is waited for.
-    constexpr int U = 8;
-    const float* src = first ? a.dv : a.v;
-    const int g8 = g.Rk / 8;
-    const bool vec = a.R % 4 == 0;
     const int q = warp & 3, f = q * 32 + lane;  // of the sums: lane = feature
     int drained = 0;
     auto drain = [&] {  // the parts of a rank are Rk columns apart
@@ -215,55 +246,19 @@ __global__ void __launch_bounds__(kAoThreads)
     };
     for (int i = 0; tiles.next(row0, rows); ++i) {
       const int s = i % g.stages, use = i / g.stages;
-      if (s == warp - 2) {
-        unsigned char* vs = sm + s * stage + kAoXBytes;
-        const int rows16 = (rows + 15) & ~15, units = rows16 * g8;
-        for (int u0 = lane; u0 - lane < units; u0 += 32 * U) {
-          float v[U][8];
-#pragma unroll
-          for (int k = 0; k < U; ++k) {
-            const int u = u0 + 32 * k, r = u / g8, c = (u % g8) * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[k][j] = 0.f;
-            if (r < rows) {
-              const float* p = src + (size_t)(row0 + r) * a.R + c;
-              if (vec && c + 8 <= a.R) {
-                const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
-                v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
-                v[k][4] = y.x, v[k][5] = y.y, v[k][6] = y.z, v[k][7] = y.w;
-              } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  if (c + j < a.R) v[k][j] = p[j];
-              }
-            }
-          }
-          if (u0 == lane && use > 0) wait(&empty[s], (use - 1) & 1);
-#pragma unroll
-          for (int k = 0; k < U; ++k) {
-            const int u = u0 + 32 * k, r = u / g8, c = (u % g8) * 8;
-            uint4 o[3];
-            ad_split8<3>(v[k], o);
-            if (u < units) {
-#pragma unroll
-              for (int h = 0; h < 3; ++h) {
-                const int n = h * g.Rk + c;
-                *reinterpret_cast<uint4*>(vs + (n / 64) * kAoAtom + r * 128 + (((n % 64) / 8) ^ (r & 7)) * 16) = o[h];
-              }
-            }
-          }
+      // the rest of the last 16 rows belongs to others, whatever it is: each slot has a warp that clears it (and waits
+      // for every use of its slot, so that it is never a phase behind)
+      if (s == warp - 2) wait(&full[s], use & 1);
+      __syncwarp();
+      if (s == warp - 2 && rows % 16) {
+        const int rest = 16 - rows % 16, pieces = (2 + g.atoms) * 8;
+        for (int u = lane; u < rest * pieces; u += 32) {
+          const int r = rows + u / pieces, p = u % pieces;
+          *reinterpret_cast<uint4*>(sm + s * stage + (p / 8) * kAoAtom + r * 128 + (p % 8) * 16) = make_uint4(0, 0, 0, 0);
         }
-        if (rows16 != rows) {
-          // the rest of the last 16 rows belongs to others, whatever it is
-          wait(&full[s], use & 1);
-          for (int u = lane; u < (rows16 - rows) * 16; u += 32) {
-            const int r = rows + u / 16, p = u % 16;
-            *reinterpret_cast<uint4*>(sm + s * stage + (p / 8) * kAoAtom + r * 128 + (p % 8) * 16) = make_uint4(0, 0, 0, 0);
-          }
-        }
-        asm volatile("fence.proxy.async;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ready[s]);
+        if (lane == 0) mbar_arrive(&clean[s]);
       }
       // with two accumulators the one before last's sums are taken over while the products of the last one run
       if (i % kAoDrain == kAoDrain - 1 && i / kAoDrain >= g.acc - 1) drain();
@@ -363,7 +358,7 @@ int ad_launch_outer(const AdGradArgs& a, int sms, cudaStream_t s) {
   g.tmem = 32;
   while (g.tmem < g.acc * 3 * g.Rk) g.tmem *= 2;
   const int stage = kAoXBytes + g.atoms * kAoAtom;
-  // two CTAs a SM up to 32 ranks, else one; a slot for each of the four warps that split v at most
+  // two CTAs a SM up to 32 ranks, else one; a slot for each of the four warps that clear rows at most
   g.stages = std::min(4, ((g.Rk <= 32 ? 112 : 224) * 1024 - g.Rk * kAoFeat * 4) / stage);
   g.off_part = g.stages * stage;
   g.off_bar = g.off_part + g.Rk * kAoFeat * 4;
@@ -374,13 +369,22 @@ int ad_launch_outer(const AdGradArgs& a, int sms, cudaStream_t s) {
   const long long busy = (long long)blocks * std::min(a.L, a.n_seq);
   g.S = 1;
   while (g.S < 8 && busy * g.S * 2 <= 2ll * sms && a.T >= 128 * g.S) g.S *= 2;
-  CUtensorMap mx, my;
+  CUtensorMap mx, my, mv;
   for (int w = 0; w < 2; ++w) {
     const uint64_t ld = (uint64_t)(w ? a.ldy : a.ldx) * 2;
     const uint64_t dims[3] = {(uint64_t)(w ? a.N : a.K), (uint64_t)a.T, 1}, st[2] = {ld, ld};
     const uint32_t box[3] = {64, kAoRows, 1};
     if (int rc = encode_tmap_3d_bf16(w ? &my : &mx, w ? a.dy : a.x, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B)) return rc;
   }
+  {
+    const uint64_t ld = (uint64_t)g.Rk * 6;
+    const uint64_t dims[3] = {(uint64_t)g.Rk * 3, (uint64_t)a.T, 2}, st[2] = {ld, ld * a.T};
+    const uint32_t box[3] = {64, kAoRows, 1};
+    if (int rc = encode_tmap_3d_bf16(&mv, a.parts, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B)) return rc;
+  }
+  const long long units = 2ll * a.T * (g.Rk / 8);
+  MOE_CUDA_TRY(launch_pdl(adapters_parts_kernel, dim3((unsigned)std::min<long long>((units + kApThreads - 1) / kApThreads, 8ll * sms)),
+                          dim3(kApThreads), 0, s, a, g.Rk));
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = g.S;
@@ -397,7 +401,7 @@ int ad_launch_outer(const AdGradArgs& a, int sms, cudaStream_t s) {
   cfg.numAttrs = 2;
   static bool done[64] = {};
   MOE_CUDA_TRY(ensure_smem(adapters_outer_tile_kernel, 227 * 1024 - 512, done));
-  MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, adapters_outer_tile_kernel, a, g, mx, my));
+  MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, adapters_outer_tile_kernel, a, g, mx, my, mv));
   return MOE_OK;
 }
 

@@ -20,7 +20,6 @@
 namespace moe {
 
 constexpr int kAtThreads = 192;  // TMA warp, MMA warp, four epilogue warps
-constexpr int kAtCluster = 8;
 constexpr int kAtRows = 128;     // rows of a tile, at most (MMA M)
 constexpr int kAtCols = 128;     // outputs of a step of the second product
 constexpr uint32_t kAtTmem = 256;
@@ -97,11 +96,11 @@ __device__ void at_find(const AdArgs& a, const AtGeo& g, int ti, int* tmp, int* 
 // Where 16-byte piece i of the partial sums lies: rows a power of two apart meet no bank twice.
 __device__ __forceinline__ uint32_t at_piece(uint32_t i) { return (i ^ ((i >> 3) & 7)) * 16; }
 
-template <bool F32>
-__global__ void __launch_bounds__(kAtThreads, 1)
+template <bool F32, int C>
+__global__ void __launch_bounds__(kAtThreads, 2)
     adapters_tile_kernel(const AdArgs a, const AtGeo g, const __grid_constant__ CUtensorMap mapX,
                          const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB) {
-  constexpr int NS = F32 ? 3 : 2, C = kAtCluster;
+  constexpr int NS = F32 ? 3 : 2;
   constexpr int kSize = F32 ? 4 : 2;
   extern __shared__ __align__(1024) unsigned char sm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -463,13 +462,52 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   if (g.beside) pdl_wait();
 }
 
-int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, bool beside, int sms, cudaStream_t s) {
+template <bool F32, int C>
+static int at_launch(const AdArgs& a, const AtGeo& g, int bytes, const CUtensorMap& mx, const CUtensorMap& ma,
+                     const CUtensorMap& mb, cudaStream_t s) {
+  const long long tiles = std::min<long long>(a.T, a.T / g.tile + a.n_seq + 2ll);
+  if (tiles * C > 0x7fffffffll) return MOE_ERR_ARG;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = C;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * C));
+  cfg.blockDim = dim3(kAtThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  static bool done[64] = {};
+  constexpr int kMost = 227 * 1024 - 512;
+  if (bytes > kMost) return MOE_ERR_ARG;
+  MOE_CUDA_TRY(ensure_smem(adapters_tile_kernel<F32, C>, kMost, done));
+  MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, adapters_tile_kernel<F32, C>, a, g, mx, ma, mb));
+  return MOE_OK;
+}
+
+int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, bool beside, cudaStream_t s) {
   AtGeo g = {};
   const int NS = f32 ? 3 : 2;
   g.Rk = (a.R + 15) / 16 * 16;
-  // rows of a tile: fewer where that gives the SMs something to do
-  g.tile = kAtRows;
-  while (g.tile > 32 && ((long long)a.T / g.tile + 1) * kAtCluster <= sms) g.tile /= 2;
+  // CTAs of a cluster and rows of a tile, by an estimate of the time: a CTA takes 9 us and its share of the tile's bytes
+  // at 22 KB/us (44 where it has an SM to itself); 30 clusters of 8 CTAs, 72 of 4 or 152 of 2 run at once (half of them,
+  // one CTA a SM).  Measured: 4096 rows of R 64 (2048 x 4096) 31.0 us with 8 and 128, 31.5 with 4 and 64, 38 with 2 and
+  // 32; 16,384 of R 16 (2048 x 2048) 66 with 8 and 128, 56 with 4, 52 with 2; 1024 of R 16 16.8 with 8 and 128, 13.6 with
+  // 8 and 32; 2000 of R 128 (4096 x 4096) 34 with 4 and 64, 48 with 8 and 128.
+  int C = 8;
+  double best = 0.;
+  for (int c = 2; c <= 8; c *= 2)
+    for (int tile = 32; tile <= kAtRows; tile *= 2) {
+      if (g.Rk > 64 && f32 && tile > 64) continue;
+      const double bytes = (tile * (2. * a.K + (f32 ? 4. : 2.) * (a.base ? 2 : 1) * (a.out ? a.N : 0)) + 2. * a.R * ((double)a.K + a.N)) / c;
+      const int most = (c == 8 ? 240 : c == 4 ? 288 : 304) / (g.Rk > 64 ? 2 : 1);
+      const double t = (9. + bytes / (g.Rk > 64 ? 44e3 : 22e3)) * std::max(1., ((double)a.T / tile + 1.) * c / most);
+      if (best == 0. || t < best) best = t, C = c, g.tile = tile;
+    }
   g.short_rows = short_rows;
   g.beside = beside;
   const int stage1 = kAtXBytes + g.Rk * 128;
@@ -492,33 +530,9 @@ int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, bool beside, int 
     const uint32_t box[3] = {64, (uint32_t)g.Rk, 1};
     if (int rc = encode_tmap_3d_bf16(w ? &mb : &ma, w ? a.w2 : a.w1, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B)) return rc;
   }
-  const long long tiles = std::min<long long>(a.T, a.T / g.tile + a.n_seq + 2ll);
-  if (tiles * kAtCluster > 0x7fffffffll) return MOE_ERR_ARG;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = kAtCluster;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * kAtCluster));
-  cfg.blockDim = dim3(kAtThreads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 2;
-  static bool d0[64] = {}, d1[64] = {};
-  constexpr int kMost = 227 * 1024 - 512;
-  if (bytes > kMost) return MOE_ERR_ARG;
-  if (f32) {
-    MOE_CUDA_TRY(ensure_smem(adapters_tile_kernel<true>, kMost, d1));
-    MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, adapters_tile_kernel<true>, a, g, mx, ma, mb));
-  } else {
-    MOE_CUDA_TRY(ensure_smem(adapters_tile_kernel<false>, kMost, d0));
-    MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, adapters_tile_kernel<false>, a, g, mx, ma, mb));
-  }
-  return MOE_OK;
+  if (C == 8) return f32 ? at_launch<true, 8>(a, g, bytes, mx, ma, mb, s) : at_launch<false, 8>(a, g, bytes, mx, ma, mb, s);
+  if (C == 2) return f32 ? at_launch<true, 2>(a, g, bytes, mx, ma, mb, s) : at_launch<false, 2>(a, g, bytes, mx, ma, mb, s);
+  return f32 ? at_launch<true, 4>(a, g, bytes, mx, ma, mb, s) : at_launch<false, 4>(a, g, bytes, mx, ma, mb, s);
 }
 
 }  // namespace moe
