@@ -2,6 +2,7 @@
 #pragma once
 
 #include "internal.cuh"
+#include "tc05.cuh"
 
 namespace moe {
 
@@ -69,6 +70,17 @@ __device__ __forceinline__ void ad_split8(const float (&v)[8], uint4 (&o)[NS]) {
   }
 #pragma unroll
   for (int s = 0; s < NS; ++s) o[s] = make_uint4(w[s][0], w[s][1], w[s][2], w[s][3]);
+}
+
+// Bounded wait of a whole warp; false after a timeout, its own (flagged) or another warp's.
+__device__ __forceinline__ bool ad_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+  for (int i = 0; i < kWaitPolls; ++i) {
+    if (__all_sync(MOE_FULL_MASK, mbar_try_wait(bar, parity))) return true;
+    if ((i & 255) == 255 && __any_sync(MOE_FULL_MASK, *abort_flag)) return false;
+  }
+  *abort_flag = 1;
+  set_status(status, MOE_DEV_TIMEOUT);
+  return false;
 }
 
 struct AdGradArgs {

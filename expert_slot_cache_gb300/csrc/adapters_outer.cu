@@ -12,7 +12,6 @@
 #include <algorithm>
 
 #include "adapters.cuh"
-#include "tc05.cuh"
 
 namespace moe {
 
@@ -71,9 +70,11 @@ struct AoTiles {
   }
 };
 
-__device__ __forceinline__ float ao_remote(const float* p, uint32_t rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(p), rank)));
+__device__ __forceinline__ float4 ao_remote(const float* p, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(mapa_shared(smem_u32(p), rank)));
   return v;
 }
 
@@ -158,65 +159,76 @@ __global__ void __launch_bounds__(kAoThreads)
   const int total = *s_total;
   AoTiles tiles{a, l, (int)((long long)total * rank / S), (int)((long long)total * (rank + 1) / S)};
   const int nt = tiles.hi - tiles.lo;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {  // bounded; nothing is waited for after a timeout
-    if (!*abort_flag && !mbar_wait(bar, parity)) {
-      *abort_flag = 1;
-      set_status(a.status, MOE_DEV_TIMEOUT);
-    }
+  bool dead = false;  // (of a whole warp) nothing is waited for or issued after a timeout
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!dead) dead = !ad_wait(bar, parity, abort_flag, a.status);
   };
   int row0 = 0, rows = 0;
+  // The loops that issue copies and products are run by whole warps, so that their operands stay in uniform registers.
   if (warp == 0) {
-    int issued = 0;
-    for (int i = 0; tiles.next(row0, rows); ++i) {
-      if (lane == 0) {
-        const int s = i % g.stages, use = i / g.stages;
-        if (use > 0) wait(&empty[s], (use - 1) & 1);
-        if (!*abort_flag) {
-          unsigned char* st = sm + s * stage;
-          mbar_expect_tx(&full[s], (uint32_t)stage);
-          tma_load_3d(st, first ? &mapX : &mapY, &full[s], f0, row0, 0);
-          tma_load_3d(st + kAoAtom, first ? &mapX : &mapY, &full[s], f0 + 64, row0, 0);
-          for (int n = 0; n < g.atoms; ++n)
-            tma_load_3d(st + kAoXBytes + n * kAoAtom, &mapV, &full[s], n * 64, row0, first ? 0 : 1);
-          issued = i + 1;
-        }
+    const bool lead = elect_one();
+    const CUtensorMap* map = first ? &mapX : &mapY;
+    int s = 0, issued = 0;
+    uint32_t ph = 1;
+    while (tiles.next(row0, rows) && !dead) {
+      if (issued >= g.stages) wait(&empty[s], ph);
+      if (lead && !dead) {
+        unsigned char* st = sm + s * stage;
+        mbar_expect_tx(&full[s], (uint32_t)stage);
+        tma_load_3d(st, map, &full[s], f0, row0, 0);
+        tma_load_3d(st + kAoAtom, map, &full[s], f0 + 64, row0, 0);
+        for (int n = 0; n < g.atoms; ++n)
+          tma_load_3d(st + kAoXBytes + n * kAoAtom, &mapV, &full[s], n * 64, row0, first ? 0 : 1);
       }
       __syncwarp();
+      issued += !dead;
+      if (++s == g.stages) s = 0, ph ^= 1;
     }
     // after a timeout every copy lands before the CTA may go
-    if (lane == 0 && *abort_flag)
-      for (int s = 0; s < g.stages && s < issued; ++s) mbar_wait(&full[s], ((issued - 1 - s) / g.stages) & 1);
+    if (dead || *abort_flag)
+      for (int j = max(0, issued - g.stages); j < issued; ++j) mbar_wait(&full[j % g.stages], (j / g.stages) & 1);
     __syncwarp();
   } else if (warp == 1) {
+    const bool lead = elect_one();
     const int cols = 3 * g.Rk, n1 = cols <= 256 ? cols : 192;
     const uint32_t id1 = idesc_bf16(kAoFeat, n1, 1, 1), id2 = idesc_bf16(kAoFeat, max(cols - n1, 16), 1, 1);
-    const uint32_t base = smem_u32(sm);
-    uint32_t cleaned = 0;  // parity of a slot's `clean`
+    const uint64_t a0 = smem_desc_l(smem_u32(sm), kAoAtom, 1024, kLayoutSw128);
+    const uint64_t b0 = smem_desc_l(smem_u32(sm) + kAoXBytes, kAoAtom, 1024, kLayoutSw128);
+    constexpr uint32_t kStep = 2048 >> 4;  // 16 rows
+    int s = 0, n = 0, b = 0;  // slot; tile of the accumulator; accumulator
+    uint32_t ph = 0, tph = 1, cleaned = 0;  // phases of slots and accumulators; of a slot's `clean`
     for (int i = 0; tiles.next(row0, rows); ++i) {
-      if (lane == 0) {
-        const int s = i % g.stages, use = i / g.stages;
-        const int j = i / kAoDrain, b = j % g.acc;
-        if (i % kAoDrain == 0 && j >= g.acc) wait(&tempty[b], (j / g.acc - 1) & 1);
-        wait(&full[s], use & 1);
-        if (rows % 16) {
-          wait(&clean[s], (cleaned >> s) & 1);
-          cleaned ^= 1u << s;
-        }
-        tc_fence_after();
-        if (!*abort_flag) {
-          const uint32_t d = tmem + b * cols;
-          const uint64_t ad = smem_desc_l(base + s * stage, kAoAtom, 1024, kLayoutSw128);
-          const uint64_t bd = smem_desc_l(base + s * stage + kAoXBytes, kAoAtom, 1024, kLayoutSw128);
-          for (int k = 0; k * 16 < rows; ++k) {  // 16 rows at a time
-            const uint32_t on = i % kAoDrain + k != 0;
-            umma_f16(d, ad + k * (2048 >> 4), bd + k * (2048 >> 4), id1, on);
-            if (cols > n1) umma_f16(d + n1, ad + k * (2048 >> 4), bd + (3 * kAoAtom >> 4) + k * (2048 >> 4), id2, on);
+      if (n == 0 && i >= kAoDrain * g.acc) wait(&tempty[b], tph);
+      wait(&full[s], ph);
+      if (rows % 16) {
+        wait(&clean[s], (cleaned >> s) & 1);
+        cleaned ^= 1u << s;
+      }
+      tc_fence_after();
+      const bool last = ++n == kAoDrain || i == nt - 1;
+      if (lead && !dead) {
+        const uint32_t d = tmem + b * cols;
+        const uint64_t ad = a0 + (uint64_t)(s * (stage >> 4)), bd = b0 + (uint64_t)(s * (stage >> 4));
+        if (rows > 48) {
+          umma_f16_k64(d, ad, bd, id1, n > 1, kStep, kStep);
+          if (cols > n1) umma_f16_k64(d + n1, ad, bd + (3 * kAoAtom >> 4), id2, n > 1, kStep, kStep);
+        } else {
+          for (int k = 0; k * 16 < rows; ++k) {
+            umma_f16(d, ad + k * kStep, bd + k * kStep, id1, n > 1 || k);
+            if (cols > n1) umma_f16(d + n1, ad + k * kStep, bd + (3 * kAoAtom >> 4) + k * kStep, id2, n > 1 || k);
           }
         }
+      }
+      if (lead) {
         umma_commit(&empty[s]);
-        if (i % kAoDrain == kAoDrain - 1 || i == nt - 1) umma_commit(&tfull[b]);
+        if (last) umma_commit(&tfull[b]);
       }
       __syncwarp();
+      if (++s == g.stages) s = 0, ph ^= 1;
+      if (last) {
+        n = 0;
+        if (++b == g.acc) b = 0, tph ^= 1;
+      }
     }
   } else {
     const int q = warp & 3, f = q * 32 + lane;  // of the sums: lane = feature
@@ -224,7 +236,6 @@ __global__ void __launch_bounds__(kAoThreads)
     auto drain = [&] {  // the parts of a rank are Rk columns apart
       const int j = drained++, b = j % g.acc;
       wait(&tfull[b], (j / g.acc) & 1);
-      __syncwarp();
       tc_fence_after();
       for (int c = 0; c < g.Rk; c += 16) {
         float v[16], w[16], x[16];
@@ -249,7 +260,6 @@ __global__ void __launch_bounds__(kAoThreads)
       // the rest of the last 16 rows belongs to others, whatever it is: each slot has a warp that clears it (and waits
       // for every use of its slot, so that it is never a phase behind)
       if (s == warp - 2) wait(&full[s], use & 1);
-      __syncwarp();
       if (s == warp - 2 && rows % 16) {
         const int rest = 16 - rows % 16, pieces = (2 + g.atoms) * 8;
         for (int u = lane; u < rest * pieces; u += 32) {
@@ -273,11 +283,14 @@ __global__ void __launch_bounds__(kAoThreads)
   {
     const int r0 = a.R * rank / S, r1 = a.R * (rank + 1) / S;
     float* out = (first ? a.da : a.db) + (size_t)l * a.R * F + f0;
-    for (int i = threadIdx.x; i < (r1 - r0) * kAoFeat; i += kAoThreads) {
-      const int r = r0 + i / kAoFeat, f = i % kAoFeat;
-      float v = 0.f;
-      for (int p = 0; p < S; ++p) v += ao_remote(part + r * kAoFeat + f, p);
-      if (f0 + f < F) out[(size_t)r * F + f] = v;
+    for (int i = threadIdx.x; i < (r1 - r0) * (kAoFeat / 4); i += kAoThreads) {
+      const int r = r0 + i / (kAoFeat / 4), f = i % (kAoFeat / 4) * 4;
+      float4 p[8], v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) p[c] = c < S ? ao_remote(part + r * kAoFeat + f, c) : v;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v.x += p[c].x, v.y += p[c].y, v.z += p[c].z, v.w += p[c].w;
+      if (f0 + f < F) *reinterpret_cast<float4*>(out + (size_t)r * F + f) = v;
     }
     __syncwarp();
   }

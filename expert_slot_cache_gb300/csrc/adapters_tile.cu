@@ -15,7 +15,6 @@
 #include <algorithm>
 
 #include "adapters.cuh"
-#include "tc05.cuh"
 
 namespace moe {
 
@@ -178,11 +177,9 @@ __global__ void __launch_bounds__(kAtThreads, 2)
                    : "memory");
     }
   }
-  auto wait = [&](uint64_t* bar, uint32_t parity) {  // bounded; nothing is waited for after a timeout
-    if (!*abort_flag && !mbar_wait(bar, parity)) {
-      *abort_flag = 1;
-      set_status(a.status, MOE_DEV_TIMEOUT);
-    }
+  bool dead = false;  // (of a whole warp) nothing is waited for or issued after a timeout
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!dead) dead = !ad_wait(bar, parity, abort_flag, a.status);
   };
   const int kc = (a.K + 63) / 64, kc0 = kc * rank / C, kc1 = kc * (rank + 1) / C, nk = kc1 - kc0;
   const int nacc = min(min((nk + 3) / 4, kAtAcc), (int)kAtTmem / g.Rk);  // accumulators of D1, taken in turn
@@ -190,48 +187,56 @@ __global__ void __launch_bounds__(kAtThreads, 2)
   const int per = g.tile / C;                             // rows that a CTA adds up
   const int mine = max(0, min(per, rows - rank * per));
   const int atoms = (NS * g.Rk + 63) / 64;                // of v: 128 lanes x 128 bytes
-  int loaded2 = 0;
-  auto load2 = [&](int i) {  // step i of the second product
-    unsigned char* st = ring2 + (i % kAtStages2) * stage2;
-    uint64_t* bar = &full2[i % kAtStages2];
-    mbar_expect_tx(bar, (uint32_t)stage2);
-    tma_load_3d(st, &mapB, bar, (nt0 + i) * kAtCols, 0, l);
-    tma_load_3d(st + g.Rk * 128, &mapB, bar, (nt0 + i) * kAtCols + 64, 0, l);
+  // ---- the first product.  The loops that issue copies and products are run by whole warps, so that their operands
+  // stay in uniform registers.
+  const bool lead = elect_one();
+  int loaded1 = 0, loaded2 = 0;
+  auto load2 = [&] {  // the next step of the second product
+    const int i = loaded2 % kAtStages2;
+    if (lead) {
+      unsigned char* st = ring2 + i * stage2;
+      mbar_expect_tx(&full2[i], (uint32_t)stage2);
+      tma_load_3d(st, &mapB, &full2[i], (nt0 + loaded2) * kAtCols, 0, l);
+      tma_load_3d(st + g.Rk * 128, &mapB, &full2[i], (nt0 + loaded2) * kAtCols + 64, 0, l);
+    }
+    __syncwarp();
+    ++loaded2;
   };
-  // ---- the first product
   if (warp == 0) {
-    if (lane == 0) {
-      for (int i = 0; i < nk && !*abort_flag; ++i) {
-        const int s = i % g.stages1, use = i / g.stages1;
-        if (use > 0) wait(&empty1[s], (use - 1) & 1);
-        if (*abort_flag) break;
+    int s = 0;
+    uint32_t ph = 1;
+    for (int i = 0; i < nk && !dead; ++i) {
+      if (i >= g.stages1) wait(&empty1[s], ph);
+      if (dead) break;
+      if (lead) {
         unsigned char* st = sm + s * stage1;
         mbar_expect_tx(&full1[s], (uint32_t)(g.tile + g.Rk) * 128);
         tma_load_3d(st, &mapX, &full1[s], (kc0 + i) * 64, row0, 0);
         tma_load_3d(st + kAtXBytes, &mapA, &full1[s], (kc0 + i) * 64, 0, l);
       }
-      for (; loaded2 < min(nt, kAtStages2) && !*abort_flag; ++loaded2) load2(loaded2);
-      mbar_expect_tx(vfull, (uint32_t)(atoms * 128 * (rows - mine)));
+      __syncwarp();
+      ++loaded1;
+      if (++s == g.stages1) s = 0, ph ^= 1;
     }
+    while (loaded2 < min(nt, kAtStages2) && !dead) load2();
+    if (lead) mbar_expect_tx(vfull, (uint32_t)(atoms * 128 * (rows - mine)));
     __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0 && nk > 0) {
-      const uint32_t idesc = idesc_bf16(kAtRows, g.Rk, 0, 0);
-      const uint32_t base = smem_u32(sm);
-      for (int i = 0; i < nk; ++i) {
-        const int s = i % g.stages1, use = i / g.stages1;
-        wait(&full1[s], use & 1);
-        tc_fence_after();
-        if (!*abort_flag) {
-          const uint64_t ad = at_desc(base + s * stage1, 16, 1024), bd = at_desc(base + s * stage1 + kAtXBytes, 16, 1024);
-          const uint32_t d = tmem + (i % nacc) * g.Rk;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) umma_f16(d, ad + 2 * q, bd + 2 * q, idesc, q != 0 || i >= nacc);
-        }
-        umma_commit(&empty1[s]);
-      }
-      umma_commit(d1full);
+  } else if (warp == 1 && nk > 0) {
+    const uint32_t idesc = idesc_bf16(kAtRows, g.Rk, 0, 0);
+    const uint64_t a0 = at_desc(smem_u32(sm), 16, 1024), b0 = at_desc(smem_u32(sm) + kAtXBytes, 16, 1024);
+    int s = 0, n = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < nk; ++i) {
+      wait(&full1[s], ph);
+      tc_fence_after();
+      const uint64_t at = (uint64_t)(s * (stage1 >> 4));
+      if (lead && !dead) umma_f16_k64(tmem + n * g.Rk, a0 + at, b0 + at, idesc, i >= nacc, 2, 2);
+      if (lead) umma_commit(&empty1[s]);
+      __syncwarp();
+      if (++s == g.stages1) s = 0, ph ^= 1;
+      if (++n == nacc) n = 0;
     }
+    if (lead) umma_commit(d1full);
     __syncwarp();
   }
   const int q = warp & 3, row = (q * 32 + lane) % g.tile, copy = q * 32 / g.tile;
@@ -241,7 +246,6 @@ __global__ void __launch_bounds__(kAtThreads, 2)
     scale = a.scale[l];
     if (nk > 0) {
       wait(d1full, 0);
-      __syncwarp();
       tc_fence_after();
     }
     const uint32_t dst = mapa_shared(smem_u32(part), (uint32_t)(row / per));
@@ -310,7 +314,6 @@ __global__ void __launch_bounds__(kAtThreads, 2)
     }
     if (a.out && copies > 1) {
       wait(vfull, 0);
-      __syncwarp();
       for (int i = threadIdx.x - 64; i < rows * NS * g8; i += 128) {
         const uint32_t at = v_at(i / (NS * g8), i % (NS * g8));
         const uint4 v = *reinterpret_cast<const uint4*>(sm + at);
@@ -326,47 +329,46 @@ __global__ void __launch_bounds__(kAtThreads, 2)
   // ---- the second product
   if (warp == 0) {
     at_cluster_arrive();
-    if (lane == 0) {
-      for (; loaded2 < nt && !*abort_flag; ++loaded2) {
-        wait(&empty2[loaded2 % kAtStages2], (loaded2 / kAtStages2 - 1) & 1);
-        if (*abort_flag) break;
-        load2(loaded2);
-      }
-      // after a timeout every copy lands before the CTA may go
-      if (*abort_flag) {
-        for (int s = 0; s < g.stages1 && s < nk; ++s) mbar_wait(&full1[s], ((nk - 1 - s) / g.stages1) & 1);
-        for (int s = 0; s < kAtStages2 && s < loaded2; ++s) mbar_wait(&full2[s], ((loaded2 - 1 - s) / kAtStages2) & 1);
-      }
+    while (loaded2 < nt && !dead) {
+      wait(&empty2[loaded2 % kAtStages2], (loaded2 / kAtStages2 - 1) & 1);
+      if (!dead) load2();
+    }
+    // after a timeout every copy lands before the CTA may go
+    if (dead || *abort_flag) {
+      for (int j = max(0, loaded1 - g.stages1); j < loaded1; ++j) mbar_wait(&full1[j % g.stages1], (j / g.stages1) & 1);
+      for (int j = max(0, loaded2 - kAtStages2); j < loaded2; ++j) mbar_wait(&full2[j % kAtStages2], (j / kAtStages2) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && a.out) {
+    if (a.out) {
       wait(vfull, 0);
       if (copies > 1) wait(vrep, 0);
       at_fence_async();
     }
-    __syncwarp();
     at_cluster_arrive();
-    if (lane == 0 && nt > 0) {
-      const uint32_t idesc = idesc_bf16(kAtRows, kAtCols, 0, 1);
-      const uint32_t base = smem_u32(sm);
-      for (int i = 0; i < nt; ++i) {
-        const int s = i % kAtStages2, b = i & 1;
-        wait(&full2[s], (i / kAtStages2) & 1);
-        if (i >= 2) wait(&tempty[b], (i / 2 - 1) & 1);
-        tc_fence_after();
-        if (!*abort_flag) {
-          const uint64_t bd = at_desc(smem_u32(ring2) + s * stage2, g.Rk * 128, 1024);
-          for (int k = 0; k < NS * g.Rk; k += 16) {
-            const uint64_t ad = at_desc(base + (k / 64) * kAtXBytes + (k % 64) * 2, 16, 1024);
-            umma_f16(tmem + b * kAtCols, ad, bd + (uint64_t)(k % g.Rk / 16) * (2048 >> 4), idesc, k != 0);
-          }
+    const uint32_t idesc = idesc_bf16(kAtRows, kAtCols, 0, 1);
+    const uint64_t a0 = at_desc(smem_u32(sm), 16, 1024), b0 = at_desc(smem_u32(ring2), g.Rk * 128, 1024);
+    for (int i = 0; i < nt; ++i) {
+      const int s = i % kAtStages2, b = i & 1;
+      wait(&full2[s], (i / kAtStages2) & 1);
+      if (i >= 2) wait(&tempty[b], (i / 2 - 1) & 1);
+      tc_fence_after();
+      if (lead && !dead) {
+        uint64_t bd = b0 + (uint64_t)(s * (stage2 >> 4));
+        int r = 0;  // 16 ranks of B at a time, NS times over
+        for (int k = 0; k < NS * g.Rk; k += 16) {
+          umma_f16(tmem + b * kAtCols, a0 + (uint64_t)((k / 64) * (kAtXBytes >> 4) + (k % 64) / 8), bd, idesc, k != 0);
+          r += 16;
+          bd += 2048 >> 4;
+          if (r == g.Rk) r = 0, bd = b0 + (uint64_t)(s * (stage2 >> 4));
         }
+      }
+      if (lead) {
         umma_commit(&empty2[s]);
         umma_commit(&tfull[b]);
       }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
     constexpr int kChunk = F32 ? 32 : 64, kPer = kAtCols / kChunk;  // outputs of a chunk (128 bytes); chunks of a step
     unsigned char* buf = part + (warp - 2) * 2 * kAtStage;
@@ -398,7 +400,6 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         fetch(ch + copies, slot ^ 1);
         if (!waited) {
           wait(&tfull[b], (i / 2) & 1);
-          __syncwarp();
           tc_fence_after();
           waited = true;
         }
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         }
         __syncwarp();
         const int n = col(ch) + pc * (16 / kSize);
-        const bool store = n < a.N && !*abort_flag;
+        const bool store = n < a.N && !dead;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int r = k * 4 + pr;
@@ -443,7 +444,6 @@ __global__ void __launch_bounds__(kAtThreads, 2)
       }
       if (!waited) {  // nothing of this step: in step with the others all the same
         wait(&tfull[b], (i / 2) & 1);
-        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();

@@ -104,6 +104,33 @@ __device__ __forceinline__ void tmem_ld_w(uint32_t taddr, float* v) {
   for (int i = 0; i < W; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// One lane of the (converged) warp.  The loops that issue copies and MMAs are run by whole warps, so that
+// their operands stay in uniform registers; only the issue itself is one lane's.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
+// Four MMAs over 64 of the inner dimension (16 each): A advances by `a_step` and B by `b_step` descriptor units; the first
+// accumulates onto D when `accumulate` is nonzero, the other three always do.
+__device__ __forceinline__ void umma_f16_k64(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate, uint32_t a_step, uint32_t b_step) {
+  asm volatile(
+      "{\n"
+      " .reg .pred p, t;\n"
+      " setp.ne.b32 p, %4, 0;\n"
+      " setp.eq.b32 t, 0, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %5, %6, %3, t;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %7, %8, %3, t;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %9, %10, %3, t;\n"
+      "}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "l"(adesc + a_step), "l"(bdesc + b_step),
+      "l"(adesc + 2 * a_step), "l"(bdesc + 2 * b_step), "l"(adesc + 3 * a_step), "l"(bdesc + 3 * b_step)
+      : "memory");
+}
+
 // Prefetch a tensor map (kernel parameter) into the descriptor cache.
 __device__ __forceinline__ void prefetch_tmap(const void* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");

@@ -106,14 +106,6 @@ struct W4RowMaps {
 // Rows are kept in whole stages, the rest zeros.
 __host__ __device__ inline int w4g_ld(int K) { return (K + kGK - 1) / kGK * kGK; }
 
-// One lane of the (converged) warp.  The loops that issue copies and MMAs are run by whole warps, so that
-// their operands stay in uniform registers; only the issue itself is one lane's.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
-  return p != 0;
-}
-
 // D[tmem of both CTAs] (+)= A[tmem of both] x B[smem of both], over one 64-deep stage: four MMAs; the first
 // accumulates when `accumulate` is nonzero.
 __device__ __forceinline__ void umma_f16_ts_pair_k64(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
