@@ -13,6 +13,7 @@
 // v = scale x A^T enters the second product as a sum of two (bf16 results) or three (fp32 results) bf16 numbers: 16 or
 // 24 significant bits.  The products cost little beside the bytes: 2 R flops a byte of x.
 #include <algorithm>
+#include <cmath>
 
 #include "adapters.cuh"
 
@@ -495,9 +496,9 @@ int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, bool beside, cuda
   g.Rk = (a.R + 15) / 16 * 16;
   // CTAs of a cluster and rows of a tile, by an estimate of the time: a CTA takes 9 us and its share of the tile's bytes
   // at 22 KB/us (44 where it has an SM to itself); 30 clusters of 8 CTAs, 72 of 4 or 152 of 2 run at once (half of them,
-  // one CTA a SM).  Measured: 4096 rows of R 64 (2048 x 4096) 31.0 us with 8 and 128, 31.5 with 4 and 64, 38 with 2 and
-  // 32; 16,384 of R 16 (2048 x 2048) 66 with 8 and 128, 56 with 4, 52 with 2; 1024 of R 16 16.8 with 8 and 128, 13.6 with
-  // 8 and 32; 2000 of R 128 (4096 x 4096) 34 with 4 and 64, 48 with 8 and 128.
+  // one CTA a SM).  Measured: 4096 rows of R 64 (2048 x 4096) 30.0 us with 8 and 128, 30.4 with 4 and 64, 35 with 2 and
+  // 32; 16,384 of R 16 (2048 x 2048) 60 with 8 and 128, 53 with 4, 49 with 2; 1024 of R 16 15.4 with 8 and 128, 12.3 with
+  // 8 and 32, 14.2 with 4 and 32; 2000 of R 128 (4096 x 4096) 29 with 4 and 64, 44 with 8 and 128.
   int C = 8;
   double best = 0.;
   for (int c = 2; c <= 8; c *= 2)
@@ -505,7 +506,9 @@ int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, bool beside, cuda
       if (g.Rk > 64 && f32 && tile > 64) continue;
       const double bytes = (tile * (2. * a.K + (f32 ? 4. : 2.) * (a.base ? 2 : 1) * (a.out ? a.N : 0)) + 2. * a.R * ((double)a.K + a.N)) / c;
       const int most = (c == 8 ? 240 : c == 4 ? 288 : 304) / (g.Rk > 64 ? 2 : 1);
-      const double t = (9. + bytes / (g.Rk > 64 ? 44e3 : 22e3)) * std::max(1., ((double)a.T / tile + 1.) * c / most);
+      double rounds = std::max(1., ((double)a.T / tile + 1.) * c / most);
+      if (g.Rk > 64) rounds = std::ceil(rounds);  // (two CTAs a SM overlap theirs)
+      const double t = (9. + bytes / (g.Rk > 64 ? 44e3 : 22e3)) * rounds;
       if (best == 0. || t < best) best = t, C = c, g.tile = tile;
     }
   g.short_rows = short_rows;

@@ -58,6 +58,7 @@ __device__ __forceinline__ float grp_logit(const void* p, size_t i) {
   return BF16 ? bf16_to_f32(reinterpret_cast<const uint16_t*>(p)[i]) : reinterpret_cast<const float*>(p)[i];
 }
 
+__device__ __forceinline__ float grp_sigmoid(float l) { return __fdividef(1.f, 1.f + expf(-l)); }
 // Whether fp32 does not tell the order of two scores of these keys (m at most ml).
 __device__ __forceinline__ bool grp_close(uint32_t ml, uint32_t m, float rel, float bmax) {
   if (m <= 1u) return false;  // nothing, or a NaN
@@ -151,11 +152,20 @@ __device__ __noinline__ int grp_pick64(const GroupArgs& a, size_t row) {
 
 // One warp routes a token.  Lane (g, i) holds the vectors i, i + lanes, ... of V experts of group g, so that a group's
 // score takes log2(lanes) shuffles.
+//
+// The k best: k of the lanes' best elements are at or above the k-th largest of them, so only elements at or above it (a
+// tolerance below it, with a bias) can be picked.  They are some 12 to 16 as a rule; a lane takes each, and its place is
+// the number of those that are larger.  (k maxima one after the other, each over all elements, took three times as long;
+// they remain for tokens with more than 32 such elements, which have many equal logits.)
 template <int V, int NQ, bool BF16>
 __global__ void __launch_bounds__(kGrpThreads) group_route_kernel(const GroupArgs a) {
   constexpr int NE = NQ * V;
+  constexpr bool kKeepBias = NE <= 32;  // in registers
+  __shared__ uint32_t s_key[kGrpThreads / 32][32];
+  __shared__ int s_e[kGrpThreads / 32][32];
   pdl_wait();
-  const int lane = threadIdx.x & 31, g = lane / a.lanes, i0 = lane % a.lanes;
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / a.lanes, i0 = lane % a.lanes;
   const bool sig = a.flags & MOE_ROUTE_SIGMOID, raw = a.flags & MOE_ROUTE_RAW, gmax = a.flags & MOE_ROUTE_GROUP_MAX;
   const bool limited = a.topk_group < a.n_group;
   const bool sums = limited && !gmax;         // groups are chosen by sums of scores
@@ -164,20 +174,22 @@ __global__ void __launch_bounds__(kGrpThreads) group_route_kernel(const GroupArg
   const int e0 = g * a.group + i0 * V;        // vector q starts at expert e0 + q lanes V
   const int step = a.lanes * V;
   const int held = g < a.n_group ? max(0, a.group - i0 * V + step - 1) / step : 0;  // vectors of this lane
-  float bmax = 0.f;
+  float bias[kKeepBias ? NE : 1], bmax = 0.f;
   if (a.bias) {
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
 #pragma unroll
       for (int j = 0; j < V; ++j)
         if (q < held) {
-          const float b = fabsf(a.bias[e0 + q * step + j]);
-          if (b < INFINITY) bmax = fmaxf(bmax, b);
+          const float b = a.bias[e0 + q * step + j];
+          if (kKeepBias) bias[q * V + j] = b;
+          if (fabsf(b) < INFINITY) bmax = fmaxf(bmax, fabsf(b));
         }
     bmax = __uint_as_float(__reduce_max_sync(MOE_FULL_MASK, __float_as_uint(bmax)));
   }
+  auto bias_at = [&](int q, int j) { return kKeepBias ? bias[q * V + j] : a.bias[e0 + q * step + j]; };
   const int warps = gridDim.x * (kGrpThreads / 32);
-  for (int t = blockIdx.x * (kGrpThreads / 32) + (threadIdx.x >> 5); t < a.T; t += warps) {
+  for (int t = blockIdx.x * (kGrpThreads / 32) + warp; t < a.T; t += warps) {
     const size_t row = (size_t)t * a.E;
     if (a.mask && !a.mask[t]) {
       if (lane < a.k) {
@@ -220,8 +232,8 @@ __global__ void __launch_bounds__(kGrpThreads) group_route_kernel(const GroupArg
         const int u = q * V + j;
         float c = l[u];
         if (scores) {
-          const float s = sig ? __fdividef(1.f, 1.f + expf(-c)) : expf(c - mx) * inv;
-          const float v = a.bias && q < held ? s + a.bias[e0 + q * step + j] : s;
+          const float s = sig ? grp_sigmoid(c) : expf(c - mx) * inv;
+          const float v = a.bias && q < held ? s + bias_at(q, j) : s;
           if (a.bias) c = v;
           if (q < held) {
             b2 = fmaxf(b2, fminf(b1, v));
@@ -230,9 +242,10 @@ __global__ void __launch_bounds__(kGrpThreads) group_route_kernel(const GroupArg
         }
         key[u] = q < held ? grp_key(c) : 0u;
       }
-    // Error bound of a difference of two scores, relative to them: exp, a reciprocal and two roundings each (2^-21),
-    // and for a softmax the rounding of an argument below 64 and the sum's (2^-18).
-    const float rel = sig ? 0x1p-19f : 0x1p-17f;
+    // Error bound of a difference of two scores, relative to them: an exp, a reciprocal (2 units in the last place
+    // each, 2^-22) and two roundings (2^-24), of either; for a softmax the rounding of an argument below 64 and the
+    // sum's (2^-18).
+    const float rel = sig ? 0x1p-20f : 0x1p-17f;
     bool close = false;
     if (limited) {
       uint32_t gk = 0;
@@ -264,61 +277,144 @@ __global__ void __launch_bounds__(kGrpThreads) group_route_kernel(const GroupArg
         close = !(lo - hi > 2.f * rel * (fabsf(lo) + 2.f * bmax) + 1e-30f);
       }
     }
-    // the k best, one after the other
-    int mine = -1, last = -1;
-    uint32_t ml = 0;
-    for (int j = 0; j < a.k && !close; ++j) {
+    int place = lane, e = -1;  // of the expert that this lane has, if place < k
+    float z = -INFINITY;
+    bool exact = close;
+    if (!exact) {
       uint32_t best = 0;
 #pragma unroll
       for (int u = 0; u < NE; ++u) best = max(best, key[u]);
-      const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, best);
-      int e = INT_MAX;
-#pragma unroll
-      for (int q = NQ - 1; q >= 0; --q)
-#pragma unroll
-        for (int v = V - 1; v >= 0; --v)
-          if (key[q * V + v] == m) e = e0 + q * step + v;
-      e = __reduce_min_sync(MOE_FULL_MASK, best == m ? e : INT_MAX);
-#pragma unroll
-      for (int q = 0; q < NQ; ++q)
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (e0 + q * step + v == e) key[q * V + v] = 0u;
-      if (a.bias) {
-        if (j > 0 && grp_close(ml, m, rel, bmax))
-          close = grp_logit<BF16>(a.logits, row + e) != grp_logit<BF16>(a.logits, row + last) || a.bias[e] != a.bias[last];
-        ml = m;
-        last = e;
+      int larger = 0;
+#pragma unroll 8
+      for (int h = 0; h < 32; ++h) {
+        const uint32_t o = __shfl_sync(MOE_FULL_MASK, best, h);
+        larger += o > best || (o == best && h < lane);
       }
-      if (lane == j) mine = e;
-    }
-    if (a.bias && !close && ml > 1) {
-      // the last pick and what is left
-      const float ll = grp_logit<BF16>(a.logits, row + last), lb = a.bias[last];
-      const bool finite = fabsf(grp_value(ml)) < INFINITY;
-      uint32_t next = 0;
+      uint32_t thr = max(__reduce_max_sync(MOE_FULL_MASK, larger == a.k - 1 ? best : 0u), 1u);
+      if (a.bias && thr > 1u) {
+        const float f = grp_value(thr);
+        if (fabsf(f) < INFINITY) thr = grp_key(f - (rel * (fabsf(f) + bmax) + 1e-30f));
+      }
+      int n = 0;
 #pragma unroll
-      for (int q = 0; q < NQ; ++q)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const uint32_t m = key[q * V + v];
-          if (m == ml) close |= finite && (l[q * V + v] != ll || a.bias[e0 + q * step + v] != lb);
-          else next = max(next, m);
+      for (int u = 0; u < NE; ++u) {
+        const unsigned m = __ballot_sync(MOE_FULL_MASK, key[u] >= thr);
+        if (m) {
+          const int at = n + __popc(m & lanemask_lt());
+          if (key[u] >= thr && at < 32) {
+            s_key[warp][at] = key[u];
+            s_e[warp][at] = e0 + u / V * step + u % V;
+          }
+          n += __popc(m);
         }
-      next = __reduce_max_sync(MOE_FULL_MASK, next);
-      close = __any_sync(MOE_FULL_MASK, close) || grp_close(ml, next, rel, bmax);
+      }
+      if (n <= 32) {
+        __syncwarp();
+        const bool on = lane < n;
+        const uint32_t mine = on ? s_key[warp][lane] : 0u;
+        e = on ? s_e[warp][lane] : -1;
+        __syncwarp();
+        float bb = 0.f;
+        if (on) {
+          z = grp_logit<BF16>(a.logits, row + e);
+          if (a.bias) bb = a.bias[e];
+        }
+        uint32_t above = 0xffffffffu;  // the next larger one
+        int same = 0;
+        place = 0;
+        for (int j = 0; j < n; ++j) {
+          const uint32_t o = __shfl_sync(MOE_FULL_MASK, mine, j);
+          place += o > mine;
+          same += o == mine;
+          if (o > mine) above = min(above, o);
+        }
+        bool unsure = a.bias && on && place >= 1 && place <= a.k && above != 0xffffffffu && grp_close(above, mine, rel, bmax);
+        if (__any_sync(MOE_FULL_MASK, on && same > 1)) {
+          for (int j = 0; j < n; ++j) {
+            const uint32_t o = __shfl_sync(MOE_FULL_MASK, mine, j);
+            const int oe = __shfl_sync(MOE_FULL_MASK, e, j);
+            const float oz = __shfl_sync(MOE_FULL_MASK, z, j), ob = __shfl_sync(MOE_FULL_MASK, bb, j);
+            if (on && o == mine) {
+              place += oe < e;
+              // equal scores of other logits are equal in fp32 alone (but for infinities)
+              unsure |= a.bias && mine > 1u && fabsf(grp_value(mine)) < INFINITY && (oz != z || ob != bb);
+            }
+          }
+        }
+        if (!on) place = 32;
+        if (__any_sync(MOE_FULL_MASK, unsure)) {
+          exact = !sig;  // (a softmax needs its sum in 64 bits, too)
+          if (sig) {
+            const uint64_t c = on ? grp_key64(1. / (1. + exp(-(double)z)) + (double)bb) : 0ull;
+            place = on ? 0 : 32;
+            for (int j = 0; j < n; ++j) {
+              const uint64_t o = __shfl_sync(MOE_FULL_MASK, c, j);
+              const int oe = __shfl_sync(MOE_FULL_MASK, e, j);
+              place += o > c || (o == c && oe < e);
+            }
+          }
+        }
+      } else {
+        // one after the other: many are equal
+        int last = -1;
+        uint32_t ml = 0;
+        place = lane;
+        for (int j = 0; j < a.k && !exact; ++j) {
+          best = 0;
+#pragma unroll
+          for (int u = 0; u < NE; ++u) best = max(best, key[u]);
+          const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, best);
+          int x = INT_MAX;
+#pragma unroll
+          for (int u = NE - 1; u >= 0; --u)
+            if (key[u] == m) x = e0 + u / V * step + u % V;
+          x = __reduce_min_sync(MOE_FULL_MASK, best == m ? x : INT_MAX);
+#pragma unroll
+          for (int u = 0; u < NE; ++u)
+            if (e0 + u / V * step + u % V == x) key[u] = 0u;
+          if (a.bias) {
+            if (j > 0 && grp_close(ml, m, rel, bmax))
+              exact = grp_logit<BF16>(a.logits, row + x) != grp_logit<BF16>(a.logits, row + last) || a.bias[x] != a.bias[last];
+            ml = m;
+            last = x;
+          }
+          if (lane == j) e = x;
+        }
+        if (a.bias && !exact && ml > 1u) {
+          // the last pick and what is left
+          const float ll = grp_logit<BF16>(a.logits, row + last), lb = a.bias[last];
+          const bool finite = fabsf(grp_value(ml)) < INFINITY;
+          uint32_t next = 0;
+#pragma unroll
+          for (int q = 0; q < NQ; ++q)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+              const uint32_t m = key[q * V + v];
+              if (m == ml) exact |= finite && (l[q * V + v] != ll || bias_at(q, v) != lb);
+              else next = max(next, m);
+            }
+          next = __reduce_max_sync(MOE_FULL_MASK, next);
+          exact = __any_sync(MOE_FULL_MASK, exact) || grp_close(ml, next, rel, bmax);
+        }
+        if (lane < a.k && !exact) z = grp_logit<BF16>(a.logits, row + e);
+      }
     }
-    if (close) mine = grp_pick64<V, NQ, BF16>(a, row);
-    // weights: lane j has pick j
-    const bool on = lane < a.k;
-    const float z = on ? grp_logit<BF16>(a.logits, row + mine) : -INFINITY;
+    if (exact) {
+      place = lane;
+      e = grp_pick64<V, NQ, BF16>(a, row);
+      if (lane < a.k) z = grp_logit<BF16>(a.logits, row + e);
+    }
+    // weights, over the lanes with a place
+    const bool on = place < a.k;
     float w = 0.f;
     if (raw) {
       if (on) w = sig ? 1.f / (1.f + expf(-z)) : expf(z - mx) / sum;
     } else {
-      float top = z;
-#pragma unroll
-      for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(MOE_FULL_MASK, top, o));
+      float top = __uint_as_float(0xff800000u);
+      {
+        const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, on ? grp_key(z) : 0u);
+        if (m > 1u) top = grp_value(m);
+      }
       if (on) {
         if (sig) {
           // sigmoid(z) / exp(min(top, 0)): a row of large negative logits keeps its proportions
@@ -330,12 +426,12 @@ __global__ void __launch_bounds__(kGrpThreads) group_route_kernel(const GroupArg
       }
       float all = w;
 #pragma unroll
-      for (int o = 8; o; o >>= 1) all += __shfl_xor_sync(MOE_FULL_MASK, all, o);
+      for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(MOE_FULL_MASK, all, o);
       w = all == 0.f ? 0.f : w / all;  // picks of -inf alone have no weight
     }
     if (on) {
-      a.ids[(size_t)t * a.k + lane] = mine;
-      a.w[(size_t)t * a.k + lane] = w * a.scale;
+      a.ids[(size_t)t * a.k + place] = e;
+      a.w[(size_t)t * a.k + place] = w * a.scale;
     }
   }
 }
