@@ -5,13 +5,14 @@
 // groups stay, and the k best c among their experts are picked; w_j = scale s_j (/ sum_j s_j).  Equal values: the lower
 // index first.
 //
-// The picks are whole numbers, so they are those of 64-bit arithmetic: c is formed in fp32, and a token for which two
-// neighbours in the order are closer than the fp32 error bound (and not the same logit with the same bias) is picked
-// again in fp64 by its warp.  That is one token in some thousands.
+// The picks are whole numbers, so they are those of 64-bit arithmetic: c is formed in fp32, and where two neighbours in
+// the order are closer than the fp32 error bound (and not the same logit with the same bias), the candidates of the token,
+// or the best of its groups, are compared again in fp64.  That is some tokens in a thousand.
 //
 // The bytes of the logits, read once, bound a large batch; what a warp does for a token (k reductions one after the
 // other) bounds it in practice, and the launch a small one.
 #include <algorithm>
+#include <cstdlib>
 
 #include "internal.cuh"
 
@@ -58,12 +59,19 @@ __device__ __forceinline__ float grp_logit(const void* p, size_t i) {
   return BF16 ? bf16_to_f32(reinterpret_cast<const uint16_t*>(p)[i]) : reinterpret_cast<const float*>(p)[i];
 }
 
-__device__ __forceinline__ float grp_sigmoid(float l) { return __fdividef(1.f, 1.f + expf(-l)); }
+// sigmoid within 2^-21 of itself above l = -8, within 2e-10 below (the rounding of the exponent is |l| 2^-24 of it).
+__device__ __forceinline__ float grp_sigmoid(float l) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
+constexpr float kGrpTiny = 0x1p-31f;  // 4.7e-10
 // Whether fp32 does not tell the order of two scores of these keys (m at most ml).
 __device__ __forceinline__ bool grp_close(uint32_t ml, uint32_t m, float rel, float bmax) {
   if (m <= 1u) return false;  // nothing, or a NaN
   const float a = grp_value(ml), b = grp_value(m);
-  return !(a - b > rel * (fabsf(a) + bmax) + 1e-30f) && !(isinf(a) && a == b);
+  return !(a - b > rel * (fabsf(a) + bmax) + kGrpTiny) && !(isinf(a) && a == b);
 }
 
 // V consecutive logits (16 bytes, or one).
@@ -78,6 +86,35 @@ __device__ __forceinline__ void grp_load(const void* p, size_t i, float* v) {
     for (int j = 0; j < V; ++j)
       v[j] = BF16 ? (j & 1 ? bf16_hi(u[j / 2]) : bf16_lo(u[j / 2])) : __uint_as_float(u[j & 3]);
   }
+}
+
+// sum_e exp(logit - mx) of a token in fp64, by the whole warp.
+template <bool BF16>
+__device__ __noinline__ double grp_sum64(const GroupArgs& a, size_t row, float mx) {
+  double s = 0.;
+  for (int e = threadIdx.x & 31; e < a.E; e += 32) s += exp((double)grp_logit<BF16>(a.logits, row + e) - (double)mx);
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(MOE_FULL_MASK, s, o);
+  return s;
+}
+
+// The two best c of the lane's experts in fp64, among those whose c is at least thr in fp32.
+template <int V, int NQ, bool BF16>
+__device__ __noinline__ double2 grp_best64(const GroupArgs& a, size_t row, float thr, float mx, float inv, double sum) {
+  const int lane = threadIdx.x & 31, g = lane / a.lanes, i0 = lane % a.lanes;
+  const bool sig = a.flags & MOE_ROUTE_SIGMOID;
+  double b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll 1
+  for (int u = 0; u < NQ * V; ++u) {
+    const int i = (u / V * a.lanes + i0) * V + u % V;
+    if (g >= a.n_group || i >= a.group) break;
+    const float l = grp_logit<BF16>(a.logits, row + g * a.group + i), b = a.bias ? a.bias[g * a.group + i] : 0.f;
+    if ((sig ? grp_sigmoid(l) : expf(l - mx) * inv) + b >= thr) {
+      const double c = (sig ? 1. / (1. + exp(-(double)l)) : exp((double)l - (double)mx) / sum) + (double)b;
+      b2 = fmax(b2, fmin(b1, c));
+      b1 = fmax(b1, c);
+    }
+  }
+  return make_double2(b1, b2);
 }
 
 // The picks of one token in fp64, by the whole warp; lane j returns pick j.  A lane holds the experts it holds in
@@ -158,7 +195,7 @@ __device__ __noinline__ int grp_pick64(const GroupArgs& a, size_t row) {
 // the number of those that are larger.  (k maxima one after the other, each over all elements, took three times as long;
 // they remain for tokens with more than 32 such elements, which have many equal logits.)
 template <int V, int NQ, bool BF16>
-__global__ void __launch_bounds__(kGrpThreads) group_route_kernel(const GroupArgs a) {
+__global__ void __launch_bounds__(kGrpThreads) group_route_kernel(const GroupArgs a, int per) {
   constexpr int NE = NQ * V;
   constexpr bool kKeepBias = NE <= 32;  // in registers
   __shared__ uint32_t s_key[kGrpThreads / 32][32];
@@ -188,8 +225,8 @@ __global__ void __launch_bounds__(kGrpThreads) group_route_kernel(const GroupArg
     bmax = __uint_as_float(__reduce_max_sync(MOE_FULL_MASK, __float_as_uint(bmax)));
   }
   auto bias_at = [&](int q, int j) { return kKeepBias ? bias[q * V + j] : a.bias[e0 + q * step + j]; };
-  const int warps = gridDim.x * (kGrpThreads / 32);
-  for (int t = blockIdx.x * (kGrpThreads / 32) + warp; t < a.T; t += warps) {
+  const int t0 = (blockIdx.x * (kGrpThreads / 32) + warp) * per;
+  for (int t = t0; t < min(t0 + per, a.T); ++t) {
     const size_t row = (size_t)t * a.E;
     if (a.mask && !a.mask[t]) {
       if (lane < a.k) {
@@ -242,71 +279,119 @@ __global__ void __launch_bounds__(kGrpThreads) group_route_kernel(const GroupArg
         }
         key[u] = q < held ? grp_key(c) : 0u;
       }
-    // Error bound of a difference of two scores, relative to them: an exp, a reciprocal (2 units in the last place
-    // each, 2^-22) and two roundings (2^-24), of either; for a softmax the rounding of an argument below 64 and the
-    // sum's (2^-18).
+    // Error bound of a difference of two scores: that of either sigmoid and the roundings of s + bias (2^-24); for a
+    // softmax the rounding of an argument below 64 and the sum's (2^-18).
     const float rel = sig ? 0x1p-20f : 0x1p-17f;
-    bool close = false;
+    double sum64 = 0.;
     if (limited) {
-      uint32_t gk = 0;
-      if (gmax) {
-#pragma unroll
-        for (int u = 0; u < NE; ++u) gk = max(gk, key[u]);
-        for (int o = a.lanes / 2; o; o >>= 1) gk = max(gk, __shfl_xor_sync(MOE_FULL_MASK, gk, o));
-      } else {
+      if (scores)
         for (int o = a.lanes / 2; o; o >>= 1) {
           const float o1 = __shfl_xor_sync(MOE_FULL_MASK, b1, o), o2 = __shfl_xor_sync(MOE_FULL_MASK, b2, o);
           b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
           b1 = fmaxf(b1, o1);
         }
-        gk = grp_key(a.group == 1 ? b1 : b1 + b2);
+      const bool one = gmax || a.group == 1;
+      uint32_t gk = 0;
+      if (scores) {
+        gk = grp_key(one ? b1 : b1 + b2);
+      } else {
+#pragma unroll
+        for (int u = 0; u < NE; ++u) gk = max(gk, key[u]);
+        for (int o = a.lanes / 2; o; o >>= 1) gk = max(gk, __shfl_xor_sync(MOE_FULL_MASK, gk, o));
       }
       int before = 0;
       for (int h = 0; h < a.n_group; ++h) {
         const uint32_t ok = __shfl_sync(MOE_FULL_MASK, gk, h * a.lanes);
         before += ok > gk || (ok == gk && h < g);
       }
-      const bool in = before < a.topk_group && g < a.n_group;
+      bool in = before < a.topk_group && g < a.n_group;
+      if (scores) {
+        const float lo = grp_value(__reduce_min_sync(MOE_FULL_MASK, in ? gk : 0xffffffffu));
+        const float hi = grp_value(__reduce_max_sync(MOE_FULL_MASK, !in && g < a.n_group ? gk : 0u));
+        if (!(lo - hi > 2.f * (rel * (fabsf(lo) + 2.f * bmax) + kGrpTiny))) {
+          // the groups in fp64, of what may be their best (without a bias a softmax's sum does not matter)
+          sum64 = !sig && a.bias ? grp_sum64<BF16>(a, row, mx) : 1.;
+          const float low = one ? b1 : b2;
+          double2 x = grp_best64<V, NQ, BF16>(a, row, low - 2.f * (rel * (fabsf(low) + bmax) + kGrpTiny), mx, inv, sum64);
+          for (int o = a.lanes / 2; o; o >>= 1) {
+            const double o1 = __shfl_xor_sync(MOE_FULL_MASK, x.x, o), o2 = __shfl_xor_sync(MOE_FULL_MASK, x.y, o);
+            x.y = fmax(fmin(x.x, o1), fmax(x.y, o2));
+            x.x = fmax(x.x, o1);
+          }
+          const uint64_t gk64 = grp_key64(one ? x.x : x.x + x.y);
+          before = 0;
+          for (int h = 0; h < a.n_group; ++h) {
+            const uint64_t ok = __shfl_sync(MOE_FULL_MASK, gk64, h * a.lanes);
+            before += ok > gk64 || (ok == gk64 && h < g);
+          }
+          in = before < a.topk_group && g < a.n_group;
+        }
+      }
       if (!in) {
 #pragma unroll
         for (int u = 0; u < NE; ++u) key[u] = 0u;
       }
-      if (sums || a.bias) {
-        const float lo = grp_value(__reduce_min_sync(MOE_FULL_MASK, in ? gk : 0xffffffffu));
-        const float hi = grp_value(__reduce_max_sync(MOE_FULL_MASK, !in && g < a.n_group ? gk : 0u));
-        close = !(lo - hi > 2.f * rel * (fabsf(lo) + 2.f * bmax) + 1e-30f);
-      }
     }
     int place = lane, e = -1;  // of the expert that this lane has, if place < k
     float z = -INFINITY;
-    bool exact = close;
-    if (!exact) {
-      uint32_t best = 0;
+    bool exact = false;
+    {
+      // the k-th largest of the lanes' best elements, or where lanes are few of their vectors'
+      uint32_t thr = 1u, top[NQ], best = 0;
 #pragma unroll
-      for (int u = 0; u < NE; ++u) best = max(best, key[u]);
-      int larger = 0;
-#pragma unroll 8
-      for (int h = 0; h < 32; ++h) {
-        const uint32_t o = __shfl_sync(MOE_FULL_MASK, best, h);
-        larger += o > best || (o == best && h < lane);
+      for (int q = 0; q < NQ; ++q) {
+        top[q] = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) top[q] = max(top[q], key[q * V + v]);
+        best = max(best, top[q]);
       }
-      uint32_t thr = max(__reduce_max_sync(MOE_FULL_MASK, larger == a.k - 1 ? best : 0u), 1u);
+      if (a.topk_group * a.lanes >= a.k || NQ == 1) {
+        for (int seen = 0; seen < a.k;) {
+          const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, best);
+          if (m == 0) break;
+          const unsigned at = __ballot_sync(MOE_FULL_MASK, best == m);
+          seen += __popc(at);
+          if (seen >= a.k) thr = m;
+          if (best == m) best = 0;
+        }
+      } else {
+        for (int seen = 0; seen < a.k;) {
+          const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, best);
+          if (m == 0) break;
+          int here = 0;
+          best = 0;
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            here += top[q] == m;
+            if (top[q] == m) top[q] = 0;
+            best = max(best, top[q]);
+          }
+          seen += __reduce_add_sync(MOE_FULL_MASK, here);
+          if (seen >= a.k) thr = m;
+        }
+      }
       if (a.bias && thr > 1u) {
         const float f = grp_value(thr);
-        if (fabsf(f) < INFINITY) thr = grp_key(f - (rel * (fabsf(f) + bmax) + 1e-30f));
+        if (fabsf(f) < INFINITY) thr = grp_key(f - (rel * (fabsf(f) + bmax) + kGrpTiny));
       }
-      int n = 0;
+      int n = 0, mineat = 0;
 #pragma unroll
-      for (int u = 0; u < NE; ++u) {
-        const unsigned m = __ballot_sync(MOE_FULL_MASK, key[u] >= thr);
-        if (m) {
-          const int at = n + __popc(m & lanemask_lt());
-          if (key[u] >= thr && at < 32) {
-            s_key[warp][at] = key[u];
-            s_e[warp][at] = e0 + u / V * step + u % V;
+      for (int u = 0; u < NE; ++u) n += key[u] >= thr;
+      mineat = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(MOE_FULL_MASK, mineat, o);
+        if (lane >= o) mineat += x;
+      }
+      mineat -= n;
+      n = __shfl_sync(MOE_FULL_MASK, mineat + n, 31);
+      if (n <= 32) {
+#pragma unroll
+        for (int u = 0; u < NE; ++u)
+          if (key[u] >= thr) {
+            s_key[warp][mineat] = key[u];
+            s_e[warp][mineat++] = e0 + u / V * step + u % V;
           }
-          n += __popc(m);
-        }
       }
       if (n <= 32) {
         __syncwarp();
@@ -322,6 +407,7 @@ __global__ void __launch_bounds__(kGrpThreads) group_route_kernel(const GroupArg
         uint32_t above = 0xffffffffu;  // the next larger one
         int same = 0;
         place = 0;
+#pragma unroll 4
         for (int j = 0; j < n; ++j) {
           const uint32_t o = __shfl_sync(MOE_FULL_MASK, mine, j);
           place += o > mine;
@@ -343,15 +429,14 @@ __global__ void __launch_bounds__(kGrpThreads) group_route_kernel(const GroupArg
         }
         if (!on) place = 32;
         if (__any_sync(MOE_FULL_MASK, unsure)) {
-          exact = !sig;  // (a softmax needs its sum in 64 bits, too)
-          if (sig) {
-            const uint64_t c = on ? grp_key64(1. / (1. + exp(-(double)z)) + (double)bb) : 0ull;
-            place = on ? 0 : 32;
-            for (int j = 0; j < n; ++j) {
-              const uint64_t o = __shfl_sync(MOE_FULL_MASK, c, j);
-              const int oe = __shfl_sync(MOE_FULL_MASK, e, j);
-              place += o > c || (o == c && oe < e);
-            }
+          if (!sig && sum64 == 0.) sum64 = grp_sum64<BF16>(a, row, mx);
+          const double s = sig ? 1. / (1. + exp(-(double)z)) : exp((double)z - (double)mx) / sum64;
+          const uint64_t c = on ? grp_key64(s + (double)bb) : 0ull;
+          place = on ? 0 : 32;
+          for (int j = 0; j < n; ++j) {
+            const uint64_t o = __shfl_sync(MOE_FULL_MASK, c, j);
+            const int oe = __shfl_sync(MOE_FULL_MASK, e, j);
+            place += o > c || (o == c && oe < e);
           }
         }
       } else {
@@ -360,7 +445,7 @@ __global__ void __launch_bounds__(kGrpThreads) group_route_kernel(const GroupArg
         uint32_t ml = 0;
         place = lane;
         for (int j = 0; j < a.k && !exact; ++j) {
-          best = 0;
+          uint32_t best = 0;
 #pragma unroll
           for (int u = 0; u < NE; ++u) best = max(best, key[u]);
           const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, best);
@@ -575,8 +660,10 @@ static int grp_sms(int* sms) {
 
 template <int V, int NQ, bool BF16>
 static int launch_groups(const GroupArgs& a, int sms, cudaStream_t s) {
-  const int grid = std::min((a.T + 7) / 8, sms * 4);
-  MOE_CUDA_TRY(launch_pdl(group_route_kernel<V, NQ, BF16>, dim3(grid), dim3(kGrpThreads), 0, s, a));
+  int per = a.T >= sms * 32 ? 2 : 1;
+  if (getenv("GR_PER")) per = atoi(getenv("GR_PER"));
+  constexpr int W = kGrpThreads / 32;
+  MOE_CUDA_TRY(launch_pdl(group_route_kernel<V, NQ, BF16>, dim3((a.T + W * per - 1) / (W * per)), dim3(kGrpThreads), 0, s, a, per));
   return MOE_OK;
 }
 
