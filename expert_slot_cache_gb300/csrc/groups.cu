@@ -12,7 +12,6 @@
 // The bytes of the logits, read once, bound a large batch; what a warp does for a token (k reductions one after the
 // other) bounds it in practice, and the launch a small one.
 #include <algorithm>
-#include <cstdlib>
 
 #include "internal.cuh"
 
@@ -74,18 +73,29 @@ __device__ __forceinline__ bool grp_close(uint32_t ml, uint32_t m, float rel, fl
   return !(a - b > rel * (fabsf(a) + bmax) + kGrpTiny) && !(isinf(a) && a == b);
 }
 
-// V consecutive logits (16 bytes, or one).
+// V consecutive logits (16 bytes, or one), as they are.
+template <bool BF16, int V>
+struct GrpRaw {
+  uint32_t r[V == 1 ? 1 : 4];
+  __device__ __forceinline__ void load(const void* p, size_t i) {
+    if constexpr (V == 1) {
+      r[0] = __float_as_uint(grp_logit<BF16>(p, i));
+    } else {
+      const uint4 v = ldg_stream(reinterpret_cast<const uint8_t*>(p) + i * (BF16 ? 2 : 4));
+      r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+    }
+  }
+  __device__ __forceinline__ float at(int j) const {
+    if constexpr (V == 1 || !BF16) return __uint_as_float(r[j]);
+    else return j & 1 ? bf16_hi(r[j / 2]) : bf16_lo(r[j / 2]);
+  }
+};
 template <bool BF16, int V>
 __device__ __forceinline__ void grp_load(const void* p, size_t i, float* v) {
-  if constexpr (V == 1) {
-    v[0] = grp_logit<BF16>(p, i);
-  } else {
-    const uint4 r = ldg_stream(reinterpret_cast<const uint8_t*>(p) + i * (BF16 ? 2 : 4));
-    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+  GrpRaw<BF16, V> x;
+  x.load(p, i);
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      v[j] = BF16 ? (j & 1 ? bf16_hi(u[j / 2]) : bf16_lo(u[j / 2])) : __uint_as_float(u[j & 3]);
-  }
+  for (int j = 0; j < V; ++j) v[j] = x.at(j);
 }
 
 // sum_e exp(logit - mx) of a token in fp64, by the whole warp.
@@ -97,24 +107,22 @@ __device__ __noinline__ double grp_sum64(const GroupArgs& a, size_t row, float m
   return s;
 }
 
-// The two best c of the lane's experts in fp64, among those whose c is at least thr in fp32.
-template <int V, int NQ, bool BF16>
-__device__ __noinline__ double2 grp_best64(const GroupArgs& a, size_t row, float thr, float mx, float inv, double sum) {
-  const int lane = threadIdx.x & 31, g = lane / a.lanes, i0 = lane % a.lanes;
-  const bool sig = a.flags & MOE_ROUTE_SIGMOID;
-  double b1 = -INFINITY, b2 = -INFINITY;
-#pragma unroll 1
-  for (int u = 0; u < NQ * V; ++u) {
-    const int i = (u / V * a.lanes + i0) * V + u % V;
-    if (g >= a.n_group || i >= a.group) break;
-    const float l = grp_logit<BF16>(a.logits, row + g * a.group + i), b = a.bias ? a.bias[g * a.group + i] : 0.f;
-    if ((sig ? grp_sigmoid(l) : expf(l - mx) * inv) + b >= thr) {
-      const double c = (sig ? 1. / (1. + exp(-(double)l)) : exp((double)l - (double)mx) / sum) + (double)b;
-      b2 = fmax(b2, fmin(b1, c));
-      b1 = fmax(b1, c);
-    }
+// One expert's s in fp64.
+__device__ __noinline__ double grp_score64(float l, bool sig, float mx, double sum) {
+  return sig ? 1. / (1. + exp(-(double)l)) : exp((double)l - (double)mx) / sum;
+}
+
+// A warp's exclusive prefix sum of n; `n` becomes the total.
+__device__ __forceinline__ int grp_scan(int& n) {
+  int at = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(MOE_FULL_MASK, at, o);
+    if ((threadIdx.x & 31) >= o) at += x;
   }
-  return make_double2(b1, b2);
+  at -= n;
+  n = __shfl_sync(MOE_FULL_MASK, at + n, 31);
+  return at;
 }
 
 // The picks of one token in fp64, by the whole warp; lane j returns pick j.  A lane holds the experts it holds in
@@ -187,118 +195,123 @@ __device__ __noinline__ int grp_pick64(const GroupArgs& a, size_t row) {
   return mine;
 }
 
+// CTAs of a SM (16,384 x 512, 16 elements a lane: 37 us with two, 41 with three and registers in memory, 42 with four).
+constexpr int grp_resident(int elements) { return elements <= 8 ? 3 : elements <= 32 ? 2 : 1; }
+
 // One warp routes a token.  Lane (g, i) holds the vectors i, i + lanes, ... of V experts of group g, so that a group's
-// score takes log2(lanes) shuffles.
+// score takes log2(lanes) shuffles.  FULL: every lane holds NQ vectors.
 //
 // The k best: k of the lanes' best elements are at or above the k-th largest of them, so only elements at or above it (a
 // tolerance below it, with a bias) can be picked.  They are some 12 to 16 as a rule; a lane takes each, and its place is
-// the number of those that are larger.  (k maxima one after the other, each over all elements, took three times as long;
+// the number of those that are larger.  (k maxima one after the other, each over all elements, took twice as long;
 // they remain for tokens with more than 32 such elements, which have many equal logits.)
-template <int V, int NQ, bool BF16>
-__global__ void __launch_bounds__(kGrpThreads) group_route_kernel(const GroupArgs a, int per) {
+template <int V, int NQ, bool BF16, bool FULL>
+__global__ void __launch_bounds__(kGrpThreads, grp_resident(NQ * V)) group_route_kernel(const GroupArgs a) {
   constexpr int NE = NQ * V;
   constexpr bool kKeepBias = NE <= 32;  // in registers
-  __shared__ uint32_t s_key[kGrpThreads / 32][32];
-  __shared__ int s_e[kGrpThreads / 32][32];
+  __shared__ uint16_t s_e[kGrpThreads / 32][32];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / a.lanes, i0 = lane % a.lanes;
   const bool sig = a.flags & MOE_ROUTE_SIGMOID, raw = a.flags & MOE_ROUTE_RAW, gmax = a.flags & MOE_ROUTE_GROUP_MAX;
   const bool limited = a.topk_group < a.n_group;
-  const bool sums = limited && !gmax;         // groups are chosen by sums of scores
-  const bool scores = a.bias || sums;         // scores are needed for the choice
-  const bool total = !sig && (scores || raw);  // the softmax over all experts is
-  const int e0 = g * a.group + i0 * V;        // vector q starts at expert e0 + q lanes V
+  const bool scores = a.bias || (limited && !gmax);  // scores are needed for the choice
+  const bool total = !sig && (scores || raw);         // the softmax over all experts is
+  const int e0 = g * a.group + i0 * V;               // vector q starts at expert e0 + q lanes V
   const int step = a.lanes * V;
-  const int held = g < a.n_group ? max(0, a.group - i0 * V + step - 1) / step : 0;  // vectors of this lane
+  const int held = FULL ? NQ : g < a.n_group ? max(0, a.group - i0 * V + step - 1) / step : 0;  // vectors of this lane
+  const float kNone = __uint_as_float(0x7fffffffu);  // NaN: at or above nothing
   float bias[kKeepBias ? NE : 1], bmax = 0.f;
-  if (a.bias) {
+  auto bias_at = [&](int u) {
+    return kKeepBias ? bias[u] : u / V < held ? a.bias[e0 + u / V * step + u % V] : 0.f;
+  };
+  auto expert = [&](int u) { return e0 + u / V * step + u % V; };
+  // a token's logits are on their way while the one before is routed, where registers suffice
+  constexpr bool kAhead = NE <= 32;
+  GrpRaw<BF16, V> next[NQ];
+  bool valid = true;
+  auto fetch = [&](int t) {
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
+      if (FULL || q < held) next[q].load(a.logits, (size_t)t * a.E + e0 + q * step);
+    valid = !a.mask || a.mask[t];
+  };
+  const int warps = gridDim.x * (kGrpThreads / 32);
+  int t = blockIdx.x * (kGrpThreads / 32) + warp;
+  if (kAhead && t < a.T) fetch(t);
+  if (a.bias) {
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (q < held) {
-          const float b = a.bias[e0 + q * step + j];
-          if (kKeepBias) bias[q * V + j] = b;
-          if (fabsf(b) < INFINITY) bmax = fmaxf(bmax, fabsf(b));
-        }
+    for (int u = 0; u < NE; ++u) {
+      const float b = FULL || u / V < held ? a.bias[expert(u)] : 0.f;
+      if (kKeepBias) bias[u] = b;
+      if (fabsf(b) < INFINITY) bmax = fmaxf(bmax, fabsf(b));
+    }
     bmax = __uint_as_float(__reduce_max_sync(MOE_FULL_MASK, __float_as_uint(bmax)));
   }
-  auto bias_at = [&](int q, int j) { return kKeepBias ? bias[q * V + j] : a.bias[e0 + q * step + j]; };
-  const int t0 = (blockIdx.x * (kGrpThreads / 32) + warp) * per;
-  for (int t = t0; t < min(t0 + per, a.T); ++t) {
+  for (; t < a.T; t += warps) {
     const size_t row = (size_t)t * a.E;
-    if (a.mask && !a.mask[t]) {
+    if (!kAhead) fetch(t);
+    float c[NE];  // the logits, then what is compared; kNone for what is not there
+#pragma unroll
+    for (int u = 0; u < NE; ++u) c[u] = FULL || u / V < held ? next[u / V].at(u % V) : kNone;
+    const bool padding = !valid;
+    if (kAhead && t + warps < a.T) fetch(t + warps);
+    if (padding) {
       if (lane < a.k) {
         a.ids[(size_t)t * a.k + lane] = -1;
         a.w[(size_t)t * a.k + lane] = 0.f;
       }
       continue;
     }
-    float l[NE];
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      if (q < held) {
-        grp_load<BF16, V>(a.logits, row + e0 + q * step, l + q * V);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) l[q * V + j] = -INFINITY;
-      }
-    }
-    float mx = 0.f, sum = 1.f;
+    float mx = 0.f, sum = 1.f, inv = 1.f;
     if (total) {
       mx = -INFINITY;
 #pragma unroll
-      for (int u = 0; u < NE; ++u) mx = fmaxf(mx, l[u]);
+      for (int u = 0; u < NE; ++u) mx = fmaxf(mx, c[u]);
 #pragma unroll
       for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(MOE_FULL_MASK, mx, o));
       sum = 0.f;
 #pragma unroll
       for (int u = 0; u < NE; ++u)
-        if (u / V < held) sum += expf(l[u] - mx);
+        if (FULL || u / V < held) sum += expf(c[u] - mx);
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(MOE_FULL_MASK, sum, o);
+      inv = 1.f / sum;
     }
-    const float inv = 1.f / sum;
-    uint32_t key[NE];
+    auto score = [&](float l) { return sig ? grp_sigmoid(l) : expf(l - mx) * inv; };
     float b1 = -INFINITY, b2 = -INFINITY;
+    if (a.bias) {
 #pragma unroll
-    for (int q = 0; q < NQ; ++q)
+      for (int u = 0; u < NE; ++u) c[u] = score(c[u]) + bias_at(u);
+    }
+    if (limited && scores) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int u = q * V + j;
-        float c = l[u];
-        if (scores) {
-          const float s = sig ? grp_sigmoid(c) : expf(c - mx) * inv;
-          const float v = a.bias && q < held ? s + bias_at(q, j) : s;
-          if (a.bias) c = v;
-          if (q < held) {
-            b2 = fmaxf(b2, fminf(b1, v));
-            b1 = fmaxf(b1, v);
-          }
-        }
-        key[u] = q < held ? grp_key(c) : 0u;
+      for (int u = 0; u < NE; ++u) {
+        const float v = a.bias ? c[u] : score(c[u]);
+        b2 = fmaxf(b2, fminf(b1, v == v ? v : -INFINITY));
+        b1 = fmaxf(b1, v);
       }
+    }
     // Error bound of a difference of two scores: that of either sigmoid and the roundings of s + bias (2^-24); for a
     // softmax the rounding of an argument below 64 and the sum's (2^-18).
     const float rel = sig ? 0x1p-20f : 0x1p-17f;
     double sum64 = 0.;
     if (limited) {
-      if (scores)
+      const bool one = gmax || a.group == 1;
+      float best = b1;
+      if (scores) {
         for (int o = a.lanes / 2; o; o >>= 1) {
           const float o1 = __shfl_xor_sync(MOE_FULL_MASK, b1, o), o2 = __shfl_xor_sync(MOE_FULL_MASK, b2, o);
           b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
           b1 = fmaxf(b1, o1);
         }
-      const bool one = gmax || a.group == 1;
-      uint32_t gk = 0;
-      if (scores) {
-        gk = grp_key(one ? b1 : b1 + b2);
+        best = one ? b1 : b1 + b2;
       } else {
 #pragma unroll
-        for (int u = 0; u < NE; ++u) gk = max(gk, key[u]);
-        for (int o = a.lanes / 2; o; o >>= 1) gk = max(gk, __shfl_xor_sync(MOE_FULL_MASK, gk, o));
+        for (int u = 0; u < NE; ++u) best = fmaxf(best, c[u]);
+        for (int o = a.lanes / 2; o; o >>= 1) best = fmaxf(best, __shfl_xor_sync(MOE_FULL_MASK, best, o));
       }
+      const uint32_t gk = g < a.n_group ? grp_key(best) : 0u;
       int before = 0;
       for (int h = 0; h < a.n_group; ++h) {
         const uint32_t ok = __shfl_sync(MOE_FULL_MASK, gk, h * a.lanes);
@@ -307,18 +320,38 @@ __global__ void __launch_bounds__(kGrpThreads) group_route_kernel(const GroupArg
       bool in = before < a.topk_group && g < a.n_group;
       if (scores) {
         const float lo = grp_value(__reduce_min_sync(MOE_FULL_MASK, in ? gk : 0xffffffffu));
-        const float hi = grp_value(__reduce_max_sync(MOE_FULL_MASK, !in && g < a.n_group ? gk : 0u));
+        const float hi = grp_value(__reduce_max_sync(MOE_FULL_MASK, !in ? gk : 0u));
         if (!(lo - hi > 2.f * (rel * (fabsf(lo) + 2.f * bmax) + kGrpTiny))) {
           // the groups in fp64, of what may be their best (without a bias a softmax's sum does not matter)
           sum64 = !sig && a.bias ? grp_sum64<BF16>(a, row, mx) : 1.;
-          const float low = one ? b1 : b2;
-          double2 x = grp_best64<V, NQ, BF16>(a, row, low - 2.f * (rel * (fabsf(low) + bmax) + kGrpTiny), mx, inv, sum64);
-          for (int o = a.lanes / 2; o; o >>= 1) {
-            const double o1 = __shfl_xor_sync(MOE_FULL_MASK, x.x, o), o2 = __shfl_xor_sync(MOE_FULL_MASK, x.y, o);
-            x.y = fmax(fmin(x.x, o1), fmax(x.y, o2));
-            x.x = fmax(x.x, o1);
+          const float low = one ? b1 : b2, least = low - 2.f * (rel * (fabsf(low) + bmax) + kGrpTiny);
+          int m = 0;
+#pragma unroll
+          for (int u = 0; u < NE; ++u) m += (a.bias ? c[u] : score(c[u])) >= least;
+          const int first = grp_scan(m);
+          double x1 = -INFINITY, x2 = -INFINITY;
+          for (int from = 0; from < m; from += 32) {  // a lane computes one of them
+            int i = first - from;
+#pragma unroll
+            for (int u = 0; u < NE; ++u)
+              if ((a.bias ? c[u] : score(c[u])) >= least) {
+                if (i >= 0 && i < 32) s_e[warp][i] = (uint16_t)expert(u);
+                ++i;
+              }
+            __syncwarp();
+            const int x = from + lane < m ? s_e[warp][lane] : -1;
+            double v = 0.;
+            if (x >= 0) v = grp_score64(grp_logit<BF16>(a.logits, row + x), sig, mx, sum64) + (a.bias ? (double)a.bias[x] : 0.);
+            for (int j = 0; j < min(32, m - from); ++j) {
+              const double o = __shfl_sync(MOE_FULL_MASK, v, j);
+              if (__shfl_sync(MOE_FULL_MASK, x, j) / a.group == g) {
+                x2 = fmax(x2, fmin(x1, o));
+                x1 = fmax(x1, o);
+              }
+            }
+            __syncwarp();
           }
-          const uint64_t gk64 = grp_key64(one ? x.x : x.x + x.y);
+          const uint64_t gk64 = g < a.n_group ? grp_key64(one ? x1 : x1 + x2) : 0ull;
           before = 0;
           for (int h = 0; h < a.n_group; ++h) {
             const uint64_t ok = __shfl_sync(MOE_FULL_MASK, gk64, h * a.lanes);
@@ -327,162 +360,145 @@ __global__ void __launch_bounds__(kGrpThreads) group_route_kernel(const GroupArg
           in = before < a.topk_group && g < a.n_group;
         }
       }
-      if (!in) {
 #pragma unroll
-        for (int u = 0; u < NE; ++u) key[u] = 0u;
-      }
+      for (int u = 0; u < NE; ++u) c[u] = in ? c[u] : kNone;
     }
-    int place = lane, e = -1;  // of the expert that this lane has, if place < k
-    float z = -INFINITY;
-    bool exact = false;
+    // the k-th largest of the lanes' best elements, or where lanes are few of their vectors'
+    float thr = -INFINITY;
     {
-      // the k-th largest of the lanes' best elements, or where lanes are few of their vectors'
-      uint32_t thr = 1u, top[NQ], best = 0;
+      float top[NQ], best = -INFINITY;
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
-        top[q] = 0;
+        top[q] = c[q * V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) top[q] = max(top[q], key[q * V + v]);
-        best = max(best, top[q]);
+        for (int v = 1; v < V; ++v) top[q] = fmaxf(top[q], c[q * V + v]);
+        best = fmaxf(best, top[q]);
       }
+      constexpr uint32_t kLowest = 0x007fffffu;  // -inf
       if (a.topk_group * a.lanes >= a.k || NQ == 1) {
+        uint32_t mine = grp_key(best);
         for (int seen = 0; seen < a.k;) {
-          const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, best);
-          if (m == 0) break;
-          const unsigned at = __ballot_sync(MOE_FULL_MASK, best == m);
-          seen += __popc(at);
-          if (seen >= a.k) thr = m;
-          if (best == m) best = 0;
+          const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, mine);
+          if (m <= kLowest) break;
+          seen += __popc(__ballot_sync(MOE_FULL_MASK, mine == m));
+          if (seen >= a.k) thr = grp_value(m);
+          if (mine == m) mine = 0;
         }
       } else {
         for (int seen = 0; seen < a.k;) {
-          const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, best);
-          if (m == 0) break;
+          const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, grp_key(best));
+          if (m <= kLowest) break;
+          const float f = grp_value(m);
           int here = 0;
-          best = 0;
+          best = -INFINITY;
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
-            here += top[q] == m;
-            if (top[q] == m) top[q] = 0;
-            best = max(best, top[q]);
+            here += top[q] == f;
+            if (top[q] == f) top[q] = -INFINITY;
+            best = fmaxf(best, top[q]);
           }
           seen += __reduce_add_sync(MOE_FULL_MASK, here);
-          if (seen >= a.k) thr = m;
+          if (seen >= a.k) thr = f;
         }
       }
-      if (a.bias && thr > 1u) {
-        const float f = grp_value(thr);
-        if (fabsf(f) < INFINITY) thr = grp_key(f - (rel * (fabsf(f) + bmax) + kGrpTiny));
-      }
-      int n = 0, mineat = 0;
+    }
+    if (a.bias && fabsf(thr) < INFINITY) thr -= rel * (fabsf(thr) + bmax) + kGrpTiny;
+    int n = 0;
 #pragma unroll
-      for (int u = 0; u < NE; ++u) n += key[u] >= thr;
-      mineat = n;
+    for (int u = 0; u < NE; ++u) n += c[u] >= thr;
+    int at = grp_scan(n);
+    int place = lane, e = -1;  // of the expert that this lane has, if place < k
+    float z = -INFINITY;
+    bool exact = n < a.k;  // NaN among the picks
+    if (n <= 32 && !exact) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(MOE_FULL_MASK, mineat, o);
-        if (lane >= o) mineat += x;
+      for (int u = 0; u < NE; ++u)
+        if (c[u] >= thr) s_e[warp][at++] = (uint16_t)expert(u);
+      __syncwarp();
+      const bool on = lane < n;
+      float bb = 0.f;
+      uint32_t mine = 0u;
+      if (on) {
+        e = s_e[warp][lane];
+        z = grp_logit<BF16>(a.logits, row + e);
+        if (a.bias) bb = a.bias[e];
+        mine = grp_key(a.bias ? score(z) + bb : z);
       }
-      mineat -= n;
-      n = __shfl_sync(MOE_FULL_MASK, mineat + n, 31);
-      if (n <= 32) {
-#pragma unroll
-        for (int u = 0; u < NE; ++u)
-          if (key[u] >= thr) {
-            s_key[warp][mineat] = key[u];
-            s_e[warp][mineat++] = e0 + u / V * step + u % V;
-          }
-      }
-      if (n <= 32) {
-        __syncwarp();
-        const bool on = lane < n;
-        const uint32_t mine = on ? s_key[warp][lane] : 0u;
-        e = on ? s_e[warp][lane] : -1;
-        __syncwarp();
-        float bb = 0.f;
-        if (on) {
-          z = grp_logit<BF16>(a.logits, row + e);
-          if (a.bias) bb = a.bias[e];
-        }
-        uint32_t above = 0xffffffffu;  // the next larger one
-        int same = 0;
-        place = 0;
+      __syncwarp();
+      uint32_t above = 0xffffffffu;  // the next larger one
+      int same = 0;
+      place = 0;
 #pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const uint32_t o = __shfl_sync(MOE_FULL_MASK, mine, j);
+        place += o > mine;
+        same += o == mine;
+        if (o > mine) above = min(above, o);
+      }
+      bool unsure = a.bias && on && place >= 1 && place <= a.k && above != 0xffffffffu && grp_close(above, mine, rel, bmax);
+      if (__any_sync(MOE_FULL_MASK, on && same > 1)) {
         for (int j = 0; j < n; ++j) {
           const uint32_t o = __shfl_sync(MOE_FULL_MASK, mine, j);
-          place += o > mine;
-          same += o == mine;
-          if (o > mine) above = min(above, o);
-        }
-        bool unsure = a.bias && on && place >= 1 && place <= a.k && above != 0xffffffffu && grp_close(above, mine, rel, bmax);
-        if (__any_sync(MOE_FULL_MASK, on && same > 1)) {
-          for (int j = 0; j < n; ++j) {
-            const uint32_t o = __shfl_sync(MOE_FULL_MASK, mine, j);
-            const int oe = __shfl_sync(MOE_FULL_MASK, e, j);
-            const float oz = __shfl_sync(MOE_FULL_MASK, z, j), ob = __shfl_sync(MOE_FULL_MASK, bb, j);
-            if (on && o == mine) {
-              place += oe < e;
-              // equal scores of other logits are equal in fp32 alone (but for infinities)
-              unsure |= a.bias && mine > 1u && fabsf(grp_value(mine)) < INFINITY && (oz != z || ob != bb);
-            }
+          const int oe = __shfl_sync(MOE_FULL_MASK, e, j);
+          const float oz = __shfl_sync(MOE_FULL_MASK, z, j), ob = __shfl_sync(MOE_FULL_MASK, bb, j);
+          if (on && o == mine) {
+            place += oe < e;
+            // equal scores of other logits are equal in fp32 alone (but for infinities)
+            unsure |= a.bias && fabsf(grp_value(mine)) < INFINITY && (oz != z || ob != bb);
           }
         }
-        if (!on) place = 32;
-        if (__any_sync(MOE_FULL_MASK, unsure)) {
-          if (!sig && sum64 == 0.) sum64 = grp_sum64<BF16>(a, row, mx);
-          const double s = sig ? 1. / (1. + exp(-(double)z)) : exp((double)z - (double)mx) / sum64;
-          const uint64_t c = on ? grp_key64(s + (double)bb) : 0ull;
-          place = on ? 0 : 32;
-          for (int j = 0; j < n; ++j) {
-            const uint64_t o = __shfl_sync(MOE_FULL_MASK, c, j);
-            const int oe = __shfl_sync(MOE_FULL_MASK, e, j);
-            place += o > c || (o == c && oe < e);
-          }
-        }
-      } else {
-        // one after the other: many are equal
-        int last = -1;
-        uint32_t ml = 0;
-        place = lane;
-        for (int j = 0; j < a.k && !exact; ++j) {
-          uint32_t best = 0;
-#pragma unroll
-          for (int u = 0; u < NE; ++u) best = max(best, key[u]);
-          const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, best);
-          int x = INT_MAX;
-#pragma unroll
-          for (int u = NE - 1; u >= 0; --u)
-            if (key[u] == m) x = e0 + u / V * step + u % V;
-          x = __reduce_min_sync(MOE_FULL_MASK, best == m ? x : INT_MAX);
-#pragma unroll
-          for (int u = 0; u < NE; ++u)
-            if (e0 + u / V * step + u % V == x) key[u] = 0u;
-          if (a.bias) {
-            if (j > 0 && grp_close(ml, m, rel, bmax))
-              exact = grp_logit<BF16>(a.logits, row + x) != grp_logit<BF16>(a.logits, row + last) || a.bias[x] != a.bias[last];
-            ml = m;
-            last = x;
-          }
-          if (lane == j) e = x;
-        }
-        if (a.bias && !exact && ml > 1u) {
-          // the last pick and what is left
-          const float ll = grp_logit<BF16>(a.logits, row + last), lb = a.bias[last];
-          const bool finite = fabsf(grp_value(ml)) < INFINITY;
-          uint32_t next = 0;
-#pragma unroll
-          for (int q = 0; q < NQ; ++q)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-              const uint32_t m = key[q * V + v];
-              if (m == ml) exact |= finite && (l[q * V + v] != ll || bias_at(q, v) != lb);
-              else next = max(next, m);
-            }
-          next = __reduce_max_sync(MOE_FULL_MASK, next);
-          exact = __any_sync(MOE_FULL_MASK, exact) || grp_close(ml, next, rel, bmax);
-        }
-        if (lane < a.k && !exact) z = grp_logit<BF16>(a.logits, row + e);
       }
+      if (!on) place = 32;
+      if (__any_sync(MOE_FULL_MASK, unsure)) {
+        if (!sig && sum64 == 0.) sum64 = grp_sum64<BF16>(a, row, mx);
+        const double s = grp_score64(z, sig, mx, sum64);
+        const uint64_t x = on ? grp_key64(s + (double)bb) : 0ull;
+        place = on ? 0 : 32;
+        for (int j = 0; j < n; ++j) {
+          const uint64_t o = __shfl_sync(MOE_FULL_MASK, x, j);
+          const int oe = __shfl_sync(MOE_FULL_MASK, e, j);
+          place += o > x || (o == x && oe < e);
+        }
+      }
+    } else if (!exact) {
+      // one after the other: many are equal
+      int last = -1;
+      uint32_t ml = 0;
+      for (int j = 0; j < a.k && !exact; ++j) {
+        float best = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < NE; ++u) best = fmaxf(best, c[u]);
+        const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, grp_key(best));
+        const float f = grp_value(m);
+        int x = INT_MAX;
+#pragma unroll
+        for (int u = NE - 1; u >= 0; --u)
+          if (c[u] == f) x = expert(u);
+        x = __reduce_min_sync(MOE_FULL_MASK, x);
+#pragma unroll
+        for (int u = 0; u < NE; ++u)
+          if (expert(u) == x) c[u] = kNone;
+        if (a.bias) {
+          if (j > 0 && grp_close(ml, m, rel, bmax))
+            exact = grp_logit<BF16>(a.logits, row + x) != grp_logit<BF16>(a.logits, row + last) || a.bias[x] != a.bias[last];
+          ml = m;
+          last = x;
+        }
+        if (lane == j) e = x;
+      }
+      if (a.bias && !exact) {
+        // the last pick and what is left
+        const float ll = grp_logit<BF16>(a.logits, row + last), lb = a.bias[last], fl = grp_value(ml);
+        float next = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < NE; ++u) {
+          if (c[u] == fl) exact |= fabsf(fl) < INFINITY && (grp_logit<BF16>(a.logits, row + expert(u)) != ll || bias_at(u) != lb);
+          else next = fmaxf(next, c[u]);
+        }
+        const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, grp_key(next));
+        exact = __any_sync(MOE_FULL_MASK, exact) || grp_close(ml, m, rel, bmax);
+      }
+      if (lane < a.k && !exact) z = grp_logit<BF16>(a.logits, row + e);
     }
     if (exact) {
       place = lane;
@@ -495,19 +511,11 @@ __global__ void __launch_bounds__(kGrpThreads) group_route_kernel(const GroupArg
     if (raw) {
       if (on) w = sig ? 1.f / (1.f + expf(-z)) : expf(z - mx) / sum;
     } else {
-      float top = __uint_as_float(0xff800000u);
-      {
-        const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, on ? grp_key(z) : 0u);
-        if (m > 1u) top = grp_value(m);
-      }
+      const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, on ? grp_key(z) : 0u);
+      const float top = m > 0x007fffffu ? grp_value(m) : 0.f;  // (0 in the place of -inf)
       if (on) {
-        if (sig) {
-          // sigmoid(z) / exp(min(top, 0)): a row of large negative logits keeps its proportions
-          const float em = expf(-fabsf(z));
-          w = expf(fminf(z, 0.f) - (top == -INFINITY ? 0.f : fminf(top, 0.f))) / (1.f + em);
-        } else {
-          w = expf(z - (top == -INFINITY ? 0.f : top));
-        }
+        // sigmoid(z) / exp(min(top, 0)): a row of large negative logits keeps its proportions
+        w = sig ? expf(fminf(z, 0.f) - fminf(top, 0.f)) / (1.f + expf(-fabsf(z))) : expf(z - top);
       }
       float all = w;
 #pragma unroll
@@ -660,10 +668,13 @@ static int grp_sms(int* sms) {
 
 template <int V, int NQ, bool BF16>
 static int launch_groups(const GroupArgs& a, int sms, cudaStream_t s) {
-  int per = a.T >= sms * 32 ? 2 : 1;
-  if (getenv("GR_PER")) per = atoi(getenv("GR_PER"));
-  constexpr int W = kGrpThreads / 32;
-  MOE_CUDA_TRY(launch_pdl(group_route_kernel<V, NQ, BF16>, dim3((a.T + W * per - 1) / (W * per)), dim3(kGrpThreads), 0, s, a, per));
+  // as many CTAs as are resident: a warp keeps the bias and has the next token's logits on their way
+  constexpr int W = kGrpThreads / 32, NE = NQ * V;
+  const dim3 grid(std::min((a.T + W - 1) / W, sms * grp_resident(NE))), block(kGrpThreads);
+  if (V > 1 && a.lanes * a.n_group == 32 && a.group == a.lanes * V * NQ)
+    MOE_CUDA_TRY(launch_pdl(group_route_kernel<V, NQ, BF16, (V > 1)>, grid, block, 0, s, a));
+  else
+    MOE_CUDA_TRY(launch_pdl(group_route_kernel<V, NQ, BF16, false>, grid, block, 0, s, a));
   return MOE_OK;
 }
 
