@@ -545,73 +545,86 @@ __device__ __forceinline__ void grp_put(void* p, size_t i, float v) {
   else reinterpret_cast<float*>(p)[i] = v;
 }
 
-// The gradient of a token's weights, one warp a token.  With W = sum_i g_i w_i / scale over its picks:
+// The gradient of a token's weights, L lanes (at least its picks) a token.  With W = sum_i g_i w_i / scale over its picks:
 //   renormalised      w_j (g_j - W)   [sigmoid: (1 - s_j)]         in the picks alone
 //   not, sigmoid      scale g_j s_j (1 - s_j)                      in the picks alone
-//   not, softmax      s_e (scale G_e - sum_i scale g_i s_i)        everywhere; G_e: the g of the picks of e
-// The row is written in whole vectors first and the picks' values over it by the same warp.  A pick that is there
-// twice adds up, in the order of the picks.
-template <int V, bool BF16>
+//   not, softmax      s_e (scale G_e - sum_i scale g_i s_i)        everywhere (DENSE); G_e: the g of the picks of e
+// The row is written in whole vectors first (NC a lane) and the picks' values over it by the same warp.  A pick that is
+// there twice adds up, in the order of the picks.  Bound by the bytes: 30,011 x 288 bf16, dense.
+template <int V, int NC, int L, bool BF16, bool DENSE>
 __global__ void __launch_bounds__(kGrpThreads) group_grad_kernel(const GroupGradArgs a) {
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const bool sig = a.flags & MOE_ROUTE_SIGMOID, raw = a.flags & MOE_ROUTE_RAW, dense = raw && !sig;
-  const int warps = gridDim.x * (kGrpThreads / 32);
-  for (int t = blockIdx.x * (kGrpThreads / 32) + (threadIdx.x >> 5); t < a.T; t += warps) {
-    const size_t row = (size_t)t * a.E;
-    int e = -1;
-    if (lane < a.k) {
-      e = a.ids[(size_t)t * a.k + lane];
-      if (e < -1 || e >= a.E) set_status(a.status, MOE_DEV_BAD_EXPERT);
-      if (e >= a.E) e = -1;
-    }
-    const bool on = e >= 0;
-    const bool any = __any_sync(MOE_FULL_MASK, on);
-    const float gj = on ? a.gw[(size_t)t * a.k + lane] * a.scale : 0.f;
-    const float z = on ? grp_logit<BF16>(a.logits, row + e) : -INFINITY;
-    float mx = 0.f, inv = 0.f;
-    float p = 0.f, jac = 1.f;  // the pick's share of the sum that its weight is over
-    if (!raw || dense) {
-      mx = z;
-      if (dense && any)
-        for (int i = lane; i < a.E; i += 32) mx = fmaxf(mx, grp_logit<BF16>(a.logits, row + i));
+  pdl_trigger();
+  constexpr float kNone = -INFINITY;
+  const int lane = threadIdx.x & 31, gl = lane % L, lead = lane - gl;
+  const bool sig = a.flags & MOE_ROUTE_SIGMOID, raw = a.flags & MOE_ROUTE_RAW;
+  const int t = (int)((blockIdx.x * (unsigned)kGrpThreads + threadIdx.x) / L);
+  const bool in = t < a.T;
+  const size_t row = (size_t)t * a.E;
+  auto total = [](float v) {
 #pragma unroll
-      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(MOE_FULL_MASK, mx, o));
-      if (mx == -INFINITY) mx = 0.f;
-    }
-    if (on) {
-      const float em = expf(-fabsf(z));
-      if (sig) jac = (z >= 0.f ? em : 1.f) / (1.f + em);
-      if (sig && raw) p = (z >= 0.f ? 1.f : em) / (1.f + em);
-      else p = sig ? expf(fminf(z, 0.f) - fminf(mx, 0.f)) / (1.f + em) : expf(z - mx);
-    }
-    float dot = 0.f;
-    if (!raw || dense) {
-      float sum = 0.f;
-      if (dense) {
-        if (any)
-          for (int i = lane; i < a.E; i += 32) sum += expf(grp_logit<BF16>(a.logits, row + i) - mx);
-      } else {
-        sum = p;
+    for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(MOE_FULL_MASK, v, o);
+    return v;
+  };
+  GrpRaw<BF16, V> x[DENSE ? NC : 1];
+  if (DENSE) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      if (in && (c * L + gl) * V < a.E) x[c].load(a.logits, row + (c * L + gl) * V);
+  }
+  int e = -1;
+  if (in && gl < a.k) {
+    e = a.ids[(size_t)t * a.k + gl];
+    if (e < -1 || e >= a.E) set_status(a.status, MOE_DEV_BAD_EXPERT);
+    if (e >= a.E) e = -1;
+  }
+  const bool on = e >= 0;
+  const float gj = on ? a.gw[(size_t)t * a.k + gl] * a.scale : 0.f;
+  const unsigned group = L == 32 ? MOE_FULL_MASK : ((1u << (L & 31)) - 1u) << lead;
+  const bool any = (__ballot_sync(MOE_FULL_MASK, on) & group) != 0;
+  const float z = on ? grp_logit<BF16>(a.logits, row + e) : kNone;
+  float p = 0.f, jac = 1.f, dot = 0.f;  // the pick's share of the sum that its weight is over
+  float q[DENSE ? NC * V : 1], inv = 0.f, mx = z;
+  if (DENSE) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        q[c * V + j] = any && (c * L + gl) * V < a.E ? x[c].at(j) : kNone;
+        mx = fmaxf(mx, q[c * V + j]);
       }
+  }
+  if (DENSE || !raw) {
 #pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(MOE_FULL_MASK, sum, o);
-      inv = sum == 0.f ? 0.f : 1.f / sum;
-      p *= inv;
-      dot = on ? p * gj : 0.f;
+    for (int o = L / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(MOE_FULL_MASK, mx, o));
+    if (mx == -INFINITY) mx = 0.f;
+  }
+  float sum = 0.f;
+  if (DENSE) {
 #pragma unroll
-      for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(MOE_FULL_MASK, dot, o);
-    }
-    // the row without its picks
-    for (int i = lane * V; i < a.E; i += 32 * V) {
+    for (int u = 0; u < NC * V; ++u) sum += q[u] = expf(q[u] - mx);
+  }
+  if (on) {
+    const float em = expf(-fabsf(z));
+    if (sig) jac = (z >= 0.f ? em : 1.f) / (1.f + em);
+    if (sig && raw) p = (z >= 0.f ? 1.f : em) / (1.f + em);
+    else p = sig ? expf(fminf(z, 0.f) - fminf(mx, 0.f)) / (1.f + em) : expf(z - mx);
+  }
+  if (DENSE || !raw) {
+    sum = total(DENSE ? sum : p);
+    inv = sum == 0.f ? 0.f : 1.f / sum;
+    p *= inv;
+    dot = total(on ? p * gj : 0.f);
+  }
+  // the row without its picks
+  if (in) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int i = (c * L + gl) * V;
+      if (i >= a.E) break;
       float v[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[j] = 0.f;
-      if (dense && any) {
-        grp_load<BF16, V>(a.logits, row + i, v);
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = expf(v[j] - mx) * inv * -dot;
-      }
+      for (int j = 0; j < V; ++j) v[j] = DENSE && any ? q[c * V + j] * inv * -dot : 0.f;
       if constexpr (V == 1) {
         grp_put<BF16>(a.grad, row + i, v[0]);
       } else {
@@ -619,8 +632,8 @@ __global__ void __launch_bounds__(kGrpThreads) group_grad_kernel(const GroupGrad
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (BF16) {
-            const __nv_bfloat162 q = __floats2bfloat162_rn(v[(2 * j) % V], v[(2 * j + 1) % V]);
-            o[j] = *reinterpret_cast<const uint32_t*>(&q);
+            const __nv_bfloat162 w = __floats2bfloat162_rn(v[(2 * j) % V], v[(2 * j + 1) % V]);
+            o[j] = *reinterpret_cast<const uint32_t*>(&w);
           } else {
             o[j] = __float_as_uint(v[j]);
           }
@@ -629,34 +642,32 @@ __global__ void __launch_bounds__(kGrpThreads) group_grad_kernel(const GroupGrad
             make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
-    __syncwarp();
-    // the picks: the first lane of a repeated one adds all of them
-    const unsigned same = __match_any_sync(MOE_FULL_MASK, on ? e : -1 - lane);
-    const bool twice = __any_sync(MOE_FULL_MASK, on && (same & (same - 1)));
-    float v;
-    if (dense) {
-      float all = gj;
-      if (twice) {
-        all = 0.f;
-        for (int j = 0; j < a.k; ++j) {
-          const float o = __shfl_sync(MOE_FULL_MASK, gj, j);
-          if (same >> j & 1) all += o;
-        }
-      }
-      v = p * (all - dot);
-    } else {
-      const float own = raw ? p * gj * jac : p * (gj - dot) * jac;
-      v = own;
-      if (twice) {
-        v = 0.f;
-        for (int j = 0; j < a.k; ++j) {
-          const float o = __shfl_sync(MOE_FULL_MASK, own, j);
-          if (same >> j & 1) v += o;
-        }
-      }
-    }
-    if (on && (same & lanemask_lt()) == 0) grp_put<BF16>(a.grad, row + e, v);
   }
+  __syncwarp();
+  // the picks: the first lane of a repeated one adds all of them
+  const unsigned same = __match_any_sync(MOE_FULL_MASK, on ? e : -1 - lane) & group;
+  float v = DENSE ? gj : raw ? p * gj * jac : p * (gj - dot) * jac;
+  if (__any_sync(MOE_FULL_MASK, on && (same & (same - 1)))) {
+    float all = 0.f;
+    for (int j = 0; j < a.k; ++j) {
+      const float o = __shfl_sync(MOE_FULL_MASK, v, lead + j);
+      if (same >> (lead + j) & 1) all += o;
+    }
+    v = all;
+  }
+  if (DENSE) v = p * (v - dot);
+  if (on && (same & lanemask_lt()) == 0) grp_put<BF16>(a.grad, row + e, v);
+}
+
+template <int V, int NC, int L, bool BF16>
+static int launch_group_grad(const GroupGradArgs& a, cudaStream_t s) {
+  constexpr int per = kGrpThreads / L;
+  const dim3 grid((a.T + per - 1) / per), block(kGrpThreads);
+  if ((a.flags & MOE_ROUTE_RAW) && !(a.flags & MOE_ROUTE_SIGMOID))
+    MOE_CUDA_TRY(launch_pdl(group_grad_kernel<V, NC, L, BF16, true>, grid, block, 0, s, a));
+  else
+    MOE_CUDA_TRY(launch_pdl(group_grad_kernel<V, NC, L, BF16, false>, grid, block, 0, s, a));
+  return MOE_OK;
 }
 
 static int grp_sms(int* sms) {
@@ -729,16 +740,31 @@ extern "C" int moe_route_groups_grad(const void* logits, int bf16, const int32_t
   if (T < 1 || T > (1 << 26) || E < 1 || E > kMaxE || k < 1 || k > kMaxK) return MOE_ERR_ARG;
   if (rflags & ~(MOE_ROUTE_SIGMOID | MOE_ROUTE_RAW)) return MOE_ERR_ARG;
   if ((uintptr_t)logits % (bf16 ? 2 : 4) || (uintptr_t)grad_logits % (bf16 ? 2 : 4)) return MOE_ERR_ALIGN;
-  int sms = 0;
-  if (int rc = grp_sms(&sms)) return rc;
   const GroupGradArgs a{logits, ids, grad_w, T, E, k, rflags, scale, grad_logits, dev_status};
   const int v = bf16 ? 8 : 4;
   const bool vec = E % v == 0 && (uintptr_t)logits % 16 == 0 && (uintptr_t)grad_logits % 16 == 0;
-  const dim3 grid(std::min((T + 7) / 8, sms * 8)), block(kGrpThreads);
   cudaStream_t s = (cudaStream_t)stream;
-  if (vec && bf16) MOE_CUDA_TRY(launch_pdl(group_grad_kernel<8, true>, grid, block, 0, s, a));
-  else if (vec) MOE_CUDA_TRY(launch_pdl(group_grad_kernel<4, false>, grid, block, 0, s, a));
-  else if (bf16) MOE_CUDA_TRY(launch_pdl(group_grad_kernel<1, true>, grid, block, 0, s, a));
-  else MOE_CUDA_TRY(launch_pdl(group_grad_kernel<1, false>, grid, block, 0, s, a));
-  return MOE_OK;
+  const int chunks = E / v;
+  if (!vec) {
+    if (bf16) {
+      if (E <= 128) return launch_group_grad<1, 4, 32, true>(a, s);
+      if (E <= 384) return launch_group_grad<1, 12, 32, true>(a, s);
+      return launch_group_grad<1, 32, 32, true>(a, s);
+    }
+    if (E <= 128) return launch_group_grad<1, 4, 32, false>(a, s);
+    if (E <= 384) return launch_group_grad<1, 12, 32, false>(a, s);
+    return launch_group_grad<1, 32, 32, false>(a, s);
+  }
+  if (bf16) {
+    if (chunks <= 16) return launch_group_grad<8, 1, 16, true>(a, s);
+    if (chunks <= 32) return launch_group_grad<8, 2, 16, true>(a, s);
+    if (chunks <= 48) return launch_group_grad<8, 3, 16, true>(a, s);
+    if (chunks <= 64) return launch_group_grad<8, 2, 32, true>(a, s);
+    return launch_group_grad<8, 4, 32, true>(a, s);
+  }
+  if (chunks <= 32) return launch_group_grad<4, 2, 16, false>(a, s);
+  if (chunks <= 64) return launch_group_grad<4, 2, 32, false>(a, s);
+  if (chunks <= 96) return launch_group_grad<4, 3, 32, false>(a, s);
+  if (chunks <= 128) return launch_group_grad<4, 4, 32, false>(a, s);
+  return launch_group_grad<4, 8, 32, false>(a, s);
 }

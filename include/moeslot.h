@@ -581,7 +581,7 @@ int moe_route_groups(const void* logits, int bf16, const float* sel_bias, const 
  *   MOE_ROUTE_RAW, softmax  grad[t][e] = scale s_e (sum_{j: ids_j = e} grad_w_j - sum_i grad_w_i s_i)
  * and 0 elsewhere.  grad_logits is written whole.
  *   ids     device int32 [T][k]; -1: no pick (a token without any gets a zero
- *           gradient; its logits are not read); a pick may be there twice
+ *           gradient, whatever its logits); a pick may be there twice
  *   grad_w  device fp32 [T][k]
  *   grad_logits  device [T][E] output in the type of logits
  * An id outside [-1, E) sets MOE_DEV_BAD_EXPERT and counts as -1.  Picks of
