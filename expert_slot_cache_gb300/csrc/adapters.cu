@@ -144,6 +144,20 @@ __global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(const AdArgs 
       if (a.kept && c == 0) a.kept[(size_t)t * a.R + r] = sum;
     }
     __syncthreads();
+    if (a.parts && c == 0) {
+      const int Rk = (a.R + 15) / 16 * 16, g8 = Rk / 8;
+      for (int i = tid; i < 2 * g8; i += kRowThreads) {
+        const int which = i / g8, r = i % g8 * 8;
+        float v[8];
+        if (which) {
+          ad_load8(a.fwd + (size_t)t * a.R, a.R, r, v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = r + j < a.R ? s_v[r + j] : 0.f;
+        }
+        ad_put_parts(a.parts + ((size_t)which * a.T + t) * 3 * Rk, Rk, r, v);
+      }
+    }
     if (!a.out) continue;
     for (int j = n0 + tid; j < n1; j += kRowThreads) {
       float acc[8] = {};
@@ -215,7 +229,7 @@ extern "C" int moe_adapters(const void* x, long long ldx, const void* base, long
       (base && !ad_rows_ok(base, ldb, N, size)) || (uintptr_t)a % 16 || (uintptr_t)b % 16)
     return MOE_ERR_ALIGN;
   const AdArgs g{(const uint16_t*)x, (const uint16_t*)a, (const uint16_t*)b, scale, ids, seq_start, base, out, kept,
-                 dev_status, ldx, base ? ldb : 0, ldo, T, K, N, R, L, n_seq};
+                 nullptr, nullptr, dev_status, ldx, base ? ldb : 0, ldo, T, K, N, R, L, n_seq};
   return ad_run(g, out_f32 != 0, (cudaStream_t)stream);
 }
 
@@ -239,14 +253,17 @@ extern "C" int moe_adapters_grad(const void* dy, long long ldy, const void* x, l
       workspace_bytes < moe_adapters_grad_workspace_bytes(T, R))
     return MOE_ERR_ALIGN;
   cudaStream_t s = (cudaStream_t)stream;
+  // dv in fp32 for the short sequences' kernel, in parts for the tiles'
   float* dv = (float*)workspace;
+  uint16_t* parts = (uint16_t*)((char*)workspace + ad256((size_t)T * R * 4));
+  const bool tiles = ad_outer_by_tiles(T, n_seq, seq_start);
   const AdArgs g{(const uint16_t*)dy, (const uint16_t*)b, (const uint16_t*)a, scale, ids, seq_start, dx ? base : nullptr,
-                 dx, dv, dev_status, ldy, dx && base ? ldb : 0, lddx, T, N, K, R, L, n_seq};
+                 dx, da && !tiles ? dv : nullptr, kept, da && tiles ? parts : nullptr, dev_status, ldy,
+                 dx && base ? ldb : 0, lddx, T, N, K, R, L, n_seq};
   if (int rc = ad_run(g, false, s)) return rc;
   if (!da) return MOE_OK;
-  const AdGradArgs o{(const uint16_t*)x, (const uint16_t*)dy, dv, kept, ids, seq_start, da, db,
-                     (uint16_t*)((char*)workspace + ad256((size_t)T * R * 4)), dev_status, ldx, ldy, T,
-                     K, N, R, L, n_seq};
+  const AdGradArgs o{(const uint16_t*)x, (const uint16_t*)dy, dv, kept, ids, seq_start, da, db, tiles ? parts : nullptr,
+                     dev_status, ldx, ldy, T, K, N, R, L, n_seq};
   int sms = 0;
   if (int rc = ad_sms(&sms)) return rc;
   return ad_launch_outer(o, sms, s);

@@ -20,6 +20,8 @@ struct AdArgs {
   const void* base;    // [T] rows of N, ldb apart, or NULL
   void* out;           // [T] rows of N, ldo apart, or NULL: the product x W1^T alone
   float* kept;         // [T][R] scale_l x W1_l^T, or NULL
+  const float* fwd;    // [T][R] or NULL: the forward pass's values,
+  uint16_t* parts;     // which go, with this pass's, into bf16 [2][T][3 Rk]: three numbers each (or NULL)
   int32_t* status;
   long long ldx, ldb, ldo;
   int T, K, N, R, L, n_seq;
@@ -72,6 +74,24 @@ __device__ __forceinline__ void ad_split8(const float (&v)[8], uint4 (&o)[NS]) {
   for (int s = 0; s < NS; ++s) o[s] = make_uint4(w[s][0], w[s][1], w[s][2], w[s][3]);
 }
 
+// Values c .. c + 7 of a row (R of them; zeros beyond) as three numbers each, [first | second | third][Rk].
+__device__ __forceinline__ void ad_put_parts(uint16_t* row, int Rk, int c, const float (&v)[8]) {
+  uint4 o[3];
+  ad_split8<3>(v, o);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(row + k * Rk + c) = o[k];
+}
+__device__ __forceinline__ void ad_load8(const float* row, int R, int c, float (&v)[8]) {
+  const float* p = row + c;
+  if (c + 8 <= R && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < R ? p[j] : 0.f;
+  }
+}
+
 // Bounded wait of a whole warp; false after a timeout, its own (flagged) or another warp's.
 __device__ __forceinline__ bool ad_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
   for (int i = 0; i < kWaitPolls; ++i) {
@@ -92,12 +112,14 @@ struct AdGradArgs {
   const int32_t* seq;
   float* da;           // [L][R][K]
   float* db;           // [L][R][N]
-  uint16_t* parts;     // bf16 [2][T][3 Rk]: dv and v as three numbers each (workspace)
+  const uint16_t* parts;  // bf16 [2][T][3 Rk]: dv and v as three numbers each, for the rows of adapters, or NULL
   int32_t* status;
   long long ldx, ldy;
   int T, K, N, R, L, n_seq;
 };
 
+// Whether the rows' sequences are long enough, on average, for tiles in the weights' gradients.
+inline bool ad_outer_by_tiles(int T, int n_seq, const int32_t* seq) { return seq && T >= 16ll * n_seq; }
 // dA and dB.
 int ad_launch_outer(const AdGradArgs& a, int sms, cudaStream_t s);
 

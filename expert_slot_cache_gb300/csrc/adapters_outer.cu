@@ -2,10 +2,10 @@
 // sequences with adapter l, in one launch.
 //
 // Longer sequences: tcgen05.  D [128 features][R] of one adapter and one block of 128 features of x or dy, summed over
-// tiles of 64 rows by TMA as they lie (features run along, so x is MN-major, and v is too).  A kernel before writes each
-// fp32 value of v and dv as three bf16 numbers (24 bits, nothing is rounded) next to each other, as columns of one
-// product that are added in the end: done in the product's kernel by its own warps, once for every block of features, it
-// took three times as long as the product.  The tensor cores truncate what they add, so that an error grows with every
+// tiles of 64 rows by TMA as they lie (features run along, so x is MN-major, and v is too).  The kernels before write
+// each fp32 value of v and dv as three bf16 numbers (24 bits, nothing is rounded) next to each other, as columns of one
+// product that are added in the end: done by this kernel's own warps, once for every block of features, it took three
+// times as long as the product.  The tensor cores truncate what they add, so that an error grows with every
 // step in one direction: after four tiles the sums are taken over into shared memory by additions that round.
 // A cluster of CTAs divides the rows of an adapter where blocks are few; their sums meet in distributed shared memory in
 // a fixed order.  x and dy are read once, which is what bounds it.  Many short sequences: a thread per two features, on the CUDA cores (the tiles would be mostly empty).
@@ -76,36 +76,6 @@ __device__ __forceinline__ float4 ao_remote(const float* p, uint32_t rank) {
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "r"(mapa_shared(smem_u32(p), rank)));
   return v;
-}
-
-// dv and v as three bf16 numbers each: [row][first | second | third part][Rk]; a thread has 8 ranks of a row.
-constexpr int kApThreads = 256;
-__global__ void __launch_bounds__(kApThreads) adapters_parts_kernel(const AdGradArgs a, int Rk) {
-  pdl_wait();
-  pdl_trigger();
-  const int g8 = Rk / 8;
-  const long long units = (long long)a.T * g8;
-  const bool vec = a.R % 4 == 0;
-  for (long long i = (long long)blockIdx.x * kApThreads + threadIdx.x; i < 2 * units; i += (long long)gridDim.x * kApThreads) {
-    const int which = i >= units;
-    const long long u = i - which * units, t = u / g8;
-    const int c = (int)(u - t * g8) * 8;
-    const float* p = (which ? a.v : a.dv) + t * a.R + c;
-    float v[8] = {};
-    if (vec && c + 8 <= a.R) {
-      const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
-      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c + j < a.R) v[j] = p[j];
-    }
-    uint4 o[3];
-    ad_split8<3>(v, o);
-    uint16_t* q = a.parts + ((size_t)which * a.T + t) * (3 * Rk) + c;
-#pragma unroll
-    for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(q + k * Rk) = o[k];
-  }
 }
 
 __global__ void __launch_bounds__(kAoThreads)
@@ -358,7 +328,7 @@ __global__ void __launch_bounds__(kAsThreads) adapters_outer_short_kernel(const 
 }
 
 int ad_launch_outer(const AdGradArgs& a, int sms, cudaStream_t s) {
-  if (!a.seq || a.T < 16ll * a.n_seq) {
+  if (!a.parts) {
     const int per = 2 * kAsThreads, blocks_a = (a.K + per - 1) / per, blocks = blocks_a + (a.N + per - 1) / per;
     MOE_CUDA_TRY(launch_pdl(adapters_outer_short_kernel, dim3(blocks, a.L, (a.R + kAsRanks - 1) / kAsRanks), dim3(kAsThreads),
                             0, s, a, blocks_a));
@@ -395,9 +365,6 @@ int ad_launch_outer(const AdGradArgs& a, int sms, cudaStream_t s) {
     const uint32_t box[3] = {64, kAoRows, 1};
     if (int rc = encode_tmap_3d_bf16(&mv, a.parts, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B)) return rc;
   }
-  const long long units = 2ll * a.T * (g.Rk / 8);
-  MOE_CUDA_TRY(launch_pdl(adapters_parts_kernel, dim3((unsigned)std::min<long long>((units + kApThreads - 1) / kApThreads, 8ll * sms)),
-                          dim3(kApThreads), 0, s, a, g.Rk));
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = g.S;

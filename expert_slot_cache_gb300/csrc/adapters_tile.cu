@@ -296,6 +296,8 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         v[j] = c + j < a.R ? v[j] * scale : 0.f;  // beyond R: zero rows of A, but x may be infinite
         if (a.kept && c + j < a.R) a.kept[(size_t)(row0 + t) * a.R + c + j] = v[j];
       }
+      if (a.parts) ad_put_parts(a.parts + (size_t)(row0 + t) * 3 * g.Rk, g.Rk, c, v);
+      if (!a.out) continue;
       uint4 o[NS];
       ad_split8<NS>(v, o);
 #pragma unroll
@@ -313,6 +315,13 @@ __global__ void __launch_bounds__(kAtThreads, 2)
       if (lane == 0) mbar_arrive(vfull);
       __syncwarp();
     }
+    if (a.parts)
+      for (int i = threadIdx.x - 64; i < mine * g8; i += 128) {
+        const int c = (i % g8) * 8, t = row0 + rank * per + i / g8;
+        float v[8];
+        ad_load8(a.fwd + (size_t)t * a.R, a.R, c, v);
+        ad_put_parts(a.parts + ((size_t)a.T + t) * 3 * g.Rk, g.Rk, c, v);
+      }
     if (a.out && copies > 1) {
       wait(vfull, 0);
       for (int i = threadIdx.x - 64; i < rows * NS * g8; i += 128) {
