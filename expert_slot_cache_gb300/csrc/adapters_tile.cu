@@ -13,7 +13,6 @@
 // v = scale x A^T enters the second product as a sum of two (bf16 results) or three (fp32 results) bf16 numbers: 16 or
 // 24 significant bits.  The products cost little beside the bytes: 2 R flops a byte of x.
 #include <algorithm>
-#include <cmath>
 
 #include "adapters.cuh"
 
@@ -503,21 +502,22 @@ int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, bool beside, cuda
   AtGeo g = {};
   const int NS = f32 ? 3 : 2;
   g.Rk = (a.R + 15) / 16 * 16;
-  // CTAs of a cluster and rows of a tile, by an estimate of the time: a CTA takes 9 us and its share of the tile's bytes
-  // at 22 KB/us (44 where it has an SM to itself); 30 clusters of 8 CTAs, 72 of 4 or 152 of 2 run at once (half of them,
-  // one CTA a SM).  Measured: 4096 rows of R 64 (2048 x 4096) 30.0 us with 8 and 128, 30.4 with 4 and 64, 35 with 2 and
-  // 32; 16,384 of R 16 (2048 x 2048) 60 with 8 and 128, 53 with 4, 49 with 2; 1024 of R 16 15.4 with 8 and 128, 12.3 with
-  // 8 and 32, 14.2 with 4 and 32; 2000 of R 128 (4096 x 4096) 29 with 4 and 64, 44 with 8 and 128.
+  // CTAs of a cluster and rows of a tile, by an estimate of the time: rounds of as many clusters as run at once, in each a
+  // CTA takes 9 us and its share of the tile's bytes at 40 KB/us, less where the CTAs' sum would pass 6.6 MB/us.
+  // Measured: 4096 rows of R 64 (2048 x 4096) 29.9 us with 8 and 128, 30.4 with 4 and 64, 34 with 4 and 128; 5120 rows 50
+  // with 4 and 64 (two rounds); 16,384 of R 16 (2048 x 2048) 60 with 8 and 128, 53 with 4, 49 with 2; 1024 of R 16 15.4
+  // with 8 and 128, 12.3 with 8 and 32, 14.2 with 4 and 32; 2000 of R 128 (4096 x 4096) 29 with 4 and 64, 44 with 8 and
+  // 128.
   int C = 8;
   double best = 0.;
   for (int c = 2; c <= 8; c *= 2)
     for (int tile = 32; tile <= kAtRows; tile *= 2) {
       if (g.Rk > 64 && f32 && tile > 64) continue;
       const double bytes = (tile * (2. * a.K + (f32 ? 4. : 2.) * (a.base ? 2 : 1) * (a.out ? a.N : 0)) + 2. * a.R * ((double)a.K + a.N)) / c;
-      const int most = (c == 8 ? 240 : c == 4 ? 288 : 304) / (g.Rk > 64 ? 2 : 1);
-      double rounds = std::max(1., ((double)a.T / tile + 1.) * c / most);
-      if (g.Rk > 64) rounds = std::ceil(rounds);  // (two CTAs a SM overlap theirs)
-      const double t = (9. + bytes / (g.Rk > 64 ? 44e3 : 22e3)) * rounds;
+      const int most = g.Rk > 64 ? (c == 8 ? 15 : c == 4 ? 36 : 76) : (c == 8 ? 35 : c == 4 ? 75 : 152);
+      const long long n = (a.T + tile - 1) / tile + a.n_seq / 2;
+      auto round = [&](long long clusters) { return 9. + bytes / std::min(40e3, 6.6e6 / ((double)clusters * c)); };
+      const double t = (double)(n / most) * round(most) + (n % most ? round(n % most) : 0.);
       if (best == 0. || t < best) best = t, C = c, g.tile = tile;
     }
   g.short_rows = short_rows;
