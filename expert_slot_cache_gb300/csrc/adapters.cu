@@ -83,8 +83,8 @@ __device__ __forceinline__ void ad_add8(const void* base, void* out, long long i
 // products, the partial sums meet in every CTA's shared memory, and CTA c computes its share of the N outputs.  One
 // launch, no workspace.
 template <bool F32>
-__global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(const AdArgs a, int max_rows) {
-  extern __shared__ __align__(16) unsigned char ad_smem[];
+__global__ void __launch_bounds__(kRowThreads, 4) adapters_row_kernel(const AdArgs a, int max_rows) {
+  __shared__ __align__(16) float s_red[kRowThreads * 8];
   __shared__ float s_part[2][kRowCluster][kAdMaxR];
   __shared__ float s_v[kAdMaxR];
   pdl_wait();
@@ -116,19 +116,39 @@ __global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(const AdArgs 
     return;
   }
   ad_cluster_arrive();
-  const int kv = a.K / 8, k0 = kv * c / kRowCluster, k1 = kv * (c + 1) / kRowCluster;
-  uint4* xs = reinterpret_cast<uint4*>(ad_smem);
+  const int kv = a.K / 8, k0 = kv * c / kRowCluster, k1 = kv * (c + 1) / kRowCluster, kn = k1 - k0;
   const uint4* w1 = reinterpret_cast<const uint4*>(a.w1 + (size_t)l * a.R * a.K) + k0;
   const uint4* w2 = reinterpret_cast<const uint4*>(a.w2 + (size_t)l * a.R * a.N);
+  // outputs: `wide` threads side by side, the ranks divided among groups of them.  The first weights of both products
+  // are on their way before anything is waited for.
+  int wide = 32;
+  while (wide < n1 - n0 && wide < kRowThreads) wide *= 2;
+  const int groups = kRowThreads / wide, rg = tid / wide, j0 = n0 + tid % wide;
+  constexpr int P1 = 2, P2 = 4;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 h1[P1], h2[P2];
+#pragma unroll
+  for (int i = 0; i < P1; ++i) {
+    const int r = warp + i * (kRowThreads / 32);
+    h1[i] = lane < kn && r < a.R ? w1[(size_t)r * kv + lane] : zero;
+  }
+#pragma unroll
+  for (int i = 0; i < P2; ++i) {
+    const int r = rg + i * groups;
+    h2[i] = a.out && j0 < n1 && r < a.R ? w2[(size_t)r * nv + j0] : zero;
+  }
+  const float scale = a.scale[l];
   ad_cluster_wait();  // the other CTAs have started
   for (int t = t0; t < t1; ++t) {
     float(*part)[kAdMaxR] = s_part[t & 1];
     const uint4* xr = reinterpret_cast<const uint4*>(a.x + t * a.ldx) + k0;
-    for (int i = tid; i < k1 - k0; i += kRowThreads) xs[i] = xr[i];
-    __syncthreads();
-    for (int r = warp; r < a.R; r += kRowThreads / 32) {
-      float sum = 0.f;
-      for (int i = lane; i < k1 - k0; i += 32) sum = ad_dot8(xs[i], w1[(size_t)r * kv + i], sum);
+    const uint4 x0 = lane < kn ? xr[lane] : zero;
+#pragma unroll 2
+    for (int i = 0; warp + i * (kRowThreads / 32) < a.R; ++i) {
+      const int r = warp + i * (kRowThreads / 32);
+      const uint4 first = i == 0 ? h1[0] : i == 1 ? h1[1] : lane < kn ? w1[(size_t)r * kv + lane] : zero;
+      float sum = ad_dot8(x0, first, 0.f);
+      for (int k = lane + 32; k < kn; k += 32) sum = ad_dot8(xr[k], w1[(size_t)r * kv + k], sum);
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(MOE_FULL_MASK, sum, o);
       if (lane < kRowCluster) ad_store_remote(&part[c][r], lane, sum);
@@ -139,7 +159,7 @@ __global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(const AdArgs 
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < kRowCluster; ++i) sum += part[i][r];
-      sum *= a.scale[l];
+      sum *= scale;
       s_v[r] = sum;
       if (a.kept && c == 0) a.kept[(size_t)t * a.R + r] = sum;
     }
@@ -158,12 +178,33 @@ __global__ void __launch_bounds__(kRowThreads) adapters_row_kernel(const AdArgs 
         ad_put_parts(a.parts + ((size_t)which * a.T + t) * 3 * Rk, Rk, r, v);
       }
     }
-    if (!a.out) continue;
-    for (int j = n0 + tid; j < n1; j += kRowThreads) {
-      float acc[8] = {};
-      for (int r = 0; r < a.R; ++r) ad_axpy8(s_v[r], w2[(size_t)r * nv + j], acc);
-      ad_add8<F32>(a.base, a.out, t * a.ldb + 8 * j, t * a.ldo + 8 * j, acc);
-    }
+    if (a.out)
+      for (int from = n0; from < n1; from += wide) {  // (the same rounds for every thread)
+        const int j = from + tid % wide;
+        float acc[8] = {};
+        if (j < n1) {
+#pragma unroll
+          for (int i = 0; i < P2; ++i) {
+            const int r = rg + i * groups;
+            if (r < a.R) ad_axpy8(s_v[r], from == n0 ? h2[i] : w2[(size_t)r * nv + j], acc);
+          }
+#pragma unroll 4
+          for (int r = rg + P2 * groups; r < a.R; r += groups) ad_axpy8(s_v[r], w2[(size_t)r * nv + j], acc);
+        }
+        if (groups > 1) {
+          if (rg > 0)
+#pragma unroll
+            for (int i = 0; i < 8; i += 4)
+              *reinterpret_cast<float4*>(&s_red[(tid - wide) * 8 + i]) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+          __syncthreads();
+          if (rg == 0)
+            for (int q = 0; q < groups - 1; ++q)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) acc[i] += s_red[(q * wide + tid) * 8 + i];
+        }
+        if (rg == 0 && j < n1) ad_add8<F32>(a.base, a.out, t * a.ldb + 8 * j, t * a.ldo + 8 * j, acc);
+      }
+    __syncthreads();  // s_v and s_red are free again
   }
 }
 
@@ -178,7 +219,6 @@ static int ad_launch_rows(const AdArgs& a, bool f32, int units, int max_rows, cu
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)units * kRowCluster);
   cfg.blockDim = dim3(kRowThreads);
-  cfg.dynamicSmemBytes = (size_t)(a.K / 8 / kRowCluster + 1) * 16;
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 2;
