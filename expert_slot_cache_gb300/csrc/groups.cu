@@ -24,6 +24,7 @@ struct GroupArgs {
   int T, E, k;
   int n_group, group, topk_group;  // group = E / n_group experts
   int lanes;                       // lanes of a group: a power of two
+  uint32_t magic;                  // ceil(2^20 / group): e magic / 2^20 is the group of e < 1024
   int flags;
   float scale;
   int32_t* ids;
@@ -125,28 +126,27 @@ __device__ __forceinline__ int grp_scan(int& n) {
   return at;
 }
 
-// The picks of one token in fp64, by the whole warp; lane j returns pick j.  A lane holds the experts it holds in
-// the kernel below: group lane / lanes, vectors lane % lanes + q lanes of V.
-template <int V, int NQ, bool BF16>
+// The picks of one token in fp64, by the whole warp; lane j returns pick j.  A lane holds every lanes-th expert of
+// group lane / lanes, which are at most 64.
+template <bool BF16>
 __device__ __noinline__ int grp_pick64(const GroupArgs& a, size_t row) {
   const int lane = threadIdx.x & 31, g = lane / a.lanes, i0 = lane % a.lanes;
   const bool sig = a.flags & MOE_ROUTE_SIGMOID;
-  uint64_t key[NQ * V];
+  constexpr int NE = 64;
+  uint64_t key[NE];
+  const int held = g < a.n_group ? (a.group - i0 + a.lanes - 1) / a.lanes : 0;
   double mx = -INFINITY, sum = 0.;
-  auto at = [&](int u) {  // the lane's u-th expert, or -1
-    const int i = (u / V * a.lanes + i0) * V + u % V;
-    return g < a.n_group && i < a.group ? g * a.group + i : -1;
-  };
+  auto at = [&](int u) { return u < held ? g * a.group + u * a.lanes + i0 : -1; };  // the lane's u-th expert, or -1
   if (!sig) {
-    for (int u = 0; u < NQ * V; ++u)
+    for (int u = 0; u < held; ++u)
       if (at(u) >= 0) mx = fmax(mx, (double)grp_logit<BF16>(a.logits, row + at(u)));
     for (int o = 16; o; o >>= 1) mx = fmax(mx, __shfl_xor_sync(MOE_FULL_MASK, mx, o));
-    for (int u = 0; u < NQ * V; ++u)
+    for (int u = 0; u < held; ++u)
       if (at(u) >= 0) sum += exp((double)grp_logit<BF16>(a.logits, row + at(u)) - mx);
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(MOE_FULL_MASK, sum, o);
   }
   double b1 = -INFINITY, b2 = -INFINITY;
-  for (int u = 0; u < NQ * V; ++u) {
+  for (int u = 0; u < held; ++u) {
     const int e = at(u);
     key[u] = 0;
     if (e < 0) continue;
@@ -166,7 +166,7 @@ __device__ __noinline__ int grp_pick64(const GroupArgs& a, size_t row) {
     uint64_t gk;
     if (a.flags & MOE_ROUTE_GROUP_MAX) {
       gk = 0;
-      for (int u = 0; u < NQ * V; ++u) gk = max(gk, key[u]);
+      for (int u = 0; u < held; ++u) gk = max(gk, key[u]);
       for (int o = a.lanes / 2; o; o >>= 1) gk = max(gk, __shfl_xor_sync(MOE_FULL_MASK, gk, o));
     } else {
       gk = grp_key64(a.group == 1 ? b1 : b1 + b2);
@@ -177,18 +177,18 @@ __device__ __noinline__ int grp_pick64(const GroupArgs& a, size_t row) {
       before += ok > gk || (ok == gk && h < g);
     }
     if (before >= a.topk_group)
-      for (int u = 0; u < NQ * V; ++u) key[u] = 0;
+      for (int u = 0; u < held; ++u) key[u] = 0;
   }
   int mine = -1;
   for (int j = 0; j < a.k; ++j) {
     uint64_t best = 0;
-    for (int u = 0; u < NQ * V; ++u) best = max(best, key[u]);
+    for (int u = 0; u < held; ++u) best = max(best, key[u]);
     const uint64_t m = grp_max64(best);
     int e = INT_MAX;
-    for (int u = NQ * V - 1; u >= 0; --u)
+    for (int u = held - 1; u >= 0; --u)
       if (key[u] == m && at(u) >= 0) e = at(u);
     e = __reduce_min_sync(MOE_FULL_MASK, e);
-    for (int u = 0; u < NQ * V; ++u)
+    for (int u = 0; u < held; ++u)
       if (at(u) == e) key[u] = 0;
     if (lane == j) mine = e;
   }
@@ -196,20 +196,21 @@ __device__ __noinline__ int grp_pick64(const GroupArgs& a, size_t row) {
 }
 
 // CTAs of a SM (16,384 x 512, 16 elements a lane: 37 us with two, 41 with three and registers in memory, 42 with four).
-constexpr int grp_resident(int elements) { return elements <= 8 ? 3 : elements <= 32 ? 2 : 1; }
+constexpr int grp_resident(int elements) { return elements <= 8 ? 3 : 2; }
 
-// One warp routes a token.  Lane (g, i) holds the vectors i, i + lanes, ... of V experts of group g, so that a group's
-// score takes log2(lanes) shuffles.  FULL: every lane holds NQ vectors.
+// One warp routes a token.  Where the groups fill the lanes, lane (g, i) holds the vectors i, i + lanes, ... of V experts
+// of group g, so that a group's score takes log2(lanes) shuffles.  FLAT: the lanes hold the row's vectors in turn, and the
+// groups' scores are taken from shared memory.
 //
 // The k best: k of the lanes' best elements are at or above the k-th largest of them, so only elements at or above it (a
 // tolerance below it, with a bias) can be picked.  They are some 12 to 16 as a rule; a lane takes each, and its place is
 // the number of those that are larger.  (k maxima one after the other, each over all elements, took twice as long;
 // they remain for tokens with more than 32 such elements, which have many equal logits.)
-template <int V, int NQ, bool BF16, bool FULL>
+template <int V, int NQ, bool BF16, bool FLAT>
 __global__ void __launch_bounds__(kGrpThreads, grp_resident(NQ * V)) group_route_kernel(const GroupArgs a) {
   constexpr int NE = NQ * V;
-  constexpr bool kKeepBias = NE <= 32;  // in registers
   __shared__ uint16_t s_e[kGrpThreads / 32][32];
+  __shared__ float s_c[FLAT ? kGrpThreads / 32 : 1][FLAT ? kMaxE : 1], s_least[FLAT ? kGrpThreads / 32 : 1][32];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane / a.lanes, i0 = lane % a.lanes;
@@ -217,45 +218,41 @@ __global__ void __launch_bounds__(kGrpThreads, grp_resident(NQ * V)) group_route
   const bool limited = a.topk_group < a.n_group;
   const bool scores = a.bias || (limited && !gmax);  // scores are needed for the choice
   const bool total = !sig && (scores || raw);         // the softmax over all experts is
-  const int e0 = g * a.group + i0 * V;               // vector q starts at expert e0 + q lanes V
-  const int step = a.lanes * V;
-  const int held = FULL ? NQ : g < a.n_group ? max(0, a.group - i0 * V + step - 1) / step : 0;  // vectors of this lane
+  const int e0 = FLAT ? lane * V : g * a.group + i0 * V;  // vector q starts at expert e0 + q step
+  const int step = FLAT ? 32 * V : a.lanes * V;
   const float kNone = __uint_as_float(0x7fffffffu);  // NaN: at or above nothing
-  float bias[kKeepBias ? NE : 1], bmax = 0.f;
-  auto bias_at = [&](int u) {
-    return kKeepBias ? bias[u] : u / V < held ? a.bias[e0 + u / V * step + u % V] : 0.f;
-  };
+  float bias[NE], bmax = 0.f;
   auto expert = [&](int u) { return e0 + u / V * step + u % V; };
-  // a token's logits are on their way while the one before is routed, where registers suffice
-  constexpr bool kAhead = NE <= 32;
+  auto there = [&](int u) { return !FLAT || expert(u) < a.E; };
+  auto group_of = [&](int u) { return FLAT ? (int)((uint32_t)expert(u) * a.magic >> 20) : g; };
+  // a token's logits are on their way while the one before is routed
   GrpRaw<BF16, V> next[NQ];
   bool valid = true;
   auto fetch = [&](int t) {
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
-      if (FULL || q < held) next[q].load(a.logits, (size_t)t * a.E + e0 + q * step);
+      if (there(q * V)) next[q].load(a.logits, (size_t)t * a.E + e0 + q * step);
     valid = !a.mask || a.mask[t];
   };
   const int warps = gridDim.x * (kGrpThreads / 32);
   int t = blockIdx.x * (kGrpThreads / 32) + warp;
-  if (kAhead && t < a.T) fetch(t);
+  if (t < a.T) fetch(t);
   if (a.bias) {
 #pragma unroll
     for (int u = 0; u < NE; ++u) {
-      const float b = FULL || u / V < held ? a.bias[expert(u)] : 0.f;
-      if (kKeepBias) bias[u] = b;
+      const float b = there(u) ? a.bias[expert(u)] : 0.f;
+      bias[u] = b;
       if (fabsf(b) < INFINITY) bmax = fmaxf(bmax, fabsf(b));
     }
     bmax = __uint_as_float(__reduce_max_sync(MOE_FULL_MASK, __float_as_uint(bmax)));
   }
   for (; t < a.T; t += warps) {
     const size_t row = (size_t)t * a.E;
-    if (!kAhead) fetch(t);
     float c[NE];  // the logits, then what is compared; kNone for what is not there
 #pragma unroll
-    for (int u = 0; u < NE; ++u) c[u] = FULL || u / V < held ? next[u / V].at(u % V) : kNone;
+    for (int u = 0; u < NE; ++u) c[u] = there(u) ? next[u / V].at(u % V) : kNone;
     const bool padding = !valid;
-    if (kAhead && t + warps < a.T) fetch(t + warps);
+    if (t + warps < a.T) fetch(t + warps);
     if (padding) {
       if (lane < a.k) {
         a.ids[(size_t)t * a.k + lane] = -1;
@@ -273,23 +270,35 @@ __global__ void __launch_bounds__(kGrpThreads, grp_resident(NQ * V)) group_route
       sum = 0.f;
 #pragma unroll
       for (int u = 0; u < NE; ++u)
-        if (FULL || u / V < held) sum += expf(c[u] - mx);
+        if (there(u)) sum += expf(c[u] - mx);
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(MOE_FULL_MASK, sum, o);
       inv = 1.f / sum;
     }
     auto score = [&](float l) { return sig ? grp_sigmoid(l) : expf(l - mx) * inv; };
-    float b1 = -INFINITY, b2 = -INFINITY;
     if (a.bias) {
 #pragma unroll
-      for (int u = 0; u < NE; ++u) c[u] = score(c[u]) + bias_at(u);
+      for (int u = 0; u < NE; ++u) c[u] = score(c[u]) + bias[u];
     }
-    if (limited && scores) {
-#pragma unroll
-      for (int u = 0; u < NE; ++u) {
-        const float v = a.bias ? c[u] : score(c[u]);
+    // the two best of the lane's part of its group (without a sum of scores: of what is compared)
+    float b1 = -INFINITY, b2 = -INFINITY;
+    if (limited) {
+      auto better = [&](float v) {
         b2 = fmaxf(b2, fminf(b1, v == v ? v : -INFINITY));
         b1 = fmaxf(b1, v);
+      };
+      const bool compared = a.bias || gmax;
+      if constexpr (FLAT) {
+#pragma unroll
+        for (int u = 0; u < NE; ++u)
+          if (there(u)) s_c[warp][expert(u)] = compared ? c[u] : score(c[u]);
+        __syncwarp();
+        if (g < a.n_group)
+          for (int i = i0; i < a.group; i += a.lanes) better(s_c[warp][g * a.group + i]);
+        __syncwarp();
+      } else {
+#pragma unroll
+        for (int u = 0; u < NE; ++u) better(compared ? c[u] : score(c[u]));
       }
     }
     // Error bound of a difference of two scores: that of either sigmoid and the roundings of s + bias (2^-24); for a
@@ -298,19 +307,12 @@ __global__ void __launch_bounds__(kGrpThreads, grp_resident(NQ * V)) group_route
     double sum64 = 0.;
     if (limited) {
       const bool one = gmax || a.group == 1;
-      float best = b1;
-      if (scores) {
-        for (int o = a.lanes / 2; o; o >>= 1) {
-          const float o1 = __shfl_xor_sync(MOE_FULL_MASK, b1, o), o2 = __shfl_xor_sync(MOE_FULL_MASK, b2, o);
-          b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
-          b1 = fmaxf(b1, o1);
-        }
-        best = one ? b1 : b1 + b2;
-      } else {
-#pragma unroll
-        for (int u = 0; u < NE; ++u) best = fmaxf(best, c[u]);
-        for (int o = a.lanes / 2; o; o >>= 1) best = fmaxf(best, __shfl_xor_sync(MOE_FULL_MASK, best, o));
+      for (int o = a.lanes / 2; o; o >>= 1) {
+        const float o1 = __shfl_xor_sync(MOE_FULL_MASK, b1, o), o2 = __shfl_xor_sync(MOE_FULL_MASK, b2, o);
+        b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+        b1 = fmaxf(b1, o1);
       }
+      const float best = one ? b1 : b1 + b2;
       const uint32_t gk = g < a.n_group ? grp_key(best) : 0u;
       int before = 0;
       for (int h = 0; h < a.n_group; ++h) {
@@ -325,16 +327,21 @@ __global__ void __launch_bounds__(kGrpThreads, grp_resident(NQ * V)) group_route
           // the groups in fp64, of what may be their best (without a bias a softmax's sum does not matter)
           sum64 = !sig && a.bias ? grp_sum64<BF16>(a, row, mx) : 1.;
           const float low = one ? b1 : b2, least = low - 2.f * (rel * (fabsf(low) + bmax) + kGrpTiny);
+          if constexpr (FLAT) {
+            if (i0 == 0) s_least[warp][g] = least;
+            __syncwarp();
+          }
+          auto near = [&](int u) { return (a.bias ? c[u] : score(c[u])) >= (FLAT ? s_least[warp][group_of(u) & 31] : least); };
           int m = 0;
 #pragma unroll
-          for (int u = 0; u < NE; ++u) m += (a.bias ? c[u] : score(c[u])) >= least;
+          for (int u = 0; u < NE; ++u) m += near(u);
           const int first = grp_scan(m);
           double x1 = -INFINITY, x2 = -INFINITY;
           for (int from = 0; from < m; from += 32) {  // a lane computes one of them
             int i = first - from;
 #pragma unroll
             for (int u = 0; u < NE; ++u)
-              if ((a.bias ? c[u] : score(c[u])) >= least) {
+              if (near(u)) {
                 if (i >= 0 && i < 32) s_e[warp][i] = (uint16_t)expert(u);
                 ++i;
               }
@@ -360,8 +367,14 @@ __global__ void __launch_bounds__(kGrpThreads, grp_resident(NQ * V)) group_route
           in = before < a.topk_group && g < a.n_group;
         }
       }
+      if constexpr (FLAT) {
+        const unsigned live = __ballot_sync(MOE_FULL_MASK, in);  // (bit h lanes: group h)
 #pragma unroll
-      for (int u = 0; u < NE; ++u) c[u] = in ? c[u] : kNone;
+        for (int u = 0; u < NE; ++u) c[u] = live >> ((group_of(u) * a.lanes) & 31) & 1 ? c[u] : kNone;
+      } else {
+#pragma unroll
+        for (int u = 0; u < NE; ++u) c[u] = in ? c[u] : kNone;
+      }
     }
     // the k-th largest of the lanes' best elements, or where lanes are few of their vectors'
     float thr = -INFINITY;
@@ -375,7 +388,7 @@ __global__ void __launch_bounds__(kGrpThreads, grp_resident(NQ * V)) group_route
         best = fmaxf(best, top[q]);
       }
       constexpr uint32_t kLowest = 0x007fffffu;  // -inf
-      if (a.topk_group * a.lanes >= a.k || NQ == 1) {
+      if (FLAT || a.topk_group * a.lanes >= a.k || NQ == 1) {
         uint32_t mine = grp_key(best);
         for (int seen = 0; seen < a.k;) {
           const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, mine);
@@ -492,7 +505,7 @@ __global__ void __launch_bounds__(kGrpThreads, grp_resident(NQ * V)) group_route
         float next = -INFINITY;
 #pragma unroll
         for (int u = 0; u < NE; ++u) {
-          if (c[u] == fl) exact |= fabsf(fl) < INFINITY && (grp_logit<BF16>(a.logits, row + expert(u)) != ll || bias_at(u) != lb);
+          if (c[u] == fl) exact |= fabsf(fl) < INFINITY && (grp_logit<BF16>(a.logits, row + expert(u)) != ll || bias[u] != lb);
           else next = fmaxf(next, c[u]);
         }
         const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, grp_key(next));
@@ -502,7 +515,7 @@ __global__ void __launch_bounds__(kGrpThreads, grp_resident(NQ * V)) group_route
     }
     if (exact) {
       place = lane;
-      e = grp_pick64<V, NQ, BF16>(a, row);
+      e = grp_pick64<BF16>(a, row);
       if (lane < a.k) z = grp_logit<BF16>(a.logits, row + e);
     }
     // weights, over the lanes with a place
@@ -682,10 +695,10 @@ static int launch_groups(const GroupArgs& a, int sms, cudaStream_t s) {
   // as many CTAs as are resident: a warp keeps the bias and has the next token's logits on their way
   constexpr int W = kGrpThreads / 32, NE = NQ * V;
   const dim3 grid(std::min((a.T + W - 1) / W, sms * grp_resident(NE))), block(kGrpThreads);
-  if (V > 1 && a.lanes * a.n_group == 32 && a.group == a.lanes * V * NQ)
-    MOE_CUDA_TRY(launch_pdl(group_route_kernel<V, NQ, BF16, (V > 1)>, grid, block, 0, s, a));
+  if (V > 1 && a.lanes * a.n_group == 32 && a.group == a.lanes * NE)
+    MOE_CUDA_TRY(launch_pdl(group_route_kernel<V, NQ, BF16, (V == 1)>, grid, block, 0, s, a));
   else
-    MOE_CUDA_TRY(launch_pdl(group_route_kernel<V, NQ, BF16, false>, grid, block, 0, s, a));
+    MOE_CUDA_TRY(launch_pdl(group_route_kernel<V, NQ, BF16, true>, grid, block, 0, s, a));
   return MOE_OK;
 }
 
@@ -707,30 +720,30 @@ extern "C" int moe_route_groups(const void* logits, int bf16, const float* sel_b
   int lanes = 32;
   while (lanes * n_group > 32) lanes /= 2;
   const int group = E / n_group;
-  const GroupArgs a{logits, sel_bias, token_mask, T, E, k, n_group, group, topk_group, lanes, rflags, scale, ids, w};
+  const GroupArgs a{logits, sel_bias, token_mask, T, E, k, n_group, group, topk_group, lanes,
+                    (uint32_t)(((1 << 20) + group - 1) / group), rflags, scale, ids, w};
   cudaStream_t s = (cudaStream_t)stream;
-  const int v = bf16 ? 8 : 4;
-  const int each = (group + lanes - 1) / lanes;  // experts of a lane
-  const int quads = (group + lanes * v - 1) / (lanes * v);
-  if (group % v == 0 && (uintptr_t)logits % 16 == 0 && quads * v <= 32) {
+  // 16-byte vectors where every row starts on one
+  const int v = bf16 ? 8 : 4, each = (E + 31) / 32, vecs = (E / v + 31) / 32;  // of a lane
+  if (E % v == 0 && (uintptr_t)logits % 16 == 0) {
     if (bf16) {
-      if (quads <= 1) return launch_groups<8, 1, true>(a, sms, s);
-      if (quads <= 2) return launch_groups<8, 2, true>(a, sms, s);
+      if (vecs <= 1) return launch_groups<8, 1, true>(a, sms, s);
+      if (vecs <= 2) return launch_groups<8, 2, true>(a, sms, s);
       return launch_groups<8, 4, true>(a, sms, s);
     }
-    if (quads <= 1) return launch_groups<4, 1, false>(a, sms, s);
-    if (quads <= 2) return launch_groups<4, 2, false>(a, sms, s);
-    if (quads <= 4) return launch_groups<4, 4, false>(a, sms, s);
+    if (vecs <= 1) return launch_groups<4, 1, false>(a, sms, s);
+    if (vecs <= 2) return launch_groups<4, 2, false>(a, sms, s);
+    if (vecs <= 4) return launch_groups<4, 4, false>(a, sms, s);
     return launch_groups<4, 8, false>(a, sms, s);
   }
   if (bf16) {
     if (each <= 4) return launch_groups<1, 4, true>(a, sms, s);
     if (each <= 16) return launch_groups<1, 16, true>(a, sms, s);
-    return launch_groups<1, 64, true>(a, sms, s);
+    return launch_groups<1, 32, true>(a, sms, s);
   }
   if (each <= 4) return launch_groups<1, 4, false>(a, sms, s);
   if (each <= 16) return launch_groups<1, 16, false>(a, sms, s);
-  return launch_groups<1, 64, false>(a, sms, s);
+  return launch_groups<1, 32, false>(a, sms, s);
 }
 
 extern "C" int moe_route_groups_grad(const void* logits, int bf16, const int32_t* ids, const float* grad_w, int T, int E,
