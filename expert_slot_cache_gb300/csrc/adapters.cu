@@ -263,7 +263,7 @@ extern "C" int moe_adapters(const void* x, long long ldx, const void* base, long
                             int32_t* dev_status, moe_stream_t stream) {
   if (!x || !a || !b || !scale || !ids || !out || (out_f32 != 0 && out_f32 != 1)) return MOE_ERR_ARG;
   if (!ad_shape(T, K, N, R, L, seq_start, n_seq)) return MOE_ERR_ARG;
-  if (ldx < K || ldo < N || (base && ldb < N)) return MOE_ERR_ARG;
+  if (ldx < K || ldo < N || (base && ldb < N) || out == x || (out == base && ldb != ldo)) return MOE_ERR_ARG;
   const int size = out_f32 ? 4 : 2;
   if (K % 8 || N % 8 || !ad_rows_ok(x, ldx, K, 2) || !ad_rows_ok(out, ldo, N, size) ||
       (base && !ad_rows_ok(base, ldb, N, size)) || (uintptr_t)a % 16 || (uintptr_t)b % 16)
@@ -287,6 +287,7 @@ extern "C" int moe_adapters_grad(const void* dy, long long ldy, const void* x, l
     return MOE_ERR_ARG;
   if (!ad_shape(T, K, N, R, L, seq_start, n_seq)) return MOE_ERR_ARG;
   if (ldy < N || (da && ldx < K) || (dx && lddx < K) || (dx && base && ldb < K)) return MOE_ERR_ARG;
+  if (dx && (dx == dy || dx == x || (dx == base && ldb != lddx))) return MOE_ERR_ARG;
   if (K % 8 || N % 8 || !ad_rows_ok(dy, ldy, N, 2) || (da && !ad_rows_ok(x, ldx, K, 2)) ||
       (dx && !ad_rows_ok(dx, lddx, K, 2)) || (dx && base && !ad_rows_ok(base, ldb, K, 2)) || (uintptr_t)a % 16 ||
       (uintptr_t)b % 16 || (uintptr_t)da % 16 || (uintptr_t)db % 16 || (uintptr_t)workspace % 256 ||

@@ -610,16 +610,20 @@ int moe_route_groups_grad(const void* logits, int bf16, const int32_t* ids, cons
  *   seq_start  device int32 [n_seq + 1], ascending, empty sequences allowed, or
  *           NULL with n_seq = T: every row is a sequence of its own (decoding).
  *           Rows before the first and behind the last sequence have no adapter.
- *   out     device [T] rows of N, ldo apart: bf16, or fp32 with out_f32 = 1
+ *   out     device [T] rows of N, ldo apart: bf16, or fp32 with out_f32 = 1; rows
+ *           of x and out do not overlap
  *   kept    device fp32 [T][R] output, v (0 without an adapter), for the gradient,
  *           or NULL
- * Sums are fp32; the result does not depend on thread timing.  x of a row
- * reaches no other row.
+ * Sums are fp32; v takes part in its product with 16 significant bits (24 for
+ * fp32 results) where sequences are long.  The result does not depend on thread
+ * timing; its last bits depend on the batch's sequences.  x of a row reaches no
+ * other row.  (Waits are bounded: one that gives up sets MOE_DEV_TIMEOUT.)
  * An id outside [-1, L) sets MOE_DEV_BAD_EXPERT and counts as -1; a descending
  * seq_start sets MOE_DEV_BAD_GROUPS.
  * Errors: MOE_ERR_ARG on NULL pointers, T not in [1, 2^24], K or N not in
- * [8, 2^17], R not in [1, 128], L not in [1, 65535], n_seq < 1 or leading
- * dimensions too small; MOE_ERR_ALIGN if K or N is no multiple of 8, or a matrix
+ * [8, 2^17], R not in [1, 128], L not in [1, 65535], n_seq not in [1, 2^24],
+ * leading dimensions too small, out = x, or out = base with another leading
+ * dimension; MOE_ERR_ALIGN if K or N is no multiple of 8, or a matrix
  * or a row of one does not start on 16 bytes.
  */
 int moe_adapters(const void* x, long long ldx, const void* base, long long ldb, int T, int K, int N, int R, int L,
@@ -637,12 +641,15 @@ int moe_adapters(const void* x, long long ldx, const void* base, long long ldb, 
  *   x, kept as in and from moe_adapters (not needed without da and db)
  *   base    device bf16 [T] rows of K, ldb apart, or NULL: the gradient in x of
  *           the projection itself; it may be dx
- *   dx      device bf16 [T] rows of K, lddx apart, or NULL
+ *   dx      device bf16 [T] rows of K, lddx apart, or NULL; it overlaps neither
+ *           dy nor x
  *   da, db  device fp32 [L][R][K] and [L][R][N], written whole (0 for adapters
  *           without rows), or both NULL
  *   workspace  device, moe_adapters_grad_workspace_bytes(T, R), 256-byte aligned
- * Sums are fp32, in an order that does not depend on thread timing.
- * Errors: as moe_adapters; MOE_ERR_ARG without dx, da and db; MOE_ERR_ALIGN for
+ * Sums are fp32, in an order that does not depend on thread timing; dv and kept
+ * take part in da and db with all their bits.
+ * Errors: as moe_adapters; MOE_ERR_ARG without dx, da and db, with only one of
+ * da and db, or dx = dy or x; MOE_ERR_ALIGN for
  * an unaligned or small workspace.
  */
 size_t moe_adapters_grad_workspace_bytes(int T, int R);

@@ -33,9 +33,12 @@ def test_forward(b, p):
     assert call(R=0) == ARG and call(R=129) == ARG and call(L=0) == ARG and call(L=65536) == ARG
     assert call(n=0) == ARG and call(seq=None, n=3) == ARG and call(f32=2) == ARG
     assert call(ldx=56) == ARG and call(ldo=24) == ARG and call(ldb=24) == ARG
-    assert call(K=60) == ALIGN and call(N=30, ldo=32, ldb=32) == ALIGN and call(ldx=68) == ALIGN and call(ldo=36) == ALIGN
-    assert call(ldb=36) == ALIGN and call(x=p + 2) == ALIGN and call(out=p + 8) == ALIGN and call(base=p + 8) == ALIGN
-    assert call(a=p + 8) == ALIGN and call(w=p + 8) == ALIGN and call(ldo=34, f32=1) == ALIGN
+    assert call() == ARG  # out is x
+    q = p + 4096
+    assert call(out=q, base=q, ldb=40) == ARG and call(n=(1 << 24) + 1) == ARG
+    for kw in (dict(K=60), dict(N=30), dict(ldx=68), dict(ldo=36), dict(ldb=36), dict(x=p + 2), dict(out=q + 8), dict(base=p + 8),
+               dict(a=p + 8), dict(w=p + 8), dict(ldo=34, f32=1)):
+        assert call(**dict(dict(out=q), **kw)) == ALIGN, kw
 
 
 def test_gradient(b, p):
@@ -49,8 +52,11 @@ def test_gradient(b, p):
     assert call(dx=None, da=None, db=None) == ARG
     assert call(T=0) == ARG and call(R=129) == ARG and call(L=0) == ARG and call(seq=None) == ARG
     assert call(ldy=24) == ARG and call(ldx=56) == ARG and call(ldb=56) == ARG and call(lddx=56) == ARG
-    assert call(K=60) == ALIGN and call(dy=p + 2) == ALIGN and call(dx=p + 8) == ALIGN and call(da=p + 4) == ALIGN
-    assert call(ws=p + 16) == ALIGN and call(nws=16) == ALIGN
+    q = p + 4096
+    assert call(dy=q) == ARG and call(x=q) == ARG  # dx is x, dx is dy
+    assert call(dx=q, base=q, ldb=72) == ARG
+    for kw in (dict(K=60), dict(dy=p + 2), dict(dx=q + 8), dict(da=p + 4), dict(ws=p + 16), dict(nws=16)):
+        assert call(**dict(dict(dx=q), **kw)) == ALIGN, kw
     assert int(b._adapters_grad_ws(0, 8)) == 0 and int(b._adapters_grad_ws(4, 129)) == 0 and int(b._adapters_grad_ws(4, 8)) >= 128
 
 
