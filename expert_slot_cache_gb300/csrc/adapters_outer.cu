@@ -87,12 +87,13 @@ __global__ void __launch_bounds__(kAoThreads)
   const int block = blockIdx.x / S, l = blockIdx.y;
   const bool first = block < g.blocks_a;
   const int F = first ? a.K : a.N, f0 = (block - (first ? 0 : g.blocks_a)) * kAoFeat;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + g.off_bar);  // x and v have landed
-  uint64_t* clean = full + 4;                                    // rows of others are zeroed
-  uint64_t* empty = clean + 4;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + g.off_bar);  // a tile is ready
+  uint64_t* landed = full + 4;                                   // one whose last rows are to be cleared has landed
+  uint64_t* empty = landed + 4;
   uint64_t* tfull = empty + 4;   // an accumulator's tiles are done
   uint64_t* tempty = tfull + 2;  // and taken over
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tempty + 2);
+  uint64_t* done = tempty + 2;   // every product is
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done + 1);
   int* s_total = reinterpret_cast<int*>(s_tmem + 1);
   volatile int* abort_flag = s_total + 1;
   float* part = reinterpret_cast<float*>(sm + g.off_part);  // [Rk][128]
@@ -100,7 +101,8 @@ __global__ void __launch_bounds__(kAoThreads)
   if (threadIdx.x == 0) {
     prefetch_tmap(first ? &mapX : &mapY);
     prefetch_tmap(&mapV);
-    for (int i = 0; i < g.stages; ++i) mbar_init(&full[i], 1), mbar_init(&clean[i], 1), mbar_init(&empty[i], 1);
+    for (int i = 0; i < g.stages; ++i) mbar_init(&full[i], 1), mbar_init(&landed[i], 1), mbar_init(&empty[i], 1);
+    mbar_init(done, 1);
     for (int i = 0; i < g.acc; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 4);
     *abort_flag = 0;
     *s_total = 0;
@@ -139,24 +141,32 @@ __global__ void __launch_bounds__(kAoThreads)
     const bool lead = elect_one();
     const CUtensorMap* map = first ? &mapX : &mapY;
     int s = 0, issued = 0;
-    uint32_t ph = 1;
+    uint32_t ph = 1, cleared = 0, last = 0;  // of a slot: the number of its tiles to be cleared, whether its last is one
     while (tiles.next(row0, rows) && !dead) {
       if (issued >= g.stages) wait(&empty[s], ph);
-      if (lead && !dead) {
+      if (dead) break;
+      uint64_t* bar = rows % 16 ? &landed[s] : &full[s];
+      last = rows % 16 ? last | 1u << s : last & ~(1u << s);
+      cleared ^= rows % 16 ? 1u << s : 0u;  // (its parity)
+      if (lead) {
         unsigned char* st = sm + s * stage;
-        mbar_expect_tx(&full[s], (uint32_t)stage);
-        tma_load_3d(st, map, &full[s], f0, row0, 0);
-        tma_load_3d(st + kAoAtom, map, &full[s], f0 + 64, row0, 0);
+        mbar_expect_tx(bar, (uint32_t)stage);
+        tma_load_3d(st, map, bar, f0, row0, 0);
+        tma_load_3d(st + kAoAtom, map, bar, f0 + 64, row0, 0);
         for (int n = 0; n < g.atoms; ++n)
-          tma_load_3d(st + kAoXBytes + n * kAoAtom, &mapV, &full[s], n * 64, row0, first ? 0 : 1);
+          tma_load_3d(st + kAoXBytes + n * kAoAtom, &mapV, bar, n * 64, row0, first ? 0 : 1);
       }
       __syncwarp();
-      issued += !dead;
+      ++issued;
       if (++s == g.stages) s = 0, ph ^= 1;
     }
     // after a timeout every copy lands before the CTA may go
     if (dead || *abort_flag)
-      for (int j = max(0, issued - g.stages); j < issued; ++j) mbar_wait(&full[j % g.stages], (j / g.stages) & 1);
+      for (int j = max(0, issued - g.stages); j < issued; ++j) {
+        const int q = j % g.stages;
+        if (last >> q & 1) mbar_wait(&landed[q], ~(cleared >> q) & 1);
+        else mbar_wait(&full[q], (j / g.stages) & 1);
+      }
     __syncwarp();
   } else if (warp == 1) {
     const bool lead = elect_one();
@@ -166,14 +176,10 @@ __global__ void __launch_bounds__(kAoThreads)
     const uint64_t b0 = smem_desc_l(smem_u32(sm) + kAoXBytes, kAoAtom, 1024, kLayoutSw128);
     constexpr uint32_t kStep = 2048 >> 4;  // 16 rows
     int s = 0, n = 0, b = 0;  // slot; tile of the accumulator; accumulator
-    uint32_t ph = 0, tph = 1, cleaned = 0;  // phases of slots and accumulators; of a slot's `clean`
+    uint32_t ph = 0, tph = 1;  // phases of slots and accumulators
     for (int i = 0; tiles.next(row0, rows); ++i) {
       if (n == 0 && i >= kAoDrain * g.acc) wait(&tempty[b], tph);
       wait(&full[s], ph);
-      if (rows % 16) {
-        wait(&clean[s], (cleaned >> s) & 1);
-        cleaned ^= 1u << s;
-      }
       tc_fence_after();
       const bool last = ++n == kAoDrain || i == nt - 1;
       if (lead && !dead) {
@@ -200,9 +206,12 @@ __global__ void __launch_bounds__(kAoThreads)
         if (++b == g.acc) b = 0, tph ^= 1;
       }
     }
+    if (lead) umma_commit(done);
+    __syncwarp();
+    mbar_wait(done, 0);  // also after a timeout: nothing of this CTA is read or written any more
   } else {
     const int q = warp & 3, f = q * 32 + lane;  // of the sums: lane = feature
-    int drained = 0;
+    int drained = 0, cleared = 0;
     auto drain = [&] {  // the parts of a rank are Rk columns apart
       const int j = drained++, b = j % g.acc;
       wait(&tfull[b], (j / g.acc) & 1);
@@ -226,11 +235,13 @@ __global__ void __launch_bounds__(kAoThreads)
       if (lane == 0) mbar_arrive(&tempty[b]);
     };
     for (int i = 0; tiles.next(row0, rows); ++i) {
-      const int s = i % g.stages, use = i / g.stages;
-      // the rest of the last 16 rows belongs to others, whatever it is: each slot has a warp that clears it (and waits
-      // for every use of its slot, so that it is never a phase behind)
-      if (s == warp - 2) wait(&full[s], use & 1);
+      const int s = i % g.stages;
+      // The rest of the last 16 rows belongs to others, whatever it is: each slot has a warp that clears it, and makes the
+      // tile ready in the place of its copies.  (The warp waits for such tiles alone, on a barrier of their own: the slot
+      // is not used again before, so that it can be neither behind nor ahead of the barrier's phases.)
       if (s == warp - 2 && rows % 16) {
+        wait(&landed[s], cleared & 1);
+        ++cleared;
         const int rest = 16 - rows % 16, pieces = (2 + g.atoms) * 8;
         for (int u = lane; u < rest * pieces; u += 32) {
           const int r = rows + u / pieces, p = u % pieces;
@@ -238,7 +249,7 @@ __global__ void __launch_bounds__(kAoThreads)
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(&clean[s]);
+        if (lane == 0) mbar_arrive(&full[s]);
       }
       // with two accumulators the one before last's sums are taken over while the products of the last one run
       if (i % kAoDrain == kAoDrain - 1 && i / kAoDrain >= g.acc - 1) drain();

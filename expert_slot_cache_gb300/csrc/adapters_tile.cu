@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(kAtThreads, 2)
   uint64_t* d1full = tempty + 2;
   uint64_t* vfull = d1full + 1;                    // v of all rows is there,
   uint64_t* vrep = vfull + 1;                      // in all the lanes
-  int* s_tile = reinterpret_cast<int*>(vrep + 1);  // [4]
+  uint64_t* done = vrep + 1;                       // every product is
+  int* s_tile = reinterpret_cast<int*>(done + 1);  // [4]
   int* s_scan = s_tile + 4;                          // [33]
   volatile int* abort_flag = s_scan + 33;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_scan + 34);
@@ -127,6 +128,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
     mbar_init(d1full, 1);
     mbar_init(vfull, 2);
     mbar_init(vrep, 4);
+    mbar_init(done, 1);
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -378,6 +380,9 @@ __global__ void __launch_bounds__(kAtThreads, 2)
       }
       __syncwarp();
     }
+    if (lead) umma_commit(done);
+    __syncwarp();
+    mbar_wait(done, 0);  // also after a timeout: nothing of this CTA is read or written any more
   } else {
     constexpr int kChunk = F32 ? 32 : 64, kPer = kAtCols / kChunk;  // outputs of a chunk (128 bytes); chunks of a step
     unsigned char* buf = part + (warp - 2) * 2 * kAtStage;

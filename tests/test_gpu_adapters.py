@@ -170,6 +170,26 @@ def test_many_passes_over_long_sequences(R):
     assert int(op.dev_status.item()) == 0
 
 
+def test_a_thousand_gradients():
+    """A ring of three slots, tiles with rows to be cleared among others, launches that overlap: no wait gives up."""
+    import expert_slot_cache_gb300 as M
+    lengths = [1261, 0, 996, 567, 1068, 19, 1740, 236, 759, 409, 1137]
+    for R, K, N, L in ((32, 2048, 4096, 3), (24, 264, 136, 2), (48, 512, 512, 1)):
+        x, a, b, scale, ids, starts = case(8192, K, N, R, L, 7, lengths, none=0.0)
+        g = torch.Generator(device=DEV).manual_seed(8)
+        dy, kept = normal(8192, N, g=g, size=0.01), torch.empty(8192, R, device=DEV)
+        op = M.Adapters(a, b, scale)
+        op.forward(x, ids, None, starts, kept=kept)
+        want = op.grad(dy, x, kept, ids, None, starts)
+        off = torch.zeros((), dtype=torch.int64, device=DEV)
+        for i in range(340):
+            r = op.grad(dy, x, kept, ids, None, starts)
+            off += sum((p != q).sum() for p, q in zip(r, want))
+            if i % 50 == 0:
+                assert int(op.dev_status.item()) == 0  # (stops here, should a wait have given up)
+        assert int(off) == 0 and int(op.dev_status.item()) == 0
+
+
 def test_large_values_and_other_rows_nan():
     """NaN and infinities stay in their rows, whatever the tile; rows of no sequence are not read into anything."""
     import expert_slot_cache_gb300 as M
