@@ -518,7 +518,7 @@ class Adapters:
 
     def _sequences(self, T, ids, seq_start):
         n = T if seq_start is None else seq_start.numel() - 1
-        if ids.dtype != torch.int32 or ids.shape != (n,) or not ids.is_contiguous():
+        if ids.dtype is not torch.int32 or ids.shape != (n,) or not ids.is_contiguous():
             raise ValueError(f"ids: need contiguous int32 [{n}], got {ids.dtype} {tuple(ids.shape)}")
         if seq_start is not None:
             _want(seq_start, "seq_start", torch.int32, (n + 1,))
@@ -526,7 +526,7 @@ class Adapters:
 
     @staticmethod
     def _rows(t, what, T, n, dtype):
-        if t.dtype != dtype or t.shape != (T, n) or (t.stride(1) != 1 and n > 1):
+        if t.dtype is not dtype or t.shape != (T, n) or t.stride(1) != 1:
             raise ValueError(f"{what}: need {dtype} ({T}, {n}) with a contiguous last dimension, got {t.dtype} "
                              f"{tuple(t.shape)}")
         return t.data_ptr(), t.stride(0) if T > 1 else n
@@ -558,18 +558,22 @@ class Adapters:
         if kept is not None:
             _want(kept, "kept", torch.float32, (T, self.R))
         dev = self._index
-        if (dev < 0 or x.get_device() != dev or ids.get_device() != dev
-                or any(t is not None and t.get_device() != dev for t in (base, seq_start, out, kept))):
+        if (dev < 0 or x.get_device() != dev or ids.get_device() != dev or _elsewhere(base, dev)
+                or _elsewhere(seq_start, dev) or _elsewhere(out, dev) or _elsewhere(kept, dev)):
             _on(self.device, x=x, ids=ids, base=base, seq_start=seq_start, out=out, kept=kept)
         if _current_device() != dev:
             with torch.cuda.device(self.device):
                 return self.forward(x, ids, base, seq_start, out, out_dtype, kept, stream)
         if out is None:
             out = _result(stream, T, self.N, dtype=dtype, device=self.device)
-        po, ldo = self._rows(out, "out", T, self.N, dtype)
-        _ck(_adapters(px, ldx, pb, ldb, T, self.K, self.N, self.R, self.L, self._a, self._b, self._scale, ids.data_ptr(),
-                      None if seq_start is None else seq_start.data_ptr(), n, po, ldo, f32,
-                      None if kept is None else kept.data_ptr(), self._status, _here(dev, stream)), "moe_adapters")
+            po, ldo = out.data_ptr(), self.N
+        else:
+            po, ldo = (pb, ldb) if out is base else self._rows(out, "out", T, self.N, dtype)
+        rc = _adapters(px, ldx, pb, ldb, T, self.K, self.N, self.R, self.L, self._a, self._b, self._scale, ids.data_ptr(),
+                       None if seq_start is None else seq_start.data_ptr(), n, po, ldo, f32,
+                       None if kept is None else kept.data_ptr(), self._status, _here(dev, stream))
+        if rc:
+            _ck(rc, "moe_adapters")
         return out
 
     def grad(self, dy: torch.Tensor, x: Optional[torch.Tensor], kept: Optional[torch.Tensor], ids: torch.Tensor,
@@ -591,8 +595,8 @@ class Adapters:
             pk = kept.data_ptr()
         pb, ldb = (None, 0) if base is None else self._rows(base, "base", T, self.K, torch.bfloat16)
         dev = self._index
-        if (dev < 0 or dy.get_device() != dev or ids.get_device() != dev
-                or any(t is not None and t.get_device() != dev for t in (x, kept, base, seq_start))):
+        if (dev < 0 or dy.get_device() != dev or ids.get_device() != dev or _elsewhere(x, dev) or _elsewhere(kept, dev)
+                or _elsewhere(base, dev) or _elsewhere(seq_start, dev)):
             _on(self.device, dy=dy, x=x, kept=kept, ids=ids, base=base, seq_start=seq_start)
         if _current_device() != dev:
             with torch.cuda.device(self.device):
@@ -812,10 +816,14 @@ class GroupRoute(NamedTuple):
 
 def _logits_ok(logits: torch.Tensor) -> bool:
     """Whether the logits are bf16; refuses what is neither bf16 nor fp32."""
-    bf16 = logits.dtype == torch.bfloat16
-    if not (bf16 or logits.dtype == torch.float32) or logits.dim() != 2 or not logits.is_contiguous():
+    bf16 = logits.dtype is torch.bfloat16
+    if not (bf16 or logits.dtype is torch.float32) or logits.dim() != 2 or not logits.is_contiguous():
         raise ValueError(f"logits: need contiguous fp32 or bf16 [T][E], got {logits.dtype} {tuple(logits.shape)}")
     return bf16
+
+
+def _elsewhere(t: Optional[torch.Tensor], index: int) -> bool:
+    return t is not None and t.get_device() != index
 
 
 def route_groups(logits: torch.Tensor, k: int, n_group: int = 1, topk_group: int = 1,
@@ -828,23 +836,30 @@ def route_groups(logits: torch.Tensor, k: int, n_group: int = 1, topk_group: int
     """
     bf16 = _logits_ok(logits)
     T, E = logits.shape
+    bias = mask = None
     if sel_bias is not None:
-        _want(sel_bias, "sel_bias", torch.float32, (E,))
+        if sel_bias.dtype is not torch.float32 or sel_bias.shape != (E,) or not sel_bias.is_contiguous():
+            _want(sel_bias, "sel_bias", torch.float32, (E,))
+        bias = sel_bias.data_ptr()
     if token_mask is not None:
-        _want(token_mask, "token_mask", torch.bool if token_mask.dtype == torch.bool else torch.uint8, (T,))
+        _want(token_mask, "token_mask", torch.bool if token_mask.dtype is torch.bool else torch.uint8, (T,))
+        mask = token_mask.data_ptr()
     dev, index = logits.device, logits.get_device()
-    if index < 0 or any(t is not None and t.get_device() != index for t in (sel_bias, token_mask)):
+    if index < 0 or _elsewhere(sel_bias, index) or _elsewhere(token_mask, index):
         _on(dev, sel_bias=sel_bias, token_mask=token_mask)
     if stream is not None or _current_device() != index:  # results for the stream that the kernel runs on
         with torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream):
             return route_groups(logits, k, n_group, topk_group, sel_bias, token_mask, sigmoid, group_max, renormalise,
                                 scale)
-    ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev)
-    w = torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev)
+    if k < 1:
+        raise MoeError(-1, "moe_route_groups")
+    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    w = torch.empty((T, k), dtype=torch.float32, device=dev)
     flags = (ROUTE_SIGMOID if sigmoid else 0) | (ROUTE_GROUP_MAX if group_max else 0) | (0 if renormalise else ROUTE_RAW)
-    _ck(_route_groups(logits.data_ptr(), bf16, None if sel_bias is None else sel_bias.data_ptr(),
-                      None if token_mask is None else token_mask.data_ptr(), T, E, k, n_group, topk_group, flags, scale,
-                      ids.data_ptr(), w.data_ptr(), _here(index)), "moe_route_groups")
+    rc = _route_groups(logits.data_ptr(), bf16, bias, mask, T, E, k, n_group, topk_group, flags, scale, ids.data_ptr(),
+                       w.data_ptr(), _here(index))
+    if rc:
+        _ck(rc, "moe_route_groups")
     return GroupRoute(ids, w)
 
 
@@ -858,7 +873,7 @@ def route_groups_grad(logits: torch.Tensor, ids: torch.Tensor, grad_w: torch.Ten
         raise ValueError(f"ids: need contiguous int32 [{T}][k], got {ids.dtype} {tuple(ids.shape)}")
     _want(grad_w, "grad_w", torch.float32, (T, k))
     dev, index = logits.device, logits.get_device()
-    if index < 0 or any(t is not None and t.get_device() != index for t in (ids, grad_w, dev_status)):
+    if index < 0 or ids.get_device() != index or grad_w.get_device() != index or _elsewhere(dev_status, index):
         _on(dev, ids=ids, grad_w=grad_w, dev_status=dev_status)
     if stream is not None or _current_device() != index:
         with torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream):

@@ -684,9 +684,12 @@ static int launch_group_grad(const GroupGradArgs& a, cudaStream_t s) {
 }
 
 static int grp_sms(int* sms) {
+  static int seen[64] = {};
   int dev = 0;
   MOE_CUDA_TRY(cudaGetDevice(&dev));
-  MOE_CUDA_TRY(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
+  if (dev < 0 || dev >= 64) return MOE_ERR_CUDA;
+  if (seen[dev] == 0) MOE_CUDA_TRY(cudaDeviceGetAttribute(&seen[dev], cudaDevAttrMultiProcessorCount, dev));
+  *sms = seen[dev];
   return MOE_OK;
 }
 
