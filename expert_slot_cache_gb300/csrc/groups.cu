@@ -82,7 +82,7 @@ struct GrpRaw {
     if constexpr (V == 1) {
       r[0] = __float_as_uint(grp_logit<BF16>(p, i));
     } else {
-      const uint4 v = ldg_stream(reinterpret_cast<const uint8_t*>(p) + i * (BF16 ? 2 : 4));
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(p) + i * (BF16 ? 2 : 4)));
       r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
     }
   }
