@@ -81,7 +81,8 @@ __device__ __forceinline__ void ad_add8(const void* base, void* out, long long i
 
 // One cluster of CTAs per row, or per sequence of up to max_rows rows: CTA c takes its share of the K inputs for all R
 // products, the partial sums meet in every CTA's shared memory, and CTA c computes its share of the N outputs.  One
-// launch, no workspace.
+// launch, no workspace.  One row of R 16 (2048 x 2048) 3.9 us, 64 rows of 64 adapters (2048 x 4096, 1.3 us of weight bytes)
+// 5.5: the launch, ids -> weights -> cluster -> outputs.  With 64 registers four CTAs are resident (three: 8.6, five: 7.0).
 template <bool F32>
 __global__ void __launch_bounds__(kRowThreads, 4) adapters_row_kernel(const AdArgs a, int max_rows) {
   __shared__ __align__(16) float s_red[kRowThreads * 8];
@@ -234,7 +235,9 @@ static int ad_sms(int* sms) {
   return MOE_OK;
 }
 
-constexpr int kShortRows = 4;  // sequences of up to so many rows take the row kernel in a batch of short and long ones
+// Sequences of up to so many rows take the row kernel in a batch of short and long ones (36 single rows and four prompts of
+// 1001 rows: 15.3 us; a tile of 32 rows takes 9 us for one row, too).
+constexpr int kShortRows = 4;
 
 static int ad_run(const AdArgs& a, bool f32, cudaStream_t s) {
   if (!a.seq || a.T <= kShortRows) return ad_launch_rows(a, f32, a.T, 0, s);

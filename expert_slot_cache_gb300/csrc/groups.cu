@@ -9,8 +9,9 @@
 // the order are closer than the fp32 error bound (and not the same logit with the same bias), the candidates of the token,
 // or the best of its groups, are compared again in fp64.  That is some tokens in a thousand.
 //
-// The bytes of the logits, read once, bound a large batch; what a warp does for a token (k reductions one after the
-// other) bounds it in practice, and the launch a small one.
+// The bytes of the logits, read once, would bound a large batch (16,384 x 512 fp32: 5.2 us); the instructions of a warp
+// for a token, about 1,200, bound it in practice (35 us, issued every second cycle), and the launch a small one (one
+// token 3.4 us).
 #include <algorithm>
 
 #include "internal.cuh"
@@ -45,9 +46,6 @@ __device__ __forceinline__ uint64_t grp_key64(double v) {
   const uint64_t b = (uint64_t)__double_as_longlong(v + 0.);
   return v != v ? 1ull : b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
 }
-__device__ __forceinline__ double grp_value64(uint64_t key) {
-  return __longlong_as_double((long long)(key >> 63 ? key ^ 0x8000000000000000ull : ~key));
-}
 __device__ __forceinline__ uint64_t grp_max64(uint64_t v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v = max(v, __shfl_xor_sync(MOE_FULL_MASK, v, o));
@@ -59,13 +57,19 @@ __device__ __forceinline__ float grp_logit(const void* p, size_t i) {
   return BF16 ? bf16_to_f32(reinterpret_cast<const uint16_t*>(p)[i]) : reinterpret_cast<const float*>(p)[i];
 }
 
-// sigmoid within 2^-21 of itself above l = -8, within 2e-10 below (the rounding of the exponent is |l| 2^-24 of it).
+// sigmoid(l).  In units of 2^-24 of itself: e is off by 4 (its instruction) and 1.5 |l| (the rounding of its argument),
+// which counts e / (1 + e) times, the sum by 1, the reciprocal by 2.
 __device__ __forceinline__ float grp_sigmoid(float l) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.4426950408889634f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return r;
 }
+// How far apart two scores have to be for fp32 to tell their order: rel (|c| + max |bias|) + kGrpTiny.
+// Sigmoid, rel = 2^-19 (32 units): two scores are off by 2 (3 + (4 + 1.5 |l|) e / (1 + e)) units of s <= |c| + |bias| and by
+// one each from the addition of the bias: below 32 for l > -5.3; further down 3 (|l| - 5.3) units of s < e^l more, at most
+// 3.3e-10.  Softmax, rel = 2^-17 (128 units): 2 (4 + |l - max| + 44) + 2, for sums of 37 additions; beyond |l - max| = 15
+// the rest is below 1e-14.
 constexpr float kGrpTiny = 0x1p-31f;  // 4.7e-10
 // Whether fp32 does not tell the order of two scores of these keys (m at most ml).
 __device__ __forceinline__ bool grp_close(uint32_t ml, uint32_t m, float rel, float bmax) {
@@ -145,6 +149,7 @@ __device__ __noinline__ int grp_pick64(const GroupArgs& a, size_t row) {
       if (at(u) >= 0) sum += exp((double)grp_logit<BF16>(a.logits, row + at(u)) - mx);
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(MOE_FULL_MASK, sum, o);
   }
+  const bool best = a.flags & MOE_ROUTE_GROUP_MAX;
   double b1 = -INFINITY, b2 = -INFINITY;
   for (int u = 0; u < held; ++u) {
     const int e = at(u);
@@ -152,10 +157,10 @@ __device__ __noinline__ int grp_pick64(const GroupArgs& a, size_t row) {
     if (e < 0) continue;
     const double l = (double)grp_logit<BF16>(a.logits, row + e);
     const double s = sig ? 1. / (1. + exp(-l)) : exp(l - mx) / sum;
-    const double c = a.bias ? s + (double)a.bias[e] : s;
-    b2 = fmax(b2, fmin(b1, c));
-    b1 = fmax(b1, c);
-    key[u] = grp_key64(a.bias ? c : l);
+    const double c = a.bias ? s + (double)a.bias[e] : l, v = a.bias || best ? c : s;
+    b2 = fmax(b2, fmin(b1, v == v ? v : -INFINITY));
+    b1 = fmax(b1, v);
+    key[u] = grp_key64(c);
   }
   if (a.topk_group < a.n_group) {
     for (int o = a.lanes / 2; o; o >>= 1) {
@@ -163,14 +168,7 @@ __device__ __noinline__ int grp_pick64(const GroupArgs& a, size_t row) {
       b2 = fmax(fmin(b1, o1), fmax(b2, o2));
       b1 = fmax(b1, o1);
     }
-    uint64_t gk;
-    if (a.flags & MOE_ROUTE_GROUP_MAX) {
-      gk = 0;
-      for (int u = 0; u < held; ++u) gk = max(gk, key[u]);
-      for (int o = a.lanes / 2; o; o >>= 1) gk = max(gk, __shfl_xor_sync(MOE_FULL_MASK, gk, o));
-    } else {
-      gk = grp_key64(a.group == 1 ? b1 : b1 + b2);
-    }
+    const uint64_t gk = g < a.n_group ? grp_key64(best || a.group == 1 ? b1 : b1 + b2) : 0ull;
     int before = 0;
     for (int h = 0; h < a.n_group; ++h) {
       const uint64_t ok = __shfl_sync(MOE_FULL_MASK, gk, h * a.lanes);
@@ -301,9 +299,7 @@ __global__ void __launch_bounds__(kGrpThreads, grp_resident(NQ * V)) group_route
         for (int u = 0; u < NE; ++u) better(compared ? c[u] : score(c[u]));
       }
     }
-    // Error bound of a difference of two scores: that of either sigmoid and the roundings of s + bias (2^-24); for a
-    // softmax the rounding of an argument below 64 and the sum's (2^-18).
-    const float rel = sig ? 0x1p-20f : 0x1p-17f;
+    const float rel = sig ? 0x1p-19f : 0x1p-17f;
     double sum64 = 0.;
     if (limited) {
       const bool one = gmax || a.group == 1;
@@ -563,7 +559,9 @@ __device__ __forceinline__ void grp_put(void* p, size_t i, float v) {
 //   not, sigmoid      scale g_j s_j (1 - s_j)                      in the picks alone
 //   not, softmax      s_e (scale G_e - sum_i scale g_i s_i)        everywhere (DENSE); G_e: the g of the picks of e
 // The row is written in whole vectors first (NC a lane) and the picks' values over it by the same warp.  A pick that is
-// there twice adds up, in the order of the picks.  Bound by the bytes: 30,011 x 288 bf16, dense.
+// there twice adds up, in the order of the picks.  30,011 x 288 bf16, every logit: 12.8 us where the bytes take 5.5; the
+// chain ids -> logits -> sums -> row is what a CTA waits for, and three rounds of CTAs follow each other (a warp a token
+// and the row read three times took 23).
 template <int V, int NC, int L, bool BF16, bool DENSE>
 __global__ void __launch_bounds__(kGrpThreads) group_grad_kernel(const GroupGradArgs a) {
   pdl_wait();

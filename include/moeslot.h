@@ -555,7 +555,8 @@ int moe_balance_loss(const void* logits, int bf16, const int32_t* ids, const uin
  * the topk_group groups of highest score stay, the k highest c of their experts
  * are picked, in descending order, and
  *   w[t][j] = scale * s_j / sum_i s_i   over the picks, with MOE_ROUTE_RAW scale * s_j.
- * Equal values: the lower index first.  NaN ranks behind everything else.  The
+ * Equal values: the lower index first.  NaN ranks behind everything else (in a
+ * group's score it counts as -inf).  The
  * picks are those of 64-bit arithmetic; they do not depend on thread timing.
  * Renormalised picks that are all -inf have weight 0.
  *   logits     device [T][E], fp32 or bf16 (bf16 = 1)
