@@ -5,8 +5,9 @@
 // each CTA adds up some of the rows in a fixed order, scales them and hands them to all; then CTA c multiplies them by
 // its share of the N outputs (D2 [rows][128], double-buffered; B_l as it lies, MN-major) and adds base on the way out.
 // Nothing but x, A, B, base and out crosses the memory, so those bytes bound a large batch: 4096 rows of R 64, 2048 x 4096,
-// take 30 us where they take 13; the second product with its 67 MB takes 8, some 12 go to dependent steps before (x's way
-// in 3, sums through the cluster 3, v's way to the other CTAs 2.5, at 14 B a clock and SM).  64 rows of R 16 take 9.4 us.
+// take 26.5 us where they take 13; the second product with its 67 MB takes 8, some 12 go to dependent steps before (x's way
+// in 3, sums through the cluster 3, v's way to the other CTAs 2.5, at 14 B a clock and SM).  64 rows of R 16 take 9.3 us.
+// Sending base to L2 while the first product runs costs more than it hides (4096 rows 30 us, 16,384 of R 16 50 for 41).
 //
 // The rows of a tile of 32 or 64 stand in the 128 lanes of D several times, so that all four epilogue warps (each reads
 // 32 lanes) have columns to store.  The tensor cores truncate what they add: D1 is several accumulators in turn, added
@@ -170,17 +171,6 @@ __global__ void __launch_bounds__(kAtThreads, 2)
   const int nt = a.out ? nt1 - nt0 : 0;
   at_cluster_arrive_relaxed();    // waited for where another CTA's shared memory is written first
   if (!g.beside) pdl_trigger();  // (after the allocation: a kernel that starts now may allocate, too)
-  if (warp >= 2 && nt > 0 && a.base) {
-    // base on its way to L2 while the first product runs
-    const int t = (int)threadIdx.x - 64;
-    if (t < rows) {
-      const int n0 = nt0 * kAtCols, n = min(nt1 * kAtCols, a.N) - n0;
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<const uint8_t*>(a.base) +
-                                                                     ((row0 + t) * a.ldb + n0) * kSize),
-                   "r"(n * kSize)
-                   : "memory");
-    }
-  }
   bool dead = false;  // (of a whole warp) nothing is waited for or issued after a timeout
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (!dead) dead = !ad_wait(bar, parity, abort_flag, a.status);
@@ -511,10 +501,10 @@ int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, bool beside, cuda
   g.Rk = (a.R + 15) / 16 * 16;
   // CTAs of a cluster and rows of a tile, by an estimate of the time: rounds of as many clusters as run at once, in each a
   // CTA takes 9 us and its share of the tile's bytes at 40 KB/us, less where the CTAs' sum would pass 6.6 MB/us.
-  // Measured: 4096 rows of R 64 (2048 x 4096) 29.9 us with 8 and 128, 30.4 with 4 and 64, 34 with 4 and 128; 5120 rows 50
-  // with 4 and 64 (two rounds); 16,384 of R 16 (2048 x 2048) 60 with 8 and 128, 53 with 4, 49 with 2; 1024 of R 16 15.4
-  // with 8 and 128, 12.3 with 8 and 32, 14.2 with 4 and 32; 2000 of R 128 (4096 x 4096) 29 with 4 and 64, 44 with 8 and
-  // 128.
+  // Measured: 4096 rows of R 64 (2048 x 4096) 26.5 us with 8 and 128, 27.2 with 4 and 64, 30.7 with 4 and 128; 12,000 rows
+  // 64 with 2 and 128, 73 with 4 or 8; 16,384 of R 16 (2048 x 2048) 56 with 8 and 128, 45 with 4, 41 with 2; 1024 of R 16
+  // 15.3 with 8 and 128, 13.1 with 8 and 64, 12.3 with 8 and 32; 2000 of R 128 (4096 x 4096) 27 with 4 and 64, 43 with 8
+  // and 128.
   int C = 8;
   double best = 0.;
   for (int c = 2; c <= 8; c *= 2)
