@@ -10,8 +10,7 @@
 // or the best of its groups, are compared again in fp64.  That is some tokens in a thousand.
 //
 // The bytes of the logits, read once, would bound a large batch (16,384 x 512 fp32: 5.2 us); the instructions of a warp
-// for a token, about 1,200, bound it in practice (35 us, issued every second cycle), and the launch a small one (one
-// token 3.4 us).
+// for a token, about 1,100, bound it in practice (31.5 us), and the launch a small one (one token 3.2 us).
 #include <algorithm>
 
 #include "internal.cuh"
@@ -25,6 +24,7 @@ struct GroupArgs {
   int T, E, k;
   int n_group, group, topk_group;  // group = E / n_group experts
   int lanes;                       // lanes of a group: a power of two
+  int live;                        // lanes that hold experts of the best groups, about
   uint32_t magic;                  // ceil(2^20 / group): e magic / 2^20 is the group of e < 1024
   int flags;
   float scale;
@@ -193,9 +193,14 @@ __device__ __noinline__ int grp_pick64(const GroupArgs& a, size_t row) {
   return mine;
 }
 
-// CTAs of a SM (16,384 x 512, 16 elements a lane: 37 us with two, 41 with three and registers in memory, 42 with four).
-constexpr int grp_resident(int elements) { return elements <= 8 ? 3 : 2; }
-
+// Whether the next logits and the bias of a lane's elements wait in shared memory: with more than 8 (256 bf16 logits: 15.2
+// us in registers, 15.6 so; 16,384 x 512: 33.6 and 31.5; 8192 x 1024 77.8 and 74.4).
+template <int V, int NE, bool FLAT>
+constexpr bool kGrpAhead = !FLAT && V > 1 && NE > 8;
+// CTAs of a SM (16,384 x 512, 16 elements a lane, in shared memory: 34 us with two, 31.5 with three, 32.8 with four;
+// 8192 x 288, 12 in registers: 34.8 with two, 35.9 with three).
+template <int V, int NE, bool FLAT>
+constexpr int kGrpResident = NE <= 8 || (kGrpAhead<V, NE, FLAT> && NE <= 16) ? 3 : 2;
 // One warp routes a token.  Where the groups fill the lanes, lane (g, i) holds the vectors i, i + lanes, ... of V experts
 // of group g, so that a group's score takes log2(lanes) shuffles.  FLAT: the lanes hold the row's vectors in turn, and the
 // groups' scores are taken from shared memory.
@@ -203,11 +208,15 @@ constexpr int grp_resident(int elements) { return elements <= 8 ? 3 : 2; }
 // The k best: k of the lanes' best elements are at or above the k-th largest of them, so only elements at or above it (a
 // tolerance below it, with a bias) can be picked.  They are some 12 to 16 as a rule; a lane takes each, and its place is
 // the number of those that are larger.  (k maxima one after the other, each over all elements, took twice as long;
-// they remain for tokens with more than 32 such elements, which have many equal logits.)
+// they remain for tokens with more than 32 such elements: many equal logits.)
 template <int V, int NQ, bool BF16, bool FLAT>
-__global__ void __launch_bounds__(kGrpThreads, grp_resident(NQ * V)) group_route_kernel(const GroupArgs a) {
+__global__ void __launch_bounds__(kGrpThreads, kGrpResident<V, NQ * V, FLAT>) group_route_kernel(const GroupArgs a) {
   constexpr int NE = NQ * V;
+  constexpr bool kAhead = kGrpAhead<V, NE, FLAT>;
+  __shared__ uint4 s_x[kAhead ? kGrpThreads / 32 : 1][kAhead ? NQ : 1][32];  // a lane's next logits
+  __shared__ float4 s_b[kAhead ? NE / 4 : 1][32];                             // and the bias of its experts
   __shared__ uint16_t s_e[kGrpThreads / 32][32];
+  __shared__ __align__(16) uint32_t s_top[kGrpThreads / 32][32];
   __shared__ float s_c[FLAT ? kGrpThreads / 32 : 1][FLAT ? kMaxE : 1], s_least[FLAT ? kGrpThreads / 32 : 1][32];
   pdl_wait();
   pdl_trigger();
@@ -219,17 +228,23 @@ __global__ void __launch_bounds__(kGrpThreads, grp_resident(NQ * V)) group_route
   const int e0 = FLAT ? lane * V : g * a.group + i0 * V;  // vector q starts at expert e0 + q step
   const int step = FLAT ? 32 * V : a.lanes * V;
   const float kNone = __uint_as_float(0x7fffffffu);  // NaN: at or above nothing
-  float bias[NE], bmax = 0.f;
+  float bias[kAhead ? 1 : NE], bmax = 0.f;
   auto expert = [&](int u) { return e0 + u / V * step + u % V; };
   auto there = [&](int u) { return !FLAT || expert(u) < a.E; };
   auto group_of = [&](int u) { return FLAT ? (int)((uint32_t)expert(u) * a.magic >> 20) : g; };
-  // a token's logits are on their way while the one before is routed
-  GrpRaw<BF16, V> next[NQ];
+  // a token's logits are on their way while the one before is routed (a lane reads what it copied itself)
+  GrpRaw<BF16, V> next[kAhead ? 1 : NQ];
   bool valid = true;
   auto fetch = [&](int t) {
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
-      if (there(q * V)) next[q].load(a.logits, (size_t)t * a.E + e0 + q * step);
+      if constexpr (kAhead) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(&s_x[warp][q][lane])),
+                     "l"(reinterpret_cast<const uint8_t*>(a.logits) + ((size_t)t * a.E + e0 + q * step) * (BF16 ? 2 : 4))
+                     : "memory");
+      } else {
+        if (there(q * V)) next[q].load(a.logits, (size_t)t * a.E + e0 + q * step);
+      }
     valid = !a.mask || a.mask[t];
   };
   const int warps = gridDim.x * (kGrpThreads / 32);
@@ -239,16 +254,30 @@ __global__ void __launch_bounds__(kGrpThreads, grp_resident(NQ * V)) group_route
 #pragma unroll
     for (int u = 0; u < NE; ++u) {
       const float b = there(u) ? a.bias[expert(u)] : 0.f;
-      bias[u] = b;
+      if constexpr (!kAhead) bias[u] = b;
+      else if (warp == 0) reinterpret_cast<float*>(&s_b[u / 4][lane])[u % 4] = b;
       if (fabsf(b) < INFINITY) bmax = fmaxf(bmax, fabsf(b));
     }
     bmax = __uint_as_float(__reduce_max_sync(MOE_FULL_MASK, __float_as_uint(bmax)));
+    if constexpr (kAhead) __syncthreads();
   }
+  auto bias_of = [&](int u) { return kAhead ? reinterpret_cast<const float*>(&s_b[u / 4][lane])[u % 4] : bias[kAhead ? 0 : u]; };
   for (; t < a.T; t += warps) {
     const size_t row = (size_t)t * a.E;
     float c[NE];  // the logits, then what is compared; kNone for what is not there
 #pragma unroll
-    for (int u = 0; u < NE; ++u) c[u] = there(u) ? next[u / V].at(u % V) : kNone;
+    for (int q = 0; q < NQ; ++q) {
+      GrpRaw<BF16, V> x;
+      if constexpr (kAhead) {
+        if (q == 0) asm volatile("cp.async.wait_all;" ::: "memory");
+        const uint4 v = s_x[warp][q][lane];
+        x.r[0] = v.x, x.r[1] = v.y, x.r[2] = v.z, x.r[3] = v.w;
+      } else {
+        x = next[q];
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) c[q * V + v] = there(q * V) ? x.at(v) : kNone;
+    }
     const bool padding = !valid;
     if (t + warps < a.T) fetch(t + warps);
     if (padding) {
@@ -276,7 +305,15 @@ __global__ void __launch_bounds__(kGrpThreads, grp_resident(NQ * V)) group_route
     auto score = [&](float l) { return sig ? grp_sigmoid(l) : expf(l - mx) * inv; };
     if (a.bias) {
 #pragma unroll
-      for (int u = 0; u < NE; ++u) c[u] = score(c[u]) + bias[u];
+      for (int u = 0; u < NE; u += 4) {
+        float4 b;
+        if constexpr (kAhead) b = s_b[u / 4][lane];
+        else b = make_float4(bias[u], bias[u + 1], bias[u + 2], bias[u + 3]);
+        c[u] = score(c[u]) + b.x;
+        c[u + 1] = score(c[u + 1]) + b.y;
+        c[u + 2] = score(c[u + 2]) + b.z;
+        c[u + 3] = score(c[u + 3]) + b.w;
+      }
     }
     // the two best of the lane's part of its group (without a sum of scores: of what is compared)
     float b1 = -INFINITY, b2 = -INFINITY;
@@ -372,26 +409,43 @@ __global__ void __launch_bounds__(kGrpThreads, grp_resident(NQ * V)) group_route
         for (int u = 0; u < NE; ++u) c[u] = in ? c[u] : kNone;
       }
     }
-    // the k-th largest of the lanes' best elements, or where lanes are few of their vectors'
+    // the k-th largest of the lanes' best elements, or where lanes are few of the best of each 2 or 4: with k lanes the
+    // lowest of their best has more than 32 elements above it too often (8192 x 1024, 8 lanes, k 8: 75 us, so 41; 8192 x
+    // 512, 16 lanes, k 16: 82 and 26), with 5 k / 4 it has 12 to 20
     float thr = -INFINITY;
     {
-      float top[NQ], best = -INFINITY;
+      constexpr int CH = V == 1 ? 1 : NE <= 8 ? 2 : 4, NT = NE / CH;
+      float top[NT], best = -INFINITY;
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        top[q] = c[q * V];
+      for (int q = 0; q < NT; ++q) {
+        top[q] = c[q * CH];
 #pragma unroll
-        for (int v = 1; v < V; ++v) top[q] = fmaxf(top[q], c[q * V + v]);
+        for (int v = 1; v < CH; ++v) top[q] = fmaxf(top[q], c[q * CH + v]);
         best = fmaxf(best, top[q]);
       }
       constexpr uint32_t kLowest = 0x007fffffu;  // -inf
-      if (FLAT || a.topk_group * a.lanes >= a.k || NQ == 1) {
+      if (V == 1 || 4 * a.live >= 5 * a.k) {
         uint32_t mine = grp_key(best);
-        for (int seen = 0; seen < a.k;) {
-          const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, mine);
-          if (m <= kLowest) break;
-          seen += __popc(__ballot_sync(MOE_FULL_MASK, mine == m));
-          if (seen >= a.k) thr = grp_value(m);
-          if (mine == m) mine = 0;
+        if (a.k > 4) {  // (4: 20.0 us either way, 2: 17.0 one after the other and 17.5, 10: 33.6 counted and 35)
+          s_top[warp][lane] = mine;
+          __syncwarp();
+          int above = 0;  // lanes at or above this one's
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const uint4 o = *reinterpret_cast<const uint4*>(&s_top[warp][j]);
+            above += (o.x >= mine) + (o.y >= mine) + (o.z >= mine) + (o.w >= mine);
+          }
+          __syncwarp();
+          const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, above >= a.k ? mine : 0u);
+          if (m > kLowest) thr = grp_value(m);
+        } else {
+          for (int seen = 0; seen < a.k;) {
+            const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, mine);
+            if (m <= kLowest) break;
+            seen += __popc(__ballot_sync(MOE_FULL_MASK, mine == m));
+            if (seen >= a.k) thr = grp_value(m);
+            if (mine == m) mine = 0;
+          }
         }
       } else {
         for (int seen = 0; seen < a.k;) {
@@ -401,7 +455,7 @@ __global__ void __launch_bounds__(kGrpThreads, grp_resident(NQ * V)) group_route
           int here = 0;
           best = -INFINITY;
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) {
+          for (int q = 0; q < NT; ++q) {
             here += top[q] == f;
             if (top[q] == f) top[q] = -INFINITY;
             best = fmaxf(best, top[q]);
@@ -501,7 +555,7 @@ __global__ void __launch_bounds__(kGrpThreads, grp_resident(NQ * V)) group_route
         float next = -INFINITY;
 #pragma unroll
         for (int u = 0; u < NE; ++u) {
-          if (c[u] == fl) exact |= fabsf(fl) < INFINITY && (grp_logit<BF16>(a.logits, row + expert(u)) != ll || bias[u] != lb);
+          if (c[u] == fl) exact |= fabsf(fl) < INFINITY && (grp_logit<BF16>(a.logits, row + expert(u)) != ll || bias_of(u) != lb);
           else next = fmaxf(next, c[u]);
         }
         const uint32_t m = __reduce_max_sync(MOE_FULL_MASK, grp_key(next));
@@ -691,16 +745,21 @@ static int grp_sms(int* sms) {
   return MOE_OK;
 }
 
+template <int V, int NQ, bool BF16, bool FLAT>
+static int launch_groups_as(GroupArgs a, int sms, cudaStream_t s) {
+  a.live = std::min(32, a.topk_group * (FLAT ? std::max(a.group / V, 1) : a.lanes));
+  // as many CTAs as are resident: a warp keeps the bias and has the next token's logits on their way
+  constexpr int W = kGrpThreads / 32;
+  const dim3 grid(std::min((a.T + W - 1) / W, sms * kGrpResident<V, NQ * V, FLAT>)), block(kGrpThreads);
+  MOE_CUDA_TRY(launch_pdl(group_route_kernel<V, NQ, BF16, FLAT>, grid, block, 0, s, a));
+  return MOE_OK;
+}
+
 template <int V, int NQ, bool BF16>
 static int launch_groups(const GroupArgs& a, int sms, cudaStream_t s) {
-  // as many CTAs as are resident: a warp keeps the bias and has the next token's logits on their way
-  constexpr int W = kGrpThreads / 32, NE = NQ * V;
-  const dim3 grid(std::min((a.T + W - 1) / W, sms * grp_resident(NE))), block(kGrpThreads);
-  if (V > 1 && a.lanes * a.n_group == 32 && a.group == a.lanes * NE)
-    MOE_CUDA_TRY(launch_pdl(group_route_kernel<V, NQ, BF16, (V == 1)>, grid, block, 0, s, a));
-  else
-    MOE_CUDA_TRY(launch_pdl(group_route_kernel<V, NQ, BF16, true>, grid, block, 0, s, a));
-  return MOE_OK;
+  if (V > 1 && a.lanes * a.n_group == 32 && a.group == a.lanes * NQ * V)
+    return launch_groups_as<V, NQ, BF16, (V == 1)>(a, sms, s);
+  return launch_groups_as<V, NQ, BF16, true>(a, sms, s);
 }
 
 }  // namespace moe
@@ -721,11 +780,12 @@ extern "C" int moe_route_groups(const void* logits, int bf16, const float* sel_b
   int lanes = 32;
   while (lanes * n_group > 32) lanes /= 2;
   const int group = E / n_group;
-  const GroupArgs a{logits, sel_bias, token_mask, T, E, k, n_group, group, topk_group, lanes,
+  const int v = bf16 ? 8 : 4;
+  const GroupArgs a{logits, sel_bias, token_mask, T, E, k, n_group, group, topk_group, lanes, 0,
                     (uint32_t)(((1 << 20) + group - 1) / group), rflags, scale, ids, w};
   cudaStream_t s = (cudaStream_t)stream;
   // 16-byte vectors where every row starts on one
-  const int v = bf16 ? 8 : 4, each = (E + 31) / 32, vecs = (E / v + 31) / 32;  // of a lane
+  const int each = (E + 31) / 32, vecs = (E / v + 31) / 32;  // of a lane
   if (E % v == 0 && (uintptr_t)logits % 16 == 0) {
     if (bf16) {
       if (vecs <= 1) return launch_groups<8, 1, true>(a, sms, s);

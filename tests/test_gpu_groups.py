@@ -153,6 +153,21 @@ def test_infinities_nan_and_padding(dtype, sigmoid):
     assert torch.equal(r.ids, r8.ids) and torch.equal(r.w, r8.w)
 
 
+@pytest.mark.parametrize("ties", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E,k,G,g", [(8000, 512, 10, 8, 4), (500, 1024, 8, 16, 4), (300, 512, 16, 8, 4), (300, 256, 16, 8, 4),
+                                       (300, 128, 16, 8, 2), (300, 64, 16, 1, 1), (300, 64, 8, 1, 1), (200, 72, 12, 2, 1),
+                                       (200, 1024, 16, 32, 1), (200, 496, 16, 31, 1)])
+def test_few_lanes_and_many_rounds(T, E, k, G, g, dtype, ties):
+    """Picks out of few lanes' experts, about as many lanes as picks; more tokens than warps, some of them padding."""
+    logits = draw(T, E, T + E + k, dtype)
+    if ties:
+        logits = torch.round(logits * 2) / 2
+    mask = torch.rand(T, device=DEV, generator=torch.Generator(device=DEV).manual_seed(E)) > 0.1
+    check(logits, k, n_group=G, topk_group=g, bias=steps(E, k), sigmoid=True, mask=mask, scale=2.5)
+    check(logits, k, n_group=G, topk_group=g, group_max=True, renormalise=False, mask=mask)
+
+
 def test_against_the_router():
     """Without groups, bias and scale: the picks and weights of the router that takes x."""
     import expert_slot_cache_gb300 as M
