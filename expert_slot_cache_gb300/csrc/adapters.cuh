@@ -49,17 +49,16 @@ __device__ __forceinline__ int ad_sequence(const AdArgs& a, int t) {
 // The sequences of more than short_rows rows (and the rows of none), by tiles.
 int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, bool beside, cudaStream_t s);
 
-// v as a sum of NS bf16 numbers, eight values at once (packed pairs): truncation leaves an exact rest, so three of them
-// are all 24 bits; the last of two is rounded.  A rest of an infinity or a NaN counts as 0.
-template <int NS>
-__device__ __forceinline__ void ad_split8(const float (&v)[8], uint4 (&o)[NS]) {
-  uint32_t w[NS][4];
+// v as a sum of three bf16 numbers, eight values at once (packed pairs): truncation leaves an exact rest, so that they are
+// all 24 bits.  A rest of an infinity or a NaN counts as 0.
+__device__ __forceinline__ void ad_split8(const float (&v)[8], uint4 (&o)[3]) {
+  uint32_t w[3][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float x = v[2 * i], y = v[2 * i + 1];
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      if (s == NS - 1) {
+    for (int s = 0; s < 3; ++s) {
+      if (s == 2) {
         const __nv_bfloat162 q = __floats2bfloat162_rn(x, y);
         w[s][i] = *reinterpret_cast<const uint32_t*>(&q);
       } else {
@@ -71,13 +70,13 @@ __device__ __forceinline__ void ad_split8(const float (&v)[8], uint4 (&o)[NS]) {
     }
   }
 #pragma unroll
-  for (int s = 0; s < NS; ++s) o[s] = make_uint4(w[s][0], w[s][1], w[s][2], w[s][3]);
+  for (int s = 0; s < 3; ++s) o[s] = make_uint4(w[s][0], w[s][1], w[s][2], w[s][3]);
 }
 
 // Values c .. c + 7 of a row (R of them; zeros beyond) as three numbers each, [first | second | third][Rk].
 __device__ __forceinline__ void ad_put_parts(uint16_t* row, int Rk, int c, const float (&v)[8]) {
   uint4 o[3];
-  ad_split8<3>(v, o);
+  ad_split8(v, o);
 #pragma unroll
   for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(row + k * Rk + c) = o[k];
 }

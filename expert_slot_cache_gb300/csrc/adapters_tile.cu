@@ -13,8 +13,9 @@
 // 32 lanes) have columns to store.  The tensor cores truncate what they add: D1 is several accumulators in turn, added
 // by additions that round.
 //
-// v = scale x A^T enters the second product as a sum of two (bf16 results) or three (fp32 results) bf16 numbers: 16 or
-// 24 significant bits.  The products cost little beside the bytes: 2 R flops a byte of x.
+// v = scale x A^T enters the second product as a sum of three bf16 numbers, which are its 24 bits: with two (16 bits) a
+// result in which ranks nearly cancel was off by more than fp32 sums are.  (The third costs 4096 rows of R 64 1.3 us of 27.7,
+// most of it on v's way to the other CTAs.)  The products cost little beside the bytes: 2 R flops a byte of x.
 #include <algorithm>
 
 #include "adapters.cuh"
@@ -29,6 +30,7 @@ constexpr int kAtXBytes = kAtRows * 128;  // 64 inputs of a tile's rows
 constexpr int kAtStage = 4096;            // 32 rows x 128 bytes of results
 constexpr int kAtStages2 = 2;
 constexpr int kAtAcc = 4;
+constexpr int kAtParts = 3;  // bf16 numbers that v's fp32 is the sum of
 
 struct AtGeo {
   int tile, Rk, stages1;        // rows of a tile, R in sixteens, slots of the first ring
@@ -102,7 +104,6 @@ template <bool F32, int C>
 __global__ void __launch_bounds__(kAtThreads, 2)
     adapters_tile_kernel(const AdArgs a, const AtGeo g, const __grid_constant__ CUtensorMap mapX,
                          const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB) {
-  constexpr int NS = F32 ? 3 : 2;
   constexpr int kSize = F32 ? 4 : 2;
   extern __shared__ __align__(1024) unsigned char sm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
   const int copies = kAtRows / g.tile;                    // of a tile's rows in the 128 lanes
   const int per = g.tile / C;                             // rows that a CTA adds up
   const int mine = max(0, min(per, rows - rank * per));
-  const int atoms = (NS * g.Rk + 63) / 64;                // of v: 128 lanes x 128 bytes
+  const int atoms = (kAtParts * g.Rk + 63) / 64;                // of v: 128 lanes x 128 bytes
   // ---- the first product.  The loops that issue copies and products are run by whole warps, so that their operands
   // stay in uniform registers.
   const bool lead = elect_one();
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
   }
   cluster_sync();  // partial sums are there; the first ring is free in every CTA (its products are done)
   if (warp >= 2) {
-    // piece p (8 of the NS Rk values) of row t
+    // piece p (8 of the 3 Rk values) of row t
     auto v_at = [&](int t, int p) { return (uint32_t)((p / 8) * kAtXBytes + t * 128 + ((p % 8) ^ (t & 7)) * 16); };
     const int g8 = g.Rk / 8;
     for (int i = threadIdx.x - 64; i < mine * g8; i += 128) {
@@ -291,10 +292,10 @@ __global__ void __launch_bounds__(kAtThreads, 2)
       }
       if (a.parts) ad_put_parts(a.parts + (size_t)(row0 + t) * 3 * g.Rk, g.Rk, c, v);
       if (!a.out) continue;
-      uint4 o[NS];
-      ad_split8<NS>(v, o);
+      uint4 o[kAtParts];
+      ad_split8(v, o);
 #pragma unroll
-      for (int s = 0; s < NS; ++s) *reinterpret_cast<uint4*>(sm + v_at(t, s * g8 + c / 8)) = o[s];
+      for (int s = 0; s < kAtParts; ++s) *reinterpret_cast<uint4*>(sm + v_at(t, s * g8 + c / 8)) = o[s];
     }
     at_fence_async();
     named_sync(1, 128);
@@ -317,8 +318,8 @@ __global__ void __launch_bounds__(kAtThreads, 2)
       }
     if (a.out && copies > 1) {
       wait(vfull, 0);
-      for (int i = threadIdx.x - 64; i < rows * NS * g8; i += 128) {
-        const uint32_t at = v_at(i / (NS * g8), i % (NS * g8));
+      for (int i = threadIdx.x - 64; i < rows * kAtParts * g8; i += 128) {
+        const uint32_t at = v_at(i / (kAtParts * g8), i % (kAtParts * g8));
         const uint4 v = *reinterpret_cast<const uint4*>(sm + at);
         for (int n = 1; n < copies; ++n) *reinterpret_cast<uint4*>(sm + at + n * g.tile * 128) = v;
       }
@@ -358,8 +359,8 @@ __global__ void __launch_bounds__(kAtThreads, 2)
       tc_fence_after();
       if (lead && !dead) {
         uint64_t bd = b0 + (uint64_t)(s * (stage2 >> 4));
-        int r = 0;  // 16 ranks of B at a time, NS times over
-        for (int k = 0; k < NS * g.Rk; k += 16) {
+        int r = 0;  // 16 ranks of B at a time, three times over
+        for (int k = 0; k < kAtParts * g.Rk; k += 16) {
           umma_f16(tmem + b * kAtCols, a0 + (uint64_t)((k / 64) * (kAtXBytes >> 4) + (k % 64) / 8), bd, idesc, k != 0);
           r += 16;
           bd += 2048 >> 4;
@@ -497,7 +498,6 @@ static int at_launch(const AdArgs& a, const AtGeo& g, int bytes, const CUtensorM
 
 int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, bool beside, cudaStream_t s) {
   AtGeo g = {};
-  const int NS = f32 ? 3 : 2;
   g.Rk = (a.R + 15) / 16 * 16;
   // CTAs of a cluster and rows of a tile, by an estimate of the time: rounds of as many clusters as run at once, in each a
   // CTA takes 9 us and its share of the tile's bytes at 40 KB/us, less where the CTAs' sum would pass 6.6 MB/us.
@@ -522,7 +522,7 @@ int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, bool beside, cuda
   const int stage1 = kAtXBytes + g.Rk * 128;
   // two CTAs a SM up to 64 ranks
   g.stages1 = g.Rk <= 16 ? 4 : g.Rk <= 32 ? 3 : g.Rk <= 64 ? 2 : 3;
-  const int ring1 = std::max(g.stages1 * stage1, (NS * g.Rk + 63) / 64 * kAtXBytes);
+  const int ring1 = std::max(g.stages1 * stage1, (kAtParts * g.Rk + 63) / 64 * kAtXBytes);
   g.off2 = ring1;
   g.off_part = g.off2 + kAtStages2 * g.Rk * 256;
   g.off_bar = g.off_part + std::max(8 * kAtStage, g.tile * g.Rk * 4);

@@ -615,9 +615,9 @@ int moe_route_groups_grad(const void* logits, int bf16, const int32_t* ids, cons
  *           of x and out do not overlap
  *   kept    device fp32 [T][R] output, v (0 without an adapter), for the gradient,
  *           or NULL
- * Sums are fp32; v takes part in its product with 16 significant bits (24 for
- * fp32 results) where sequences are long.  The result does not depend on thread
- * timing; its last bits depend on the batch's sequences.  x of a row reaches no
+ * Sums are fp32, and v takes part in its product with all its 24 bits.  The
+ * result does not depend on thread timing; its last bits depend on the batch's
+ * sequences.  x of a row reaches no
  * other row.  (Waits are bounded: one that gives up sets MOE_DEV_TIMEOUT.)
  * An id outside [-1, L) sets MOE_DEV_BAD_EXPERT and counts as -1; a descending
  * seq_start sets MOE_DEV_BAD_GROUPS.

@@ -1,0 +1,33 @@
+"""The bits that the adapters' sums keep: v whole in its product."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV, BF, I32 = "cuda", torch.bfloat16, torch.int32
+
+
+def two_ranks(T, n, m, low):
+    """x [T][n], a [2][n], b [2][m] with x a_0 = 1 + 2^-9 + low, x a_1 = 1 + 2^-9, b_0 = 1, b_1 = -1."""
+    x, a, b = torch.zeros(T, n, dtype=BF, device=DEV), torch.zeros(1, 2, n, dtype=BF, device=DEV), torch.ones(1, 2, m, dtype=BF, device=DEV)
+    x[:, 0], x[:, 1], x[:, 2] = 1.0, 2.0 ** -9, low
+    a[0, 0, :3] = 1.0
+    a[0, 1, :2] = 1.0
+    b[0, 1] = -1.0
+    return x, a, b
+
+
+@pytest.mark.parametrize("low", [2.0 ** -14, 2.0 ** -18, 2.0 ** -20])
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("T", [1, 40, 300, 2000])
+def test_differences_of_close_values(T, dtype, low):
+    """out = low, exactly: v is held in fp32 (24 bits) and its product is with all of them."""
+    import expert_slot_cache_gb300 as M
+    x, a, b = two_ranks(T, 136, 72, low)
+    ids, starts = torch.zeros(1, dtype=I32, device=DEV), torch.tensor([0, T], dtype=I32, device=DEV)
+    one = torch.ones(1, device=DEV)
+    op = M.Adapters(a, b, one)
+    kept = torch.empty(T, 2, device=DEV)
+    assert bool((op.forward(x, ids, None, starts, out_dtype=dtype, kept=kept) == low).all())
+    if dtype == BF:  # dx is the same with A and B exchanged
+        rev = M.Adapters(b, a, one)
+        assert bool((rev.grad(x, None, None, ids, None, starts, with_weights=False).dx == low).all())
