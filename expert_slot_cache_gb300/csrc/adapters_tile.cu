@@ -10,8 +10,11 @@
 // Sending base to L2 while the first product runs costs more than it hides (4096 rows 30 us, 16,384 of R 16 50 for 41).
 //
 // The rows of a tile of 32 or 64 stand in the 128 lanes of D several times, so that all four epilogue warps (each reads
-// 32 lanes) have columns to store.  The tensor cores truncate what they add: D1 is several accumulators in turn, added
-// by additions that round.
+// 32 lanes) have columns to store.  The tensor cores truncate what they add, so that an error grows with every step in one
+// direction: D1 is several accumulators in turn, of 16 additions each at most, added by additions that round.  Where four of
+// them are not enough (DRAINS: more than 1024 inputs a CTA), the epilogue warps take each over into a sum in TMEM while the
+// others are filled.  (200 rows of 131,072 inputs, R 16: 86 us; with four accumulators of 256 additions 73, and v off by
+// 5e-6.  A kernel of its own: as a branch of the one kernel it cost the others 1 to 3%.)
 //
 // v = scale x A^T enters the second product as a sum of three bf16 numbers, which are its 24 bits: with two (16 bits) a
 // result in which ranks nearly cancel was off by more than fp32 sums are.  (The third costs 4096 rows of R 64 1.3 us of 27.7,
@@ -25,15 +28,16 @@ namespace moe {
 constexpr int kAtThreads = 192;  // TMA warp, MMA warp, four epilogue warps
 constexpr int kAtRows = 128;     // rows of a tile, at most (MMA M)
 constexpr int kAtCols = 128;     // outputs of a step of the second product
-constexpr uint32_t kAtTmem = 256;
 constexpr int kAtXBytes = kAtRows * 128;  // 64 inputs of a tile's rows
 constexpr int kAtStage = 4096;            // 32 rows x 128 bytes of results
 constexpr int kAtStages2 = 2;
-constexpr int kAtAcc = 4;
+constexpr int kAtAcc = 4;    // accumulators of D1; or three and their sum,
+constexpr int kAtDrain = 4;  // after so many steps of 64 inputs (four additions each)
 constexpr int kAtParts = 3;  // bf16 numbers that v's fp32 is the sum of
 
 struct AtGeo {
   int tile, Rk, stages1;        // rows of a tile, R in sixteens, slots of the first ring
+  int tmem;                     // TMEM columns: kAtAcc accumulators, two steps of D2
   int off2, off_part, off_bar;  // second ring, partial sums / staging, barriers
   int short_rows;               // sequences of up to so many rows are the row kernel's,
   int beside;                   // which has been launched before this one and may still run
@@ -100,7 +104,7 @@ __device__ void at_find(const AdArgs& a, const AtGeo& g, int ti, int* tmp, int* 
 // Where 16-byte piece i of the partial sums lies: rows a power of two apart meet no bank twice.
 __device__ __forceinline__ uint32_t at_piece(uint32_t i) { return (i ^ ((i >> 3) & 7)) * 16; }
 
-template <bool F32, int C>
+template <bool F32, int C, bool DRAINS>
 __global__ void __launch_bounds__(kAtThreads, 2)
     adapters_tile_kernel(const AdArgs a, const AtGeo g, const __grid_constant__ CUtensorMap mapX,
                          const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB) {
@@ -118,8 +122,10 @@ __global__ void __launch_bounds__(kAtThreads, 2)
   uint64_t* vfull = d1full + 1;                    // v of all rows is there,
   uint64_t* vrep = vfull + 1;                      // in all the lanes
   uint64_t* done = vrep + 1;                       // every product is
-  int* s_tile = reinterpret_cast<int*>(done + 1);  // [4]
-  int* s_scan = s_tile + 4;                          // [33]
+  uint64_t* afull = done + 1;                      // an accumulator of D1 is done,
+  uint64_t* aempty = afull + kAtAcc - 1;           // and taken over
+  int* s_tile = reinterpret_cast<int*>(aempty + kAtAcc - 1);  // [4]
+  int* s_scan = s_tile + 4;                                   // [33]
   volatile int* abort_flag = s_scan + 33;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_scan + 34);
   if (threadIdx.x == 0) {
@@ -133,13 +139,15 @@ __global__ void __launch_bounds__(kAtThreads, 2)
     mbar_init(vfull, 2);
     mbar_init(vrep, 4);
     mbar_init(done, 1);
+    if (DRAINS)
+      for (int i = 0; i < kAtAcc - 1; ++i) mbar_init(&afull[i], 1), mbar_init(&aempty[i], 4);
     *abort_flag = 0;
     mbar_fence_init();
   }
   // The row kernel waited for what came before it and reads and writes other rows: only the end has to be in order.
   if (!g.beside) pdl_wait();
   if (warp == 1) {  // (after the wait: a kernel before this one may have tensor memory to allocate yet)
-    tmem_alloc(s_tmem, kAtTmem);
+    tmem_alloc(s_tmem, g.tmem);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -148,7 +156,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
   const uint32_t tmem = *s_tmem;
   const int row0 = s_tile[0], rows = s_tile[1], l = s_tile[2];
   if (rows == 0 || l < 0) {  // (the whole cluster)
-    if (warp == 1) tmem_dealloc(tmem, kAtTmem);
+    if (warp == 1) tmem_dealloc(tmem, g.tmem);
     if (g.beside) pdl_wait();
     if (rows == 0) return;
   }
@@ -177,7 +185,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
     if (!dead) dead = !ad_wait(bar, parity, abort_flag, a.status);
   };
   const int kc = (a.K + 63) / 64, kc0 = kc * rank / C, kc1 = kc * (rank + 1) / C, nk = kc1 - kc0;
-  const int nacc = min(min((nk + 3) / 4, kAtAcc), (int)kAtTmem / g.Rk);  // accumulators of D1, taken in turn
+  const int nacc = DRAINS ? kAtAcc - 1 : (nk + kAtDrain - 1) / kAtDrain;  // accumulators of D1, taken in turn
   const int copies = kAtRows / g.tile;                    // of a tile's rows in the 128 lanes
   const int per = g.tile / C;                             // rows that a CTA adds up
   const int mine = max(0, min(per, rows - rank * per));
@@ -220,16 +228,21 @@ __global__ void __launch_bounds__(kAtThreads, 2)
     const uint32_t idesc = idesc_bf16(kAtRows, g.Rk, 0, 0);
     const uint64_t a0 = at_desc(smem_u32(sm), 16, 1024), b0 = at_desc(smem_u32(sm) + kAtXBytes, 16, 1024);
     int s = 0, n = 0;
-    uint32_t ph = 0;
+    uint32_t ph = 0, aph = 1;
     for (int i = 0; i < nk; ++i) {
+      const bool first = DRAINS ? i % kAtDrain == 0 : i < nacc, last = DRAINS && (i % kAtDrain == kAtDrain - 1 || i == nk - 1);
+      if (DRAINS && first && i >= kAtDrain * nacc) wait(&aempty[n], aph);
       wait(&full1[s], ph);
       tc_fence_after();
       const uint64_t at = (uint64_t)(s * (stage1 >> 4));
-      if (lead && !dead) umma_f16_k64(tmem + n * g.Rk, a0 + at, b0 + at, idesc, i >= nacc, 2, 2);
+      if (lead && !dead) umma_f16_k64(tmem + n * g.Rk, a0 + at, b0 + at, idesc, !first, 2, 2);
       if (lead) umma_commit(&empty1[s]);
+      if (last) {
+        if (lead) umma_commit(&afull[n]);
+      }
       __syncwarp();
       if (++s == g.stages1) s = 0, ph ^= 1;
-      if (++n == nacc) n = 0;
+      if ((!DRAINS || last) && ++n == nacc) n = 0, aph ^= 1;
     }
     if (lead) umma_commit(d1full);
     __syncwarp();
@@ -239,6 +252,27 @@ __global__ void __launch_bounds__(kAtThreads, 2)
   float scale = 0.f;
   if (warp >= 2) {
     scale = a.scale[l];
+    if constexpr (DRAINS) {
+      const uint32_t sum = tmem + lanes + (kAtAcc - 1) * g.Rk;
+      for (int j = 0; j * kAtDrain < nk; ++j) {
+        const int n = j % nacc;
+        wait(&afull[n], (j / nacc) & 1);
+        tc_fence_after();
+        for (int c = 0; c < g.Rk && copy == 0; c += 16) {
+          float v[16], w[16];
+          tmem_ld_w<16>(tmem + lanes + n * g.Rk + c, v);
+          if (j) tmem_ld_w<16>(sum + c, w);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = j ? v[i] + w[i] : v[i];
+          tmem_st16(sum + c, v);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&aempty[n]);
+      }
+    }
     if (nk > 0) {
       wait(d1full, 0);
       tc_fence_after();
@@ -246,11 +280,13 @@ __global__ void __launch_bounds__(kAtThreads, 2)
     const uint32_t dst = mapa_shared(smem_u32(part), (uint32_t)(row / per));
     const int first = (rank * per + row % per) * (g.Rk / 4);
     at_cluster_wait();  // every CTA of the cluster has started
+    const uint32_t d1 = tmem + lanes + (DRAINS ? (kAtAcc - 1) * g.Rk : 0);  // what is left to be added up
+    const int left = DRAINS ? min(nk, 1) : nacc;
     for (int c = 0; c < g.Rk && copy == 0; c += 16) {
       float w[kAtAcc][16];
 #pragma unroll
       for (int n = 0; n < kAtAcc; ++n)
-        if (n < nacc) tmem_ld_w<16>(tmem + lanes + n * g.Rk + c, w[n]);
+        if (n < left) tmem_ld_w<16>(d1 + n * g.Rk + c, w[n]);
       tmem_ld_wait();
       float v[16];
 #pragma unroll
@@ -258,7 +294,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         v[i] = 0.f;
 #pragma unroll
         for (int n = 0; n < kAtAcc; ++n)
-          if (n < nacc) v[i] += w[n][i];
+          if (n < left) v[i] += w[n][i];
       }
       if (row < rows) {
 #pragma unroll
@@ -462,15 +498,15 @@ __global__ void __launch_bounds__(kAtThreads, 2)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kAtTmem);
+    tmem_dealloc(tmem, g.tmem);
     __syncwarp();
   }
   at_cluster_wait();
   if (g.beside) pdl_wait();
 }
 
-template <bool F32, int C>
-static int at_launch(const AdArgs& a, const AtGeo& g, int bytes, const CUtensorMap& mx, const CUtensorMap& ma,
+template <bool F32, int C, bool DRAINS>
+static int at_launch_as(const AdArgs& a, const AtGeo& g, int bytes, const CUtensorMap& mx, const CUtensorMap& ma,
                      const CUtensorMap& mb, cudaStream_t s) {
   const long long tiles = std::min<long long>(a.T, a.T / g.tile + a.n_seq + 2ll);
   if (tiles * C > 0x7fffffffll) return MOE_ERR_ARG;
@@ -491,9 +527,16 @@ static int at_launch(const AdArgs& a, const AtGeo& g, int bytes, const CUtensorM
   static bool done[64] = {};
   constexpr int kMost = 227 * 1024 - 512;
   if (bytes > kMost) return MOE_ERR_ARG;
-  MOE_CUDA_TRY(ensure_smem(adapters_tile_kernel<F32, C>, kMost, done));
-  MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, adapters_tile_kernel<F32, C>, a, g, mx, ma, mb));
+  MOE_CUDA_TRY(ensure_smem(adapters_tile_kernel<F32, C, DRAINS>, kMost, done));
+  MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, adapters_tile_kernel<F32, C, DRAINS>, a, g, mx, ma, mb));
   return MOE_OK;
+}
+
+template <bool F32, int C>
+static int at_launch(const AdArgs& a, const AtGeo& g, int bytes, const CUtensorMap& mx, const CUtensorMap& ma,
+                     const CUtensorMap& mb, cudaStream_t s) {
+  return a.K > 64 * C * kAtDrain * kAtAcc ? at_launch_as<F32, C, true>(a, g, bytes, mx, ma, mb, s)
+                                          : at_launch_as<F32, C, false>(a, g, bytes, mx, ma, mb, s);
 }
 
 int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, bool beside, cudaStream_t s) {
@@ -519,6 +562,7 @@ int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, bool beside, cuda
     }
   g.short_rows = short_rows;
   g.beside = beside;
+  g.tmem = g.Rk <= 64 ? 256 : 512;  // (above 64 ranks a CTA has its SM for itself)
   const int stage1 = kAtXBytes + g.Rk * 128;
   // two CTAs a SM up to 64 ranks
   g.stages1 = g.Rk <= 16 ? 4 : g.Rk <= 32 ? 3 : g.Rk <= 64 ? 2 : 3;

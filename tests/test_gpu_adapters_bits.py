@@ -1,4 +1,4 @@
-"""The bits that the adapters' sums keep: v whole in its product."""
+"""The bits that the adapters' sums keep: v whole in its product, no drift where there are many features."""
 import pytest
 import torch
 
@@ -31,3 +31,22 @@ def test_differences_of_close_values(T, dtype, low):
     if dtype == BF:  # dx is the same with A and B exchanged
         rev = M.Adapters(b, a, one)
         assert bool((rev.grad(x, None, None, ids, None, starts, with_weights=False).dx == low).all())
+
+
+@pytest.mark.parametrize("R", [3, 64, 80, 128])
+def test_sums_over_many_features_do_not_drift(R):
+    """A truncated addition takes less than 2^-23 of the sum, always downwards; one that rounds has no direction.  With at
+    most 16 truncated ones in a row the mean of (v - exact) / exact over many sums of positive terms is within
+    16 * 2^-23 of 0, however many features there are."""
+    import expert_slot_cache_gb300 as M
+    T, K = 200, 131072
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = (torch.rand(T, K, generator=g, device=DEV) + 0.5).to(BF)
+    a = (torch.rand(1, R, K, generator=g, device=DEV) + 0.5).to(BF)
+    b = torch.zeros(1, R, 16, dtype=BF, device=DEV)
+    op = M.Adapters(a, b, torch.ones(1, device=DEV))
+    kept = torch.empty(T, R, device=DEV)
+    op.forward(x, torch.zeros(1, dtype=I32, device=DEV), None, torch.tensor([0, T], dtype=I32, device=DEV), kept=kept)
+    v = x.double() @ a[0].double().T
+    mean = float(((kept.double() - v) / v).mean())
+    assert abs(mean) <= 16 * 2.0 ** -23, mean
