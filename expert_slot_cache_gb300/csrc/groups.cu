@@ -498,10 +498,13 @@ __global__ void __launch_bounds__(kGrpThreads, kGrpResident<V, NQ * V, FLAT>) gr
         same += o == mine;
         if (o > mine) above = min(above, o);
       }
-      bool unsure = a.bias && on && place >= 1 && place <= a.k && above != 0xffffffffu && grp_close(above, mine, rel, bmax);
+      const bool close = a.bias && on && place >= 1 && above != 0xffffffffu && grp_close(above, mine, rel, bmax);
+      bool unsure = close && place <= a.k;
       if (__any_sync(MOE_FULL_MASK, on && same > 1)) {
+        int larger = 0;  // than the next larger one: with several of that, one may have a place though this one has none
         for (int j = 0; j < n; ++j) {
           const uint32_t o = __shfl_sync(MOE_FULL_MASK, mine, j);
+          larger += o > above;
           const int oe = __shfl_sync(MOE_FULL_MASK, e, j);
           const float oz = __shfl_sync(MOE_FULL_MASK, z, j), ob = __shfl_sync(MOE_FULL_MASK, bb, j);
           if (on && o == mine) {
@@ -510,6 +513,7 @@ __global__ void __launch_bounds__(kGrpThreads, kGrpResident<V, NQ * V, FLAT>) gr
             unsure |= a.bias && fabsf(grp_value(mine)) < INFINITY && (oz != z || ob != bb);
           }
         }
+        unsure |= close && larger < a.k;
       }
       if (!on) place = 32;
       if (__any_sync(MOE_FULL_MASK, unsure)) {
