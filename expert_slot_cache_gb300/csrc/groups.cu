@@ -112,6 +112,12 @@ __device__ __noinline__ double grp_sum64(const GroupArgs& a, size_t row, float m
   return s;
 }
 
+// A group's score from its two best.  One of +inf (a bias that pins an expert) is the score, whatever stands beside it.
+template <class F>
+__device__ __forceinline__ F grp_score(F b1, F b2, bool one) {
+  return one || b1 == (F)INFINITY ? b1 : b1 + b2;
+}
+
 // One expert's s in fp64.
 __device__ __noinline__ double grp_score64(float l, bool sig, float mx, double sum) {
   return sig ? 1. / (1. + exp(-(double)l)) : exp((double)l - (double)mx) / sum;
@@ -168,7 +174,7 @@ __device__ __noinline__ int grp_pick64(const GroupArgs& a, size_t row) {
       b2 = fmax(fmin(b1, o1), fmax(b2, o2));
       b1 = fmax(b1, o1);
     }
-    const uint64_t gk = g < a.n_group ? grp_key64(best || a.group == 1 ? b1 : b1 + b2) : 0ull;
+    const uint64_t gk = g < a.n_group ? grp_key64(grp_score(b1, b2, best || a.group == 1)) : 0ull;
     int before = 0;
     for (int h = 0; h < a.n_group; ++h) {
       const uint64_t ok = __shfl_sync(MOE_FULL_MASK, gk, h * a.lanes);
@@ -345,7 +351,7 @@ __global__ void __launch_bounds__(kGrpThreads, kGrpResident<V, NQ * V, FLAT>) gr
         b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
         b1 = fmaxf(b1, o1);
       }
-      const float best = one ? b1 : b1 + b2;
+      const float best = grp_score(b1, b2, one);
       const uint32_t gk = g < a.n_group ? grp_key(best) : 0u;
       int before = 0;
       for (int h = 0; h < a.n_group; ++h) {
@@ -359,7 +365,8 @@ __global__ void __launch_bounds__(kGrpThreads, kGrpResident<V, NQ * V, FLAT>) gr
         if (!(lo - hi > 2.f * (rel * (fabsf(lo) + 2.f * bmax) + kGrpTiny))) {
           // the groups in fp64, of what may be their best (without a bias a softmax's sum does not matter)
           sum64 = !sig && a.bias ? grp_sum64<BF16>(a, row, mx) : 1.;
-          const float low = one ? b1 : b2, least = low - 2.f * (rel * (fabsf(low) + bmax) + kGrpTiny);
+          const float low = one ? b1 : b2;
+          const float least = isinf(low) ? low : low - 2.f * (rel * (fabsf(low) + bmax) + kGrpTiny);
           if constexpr (FLAT) {
             if (i0 == 0) s_least[warp][g] = least;
             __syncwarp();
@@ -391,7 +398,7 @@ __global__ void __launch_bounds__(kGrpThreads, kGrpResident<V, NQ * V, FLAT>) gr
             }
             __syncwarp();
           }
-          const uint64_t gk64 = g < a.n_group ? grp_key64(one ? x1 : x1 + x2) : 0ull;
+          const uint64_t gk64 = g < a.n_group ? grp_key64(grp_score(x1, x2, one)) : 0ull;
           before = 0;
           for (int h = 0; h < a.n_group; ++h) {
             const uint64_t ok = __shfl_sync(MOE_FULL_MASK, gk64, h * a.lanes);

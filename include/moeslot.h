@@ -560,7 +560,8 @@ int moe_balance_loss(const void* logits, int bf16, const int32_t* ids, const uin
  * picks are those of 64-bit arithmetic; they do not depend on thread timing.
  * Renormalised picks that are all -inf have weight 0.
  *   logits     device [T][E], fp32 or bf16 (bf16 = 1)
- *   sel_bias   device fp32 [E] or NULL; -inf: never picked while k others stay
+ *   sel_bias   device fp32 [E] or NULL; -inf: never picked while k others stay;
+ *              +inf: before all others, and its group's score is +inf
  *   token_mask device uint8 [T], 0 = padding, or NULL; padding gets ids -1 and
  *              weights 0, its logits are not read into any result
  *   ids        device int32 [T][k] output
