@@ -639,7 +639,7 @@ class AdapterAdd(torch.autograd.Function):
         need_x, need_a, need_b = ctx.needs_input_grad[:3]
         rows = dy.detach()
         if rows.stride(1) != 1 or rows.stride(0) % 8 or rows.stride(0) < op.N or rows.data_ptr() % 16:
-            rows = rows.contiguous()
+            rows = rows.clone(memory_format=torch.contiguous_format)  # (contiguous() leaves a contiguous one on its address)
         dx = da = db = None
         if need_x or need_a or need_b:
             g = op.grad(rows, x, kept, ids, None, seq_start, need_x, need_a or need_b)
