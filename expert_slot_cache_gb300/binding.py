@@ -373,6 +373,13 @@ def _want(t: torch.Tensor, what: str, dtype, shape=None) -> None:
                          + f", got {t.dtype} {tuple(t.shape)}")
 
 
+def _want_status(t: torch.Tensor, dev: torch.device) -> None:
+    if t.dtype != torch.int32 or t.numel() < 1:
+        raise ValueError(f"dev_status: need int32 [1], got {t.dtype} {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"dev_status: on {t.device}, the call runs on {dev}")
+
+
 @_for_its_stream
 def w4_pack(codes: torch.Tensor, scales: torch.Tensor, group: int, stream=None) -> torch.Tensor:
     """codes uint8 [..., K, N] (0..15), scales bf16 [..., ceil(K / group), N] -> packed uint8 [..., w4_bytes]."""
@@ -496,10 +503,12 @@ class Adapters:
     ``a`` bf16 [L][R][K], ``b`` bf16 [L][R][N] and ``scale`` fp32 [L] are read where they are: what is written into them
     counts from the next call on.  Sequence q of a batch is the rows [seq_start[q], seq_start[q + 1]) with the adapter
     ids[q] (int32, -1: none); without ``seq_start`` every row is a sequence of its own.  Rows may be row-strided views
-    on 16 bytes.  ``AdapterAdd`` is the form for autograd; forward and grad carry no gradient themselves.
+    on 16 bytes.  ``AdapterAdd`` is the form for autograd; forward and grad carry no gradient themselves.  Errors found on
+    the device are recorded in ``dev_status`` (int32 [1]; the caller's, or one of its own).
     """
 
-    def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor):
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scale: torch.Tensor, dev_status: Optional[torch.Tensor] = None, *,
+                 _record: bool = True):
         if a.dim() != 3 or b.dim() != 3 or a.shape[:2] != b.shape[:2]:
             raise ValueError(f"a, b: need [L][R][K] and [L][R][N], got {tuple(a.shape)} and {tuple(b.shape)}")
         _want(a, "a", torch.bfloat16)
@@ -513,8 +522,13 @@ class Adapters:
         self.device, self._index = a.device, a.get_device()
         if b.device != a.device or scale.device != a.device:
             raise ValueError(f"a, b, scale: on {a.device}, {b.device} and {scale.device}")
-        self.dev_status = torch.zeros(1, dtype=torch.int32, device=a.device)
-        self._a, self._b, self._scale, self._status = (t.data_ptr() for t in (a, b, scale, self.dev_status))
+        if dev_status is not None:
+            _want_status(dev_status, a.device)
+        elif _record:
+            dev_status = torch.zeros(1, dtype=torch.int32, device=a.device)
+        self.dev_status = dev_status
+        self._a, self._b, self._scale = a.data_ptr(), b.data_ptr(), scale.data_ptr()
+        self._status = None if dev_status is None else dev_status.data_ptr()
 
     def _sequences(self, T, ids, seq_start):
         n = T if seq_start is None else seq_start.numel() - 1
@@ -615,27 +629,29 @@ class Adapters:
 
 
 class AdapterAdd(torch.autograd.Function):
-    """Adapters for autograd: ``out = AdapterAdd.apply(x, a, b, scale, ids, base, seq_start)``, bf16.
+    """Adapters for autograd: ``out = AdapterAdd.apply(x, a, b, scale, ids, base, seq_start, dev_status)``, bf16.
 
-    Gradients in x, a, b and base (none in scale).  There is no second derivative: differentiating the gradient again
+    Gradients in x, a, b and base (none in scale).  Errors found on the device in either pass are recorded in
+    ``dev_status`` (int32 [1]), where it is given.  There is no second derivative: differentiating the gradient again
     raises.
     """
 
     @staticmethod
-    def forward(ctx, x, a, b, scale, ids, base=None, seq_start=None):
+    def forward(ctx, x, a, b, scale, ids, base=None, seq_start=None, dev_status=None):
         if base is not None and base.dtype != torch.bfloat16:
             raise ValueError(f"base: bfloat16 where a gradient is wanted, got {base.dtype}")
         need = any(ctx.needs_input_grad[1:3])
-        op = Adapters(a, b, scale)
+        op = Adapters(a, b, scale, dev_status, _record=False)
         kept = torch.empty((x.shape[0], op.R), dtype=torch.float32, device=x.device) if need else None
         out = op.forward(x, ids, base, seq_start, kept=kept)
         ctx.save_for_backward(x if need else None, a, b, scale, ids, seq_start, kept)
+        ctx.dev_status = dev_status
         return out
 
     @staticmethod
     def backward(ctx, dy):
         x, a, b, scale, ids, seq_start, kept = ctx.saved_tensors
-        op = Adapters(a.detach(), b.detach(), scale.detach())
+        op = Adapters(a.detach(), b.detach(), scale.detach(), ctx.dev_status, _record=False)
         need_x, need_a, need_b = ctx.needs_input_grad[:3]
         rows = dy.detach()
         if rows.stride(1) != 1 or rows.stride(0) % 8 or rows.stride(0) < op.N or rows.data_ptr() % 16:
@@ -648,7 +664,7 @@ class AdapterAdd(torch.autograd.Function):
             db = g.db.to(b.dtype) if need_b else None
             if torch.is_grad_enabled():
                 dx, da, db = _FirstGrad.apply("AdapterAdd", 3, dx, da, db, dy, x, a, b)
-        return dx, da, db, None, None, dy if ctx.needs_input_grad[5] else None, None
+        return dx, da, db, None, None, dy if ctx.needs_input_grad[5] else None, None, None
 
 
 @_for_its_stream
@@ -872,9 +888,11 @@ def route_groups_grad(logits: torch.Tensor, ids: torch.Tensor, grad_w: torch.Ten
     if ids.dtype != torch.int32 or ids.shape != (T, k) or not ids.is_contiguous():
         raise ValueError(f"ids: need contiguous int32 [{T}][k], got {ids.dtype} {tuple(ids.shape)}")
     _want(grad_w, "grad_w", torch.float32, (T, k))
+    if dev_status is not None:
+        _want_status(dev_status, logits.device)
     dev, index = logits.device, logits.get_device()
-    if index < 0 or ids.get_device() != index or grad_w.get_device() != index or _elsewhere(dev_status, index):
-        _on(dev, ids=ids, grad_w=grad_w, dev_status=dev_status)
+    if index < 0 or ids.get_device() != index or grad_w.get_device() != index:
+        _on(dev, ids=ids, grad_w=grad_w)
     if stream is not None or _current_device() != index:
         with torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream):
             return route_groups_grad(logits, ids, grad_w, sigmoid, renormalise, scale, dev_status)
@@ -901,18 +919,21 @@ class _FirstGrad(torch.autograd.Function):
 
 class RouteGroups(torch.autograd.Function):
     """route_groups for autograd: ``ids, w = RouteGroups.apply(logits, k, n_group, topk_group, sel_bias, token_mask,
-    sigmoid, group_max, renormalise, scale)``.
+    sigmoid, group_max, renormalise, scale, dev_status)``.
 
-    The weights have a gradient in the logits, the picks none (nor has the bias).  There is no second derivative:
+    The weights have a gradient in the logits, the picks none (nor has the bias).  Errors that the backward pass finds on
+    the device are recorded in ``dev_status`` (int32 [1]), where it is given.  There is no second derivative:
     differentiating the gradient again raises.
     """
 
     @staticmethod
     def forward(ctx, logits, k, n_group=1, topk_group=1, sel_bias=None, token_mask=None, sigmoid=False, group_max=False,
-                renormalise=True, scale=1.0):
+                renormalise=True, scale=1.0, dev_status=None):
+        if dev_status is not None:
+            _want_status(dev_status, logits.device)
         r = route_groups(logits, k, n_group, topk_group, sel_bias, token_mask, sigmoid, group_max, renormalise, scale)
         ctx.save_for_backward(logits, r.ids)
-        ctx.args = sigmoid, renormalise, scale
+        ctx.args = sigmoid, renormalise, scale, dev_status
         ctx.mark_non_differentiable(r.ids)
         return r.ids, r.w
 
@@ -922,7 +943,7 @@ class RouteGroups(torch.autograd.Function):
         grad = route_groups_grad(logits, ids, grad_w.detach().float().contiguous(), *ctx.args)
         if torch.is_grad_enabled():
             grad = _FirstGrad.apply("RouteGroups", 1, grad, logits, grad_w)[0]
-        return (grad,) + (None,) * 9
+        return (grad,) + (None,) * 10
 
 
 def ffn_workspace_bytes(T: int, H: int, k: int, I: int) -> int:
