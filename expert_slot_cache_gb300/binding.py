@@ -466,6 +466,8 @@ class W4Linear:
             adapters.check(x, adapter_ids, seq_start, self.out_dtype, out)  # nothing is written where the second call refuses
             out = self.forward(x, out, stream)
             return adapters.forward(x, adapter_ids, out, seq_start, out, stream=stream)
+        if adapter_ids is not None or seq_start is not None:
+            raise ValueError("adapter_ids, seq_start: given without adapters")
         T, K = x.shape
         if T > self.max_tokens or K != self.K:
             raise ValueError(f"x is {T} x {K}; the layer takes up to {self.max_tokens} rows of {self.K}")
