@@ -250,9 +250,18 @@ static bool ad_shape(int T, int K, int N, int R, int L, const int32_t* seq, int 
   return T >= 1 && T <= (1 << 24) && K >= 8 && K <= (1 << 17) && N >= 8 && N <= (1 << 17) && R >= 1 && R <= kAdMaxR &&
          L >= 1 && L <= 65535 && n_seq >= 1 && n_seq <= (1 << 24) && (seq || n_seq == T);
 }
-// Rows of `ld` elements of `size` bytes that hold n: on 16 bytes, one behind the other.
-static bool ad_rows_ok(const void* p, long long ld, int n, int size) {
-  return (uintptr_t)p % 16 == 0 && ld * size % 16 == 0 && ld < (1ll << 31);
+// Rows of n elements, ld apart.
+static bool ad_ld_ok(long long ld, int n) { return ld >= n && ld < (1ll << 31); }
+// Rows of `ld` elements of `size` bytes start on 16 bytes.
+static bool ad_rows_ok(const void* p, long long ld, int size) { return (uintptr_t)p % 16 == 0 && ld * size % 16 == 0; }
+// Whether T rows of n bytes, ld apart, and T rows of m bytes, le apart, have no byte in common: apart, or side by side in
+// rows of one stride.  (Rows of two strides over one range count as overlapping.)
+static bool ad_apart(const void* p, long long ld, long long n, const void* q, long long le, long long m, int T) {
+  const long long a = (long long)(uintptr_t)p, b = (long long)(uintptr_t)q;
+  if (a + (T - 1) * ld + n <= b || b + (T - 1) * le + m <= a) return true;
+  if (T == 1 || ld != le) return false;
+  const long long d = ((b - a) % ld + ld) % ld;  // q's rows begin d bytes into p's
+  return d >= n && d + m <= ld;
 }
 static size_t ad256(size_t v) { return (v + 255) & ~size_t(255); }
 
@@ -266,10 +275,12 @@ extern "C" int moe_adapters(const void* x, long long ldx, const void* base, long
                             int32_t* dev_status, moe_stream_t stream) {
   if (!x || !a || !b || !scale || !ids || !out || (out_f32 != 0 && out_f32 != 1)) return MOE_ERR_ARG;
   if (!ad_shape(T, K, N, R, L, seq_start, n_seq)) return MOE_ERR_ARG;
-  if (ldx < K || ldo < N || (base && ldb < N) || out == x || (out == base && ldb != ldo)) return MOE_ERR_ARG;
+  if (!ad_ld_ok(ldx, K) || !ad_ld_ok(ldo, N) || (base && !ad_ld_ok(ldb, N))) return MOE_ERR_ARG;
   const int size = out_f32 ? 4 : 2;
-  if (K % 8 || N % 8 || !ad_rows_ok(x, ldx, K, 2) || !ad_rows_ok(out, ldo, N, size) ||
-      (base && !ad_rows_ok(base, ldb, N, size)) || (uintptr_t)a % 16 || (uintptr_t)b % 16)
+  if (!ad_apart(x, ldx * 2, K * 2, out, ldo * size, N * size, T) ||
+      (base && (base != out || ldb != ldo) && !ad_apart(base, ldb * size, N * size, out, ldo * size, N * size, T)))
+    return MOE_ERR_ARG;
+  if (K % 8 || N % 8 || !ad_rows_ok(x, ldx, 2) || !ad_rows_ok(out, ldo, size) || (base && !ad_rows_ok(base, ldb, size)) || (uintptr_t)a % 16 || (uintptr_t)b % 16)
     return MOE_ERR_ALIGN;
   const AdArgs g{(const uint16_t*)x, (const uint16_t*)a, (const uint16_t*)b, scale, ids, seq_start, base, out, kept,
                  nullptr, nullptr, dev_status, ldx, base ? ldb : 0, ldo, T, K, N, R, L, n_seq};
@@ -289,10 +300,14 @@ extern "C" int moe_adapters_grad(const void* dy, long long ldy, const void* x, l
   if (!dy || !a || !b || !scale || !ids || !workspace || (!dx && !da) || (!da != !db) || (da && (!x || !kept)))
     return MOE_ERR_ARG;
   if (!ad_shape(T, K, N, R, L, seq_start, n_seq)) return MOE_ERR_ARG;
-  if (ldy < N || (da && ldx < K) || (dx && lddx < K) || (dx && base && ldb < K)) return MOE_ERR_ARG;
-  if (dx && (dx == dy || dx == x || (dx == base && ldb != lddx))) return MOE_ERR_ARG;
-  if (K % 8 || N % 8 || !ad_rows_ok(dy, ldy, N, 2) || (da && !ad_rows_ok(x, ldx, K, 2)) ||
-      (dx && !ad_rows_ok(dx, lddx, K, 2)) || (dx && base && !ad_rows_ok(base, ldb, K, 2)) || (uintptr_t)a % 16 ||
+  if (!ad_ld_ok(ldy, N) || (da && !ad_ld_ok(ldx, K)) || (dx && !ad_ld_ok(lddx, K)) || (dx && base && !ad_ld_ok(ldb, K)))
+    return MOE_ERR_ARG;
+  if (dx && (dx == x || !ad_apart(dy, ldy * 2, N * 2, dx, lddx * 2, K * 2, T) ||
+             (da && !ad_apart(x, ldx * 2, K * 2, dx, lddx * 2, K * 2, T)) ||
+             (base && (base != dx || ldb != lddx) && !ad_apart(base, ldb * 2, K * 2, dx, lddx * 2, K * 2, T))))
+    return MOE_ERR_ARG;
+  if (K % 8 || N % 8 || !ad_rows_ok(dy, ldy, 2) || (da && !ad_rows_ok(x, ldx, 2)) || (dx && !ad_rows_ok(dx, lddx, 2)) ||
+      (dx && base && !ad_rows_ok(base, ldb, 2)) || (uintptr_t)a % 16 ||
       (uintptr_t)b % 16 || (uintptr_t)da % 16 || (uintptr_t)db % 16 || (uintptr_t)workspace % 256 ||
       workspace_bytes < moe_adapters_grad_workspace_bytes(T, R))
     return MOE_ERR_ALIGN;

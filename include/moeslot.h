@@ -604,7 +604,7 @@ int moe_route_groups_grad(const void* logits, int bf16, const int32_t* ids, cons
  *   out[t] = base[t] + v[t] B_l            (base NULL: 0), rounded once
  *   x       device bf16 [T] rows of K, ldx elements apart (ldx >= K)
  *   base    device [T] rows of N, ldb apart, of the type of out, or NULL; it may
- *           be out itself (then ldb = ldo)
+ *           be out itself (then ldb = ldo), else no byte of it may be out's
  *   a, b    device bf16 [L][R][K] and [L][R][N]: rank r of A reads, rank r of B
  *           writes one run of features.  Smaller ranks: zero rows.
  *   scale   device fp32 [L]
@@ -612,8 +612,9 @@ int moe_route_groups_grad(const void* logits, int bf16, const int32_t* ids, cons
  *   seq_start  device int32 [n_seq + 1], ascending, empty sequences allowed, or
  *           NULL with n_seq = T: every row is a sequence of its own (decoding).
  *           Rows before the first and behind the last sequence have no adapter.
- *   out     device [T] rows of N, ldo apart: bf16, or fp32 with out_f32 = 1; rows
- *           of x and out do not overlap
+ *   out     device [T] rows of N, ldo apart: bf16, or fp32 with out_f32 = 1; no
+ *           byte of it may be x's (columns side by side of one buffer are fine,
+ *           with one stride), nor any other argument's
  *   kept    device fp32 [T][R] output, v (0 without an adapter), for the gradient,
  *           or NULL
  * Sums are fp32, and v takes part in its product with all its 24 bits.  The
@@ -624,9 +625,9 @@ int moe_route_groups_grad(const void* logits, int bf16, const int32_t* ids, cons
  * seq_start sets MOE_DEV_BAD_GROUPS.
  * Errors: MOE_ERR_ARG on NULL pointers, T not in [1, 2^24], K or N not in
  * [8, 2^17], R not in [1, 128], L not in [1, 65535], n_seq not in [1, 2^24],
- * leading dimensions too small, out = x, or out = base with another leading
- * dimension; MOE_ERR_ALIGN if K or N is no multiple of 8, or a matrix
- * or a row of one does not start on 16 bytes.
+ * leading dimensions too small or not below 2^31, or out over x, or over base
+ * otherwise than as base itself; MOE_ERR_ALIGN if K or N is no multiple of 8, or
+ * a matrix or a row of one does not start on 16 bytes.
  */
 int moe_adapters(const void* x, long long ldx, const void* base, long long ldb, int T, int K, int N, int R, int L,
                  const void* a, const void* b, const float* scale, const int32_t* ids, const int32_t* seq_start,
@@ -643,16 +644,16 @@ int moe_adapters(const void* x, long long ldx, const void* base, long long ldb, 
  *   x, kept as in and from moe_adapters (not needed without da and db)
  *   base    device bf16 [T] rows of K, ldb apart, or NULL: the gradient in x of
  *           the projection itself; it may be dx
- *   dx      device bf16 [T] rows of K, lddx apart, or NULL; it overlaps neither
- *           dy nor x
+ *   dx      device bf16 [T] rows of K, lddx apart, or NULL; no byte of it may be
+ *           another argument's, but for base = dx
  *   da, db  device fp32 [L][R][K] and [L][R][N], written whole (0 for adapters
  *           without rows), or both NULL
  *   workspace  device, moe_adapters_grad_workspace_bytes(T, R), 256-byte aligned
  * Sums are fp32, in an order that does not depend on thread timing; dv and kept
  * take part in da and db with all their bits.
  * Errors: as moe_adapters; MOE_ERR_ARG without dx, da and db, with only one of
- * da and db, or dx = dy or x; MOE_ERR_ALIGN for
- * an unaligned or small workspace.
+ * da and db, or with dx over dy or x, or over base otherwise than as base
+ * itself; MOE_ERR_ALIGN for an unaligned or small workspace.
  */
 size_t moe_adapters_grad_workspace_bytes(int T, int R);
 int moe_adapters_grad(const void* dy, long long ldy, const void* x, long long ldx, const float* kept, const void* base,
