@@ -493,6 +493,15 @@ class W4Linear:
 # Low-rank adapters beside a projection
 # ---------------------------------------------------------------------------
 
+def _rows_apart(x: torch.Tensor, y: torch.Tensor) -> bool:
+    """Whether two matrices of as many rows have no byte in common: apart, or side by side in rows of one stride."""
+    (p, ld, n), (q, le, m) = ((t.data_ptr(), t.stride(0) * t.element_size(), t.shape[1] * t.element_size()) for t in (x, y))
+    T = x.shape[0]
+    if p + (T - 1) * ld + n <= q or q + (T - 1) * le + m <= p:
+        return True
+    return T > 1 and ld == le and (q - p) % ld >= n and (q - p) % ld + m <= ld
+
+
 class AdapterGrads(NamedTuple):
     dx: Optional[torch.Tensor]  # bf16 [T][K]
     da: Optional[torch.Tensor]  # fp32 [L][R][K]
@@ -550,12 +559,17 @@ class Adapters:
     def check(self, x, ids, seq_start, dtype, out) -> None:
         """Refuses what forward would refuse."""
         T = x.shape[0]
-        self._sequences(T, ids, seq_start)
+        if self._sequences(T, ids, seq_start) < 1:
+            raise MoeError(-1, "Adapters (no sequence)")
         for what, t, n, kind in (("x", x, self.K, torch.bfloat16), ("out", out, self.N, dtype)):
             if t is not None:
                 at, ld = self._rows(t, what, T, n, kind)
+                if ld < n:
+                    raise MoeError(-1, f"Adapters ({what})")
                 if at % 16 or ld * t.element_size() % 16:
                     raise MoeError(-3, f"Adapters ({what})")
+        if out is not None and not _rows_apart(x, out):
+            raise MoeError(-1, "Adapters (out over x)")
         _on(self.device, x=x, ids=ids, seq_start=seq_start, out=out)
 
     def forward(self, x: torch.Tensor, ids: torch.Tensor, base: Optional[torch.Tensor] = None,

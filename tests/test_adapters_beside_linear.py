@@ -27,3 +27,20 @@ def test_ids_without_adapters(lin):
         with pytest.raises(ValueError, match="without adapters"):
             lin.forward(x, **kw)
     assert not lin.written
+
+
+def test_refused_before_anything_is_written(lin):
+    x, ids, starts = Z(4, 64, dtype=BF), Z(2, dtype=I32), Z(3, dtype=I32)
+    buf = Z(4 * 64 + 4096, dtype=BF)
+    buf = buf[(-buf.data_ptr() % 16) // 2:]
+    rows = buf[:256].view(4, 64)
+    bad = [dict(adapter_ids=ids[:0], seq_start=starts[:1]),               # no sequence
+           dict(x=buf[:64].expand(4, 64)),                                # rows on top of each other
+           dict(out=buf.as_strided((4, 64), (56, 1))),
+           dict(x=rows, out=rows),                                        # in place
+           dict(x=rows, out=buf[64:64 + 256].view(4, 64)),                # over the next rows
+           dict(out=buf[4:260].view(4, 64))]                              # not on 16 bytes
+    for kw in bad:
+        with pytest.raises((ValueError, lin.b.MoeError)):
+            lin.forward(**dict(dict(x=x, adapters=lin.op, adapter_ids=ids, seq_start=starts), **kw))
+        assert not lin.written, kw
