@@ -300,6 +300,8 @@ extern "C" int moe_adapters_grad(const void* dy, long long ldy, const void* x, l
   if (!dy || !a || !b || !scale || !ids || !workspace || (!dx && !da) || (!da != !db) || (da && (!x || !kept)))
     return MOE_ERR_ARG;
   if (!ad_shape(T, K, N, R, L, seq_start, n_seq)) return MOE_ERR_ARG;
+  // each block of features of each adapter looks at all sequences: about a second's work at the limit
+  if (da && (long long)L * n_seq > (1ll << 44) / (K + N)) return MOE_ERR_ARG;
   if (!ad_ld_ok(ldy, N) || (da && !ad_ld_ok(ldx, K)) || (dx && !ad_ld_ok(lddx, K)) || (dx && base && !ad_ld_ok(ldb, K)))
     return MOE_ERR_ARG;
   if (dx && (dx == x || !ad_apart(dy, ldy * 2, N * 2, dx, lddx * 2, K * 2, T) ||

@@ -51,10 +51,18 @@ struct AoTiles {
       }
       if (m == 0) {
         if (s >= a.n_seq) return false;
-        const int q = s + (threadIdx.x & 31);
-        s += 32;
+        // the next 32 sequences with one of l's, four times 32 looked at at once
+        int q = s + (threadIdx.x & 31), id[4];
+        unsigned any[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) id[i] = q + 32 * i < a.n_seq ? a.ids[q + 32 * i] : -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) any[i] = __ballot_sync(MOE_FULL_MASK, id[i] == l);
+        const int skip = any[0] ? 0 : any[1] ? 1 : any[2] ? 2 : 3;
+        q += 32 * skip;
+        s += 32 * (skip + 1);
         t0 = n = 0;
-        if (q < a.n_seq && a.ids[q] == l) {
+        if ((any[0] ? id[0] : any[1] ? id[1] : any[2] ? id[2] : id[3]) == l) {
           t0 = a.seq ? min(max(a.seq[q], 0), a.T) : q;
           n = a.seq ? max(min(max(a.seq[q + 1], 0), a.T) - t0, 0) : 1;
         }
@@ -121,11 +129,17 @@ __global__ void __launch_bounds__(kAoThreads)
   tc_fence_after();
   pdl_trigger();
   int mine = 0;
-  for (int q = threadIdx.x; q < a.n_seq; q += kAoThreads)
-    if (a.ids[q] == l) {
-      const int n = a.seq ? min(max(a.seq[q + 1], 0), a.T) - min(max(a.seq[q], 0), a.T) : 1;
-      if (n > 0) mine += (n + kAoRows - 1) / kAoRows;
-    }
+  for (int q0 = threadIdx.x; q0 < a.n_seq; q0 += 4 * kAoThreads) {
+    int id[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) id[i] = q0 + i * kAoThreads < a.n_seq ? a.ids[q0 + i * kAoThreads] : -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (id[i] == l) {
+        const int q = q0 + i * kAoThreads, n = a.seq ? min(max(a.seq[q + 1], 0), a.T) - min(max(a.seq[q], 0), a.T) : 1;
+        if (n > 0) mine += (n + kAoRows - 1) / kAoRows;
+      }
+  }
   __syncwarp();
   mine = __reduce_add_sync(MOE_FULL_MASK, mine);
   if (lane == 0 && mine) atomicAdd(s_total, mine);
@@ -299,9 +313,19 @@ __global__ void __launch_bounds__(kAsThreads) adapters_outer_short_kernel(const 
   const long long ld = first ? a.ldx : a.ldy;
   const float* v = (first ? a.dv : a.v) + r0;
   float acc[2 * kAsRanks] = {};
-  // sequences 128 at a time; their rows listed in order, up to kAsList of them at a time
+  // sequences 128 at a time (512 without any of l's are passed over at once); their rows listed in order, up to kAsList of
+  // them at a time
   for (int q0 = 0; q0 < a.n_seq; q0 += kAsThreads) {
     const int q = q0 + (int)threadIdx.x;
+    if (q0 % (4 * kAsThreads) == 0 && a.n_seq > 4 * kAsThreads) {
+      bool any = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) any |= q + i * kAsThreads < a.n_seq && a.ids[q + i * kAsThreads] == l;
+      if (!__syncthreads_or(any)) {
+        q0 += 3 * kAsThreads;
+        continue;
+      }
+    }
     int t = 0, n = 0;
     if (q < a.n_seq && a.ids[q] == l) {
       t = a.seq ? min(max(a.seq[q], 0), a.T) : q;

@@ -652,8 +652,8 @@ int moe_adapters(const void* x, long long ldx, const void* base, long long ldb, 
  * Sums are fp32, in an order that does not depend on thread timing; dv and kept
  * take part in da and db with all their bits.
  * Errors: as moe_adapters; MOE_ERR_ARG without dx, da and db, with only one of
- * da and db, or with dx over dy or x, or over base otherwise than as base
- * itself; MOE_ERR_ALIGN for an unaligned or small workspace.
+ * da and db, with L n_seq (K + N) > 2^44 where there are da and db, or with dx
+ * over dy or x, or over base otherwise than as base itself; MOE_ERR_ALIGN for an unaligned or small workspace.
  */
 size_t moe_adapters_grad_workspace_bytes(int T, int R);
 int moe_adapters_grad(const void* dy, long long ldy, const void* x, long long ldx, const float* kept, const void* base,
