@@ -128,6 +128,9 @@ __global__ void __launch_bounds__(kAoThreads)
   __syncthreads();
   tc_fence_after();
   pdl_trigger();
+  // An adapter has no more tiles than `most`: starts that descend (flagged by the kernels before) make its sequences overlap,
+  // and no more work.
+  const int most = a.T / kAoRows + a.n_seq;
   int mine = 0;
   for (int q0 = threadIdx.x; q0 < a.n_seq; q0 += 4 * kAoThreads) {
     int id[4];
@@ -137,15 +140,15 @@ __global__ void __launch_bounds__(kAoThreads)
     for (int i = 0; i < 4; ++i)
       if (id[i] == l) {
         const int q = q0 + i * kAoThreads, n = a.seq ? min(max(a.seq[q + 1], 0), a.T) - min(max(a.seq[q], 0), a.T) : 1;
-        if (n > 0) mine += (n + kAoRows - 1) / kAoRows;
+        if (n > 0) mine = min(mine + (n + kAoRows - 1) / kAoRows, most);
       }
   }
   __syncwarp();
-  mine = __reduce_add_sync(MOE_FULL_MASK, mine);
+  mine = min((int)__reduce_add_sync(MOE_FULL_MASK, mine), most);  // (a warp's sum is below 2^30)
   if (lane == 0 && mine) atomicAdd(s_total, mine);
   __syncthreads();
   const uint32_t tmem = *s_tmem;
-  const int total = *s_total;
+  const int total = min(*s_total, most);
   AoTiles tiles{a, l, (int)((long long)total * rank / S), (int)((long long)total * (rank + 1) / S)};
   const int nt = tiles.hi - tiles.lo;
   bool dead = false;  // (of a whole warp) nothing is waited for or issued after a timeout
@@ -313,9 +316,10 @@ __global__ void __launch_bounds__(kAsThreads) adapters_outer_short_kernel(const 
   const long long ld = first ? a.ldx : a.ldy;
   const float* v = (first ? a.dv : a.v) + r0;
   float acc[2 * kAsRanks] = {};
+  unsigned left = (unsigned)a.T;  // rows: sequences that overlap (starts that descend, flagged before) are no more work
   // sequences 128 at a time (512 without any of l's are passed over at once); their rows listed in order, up to kAsList of
   // them at a time
-  for (int q0 = 0; q0 < a.n_seq; q0 += kAsThreads) {
+  for (int q0 = 0; q0 < a.n_seq && left > 0; q0 += kAsThreads) {
     const int q = q0 + (int)threadIdx.x;
     if (q0 % (4 * kAsThreads) == 0 && a.n_seq > 4 * kAsThreads) {
       bool any = false;
@@ -331,8 +335,10 @@ __global__ void __launch_bounds__(kAsThreads) adapters_outer_short_kernel(const 
       t = a.seq ? min(max(a.seq[q], 0), a.T) : q;
       n = a.seq ? max(min(max(a.seq[q + 1], 0), a.T) - t, 0) : 1;
     }
-    int total;
-    const int at = block_exclusive_scan(n, s_scan, &total);
+    int sum;
+    const int at = block_exclusive_scan(n, s_scan, &sum);  // (at most 2^31)
+    const int total = (int)min((unsigned)sum, left);
+    left -= (unsigned)total;
     for (int base = 0; base < total; base += kAsList) {
       for (int i = max(base - at, 0); i < min(n, base + kAsList - at); ++i) s_row[at + i - base] = t + i;
       __syncthreads();
