@@ -314,17 +314,18 @@ extern "C" int moe_adapters_grad(const void* dy, long long ldy, const void* x, l
       workspace_bytes < moe_adapters_grad_workspace_bytes(T, R))
     return MOE_ERR_ALIGN;
   cudaStream_t s = (cudaStream_t)stream;
-  // dv in fp32 for the short sequences' kernel, in parts for the tiles'
+  // dv in fp32 for the short sequences' kernel, in parts (with kept) for the tiles'
   float* dv = (float*)workspace;
   uint16_t* parts = (uint16_t*)((char*)workspace + ad256((size_t)T * R * 4));
-  const bool tiles = ad_outer_by_tiles(T, n_seq, seq_start);
+  const AdOuter by = ad_outer_by(T, n_seq, seq_start);
+  const bool tiles = by != AdOuter::kShort;
   const AdArgs g{(const uint16_t*)dy, (const uint16_t*)b, (const uint16_t*)a, scale, ids, seq_start, dx ? base : nullptr,
-                 dx, da && !tiles ? dv : nullptr, kept, da && tiles ? parts : nullptr, dev_status, ldy,
+                 dx, da && by != AdOuter::kTiles ? dv : nullptr, kept, da && tiles ? parts : nullptr, dev_status, ldy,
                  dx && base ? ldb : 0, lddx, T, N, K, R, L, n_seq};
   if (int rc = ad_run(g, false, s)) return rc;
   if (!da) return MOE_OK;
   const AdGradArgs o{(const uint16_t*)x, (const uint16_t*)dy, dv, kept, ids, seq_start, da, db, tiles ? parts : nullptr,
-                     dev_status, ldx, ldy, T, K, N, R, L, n_seq};
+                     dev_status, ldx, ldy, T, K, N, R, L, n_seq, by == AdOuter::kBoth};
   int sms = 0;
   if (int rc = ad_sms(&sms)) return rc;
   return ad_launch_outer(o, sms, s);

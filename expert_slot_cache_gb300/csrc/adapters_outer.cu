@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kAoThreads)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done + 1);
   int* s_total = reinterpret_cast<int*>(s_tmem + 1);
   volatile int* abort_flag = s_total + 1;
+  unsigned* s_excess = reinterpret_cast<unsigned*>(s_total + 2);
   float* part = reinterpret_cast<float*>(sm + g.off_part);  // [Rk][128]
   const int stage = kAoXBytes + g.atoms * kAoAtom;
   if (threadIdx.x == 0) {
@@ -117,6 +118,7 @@ __global__ void __launch_bounds__(kAoThreads)
     for (int i = 0; i < g.acc; ++i) mbar_init(&tfull[i], 1), mbar_init(&tempty[i], 4);
     *abort_flag = 0;
     *s_total = 0;
+    *s_excess = 0;
     mbar_fence_init();
   }
   pdl_wait();
@@ -132,6 +134,7 @@ __global__ void __launch_bounds__(kAoThreads)
   // and no more work.
   const int most = a.T / kAoRows + a.n_seq;
   int mine = 0;
+  unsigned excess = 0;
   for (int q0 = threadIdx.x; q0 < a.n_seq; q0 += 4 * kAoThreads) {
     int id[4];
 #pragma unroll
@@ -140,14 +143,22 @@ __global__ void __launch_bounds__(kAoThreads)
     for (int i = 0; i < 4; ++i)
       if (id[i] == l) {
         const int q = q0 + i * kAoThreads, n = a.seq ? min(max(a.seq[q + 1], 0), a.T) - min(max(a.seq[q], 0), a.T) : 1;
-        if (n > 0) mine = min(mine + (n + kAoRows - 1) / kAoRows, most);
+        if (n > 0) mine = min(mine + (n + kAoRows - 1) / kAoRows, most), excess += (unsigned)(n - kAdLong);
       }
   }
   __syncwarp();
   mine = min((int)__reduce_add_sync(MOE_FULL_MASK, mine), most);  // (a warp's sum is below 2^30)
   if (lane == 0 && mine) atomicAdd(s_total, mine);
+  if (a.both) {
+    excess = __reduce_add_sync(MOE_FULL_MASK, excess);
+    if (lane == 0) atomicAdd(s_excess, excess);
+  }
   __syncthreads();
   const uint32_t tmem = *s_tmem;
+  if (a.both && (int)*s_excess < 0) {  // (the whole cluster) rows fewer than kAdLong a sequence: the other kernel's
+    if (warp == 1) tmem_dealloc(tmem, g.tmem);
+    return;
+  }
   const int total = min(*s_total, most);
   AoTiles tiles{a, l, (int)((long long)total * rank / S), (int)((long long)total * (rank + 1) / S)};
   const int nt = tiles.hi - tiles.lo;
@@ -302,13 +313,35 @@ __global__ void __launch_bounds__(kAoThreads)
   }
 }
 
+// Whether an adapter's rows are kAdLong a sequence or more, as the kernel above finds it (by all threads of the CTA).
+__device__ __forceinline__ bool ao_long(const AdGradArgs& a, int l, unsigned* excess) {
+  if (threadIdx.x == 0) *excess = 0;
+  __syncthreads();
+  unsigned mine = 0;
+  for (int q0 = threadIdx.x; q0 < a.n_seq; q0 += 4 * blockDim.x) {
+    int id[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) id[i] = q0 + i * blockDim.x < a.n_seq ? a.ids[q0 + i * blockDim.x] : -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (id[i] == l) {
+        const int q = q0 + i * blockDim.x, n = min(max(a.seq[q + 1], 0), a.T) - min(max(a.seq[q], 0), a.T);
+        if (n > 0) mine += (unsigned)(n - kAdLong);
+      }
+  }
+  __syncwarp();
+  mine = __reduce_add_sync(MOE_FULL_MASK, mine);
+  if ((threadIdx.x & 31) == 0) atomicAdd(excess, mine);
+  __syncthreads();
+  return (int)*excess >= 0;
+}
+
 // Short sequences: a thread has two features and 16 ranks; the rows of the adapter are listed in shared memory.
 constexpr int kAsThreads = 128;
 constexpr int kAsRanks = 16;
 constexpr int kAsList = 1024;
-__global__ void __launch_bounds__(kAsThreads) adapters_outer_short_kernel(const AdGradArgs a, int blocks_a) {
+__device__ __forceinline__ void ao_short(const AdGradArgs& a, int blocks_a) {
   __shared__ int s_row[kAsList], s_scan[33];
-  pdl_wait();
   const bool first = (int)blockIdx.x < blocks_a;
   const int F = first ? a.K : a.N, f = (((int)blockIdx.x - (first ? 0 : blocks_a)) * kAsThreads + threadIdx.x) * 2;
   const int l = blockIdx.y, r0 = blockIdx.z * kAsRanks, nr = min(kAsRanks, a.R - r0);
@@ -370,14 +403,27 @@ __global__ void __launch_bounds__(kAsThreads) adapters_outer_short_kernel(const 
   for (int j = 0; j < kAsRanks; ++j)
     if (j < nr) *reinterpret_cast<float2*>(o + (size_t)j * F) = make_float2(acc[2 * j], acc[2 * j + 1]);
 }
+__global__ void __launch_bounds__(kAsThreads) adapters_outer_short_kernel(const AdGradArgs a, int blocks_a) {
+  if (!a.both) {
+    pdl_wait();
+    ao_short(a, blocks_a);
+    return;
+  }
+  // The kernel of the tiles has waited for what came before it and writes other adapters: only the end has to be in order.
+  __shared__ unsigned s_excess;
+  if (!ao_long(a, blockIdx.y, &s_excess)) ao_short(a, blocks_a);
+  if (blockIdx.x + blockIdx.y + blockIdx.z == 0) pdl_wait();
+}
+
+static int ad_launch_outer_short(const AdGradArgs& a, cudaStream_t s) {
+  const int per = 2 * kAsThreads, blocks_a = (a.K + per - 1) / per, blocks = blocks_a + (a.N + per - 1) / per;
+  MOE_CUDA_TRY(launch_pdl(adapters_outer_short_kernel, dim3(blocks, a.L, (a.R + kAsRanks - 1) / kAsRanks), dim3(kAsThreads), 0, s,
+                          a, blocks_a));
+  return MOE_OK;
+}
 
 int ad_launch_outer(const AdGradArgs& a, int sms, cudaStream_t s) {
-  if (!a.parts) {
-    const int per = 2 * kAsThreads, blocks_a = (a.K + per - 1) / per, blocks = blocks_a + (a.N + per - 1) / per;
-    MOE_CUDA_TRY(launch_pdl(adapters_outer_short_kernel, dim3(blocks, a.L, (a.R + kAsRanks - 1) / kAsRanks), dim3(kAsThreads),
-                            0, s, a, blocks_a));
-    return MOE_OK;
-  }
+  if (!a.parts) return ad_launch_outer_short(a, s);
   AoGeo g = {};
   g.Rk = (a.R + 15) / 16 * 16;
   g.atoms = (3 * g.Rk + 63) / 64;
@@ -426,7 +472,7 @@ int ad_launch_outer(const AdGradArgs& a, int sms, cudaStream_t s) {
   static bool done[64] = {};
   MOE_CUDA_TRY(ensure_smem(adapters_outer_tile_kernel, 227 * 1024 - 512, done));
   MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, adapters_outer_tile_kernel, a, g, mx, my, mv));
-  return MOE_OK;
+  return a.both ? ad_launch_outer_short(a, s) : MOE_OK;
 }
 
 }  // namespace moe
