@@ -438,7 +438,8 @@ class W4Linear:
     only: the result carries no gradient.
 
     ``forward(x, adapters=, adapter_ids=, seq_start=)`` adds the low-rank part of each request's adapter (``Adapters``)
-    to the result, in place.
+    to the result, in place: a bf16 result is rounded once as the projection's and once more as the sum (a layer with
+    ``out_dtype=torch.float32`` keeps the sum in fp32).
     """
 
     def __init__(self, packed: torch.Tensor, K: int, N: int, group: int, max_tokens: int = 1,

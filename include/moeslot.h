@@ -556,9 +556,12 @@ int moe_balance_loss(const void* logits, int bf16, const int32_t* ids, const uin
  * are picked, in descending order, and
  *   w[t][j] = scale * s_j / sum_i s_i   over the picks, with MOE_ROUTE_RAW scale * s_j.
  * Equal values: the lower index first.  NaN ranks behind everything else (in a
- * group's score it counts as -inf).  The
- * picks are those of 64-bit arithmetic; they do not depend on thread timing.
- * Renormalised picks that are all -inf have weight 0.
+ * group's score it counts as -inf); one NaN or +inf among a token's logits makes
+ * each of its softmax scores a NaN, so that the lowest indices win wherever
+ * scores are compared (with a bias, or by group without one).  The picks are
+ * those of 64-bit arithmetic; they do not depend on thread timing.  Renormalised
+ * weights are computed from the picks' logits alone; picks that are all -inf
+ * have weight 0.
  *   logits     device [T][E], fp32 or bf16 (bf16 = 1)
  *   sel_bias   device fp32 [E] or NULL; -inf: never picked while k others stay;
  *              +inf: before all others, and its group's score is +inf
@@ -596,7 +599,9 @@ int moe_route_groups_grad(const void* logits, int bf16, const int32_t* ids, cons
 
 /*
  * Low-rank adapters of many requests beside a shared projection (moe_w4_linear,
- * a bf16 product): base is the projection's result.  The pages have one model
+ * a bf16 product): base is the projection's result, as it was rounded to its
+ * type (a bf16 result with adapters is rounded twice; with out_f32 = 1 in both
+ * calls it is not).  The pages have one model
  * for all requests; an adapter is a request's own small correction to it.
  * Sequence q is the rows [seq_start[q], seq_start[q + 1]) and has adapter
  * l = ids[q]:
@@ -611,6 +616,8 @@ int moe_route_groups_grad(const void* logits, int bf16, const int32_t* ids, cons
  *   ids     device int32 [n_seq], -1: no adapter (out = base)
  *   seq_start  device int32 [n_seq + 1], ascending, empty sequences allowed, or
  *           NULL with n_seq = T: every row is a sequence of its own (decoding).
+ *           Empty sequences change no result and cost little each; they may pad
+ *           the starts of a captured graph.
  *           Rows before the first and behind the last sequence have no adapter.
  *   out     device [T] rows of N, ldo apart: bf16, or fp32 with out_f32 = 1; no
  *           byte of it may be x's (columns side by side of one buffer are fine,
