@@ -274,20 +274,28 @@ __global__ void __launch_bounds__(kAtThreads, 2)
     const uint64_t a0 = at_desc(smem_u32(sm), 16, 1024), b0 = at_desc(smem_u32(sm) + kAtXBytes, 16, 1024);
     int s = 0, n = 0;
     uint32_t ph = 0, aph = 1;
-    for (int i = 0; i < nk; ++i) {
-      const bool first = DRAINS ? i % kAtDrain == 0 : i < nacc, last = DRAINS && (i % kAtDrain == kAtDrain - 1 || i == nk - 1);
-      if (DRAINS && first && i >= kAtDrain * nacc) wait(&aempty[n], aph);
+    auto step = [&](bool first) {
       wait(&full1[s], ph);
       tc_fence_after();
       const uint64_t at = (uint64_t)(s * (stage1 >> 4));
       if (lead && !dead) umma_f16_k64(tmem + n * g.Rk, a0 + at, b0 + at, idesc, !first, 2, 2);
       if (lead) umma_commit(&empty1[s]);
-      if (last) {
-        if (lead) umma_commit(&afull[n]);
-      }
       __syncwarp();
       if (++s == g.stages1) s = 0, ph ^= 1;
-      if ((!DRAINS || last) && ++n == nacc) n = 0, aph ^= 1;
+    };
+    if constexpr (DRAINS) {
+      for (int i = 0; i < nk; i += kAtDrain) {
+        if (i >= kAtDrain * nacc) wait(&aempty[n], aph);
+        for (int k = i; k < min(i + kAtDrain, nk); ++k) step(k == i);
+        if (lead) umma_commit(&afull[n]);
+        __syncwarp();
+        if (++n == nacc) n = 0, aph ^= 1;
+      }
+    } else {
+      for (int i = 0; i < nk; ++i) {
+        step(i < nacc);
+        if (++n == nacc) n = 0;
+      }
     }
     if (lead) umma_commit(d1full);
     __syncwarp();

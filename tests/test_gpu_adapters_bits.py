@@ -2,6 +2,8 @@
 import pytest
 import torch
 
+from tests.test_gpu_adapters import check
+
 pytestmark = pytest.mark.gpu
 DEV, BF, I32 = "cuda", torch.bfloat16, torch.int32
 
@@ -50,3 +52,11 @@ def test_sums_over_many_features_do_not_drift(R):
     v = x.double() @ a[0].double().T
     mean = float(((kept.double() - v) / v).mean())
     assert abs(mean) <= 16 * 2.0 ** -23, mean
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("T,K,N,R", [(70, 20008, 72, 20), (300, 8264, 9000, 70), (1500, 4160, 264, 128), (5000, 2120, 136, 33), (2500, 131072, 8, 16),
+                                     (33, 40000, 40000, 100)])
+def test_sums_taken_over(T, K, N, R, dtype):
+    """More than 1024 features a CTA, in clusters and tiles of every size; both passes, rows of two sequences."""
+    check(T, K, N, R, 2, T + R, lengths=[T - 21, 21], dtype=dtype, none=0.0)
