@@ -236,7 +236,7 @@ static int ad_sms(int* sms) {
 }
 
 // Sequences of up to so many rows take the row kernel in a batch of short and long ones (36 single rows and four prompts of
-// 1001 rows: 15.3 us; a tile of 32 rows takes 9 us for one row, too).
+// 1001 rows: 15.4 us; a tile of 32 rows takes 8 us for one row, too).
 constexpr int kShortRows = 4;
 
 static int ad_run(const AdArgs& a, bool f32, cudaStream_t s) {

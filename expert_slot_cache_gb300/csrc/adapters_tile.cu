@@ -5,20 +5,20 @@
 // each CTA adds up some of the rows in a fixed order, scales them and hands them to all; then CTA c multiplies them by
 // its share of the N outputs (D2 [rows][128], double-buffered; B_l as it lies, MN-major) and adds base on the way out.
 // Nothing but x, A, B, base and out crosses the memory, so those bytes bound a large batch: 4096 rows of R 64, 2048 x 4096,
-// take 26.5 us where they take 13; the second product with its 67 MB takes 8, some 12 go to dependent steps before (x's way
-// in 3, sums through the cluster 3, v's way to the other CTAs 2.5, at 14 B a clock and SM).  64 rows of R 16 take 9.3 us.
-// Sending base to L2 while the first product runs costs more than it hides (4096 rows 30 us, 16,384 of R 16 50 for 41).
+// take 27.6 us where they take 13; the second product with its 67 MB takes 8, some 13 go to dependent steps before (x's way
+// in 3, sums through the cluster 3, v's way to the other CTAs some 3.7, at 14 B a clock and SM).  64 rows of R 16 take 8.3 us.
+// Sending base to L2 while the first product runs costs more than it hides (4096 rows 3.6 us more, 16,384 of R 16 8.3).
 //
 // The rows of a tile of 32 or 64 stand in the 128 lanes of D several times, so that all four epilogue warps (each reads
 // 32 lanes) have columns to store.  The tensor cores truncate what they add, so that an error grows with every step in one
 // direction: D1 is several accumulators in turn, of 16 additions each at most, added by additions that round.  Where four of
 // them are not enough (DRAINS: more than 1024 inputs a CTA), the epilogue warps take each over into a sum in TMEM while the
-// others are filled.  (200 rows of 131,072 inputs, R 16: 86 us; with four accumulators of 256 additions 73, and v off by
+// others are filled.  (200 rows of 131,072 inputs, R 16: 87 us; with four accumulators of 256 additions 73, and v off by
 // 5e-6.  A kernel of its own: as a branch of the one kernel it cost the others 1 to 3%.)
 //
 // v = scale x A^T enters the second product as a sum of three bf16 numbers, which are its 24 bits: with two (16 bits) a
-// result in which ranks nearly cancel was off by more than fp32 sums are.  (The third costs 4096 rows of R 64 1.3 us of 27.7,
-// most of it on v's way to the other CTAs.)  The products cost little beside the bytes: 2 R flops a byte of x.
+// result in which ranks nearly cancel was off by more than fp32 sums are.  (The third costs 4096 rows of R 64 1.2 us of 27.6,
+// on v's way to the other CTAs.)  The products cost little beside the bytes: 2 R flops a byte of x.
 #include <algorithm>
 
 #include "adapters.cuh"
@@ -598,10 +598,10 @@ int ad_launch_tiles(const AdArgs& a, bool f32, int short_rows, bool beside, cuda
   g.Rk = (a.R + 15) / 16 * 16;
   // CTAs of a cluster and rows of a tile, by an estimate of the time: rounds of as many clusters as run at once, in each a
   // CTA takes 9 us and its share of the tile's bytes at 40 KB/us, less where the CTAs' sum would pass 6.6 MB/us.
-  // Measured: 4096 rows of R 64 (2048 x 4096) 26.5 us with 8 and 128, 27.2 with 4 and 64, 30.7 with 4 and 128; 12,000 rows
-  // 64 with 2 and 128, 73 with 4 or 8; 16,384 of R 16 (2048 x 2048) 56 with 8 and 128, 45 with 4, 41 with 2; 1024 of R 16
-  // 15.3 with 8 and 128, 13.1 with 8 and 64, 12.3 with 8 and 32; 2000 of R 128 (4096 x 4096) 27 with 4 and 64, 43 with 8
-  // and 128.
+  // Measured: 4096 rows of R 64 (2048 x 4096) 27.3 us with 8 and 128, 28.8 with 4 and 64, 31.9 with 4 and 128; 12,000 rows
+  // 67 with 2 and 128, 76 with 4 or 8; 16,384 of R 16 (2048 x 2048) 56 with 8 and 128, 45 with 4, 41 with 2; 1024 of R 16
+  // 11.0 with 8 and 128, 10.3 with 8 and 64, 10.9 with 8 and 32; 2000 of R 128 (4096 x 4096) 30 with 4 and 64, 35 with 4 and
+  // 128, 46 with 8 and 128.
   int C = 8;
   double best = 0.;
   for (int c = 2; c <= 8; c *= 2)

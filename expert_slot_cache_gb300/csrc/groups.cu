@@ -10,7 +10,7 @@
 // or the best of its groups, are compared again in fp64.  That is some tokens in a thousand.
 //
 // The bytes of the logits, read once, would bound a large batch (16,384 x 512 fp32: 5.2 us); the instructions of a warp
-// for a token, about 1,250, bound it in practice (31.5 us, issued in 61% of the cycles), and the launch a small one (one token 3.2 us).
+// for a token, about 1,250, bound it in practice (31.7 us, issued in 61% of the cycles), and the launch a small one (one token 3.1 us).
 #include <algorithm>
 
 #include "internal.cuh"

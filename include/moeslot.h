@@ -626,8 +626,8 @@ int moe_route_groups_grad(const void* logits, int bf16, const int32_t* ids, cons
  *           or NULL
  * Sums are fp32, and v takes part in its product with all its 24 bits.  The
  * result does not depend on thread timing; its last bits depend on the batch's
- * sequences.  x of a row reaches no
- * other row.  (Waits are bounded: one that gives up sets MOE_DEV_TIMEOUT.)
+ * sequences and on which matrices are given.  x of a row reaches no other row.
+ * (Waits are bounded: one that gives up sets MOE_DEV_TIMEOUT.)
  * An id outside [-1, L) sets MOE_DEV_BAD_EXPERT and counts as -1; a descending
  * seq_start sets MOE_DEV_BAD_GROUPS.
  * Errors: MOE_ERR_ARG on NULL pointers, T not in [1, 2^24], K or N not in
